@@ -21,7 +21,9 @@
  * moe_mxfp4_prepack, moe_gather_rows_f16, moe_grouped_gemm_swiglu_mxfp4,
  * moe_grouped_gemm_mxfp4) and the W4A8 path on the block-scaled MMA
  * (moe_w4a8_prepack, moe_gather_rows_mx, moe_grouped_gemm_swiglu_w4a8,
- * moe_grouped_gemm_w4a8, moe_layer_forward_w4a8).
+ * moe_grouped_gemm_w4a8, moe_layer_forward_w4a8); and the attention that comes
+ * before it in the decoder layer, over a paged 8-bit key/value cache:
+ * moe_kv_append, moe_paged_attention, moe_kv_gather, moe_rope_table.
  *
  * Sources (page titles and sections):
  *  [Q3]  "Qwen3-MoE low-latency inference practice on Atlas A3/950 clusters"
@@ -541,6 +543,113 @@ MOE_API int moe_layer_kernel_launches(const moe_layer_desc* d);
  * 2 pair_pos[P], 3 x_exp[P,H], 4 act[P,I], 5 y_perm[P,H], 6 act_s[T,I_s],
  * 7 shared[T,H].  Writes min(n, 8) values into out; returns 8. */
 MOE_API int moe_layer_workspace_offsets(const moe_layer_desc* d, size_t* out, int n);
+
+/*
+ * Attention over a paged key/value cache held in 8 bits: the other half of the decoder layer that
+ * the expert layer belongs to.  moe_kv_append normalises, rotates and stores the new tokens of a
+ * batch, moe_paged_attention lets their queries read the cache, moe_kv_gather reads tokens back.
+ * [HY3] 1.1 (grouped query heads, per-head RMS norm of queries and keys, rotation), 4 (cache
+ * written by slot); the inference note's section on KV paging.
+ *
+ * The cache.  A page holds `page` consecutive tokens of one sequence; its index in the pool is
+ * page_table[b, position / page].  Codes are E4M3 bytes, [n_pages, Hkv, page, D]; one E8M0 byte s
+ * per page and head, [n_pages, Hkv], scales them by 2^(s - 127), for keys and values separately.
+ * Nothing outside the tokens that were appended is read as a number: a page may hold any bytes
+ * behind its sequence's last token.  The scale arrays need no alignment (slices of one array over
+ * all layers will do).
+ *
+ * The batch is ragged.  Sequence b brings the new tokens q_start[b] .. q_start[b+1] - 1 of the T
+ * rows (it may bring none), q_start[0] = 0 and q_start[B] = T; kv_len[b] counts its tokens after
+ * the call, the new ones being the last.  Lengths, starts and page table are device arrays, so a
+ * captured graph follows them.  Different sequences' pages must differ where a call appends.
+ *
+ * Limits: D == 128; page one of 16, 32, 64, 128; Hq % Hkv == 0, Hq <= 1024; B <= 65536; T * Hq,
+ * n_pages * Hkv * page and max_pages * page below 2^31 (the cache itself may pass 2^31 bytes).
+ *
+ * On the device: starts or lengths that contradict each other, a page outside the pool or the
+ * table, and a position beyond max_pos set the workspace's status to MOE_ERR_DEVICE_CHECK; tokens
+ * concerned are left out (append: not stored, their rows of q_out not written; gather: rows of
+ * zeros; attention: keys on such a page are not seen, a row that sees no key is zero).
+ */
+typedef struct moe_kv_desc {
+  int32_t B;          /* sequences */
+  int32_t T;          /* new tokens, over all sequences */
+  int32_t Hq;         /* query heads; head h reads key/value head h / (Hq / Hkv) */
+  int32_t Hkv;        /* key/value heads */
+  int32_t D;          /* elements per head: 128 */
+  int32_t page;       /* tokens per page (and per scale) */
+  int32_t n_pages;    /* pages in the pool */
+  int32_t max_pages;  /* columns of the page table */
+} moe_kv_desc;
+
+typedef struct moe_kv_cache {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+} moe_kv_cache;
+
+/* cos_sin [max_pos, rot_dim] fp32 out: row p holds cos(p f_i), then sin(p f_i), f_i = base^(-2i /
+ * rot_dim), i < rot_dim / 2, computed in double.  rot_dim % 16 == 0, <= 128.  Once, at load time. */
+MOE_API int moe_rope_table(int max_pos, int rot_dim, double base, float* cos_sin, void* stream);
+
+/*
+ * Appends the new tokens.
+ *
+ *  q [T,Hq,D], k, v [T,Hkv,D]: bf16; token t of each starts at t * its stride (elements, a multiple
+ *      of 8), the heads of a token are dense -- so all three may be parts of one projection's rows.
+ *      q and q_out may both be NULL.
+ *  q_start [B+1], kv_len [B], page_table [B,max_pages]: int32.
+ *  cos_sin [max_pos,rot_dim] as moe_rope_table writes it (any other table of angles will do).  The
+ *      first rot_dim elements of each query and key head are rotated by their token's position in
+ *      its sequence: pairs (i, i + rot_dim/2), or (2i, 2i+1) when interleaved != 0.  rot_dim % 16
+ *      == 0; 0 rotates nothing (cos_sin may be NULL).
+ *  q_norm_weight, k_norm_weight [D] bf16 or NULL: RMS norm of each head before the rotation, with
+ *      eps >= 0 added to the mean square.
+ *  q_out [T,Hq,D] bf16 out, dense (rounded once, from fp32).  q_out == q is allowed when q is dense.
+ *  kv: the cache (host struct of device pointers).  With a the largest finite magnitude among a page's
+ *      new tokens of one head, the exponent becomes max(-64, ceil(log2(a / 448)), the page's present
+ *      one if it already holds earlier tokens of the sequence); when it grows, the earlier codes are
+ *      rounded again to the new scale.  Infinities saturate.  A NaN in a token's key or value makes
+ *      that token's key row NaN (and the value zero there): queries that see it become NaN, others
+ *      do not.
+ *  ws: at least moe_status_bytes(); holds the status word only.
+ * Appending the same tokens again gives the same cache.
+ */
+MOE_API int moe_kv_append(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const uint16_t* k,
+                          long long k_stride, const uint16_t* v, long long v_stride, const int32_t* q_start,
+                          const int32_t* kv_len, const int32_t* page_table, const float* cos_sin, int max_pos,
+                          int rot_dim, int interleaved, const uint16_t* q_norm_weight, const uint16_t* k_norm_weight,
+                          float eps, uint16_t* q_out, const moe_kv_cache* kv, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Reads cached tokens back: row r of sequence b, out_start[b] <= r < out_start[b+1], is its token
+ * start[b] + r - out_start[b]; out_start[0] = 0, out_start[B] = n_rows (T and Hq of d are not used).
+ *  start [B], out_start [B+1], page_table [B,max_pages]: int32.
+ *  k, v [n_rows,Hkv,D] bf16 out: code * 2^(s - 127), exact.
+ */
+MOE_API int moe_kv_gather(const moe_kv_desc* d, const int32_t* start, const int32_t* out_start,
+                          const int32_t* page_table, const moe_kv_cache* kv, int n_rows, uint16_t* k, uint16_t* v,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * out[t,h] = sum_j p_j v_j,  p = softmax over the keys j that token t sees of scale * q[t,h] . k_j.
+ * The new token at position i sees the keys j < kv_len[b], j <= i if causal, and j > i - window if
+ * window > 0 (causal only).  A row that sees nothing is zero.
+ *
+ *  q [T,Hq,D] bf16, token stride q_stride (elements, a multiple of 8); normally q_out of moe_kv_append.
+ *  max_q: at least the new tokens of any one sequence (1 when decoding); sequences that bring more set
+ *      the status and their rows past max_q are not written.
+ *  scale > 0, finite.
+ *  out [T,Hq,D] bf16, dense.
+ *  ws: at least moe_paged_attention_workspace_size(d, max_q) bytes (0: invalid d), which suits every
+ *      call with the same B, T, Hq, Hkv and max_q; its status word must have been initialised once.
+ */
+MOE_API size_t moe_paged_attention_workspace_size(const moe_kv_desc* d, int max_q);
+MOE_API int moe_paged_attention(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const int32_t* q_start,
+                                const int32_t* kv_len, const int32_t* page_table, const moe_kv_cache* kv, int max_q,
+                                float scale, int causal, int window, uint16_t* out, void* ws, size_t ws_bytes,
+                                void* stream);
 
 #ifdef __cplusplus
 }

@@ -9,7 +9,9 @@ Functions carry the C names:
 
     moe_gating_topk, moe_init_routing, moe_grouped_gemm_swiglu, moe_grouped_gemm,
     moe_finalize_routing, moe_layer_forward (+ MoELayer, which owns a workspace); the front end
-    moe_add_rms_norm_cast and moe_router_logits; moe_init_routing_range.
+    moe_add_rms_norm_cast and moe_router_logits; moe_init_routing_range; the attention over a paged
+    8-bit key/value cache: moe_kv_append, moe_kv_gather, moe_paged_attention, moe_rope_table (+ KVCache,
+    its buffers, and AttentionLayer, which owns a cache and a workspace).
 """
 from __future__ import annotations
 
@@ -38,6 +40,14 @@ class MoEError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
         super().__init__(f"{what} failed: {status_string(status)} ({status})")
+
+
+class moe_kv_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "Hq", "Hkv", "D", "page", "n_pages", "max_pages")]
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scale", "v_scale")]
 
 
 class moe_layer_desc(ctypes.Structure):
@@ -133,6 +143,19 @@ _SIGS = {
                                  [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
                                   ctypes.POINTER(ctypes.c_void_p), ctypes.c_int]),
     "moe_layer_kernel_launches": (ctypes.c_int, [ctypes.POINTER(moe_layer_desc)]),
+    "moe_rope_table": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_double, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_kv_append": (ctypes.c_int, [ctypes.POINTER(moe_kv_desc)] + [ctypes.c_void_p, ctypes.c_longlong] * 3 +
+                      [ctypes.c_void_p] * 4 + [ctypes.c_int] * 3 + [ctypes.c_void_p] * 2 +
+                      [ctypes.c_float, ctypes.c_void_p, ctypes.POINTER(moe_kv_cache), ctypes.c_void_p,
+                       ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_kv_gather": (ctypes.c_int, [ctypes.POINTER(moe_kv_desc)] + [ctypes.c_void_p] * 3 +
+                      [ctypes.POINTER(moe_kv_cache), ctypes.c_int] + [ctypes.c_void_p] * 3 +
+                      [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_paged_attention_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(moe_kv_desc), ctypes.c_int]),
+    "moe_paged_attention": (ctypes.c_int, [ctypes.POINTER(moe_kv_desc), ctypes.c_void_p, ctypes.c_longlong] +
+                            [ctypes.c_void_p] * 3 + [ctypes.POINTER(moe_kv_cache), ctypes.c_int, ctypes.c_float,
+                                                     ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                                     ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 
@@ -764,3 +787,7 @@ class MoELayer:
         off = self.offsets_bytes[i]
         nbytes = n * (4 if dt == torch.int32 else 2)
         return self.ws[off:off + nbytes].view(dt).view(shape)
+
+
+from .attention import (AttentionLayer, KVCache, moe_kv_append, moe_kv_gather, moe_paged_attention,  # noqa: E402,F401
+                        moe_paged_attention_workspace, moe_rope_table)

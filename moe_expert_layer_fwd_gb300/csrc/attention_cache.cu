@@ -1,0 +1,420 @@
+// The paged 8-bit key/value cache: appending with normalisation and rotation, reading back, the rotation table.
+//
+// Sources: Hy3 295B MoE practice, section 1.1 (per-head RMS norm of queries and keys before the rotation, grouped query
+// heads) and 4 (new keys and values scattered into the cache by slot); the inference note's KV paging section (pages
+// of a fixed number of tokens, a page table per sequence).  The 8-bit format is this library's own choice: E4M3 codes
+// and one E8M0 scale per (page, head), the element and scale types of its MXFP8 token rows.
+//
+// Append, for a new token at position p of its sequence (both halves of a pair (a, b) come from one head):
+//   x^   = x * rsqrt(mean(x^2) + eps) * w              (queries and keys, when norm weights are given)
+//   a'   = a cos(p f_i) - b sin(p f_i),  b' = a sin(p f_i) + b cos(p f_i)        (the first `rot` elements)
+//   e    = max(-64, ceil(log2(amax / 448)), the page's exponent if it holds earlier tokens of the sequence)
+//   code = e4m3(x' * 2^-e)
+// with amax over the page's new tokens of one head.  A power of two costs an E4M3 value nothing but range: relative
+// precision is the same at every scale, and when e grows the earlier codes are rescaled exactly unless they become
+// subnormal.  Everything between the bf16 input and the one rounding of the output is fp32.
+#include "attention_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kAppendThreads = 512;
+constexpr int kWarps = kAppendThreads / 32;
+constexpr int kRowsPerWarp = 8;    // cache rows of one page a warp holds: 4 steps of 2 rows, 16 lanes x 8 elements each
+constexpr int kQHeads = 8;         // query heads of one token that a warp rotates: 4 steps of 2
+
+// A row in registers: lane l of a half-warp holds elements 8l .. 8l+7.
+__device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(w[i]);
+    x[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+__device__ __forceinline__ uint4 shfl4(const uint4& r, int src) {
+  uint4 o;
+  o.x = __shfl_sync(0xffffffffu, r.x, src, 16);
+  o.y = __shfl_sync(0xffffffffu, r.y, src, 16);
+  o.z = __shfl_sync(0xffffffffu, r.z, src, 16);
+  o.w = __shfl_sync(0xffffffffu, r.w, src, 16);
+  return o;
+}
+
+// What a lane needs of the rotation, the same for every row of a token.
+struct Rotary {
+  float cs[8], sn[8];  // half-split: of elements 8 (l mod rot/16) + i; interleaved: of pairs 4l + (i / 2)
+  int partner;         // lane holding the other halves of the pairs (half-split)
+  bool on, upper;
+};
+
+__device__ __forceinline__ void rotary_lane(Rotary& r, const KvAppendArgs& a, int l) {
+  const int half = a.rot >> 4;  // lanes of one half of the rotated part
+  r.on = l < 2 * half;
+  r.upper = !a.interleaved && l >= half;
+  r.partner = !r.on || a.interleaved ? l : (r.upper ? l - half : l + half);
+}
+
+__device__ __forceinline__ void rotary_load(Rotary& r, const KvAppendArgs& a, int l, int pos) {
+  if (!r.on) return;
+  const float* row = a.cos_sin + (size_t)pos * a.rot;
+  if (a.interleaved) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(row + 4 * l));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(row + (a.rot >> 1) + 4 * l));
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      r.cs[i] = cc[i >> 1];
+      r.sn[i] = ss[i >> 1];
+    }
+  } else {
+    const float* p = row + 8 * (r.upper ? l - (a.rot >> 4) : l);
+    const float* q = p + (a.rot >> 1);
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 c = __ldg(reinterpret_cast<const float4*>(p + i));
+      const float4 s = __ldg(reinterpret_cast<const float4*>(q + i));
+      r.cs[i] = c.x; r.cs[i + 1] = c.y; r.cs[i + 2] = c.z; r.cs[i + 3] = c.w;
+      r.sn[i] = s.x; r.sn[i + 1] = s.y; r.sn[i + 2] = s.z; r.sn[i + 3] = s.w;
+    }
+  }
+}
+
+// Normalises (own / other: the norm weights of this lane's and of its partner's elements) and rotates one row.
+// Products and sums are rounded one by one (no fused multiply-add), so that the result does not depend on which
+// of a pair's two products a compiler chooses to fuse.
+__device__ __forceinline__ void norm_rotate(const uint4& raw, const Rotary& r, const KvAppendArgs& a, bool norm,
+                                            const uint4& own, const uint4& other, float (&x)[8]) {
+  float y[8];
+  unpack8(raw, x);
+  unpack8(shfl4(raw, r.partner), y);
+  if (norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+#pragma unroll
+    for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, 16);
+    const float rs = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
+    float w[8], u[8];
+    unpack8(own, w);
+    unpack8(other, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = __fmul_rn(__fmul_rn(x[i], rs), w[i]);
+      y[i] = __fmul_rn(__fmul_rn(y[i], rs), u[i]);
+    }
+  }
+  if (!r.on) return;
+  if (a.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float p = x[i], q = x[i + 1];
+      x[i] = __fsub_rn(__fmul_rn(p, r.cs[i]), __fmul_rn(q, r.sn[i]));
+      x[i + 1] = __fadd_rn(__fmul_rn(p, r.sn[i]), __fmul_rn(q, r.cs[i]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float c = __fmul_rn(x[i], r.cs[i]), s = __fmul_rn(y[i], r.sn[i]);
+      x[i] = r.upper ? __fadd_rn(s, c) : __fsub_rn(c, s);
+    }
+  }
+}
+
+// The smallest exponent >= -64 with amax * 2^-e <= 448 = 1.75 * 2^8.
+__device__ __forceinline__ int scale_exponent(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return max(e, kMinScaleExp);
+}
+
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv) {
+  uint2 o;
+  o.x = e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16);
+  o.y = e4m3x2(x[4] * inv, x[5] * inv) | (e4m3x2(x[6] * inv, x[7] * inv) << 16);
+  return o;
+}
+
+__device__ __forceinline__ uint32_t rescale4(uint32_t codes, float f) {
+  const float2 a = e4m3x2_f32(codes & 0xFFFFu), b = e4m3x2_f32(codes >> 16);
+  return e4m3x2(a.x * f, a.y * f) | (e4m3x2(b.x * f, b.y * f) << 16);
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? a : 0.f;  // infinities and NaN do not set the scale
+}
+
+// Blocks [0, kv_blocks): cache units.  A unit is one touched page of one sequence and one head; page / 8 warps hold
+// its rows.  Sequence b's touched pages take the slots from q_start[b] / page + 2b on: n new tokens touch at most
+// (n - 1) / page + 2 pages, so the slots of different sequences never meet and T / page + 2B of them are enough.
+// Every unit is found from the lengths on the device: the host never needs them.
+// The other blocks: queries, a warp per (token, 8 heads).
+__global__ void __launch_bounds__(kAppendThreads)
+    kv_append_kernel(const KvBatch c, const KvAppendArgs a, int kv_blocks, int slots) {
+  __shared__ float s_amax[2][kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
+  Rotary rt;
+  rotary_lane(rt, a, l);
+
+  if ((int)blockIdx.x >= kv_blocks) {
+    const int chunks = (c.Hq + kQHeads - 1) / kQHeads;
+    const long long w = (long long)(blockIdx.x - kv_blocks) * kWarps + warp;
+    const int t = (int)(w / chunks), h0 = (int)(w - (long long)t * chunks) * kQHeads;
+    if (t >= c.T) return;
+    const int b = warp_search(c.B, t, [&](int i) { return __ldg(c.q_start + i); });
+    // the rows do not depend on the position: start them before its loads
+    uint4 raw[kQHeads / 2];
+#pragma unroll
+    for (int i = 0; i < kQHeads / 2; ++i) {
+      const int h = h0 + 2 * i + half;
+      raw[i] = h < c.Hq ? __ldg(reinterpret_cast<const uint4*>(a.q + (size_t)t * a.q_stride + (size_t)h * kHeadDim) + l)
+                        : make_uint4(0, 0, 0, 0);
+    }
+    SeqRange s;
+    const bool ok = load_seq(c, b, s) && t >= s.t0 && t < s.t1;
+    const int pos = ok ? s.first() + t - s.t0 : -1;
+    if (pos < 0 || pos >= a.max_pos) {
+      if (lane == 0) set_status(c.status, DEV_ERR_BOUNDS);
+      return;
+    }
+    rotary_load(rt, a, l, pos);
+    uint4 own = make_uint4(0, 0, 0, 0);
+    if (a.q_norm) own = __ldg(reinterpret_cast<const uint4*>(a.q_norm) + l);
+    const uint4 other = shfl4(own, rt.partner);
+#pragma unroll
+    for (int i = 0; i < kQHeads / 2; ++i) {
+      float x[8];
+      norm_rotate(raw[i], rt, a, a.q_norm != nullptr, own, other, x);
+      const int h = h0 + 2 * i + half;
+      if (h < c.Hq) {
+        const uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                   pack_bf16x2(x[6], x[7]));
+        reinterpret_cast<uint4*>(a.q_out + ((size_t)t * c.Hq + h) * kHeadDim)[l] = o;
+      }
+    }
+    return;
+  }
+
+  const int wpu = c.page / kRowsPerWarp;  // warps per unit
+  const int wu = warp % wpu;
+  const int unit = (int)blockIdx.x * (kWarps / wpu) + warp / wpu;
+  const int slot = unit / c.Hkv, h = unit - slot * c.Hkv;
+  // Everything up to the scale is done under `active` without leaving: the block meets at a barrier below.
+  bool active = slot < slots;
+  int b = 0, j = 0, pg = -1;
+  SeqRange s = {0, 0, 0};
+  if (active) {
+    b = warp_search(c.B, slot, [&](int i) { return (__ldg(c.q_start + i) >> c.page_log2) + 2 * i; });
+    active = load_seq(c, b, s) && s.t1 > s.t0;
+    if (active && s.first() < 0) {
+      set_status(c.status, DEV_ERR_CONFIG);
+      active = false;
+    }
+    j = (s.first() >> c.page_log2) + slot - ((s.t0 >> c.page_log2) + 2 * b);
+    active = active && j <= ((s.len - 1) >> c.page_log2) && s.len <= a.max_pos;
+    if (s.t1 > s.t0 && s.len > a.max_pos) set_status(c.status, DEV_ERR_BOUNDS);
+    if (active) active = (pg = load_page(c, b, j)) >= 0;
+  }
+  const int first = s.first();
+  const int p0 = (j << c.page_log2) + wu * kRowsPerWarp + half;  // position of this half-warp's first row
+  const size_t base = ((size_t)(pg < 0 ? 0 : pg) * c.Hkv + h) << c.page_log2;  // the unit's first code row
+  int old_k = kMinScaleExp, old_v = kMinScaleExp;
+  const bool partial = active && (j << c.page_log2) < first;
+  if (partial) {
+    old_k = min((int)c.k_scale[(size_t)pg * c.Hkv + h] - 127, 126);
+    old_v = min((int)c.v_scale[(size_t)pg * c.Hkv + h] - 127, 126);
+  }
+
+  constexpr int kSteps = kRowsPerWarp / 2;
+  uint4 kr[kSteps], vr[kSteps];
+  float kx[kSteps][8] = {};
+  unsigned here = 0;
+  float amax_k = 0.f, amax_v = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int p = p0 + 2 * i;
+    kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+    if (active && p >= first && p < s.len) {
+      here |= 1u << i;
+      const size_t t = (size_t)(s.t0 + p - first);
+      kr[i] = __ldg(reinterpret_cast<const uint4*>(a.k + t * a.k_stride + (size_t)h * kHeadDim) + l);
+      vr[i] = __ldg(reinterpret_cast<const uint4*>(a.v + t * a.v_stride + (size_t)h * kHeadDim) + l);
+    }
+  }
+  uint4 own = make_uint4(0, 0, 0, 0);
+  if (a.k_norm) own = __ldg(reinterpret_cast<const uint4*>(a.k_norm) + l);
+  const uint4 other = shfl4(own, rt.partner);
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    // A step that neither half-warp has a row in is skipped whole (the shuffles below need both).
+    if (!__any_sync(0xffffffffu, here >> i & 1)) continue;
+    if (here >> i & 1) rotary_load(rt, a, l, p0 + 2 * i);
+    norm_rotate(kr[i], rt, a, a.k_norm != nullptr, own, other, kx[i]);
+    if (here >> i & 1) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax_k = fmaxf(amax_k, finite_abs(kx[i][e]));
+      float x[8];
+      unpack8(vr[i], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax_v = fmaxf(amax_v, finite_abs(x[e]));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    amax_k = fmaxf(amax_k, __shfl_xor_sync(0xffffffffu, amax_k, o));
+    amax_v = fmaxf(amax_v, __shfl_xor_sync(0xffffffffu, amax_v, o));
+  }
+  if (lane == 0) {
+    s_amax[0][warp] = amax_k;
+    s_amax[1][warp] = amax_v;
+  }
+  __syncthreads();
+  if (!active) return;
+  const int w0 = warp - wu;
+  for (int i = 0; i < wpu; ++i) {
+    amax_k = fmaxf(amax_k, s_amax[0][w0 + i]);
+    amax_v = fmaxf(amax_v, s_amax[1][w0 + i]);
+  }
+  const int ek = max(scale_exponent(amax_k), old_k), ev = max(scale_exponent(amax_v), old_v);
+  if (wu == 0 && lane == 0) {
+    c.k_scale[(size_t)pg * c.Hkv + h] = (uint8_t)(ek + 127);
+    c.v_scale[(size_t)pg * c.Hkv + h] = (uint8_t)(ev + 127);
+  }
+  const float ik = exp2_int(-ek), iv = exp2_int(-ev);
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int p = p0 + 2 * i;
+    const size_t row = base + (size_t)(wu * kRowsPerWarp + half + 2 * i);
+    uint2* kc = reinterpret_cast<uint2*>(c.k_codes + row * kHeadDim) + l;
+    uint2* vc = reinterpret_cast<uint2*>(c.v_codes + row * kHeadDim) + l;
+    // A NaN in a token's value is kept in its key instead, as a NaN key row: the queries that see the token become
+    // NaN through their score, and those that do not are untouched (0 * NaN in the product with V would reach them).
+    float x[8];
+    unpack8(vr[i], x);
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      bad |= x[e] != x[e] || kx[i][e] != kx[i][e];
+      if (x[e] != x[e]) x[e] = 0.f;
+    }
+    const unsigned mask = __ballot_sync(0xffffffffu, (here >> i & 1) && bad);
+    if (here >> i & 1) {
+      uint2 o = quantise8(kx[i], ik);
+      if (mask >> (16 * half) & 0xFFFFu) o = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+      *kc = o;
+      *vc = quantise8(x, iv);
+    } else if (partial && p < first) {
+      if (ek > old_k) {
+        const float f = exp2_int(max(old_k - ek, -126));
+        const uint2 o = *kc;
+        *kc = make_uint2(rescale4(o.x, f), rescale4(o.y, f));
+      }
+      if (ev > old_v) {
+        const float f = exp2_int(max(old_v - ev, -126));
+        const uint2 o = *vc;
+        *vc = make_uint2(rescale4(o.x, f), rescale4(o.y, f));
+      }
+    }
+  }
+}
+
+constexpr int kGatherRowsPerBlock = 32;
+constexpr int kGatherThreads = 256;
+
+__global__ void __launch_bounds__(kGatherThreads)
+    kv_gather_kernel(const KvBatch c, const int32_t* start, const int32_t* out_start, int n_rows, uint16_t* k_out,
+                     uint16_t* v_out) {
+  __shared__ int s_page[kGatherRowsPerBlock], s_slot[kGatherRowsPerBlock];
+  const int r0 = (int)blockIdx.x * kGatherRowsPerBlock;
+  const int rows = min(kGatherRowsPerBlock, n_rows - r0);
+  if ((int)threadIdx.x < rows) {
+    const int r = r0 + (int)threadIdx.x;
+    int lo = 0, hi = c.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(out_start + mid) <= r) lo = mid; else hi = mid;
+    }
+    const long long pos = (long long)__ldg(start + lo) + r - __ldg(out_start + lo);
+    const bool ok = r >= __ldg(out_start + lo) && r < __ldg(out_start + lo + 1) && pos >= 0 &&
+                    pos < (long long)c.max_pages * c.page;
+    if (!ok) set_status(c.status, DEV_ERR_BOUNDS);
+    s_page[threadIdx.x] = ok ? load_page(c, lo, (int)(pos >> c.page_log2)) : -1;
+    s_slot[threadIdx.x] = (int)(pos & (c.page - 1));
+  }
+  __syncthreads();
+  const int per_row = c.Hkv * (kHeadDim / 16);  // 16 codes a thread
+  const bool is_v = blockIdx.y;
+  const uint8_t* codes = is_v ? c.v_codes : c.k_codes;
+  const uint8_t* scale = is_v ? c.v_scale : c.k_scale;
+  uint16_t* out = is_v ? v_out : k_out;
+  for (int i = threadIdx.x; i < rows * per_row; i += kGatherThreads) {
+    const int r = i / per_row, q = i - r * per_row, h = q >> 3, d = (q & 7) * 16;
+    const int pg = s_page[r];
+    uint4 o[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};  // a row that is not there reads as zeros
+    if (pg >= 0) {
+      const size_t unit = (size_t)pg * c.Hkv + h;
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(codes + ((unit << c.page_log2) + s_slot[r]) * kHeadDim + d));
+      // 2^e as a product of two halves, each a normal number
+      const int e = (int)__ldg(scale + unit) - 127;
+      const float f0 = exp2_int(e >> 1), f1 = exp2_int(e - (e >> 1));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t u[8];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float2 a = e4m3x2_f32(w[m] & 0xFFFFu), b = e4m3x2_f32(w[m] >> 16);
+        u[2 * m] = pack_bf16x2(a.x * f0 * f1, a.y * f0 * f1);
+        u[2 * m + 1] = pack_bf16x2(b.x * f0 * f1, b.y * f0 * f1);
+      }
+      o[0] = make_uint4(u[0], u[1], u[2], u[3]);
+      o[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    }
+    uint4* to = reinterpret_cast<uint4*>(out + ((size_t)(r0 + r) * c.Hkv + h) * kHeadDim + d);
+    to[0] = o[0];
+    to[1] = o[1];
+  }
+}
+
+// cos and sin of p * base^(-2i / rot), the angle and both functions in double: at position 10^6 the largest angle has
+// lost 20 of fp32's 24 bits.
+__global__ void rope_table_kernel(int max_pos, int rot, double base, float* cos_sin) {
+  const int half = rot >> 1;
+  const long long n = (long long)max_pos * half;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+    const long long p = i / half;
+    const int f = (int)(i - p * half);
+    double s, co;
+    sincos((double)p * pow(base, -2.0 * f / rot), &s, &co);
+    cos_sin[p * rot + f] = (float)co;
+    cos_sin[p * rot + half + f] = (float)s;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvBatch& c, const KvAppendArgs& a, cudaStream_t stream) {
+  const long long slots = (long long)c.T / c.page + 2LL * c.B;
+  const int per_block = kWarps / (c.page / kRowsPerWarp);
+  const long long kv_blocks = (slots * c.Hkv + per_block - 1) / per_block;
+  const long long chunks = (c.Hq + kQHeads - 1) / kQHeads;
+  const long long q_blocks = a.q ? ((long long)c.T * chunks + kWarps - 1) / kWarps : 0;
+  kv_append_kernel<<<(unsigned)(kv_blocks + q_blocks), kAppendThreads, 0, stream>>>(c, a, (int)kv_blocks, (int)slots);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_gather(const KvBatch& c, const int32_t* start, const int32_t* out_start, int n_rows, uint16_t* k,
+                             uint16_t* v, cudaStream_t stream) {
+  const dim3 grid((n_rows + kGatherRowsPerBlock - 1) / kGatherRowsPerBlock, 2);
+  kv_gather_kernel<<<grid, kGatherThreads, 0, stream>>>(c, start, out_start, n_rows, k, v);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rope_table(int max_pos, int rot, double base, float* cos_sin, cudaStream_t stream) {
+  const long long n = (long long)max_pos * (rot >> 1);
+  const long long blocks = (n + 255) / 256;
+  rope_table_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(max_pos, rot, base, cos_sin);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

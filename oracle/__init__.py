@@ -25,6 +25,8 @@ What it computes, step by step, each function citing the passage it follows:
   MXFP4 (E2M1 elements) expert weights.
 * ``w4a8``     -- the W4A8 layer: MXFP8 hidden state times MXFP4 expert weights, the SwiGLU
   output quantised to MXFP8 before the down projection.
+* ``attention`` -- the paged 8-bit key/value cache: norm and rotation, append, read-back, and
+  softmax attention over it (imported by name: ``from oracle import attention``).
 
 Precision: float64 everywhere, except the expert *selection*, which is an
 integer decided by floating point and is therefore taken in float32 with the
