@@ -1,0 +1,666 @@
+// Attention of few query rows per key/value head (decoding, and the check of a few speculated tokens): the cache is
+// read once and everything else is small, so the bytes of the cache bound it.
+//
+// The keys are the M operand: for one key/value head a tile of 128 keys, E4M3 as cached, times the query rows that read
+// this head (columns: new tokens x grouped heads, NC of them),
+//   S^T[128 keys, 2 NC] = K . [q_hi | q_lo]^T           tcgen05 kind::f8f6f4, M = 128, N = 2 NC
+//   u = (S_hi + S_lo) * scale * 2^(e_k + e_q) + e_v     log2 of the weight times the size of the page's values
+//   r = max(r, max_j u),  p'_j = 2^(u_j - r + 8) = hi + lo in E4M3,  l = l f + sum_j p'_j 2^-e_v
+//   O^T[128 dims, 2 NC] = V^T . [p'_hi | p'_lo]          the same instruction, V read with its dims contiguous
+// so that neither keys nor values pass through a register: TMA writes the pages' codes to shared memory with the
+// 128-byte swizzle and the tensor core reads them there, once each.  Scales never touch the codes: those of the keys
+// are multiplied onto S, those of the values are added to the exponent.  The running maximum r is the
+// one of u: the largest p' is 2^8 whatever the pages' scales are, errors are relative to the largest term of
+// the sum that is being computed, and the denominator takes the scale out again.  hi + lo keeps 8 bits of p'.
+// A thread owns one key (S, p') and one output dim (O): the accumulator stays in its registers, each tile's product is
+// read from tensor memory and added, so nothing in tensor memory is ever rescaled.
+//
+// Work: all (sequence, head, tile) in one order, cut into equal runs, one per block (two blocks per SM): a long sequence is
+// split over as many blocks as it takes, a short one shares a block.  A row whose tiles lie in one block
+// is finished there; otherwise the parts (sum, maximum, denominator) go to the workspace and a second kernel joins them in a
+// fixed order.  The host knows none of the lengths.
+//
+// Warps: 0-3 softmax (thread = key = dim), 4 TMA, 5 MMA, 6 queries.  Every wait is bounded (2 s).
+#include "attention_tiles.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 224;
+constexpr int kWholeTiles = 4;    // rows of at most so many tiles are not split
+constexpr int kMinRun = 2;        // tiles in a block's run, at least
+
+template <int NC>
+struct Cfg {
+  static constexpr int kPerSm = NC == 32 ? 1 : 2;
+  static constexpr int kStages = NC == 32 ? 5 : 3;
+  static constexpr int kQBufs = 2;  // the next segment's scores start before this one has ended
+  static constexpr int kRows = 2 * NC;                      // hi and lo rows of the queries, of the weights
+  static constexpr int kOpBytes = kRows * 128;
+  static constexpr int kPOff = kStages * 2 * kTileBytes;
+  static constexpr int kQOff = kPOff + kOpBytes;
+  static constexpr int kBarOff = kQOff + kQBufs * kOpBytes;
+  static constexpr int kNumBars = 4 * kStages + 2 * kQBufs + 7;
+  static constexpr int kQfOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // float qf[kQBufs][NC], int token[kQBufs][NC]
+  static constexpr int kMaxOff = kQfOff + kQBufs * NC * 8;  // float [NC][4]: per-warp maxima (and sums)
+  static constexpr int kMiscOff = kMaxOff + NC * 16;
+  static constexpr int kBytes = 1024 + kMiscOff + 64;
+  static constexpr int kTmemCols = 3 * kRows <= 64 ? 64 : (3 * kRows <= 128 ? 128 : 256);  // S twice, O
+  static constexpr int kOCol = 2 * kRows;
+};
+
+// A run of tiles of one (sequence, head): the tiles [i0, i1) of its nt.
+struct Segment {
+  int b, h, i0, i1;
+  SeqRange s;
+  KeyRange r;
+};
+
+// Walks the segments of a block's run of tiles.
+struct Walk {
+  const KvBatch& c;
+  const AttentionArgs& a;
+  long long left;
+  int b, h, i;
+  __device__ Walk(const KvBatch& c_, const AttentionArgs& a_, long long n, int b_, int h_, int i_)
+      : c(c_), a(a_), left(n), b(b_), h(h_), i(i_) {}
+  __device__ bool next(Segment& g) {
+    while (left > 0 && b < c.B) {
+      const bool ok = load_seq(c, b, g.s);
+      g.r = key_range(g.s, a);
+      if (!ok || g.r.nt == 0) {
+        ++b;
+        h = i = 0;
+        continue;
+      }
+      g.b = b;
+      g.h = h;
+      g.i0 = i;
+      g.i1 = (int)min((long long)g.r.nt, i + left);
+      left -= g.i1 - i;
+      i = g.i1;
+      if (i == g.r.nt) {
+        i = 0;
+        if (++h == c.Hkv) {
+          h = 0;
+          ++b;
+        }
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ int seq_tiles(const KvBatch& c, const AttentionArgs& a, int b) {
+  SeqRange s;
+  return load_seq(c, b, s) ? key_range(s, a).nt : 0;
+}
+
+// Tiles of all sequences before this thread's share of them, and of all: `threads` threads each take a run of sequences.
+__device__ __forceinline__ long long scan_tiles(const KvBatch& c, const AttentionArgs& a, int threads, long long* s_warp,
+                                                long long& mine, long long& total) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (c.B + threads - 1) / threads;
+  mine = 0;
+  for (int b = tid * per; b < min(c.B, (tid + 1) * per); ++b) mine += seq_tiles(c, a, b);
+  long long x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+  for (int w = 0; w < threads / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  __syncthreads();
+  return before + x - mine;
+}
+
+// Tiles per block: equal runs over the grid.
+__device__ __forceinline__ long long tiles_per_block(long long n, int blocks) {
+  return max((long long)kMinRun, (n + blocks - 1) / blocks);
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, kAttnTimeoutNs, status));
+}
+
+// acc[x] += column x + column NC + x of this thread's tensor-memory lane.
+template <int NC>
+__device__ __forceinline__ void add_product(uint32_t taddr, float (&acc)[NC]) {
+#pragma unroll
+  for (int y = 0; y < NC; y += 8) {
+    uint32_t s[8], t[8];
+    tmem_ld8_async(taddr + y, s);
+    tmem_ld8_async(taddr + NC + y, t);
+    tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < 8; ++x) acc[y + x] += __uint_as_float(s[x]) + __uint_as_float(t[x]);
+  }
+}
+
+template <int NC>
+__global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
+    attention_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                            const KvBatch c, const AttentionArgs a, int split, float* part_o, float2* part_rl) {
+  using C = Cfg<NC>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* k_empty = k_full + C::kStages;
+  uint64_t* v_full = k_empty + C::kStages;
+  uint64_t* v_empty = v_full + C::kStages;
+  uint64_t* q_full = v_empty + C::kStages;
+  uint64_t* q_empty = q_full + C::kQBufs;
+  uint64_t* s_full = q_empty + C::kQBufs;   // [2]
+  uint64_t* s_empty = s_full + 2;           // [2]
+  uint64_t* p_full = s_empty + 2;
+  uint64_t* o_full = p_full + 1;
+  uint64_t* done = o_full + 1;
+  float* s_qf = reinterpret_cast<float*>(smem + C::kQfOff);
+  int* s_tok = reinterpret_cast<int*>(s_qf + C::kQBufs * NC);
+  float* s_max = reinterpret_cast<float*>(smem + C::kMaxOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+  int* s_begin = reinterpret_cast<int*>(smem + C::kMiscOff + 8);  // b, h, tile
+  volatile int* s_bad = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 24);  // [4] a softmax warp gave up
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = c.Hq / c.Hkv;
+  pdl_launch_dependents();
+
+  // ---- this block's run of tiles
+  long long run = 0;
+  int slot0 = 2 * (int)blockIdx.x;
+  if (split) {
+    long long mine, total;
+    // the scan's scratch is the weights' operand, free until the roles start
+    long long* s_warp = reinterpret_cast<long long*>(smem + C::kPOff);
+    const long long before = scan_tiles(c, a, kThreads, s_warp, mine, total);
+    const long long all = total * c.Hkv, per = tiles_per_block(all, gridDim.x);
+    const long long begin = (long long)blockIdx.x * per;
+    run = min(per, all - begin);
+    if (run <= 0) return;
+    if (before * c.Hkv <= begin && begin < (before + mine) * c.Hkv) {
+      long long at = before;
+      int b = tid * ((c.B + kThreads - 1) / kThreads), nt;
+      while ((at + (nt = seq_tiles(c, a, b))) * c.Hkv <= begin) {
+        at += nt;
+        ++b;
+      }
+      const long long rel = begin - at * c.Hkv;
+      s_begin[0] = b;
+      s_begin[1] = (int)(rel / nt);
+      s_begin[2] = (int)(rel % nt);
+    }
+  } else {
+    const int b = (int)blockIdx.x / c.Hkv;
+    run = seq_tiles(c, a, b);
+    if (run <= 0) return;
+    if (tid == 0) {
+      s_begin[0] = b;
+      s_begin[1] = (int)blockIdx.x - b * c.Hkv;
+      s_begin[2] = 0;
+    }
+  }
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < C::kQBufs; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 5);  // the last QK product of a segment, and the four softmax warps
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+    }
+    mbar_init(p_full, 4);
+    mbar_init(o_full, 1);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) s_bad[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) tmem_alloc(tmem_slot, C::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk walk(c, a, run, s_begin[0], s_begin[1], s_begin[2]);
+  Segment g;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ TMA: lane = page of the tile
+    const uint64_t pol = policy_evict_first();
+    const int pages = kTile >> c.page_log2;
+    const uint32_t box = (uint32_t)c.page * kHeadDim;
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      const int32_t* row = c.page_table + (size_t)g.b * c.max_pages;
+      const int end = (g.r.hi + c.page - 1) >> c.page_log2, from = g.r.lo >> c.page_log2;
+      // page of this lane in tile i, read one tile ahead; -1: nothing to load
+      auto page_at = [&](int i) {
+        const int j = (g.r.tile0 + i) * pages + lane;
+        return lane < pages && i < g.i1 && j >= from && j < end ? __ldg(row + j) : -1;
+      };
+      int pg = page_at(g.i0);
+      for (int i = g.i0; i < g.i1; ++i) {
+        const int next = page_at(i + 1);
+        const bool have = pg >= 0 && pg < c.n_pages;
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have)) * box;
+        const int st = (int)(n % C::kStages);
+        const uint32_t ph = (n / C::kStages) & 1u;
+        uint8_t* dst = smem + st * 2 * kTileBytes + lane * box;
+        const int y = have ? (int)(((long long)pg * c.Hkv + g.h) << c.page_log2) : 0;
+        if (!(ok = warp_wait(&k_empty[st], ph ^ 1u, abort_flag, c.status))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[st], bytes);
+        __syncwarp();
+        if (have) tma_load_2d(dst, &tm_k, 0, y, &k_full[st], pol);
+        const bool vok = warp_wait(&v_empty[st], ph ^ 1u, abort_flag, c.status);
+        // on a timeout the keys of this stage are still on their way: count the fill, so that the drain waits for it
+        if (lane == 0) mbar_arrive_expect_tx(&v_full[st], vok ? bytes : 0);
+        __syncwarp();
+        if (vok && have) tma_load_2d(dst + kTileBytes, &tm_v, 0, y, &v_full[st], pol);
+        ++n;
+        pg = next;
+        ok = vok;
+        if (!ok) break;
+      }
+    }
+    // Every copy lands before the block ends.
+    if (lane == 0) {
+      for (int st = 0; st < C::kStages; ++st) {
+        const uint32_t fills = n / C::kStages + ((uint32_t)st < n % C::kStages ? 1u : 0u);
+        if (!fills) continue;
+        mbar_wait_bounded(&k_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
+        mbar_wait_bounded(&v_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA: scores run one tile ahead of the weighted sums
+    if (lane == 0) {
+      const uint32_t id_s = umma_idesc_e4m3(kTile, C::kRows, false), id_o = umma_idesc_e4m3(kHeadDim, C::kRows, true);
+      const uint64_t desc = umma_desc_sw128(smem_u32(smem));
+      uint32_t nq = 0, segs = 0;
+      bool ok = true, more = walk.next(g);
+      int i = more ? g.i0 : 0;
+      auto scores = [&]() {
+        const int st = (int)(nq % C::kStages), qb = (int)(segs % C::kQBufs), sb = (int)(nq & 1u);
+        if (i == g.i0)
+          ok = ok && mbar_wait_bounded(&q_full[qb], (segs / C::kQBufs) & 1u, abort_flag, kAttnTimeoutNs, c.status);
+        ok = ok && mbar_wait_bounded(&k_full[st], (nq / C::kStages) & 1u, abort_flag, kAttnTimeoutNs, c.status);
+        ok = ok && mbar_wait_bounded(&s_empty[sb], ((nq >> 1) & 1u) ^ 1u, abort_flag, kAttnTimeoutNs, c.status);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t ad = desc + (uint64_t)((st * 2 * kTileBytes) >> 4);
+        const uint64_t bd = desc + (uint64_t)((C::kQOff + qb * C::kOpBytes) >> 4);
+#pragma unroll
+        for (int k = 0; k < kHeadDim / 32; ++k)
+          umma_e4m3(tmem + sb * C::kRows, ad + 2 * k, bd + 2 * k, id_s, k != 0);
+        umma_commit(&k_empty[st]);
+        umma_commit(&s_full[sb]);
+        ++nq;
+        if (++i == g.i1) {
+          umma_commit(&q_empty[qb]);
+          ++segs;
+          more = walk.next(g);
+          i = more ? g.i0 : 0;
+        }
+      };
+      if (more) scores();
+      for (uint32_t n = 0; ok && n < (uint32_t)run; ++n) {
+        if (more) scores();
+        if (!ok) break;
+        const int st = (int)(n % C::kStages);
+        if (!mbar_wait_bounded(p_full, n & 1u, abort_flag, kAttnTimeoutNs, c.status)) break;
+        if (!mbar_wait_bounded(&v_full[st], (n / C::kStages) & 1u, abort_flag, kAttnTimeoutNs, c.status)) break;
+        tc_fence_after();
+        // V[token][dim]: the 128-byte rows are the K index, eight rows (1 KB) to a swizzle atom, 32 tokens an MMA
+        const uint64_t ad = desc + (uint64_t)((st * 2 * kTileBytes + kTileBytes) >> 4);
+        const uint64_t bd = desc + (uint64_t)(C::kPOff >> 4);
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k)
+          umma_e4m3(tmem + C::kOCol, ad + (uint64_t)((k * 32 * 128) >> 4), bd + 2 * k, id_o, k != 0);
+        umma_commit(&v_empty[st]);
+        umma_commit(o_full);
+      }
+      // whatever was issued has finished before tensor memory is given back (after an abort too)
+      umma_commit(done);
+      mbar_wait_bounded(done, 0, abort_flag, kAttnTimeoutNs, c.status, false);
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // ------------------------------------------------------------ queries
+    uint32_t n = 0;
+    while (walk.next(g)) {
+      const int qb = (int)(n % C::kQBufs), rows = g.s.t1 - g.s.t0, cols = min(NC, rows * G);
+      uint2 raw[NC];
+#pragma unroll
+      for (int x = 0; x < NC; ++x) {
+        raw[x] = make_uint2(0, 0);
+        if (x < cols) {
+          const int i = x / G;
+          raw[x] = __ldg(reinterpret_cast<const uint2*>(a.q + (size_t)(g.s.t0 + i) * a.q_stride +
+                                                       (size_t)(g.h * G + x - i * G) * kHeadDim) + lane);
+        }
+      }
+      if (!warp_wait(&q_empty[qb], ((n / C::kQBufs) & 1u) ^ 1u, abort_flag, c.status)) break;
+      uint8_t* op = smem + C::kQOff + qb * C::kOpBytes;
+#pragma unroll
+      for (int x = 0; x < NC; ++x) {
+        const float v[4] = {bf16_lo(raw[x].x), bf16_hi(raw[x].x), bf16_lo(raw[x].y), bf16_hi(raw[x].y)};
+        float top = 0.f;
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float m = fabsf(v[e]);
+          bad |= !(m <= 3.402823466e38f);
+          top = fmaxf(top, m);
+        }
+        top = warp_max(top);
+        bad = __any_sync(0xffffffffu, bad);
+        const int e = bad ? 0 : query_exponent(top);
+        const float inv = exp2_int(-e);
+        uint32_t h0, l0, h1, l1;
+        split_e4m3x2(v[0] * inv, v[1] * inv, h0, l0);
+        split_e4m3x2(v[2] * inv, v[3] * inv, h1, l1);
+        uint32_t hi = h0 | (h1 << 16), lo = l0 | (l1 << 16);
+        if (bad) hi = lo = 0x7F7F7F7Fu;  // a row with an infinity or NaN has NaN scores
+        const uint32_t sw = ((((uint32_t)lane >> 2) ^ (x & 7)) << 4) + (lane & 3) * 4;
+        *reinterpret_cast<uint32_t*>(op + x * 128 + sw) = hi;
+        *reinterpret_cast<uint32_t*>(op + (NC + x) * 128 + sw) = lo;
+        if (lane == 0) {
+          s_qf[qb * NC + x] = a.scale_log2 * exp2_int(e);
+          s_tok[qb * NC + x] = x < cols ? x / G : 0;
+        }
+      }
+      if (rows * G > NC && lane == 0) set_status(c.status, DEV_ERR_CONFIG);  // more new tokens than max_q
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[qb]);
+      ++n;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax: thread = key of the tile, and output dim
+    uint32_t n = 0, segs = 0;
+    bool ok = true;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    float r[NC], l[NC], acc[NC];
+    while (walk.next(g)) {
+      const int qb = (int)(segs % C::kQBufs);
+      const float* qf = s_qf + qb * NC;
+      const int* tok = s_tok + qb * NC;
+      const int32_t* row = c.page_table + (size_t)g.b * c.max_pages;
+      const int first = g.s.first(), rows = g.s.t1 - g.s.t0;
+      const int last = a.causal ? first + rows : g.r.hi;         // one past the last visible key of any row
+      const int all_lo = a.window > 0 ? max(0, first + rows - a.window) : 0;  // keys [all_lo, all_hi) are seen by
+      const int all_hi = a.causal ? first + 1 : g.r.hi;                     // every row
+#pragma unroll
+      for (int x = 0; x < NC; ++x) {
+        r[x] = -CUDART_INF_F;
+        l[x] = acc[x] = 0.f;
+      }
+      auto page_at = [&](int i) {
+        const int j = (g.r.tile0 + i) * kTile + tid;
+        const int p = i < g.i1 && j >= g.r.lo && j < g.r.hi ? __ldg(row + (j >> c.page_log2)) : -1;
+        return p < c.n_pages ? p : -1;
+      };
+      auto scales_at = [&](int p) {  // key scale | value scale << 8
+        if (p < 0) return 127u | 127u << 8;
+        const size_t u = (size_t)p * c.Hkv + g.h;
+        return (uint32_t)__ldg(c.k_scale + u) | (uint32_t)__ldg(c.v_scale + u) << 8;
+      };
+      int pg = page_at(g.i0), pg1 = page_at(g.i0 + 1);
+      uint32_t sc = scales_at(pg);
+      bool first_tile = true;
+      for (int i = g.i0; i < g.i1; ++i, ++n) {
+        const int pg2 = page_at(i + 2);
+        const uint32_t sc1 = scales_at(pg1);
+        const int j0 = (g.r.tile0 + i) * kTile, j = j0 + tid;
+        const bool there = pg >= 0 && j < last;
+        if (j >= g.r.lo && j < g.r.hi && pg < 0) set_status(c.status, DEV_ERR_BOUNDS);
+        const float ks = exp2_byte(sc & 255u);
+        const float lv = (float)((int)(sc >> 8) - 127);
+        if (first_tile) ok = ok && warp_wait(&q_full[qb], (segs / C::kQBufs) & 1u, abort_flag, c.status);
+        first_tile = false;
+        ok = ok && warp_wait(&s_full[n & 1u], (n >> 1) & 1u, abort_flag, c.status);
+        float u[NC];
+        if (ok) {
+          tc_fence_after();
+          const uint32_t at = tmem + lanes + (n & 1u) * C::kRows;
+#pragma unroll
+          for (int x = 0; x < NC; ++x) u[x] = 0.f;
+          add_product<NC>(at, u);
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&s_empty[n & 1u]);
+        const bool whole = j0 >= all_lo && j0 + kTile <= all_hi;
+#pragma unroll
+        for (int x = 0; x < NC; ++x) {
+          u[x] = fmaf(u[x] * ks, qf[x], lv);
+          bool see = there;
+          if (!whole) {
+            const int pos = first + tok[x];
+            see = see && (!a.causal || j <= pos) && (a.window == 0 || j > pos - a.window);
+          }
+          if (!see) u[x] = -CUDART_INF_F;
+          const float top = warp_max(u[x]);
+          if (lane == 0) s_max[x * 4 + warp] = top;
+        }
+        if (lane == 0 && !ok) s_bad[warp] = 1;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        // all four softmax warps leave together, so that none waits at the barrier for another that gave up
+        if (s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3]) {
+          ok = false;
+          break;
+        }
+        if (i > g.i0) {
+          ok = warp_wait(o_full, (n - 1u) & 1u, abort_flag, c.status);
+          tc_fence_after();
+        }
+        // the weighted sum of the tile before: this thread's dim of every column
+        if (ok && i > g.i0) {
+          add_product<NC>(tmem + lanes + C::kOCol, acc);
+          tc_fence_before();
+        }
+        const float un = ex2(-lv);
+        uint8_t* pw = smem + C::kPOff + (tid & 15);
+        const uint32_t chunk = (uint32_t)tid >> 4;
+#pragma unroll
+        for (int x = 0; x < NC; x += 2) {
+          float p[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float4 m = *reinterpret_cast<const float4*>(s_max + (x + y) * 4);
+            const float top = fmaxf(r[x + y], fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
+            const float ref = top == -CUDART_INF_F ? 0.f : top;
+            const float f = ex2(r[x + y] - ref);
+            r[x + y] = top;
+            p[y] = ex2(u[x + y] - ref + 8.f);
+            l[x + y] = fmaf(l[x + y], f, p[y] * un);
+            acc[x + y] *= f;
+          }
+          uint32_t hi, lo;
+          split_e4m3x2(p[0], p[1], hi, lo);
+          uint8_t* p0 = pw + x * 128 + ((chunk ^ (x & 7)) << 4);
+          uint8_t* p1 = pw + (x + 1) * 128 + ((chunk ^ ((x + 1) & 7)) << 4);
+          p0[0] = (uint8_t)hi;
+          p1[0] = (uint8_t)(hi >> 8);
+          p0[NC * 128] = (uint8_t)lo;
+          p1[NC * 128] = (uint8_t)(lo >> 8);
+        }
+        // A key that no row sees has weight 0, but its value bytes may be anything: 0 * NaN.  They become zeros.
+        const bool gone = !there || j < g.r.lo;
+        if (ok && __any_sync(0xffffffffu, gone)) {
+          const int st = (int)(n % C::kStages);
+          ok = warp_wait(&v_full[st], (n / C::kStages) & 1u, abort_flag, c.status);
+          if (ok && gone) {
+            uint4* vr = reinterpret_cast<uint4*>(smem + st * 2 * kTileBytes + kTileBytes + tid * 128);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) vr[x] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(p_full);
+        pg = pg1;
+        pg1 = pg2;
+        sc = sc1;
+        // the maxima are read by all before the next tile's are written
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      }
+      if (ok) {
+        ok = warp_wait(o_full, (n - 1u) & 1u, abort_flag, c.status);
+        tc_fence_after();
+      }
+      if (ok) {
+        add_product<NC>(tmem + lanes + C::kOCol, acc);
+        tc_fence_before();
+      }
+      // the denominators: over the warp, then over the four warps
+#pragma unroll
+      for (int x = 0; x < NC; ++x) {
+        float t = l[x];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (lane == 0) s_max[x * 4 + warp] = t;
+      }
+      if (lane == 0) {
+        if (!ok) s_bad[warp] = 1;
+        if (ok) mbar_arrive(&q_empty[qb]);
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3]) break;
+      const bool complete = g.i0 == 0 && g.i1 == g.r.nt;
+      const int slot = slot0 + (g.i0 == 0 && !complete && segs > 0 ? 1 : 0);
+      const int cols = min(NC, rows * G);
+#pragma unroll
+      for (int x = 0; x < NC; ++x) {
+        const float4 m = *reinterpret_cast<const float4*>(s_max + x * 4);
+        const float sum = (m.x + m.y) + (m.z + m.w);
+        if (x < cols) {
+          if (complete) {
+            const int i = x / G;
+            a.out[((size_t)(g.s.t0 + i) * c.Hq + g.h * G + x - i * G) * kHeadDim + tid] =
+                f32_to_bf16_rne(sum != 0.f ? acc[x] / sum : 0.f);
+          } else {
+            part_o[((size_t)slot * NC + x) * kHeadDim + tid] = acc[x];
+            if (tid == 0) part_rl[(size_t)slot * NC + x] = make_float2(r[x], sum);
+          }
+        }
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      ++segs;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Joins the parts of the rows that were split: block (sequence and head, column), thread = dim.
+template <int NC>
+__global__ void __launch_bounds__(kHeadDim)
+    attention_join_kernel(const KvBatch c, const AttentionArgs a, int blocks, const float* part_o, const float2* part_rl) {
+  __shared__ long long s_warp[4];
+  __shared__ long long s_begin;
+  pdl_wait();
+  const int b = (int)blockIdx.x / c.Hkv, h = (int)blockIdx.x - b * c.Hkv, x = (int)blockIdx.y, tid = threadIdx.x;
+  const int G = c.Hq / c.Hkv;
+  long long mine, total;
+  const long long before = scan_tiles(c, a, kHeadDim, s_warp, mine, total);
+  const int share = (c.B + kHeadDim - 1) / kHeadDim;
+  if (tid == b / share) {
+    long long at = before;
+    for (int i = tid * share; i < b; ++i) at += seq_tiles(c, a, i);
+    s_begin = at * c.Hkv;
+  }
+  __syncthreads();
+  SeqRange s;
+  if (!load_seq(c, b, s) || x >= min(NC, (s.t1 - s.t0) * G)) return;
+  const int nt = key_range(s, a).nt;
+  const long long per = tiles_per_block(total * c.Hkv, blocks);
+  const long long i0 = s_begin + (long long)h * nt, i1 = i0 + nt;
+  const long long c0 = i0 / per, c1 = (i1 - 1) / per;
+  if (c0 == c1) return;
+  // the part of block c0 is its last one (slot 1) unless its run begins with this row
+  float top = -CUDART_INF_F;
+  for (long long k = c0; k <= c1; ++k) {
+    const size_t slot = 2 * k + (k == c0 && i0 > c0 * per ? 1 : 0);
+    top = fmaxf(top, part_rl[slot * NC + x].x);
+  }
+  const float ref = top == -CUDART_INF_F ? 0.f : top;
+  float sum = 0.f, acc = 0.f;
+#pragma unroll 4
+  for (long long k = c0; k <= c1; ++k) {
+    const size_t slot = 2 * k + (k == c0 && i0 > c0 * per ? 1 : 0);
+    const float2 rl = part_rl[slot * NC + x];
+    const float f = ex2(rl.x - ref);
+    sum = fmaf(rl.y, f, sum);
+    acc = fmaf(part_o[(slot * NC + x) * kHeadDim + tid], f, acc);
+  }
+  const int i = x / G;
+  a.out[((size_t)(s.t0 + i) * c.Hq + h * G + x - i * G) * kHeadDim + tid] =
+      f32_to_bf16_rne(sum != 0.f ? acc / sum : 0.f);
+}
+
+// The columns' width that holds `cols` of them; 0: too many.
+int width_of(int cols) { return cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 32 ? 32 : 0; }
+
+int blocks_of(int nc, int n_sms) { return n_sms * (nc == 32 ? 1 : 2); }
+
+template <int NC>
+cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
+  using C = Cfg<NC>;
+  CUtensorMap tk, tv;
+  if (!make_cache_map(&tk, c.k_codes, c) || !make_cache_map(&tv, c.v_codes, c)) return cudaErrorInvalidValue;
+  auto kern = attention_decode_kernel<NC>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  if (e != cudaSuccess) return e;
+  // Rows of a few tiles at most (the table's width bounds them) are one block's each: nothing to join.
+  const bool split = (long long)c.max_pages * c.page > kWholeTiles * kTile;
+  const int blocks = split ? blocks_of(NC, n_sms) : c.B * c.Hkv;
+  float* part_o = reinterpret_cast<float*>(a.scratch);
+  float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)2 * blocks_of(NC, n_sms) * NC * kHeadDim);
+  e = launch_kernel(kern, dim3(blocks), dim3(kThreads), C::kBytes, stream, false, tk, tv, c, a, (int)split, part_o,
+                    part_rl);
+  if (e != cudaSuccess || !split) return e;
+  return launch_kernel(attention_join_kernel<NC>, dim3(c.B * c.Hkv, min(NC, a.max_q * (c.Hq / c.Hkv))), dim3(kHeadDim),
+                       0, stream, true, c, a, blocks, part_o, part_rl);
+}
+
+}  // namespace
+
+bool attention_decode_fits(int G, int max_q) { return (long long)G * max_q <= 32; }
+
+size_t attention_decode_scratch(int G, int max_q, int n_sms) {
+  const int nc = width_of(G * max_q);
+  return (size_t)2 * blocks_of(nc, n_sms) * nc * (kHeadDim * sizeof(float) + sizeof(float2));
+}
+
+cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
+  switch (width_of(c.Hq / c.Hkv * a.max_q)) {
+    case 8: return launch<8>(c, a, n_sms, stream);
+    case 16: return launch<16>(c, a, n_sms, stream);
+    default: return launch<32>(c, a, n_sms, stream);
+  }
+}
+
+}  // namespace moe

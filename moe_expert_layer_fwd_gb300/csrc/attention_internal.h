@@ -1,6 +1,7 @@
 // Launchers and shared arguments of the attention operators (paged 8-bit key/value cache).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -52,5 +53,14 @@ struct AttentionArgs {
 };
 size_t attention_scratch_bytes(int T, int B, int Hq, int Hkv, int max_q, int n_sms);
 cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
+
+
+// Few query rows per key/value head: G grouped heads times max_q new tokens at most 32.
+bool attention_decode_fits(int G, int max_q);
+size_t attention_decode_scratch(int G, int max_q, int n_sms);
+cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
+
+// The codes as a matrix of 128-byte rows (one token of one head each), boxes of one page with the 128-byte swizzle.
+bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c);
 
 }  // namespace moe

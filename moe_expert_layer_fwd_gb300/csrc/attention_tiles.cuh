@@ -1,0 +1,88 @@
+// What the attention kernels share: key tiles of 128 tokens, their distribution over blocks, tensor-core
+// descriptors for E4M3 operands and the joining of split rows.
+#pragma once
+
+#include "attention_common.cuh"
+
+#include <math_constants.h>
+
+namespace moe {
+
+constexpr int kTile = 128;                        // keys per tile
+constexpr int kTileBytes = kTile * kHeadDim;      // E4M3 codes of one head's keys (or values) of a tile: 16 KB
+constexpr unsigned long long kAttnTimeoutNs = 2000000000ull;
+
+// The keys that any new token of a sequence sees: [lo, hi), in tiles [tile0, tile0 + nt).  A sequence with new
+// tokens has at least one tile, so that its rows are written even when they see nothing.
+struct KeyRange {
+  int lo, hi, tile0, nt;
+};
+__device__ __forceinline__ KeyRange key_range(const SeqRange& s, const AttentionArgs& a) {
+  KeyRange r;
+  r.hi = s.len;
+  r.lo = a.window > 0 ? max(0, s.first() - a.window + 1) : 0;
+  r.tile0 = r.lo / kTile;
+  r.nt = s.t1 > s.t0 ? max(1, (r.hi + kTile - 1) / kTile - r.tile0) : 0;
+  return r;
+}
+
+// ---------------------------------------------------------------- tcgen05 with E4M3 operands
+// Instruction descriptor of kind::f8f6f4, E4M3 A and B, fp32 accumulator; a_mn: A stored with M contiguous.
+__device__ __forceinline__ uint32_t umma_idesc_e4m3(int M, int N, bool a_mn) {
+  uint32_t d = 0;
+  d |= 1u << 4;                    // D format: f32 (A and B format 0: E4M3)
+  d |= (a_mn ? 1u : 0u) << 15;     // A major: M
+  d |= (uint32_t)(N >> 3) << 17;
+  d |= (uint32_t)(M >> 4) << 24;
+  return d;
+}
+
+__device__ __forceinline__ void umma_e4m3(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8_async(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 2^x (ex2.approx: 2 ulp; subnormal results are zero).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 2^(s - 127) of a scale byte (255 reads as 254; 0, which no append writes, as 0).
+__device__ __forceinline__ float exp2_byte(uint32_t s) { return __int_as_float((int)min(s, 254u) << 23); }
+
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A query row in E4M3 twice over: q * 2^-e = hi + lo with hi the nearest E4M3 value and lo the rest's, e chosen so that
+// the row's largest element lies in [128, 256).  bf16 has 8 significant bits and an E4M3 value 4: the rest of a
+// rounding to 4 bits fits 4 bits again, so the sum is exact for every element above 2^-9 of the row's largest and
+// within 2^-17 of that one below.  hi . k + lo . k then takes E4M3 keys as they lie in the cache.
+__device__ __forceinline__ int query_exponent(float amax) {
+  const int e = (int)(__float_as_uint(amax) >> 23) - 127 - 7;
+  return amax > 0.f ? max(e, -100) : 0;
+}
+__device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = e4m3x2(a, b);
+  const float2 h = e4m3x2_f32(hi);
+  lo = e4m3x2(a - h.x, b - h.y);
+}
+
+}  // namespace moe
