@@ -20,13 +20,13 @@
 // is finished there; otherwise the parts (sum, maximum, denominator) go to the workspace and a second kernel joins them in a
 // fixed order.  The host knows none of the lengths.
 //
-// Warps: 0-3 softmax (thread = key = dim), 4 TMA, 5 MMA, 6 queries.  Every wait is bounded (2 s).
+// Warps: 8 or 16 softmax warps (four for each group of 4 or 8 columns), then TMA, MMA, queries.  Every wait is
+// bounded (2 s).
 #include "attention_tiles.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 224;
 constexpr int kWholeTiles = 4;    // rows of at most so many tiles are not split
 constexpr int kMinRun = 2;        // tiles in a block's run, at least
 
@@ -34,19 +34,26 @@ template <int NC>
 struct Cfg {
   static constexpr int kPerSm = NC == 32 ? 1 : 2;
   static constexpr int kStages = NC == 32 ? 5 : 3;
-  static constexpr int kQBufs = 2;  // the next segment's scores start before this one has ended
+  static constexpr int kQBufs = 2;                          // the next segment's scores start before this one has ended
+  static constexpr int kCols = NC == 8 ? 4 : 8;             // columns of a softmax thread
+  static constexpr int kGroups = NC / kCols;                // groups of four softmax warps, each with its columns
+  static constexpr int kSoftWarps = 4 * kGroups;
+  static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kQWarp = kSoftWarps + 2;
+  static constexpr int kThreads = 32 * (kSoftWarps + 3);
   static constexpr int kRows = 2 * NC;                      // hi and lo rows of the queries, of the weights
-  static constexpr int kOpBytes = kRows * 128;
+  static constexpr int kQBytes = kRows * 128;
+  static constexpr int kPBlock = kTile * 16;                // the weights of 16 columns: 16 bytes a key
   static constexpr int kPOff = kStages * 2 * kTileBytes;
-  static constexpr int kQOff = kPOff + kOpBytes;
-  static constexpr int kBarOff = kQOff + kQBufs * kOpBytes;
+  static constexpr int kQOff = kPOff + kRows / 16 * kPBlock;
+  static constexpr int kBarOff = kQOff + kQBufs * kQBytes;
   static constexpr int kNumBars = 4 * kStages + 2 * kQBufs + 7;
   static constexpr int kQfOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // float qf[kQBufs][NC], int token[kQBufs][NC]
-  static constexpr int kMaxOff = kQfOff + kQBufs * NC * 8;  // float [NC][4]: per-warp maxima (and sums)
-  static constexpr int kMiscOff = kMaxOff + NC * 16;
+  static constexpr int kMaxOff = kQfOff + kQBufs * NC * 8;  // float [3][NC][4]: maxima of even, odd tiles; denominators
+  static constexpr int kMiscOff = kMaxOff + 3 * NC * 16;
   static constexpr int kBytes = 1024 + kMiscOff + 64;
   static constexpr int kTmemCols = 3 * kRows <= 64 ? 64 : (3 * kRows <= 128 ? 128 : 256);  // S twice, O
   static constexpr int kOCol = 2 * kRows;
+  static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
 
 // A run of tiles of one (sequence, head): the tiles [i0, i1) of its nt.
@@ -131,22 +138,24 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, kAttnTimeoutNs, status));
 }
 
-// acc[x] += column x + column NC + x of this thread's tensor-memory lane.
-template <int NC>
-__device__ __forceinline__ void add_product(uint32_t taddr, float (&acc)[NC]) {
-#pragma unroll
-  for (int y = 0; y < NC; y += 8) {
-    uint32_t s[8], t[8];
-    tmem_ld8_async(taddr + y, s);
-    tmem_ld8_async(taddr + NC + y, t);
-    tmem_wait_ld();
-#pragma unroll
-    for (int x = 0; x < 8; ++x) acc[y + x] += __uint_as_float(s[x]) + __uint_as_float(t[x]);
+// acc[x] += column x + column `lo` + x of this thread's tensor-memory lane.
+template <int N>
+__device__ __forceinline__ void add_product(uint32_t taddr, int lo, float (&acc)[N]) {
+  uint32_t s[N], t[N];
+  if constexpr (N == 4) {
+    tmem_ld4_async(taddr, s);
+    tmem_ld4_async(taddr + lo, t);
+  } else {
+    tmem_ld8_async(taddr, s);
+    tmem_ld8_async(taddr + lo, t);
   }
+  tmem_wait_ld();
+#pragma unroll
+  for (int x = 0; x < N; ++x) acc[x] += __uint_as_float(s[x]) + __uint_as_float(t[x]);
 }
 
 template <int NC>
-__global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
+__global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     attention_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const KvBatch c, const AttentionArgs a, int split, float* part_o, float2* part_rl) {
   using C = Cfg<NC>;
@@ -169,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
   int* s_begin = reinterpret_cast<int*>(smem + C::kMiscOff + 8);  // b, h, tile
-  volatile int* s_bad = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 24);  // [4] a softmax warp gave up
+  volatile int* s_bad = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 24);  // [3] a softmax warp gave up (as s_max)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = c.Hq / c.Hkv;
@@ -182,14 +191,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
     long long mine, total;
     // the scan's scratch is the weights' operand, free until the roles start
     long long* s_warp = reinterpret_cast<long long*>(smem + C::kPOff);
-    const long long before = scan_tiles(c, a, kThreads, s_warp, mine, total);
+    const long long before = scan_tiles(c, a, C::kThreads, s_warp, mine, total);
     const long long all = total * c.Hkv, per = tiles_per_block(all, gridDim.x);
     const long long begin = (long long)blockIdx.x * per;
     run = min(per, all - begin);
     if (run <= 0) return;
     if (before * c.Hkv <= begin && begin < (before + mine) * c.Hkv) {
       long long at = before;
-      int b = tid * ((c.B + kThreads - 1) / kThreads), nt;
+      int b = tid * ((c.B + C::kThreads - 1) / C::kThreads), nt;
       while ((at + (nt = seq_tiles(c, a, b))) * c.Hkv <= begin) {
         at += nt;
         ++b;
@@ -219,20 +228,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
     }
     for (int i = 0; i < C::kQBufs; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 5);  // the last QK product of a segment, and the four softmax warps
+      mbar_init(&q_empty[i], 1 + C::kSoftWarps);  // the last QK product of a segment, and the softmax warps
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
+      mbar_init(&s_empty[i], C::kSoftWarps);
     }
-    mbar_init(p_full, 4);
+    mbar_init(p_full, C::kSoftWarps);
     mbar_init(o_full, 1);
     mbar_init(done, 1);
     *abort_flag = 0;
-    for (int i = 0; i < 4; ++i) s_bad[i] = 0;
+    for (int i = 0; i < 3; ++i) s_bad[i] = 0;
     fence_mbar_init();
   }
-  if (warp == 5) tmem_alloc(tmem_slot, C::kTmemCols);
+  if (warp == C::kMmaWarp) tmem_alloc(tmem_slot, C::kTmemCols);
+  if (tid == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -240,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
   Walk walk(c, a, run, s_begin[0], s_begin[1], s_begin[2]);
   Segment g;
 
-  if (warp == 4) {
+  if (warp == C::kTmaWarp) {
     // ------------------------------------------------------------ TMA: lane = page of the tile
     const uint64_t pol = policy_evict_first();
     const int pages = kTile >> c.page_log2;
@@ -289,10 +302,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
       }
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMA: scores run one tile ahead of the weighted sums
     if (lane == 0) {
-      const uint32_t id_s = umma_idesc_e4m3(kTile, C::kRows, false), id_o = umma_idesc_e4m3(kHeadDim, C::kRows, true);
+      const uint32_t id_s = umma_idesc_e4m3(kTile, C::kRows, false, false),
+                     id_o = umma_idesc_e4m3(kHeadDim, C::kRows, true, true);
       const uint64_t desc = umma_desc_sw128(smem_u32(smem));
       uint32_t nq = 0, segs = 0;
       bool ok = true, more = walk.next(g);
@@ -306,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
         if (!ok) return;
         tc_fence_after();
         const uint64_t ad = desc + (uint64_t)((st * 2 * kTileBytes) >> 4);
-        const uint64_t bd = desc + (uint64_t)((C::kQOff + qb * C::kOpBytes) >> 4);
+        const uint64_t bd = desc + (uint64_t)((C::kQOff + qb * C::kQBytes) >> 4);
 #pragma unroll
         for (int k = 0; k < kHeadDim / 32; ++k)
           umma_e4m3(tmem + sb * C::kRows, ad + 2 * k, bd + 2 * k, id_s, k != 0);
@@ -330,10 +344,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
         tc_fence_after();
         // V[token][dim]: the 128-byte rows are the K index, eight rows (1 KB) to a swizzle atom, 32 tokens an MMA
         const uint64_t ad = desc + (uint64_t)((st * 2 * kTileBytes + kTileBytes) >> 4);
-        const uint64_t bd = desc + (uint64_t)(C::kPOff >> 4);
+        const uint64_t bd = umma_desc_mn16(smem_u32(smem) + C::kPOff, C::kPBlock);
 #pragma unroll
         for (int k = 0; k < kTile / 32; ++k)
-          umma_e4m3(tmem + C::kOCol, ad + (uint64_t)((k * 32 * 128) >> 4), bd + 2 * k, id_o, k != 0);
+          umma_e4m3(tmem + C::kOCol, ad + (uint64_t)((k * 32 * 128) >> 4), bd + (uint64_t)((k * 32 * 16) >> 4), id_o, k != 0);
         umma_commit(&v_empty[st]);
         umma_commit(o_full);
       }
@@ -342,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
       mbar_wait_bounded(done, 0, abort_flag, kAttnTimeoutNs, c.status, false);
     }
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == C::kQWarp) {
     // ------------------------------------------------------------ queries
     uint32_t n = 0;
     while (walk.next(g)) {
@@ -358,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
         }
       }
       if (!warp_wait(&q_empty[qb], ((n / C::kQBufs) & 1u) ^ 1u, abort_flag, c.status)) break;
-      uint8_t* op = smem + C::kQOff + qb * C::kOpBytes;
+      uint8_t* op = smem + C::kQOff + qb * C::kQBytes;
 #pragma unroll
       for (int x = 0; x < NC; ++x) {
         const float v[4] = {bf16_lo(raw[x].x), bf16_hi(raw[x].x), bf16_lo(raw[x].y), bf16_hi(raw[x].y)};
@@ -394,27 +408,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
       ++n;
     }
   } else {
-    // ------------------------------------------------------------ softmax: thread = key of the tile, and output dim
+    // ------------------------------------------------------------ softmax: thread = key of the tile and output dim
+    constexpr int N = C::kCols;
+    const int group = warp >> 2, w4 = warp & 3, key = tid & 127, col0 = group * N;
     uint32_t n = 0, segs = 0;
     bool ok = true;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    float r[NC], l[NC], acc[NC];
+    const uint32_t mine = tmem + ((uint32_t)(w4 * 32) << 16) + col0;  // this thread's lane and columns
+    auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };
+    float r[N], l[N], acc[N];
     while (walk.next(g)) {
       const int qb = (int)(segs % C::kQBufs);
-      const float* qf = s_qf + qb * NC;
-      const int* tok = s_tok + qb * NC;
+      const float* qf = s_qf + qb * NC + col0;
+      const int* tok = s_tok + qb * NC + col0;
       const int32_t* row = c.page_table + (size_t)g.b * c.max_pages;
       const int first = g.s.first(), rows = g.s.t1 - g.s.t0;
       const int last = a.causal ? first + rows : g.r.hi;         // one past the last visible key of any row
       const int all_lo = a.window > 0 ? max(0, first + rows - a.window) : 0;  // keys [all_lo, all_hi) are seen by
       const int all_hi = a.causal ? first + 1 : g.r.hi;                     // every row
 #pragma unroll
-      for (int x = 0; x < NC; ++x) {
+      for (int x = 0; x < N; ++x) {
         r[x] = -CUDART_INF_F;
         l[x] = acc[x] = 0.f;
       }
       auto page_at = [&](int i) {
-        const int j = (g.r.tile0 + i) * kTile + tid;
+        const int j = (g.r.tile0 + i) * kTile + key;
         const int p = i < g.i1 && j >= g.r.lo && j < g.r.hi ? __ldg(row + (j >> c.page_log2)) : -1;
         return p < c.n_pages ? p : -1;
       };
@@ -425,32 +442,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
       };
       int pg = page_at(g.i0), pg1 = page_at(g.i0 + 1);
       uint32_t sc = scales_at(pg);
-      bool first_tile = true;
+      ok = ok && warp_wait(&q_full[qb], (segs / C::kQBufs) & 1u, abort_flag, c.status);
       for (int i = g.i0; i < g.i1; ++i, ++n) {
         const int pg2 = page_at(i + 2);
         const uint32_t sc1 = scales_at(pg1);
-        const int j0 = (g.r.tile0 + i) * kTile, j = j0 + tid;
+        const int j0 = (g.r.tile0 + i) * kTile, j = j0 + key;
         const bool there = pg >= 0 && j < last;
         if (j >= g.r.lo && j < g.r.hi && pg < 0) set_status(c.status, DEV_ERR_BOUNDS);
         const float ks = exp2_byte(sc & 255u);
         const float lv = (float)((int)(sc >> 8) - 127);
-        if (first_tile) ok = ok && warp_wait(&q_full[qb], (segs / C::kQBufs) & 1u, abort_flag, c.status);
-        first_tile = false;
         ok = ok && warp_wait(&s_full[n & 1u], (n >> 1) & 1u, abort_flag, c.status);
-        float u[NC];
+        float u[N];
+#pragma unroll
+        for (int x = 0; x < N; ++x) u[x] = 0.f;
         if (ok) {
           tc_fence_after();
-          const uint32_t at = tmem + lanes + (n & 1u) * C::kRows;
-#pragma unroll
-          for (int x = 0; x < NC; ++x) u[x] = 0.f;
-          add_product<NC>(at, u);
+          add_product<N>(mine + (n & 1u) * C::kRows, NC, u);
           tc_fence_before();
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&s_empty[n & 1u]);
+        float* tops = s_max + (n & 1u) * NC * 4 + col0 * 4;
         const bool whole = j0 >= all_lo && j0 + kTile <= all_hi;
 #pragma unroll
-        for (int x = 0; x < NC; ++x) {
+        for (int x = 0; x < N; ++x) {
           u[x] = fmaf(u[x] * ks, qf[x], lv);
           bool see = there;
           if (!whole) {
@@ -459,57 +474,72 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
           }
           if (!see) u[x] = -CUDART_INF_F;
           const float top = warp_max(u[x]);
-          if (lane == 0) s_max[x * 4 + warp] = top;
+          if (lane == 0) tops[x * 4 + w4] = top;
         }
-        if (lane == 0 && !ok) s_bad[warp] = 1;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        // all four softmax warps leave together, so that none waits at the barrier for another that gave up
-        if (s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3]) {
+        if (lane == 0 && !ok) s_bad[n & 1u] = 1;
+        group_sync();
+        // the warps of a group leave together, so that none waits at the barrier for one that gave up
+        if (s_bad[n & 1u]) {
           ok = false;
           break;
         }
+        // the weighted sum of the tile before: this thread's dim of its columns
         if (i > g.i0) {
           ok = warp_wait(o_full, (n - 1u) & 1u, abort_flag, c.status);
-          tc_fence_after();
-        }
-        // the weighted sum of the tile before: this thread's dim of every column
-        if (ok && i > g.i0) {
-          add_product<NC>(tmem + lanes + C::kOCol, acc);
-          tc_fence_before();
+          if (ok) {
+            tc_fence_after();
+            add_product<N>(mine + C::kOCol, NC, acc);
+            tc_fence_before();
+          }
         }
         const float un = ex2(-lv);
-        uint8_t* pw = smem + C::kPOff + (tid & 15);
-        const uint32_t chunk = (uint32_t)tid >> 4;
+        float top[N];
+        bool moved = false;
 #pragma unroll
-        for (int x = 0; x < NC; x += 2) {
-          float p[2];
+        for (int x = 0; x < N; ++x) {
+          const float4 m = *reinterpret_cast<const float4*>(tops + x * 4);
+          top[x] = fmaxf(r[x], fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
+          moved |= top[x] != r[x];
+        }
+        if (moved) {  // the same for the whole group
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float4 m = *reinterpret_cast<const float4*>(s_max + (x + y) * 4);
-            const float top = fmaxf(r[x + y], fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
-            const float ref = top == -CUDART_INF_F ? 0.f : top;
-            const float f = ex2(r[x + y] - ref);
-            r[x + y] = top;
-            p[y] = ex2(u[x + y] - ref + 8.f);
-            l[x + y] = fmaf(l[x + y], f, p[y] * un);
-            acc[x + y] *= f;
+          for (int x = 0; x < N; ++x) {
+            const float f = top[x] == -CUDART_INF_F ? 0.f : ex2(r[x] - top[x]);
+            l[x] *= f;
+            acc[x] *= f;
+            r[x] = top[x];
           }
-          uint32_t hi, lo;
-          split_e4m3x2(p[0], p[1], hi, lo);
-          uint8_t* p0 = pw + x * 128 + ((chunk ^ (x & 7)) << 4);
-          uint8_t* p1 = pw + (x + 1) * 128 + ((chunk ^ ((x + 1) & 7)) << 4);
-          p0[0] = (uint8_t)hi;
-          p1[0] = (uint8_t)(hi >> 8);
-          p0[NC * 128] = (uint8_t)lo;
-          p1[NC * 128] = (uint8_t)(lo >> 8);
+        }
+        uint32_t hi[N / 4], lo[N / 4];
+#pragma unroll
+        for (int x = 0; x < N; x += 4) {
+          float p[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            p[y] = ex2(u[x + y] - (r[x + y] == -CUDART_INF_F ? 0.f : r[x + y]) + 8.f);
+            l[x + y] = fmaf(p[y], un, l[x + y]);
+          }
+          uint32_t h0, l0, h1, l1;
+          split_e4m3x2(p[0], p[1], h0, l0);
+          split_e4m3x2(p[2], p[3], h1, l1);
+          hi[x / 4] = h0 | h1 << 16;
+          lo[x / 4] = l0 | l1 << 16;
+        }
+        // 16 columns to a block of 16 bytes a key: the hi parts of all columns, then the lo parts
+        uint8_t* pw = smem + C::kPOff + key * 16;
+#pragma unroll
+        for (int x = 0; x < N / 4; ++x) {
+          const int at = col0 + 4 * x;
+          *reinterpret_cast<uint32_t*>(pw + at / 16 * C::kPBlock + at % 16) = hi[x];
+          *reinterpret_cast<uint32_t*>(pw + (NC + at) / 16 * C::kPBlock + (NC + at) % 16) = lo[x];
         }
         // A key that no row sees has weight 0, but its value bytes may be anything: 0 * NaN.  They become zeros.
         const bool gone = !there || j < g.r.lo;
-        if (ok && __any_sync(0xffffffffu, gone)) {
+        if (group == 0 && ok && __any_sync(0xffffffffu, gone)) {
           const int st = (int)(n % C::kStages);
           ok = warp_wait(&v_full[st], (n / C::kStages) & 1u, abort_flag, c.status);
           if (ok && gone) {
-            uint4* vr = reinterpret_cast<uint4*>(smem + st * 2 * kTileBytes + kTileBytes + tid * 128);
+            uint4* vr = reinterpret_cast<uint4*>(smem + st * 2 * kTileBytes + kTileBytes + key * 128);
 #pragma unroll
             for (int x = 0; x < 8; ++x) vr[x] = make_uint4(0, 0, 0, 0);
           }
@@ -520,56 +550,53 @@ __global__ void __launch_bounds__(kThreads, Cfg<NC>::kPerSm)
         pg = pg1;
         pg1 = pg2;
         sc = sc1;
-        // the maxima are read by all before the next tile's are written
-        asm volatile("bar.sync 1, 128;" ::: "memory");
       }
+      if (ok) ok = warp_wait(o_full, (n - 1u) & 1u, abort_flag, c.status);
       if (ok) {
-        ok = warp_wait(o_full, (n - 1u) & 1u, abort_flag, c.status);
         tc_fence_after();
-      }
-      if (ok) {
-        add_product<NC>(tmem + lanes + C::kOCol, acc);
+        add_product<N>(mine + C::kOCol, NC, acc);
         tc_fence_before();
       }
-      // the denominators: over the warp, then over the four warps
+      // the denominators: over the warp, then over the group
+      float* sums = s_max + 2 * NC * 4 + col0 * 4;
 #pragma unroll
-      for (int x = 0; x < NC; ++x) {
+      for (int x = 0; x < N; ++x) {
         float t = l[x];
 #pragma unroll
         for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        if (lane == 0) s_max[x * 4 + warp] = t;
+        if (lane == 0) sums[x * 4 + w4] = t;
       }
       if (lane == 0) {
-        if (!ok) s_bad[warp] = 1;
-        if (ok) mbar_arrive(&q_empty[qb]);
+        if (!ok) s_bad[2] = 1;
+        else mbar_arrive(&q_empty[qb]);
       }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3]) break;
+      group_sync();
+      if (s_bad[2]) break;
       const bool complete = g.i0 == 0 && g.i1 == g.r.nt;
-      const int slot = slot0 + (g.i0 == 0 && !complete && segs > 0 ? 1 : 0);
+      const int slot = slot0 + (g.i0 == 0 && segs > 0 ? 1 : 0);
       const int cols = min(NC, rows * G);
 #pragma unroll
-      for (int x = 0; x < NC; ++x) {
-        const float4 m = *reinterpret_cast<const float4*>(s_max + x * 4);
+      for (int x = 0; x < N; ++x) {
+        const float4 m = *reinterpret_cast<const float4*>(sums + x * 4);
         const float sum = (m.x + m.y) + (m.z + m.w);
-        if (x < cols) {
+        const int col = col0 + x;
+        if (col < cols) {
           if (complete) {
-            const int i = x / G;
-            a.out[((size_t)(g.s.t0 + i) * c.Hq + g.h * G + x - i * G) * kHeadDim + tid] =
+            const int i = col / G;
+            a.out[((size_t)(g.s.t0 + i) * c.Hq + g.h * G + col - i * G) * kHeadDim + key] =
                 f32_to_bf16_rne(sum != 0.f ? acc[x] / sum : 0.f);
           } else {
-            part_o[((size_t)slot * NC + x) * kHeadDim + tid] = acc[x];
-            if (tid == 0) part_rl[(size_t)slot * NC + x] = make_float2(r[x], sum);
+            part_o[((size_t)slot * NC + col) * kHeadDim + key] = acc[x];
+            if (key == 0) part_rl[(size_t)slot * NC + col] = make_float2(r[x], sum);
           }
         }
       }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
       ++segs;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == C::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
@@ -639,7 +666,7 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   const int blocks = split ? blocks_of(NC, n_sms) : c.B * c.Hkv;
   float* part_o = reinterpret_cast<float*>(a.scratch);
   float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)2 * blocks_of(NC, n_sms) * NC * kHeadDim);
-  e = launch_kernel(kern, dim3(blocks), dim3(kThreads), C::kBytes, stream, false, tk, tv, c, a, (int)split, part_o,
+  e = launch_kernel(kern, dim3(blocks), dim3(C::kThreads), C::kBytes, stream, false, tk, tv, c, a, (int)split, part_o,
                     part_rl);
   if (e != cudaSuccess || !split) return e;
   return launch_kernel(attention_join_kernel<NC>, dim3(c.B * c.Hkv, min(NC, a.max_q * (c.Hq / c.Hkv))), dim3(kHeadDim),

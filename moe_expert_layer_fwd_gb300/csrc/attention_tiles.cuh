@@ -27,13 +27,26 @@ __device__ __forceinline__ KeyRange key_range(const SeqRange& s, const Attention
 }
 
 // ---------------------------------------------------------------- tcgen05 with E4M3 operands
-// Instruction descriptor of kind::f8f6f4, E4M3 A and B, fp32 accumulator; a_mn: A stored with M contiguous.
-__device__ __forceinline__ uint32_t umma_idesc_e4m3(int M, int N, bool a_mn) {
+// Instruction descriptor of kind::f8f6f4, E4M3 A and B, fp32 accumulator; a_mn, b_mn: A, B stored with M, N
+// contiguous (else K).
+__device__ __forceinline__ uint32_t umma_idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
   uint32_t d = 0;
   d |= 1u << 4;                    // D format: f32 (A and B format 0: E4M3)
-  d |= (a_mn ? 1u : 0u) << 15;     // A major: M
+  d |= (a_mn ? 1u : 0u) << 15;
+  d |= (b_mn ? 1u : 0u) << 16;
   d |= (uint32_t)(N >> 3) << 17;
   d |= (uint32_t)(M >> 4) << 24;
+  return d;
+}
+
+// Descriptor of an 8-bit operand stored without swizzle, M or N contiguous: 16 bytes (16 rows of the operand) per K index,
+// eight K indexes to 128 contiguous bytes, the next eight 128 bytes on, the next 16 rows `block` bytes on.
+__device__ __forceinline__ uint64_t umma_desc_mn16(uint32_t smem_addr, uint32_t block) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(128u >> 4) << 16;   // leading byte offset: along K
+  d |= (uint64_t)(block >> 4) << 32;  // stride byte offset: along M or N
+  d |= (uint64_t)1u << 46;            // descriptor version
   return d;
 }
 
@@ -47,6 +60,11 @@ __device__ __forceinline__ void umma_e4m3(uint32_t tmem_d, uint64_t adesc, uint6
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld4_async(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld8_async(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
