@@ -21,7 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
 SOURCES = ["gating.cu", "routing.cu", "routing_static.cu", "grouped_gemm.cu", "grouped_gemm_mxfp4.cu", "grouped_gemm_w4a8.cu",
-           "finalize.cu", "frontend.cu", "api.cu", "attention_cache.cu", "attention.cu", "attention_decode.cu", "api_attention.cu"]
+           "finalize.cu", "frontend.cu", "api.cu", "attention_cache.cu", "attention.cu", "attention_decode.cu",
+           "attention_prefill.cu", "api_attention.cu"]
 HEADERS = ["moe_common.cuh", "moe_internal.h", "attention_common.cuh", "attention_tiles.cuh",
            "attention_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -128,7 +128,7 @@ int moe_kv_gather(const moe_kv_desc* d, const int32_t* start, const int32_t* out
 
 size_t moe_paged_attention_workspace_size(const moe_kv_desc* d, int max_q) {
   if (check_desc(d) || max_q < 0) return 0;
-  return kHeader + moe::attention_scratch_bytes(d->T, d->B, d->Hq, d->Hkv, max_q, sm_count());
+  return kHeader + moe::attention_scratch_bytes(d->Hq, d->Hkv, max_q, sm_count());
 }
 
 int moe_paged_attention(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const int32_t* q_start,

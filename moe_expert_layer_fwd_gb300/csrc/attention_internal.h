@@ -51,7 +51,7 @@ struct AttentionArgs {
   int causal, window, max_q;
   void* scratch;              // after the status word of the workspace
 };
-size_t attention_scratch_bytes(int T, int B, int Hq, int Hkv, int max_q, int n_sms);
+size_t attention_scratch_bytes(int Hq, int Hkv, int max_q, int n_sms);
 cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
 
 
@@ -59,6 +59,10 @@ cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int
 bool attention_decode_fits(int G, int max_q);
 size_t attention_decode_scratch(int G, int max_q, int n_sms);
 cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
+
+// Any number of rows.
+size_t attention_prefill_scratch(int n_sms);
+cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
 
 // The codes as a matrix of 128-byte rows (one token of one head each), boxes of one page with the 128-byte swizzle.
 bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c);

@@ -1,0 +1,741 @@
+// Attention of many query rows per key/value head (prompts and chunks): matrix products bound it.
+//
+// The rows of one key/value head, new tokens x grouped heads, are the M operand: an item is 256 of them, two M = 128 tiles
+// that take turns on the tensor core -- while one's softmax runs, the other's products do -- against key tiles of 128:
+//   S[128, 128 keys] = Q_hi . K^T + Q_lo . K^T     kind::f8f6f4: queries split in two E4M3 halves, keys as cached
+//   u = S * scale * 2^(e_k + e_q) + e_v            per page of the tile: a factor and a summand for its columns
+//   p' = 2^(u - r + 7) in f16,  l += 2^-e_v sum p'
+//   O[128, 128 dims] += p' . V                     kind::f16, p' in tensor memory over S, V as exact f16 numbers
+// Two products of E4M3 cost what one of bf16 does, and the keys need no conversion; the values are converted once per tile
+// for both M tiles by four warps of their own (an E4M3 code is an f16 number; their scales stay out of them).  r follows the
+// running maximum of u, and with it O is rescaled, only when that has grown by more than 2^8 since: p' then stays below
+// 2^15, and f16 keeps 11 bits of it down to 2^-21 of the largest.
+//
+// Work: the items' tiles in one order, cut into equal runs, one per block and SM, as in the decode kernel: causal items of
+// any length fill all SMs evenly, and a chunk of few rows over a long cache is split along its keys.  The rows of a split item
+// (one at each end of a run, at most) are joined by a second kernel.
+//
+// Warps (16): 0-3 and 4-7 softmax of the M tiles (thread = row; they also load its query, rescale and write its output), 8-11
+// values, 12 TMA, 13 MMA, 14 scales of the tiles' pages.  Registers: 192 a thread for the softmax, 64 for the rest.
+// Every wait is bounded (2 s).
+#include "attention_tiles.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kM = 128;
+constexpr int kItemRows = 2 * kM;
+constexpr int kKStages = 3, kVStages = 2, kInfos = 4;
+constexpr int kMinRun = 4;  // tiles in a block's run, at least
+
+constexpr int kQOff = 0;                                 // [2 tiles][hi, lo][128 rows of 128 bytes]
+constexpr int kKOff = kQOff + 4 * kTileBytes;
+constexpr int kVOff = kKOff + kKStages * kTileBytes;     // E4M3 as cached
+constexpr int kV16Off = kVOff + kVStages * kTileBytes;   // f16 [2][2 halves of the dims][128 tokens of 128 bytes]
+constexpr int kV16Bytes = 2 * kTileBytes;
+constexpr int kInfoOff = kV16Off + 2 * kV16Bytes;
+struct TileInfo {    // per 16 keys of a tile
+  float kf[8];       // 2^e_k
+  float lv[8];       // e_v
+  float un[8];       // 2^-e_v
+  uint32_t have;     // bit i: the page of keys 16 i .. 16 i + 15 is there
+  uint32_t pad[3];
+};
+constexpr int kBarOff = kInfoOff + kInfos * (int)sizeof(TileInfo);
+constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 4 + 2 * kInfos + 2 + 2 + 2 + 2 + 1;
+constexpr int kMiscOff = kBarOff + kNumBars * 8;
+constexpr int kBytes = 1024 + kMiscOff + 128;
+static_assert(kBytes <= 232448, "shared memory");
+
+// One item (rows [256 qt, 256 qt + 256) of sequence b's n * G for head h) and the part of its tiles this run has.
+struct Part {
+  int b, h, qt, i0, i1, nt, tile0, lo, hi;  // keys [lo, hi) are seen by some row
+  SeqRange s;
+};
+
+__device__ __forceinline__ void item_range(const SeqRange& s, const AttentionArgs& a, int G, int qt, int& lo, int& hi) {
+  const int i_min = qt * kItemRows / G, i_max = min(s.t1 - s.t0 - 1, (qt * kItemRows + kItemRows - 1) / G);
+  hi = a.causal ? max(0, min(s.len, s.first() + i_max + 1)) : s.len;
+  lo = a.window > 0 ? max(0, s.first() + i_min - a.window + 1) : 0;
+}
+__device__ __forceinline__ int item_tiles(int lo, int hi) { return max(1, (hi + kTile - 1) / kTile - lo / kTile); }
+
+// Sequence b's items take the places from q_start[b] * G / 256 + b on (some stay empty), so that a place's item is
+// found without a table of all of them.
+__device__ __forceinline__ int place_of(const KvBatch& c, int G, int b) {
+  return (int)((long long)__ldg(c.q_start + b) * G / kItemRows) + b;
+}
+__device__ __forceinline__ int places(const KvBatch& c, int G) { return (int)((long long)c.T * G / kItemRows) + c.B; }
+
+// Walks places in order.
+struct Places {
+  const KvBatch& c;
+  const AttentionArgs& a;
+  int G, place, b;
+  bool ok;
+  SeqRange s;
+  __device__ Places(const KvBatch& c_, const AttentionArgs& a_, int G_, int place_) : c(c_), a(a_), G(G_), place(place_) {
+    int lo = 0, hi = c.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (place_of(c, G, mid) <= place) lo = mid; else hi = mid;
+    }
+    b = lo;
+    ok = load_seq(c, b, s);
+  }
+  // tiles of the item at this place (0: empty), for one head
+  __device__ int tiles(int& qt, int& lo, int& hi) const {
+    qt = place - place_of(c, G, b);
+    if (!ok || qt < 0 || (long long)qt * kItemRows >= (long long)(s.t1 - s.t0) * G) return 0;
+    item_range(s, a, G, qt, lo, hi);
+    return item_tiles(lo, hi);
+  }
+  __device__ void next() {
+    ++place;
+    if (b + 1 < c.B && place_of(c, G, b + 1) <= place) {
+      ++b;
+      ok = load_seq(c, b, s);
+    }
+  }
+};
+
+struct Walk {
+  Places p;
+  long long left;
+  int h, i, end;
+  __device__ Walk(const KvBatch& c, const AttentionArgs& a, int G, long long n, int place, int h_, int i_)
+      : p(c, a, G, place), left(n), h(h_), i(i_), end(places(c, G)) {}
+  __device__ bool next(Part& g) {
+    while (left > 0 && p.place < end) {
+      g.nt = p.tiles(g.qt, g.lo, g.hi);
+      if (g.nt == 0) {
+        p.next();
+        h = i = 0;
+        continue;
+      }
+      g.b = p.b;
+      g.s = p.s;
+      g.h = h;
+      g.tile0 = g.lo / kTile;
+      g.i0 = i;
+      g.i1 = (int)min((long long)g.nt, i + left);
+      left -= g.i1 - i;
+      i = g.i1;
+      if (i == g.nt) {
+        i = 0;
+        if (++h == p.c.Hkv) {
+          h = 0;
+          p.next();
+        }
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, kAttnTimeoutNs, status));
+}
+
+__device__ __forceinline__ uint32_t idesc_pv() {
+  uint32_t d = 0;
+  d |= 1u << 4;                          // D f32, A and B f16
+  d |= 1u << 16;                         // B with N (the dims) contiguous
+  d |= (uint32_t)(kHeadDim >> 3) << 17;
+  d |= (uint32_t)(kM >> 4) << 24;
+  return d;
+}
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+  return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+
+// What a block tells the joining kernel about the part that its run begins with.
+struct JoinInfo {
+  int split;       // the part is not the item's first: blocks c0 .. c1 hold its parts
+  int b, h, qt;
+  int c0, c1, slot0;  // slot0: which part of block c0
+  int pad;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                             const KvBatch c, const AttentionArgs a, float* part_o, float2* part_rl, JoinInfo* info) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  TileInfo* infos = reinterpret_cast<TileInfo*>(smem + kInfoOff);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + kBarOff);
+  uint64_t* k_empty = k_full + kKStages;
+  uint64_t* v_full = k_empty + kKStages;
+  uint64_t* v_empty = v_full + kVStages;
+  uint64_t* v16_full = v_empty + kVStages;   // [2]
+  uint64_t* v16_empty = v16_full + 2;        // [2]
+  uint64_t* i_full = v16_empty + 2;
+  uint64_t* i_empty = i_full + kInfos;
+  uint64_t* q_full = i_empty + kInfos;       // [2], by M tile, as the next three
+  uint64_t* s_full = q_full + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* done = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
+  int* s_begin = reinterpret_cast<int*>(smem + kMiscOff + 8);  // place, head, tile
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = c.Hq / c.Hkv;
+  pdl_launch_dependents();
+
+  // ---- this block's run: each thread sums a run of places
+  long long run;
+  {
+    long long* s_warp = reinterpret_cast<long long*>(smem);
+    const int n = places(c, G), per = (n + kThreads - 1) / kThreads;
+    const int p0 = min(n, tid * per), p1 = min(n, p0 + per);
+    long long mine = 0;
+    int qt, lo, hi;
+    if (p0 < p1) {
+      Places p(c, a, G, p0);
+      for (; p.place < p1; p.next()) mine += p.tiles(qt, lo, hi);
+    }
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    long long before = x - mine, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += s_warp[w];
+      total += s_warp[w];
+    }
+    const long long all = total * c.Hkv, share = max((long long)kMinRun, (all + gridDim.x - 1) / (long long)gridDim.x);
+    const long long begin = (long long)blockIdx.x * share;
+    run = min(share, all - begin);
+    if (run <= 0) {
+      if (tid == 0) info[blockIdx.x].split = 0;
+      return;
+    }
+    if (before * c.Hkv <= begin && begin < (before + mine) * c.Hkv) {
+      Places p(c, a, G, p0);
+      long long at = before;
+      int nt;
+      for (;; p.next()) {
+        nt = p.tiles(qt, lo, hi);
+        if ((at + nt) * c.Hkv > begin) break;
+        at += nt;
+      }
+      const long long rel = begin - at * c.Hkv;
+      s_begin[0] = p.place;
+      s_begin[1] = (int)(rel / nt);
+      s_begin[2] = (int)(rel % nt);
+      JoinInfo j = {};
+      j.split = rel % nt != 0;
+      if (j.split) {
+        const long long i0 = begin - rel % nt, i1 = i0 + nt;
+        j.b = p.b;
+        j.h = (int)(rel / nt);
+        j.qt = qt;
+        j.c0 = (int)(i0 / share);
+        j.c1 = (int)((i1 - 1) / share);
+        j.slot0 = i0 > (long long)j.c0 * share ? 1 : 0;
+      }
+      info[blockIdx.x] = j;
+    }
+  }
+
+  if (tid == 0) {
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 4);
+    }
+    for (int i = 0; i < kInfos; ++i) {
+      mbar_init(&i_full[i], 1);
+      mbar_init(&i_empty[i], 12);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&v16_full[i], 4);
+      mbar_init(&v16_empty[i], 1);
+      mbar_init(&q_full[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    fence_mbar_init();
+  }
+  if (warp == 13) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk walk(c, a, G, run, s_begin[0], s_begin[1], s_begin[2]);
+  Part g;
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    // ------------------------------------------------------------ softmax: thread = row of M tile mt
+    const int mt = warp >> 2, row = tid & 127;
+    const uint32_t t_s = tmem + ((uint32_t)((warp & 3) * 32) << 16) + mt * kTile;
+    const uint32_t t_o = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + mt * kHeadDim;
+    uint32_t n = 0, segs = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      const int rows = (g.s.t1 - g.s.t0) * G, rho = g.qt * kItemRows + mt * kM + row;
+      const bool live = rho < rows;
+      const int i_row = rho / G, head = g.h * G + rho - i_row * G;
+      const int pos = g.s.first() + i_row;
+      // ---- this row's query, split into two E4M3 halves
+      float qf;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(g.s.t0 + i_row) * a.q_stride + (size_t)head * kHeadDim);
+        uint4 raw[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) raw[x] = live ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
+        uint32_t top = 0;  // bf16 magnitudes order as integers
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) top = __vmaxu2(top, w[y] & 0x7FFF7FFFu);
+        }
+        top = max(top & 0xFFFFu, top >> 16);
+        const bool bad = top >= 0x7F80u;
+        const int e = bad ? 0 : query_exponent(__uint_as_float(top << 16));
+        const float inv = exp2_int(-e);
+        qf = a.scale_log2 * exp2_int(e);
+        uint8_t* hi_row = smem + kQOff + mt * 2 * kTileBytes + row * 128;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const uint32_t w[8] = {raw[2 * x].x, raw[2 * x].y, raw[2 * x].z, raw[2 * x].w,
+                                 raw[2 * x + 1].x, raw[2 * x + 1].y, raw[2 * x + 1].z, raw[2 * x + 1].w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            uint32_t h0, l0, h1, l1;
+            split_e4m3x2(bf16_lo(w[2 * y]) * inv, bf16_hi(w[2 * y]) * inv, h0, l0);
+            split_e4m3x2(bf16_lo(w[2 * y + 1]) * inv, bf16_hi(w[2 * y + 1]) * inv, h1, l1);
+            hi[y] = bad ? 0x7F7F7F7Fu : h0 | h1 << 16;  // a row with an infinity or NaN has NaN scores
+            lo[y] = bad ? 0x7F7F7F7Fu : l0 | l1 << 16;
+          }
+          const int at = (x ^ (row & 7)) << 4;
+          *reinterpret_cast<uint4*>(hi_row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(hi_row + kTileBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[mt]);
+      }
+      // keys [w_lo, w_hi) are seen by every row of this warp
+      const int warp_rho = g.qt * kItemRows + warp * 32;
+      const int w_hi = a.causal ? min(g.hi, g.s.first() + warp_rho / G + 1) : g.hi;
+      const int w_lo = a.window > 0 ? g.s.first() + (warp_rho + 31) / G - a.window + 1 : 0;
+      float r = -CUDART_INF_F, l = 0.f;
+      for (int i = g.i0; i < g.i1; ++i, ++n) {
+        const int slot = (int)(n % kInfos);
+        ok = warp_wait(&i_full[slot], (n / kInfos) & 1u, abort_flag, c.status) &&
+             warp_wait(&s_full[mt], n & 1u, abort_flag, c.status);
+        if (!ok) break;
+        const TileInfo& ti = infos[slot];
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_ld32_async(t_s + 32 * x, s[x]);
+        tmem_wait_ld();
+        const int j0 = (g.tile0 + i) * kTile;
+        if (j0 < w_lo || j0 + kTile > w_hi || ti.have != 0xFFu) {
+          const int hi_col = (a.causal ? min(g.hi, pos + 1) : g.hi) - j0, lo_col = a.window > 0 ? pos - a.window + 1 - j0 : 0;
+          const uint32_t have = ti.have;
+#pragma unroll
+          for (int x = 0; x < 128; ++x)
+            if (x >= hi_col || x < lo_col || !(have >> (x >> 4) & 1u)) s[x >> 5][x & 31] = 0xFF800000u;
+        }
+        float m = -CUDART_INF_F;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          float t0 = __uint_as_float(s[b >> 1][(b & 1) * 16]), t1 = __uint_as_float(s[b >> 1][(b & 1) * 16 + 1]);
+#pragma unroll
+          for (int x = 2; x < 16; x += 2) {
+            t0 = fmaxf(t0, __uint_as_float(s[b >> 1][(b & 1) * 16 + x]));
+            t1 = fmaxf(t1, __uint_as_float(s[b >> 1][(b & 1) * 16 + x + 1]));
+          }
+          m = fmaxf(m, fmaf(fmaxf(t0, t1), qf * ti.kf[b], ti.lv[b]));
+        }
+        const bool grow = m > r + 8.f || (r == -CUDART_INF_F && m > r);
+        if (i > g.i0 && __any_sync(0xffffffffu, grow)) {
+          // the sums so far are of the tile before: wait for its product, then bring them to the new reference
+          ok = warp_wait(&o_full[mt], (n - 1u) & 1u, abort_flag, c.status);
+          if (!ok) break;
+          tc_fence_after();
+          const float f = grow ? ex2(r - m) : 1.f;
+          l *= f;
+#pragma unroll
+          for (int x = 0; x < kHeadDim; x += 16) {
+            uint32_t o[16];
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
+                  "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+                : "r"(t_o + x));
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+            asm volatile(
+                "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t_o + x),
+                "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]), "r"(o[8]),
+                "r"(o[9]), "r"(o[10]), "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15])
+                : "memory");
+          }
+        }
+        if (grow) r = m;
+        const float base = 7.f - (r == -CUDART_INF_F ? 0.f : r);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const float kf = qf * ti.kf[b], add = base + ti.lv[b];
+          float s0 = 0.f, s1 = 0.f;
+          uint32_t* v = &s[b >> 1][(b & 1) * 16];
+#pragma unroll
+          for (int x = 0; x < 16; x += 2) {
+            const float p0 = ex2(fmaf(__uint_as_float(v[x]), kf, add));
+            const float p1 = ex2(fmaf(__uint_as_float(v[x + 1]), kf, add));
+            s0 += p0;
+            s1 += p1;
+            // packed in place: weights of keys 2c and 2c + 1 in column c
+            s[b >> 2][(b & 3) * 8 + (x >> 1)] = pack_f16x2(p0, p1);
+          }
+          l = fmaf(s0 + s1, ti.un[b], l);
+        }
+        tmem_st32(t_s, s[0]);
+        tmem_st32(t_s + 32, s[1]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&p_full[mt]);
+          mbar_arrive(&i_empty[slot]);
+        }
+      }
+      if (!ok) break;
+      ok = warp_wait(&o_full[mt], (n - 1u) & 1u, abort_flag, c.status);
+      if (!ok) break;
+      tc_fence_after();
+      const bool complete = g.i0 == 0 && g.i1 == g.nt;
+      const float inv = complete ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
+      const size_t part = (size_t)(2 * (int)blockIdx.x + (g.i0 == 0 && segs > 0 ? 1 : 0)) * kItemRows + mt * kM + row;
+      uint16_t* out = a.out + ((size_t)(g.s.t0 + i_row) * c.Hq + head) * kHeadDim;
+      if (!complete) part_rl[part] = make_float2(r, l);
+#pragma unroll
+      for (int x = 0; x < kHeadDim; x += 32) {
+        uint32_t o[32];
+        tmem_ld32_async(t_o + x, o);
+        tmem_wait_ld();
+        if (complete) {
+          if (live) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                w[z] = pack_bf16x2(__uint_as_float(o[y + 2 * z]) * inv, __uint_as_float(o[y + 2 * z + 1]) * inv);
+              *reinterpret_cast<uint4*>(out + x + y) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < 32; y += 4)
+            *reinterpret_cast<uint4*>(part_o + part * kHeadDim + x + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+        }
+      }
+      tc_fence_before();
+      ++segs;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp < 12) {
+      // ---------------------------------------------------------- values: E4M3 -> f16, keys nobody sees -> zeros
+      uint32_t n = 0;
+      bool ok = true;
+      const int w = warp - 8;
+      while (ok && walk.next(g)) {
+        for (int i = g.i0; i < g.i1; ++i, ++n) {
+          const int st = (int)(n % kVStages), slot = (int)(n % kInfos);
+          ok = warp_wait(&i_full[slot], (n / kInfos) & 1u, abort_flag, c.status) &&
+               warp_wait(&v_full[st], (n / kVStages) & 1u, abort_flag, c.status) &&
+               warp_wait(&v16_empty[n & 1u], ((n >> 1) & 1u) ^ 1u, abort_flag, c.status);
+          if (!ok) break;
+          const uint32_t have = infos[slot].have;
+          const int j0 = (g.tile0 + i) * kTile;
+          const uint8_t* src = smem + kVOff + st * kTileBytes;
+          uint8_t* dst = smem + kV16Off + (n & 1u) * kV16Bytes;
+          // a warp step: 4 tokens, 8 lanes of 16 dims each
+#pragma unroll 4
+          for (int x = 0; x < 8; ++x) {
+            const int tok = w * 32 + x * 4 + (lane >> 3), ch = lane & 7;
+            uint4 v = *reinterpret_cast<const uint4*>(src + tok * 128 + ((ch ^ (tok & 7)) << 4));
+            if (j0 + tok < g.lo || j0 + tok >= g.hi || !(have >> (tok >> 4) & 1u)) v = make_uint4(0, 0, 0, 0);
+            uint4 o0, o1;
+            o0.x = e4m3x2_f16x2(v.x & 0xFFFFu);
+            o0.y = e4m3x2_f16x2(v.x >> 16);
+            o0.z = e4m3x2_f16x2(v.y & 0xFFFFu);
+            o0.w = e4m3x2_f16x2(v.y >> 16);
+            o1.x = e4m3x2_f16x2(v.z & 0xFFFFu);
+            o1.y = e4m3x2_f16x2(v.z >> 16);
+            o1.z = e4m3x2_f16x2(v.w & 0xFFFFu);
+            o1.w = e4m3x2_f16x2(v.w >> 16);
+            // dims 16 ch .. +15: two 16-byte pieces of the row of their half (64 dims, 128 bytes, swizzled)
+            uint8_t* to = dst + (ch >> 2) * kTileBytes + tok * 128;
+            const int piece = (ch & 3) * 2;
+            *reinterpret_cast<uint4*>(to + ((piece ^ (tok & 7)) << 4)) = o0;
+            *reinterpret_cast<uint4*>(to + (((piece + 1) ^ (tok & 7)) << 4)) = o1;
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&v16_full[n & 1u]);
+            mbar_arrive(&v_empty[st]);
+            mbar_arrive(&i_empty[slot]);
+          }
+        }
+      }
+    } else if (warp == 12) {
+      // ---------------------------------------------------------- TMA: lane = page of the tile
+      const uint64_t pol = policy_evict_last();
+      const int pages = kTile >> c.page_log2;
+      const uint32_t box = (uint32_t)c.page * kHeadDim;
+      uint32_t n = 0, nv = 0;
+      bool ok = true;
+      while (ok && walk.next(g)) {
+        const int32_t* row = c.page_table + (size_t)g.b * c.max_pages;
+        const int end = (g.hi + c.page - 1) >> c.page_log2, from = g.lo >> c.page_log2;
+        auto page_at = [&](int i) {
+          const int j = (g.tile0 + i) * pages + lane;
+          return lane < pages && i < g.i1 && j >= from && j < end ? __ldg(row + j) : -1;
+        };
+        int pg = page_at(g.i0);
+        for (int i = g.i0; i < g.i1; ++i) {
+          const int next = page_at(i + 1);
+          const bool have = pg >= 0 && pg < c.n_pages;
+          const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have)) * box;
+          const int y = have ? (int)(((long long)pg * c.Hkv + g.h) << c.page_log2) : 0;
+          const int ks = (int)(n % kKStages), vs = (int)(nv % kVStages);
+          ok = warp_wait(&k_empty[ks], ((n / kKStages) & 1u) ^ 1u, abort_flag, c.status);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], bytes);
+          __syncwarp();
+          if (have) tma_load_2d(smem + kKOff + ks * kTileBytes + lane * box, &tm_k, 0, y, &k_full[ks], pol);
+          ++n;
+          ok = warp_wait(&v_empty[vs], ((nv / kVStages) & 1u) ^ 1u, abort_flag, c.status);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], bytes);
+          __syncwarp();
+          if (have) tma_load_2d(smem + kVOff + vs * kTileBytes + lane * box, &tm_v, 0, y, &v_full[vs], pol);
+          ++nv;
+          pg = next;
+        }
+      }
+      // every copy lands before the block ends
+      if (lane == 0) {
+        for (int st = 0; st < kKStages; ++st) {
+          const uint32_t fills = n / kKStages + ((uint32_t)st < n % kKStages ? 1u : 0u);
+          if (fills) mbar_wait_bounded(&k_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
+        }
+        for (int st = 0; st < kVStages; ++st) {
+          const uint32_t fills = nv / kVStages + ((uint32_t)st < nv % kVStages ? 1u : 0u);
+          if (fills) mbar_wait_bounded(&v_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 13) {
+      // ---------------------------------------------------------- MMA
+      if (lane == 0) {
+        const uint32_t id_s = umma_idesc_e4m3(kM, kTile, false, false), id_o = idesc_pv();
+        const uint64_t desc = umma_desc_sw128(smem_u32(smem));
+        // V16: 64-dim halves 16 KB apart (leading), groups of 8 tokens 1 KB apart (stride)
+        const uint64_t vdesc = (desc & ~((uint64_t)0x3FFFu << 16)) | (uint64_t)(kTileBytes >> 4) << 16;
+        uint32_t n = 0, segs = 0;
+        bool ok = true;
+        // S of M tile mt against the keys of tile number t (one commit to the softmax; the second frees the stage)
+        auto scores = [&](int mt, uint32_t t, bool first) {
+          const int st = (int)(t % kKStages);
+          if (first) ok = ok && mbar_wait_bounded(&q_full[mt], segs & 1u, abort_flag, kAttnTimeoutNs, c.status);
+          if (mt == 0) ok = ok && mbar_wait_bounded(&k_full[st], (t / kKStages) & 1u, abort_flag, kAttnTimeoutNs, c.status);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t bd = desc + (uint64_t)((kKOff + st * kTileBytes) >> 4);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint64_t ad = desc + (uint64_t)((kQOff + (mt * 2 + half) * kTileBytes) >> 4);
+#pragma unroll
+            for (int k = 0; k < kHeadDim / 32; ++k)
+              umma_e4m3(tmem + mt * kTile, ad + 2 * k, bd + 2 * k, id_s, (half | k) != 0);
+          }
+          umma_commit(&s_full[mt]);
+          if (mt == 1) umma_commit(&k_empty[st]);
+        };
+        while (ok && walk.next(g)) {
+          for (int mt = 0; mt < 2; ++mt) scores(mt, n, true);
+          for (int i = g.i0; ok && i < g.i1; ++i, ++n) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              ok = ok && mbar_wait_bounded(&p_full[mt], n & 1u, abort_flag, kAttnTimeoutNs, c.status);
+              if (mt == 0)
+                ok = ok && mbar_wait_bounded(&v16_full[n & 1u], (n >> 1) & 1u, abort_flag, kAttnTimeoutNs, c.status);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t bd = vdesc + (uint64_t)((kV16Off + (n & 1u) * kV16Bytes) >> 4);
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)
+                umma_f16_ts(tmem + 256 + mt * kHeadDim, tmem + mt * kTile + 8 * k, bd + (uint64_t)((k * 16 * 128) >> 4), id_o,
+                            i > g.i0 || k > 0);
+              umma_commit(&o_full[mt]);
+              if (mt == 1) umma_commit(&v16_empty[n & 1u]);
+              if (i + 1 < g.i1) scores(mt, n + 1, false);
+              if (!ok) break;
+            }
+          }
+          ++segs;
+        }
+        // whatever was issued has finished before tensor memory is given back (after an abort too)
+        umma_commit(done);
+        mbar_wait_bounded(done, 0, abort_flag, kAttnTimeoutNs, c.status, false);
+      }
+      __syncwarp();
+    } else if (warp == 14) {
+      // ---------------------------------------------------------- scales: lane = 16 keys of the tile
+      uint32_t n = 0;
+      bool ok = true;
+      while (ok && walk.next(g)) {
+        const int32_t* row = c.page_table + (size_t)g.b * c.max_pages;
+        auto page_at = [&](int i) {
+          const int j = (g.tile0 + i) * kTile + (lane & 7) * 16;
+          const bool in = i < g.i1 && j + 15 >= g.lo && j < g.hi;
+          const int p = in ? __ldg(row + (j >> c.page_log2)) : -1;
+          if (in && (p < 0 || p >= c.n_pages)) set_status(c.status, DEV_ERR_BOUNDS);
+          return p < c.n_pages ? p : -1;
+        };
+        int pg = page_at(g.i0);
+        for (int i = g.i0; i < g.i1; ++i, ++n) {
+          const int slot = (int)(n % kInfos);
+          uint32_t sk = 127, sv = 127;
+          if (pg >= 0) {
+            const size_t u = (size_t)pg * c.Hkv + g.h;
+            sk = __ldg(c.k_scale + u);
+            sv = __ldg(c.v_scale + u);
+          }
+          const int next = page_at(i + 1);
+          const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0) & 0xFFu;
+          ok = warp_wait(&i_empty[slot], ((n / kInfos) & 1u) ^ 1u, abort_flag, c.status);
+          if (!ok) break;
+          if (lane < 8) {
+            infos[slot].kf[lane] = exp2_byte(sk);
+            infos[slot].lv[lane] = (float)((int)sv - 127);
+            infos[slot].un[lane] = ex2((float)(127 - (int)sv));
+            if (lane == 0) infos[slot].have = have;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&i_full[slot]);
+          pg = next;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the items that runs cut: block (run, 16 rows), acting where this run holds an item's second part.
+constexpr int kJoinRows = 16;
+__global__ void __launch_bounds__(kHeadDim)
+    attention_join_rows_kernel(const KvBatch c, const AttentionArgs a, const float* part_o, const float2* part_rl,
+                               const JoinInfo* info) {
+  pdl_wait();
+  const JoinInfo j = info[blockIdx.x];
+  if (!j.split || j.c0 != (int)blockIdx.x - 1) return;
+  SeqRange s;
+  if (!load_seq(c, j.b, s)) return;
+  const int G = c.Hq / c.Hkv, rows = (s.t1 - s.t0) * G, tid = threadIdx.x;
+  for (int x = 0; x < kJoinRows; ++x) {
+    const int in_item = (int)blockIdx.y * kJoinRows + x, rho = j.qt * kItemRows + in_item;
+    if (rho >= rows) return;
+    auto part_at = [&](int k) { return (size_t)(2 * k + (k == j.c0 ? j.slot0 : 0)) * kItemRows + in_item; };
+    float top = -CUDART_INF_F;
+    for (int k = j.c0; k <= j.c1; ++k) top = fmaxf(top, part_rl[part_at(k)].x);
+    const float ref = top == -CUDART_INF_F ? 0.f : top;
+    float sum = 0.f, acc = 0.f;
+    for (int k = j.c0; k <= j.c1; ++k) {
+      const float2 rl = part_rl[part_at(k)];
+      const float f = ex2(rl.x - ref);
+      sum = fmaf(rl.y, f, sum);
+      acc = fmaf(part_o[part_at(k) * kHeadDim + tid], f, acc);
+    }
+    const int i = rho / G;
+    a.out[((size_t)(s.t0 + i) * c.Hq + j.h * G + rho - i * G) * kHeadDim + tid] =
+        f32_to_bf16_rne(sum != 0.f ? acc / sum : 0.f);
+  }
+}
+
+}  // namespace
+
+size_t attention_prefill_scratch(int n_sms) {
+  return (size_t)n_sms * (2 * kItemRows * (kHeadDim * sizeof(float) + sizeof(float2)) + sizeof(JoinInfo));
+}
+
+cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
+  CUtensorMap tk, tv;
+  if (!make_cache_map(&tk, c.k_codes, c) || !make_cache_map(&tv, c.v_codes, c)) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(attention_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e != cudaSuccess) return e;
+  float* part_o = reinterpret_cast<float*>(a.scratch);
+  float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)n_sms * 2 * kItemRows * kHeadDim);
+  JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)n_sms * 2 * kItemRows);
+  e = launch_kernel(attention_prefill_kernel, dim3(n_sms), dim3(kThreads), kBytes, stream, false, tk, tv, c, a, part_o,
+                    part_rl, info);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(attention_join_rows_kernel, dim3(n_sms, kItemRows / kJoinRows), dim3(kHeadDim), 0, stream, true, c,
+                       a, part_o, part_rl, info);
+}
+
+}  // namespace moe
