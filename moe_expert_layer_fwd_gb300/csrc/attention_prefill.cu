@@ -27,7 +27,8 @@ constexpr int kThreads = 512;
 constexpr int kM = 128;
 constexpr int kItemRows = 2 * kM;
 constexpr int kKStages = 3, kVStages = 2, kInfos = 4;
-constexpr int kMinRun = 4;  // tiles in a block's run, at least
+constexpr int kMinRun = 4;   // cost of a block's run, at least
+constexpr int kItemCost = 3;  // an item's own cost (loading its queries, writing its rows), in tiles
 
 constexpr int kQOff = 0;                                 // [2 tiles][hi, lo][128 rows of 128 bytes]
 constexpr int kKOff = kQOff + 4 * kTileBytes;
@@ -51,6 +52,7 @@ static_assert(kBytes <= 232448, "shared memory");
 // One item (rows [256 qt, 256 qt + 256) of sequence b's n * G for head h) and the part of its tiles this run has.
 struct Part {
   int b, h, qt, i0, i1, nt, tile0, lo, hi;  // keys [lo, hi) are seen by some row
+  int later;                                // not the item that the run begins in
   SeqRange s;
 };
 
@@ -60,6 +62,8 @@ __device__ __forceinline__ void item_range(const SeqRange& s, const AttentionArg
   lo = a.window > 0 ? max(0, s.first() + i_min - a.window + 1) : 0;
 }
 __device__ __forceinline__ int item_tiles(int lo, int hi) { return max(1, (hi + kTile - 1) / kTile - lo / kTile); }
+
+__device__ __forceinline__ int item_cost(int nt) { return nt > 0 ? nt + kItemCost : 0; }
 
 // Sequence b's items take the places from q_start[b] * G / 256 + b on (some stay empty), so that a place's item is
 // found without a table of all of them.
@@ -100,36 +104,40 @@ struct Places {
   }
 };
 
+// An item costs its tiles and kItemCost more, all of it at its first tile: tile i lies at the place pos(i) of the item's
+// cost, and a run has the tiles whose places it covers.
+__device__ __forceinline__ int first_tile_from(long long rel, int nt) {
+  return rel <= 0 ? 0 : (int)min((long long)nt, max(1LL, rel - kItemCost));
+}
+
 struct Walk {
   Places p;
-  long long left;
-  int h, i, end;
-  __device__ Walk(const KvBatch& c, const AttentionArgs& a, int G, long long n, int place, int h_, int i_)
-      : p(c, a, G, place), left(n), h(h_), i(i_), end(places(c, G)) {}
+  long long left, rel;  // cost left in the run; where it starts in the present item
+  int h, end, later = 0;
+  __device__ Walk(const KvBatch& c, const AttentionArgs& a, int G, long long n, int place, int h_, int rel_)
+      : p(c, a, G, place), left(n), rel(rel_), h(h_), end(places(c, G)) {}
   __device__ bool next(Part& g) {
     while (left > 0 && p.place < end) {
       g.nt = p.tiles(g.qt, g.lo, g.hi);
       if (g.nt == 0) {
         p.next();
-        h = i = 0;
         continue;
       }
       g.b = p.b;
       g.s = p.s;
       g.h = h;
       g.tile0 = g.lo / kTile;
-      g.i0 = i;
-      g.i1 = (int)min((long long)g.nt, i + left);
-      left -= g.i1 - i;
-      i = g.i1;
-      if (i == g.nt) {
-        i = 0;
-        if (++h == p.c.Hkv) {
-          h = 0;
-          p.next();
-        }
+      g.i0 = first_tile_from(rel, g.nt);
+      g.i1 = first_tile_from(rel + left, g.nt);
+      g.later = later;
+      left -= g.nt + kItemCost - rel;
+      rel = 0;
+      later = 1;
+      if (++h == p.c.Hkv) {
+        h = 0;
+        p.next();
       }
-      return true;
+      if (g.i0 < g.i1) return true;
     }
     return false;
   }
@@ -169,6 +177,33 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
+  return d;
+}
+// Pairs of floats in one 64-bit register: one instruction for two products or sums.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void f32x2_split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t x, uint64_t y) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
+// The lowest n bits (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t d;
@@ -224,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int qt, lo, hi;
     if (p0 < p1) {
       Places p(c, a, G, p0);
-      for (; p.place < p1; p.next()) mine += p.tiles(qt, lo, hi);
+      for (; p.place < p1; p.next()) mine += item_cost(p.tiles(qt, lo, hi));
     }
     long long x = mine;
 #pragma unroll
@@ -252,23 +287,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       int nt;
       for (;; p.next()) {
         nt = p.tiles(qt, lo, hi);
-        if ((at + nt) * c.Hkv > begin) break;
-        at += nt;
+        if ((at + item_cost(nt)) * c.Hkv > begin) break;
+        at += item_cost(nt);
       }
-      const long long rel = begin - at * c.Hkv;
+      const int cost = item_cost(nt);
+      const long long rel = (begin - at * c.Hkv) % cost;
       s_begin[0] = p.place;
-      s_begin[1] = (int)(rel / nt);
-      s_begin[2] = (int)(rel % nt);
+      s_begin[1] = (int)((begin - at * c.Hkv) / cost);
+      s_begin[2] = (int)rel;
+      // does this run begin inside an item, with a part of it that is not its first?
       JoinInfo j = {};
-      j.split = rel % nt != 0;
+      const int i0 = first_tile_from(rel, nt);
+      j.split = i0 > 0 && i0 < nt;
       if (j.split) {
-        const long long i0 = begin - rel % nt, i1 = i0 + nt;
+        const long long start = begin - rel, last = start + (nt == 1 ? 0 : kItemCost + nt - 1);
         j.b = p.b;
-        j.h = (int)(rel / nt);
+        j.h = s_begin[1];
         j.qt = qt;
-        j.c0 = (int)(i0 / share);
-        j.c1 = (int)((i1 - 1) / share);
-        j.slot0 = i0 > (long long)j.c0 * share ? 1 : 0;
+        j.c0 = (int)(start / share);
+        j.c1 = (int)(last / share);
+        j.slot0 = start > (long long)j.c0 * share ? 1 : 0;
       }
       info[blockIdx.x] = j;
     }
@@ -315,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int mt = warp >> 2, row = tid & 127;
     const uint32_t t_s = tmem + ((uint32_t)((warp & 3) * 32) << 16) + mt * kTile;
     const uint32_t t_o = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + mt * kHeadDim;
-    uint32_t n = 0, segs = 0;
+    uint32_t n = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
       const int rows = (g.s.t1 - g.s.t0) * G, rho = g.qt * kItemRows + mt * kM + row;
@@ -381,21 +419,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         const int j0 = (g.tile0 + i) * kTile;
         if (j0 < w_lo || j0 + kTile > w_hi || ti.have != 0xFFu) {
+          // bit x of word w: this row sees key 32 w + x of the tile
           const int hi_col = (a.causal ? min(g.hi, pos + 1) : g.hi) - j0, lo_col = a.window > 0 ? pos - a.window + 1 - j0 : 0;
-          const uint32_t have = ti.have;
 #pragma unroll
-          for (int x = 0; x < 128; ++x)
-            if (x >= hi_col || x < lo_col || !(have >> (x >> 4) & 1u)) s[x >> 5][x & 31] = 0xFF800000u;
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t pages = ti.have >> (2 * w);
+            uint32_t see = ((pages & 1u) ? 0xFFFFu : 0u) | ((pages & 2u) ? 0xFFFF0000u : 0u);
+            see &= low_bits(hi_col - 32 * w) & ~low_bits(lo_col - 32 * w);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!(see & (1u << x))) s[w][x] = 0xFF800000u;
+          }
         }
         float m = -CUDART_INF_F;
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
-          float t0 = __uint_as_float(s[b >> 1][(b & 1) * 16]), t1 = __uint_as_float(s[b >> 1][(b & 1) * 16 + 1]);
+          const uint32_t* v = &s[b >> 1][(b & 1) * 16];
+          float t0 = __uint_as_float(v[0]), t1 = __uint_as_float(v[1]);
 #pragma unroll
-          for (int x = 2; x < 16; x += 2) {
-            t0 = fmaxf(t0, __uint_as_float(s[b >> 1][(b & 1) * 16 + x]));
-            t1 = fmaxf(t1, __uint_as_float(s[b >> 1][(b & 1) * 16 + x + 1]));
+          for (int x = 2; x < 14; x += 4) {
+            t0 = max3(t0, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+            t1 = max3(t1, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
           }
+          t0 = max3(t0, __uint_as_float(v[14]), __uint_as_float(v[15]));
           m = fmaxf(m, fmaf(fmaxf(t0, t1), qf * ti.kf[b], ti.lv[b]));
         }
         const bool grow = m > r + 8.f || (r == -CUDART_INF_F && m > r);
@@ -431,17 +477,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
           const float kf = qf * ti.kf[b], add = base + ti.lv[b];
-          float s0 = 0.f, s1 = 0.f;
+          const uint64_t kf2 = f32x2(kf, kf), add2 = f32x2(add, add);
+          uint64_t sum = 0;
           uint32_t* v = &s[b >> 1][(b & 1) * 16];
 #pragma unroll
           for (int x = 0; x < 16; x += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(v[x]), kf, add));
-            const float p1 = ex2(fmaf(__uint_as_float(v[x + 1]), kf, add));
-            s0 += p0;
-            s1 += p1;
+            float z0, z1;
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), kf2, add2), z0, z1);
+            const float p0 = ex2(z0), p1 = ex2(z1);
+            sum = add_f32x2(sum, f32x2(p0, p1));
             // packed in place: weights of keys 2c and 2c + 1 in column c
             s[b >> 2][(b & 3) * 8 + (x >> 1)] = pack_f16x2(p0, p1);
           }
+          float s0, s1;
+          f32x2_split(sum, s0, s1);
           l = fmaf(s0 + s1, ti.un[b], l);
         }
         tmem_st32(t_s, s[0]);
@@ -460,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool complete = g.i0 == 0 && g.i1 == g.nt;
       const float inv = complete ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
-      const size_t part = (size_t)(2 * (int)blockIdx.x + (g.i0 == 0 && segs > 0 ? 1 : 0)) * kItemRows + mt * kM + row;
+      const size_t part = (size_t)(2 * (int)blockIdx.x + g.later) * kItemRows + mt * kM + row;
       uint16_t* out = a.out + ((size_t)(g.s.t0 + i_row) * c.Hq + head) * kHeadDim;
       if (!complete) part_rl[part] = make_float2(r, l);
 #pragma unroll
@@ -486,7 +535,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      ++segs;
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
