@@ -16,7 +16,7 @@
 // (one at each end of a run, at most) are joined by a second kernel.
 //
 // Warps (16): 0-3 and 4-7 softmax of the M tiles (thread = row; they also load its query, rescale and write its output), 8-11
-// values, 12 TMA, 13 and 15 MMA (one per M tile), 14 scales of the tiles' pages.  Registers: 192 a thread for the softmax, 64 for the rest.
+// values, 12 TMA, 13 MMA, 14 scales of the tiles' pages.  Registers: 192 a thread for the softmax, 64 for the rest.
 // Every wait is bounded (2 s).
 #include "attention_tiles.cuh"
 
@@ -44,7 +44,7 @@ struct TileInfo {    // per 16 keys of a tile
   uint32_t pad[3];
 };
 constexpr int kBarOff = kInfoOff + kInfos * (int)sizeof(TileInfo);
-constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 4 + 2 * kInfos + 2 + 2 + 2 + 2 + 2;
+constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 4 + 2 * kInfos + 2 + 2 + 2 + 2 + 1;
 constexpr int kMiscOff = kBarOff + kNumBars * 8;
 constexpr int kBytes = 1024 + kMiscOff + 128;
 static_assert(kBytes <= 232448, "shared memory");
@@ -147,6 +147,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, kAttnTimeoutNs, status));
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint32_t idesc_pv() {
   uint32_t d = 0;
   d |= 1u << 4;                          // D f32, A and B f16
@@ -241,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
-  uint64_t* done = o_full + 2;               // [2]
+  uint64_t* done = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
   int* s_begin = reinterpret_cast<int*>(smem + kMiscOff + 8);  // place, head, tile
@@ -315,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 2);
+      mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(&v_full[i], 1);
@@ -327,13 +337,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&v16_full[i], 4);
-      mbar_init(&v16_empty[i], 2);
+      mbar_init(&v16_empty[i], 1);
       mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
-      mbar_init(&done[i], 1);
     }
+    mbar_init(done, 1);
     *abort_flag = 0;
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -632,58 +642,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 13 || warp == 15) {
-      // ---------------------------------------------------------- MMA: a thread for each M tile.  An instruction of this
-      // size runs for about 64 cycles and takes longer than that to issue, so that one thread could not keep the tensor
-      // core busy.  Within a thread's stream a product that overwrites S starts after the one that read p' there.
-      if (lane == 0) {
-        const int mt = warp == 15;
-        const uint32_t id_s = umma_idesc_e4m3(kM, kTile, false, false), id_o = idesc_pv();
-        const uint64_t desc = umma_desc_sw128(smem_u32(smem));
-        // V16: 64-dim halves 16 KB apart (leading), groups of 8 tokens 1 KB apart (stride)
-        const uint64_t vdesc = (desc & ~((uint64_t)0x3FFFu << 16)) | (uint64_t)(kTileBytes >> 4) << 16;
-        const uint32_t t_s = tmem + mt * kTile, t_o = tmem + 256 + mt * kHeadDim;
+    } else if (warp == 13) {
+      // ---------------------------------------------------------- MMA.  The whole warp walks along and one lane issues, so that
+      // descriptors stay in uniform registers: with one diverged thread an instruction took ~110 cycles to issue, and one
+      // of this size runs for 64.  The order PV0 QK0 PV1 QK1 keeps the M tiles half a turn apart.  A product that
+      // overwrites S starts after the one before it in the stream that reads p' there.
+      const uint32_t id_s = umma_idesc_e4m3(kM, kTile, false, false), id_o = idesc_pv();
+      const uint64_t desc = umma_desc_sw128(smem_u32(smem));
+      // V16: 64-dim halves 16 KB apart (leading), groups of 8 tokens 1 KB apart (stride)
+      const uint64_t vdesc = (desc & ~((uint64_t)0x3FFFu << 16)) | (uint64_t)(kTileBytes >> 4) << 16;
+      uint32_t n = 0, segs = 0;
+      bool ok = true;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      auto scores = [&](int mt, uint32_t t) {  // S of M tile mt against the keys of tile number t
+        const int st = (int)(t % kKStages);
+        if (mt == 0) ok = warp_wait(&k_full[st], (t / kKStages) & 1u, abort_flag, c.status);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t bd = desc + (uint64_t)((kKOff + st * kTileBytes) >> 4);
         const uint64_t q_hi = desc + (uint64_t)((kQOff + mt * 2 * kTileBytes) >> 4), q_lo = q_hi + (kTileBytes >> 4);
-        uint32_t n = 0, segs = 0;
-        bool ok = true;
-        auto scores = [&](uint32_t t) {  // S against the keys of tile number t
-          const int st = (int)(t % kKStages);
-          ok = ok && mbar_wait_bounded(&k_full[st], (t / kKStages) & 1u, abort_flag, kAttnTimeoutNs, c.status);
-          if (!ok) return;
-          tc_fence_after();
-          const uint64_t bd = desc + (uint64_t)((kKOff + st * kTileBytes) >> 4);
+        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kHeadDim / 32; ++k) umma_e4m3(t_s, q_hi + 2 * k, bd + 2 * k, id_s, k != 0);
+          for (int k = 0; k < kHeadDim / 32; ++k) umma_e4m3(tm + mt * kTile, q_hi + 2 * k, bd + 2 * k, id_s, k != 0);
 #pragma unroll
-          for (int k = 0; k < kHeadDim / 32; ++k) umma_e4m3(t_s, q_lo + 2 * k, bd + 2 * k, id_s, 1);
+          for (int k = 0; k < kHeadDim / 32; ++k) umma_e4m3(tm + mt * kTile, q_lo + 2 * k, bd + 2 * k, id_s, 1);
           umma_commit(&s_full[mt]);
-          umma_commit(&k_empty[st]);
-        };
-        while (ok && walk.next(g)) {
-          ok = mbar_wait_bounded(&q_full[mt], segs & 1u, abort_flag, kAttnTimeoutNs, c.status);
-          if (!ok) break;
-          scores(n);
-          for (int i = g.i0; ok && i < g.i1; ++i, ++n) {
-            ok = mbar_wait_bounded(&v16_full[n & 1u], (n >> 1) & 1u, abort_flag, kAttnTimeoutNs, c.status) &&
-                 mbar_wait_bounded(&p_full[mt], n & 1u, abort_flag, kAttnTimeoutNs, c.status);
+          if (mt == 1) umma_commit(&k_empty[st]);
+        }
+        __syncwarp();
+      };
+      while (ok && walk.next(g)) {
+        const int tiles = __shfl_sync(0xffffffffu, g.i1 - g.i0, 0);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          ok = ok && warp_wait(&q_full[mt], segs & 1u, abort_flag, c.status);
+          if (ok) scores(mt, n);
+        }
+        for (int i = 0; ok && i < tiles; ++i, ++n) {
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            if (mt == 0) ok = warp_wait(&v16_full[n & 1u], (n >> 1) & 1u, abort_flag, c.status);
+            ok = ok && warp_wait(&p_full[mt], n & 1u, abort_flag, c.status);
             if (!ok) break;
             tc_fence_after();
             const uint64_t bd = vdesc + (uint64_t)((kV16Off + (n & 1u) * kV16Bytes) >> 4);
-            umma_f16_ts(t_o, t_s, bd, id_o, i > g.i0);
+            const uint32_t more = i > 0;
+            if (elect_one()) {
+              umma_f16_ts(tm + 256 + mt * kHeadDim, tm + mt * kTile, bd, id_o, more);
 #pragma unroll
-            for (int k = 1; k < kTile / 16; ++k)
-              umma_f16_ts(t_o, t_s + 8 * k, bd + (uint64_t)((k * 16 * 128) >> 4), id_o, 1);
-            umma_commit(&o_full[mt]);
-            umma_commit(&v16_empty[n & 1u]);
-            if (i + 1 < g.i1) scores(n + 1);
+              for (int k = 1; k < kTile / 16; ++k)
+                umma_f16_ts(tm + 256 + mt * kHeadDim, tm + mt * kTile + 8 * k, bd + (uint64_t)((k * 16 * 128) >> 4), id_o, 1);
+              umma_commit(&o_full[mt]);
+              if (mt == 1) umma_commit(&v16_empty[n & 1u]);
+            }
+            __syncwarp();
+            if (i + 1 < tiles) scores(mt, n + 1);
+            if (!ok) break;
           }
-          ++segs;
         }
-        // whatever was issued has finished before tensor memory is given back (after an abort too)
-        umma_commit(&done[mt]);
-        mbar_wait_bounded(&done[mt], 0, abort_flag, kAttnTimeoutNs, c.status, false);
+        ++segs;
       }
+      // whatever was issued has finished before tensor memory is given back (after an abort too)
+      if (elect_one()) umma_commit(done);
       __syncwarp();
+      mbar_wait_bounded(done, 0, abort_flag, kAttnTimeoutNs, c.status, false);
     } else if (warp == 14) {
       // ---------------------------------------------------------- scales: lane = 16 keys of the tile
       uint32_t n = 0;
