@@ -6,7 +6,7 @@
 #include <mutex>
 
 namespace moe {
-bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c) {
+bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c, int box_rows) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -19,7 +19,7 @@ bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c) {
   if (!encode) return false;
   const cuuint64_t rows = (cuuint64_t)(c.n_pages > 0 ? c.n_pages : 1) * c.Hkv * c.page;
   const cuuint64_t dims[2] = {kHeadDim, rows}, strides[1] = {kHeadDim};
-  const cuuint32_t box[2] = {kHeadDim, (cuuint32_t)c.page}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {kHeadDim, (cuuint32_t)box_rows}, step[2] = {1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

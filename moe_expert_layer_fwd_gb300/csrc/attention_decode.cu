@@ -110,6 +110,7 @@ __device__ __forceinline__ long long scan_tiles(const KvBatch& c, const Attentio
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (c.B + threads - 1) / threads;
   mine = 0;
+#pragma unroll 1
   for (int b = tid * per; b < min(c.B, (tid + 1) * per); ++b) mine += seq_tiles(c, a, b);
   long long x = mine;
 #pragma unroll
@@ -121,6 +122,7 @@ __device__ __forceinline__ long long scan_tiles(const KvBatch& c, const Attentio
   __syncthreads();
   long long before = 0;
   total = 0;
+#pragma unroll 1
   for (int w = 0; w < threads / 32; ++w) {
     if (w < warp) before += s_warp[w];
     total += s_warp[w];
@@ -132,10 +134,6 @@ __device__ __forceinline__ long long scan_tiles(const KvBatch& c, const Attentio
 // Tiles per block: equal runs over the grid.
 __device__ __forceinline__ long long tiles_per_block(long long n, int blocks) {
   return max((long long)kMinRun, (n + blocks - 1) / blocks);
-}
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, kAttnTimeoutNs, status));
 }
 
 // acc[x] += column x + column `lo` + x of this thread's tensor-memory lane.
@@ -297,8 +295,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       for (int st = 0; st < C::kStages; ++st) {
         const uint32_t fills = n / C::kStages + ((uint32_t)st < n % C::kStages ? 1u : 0u);
         if (!fills) continue;
-        mbar_wait_bounded(&k_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
-        mbar_wait_bounded(&v_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
+        mbar_wait_tries(&k_full[st], (fills - 1u) & 1u, abort_flag, c.status, false);
+        mbar_wait_tries(&v_full[st], (fills - 1u) & 1u, abort_flag, c.status, false);
       }
     }
     __syncwarp();
@@ -314,9 +312,9 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       auto scores = [&]() {
         const int st = (int)(nq % C::kStages), qb = (int)(segs % C::kQBufs), sb = (int)(nq & 1u);
         if (i == g.i0)
-          ok = ok && mbar_wait_bounded(&q_full[qb], (segs / C::kQBufs) & 1u, abort_flag, kAttnTimeoutNs, c.status);
-        ok = ok && mbar_wait_bounded(&k_full[st], (nq / C::kStages) & 1u, abort_flag, kAttnTimeoutNs, c.status);
-        ok = ok && mbar_wait_bounded(&s_empty[sb], ((nq >> 1) & 1u) ^ 1u, abort_flag, kAttnTimeoutNs, c.status);
+          ok = ok && mbar_wait_tries(&q_full[qb], (segs / C::kQBufs) & 1u, abort_flag, c.status);
+        ok = ok && mbar_wait_tries(&k_full[st], (nq / C::kStages) & 1u, abort_flag, c.status);
+        ok = ok && mbar_wait_tries(&s_empty[sb], ((nq >> 1) & 1u) ^ 1u, abort_flag, c.status);
         if (!ok) return;
         tc_fence_after();
         const uint64_t ad = desc + (uint64_t)((st * 2 * kTileBytes) >> 4);
@@ -339,8 +337,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         if (more) scores();
         if (!ok) break;
         const int st = (int)(n % C::kStages);
-        if (!mbar_wait_bounded(p_full, n & 1u, abort_flag, kAttnTimeoutNs, c.status)) break;
-        if (!mbar_wait_bounded(&v_full[st], (n / C::kStages) & 1u, abort_flag, kAttnTimeoutNs, c.status)) break;
+        if (!mbar_wait_tries(p_full, n & 1u, abort_flag, c.status)) break;
+        if (!mbar_wait_tries(&v_full[st], (n / C::kStages) & 1u, abort_flag, c.status)) break;
         tc_fence_after();
         // V[token][dim]: the 128-byte rows are the K index, eight rows (1 KB) to a swizzle atom, 32 tokens an MMA
         const uint64_t ad = desc + (uint64_t)((st * 2 * kTileBytes + kTileBytes) >> 4);
@@ -353,7 +351,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       }
       // whatever was issued has finished before tensor memory is given back (after an abort too)
       umma_commit(done);
-      mbar_wait_bounded(done, 0, abort_flag, kAttnTimeoutNs, c.status, false);
+      mbar_wait_tries(done, 0, abort_flag, c.status, false);
     }
     __syncwarp();
   } else if (warp == C::kQWarp) {
@@ -657,7 +655,7 @@ template <int NC>
 cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
   using C = Cfg<NC>;
   CUtensorMap tk, tv;
-  if (!make_cache_map(&tk, c.k_codes, c) || !make_cache_map(&tv, c.v_codes, c)) return cudaErrorInvalidValue;
+  if (!make_cache_map(&tk, c.k_codes, c, c.page) || !make_cache_map(&tv, c.v_codes, c, c.page)) return cudaErrorInvalidValue;
   auto kern = attention_decode_kernel<NC>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (e != cudaSuccess) return e;

@@ -64,7 +64,7 @@ cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, in
 size_t attention_prefill_scratch(int n_sms);
 cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
 
-// The codes as a matrix of 128-byte rows (one token of one head each), boxes of one page with the 128-byte swizzle.
-bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c);
+// The codes as a matrix of 128-byte rows (one token of one head each), boxes of box_rows rows with the 128-byte swizzle.
+bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c, int box_rows);
 
 }  // namespace moe

@@ -15,27 +15,34 @@
 // any length fill all SMs evenly, and a chunk of few rows over a long cache is split along its keys.  The rows of a split item
 // (one at each end of a run, at most) are joined by a second kernel.
 //
-// Warps (16): 0-3 and 4-7 softmax of the M tiles (thread = row; they also load its query, rescale and write its output), 8-11
-// values, 12 TMA, 13 MMA, 14 scales of the tiles' pages.  Registers: 192 a thread for the softmax, 64 for the rest.
-// Every wait is bounded (2 s).
+// Warps (24): 0-7 and 8-15 softmax of the M tiles (thread = row and half of a tile's keys; they also load the queries,
+// rescale and write the output), 16-19 values, 20 TMA, 21 MMA, 22 scales of the tiles' pages, 23 walks the run.  Registers: 96 a
+// thread for the softmax, 48 for the rest.  Every wait is bounded (2 s).
 #include "attention_tiles.cuh"
 
 namespace moe {
 namespace {
 
+constexpr int kSoftWarps = 8;
+constexpr int kValWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kScaleWarp = 14;
 constexpr int kThreads = 512;
+constexpr int kReaders = kSoftWarps + 4 + 1 + 1;  // warps that read the run's parts
 constexpr int kM = 128;
 constexpr int kItemRows = 2 * kM;
-constexpr int kKStages = 3, kVStages = 2, kInfos = 4;
+constexpr int kKeys = 128;                 // keys of a tile
+constexpr int kSBufs = 1;                  // places in tensor memory for an M tile's scores
+constexpr int kCodeBytes = kKeys * kHeadDim; // a tile's codes of keys or values: 8 KB
+constexpr int kKStages = 3, kVStages = 2, kV16s = 2, kInfos = 4, kParts = 4;
+constexpr int kPieces = kKeys / 16;
 constexpr int kMinRun = 4;   // cost of a block's run, at least
 constexpr int kItemCost = 3;  // an item's own cost (loading its queries, writing its rows), in tiles
 
 constexpr int kQOff = 0;                                 // [2 tiles][hi, lo][128 rows of 128 bytes]
 constexpr int kKOff = kQOff + 4 * kTileBytes;
-constexpr int kVOff = kKOff + kKStages * kTileBytes;     // E4M3 as cached
-constexpr int kV16Off = kVOff + kVStages * kTileBytes;   // f16 [2][2 halves of the dims][128 tokens of 128 bytes]
-constexpr int kV16Bytes = 2 * kTileBytes;
-constexpr int kInfoOff = kV16Off + 2 * kV16Bytes;
+constexpr int kVOff = kKOff + kKStages * kCodeBytes;     // E4M3 as cached
+constexpr int kV16Off = kVOff + kVStages * kCodeBytes;   // f16 [2 halves of the dims][64 tokens of 128 bytes]
+constexpr int kV16Bytes = 2 * kCodeBytes;
+constexpr int kInfoOff = kV16Off + kV16s * kV16Bytes;
 struct TileInfo {    // per 16 keys of a tile
   float kf[8];       // 2^e_k
   float lv[8];       // e_v
@@ -43,25 +50,25 @@ struct TileInfo {    // per 16 keys of a tile
   uint32_t have;     // bit i: the page of keys 16 i .. 16 i + 15 is there
   uint32_t pad[3];
 };
-constexpr int kBarOff = kInfoOff + kInfos * (int)sizeof(TileInfo);
-constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 4 + 2 * kInfos + 2 + 2 + 2 + 2 + 1;
+struct Part {  // an item (rows [256 qt, 256 qt + 256) of a sequence's n * G for head h) and the tiles [i0, i1) of it in this run
+  int b, h, qt, i0, i1, nt, tile0, lo, hi;  // keys [lo, hi) are seen by some row; nt == 0: the run is over
+  int later;                                // not the item that the run begins in
+  int t0, n, first;                         // first new token, new tokens, position of the first
+  int pad[3];
+};
+constexpr int kPartOff = kInfoOff + kInfos * (int)sizeof(TileInfo);
+constexpr int kBarOff = kPartOff + kParts * (int)sizeof(Part);
+constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * kV16s + 2 * kInfos + 2 * kParts + 2 + 6 * kSBufs + 1;
 constexpr int kMiscOff = kBarOff + kNumBars * 8;
 constexpr int kBytes = 1024 + kMiscOff + 128;
 static_assert(kBytes <= 232448, "shared memory");
-
-// One item (rows [256 qt, 256 qt + 256) of sequence b's n * G for head h) and the part of its tiles this run has.
-struct Part {
-  int b, h, qt, i0, i1, nt, tile0, lo, hi;  // keys [lo, hi) are seen by some row
-  int later;                                // not the item that the run begins in
-  SeqRange s;
-};
 
 __device__ __forceinline__ void item_range(const SeqRange& s, const AttentionArgs& a, int G, int qt, int& lo, int& hi) {
   const int i_min = qt * kItemRows / G, i_max = min(s.t1 - s.t0 - 1, (qt * kItemRows + kItemRows - 1) / G);
   hi = a.causal ? max(0, min(s.len, s.first() + i_max + 1)) : s.len;
   lo = a.window > 0 ? max(0, s.first() + i_min - a.window + 1) : 0;
 }
-__device__ __forceinline__ int item_tiles(int lo, int hi) { return max(1, (hi + kTile - 1) / kTile - lo / kTile); }
+__device__ __forceinline__ int item_tiles(int lo, int hi) { return max(1, (hi + kKeys - 1) / kKeys - lo / kKeys); }
 
 __device__ __forceinline__ int item_cost(int nt) { return nt > 0 ? nt + kItemCost : 0; }
 
@@ -124,9 +131,11 @@ struct Walk {
         continue;
       }
       g.b = p.b;
-      g.s = p.s;
+      g.t0 = p.s.t0;
+      g.n = p.s.t1 - p.s.t0;
+      g.first = p.s.first();
       g.h = h;
-      g.tile0 = g.lo / kTile;
+      g.tile0 = g.lo / kKeys;
       g.i0 = first_tile_from(rel, g.nt);
       g.i1 = first_tile_from(rel + left, g.nt);
       g.later = later;
@@ -139,13 +148,27 @@ struct Walk {
       }
       if (g.i0 < g.i1) return true;
     }
+    g.nt = 0;
     return false;
   }
 };
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, kAttnTimeoutNs, status));
-}
+// A role's place in the run's parts, which the walking warp keeps a few ahead in shared memory.
+struct Reader {
+  const Part* parts;
+  uint64_t *full, *empty;
+  uint32_t n;
+  // The next part (whole warp); false at the end of the run, or after a timeout.
+  __device__ bool next(Part& g, volatile int* abort_flag, unsigned* status) {
+    const int slot = (int)(n % kParts);
+    if (!warp_wait(&full[slot], (n / kParts) & 1u, abort_flag, status)) return false;
+    g = parts[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[slot]);
+    ++n;
+    return g.nt != 0;
+  }
+};
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -175,7 +198,7 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, ui
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -225,6 +248,45 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
   return (uint32_t)h.x | (uint32_t)h.y << 16;
 }
 
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], uint32_t see) {
+#pragma unroll
+  for (int x = 0; x < 32; ++x)
+    if (!(see & (1u << x))) s[x] = 0xFF800000u;  // -infinity
+}
+
+__device__ __forceinline__ float max16(const uint32_t* v) {
+  float t0 = __uint_as_float(v[0]), t1 = __uint_as_float(v[1]);
+#pragma unroll
+  for (int x = 2; x < 14; x += 4) {
+    t0 = max3(t0, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+    t1 = max3(t1, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
+  }
+  return fmaxf(max3(t0, __uint_as_float(v[14]), __uint_as_float(v[15])), t1);
+}
+
+// The larger bf16 magnitudes of pairs.
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t top, const uint4& v) {
+  top = __vmaxu2(top, v.x & 0x7FFF7FFFu);
+  top = __vmaxu2(top, v.y & 0x7FFF7FFFu);
+  top = __vmaxu2(top, v.z & 0x7FFF7FFFu);
+  return __vmaxu2(top, v.w & 0x7FFF7FFFu);
+}
+
+// 64 columns of this thread's tensor-memory lane times f.
+__device__ __forceinline__ void rescale_lane64(uint32_t taddr, float f) {
+#pragma unroll
+  for (int x = 0; x < 64; x += 8) {
+    uint32_t o[8];
+    tmem_ld8_async(taddr + x, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int y = 0; y < 8; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr + x), "r"(o[0]),
+                 "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                 : "memory");
+  }
+}
+
 // What a block tells the joining kernel about the part that its run begins with.
 struct JoinInfo {
   int split;       // the part is not the item's first: blocks c0 .. c1 hold its parts
@@ -243,18 +305,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_empty = k_full + kKStages;
   uint64_t* v_full = k_empty + kKStages;
   uint64_t* v_empty = v_full + kVStages;
-  uint64_t* v16_full = v_empty + kVStages;   // [2]
-  uint64_t* v16_empty = v16_full + 2;        // [2]
-  uint64_t* i_full = v16_empty + 2;
+  uint64_t* v16_full = v_empty + kVStages;
+  uint64_t* v16_empty = v16_full + kV16s;
+  uint64_t* i_full = v16_empty + kV16s;
   uint64_t* i_empty = i_full + kInfos;
-  uint64_t* q_full = i_empty + kInfos;       // [2], by M tile, as the next three
-  uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
-  uint64_t* done = o_full + 2;
+  uint64_t* r_full = i_empty + kInfos;
+  uint64_t* r_empty = r_full + kParts;
+  uint64_t* q_full = r_empty + kParts;       // [2], by M tile
+  uint64_t* s_full = q_full + 2;             // [2 M tiles][kSBufs], as the next two
+  uint64_t* p_full = s_full + 2 * kSBufs;
+  uint64_t* o_full = p_full + 2 * kSBufs;
+  uint64_t* done = o_full + 2 * kSBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
-  int* s_begin = reinterpret_cast<int*>(smem + kMiscOff + 8);  // place, head, tile
+  int* s_begin = reinterpret_cast<int*>(smem + kMiscOff + 8);  // place, head, cost into the item
+  Part* parts = reinterpret_cast<Part*>(smem + kPartOff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = c.Hq / c.Hkv;
   pdl_launch_dependents();
@@ -269,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int qt, lo, hi;
     if (p0 < p1) {
       Places p(c, a, G, p0);
+#pragma unroll 1
       for (; p.place < p1; p.next()) mine += item_cost(p.tiles(qt, lo, hi));
     }
     long long x = mine;
@@ -280,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 31) s_warp[warp] = x;
     __syncthreads();
     long long before = x - mine, total = 0;
+#pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += s_warp[w];
       total += s_warp[w];
@@ -333,57 +400,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(&i_full[i], 1);
-      mbar_init(&i_empty[i], 12);
+      mbar_init(&i_empty[i], kSoftWarps + 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kV16s; ++i) {
       mbar_init(&v16_full[i], 4);
       mbar_init(&v16_empty[i], 1);
-      mbar_init(&q_full[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 4);
+    mbar_init(done, 1);
+    for (int i = 0; i < 2 * kSBufs; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
     }
-    mbar_init(done, 1);
+    for (int i = 0; i < kParts; ++i) {
+      mbar_init(&r_full[i], 1);
+      mbar_init(&r_empty[i], kReaders);
+    }
     *abort_flag = 0;
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     fence_mbar_init();
   }
-  if (warp == 13) tmem_alloc(tmem_slot, 512);
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk walk(c, a, G, run, s_begin[0], s_begin[1], s_begin[2]);
+  Reader reader{parts, r_full, r_empty, 0};
   Part g;
 
-  if (warp < 8) {
+  if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     // ------------------------------------------------------------ softmax: thread = row of M tile mt
-    const int mt = warp >> 2, row = tid & 127;
-    const uint32_t t_s = tmem + ((uint32_t)((warp & 3) * 32) << 16) + mt * kTile;
-    const uint32_t t_o = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + mt * kHeadDim;
+    const int mt = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t t_s = lanes + mt * 128, t_o = lanes + 256 + mt * kHeadDim;
     uint32_t n = 0;
     bool ok = true;
-    while (ok && walk.next(g)) {
-      const int rows = (g.s.t1 - g.s.t0) * G, rho = g.qt * kItemRows + mt * kM + row;
-      const bool live = rho < rows;
+    while (ok && reader.next(g, abort_flag, c.status)) {
+      const int rho = g.qt * kItemRows + mt * kM + row;
+      const bool live = rho < g.n * G;
       const int i_row = rho / G, head = g.h * G + rho - i_row * G;
-      const int pos = g.s.first() + i_row;
+      const int pos = g.first + i_row;
       // ---- this row's query, split into two E4M3 halves
       float qf;
       {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(g.s.t0 + i_row) * a.q_stride + (size_t)head * kHeadDim);
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(g.t0 + i_row) * a.q_stride + (size_t)head * kHeadDim);
+        uint32_t top = 0;  // bf16 magnitudes order as integers
         uint4 raw[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x) raw[x] = live ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
-        uint32_t top = 0;  // bf16 magnitudes order as integers
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) top = __vmaxu2(top, w[y] & 0x7FFF7FFFu);
-        }
+        for (int x = 0; x < 16; ++x) top = max_magnitude(top, raw[x]);
         top = max(top & 0xFFFFu, top >> 16);
         const bool bad = top >= 0x7F80u;
         const int e = bad ? 0 : query_exponent(__uint_as_float(top << 16));
@@ -413,83 +482,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // keys [w_lo, w_hi) are seen by every row of this warp
       const int warp_rho = g.qt * kItemRows + warp * 32;
-      const int w_hi = a.causal ? min(g.hi, g.s.first() + warp_rho / G + 1) : g.hi;
-      const int w_lo = a.window > 0 ? g.s.first() + (warp_rho + 31) / G - a.window + 1 : 0;
+      const int w_hi = a.causal ? min(g.hi, g.first + warp_rho / G + 1) : g.hi;
+      const int w_lo = a.window > 0 ? g.first + (warp_rho + 31) / G - a.window + 1 : 0;
       float r = -CUDART_INF_F, l = 0.f;
       for (int i = g.i0; i < g.i1; ++i, ++n) {
         const int slot = (int)(n % kInfos);
+        const uint32_t sb = n % kSBufs, bar = mt * kSBufs + sb;
         ok = warp_wait(&i_full[slot], (n / kInfos) & 1u, abort_flag, c.status) &&
-             warp_wait(&s_full[mt], n & 1u, abort_flag, c.status);
+             warp_wait(&s_full[bar], (n / kSBufs) & 1u, abort_flag, c.status);
         if (!ok) break;
         const TileInfo& ti = infos[slot];
+        const uint32_t have = ti.have;
         tc_fence_after();
-        uint32_t s[4][32];
+        const uint32_t t_s2 = t_s + sb * kKeys;
+        uint32_t s[kKeys / 32][32];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_ld32_async(t_s + 32 * x, s[x]);
+        for (int w = 0; w < kKeys / 32; ++w) tmem_ld32_async(t_s2 + 32 * w, s[w]);
+        float kf[kPieces], lv[kPieces];
+#pragma unroll
+        for (int b = 0; b < kPieces; ++b) {
+          kf[b] = qf * ti.kf[b];
+          lv[b] = ti.lv[b];
+        }
         tmem_wait_ld();
-        const int j0 = (g.tile0 + i) * kTile;
-        if (j0 < w_lo || j0 + kTile > w_hi || ti.have != 0xFFu) {
+        const int j0 = (g.tile0 + i) * kKeys;
+        if (j0 < w_lo || j0 + kKeys > w_hi || have != (1u << kPieces) - 1u) {
           // bit x of word w: this row sees key 32 w + x of the tile
           const int hi_col = (a.causal ? min(g.hi, pos + 1) : g.hi) - j0, lo_col = a.window > 0 ? pos - a.window + 1 - j0 : 0;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t pages = ti.have >> (2 * w);
-            uint32_t see = ((pages & 1u) ? 0xFFFFu : 0u) | ((pages & 2u) ? 0xFFFF0000u : 0u);
-            see &= low_bits(hi_col - 32 * w) & ~low_bits(lo_col - 32 * w);
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!(see & (1u << x))) s[w][x] = 0xFF800000u;
+          for (int w = 0; w < kKeys / 32; ++w) {
+            const uint32_t pages = have >> (2 * w);
+            mask32(s[w], (((pages & 1u) ? 0xFFFFu : 0u) | ((pages & 2u) ? 0xFFFF0000u : 0u)) & low_bits(hi_col - 32 * w) &
+                             ~low_bits(lo_col - 32 * w));
           }
         }
         float m = -CUDART_INF_F;
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          const uint32_t* v = &s[b >> 1][(b & 1) * 16];
-          float t0 = __uint_as_float(v[0]), t1 = __uint_as_float(v[1]);
-#pragma unroll
-          for (int x = 2; x < 14; x += 4) {
-            t0 = max3(t0, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-            t1 = max3(t1, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
-          }
-          t0 = max3(t0, __uint_as_float(v[14]), __uint_as_float(v[15]));
-          m = fmaxf(m, fmaf(fmaxf(t0, t1), qf * ti.kf[b], ti.lv[b]));
-        }
+        for (int b = 0; b < kPieces; ++b) m = fmaxf(m, fmaf(max16(&s[b >> 1][(b & 1) * 16]), kf[b], lv[b]));
         const bool grow = m > r + 8.f || (r == -CUDART_INF_F && m > r);
         if (i > g.i0 && __any_sync(0xffffffffu, grow)) {
           // the sums so far are of the tile before: wait for its product, then bring them to the new reference
-          ok = warp_wait(&o_full[mt], (n - 1u) & 1u, abort_flag, c.status);
+          ok = warp_wait(&o_full[mt * kSBufs + (n - 1u) % kSBufs], ((n - 1u) / kSBufs) & 1u, abort_flag, c.status);
           if (!ok) break;
           tc_fence_after();
           const float f = grow ? ex2(r - m) : 1.f;
           l *= f;
-#pragma unroll
-          for (int x = 0; x < kHeadDim; x += 16) {
-            uint32_t o[16];
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
-                  "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                : "r"(t_o + x));
-            tmem_wait_ld();
-#pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-            asm volatile(
-                "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-                "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t_o + x),
-                "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]), "r"(o[8]),
-                "r"(o[9]), "r"(o[10]), "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15])
-                : "memory");
-          }
+          rescale_lane64(t_o, f);
+          rescale_lane64(t_o + 64, f);
+          tmem_wait_st();
         }
         if (grow) r = m;
         const float base = 7.f - (r == -CUDART_INF_F ? 0.f : r);
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          const float kf = qf * ti.kf[b], add = base + ti.lv[b];
-          const uint64_t kf2 = f32x2(kf, kf), add2 = f32x2(add, add);
+        for (int b = 0; b < kPieces; ++b) {
+          const float add = base + lv[b];
+          const uint64_t kf2 = f32x2(kf[b], kf[b]), add2 = f32x2(add, add);
           uint64_t sum = 0;
-          uint32_t* v = &s[b >> 1][(b & 1) * 16];
+          const uint32_t* v = &s[b >> 1][(b & 1) * 16];
 #pragma unroll
           for (int x = 0; x < 16; x += 2) {
             float z0, z1;
@@ -503,24 +552,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           f32x2_split(sum, s0, s1);
           l = fmaf(s0 + s1, ti.un[b], l);
         }
-        tmem_st32(t_s, s[0]);
-        tmem_st32(t_s + 32, s[1]);
+#pragma unroll
+        for (int w = 0; w < kKeys / 64; ++w) tmem_st32(t_s2 + 32 * w, s[w]);  // over the scores
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&p_full[mt]);
+          mbar_arrive(&p_full[bar]);
           mbar_arrive(&i_empty[slot]);
         }
       }
-      if (!ok) break;
-      ok = warp_wait(&o_full[mt], (n - 1u) & 1u, abort_flag, c.status);
+      // ---- the rows' outputs
+      ok = ok && warp_wait(&o_full[mt * kSBufs + (n - 1u) % kSBufs], ((n - 1u) / kSBufs) & 1u, abort_flag, c.status);
       if (!ok) break;
       tc_fence_after();
       const bool complete = g.i0 == 0 && g.i1 == g.nt;
       const float inv = complete ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
       const size_t part = (size_t)(2 * (int)blockIdx.x + g.later) * kItemRows + mt * kM + row;
-      uint16_t* out = a.out + ((size_t)(g.s.t0 + i_row) * c.Hq + head) * kHeadDim;
+      uint16_t* out = a.out + ((size_t)(g.t0 + i_row) * c.Hq + head) * kHeadDim;
       if (!complete) part_rl[part] = make_float2(r, l);
 #pragma unroll
       for (int x = 0; x < kHeadDim; x += 32) {
@@ -548,26 +597,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp < 12) {
+    if (warp < kTmaWarp) {
       // ---------------------------------------------------------- values: E4M3 -> f16, keys nobody sees -> zeros
       uint32_t n = 0;
       bool ok = true;
-      const int w = warp - 8;
-      while (ok && walk.next(g)) {
+      const int w = warp - kValWarp;
+      while (ok && reader.next(g, abort_flag, c.status)) {
         for (int i = g.i0; i < g.i1; ++i, ++n) {
           const int st = (int)(n % kVStages), slot = (int)(n % kInfos);
           ok = warp_wait(&i_full[slot], (n / kInfos) & 1u, abort_flag, c.status) &&
                warp_wait(&v_full[st], (n / kVStages) & 1u, abort_flag, c.status) &&
-               warp_wait(&v16_empty[n & 1u], ((n >> 1) & 1u) ^ 1u, abort_flag, c.status);
+               warp_wait(&v16_empty[n % kV16s], ((n / kV16s) & 1u) ^ 1u, abort_flag, c.status);
           if (!ok) break;
           const uint32_t have = infos[slot].have;
-          const int j0 = (g.tile0 + i) * kTile;
-          const uint8_t* src = smem + kVOff + st * kTileBytes;
-          uint8_t* dst = smem + kV16Off + (n & 1u) * kV16Bytes;
+          const int j0 = (g.tile0 + i) * kKeys;
+          const uint8_t* src = smem + kVOff + st * kCodeBytes;
+          uint8_t* dst = smem + kV16Off + (n % kV16s) * kV16Bytes;
           // a warp step: 4 tokens, 8 lanes of 16 dims each
-#pragma unroll 4
-          for (int x = 0; x < 8; ++x) {
-            const int tok = w * 32 + x * 4 + (lane >> 3), ch = lane & 7;
+#pragma unroll 2
+          for (int x = 0; x < kKeys / 16; ++x) {
+            const int tok = w * (kKeys / 4) + x * 4 + (lane >> 3), ch = lane & 7;
             uint4 v = *reinterpret_cast<const uint4*>(src + tok * 128 + ((ch ^ (tok & 7)) << 4));
             if (j0 + tok < g.lo || j0 + tok >= g.hi || !(have >> (tok >> 4) & 1u)) v = make_uint4(0, 0, 0, 0);
             uint4 o0, o1;
@@ -580,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             o1.z = e4m3x2_f16x2(v.w & 0xFFFFu);
             o1.w = e4m3x2_f16x2(v.w >> 16);
             // dims 16 ch .. +15: two 16-byte pieces of the row of their half (64 dims, 128 bytes, swizzled)
-            uint8_t* to = dst + (ch >> 2) * kTileBytes + tok * 128;
+            uint8_t* to = dst + (ch >> 2) * kCodeBytes + tok * 128;
             const int piece = (ch & 3) * 2;
             *reinterpret_cast<uint4*>(to + ((piece ^ (tok & 7)) << 4)) = o0;
             *reinterpret_cast<uint4*>(to + (((piece + 1) ^ (tok & 7)) << 4)) = o1;
@@ -588,44 +637,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&v16_full[n & 1u]);
+            mbar_arrive(&v16_full[n % kV16s]);
             mbar_arrive(&v_empty[st]);
             mbar_arrive(&i_empty[slot]);
           }
         }
       }
-    } else if (warp == 12) {
+    } else if (warp == kTmaWarp) {
       // ---------------------------------------------------------- TMA: lane = page of the tile
       const uint64_t pol = policy_evict_last();
-      const int pages = kTile >> c.page_log2;
-      const uint32_t box = (uint32_t)c.page * kHeadDim;
+      const int keys_log2 = min(c.page_log2, kKeys == 64 ? 6 : 7), boxes = kKeys >> keys_log2;  // keys of a box: a page, or half a page of 128
+      const uint32_t box = kHeadDim << keys_log2;
       uint32_t n = 0, nv = 0;
       bool ok = true;
-      while (ok && walk.next(g)) {
+      while (ok && reader.next(g, abort_flag, c.status)) {
         const int32_t* row = c.page_table + (size_t)g.b * c.max_pages;
-        const int end = (g.hi + c.page - 1) >> c.page_log2, from = g.lo >> c.page_log2;
+        // page of this lane's box of tile i, read one tile ahead; -1: nothing to load
         auto page_at = [&](int i) {
-          const int j = (g.tile0 + i) * pages + lane;
-          return lane < pages && i < g.i1 && j >= from && j < end ? __ldg(row + j) : -1;
+          const int j = (g.tile0 + i) * kKeys + (lane << keys_log2);
+          return lane < boxes && i < g.i1 && j + (1 << keys_log2) > g.lo && j < g.hi ? __ldg(row + (j >> c.page_log2)) : -1;
         };
         int pg = page_at(g.i0);
         for (int i = g.i0; i < g.i1; ++i) {
           const int next = page_at(i + 1);
+          const int in_page = ((g.tile0 + i) * kKeys + (lane << keys_log2)) & (c.page - 1);
           const bool have = pg >= 0 && pg < c.n_pages;
           const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have)) * box;
-          const int y = have ? (int)(((long long)pg * c.Hkv + g.h) << c.page_log2) : 0;
+          const int y = have ? (int)(((long long)pg * c.Hkv + g.h) << c.page_log2) + in_page : 0;
           const int ks = (int)(n % kKStages), vs = (int)(nv % kVStages);
           ok = warp_wait(&k_empty[ks], ((n / kKStages) & 1u) ^ 1u, abort_flag, c.status);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], bytes);
           __syncwarp();
-          if (have) tma_load_2d(smem + kKOff + ks * kTileBytes + lane * box, &tm_k, 0, y, &k_full[ks], pol);
+          if (have) tma_load_2d(smem + kKOff + ks * kCodeBytes + lane * box, &tm_k, 0, y, &k_full[ks], pol);
           ++n;
           ok = warp_wait(&v_empty[vs], ((nv / kVStages) & 1u) ^ 1u, abort_flag, c.status);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], bytes);
           __syncwarp();
-          if (have) tma_load_2d(smem + kVOff + vs * kTileBytes + lane * box, &tm_v, 0, y, &v_full[vs], pol);
+          if (have) tma_load_2d(smem + kVOff + vs * kCodeBytes + lane * box, &tm_v, 0, y, &v_full[vs], pol);
           ++nv;
           pg = next;
         }
@@ -634,86 +684,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         for (int st = 0; st < kKStages; ++st) {
           const uint32_t fills = n / kKStages + ((uint32_t)st < n % kKStages ? 1u : 0u);
-          if (fills) mbar_wait_bounded(&k_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
+          if (fills) mbar_wait_tries(&k_full[st], (fills - 1u) & 1u, abort_flag, c.status, false);
         }
         for (int st = 0; st < kVStages; ++st) {
           const uint32_t fills = nv / kVStages + ((uint32_t)st < nv % kVStages ? 1u : 0u);
-          if (fills) mbar_wait_bounded(&v_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
+          if (fills) mbar_wait_tries(&v_full[st], (fills - 1u) & 1u, abort_flag, c.status, false);
         }
       }
       __syncwarp();
-    } else if (warp == 13) {
-      // ---------------------------------------------------------- MMA.  The whole warp walks along and one lane issues, so that
-      // descriptors stay in uniform registers: with one diverged thread an instruction took ~110 cycles to issue, and one
-      // of this size runs for 64.  The order PV0 QK0 PV1 QK1 keeps the M tiles half a turn apart.  A product that
-      // overwrites S starts after the one before it in the stream that reads p' there.
-      const uint32_t id_s = umma_idesc_e4m3(kM, kTile, false, false), id_o = idesc_pv();
-      const uint64_t desc = umma_desc_sw128(smem_u32(smem));
-      // V16: 64-dim halves 16 KB apart (leading), groups of 8 tokens 1 KB apart (stride)
-      const uint64_t vdesc = (desc & ~((uint64_t)0x3FFFu << 16)) | (uint64_t)(kTileBytes >> 4) << 16;
-      uint32_t n = 0, segs = 0;
-      bool ok = true;
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      auto scores = [&](int mt, uint32_t t) {  // S of M tile mt against the keys of tile number t
-        const int st = (int)(t % kKStages);
-        if (mt == 0) ok = warp_wait(&k_full[st], (t / kKStages) & 1u, abort_flag, c.status);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t bd = desc + (uint64_t)((kKOff + st * kTileBytes) >> 4);
-        const uint64_t q_hi = desc + (uint64_t)((kQOff + mt * 2 * kTileBytes) >> 4), q_lo = q_hi + (kTileBytes >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kHeadDim / 32; ++k) umma_e4m3(tm + mt * kTile, q_hi + 2 * k, bd + 2 * k, id_s, k != 0);
-#pragma unroll
-          for (int k = 0; k < kHeadDim / 32; ++k) umma_e4m3(tm + mt * kTile, q_lo + 2 * k, bd + 2 * k, id_s, 1);
-          umma_commit(&s_full[mt]);
-          if (mt == 1) umma_commit(&k_empty[st]);
-        }
-        __syncwarp();
-      };
-      while (ok && walk.next(g)) {
-        const int tiles = __shfl_sync(0xffffffffu, g.i1 - g.i0, 0);
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          ok = ok && warp_wait(&q_full[mt], segs & 1u, abort_flag, c.status);
-          if (ok) scores(mt, n);
-        }
-        for (int i = 0; ok && i < tiles; ++i, ++n) {
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            if (mt == 0) ok = warp_wait(&v16_full[n & 1u], (n >> 1) & 1u, abort_flag, c.status);
-            ok = ok && warp_wait(&p_full[mt], n & 1u, abort_flag, c.status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t bd = vdesc + (uint64_t)((kV16Off + (n & 1u) * kV16Bytes) >> 4);
-            const uint32_t more = i > 0;
-            if (elect_one()) {
-              umma_f16_ts(tm + 256 + mt * kHeadDim, tm + mt * kTile, bd, id_o, more);
-#pragma unroll
-              for (int k = 1; k < kTile / 16; ++k)
-                umma_f16_ts(tm + 256 + mt * kHeadDim, tm + mt * kTile + 8 * k, bd + (uint64_t)((k * 16 * 128) >> 4), id_o, 1);
-              umma_commit(&o_full[mt]);
-              if (mt == 1) umma_commit(&v16_empty[n & 1u]);
-            }
-            __syncwarp();
-            if (i + 1 < tiles) scores(mt, n + 1);
-            if (!ok) break;
-          }
-        }
-        ++segs;
-      }
-      // whatever was issued has finished before tensor memory is given back (after an abort too)
-      if (elect_one()) umma_commit(done);
-      __syncwarp();
-      mbar_wait_bounded(done, 0, abort_flag, kAttnTimeoutNs, c.status, false);
-    } else if (warp == 14) {
+    } else if (warp == kScaleWarp) {
       // ---------------------------------------------------------- scales: lane = 16 keys of the tile
+      // It also walks the run, and gives the others its parts.
+      Walk walk(c, a, G, run, s_begin[0], s_begin[1], s_begin[2]);
       uint32_t n = 0;
       bool ok = true;
-      while (ok && walk.next(g)) {
+      for (uint32_t np = 0; ok; ++np) {
+        const int at = (int)(np % kParts);
+        const bool more = walk.next(g);
+        if (!warp_wait(&r_empty[at], ((np / kParts) & 1u) ^ 1u, abort_flag, c.status)) break;
+        if (lane == 0) {
+          parts[at] = g;
+          mbar_arrive(&r_full[at]);
+        }
+        __syncwarp();
+        if (!more) break;
         const int32_t* row = c.page_table + (size_t)g.b * c.max_pages;
         auto page_at = [&](int i) {
-          const int j = (g.tile0 + i) * kTile + (lane & 7) * 16;
+          const int j = (g.tile0 + i) * kKeys + (lane & (kPieces - 1)) * 16;
           const bool in = i < g.i1 && j + 15 >= g.lo && j < g.hi;
           const int p = in ? __ldg(row + (j >> c.page_log2)) : -1;
           if (in && (p < 0 || p >= c.n_pages)) set_status(c.status, DEV_ERR_BOUNDS);
@@ -729,10 +726,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             sv = __ldg(c.v_scale + u);
           }
           const int next = page_at(i + 1);
-          const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0) & 0xFFu;
+          const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0) & ((1u << kPieces) - 1u);
           ok = warp_wait(&i_empty[slot], ((n / kInfos) & 1u) ^ 1u, abort_flag, c.status);
           if (!ok) break;
-          if (lane < 8) {
+          if (lane < kPieces) {
             infos[slot].kf[lane] = exp2_byte(sk);
             infos[slot].lv[lane] = (float)((int)sv - 127);
             infos[slot].un[lane] = ex2((float)(127 - (int)sv));
@@ -743,11 +740,76 @@ __global__ void __launch_bounds__(kThreads, 1)
           pg = next;
         }
       }
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------- MMA.  The whole warp walks along and one lane issues, so that
+      // descriptors stay in uniform registers: with one diverged thread an instruction took ~110 cycles to issue, and one
+      // of this size runs for 64.  The order PV0 QK0 PV1 QK1 keeps the M tiles half a turn apart.  A product that
+      // overwrites S starts after the one before it in the stream that reads p' there.
+      const uint32_t id_s = umma_idesc_e4m3(kM, kKeys, false, false), id_o = idesc_pv();
+      const uint64_t desc = umma_desc_sw128(smem_u32(smem));
+      // V16: 64-dim halves kCodeBytes apart (leading), groups of 8 tokens 1 KB apart (stride)
+      const uint64_t vdesc = (desc & ~((uint64_t)0x3FFFu << 16)) | (uint64_t)(kCodeBytes >> 4) << 16;
+      uint32_t n0 = 0, segs = 0;
+      bool ok = true;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      while (ok && reader.next(g, abort_flag, c.status)) {
+        const int tiles = __shfl_sync(0xffffffffu, g.i1 - g.i0, 0);
+        // Step i: the weights of tile i against V (from i = 0 on), then the scores of tile i + kSBufs.  One copy of
+        // either's instructions for all steps and M tiles.
+#pragma unroll 1
+        for (int i = -kSBufs; ok && i < tiles; ++i) {
+          const uint32_t tp = n0 + i, tn = tp + kSBufs;  // number of the tile whose weights, whose scores are next
+          const bool more = i + kSBufs < tiles;
+          if (i >= 0) ok = warp_wait(&v16_full[tp % kV16s], (tp / kV16s) & 1u, abort_flag, c.status);
+          if (ok && more) ok = warp_wait(&k_full[tn % kKStages], (tn / kKStages) & 1u, abort_flag, c.status);
+#pragma unroll 1
+          for (int mt = 0; ok && mt < 2; ++mt) {
+            const uint32_t place = mt * kSBufs + tn % kSBufs, s_at = tm + mt * 128 + (tn % kSBufs) * kKeys;
+            if (i >= 0) {
+              ok = warp_wait(&p_full[place], (tp / kSBufs) & 1u, abort_flag, c.status);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t o = tm + 256 + mt * kHeadDim;
+              const uint64_t bd = vdesc + (uint64_t)(((kV16Off + (tp % kV16s) * kV16Bytes)) >> 4);
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                  umma_f16_ts(o, s_at + 8 * k, bd + (uint64_t)((k * 16 * 128) >> 4), id_o, k > 0 || i > 0);
+                umma_commit(&o_full[place]);
+                if (mt == 1) umma_commit(&v16_empty[tp % kV16s]);
+              }
+              __syncwarp();
+            } else if (i == -kSBufs) {
+              ok = warp_wait(&q_full[mt], segs & 1u, abort_flag, c.status);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            if (more) {
+              const uint64_t bd = desc + (uint64_t)((kKOff + (tn % kKStages) * kCodeBytes) >> 4);
+              const uint64_t ad = desc + (uint64_t)((kQOff + mt * 2 * kTileBytes) >> 4);
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 2 * kHeadDim / 32; ++k)  // the hi half of the queries, then the lo half
+                  umma_e4m3(s_at, ad + (k >> 2) * (kTileBytes >> 4) + 2 * (k & 3), bd + 2 * (k & 3), id_s, k != 0);
+                umma_commit(&s_full[place]);
+                if (mt == 1) umma_commit(&k_empty[tn % kKStages]);
+              }
+              __syncwarp();
+            }
+          }
+        }
+        n0 += tiles;
+        ++segs;
+      }
+      // whatever was issued has finished before tensor memory is given back (after an abort too)
+      if (elect_one()) umma_commit(done);
+      __syncwarp();
+      mbar_wait_tries(done, 0, abort_flag, c.status, false);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -792,7 +854,8 @@ size_t attention_prefill_scratch(int n_sms) {
 
 cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
   CUtensorMap tk, tv;
-  if (!make_cache_map(&tk, c.k_codes, c) || !make_cache_map(&tv, c.v_codes, c)) return cudaErrorInvalidValue;
+  const int box = c.page < kKeys ? c.page : kKeys;
+  if (!make_cache_map(&tk, c.k_codes, c, box) || !make_cache_map(&tv, c.v_codes, c, box)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attention_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
   float* part_o = reinterpret_cast<float*>(a.scratch);

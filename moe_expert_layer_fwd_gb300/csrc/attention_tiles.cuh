@@ -10,7 +10,29 @@ namespace moe {
 
 constexpr int kTile = 128;                        // keys per tile
 constexpr int kTileBytes = kTile * kHeadDim;      // E4M3 codes of one head's keys (or values) of a tile: 16 KB
-constexpr unsigned long long kAttnTimeoutNs = 2000000000ull;
+
+// Waits for the phase with the given parity (whole warp): at most kWaitTries times a suspended try of about a
+// microsecond -- one to two seconds -- or until another role raised the abort flag; then false, and the flag and
+// DEV_ERR_TIMEOUT are set.  Short on purpose: these kernels have some thirty waits in their loops, and instruction fetch
+// is what their loops wait for when each brings a timer's code along.
+constexpr int kWaitTries = 1 << 21;
+__device__ __forceinline__ bool mbar_wait_tries(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status,
+                                                bool honor_abort = true) {
+  bool ok = mbar_try_wait(bar, parity);
+#pragma unroll 1
+  for (int i = 0; !ok && i < kWaitTries; ++i) {
+    if (honor_abort && *abort_flag) return false;
+    ok = mbar_try_wait_sleep(bar, parity, 1000u);
+  }
+  if (!ok) {
+    *abort_flag = 1;
+    set_status(status, DEV_ERR_TIMEOUT);
+  }
+  return ok;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
+  return __all_sync(0xffffffffu, mbar_wait_tries(bar, parity, abort_flag, status));
+}
 
 // The keys that any new token of a sequence sees: [lo, hi), in tiles [tile0, tile0 + nt).  A sequence with new
 // tokens has at least one tile, so that its rows are written even when they see nothing.
