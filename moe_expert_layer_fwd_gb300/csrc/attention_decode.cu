@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       for (int st = 0; st < C::kStages; ++st) {
         const uint32_t fills = n / C::kStages + ((uint32_t)st < n % C::kStages ? 1u : 0u);
         if (!fills) continue;
-        mbar_wait_tries(&k_full[st], (fills - 1u) & 1u, abort_flag, c.status, false);
-        mbar_wait_tries(&v_full[st], (fills - 1u) & 1u, abort_flag, c.status, false);
+        mbar_wait_bounded(&k_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
+        mbar_wait_bounded(&v_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
       }
     }
     __syncwarp();
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       }
       // whatever was issued has finished before tensor memory is given back (after an abort too)
       umma_commit(done);
-      mbar_wait_tries(done, 0, abort_flag, c.status, false);
+      mbar_wait_bounded(done, 0, abort_flag, kAttnTimeoutNs, c.status, false);
     }
     __syncwarp();
   } else if (warp == C::kQWarp) {

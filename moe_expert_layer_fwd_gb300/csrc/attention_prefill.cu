@@ -684,11 +684,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         for (int st = 0; st < kKStages; ++st) {
           const uint32_t fills = n / kKStages + ((uint32_t)st < n % kKStages ? 1u : 0u);
-          if (fills) mbar_wait_tries(&k_full[st], (fills - 1u) & 1u, abort_flag, c.status, false);
+          if (fills) mbar_wait_bounded(&k_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
         }
         for (int st = 0; st < kVStages; ++st) {
           const uint32_t fills = nv / kVStages + ((uint32_t)st < nv % kVStages ? 1u : 0u);
-          if (fills) mbar_wait_tries(&v_full[st], (fills - 1u) & 1u, abort_flag, c.status, false);
+          if (fills) mbar_wait_bounded(&v_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
         }
       }
       __syncwarp();
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // whatever was issued has finished before tensor memory is given back (after an abort too)
       if (elect_one()) umma_commit(done);
       __syncwarp();
-      mbar_wait_tries(done, 0, abort_flag, c.status, false);
+      mbar_wait_bounded(done, 0, abort_flag, kAttnTimeoutNs, c.status, false);
     }
   }
   tc_fence_before();

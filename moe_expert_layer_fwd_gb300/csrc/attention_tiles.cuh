@@ -11,24 +11,29 @@ namespace moe {
 constexpr int kTile = 128;                        // keys per tile
 constexpr int kTileBytes = kTile * kHeadDim;      // E4M3 codes of one head's keys (or values) of a tile: 16 KB
 
-// Waits for the phase with the given parity (whole warp): at most kWaitTries times a suspended try of about a
-// microsecond -- one to two seconds -- or until another role raised the abort flag; then false, and the flag and
-// DEV_ERR_TIMEOUT are set.  Short on purpose: these kernels have some thirty waits in their loops, and instruction fetch
-// is what their loops wait for when each brings a timer's code along.
-constexpr int kWaitTries = 1 << 21;
-__device__ __forceinline__ bool mbar_wait_tries(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status,
-                                                bool honor_abort = true) {
+// Now and then while a wait lasts: has it lasted kAttnTimeoutNs (then the abort flag and DEV_ERR_TIMEOUT are set), or has
+// another role given up?  Not inline: these kernels have some thirty waits in their loops, and with a timer's code in each
+// of them instruction fetch became what the loops waited for.
+constexpr unsigned long long kAttnTimeoutNs = 2000000000ull;
+static __device__ __noinline__ bool wait_is_over(unsigned long long* since, volatile int* abort_flag, unsigned* status) {
+  const unsigned long long now = globaltimer_ns();
+  if (*since == 0) *since = now;
+  if (*abort_flag == 1) return true;
+  if (now - *since < kAttnTimeoutNs) return false;
+  *abort_flag = 1;
+  set_status(status, DEV_ERR_TIMEOUT);
+  return true;
+}
+// Waits for the phase with the given parity to complete; false when it gave up.
+__device__ __forceinline__ bool mbar_wait_tries(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
   bool ok = mbar_try_wait(bar, parity);
+  unsigned long long since = 0;
 #pragma unroll 1
-  for (int i = 0; !ok && i < kWaitTries; ++i) {
-    if (honor_abort && *abort_flag) return false;
-    ok = mbar_try_wait_sleep(bar, parity, 1000u);
+  for (uint32_t i = 1; !ok; ++i) {
+    ok = mbar_try_wait(bar, parity);
+    if ((i & 127u) == 0 && !ok && wait_is_over(&since, abort_flag, status)) return false;
   }
-  if (!ok) {
-    *abort_flag = 1;
-    set_status(status, DEV_ERR_TIMEOUT);
-  }
-  return ok;
+  return true;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
   return __all_sync(0xffffffffu, mbar_wait_tries(bar, parity, abort_flag, status));
