@@ -30,10 +30,18 @@ namespace {
 constexpr int kWholeTiles = 4;    // rows of at most so many tiles are not split
 constexpr int kMinRun = 2;        // tiles in a block's run, at least
 
+struct TileInfo {    // per 16 keys of a tile
+  float kf[8];       // 2^e_k
+  float lv[8];       // e_v
+  float un[8];       // 2^-e_v
+  uint32_t have;     // bit i: the page of keys 16 i .. 16 i + 15 is there
+  uint32_t pad[3];
+};
+
 template <int NC>
 struct Cfg {
   static constexpr int kPerSm = NC == 32 ? 1 : 2;
-  static constexpr int kStages = NC == 32 ? 5 : 3;
+  static constexpr int kStages = NC == 32 ? 5 : NC == 16 ? 2 : 3;
   static constexpr int kQBufs = 2;                          // the next segment's scores start before this one has ended
   static constexpr int kCols = NC == 8 ? 4 : 8;             // columns of a softmax thread
   static constexpr int kGroups = NC / kCols;                // groups of four softmax warps, each with its columns
@@ -44,14 +52,16 @@ struct Cfg {
   static constexpr int kQBytes = kRows * 128;
   static constexpr int kPBlock = kTile * 16;                // the weights of 16 columns: 16 bytes a key
   static constexpr int kPOff = kStages * 2 * kTileBytes;
-  static constexpr int kQOff = kPOff + kRows / 16 * kPBlock;
+  static constexpr int kPBytes = kRows / 16 * kPBlock;
+  static constexpr int kQOff = kPOff + 2 * kPBytes;         // the weights of even and odd tiles
   static constexpr int kBarOff = kQOff + kQBufs * kQBytes;
-  static constexpr int kNumBars = 4 * kStages + 2 * kQBufs + 7;
-  static constexpr int kQfOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // float qf[kQBufs][NC], int token[kQBufs][NC]
+  static constexpr int kNumBars = 4 * kStages + 2 * kQBufs + 9;
+  static constexpr int kInfoOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // TileInfo [kStages]
+  static constexpr int kQfOff = kInfoOff + kStages * (int)sizeof(TileInfo);  // float qf[kQBufs][NC], int token[kQBufs][NC]
   static constexpr int kMaxOff = kQfOff + kQBufs * NC * 8;  // float [3][NC][4]: maxima of even, odd tiles; denominators
   static constexpr int kMiscOff = kMaxOff + 3 * NC * 16;
   static constexpr int kBytes = 1024 + kMiscOff + 64;
-  static constexpr int kTmemCols = 3 * kRows <= 64 ? 64 : (3 * kRows <= 128 ? 128 : 256);  // S twice, O
+  static constexpr int kTmemCols = 4 * kRows;               // S and O, twice each
   static constexpr int kOCol = 2 * kRows;
   static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
@@ -152,6 +162,26 @@ __device__ __forceinline__ void add_product(uint32_t taddr, int lo, float (&acc)
   for (int x = 0; x < N; ++x) acc[x] += __uint_as_float(s[x]) + __uint_as_float(t[x]);
 }
 
+// The warp's maxima of N columns, each lane bringing one value of each: v[0] is that of the returned column.  Lanes halve
+// the columns they keep while they exchange the others, so N columns take N + 2 or so shuffles instead of 5 N.
+template <int N>
+__device__ __forceinline__ int columns_max(float (&v)[N], int lane) {
+  int off = 16, col = 0;
+#pragma unroll
+  for (int half = N / 2; half >= 1; half /= 2, off /= 2) {
+    const bool up = lane & off;
+#pragma unroll
+    for (int x = 0; x < half; ++x) {
+      const float send = up ? v[x] : v[half + x], keep = up ? v[half + x] : v[x];
+      v[x] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, off));
+    }
+    col += up ? half : 0;
+  }
+#pragma unroll
+  for (; off >= 1; off /= 2) v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], off));
+  return col;
+}
+
 template <int NC>
 __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     attention_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -167,9 +197,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
   uint64_t* q_empty = q_full + C::kQBufs;
   uint64_t* s_full = q_empty + C::kQBufs;   // [2]
   uint64_t* s_empty = s_full + 2;           // [2]
-  uint64_t* p_full = s_empty + 2;
-  uint64_t* o_full = p_full + 1;
-  uint64_t* done = o_full + 1;
+  uint64_t* p_full = s_empty + 2;           // [2]
+  uint64_t* o_full = p_full + 2;            // [2]
+  uint64_t* done = o_full + 2;
+  TileInfo* infos = reinterpret_cast<TileInfo*>(smem + C::kInfoOff);
   float* s_qf = reinterpret_cast<float*>(smem + C::kQfOff);
   int* s_tok = reinterpret_cast<int*>(s_qf + C::kQBufs * NC);
   float* s_max = reinterpret_cast<float*>(smem + C::kMaxOff);
@@ -231,9 +262,9 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], C::kSoftWarps);
+      mbar_init(&p_full[i], C::kSoftWarps);
+      mbar_init(&o_full[i], 1);
     }
-    mbar_init(p_full, C::kSoftWarps);
-    mbar_init(o_full, 1);
     mbar_init(done, 1);
     *abort_flag = 0;
     for (int i = 0; i < 3; ++i) s_bad[i] = 0;
@@ -252,42 +283,65 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
   Segment g;
 
   if (warp == C::kTmaWarp) {
-    // ------------------------------------------------------------ TMA: lane = page of the tile
+    // ------------------------------------------------------------ TMA: lane = 16 keys of the tile.  It also brings the scales.
     const uint64_t pol = policy_evict_first();
-    const int pages = kTile >> c.page_log2;
+    const int per_log2 = c.page_log2 - 4;  // lanes of one page
     const uint32_t box = (uint32_t)c.page * kHeadDim;
     uint32_t n = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
       const int32_t* row = c.page_table + (size_t)g.b * c.max_pages;
-      const int end = (g.r.hi + c.page - 1) >> c.page_log2, from = g.r.lo >> c.page_log2;
-      // page of this lane in tile i, read one tile ahead; -1: nothing to load
+      // page of this lane's keys in tile i (-1: none), two tiles ahead; its scales, one ahead
       auto page_at = [&](int i) {
-        const int j = (g.r.tile0 + i) * pages + lane;
-        return lane < pages && i < g.i1 && j >= from && j < end ? __ldg(row + j) : -1;
+        const int j = (g.r.tile0 + i) * kTile + (lane & 7) * 16;
+        const bool in = i < g.i1 && j + 15 >= g.r.lo && j < g.r.hi;
+        const int p = in ? __ldg(row + (j >> c.page_log2)) : -1;
+        if (in && (p < 0 || p >= c.n_pages)) set_status(c.status, DEV_ERR_BOUNDS);
+        return p < c.n_pages ? p : -1;
       };
-      int pg = page_at(g.i0);
+      auto scales_at = [&](int p) {  // key scale | value scale << 8
+        if (p < 0) return 127u | 127u << 8;
+        const size_t u = (size_t)p * c.Hkv + g.h;
+        return (uint32_t)__ldg(c.k_scale + u) | (uint32_t)__ldg(c.v_scale + u) << 8;
+      };
+      int pg = page_at(g.i0), pg1 = page_at(g.i0 + 1);
+      uint32_t sc = scales_at(pg);
+#pragma unroll 1
       for (int i = g.i0; i < g.i1; ++i) {
-        const int next = page_at(i + 1);
-        const bool have = pg >= 0 && pg < c.n_pages;
-        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have)) * box;
+        const int pg2 = page_at(i + 2);
+        const uint32_t sc1 = scales_at(pg1);
         const int st = (int)(n % C::kStages);
         const uint32_t ph = (n / C::kStages) & 1u;
-        uint8_t* dst = smem + st * 2 * kTileBytes + lane * box;
-        const int y = have ? (int)(((long long)pg * c.Hkv + g.h) << c.page_log2) : 0;
-        if (!(ok = warp_wait(&k_empty[st], ph ^ 1u, abort_flag, c.status))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&k_full[st], bytes);
-        __syncwarp();
-        if (have) tma_load_2d(dst, &tm_k, 0, y, &k_full[st], pol);
-        const bool vok = warp_wait(&v_empty[st], ph ^ 1u, abort_flag, c.status);
-        // on a timeout the keys of this stage are still on their way: count the fill, so that the drain waits for it
-        if (lane == 0) mbar_arrive_expect_tx(&v_full[st], vok ? bytes : 0);
-        __syncwarp();
-        if (vok && have) tma_load_2d(dst + kTileBytes, &tm_v, 0, y, &v_full[st], pol);
-        ++n;
-        pg = next;
-        ok = vok;
+        // pages are loaded whole: by the first of a page's lanes that has it (a tile's first page may begin before the keys
+        // that are seen, and its first lanes then have none)
+        const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0) & 0xFFu;
+        const uint32_t group = ((1u << (1 << per_log2)) - 1u) << ((lane & 7) >> per_log2 << per_log2);
+        const bool load = lane < 8 && pg >= 0 && __ffs(have & group) - 1 == lane;
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * box;
+        uint8_t* dst = smem + st * 2 * kTileBytes + ((lane & 7) >> per_log2) * box;
+        const int y = load ? (int)(((long long)pg * c.Hkv + g.h) << c.page_log2) : 0;
+        ok = warp_wait(&k_empty[st], ph ^ 1u, abort_flag, c.status) && warp_wait(&v_empty[st], ph ^ 1u, abort_flag, c.status);
         if (!ok) break;
+        if (lane < 8) {
+          infos[st].kf[lane] = exp2_byte(sc & 255u);
+          infos[st].lv[lane] = (float)((int)(sc >> 8) - 127);
+          infos[st].un[lane] = ex2((float)(127 - (int)(sc >> 8)));
+          if (lane == 0) infos[st].have = have;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&k_full[st], bytes);
+          mbar_arrive_expect_tx(&v_full[st], bytes);
+        }
+        __syncwarp();
+        if (load) {
+          tma_load_2d(dst, &tm_k, 0, y, &k_full[st], pol);
+          tma_load_2d(dst + kTileBytes, &tm_v, 0, y, &v_full[st], pol);
+        }
+        ++n;
+        pg = pg1;
+        pg1 = pg2;
+        sc = sc1;
       }
     }
     // Every copy lands before the block ends.
@@ -301,59 +355,67 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     }
     __syncwarp();
   } else if (warp == C::kMmaWarp) {
-    // ------------------------------------------------------------ MMA: scores run one tile ahead of the weighted sums
-    if (lane == 0) {
-      const uint32_t id_s = umma_idesc_e4m3(kTile, C::kRows, false, false),
-                     id_o = umma_idesc_e4m3(kHeadDim, C::kRows, true, true);
-      const uint64_t desc = umma_desc_sw128(smem_u32(smem));
-      uint32_t nq = 0, segs = 0;
-      bool ok = true, more = walk.next(g);
-      int i = more ? g.i0 : 0;
-      auto scores = [&]() {
-        const int st = (int)(nq % C::kStages), qb = (int)(segs % C::kQBufs), sb = (int)(nq & 1u);
-        if (i == g.i0)
-          ok = ok && mbar_wait_tries(&q_full[qb], (segs / C::kQBufs) & 1u, abort_flag, c.status);
-        ok = ok && mbar_wait_tries(&k_full[st], (nq / C::kStages) & 1u, abort_flag, c.status);
-        ok = ok && mbar_wait_tries(&s_empty[sb], ((nq >> 1) & 1u) ^ 1u, abort_flag, c.status);
-        if (!ok) return;
+    // ------------------------------------------------------------ MMA: scores run one tile ahead of the weighted sums.  The
+    // whole warp walks along and one lane issues: descriptors stay in uniform registers.
+    const uint32_t id_s = umma_idesc_e4m3(kTile, C::kRows, false, false), id_o = umma_idesc_e4m3(kHeadDim, C::kRows, true, true);
+    const uint64_t desc = umma_desc_sw128(smem_u32(smem));
+    const uint64_t pdesc = umma_desc_mn16(smem_u32(smem) + C::kPOff, C::kPBlock);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    uint32_t n = 0, segs = 0;  // n: tiles whose scores were issued
+    bool ok = true, more = walk.next(g);
+    int i = more ? g.i0 : 0;
+#pragma unroll 1
+    for (long long x = -1; ok && x < run; ++x) {
+      if (more) {
+        const int st = (int)(n % C::kStages), qb = (int)(segs % C::kQBufs), sb = (int)(n & 1u);
+        if (i == g.i0) ok = warp_wait(&q_full[qb], (segs / C::kQBufs) & 1u, abort_flag, c.status);
+        ok = ok && warp_wait(&k_full[st], (n / C::kStages) & 1u, abort_flag, c.status) &&
+             warp_wait(&s_empty[sb], ((n >> 1) & 1u) ^ 1u, abort_flag, c.status);
+        if (!ok) break;
         tc_fence_after();
         const uint64_t ad = desc + (uint64_t)((st * 2 * kTileBytes) >> 4);
         const uint64_t bd = desc + (uint64_t)((C::kQOff + qb * C::kQBytes) >> 4);
+        const bool ends = ++i == g.i1;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kHeadDim / 32; ++k)
-          umma_e4m3(tmem + sb * C::kRows, ad + 2 * k, bd + 2 * k, id_s, k != 0);
-        umma_commit(&k_empty[st]);
-        umma_commit(&s_full[sb]);
-        ++nq;
-        if (++i == g.i1) {
-          umma_commit(&q_empty[qb]);
+          for (int k = 0; k < kHeadDim / 32; ++k) umma_e4m3(tm + sb * C::kRows, ad + 2 * k, bd + 2 * k, id_s, k != 0);
+          umma_commit(&k_empty[st]);
+          umma_commit(&s_full[sb]);
+          if (ends) umma_commit(&q_empty[qb]);
+        }
+        __syncwarp();
+        ++n;
+        if (ends) {
           ++segs;
           more = walk.next(g);
           i = more ? g.i0 : 0;
         }
-      };
-      if (more) scores();
-      for (uint32_t n = 0; ok && n < (uint32_t)run; ++n) {
-        if (more) scores();
+      }
+      if (x >= 0) {
+        const uint32_t m = (uint32_t)x, pb = m & 1u;
+        const int st = (int)(m % C::kStages);
+        ok = warp_wait(&v_full[st], (m / C::kStages) & 1u, abort_flag, c.status) &&
+             warp_wait(&p_full[pb], (m >> 1) & 1u, abort_flag, c.status);
         if (!ok) break;
-        const int st = (int)(n % C::kStages);
-        if (!mbar_wait_tries(p_full, n & 1u, abort_flag, c.status)) break;
-        if (!mbar_wait_tries(&v_full[st], (n / C::kStages) & 1u, abort_flag, c.status)) break;
         tc_fence_after();
         // V[token][dim]: the 128-byte rows are the K index, eight rows (1 KB) to a swizzle atom, 32 tokens an MMA
         const uint64_t ad = desc + (uint64_t)((st * 2 * kTileBytes + kTileBytes) >> 4);
-        const uint64_t bd = umma_desc_mn16(smem_u32(smem) + C::kPOff, C::kPBlock);
+        const uint64_t bd = pdesc + (uint64_t)((pb * C::kPBytes) >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kTile / 32; ++k)
-          umma_e4m3(tmem + C::kOCol, ad + (uint64_t)((k * 32 * 128) >> 4), bd + (uint64_t)((k * 32 * 16) >> 4), id_o, k != 0);
-        umma_commit(&v_empty[st]);
-        umma_commit(o_full);
+          for (int k = 0; k < kTile / 32; ++k)
+            umma_e4m3(tm + C::kOCol + pb * C::kRows, ad + (uint64_t)((k * 32 * 128) >> 4), bd + (uint64_t)((k * 32 * 16) >> 4),
+                      id_o, k != 0);
+          umma_commit(&v_empty[st]);
+          umma_commit(&o_full[pb]);
+        }
+        __syncwarp();
       }
-      // whatever was issued has finished before tensor memory is given back (after an abort too)
-      umma_commit(done);
-      mbar_wait_bounded(done, 0, abort_flag, kAttnTimeoutNs, c.status, false);
     }
+    // whatever was issued has finished before tensor memory is given back (after an abort too)
+    if (elect_one()) umma_commit(done);
     __syncwarp();
+    mbar_wait_bounded(done, 0, abort_flag, kAttnTimeoutNs, c.status, false);
   } else if (warp == C::kQWarp) {
     // ------------------------------------------------------------ queries
     uint32_t n = 0;
@@ -418,7 +480,6 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       const int qb = (int)(segs % C::kQBufs);
       const float* qf = s_qf + qb * NC + col0;
       const int* tok = s_tok + qb * NC + col0;
-      const int32_t* row = c.page_table + (size_t)g.b * c.max_pages;
       const int first = g.s.first(), rows = g.s.t1 - g.s.t0;
       const int last = a.causal ? first + rows : g.r.hi;         // one past the last visible key of any row
       const int all_lo = a.window > 0 ? max(0, first + rows - a.window) : 0;  // keys [all_lo, all_hi) are seen by
@@ -428,27 +489,14 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         r[x] = -CUDART_INF_F;
         l[x] = acc[x] = 0.f;
       }
-      auto page_at = [&](int i) {
-        const int j = (g.r.tile0 + i) * kTile + key;
-        const int p = i < g.i1 && j >= g.r.lo && j < g.r.hi ? __ldg(row + (j >> c.page_log2)) : -1;
-        return p < c.n_pages ? p : -1;
-      };
-      auto scales_at = [&](int p) {  // key scale | value scale << 8
-        if (p < 0) return 127u | 127u << 8;
-        const size_t u = (size_t)p * c.Hkv + g.h;
-        return (uint32_t)__ldg(c.k_scale + u) | (uint32_t)__ldg(c.v_scale + u) << 8;
-      };
-      int pg = page_at(g.i0), pg1 = page_at(g.i0 + 1);
-      uint32_t sc = scales_at(pg);
       ok = ok && warp_wait(&q_full[qb], (segs / C::kQBufs) & 1u, abort_flag, c.status);
+#pragma unroll 1
       for (int i = g.i0; i < g.i1; ++i, ++n) {
-        const int pg2 = page_at(i + 2);
-        const uint32_t sc1 = scales_at(pg1);
-        const int j0 = (g.r.tile0 + i) * kTile, j = j0 + key;
-        const bool there = pg >= 0 && j < last;
-        if (j >= g.r.lo && j < g.r.hi && pg < 0) set_status(c.status, DEV_ERR_BOUNDS);
-        const float ks = exp2_byte(sc & 255u);
-        const float lv = (float)((int)(sc >> 8) - 127);
+        const int j0 = (g.r.tile0 + i) * kTile, j = j0 + key, st = (int)(n % C::kStages);
+        // (the keys' barrier is behind the scales; the scores come later)
+        ok = ok && warp_wait(&k_full[st], (n / C::kStages) & 1u, abort_flag, c.status);
+        const float ks = infos[st].kf[key >> 4], lv = infos[st].lv[key >> 4], un = infos[st].un[key >> 4];
+        const bool there = (infos[st].have >> (key >> 4) & 1u) && j < last;
         ok = ok && warp_wait(&s_full[n & 1u], (n >> 1) & 1u, abort_flag, c.status);
         float u[N];
 #pragma unroll
@@ -460,19 +508,23 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&s_empty[n & 1u]);
-        float* tops = s_max + (n & 1u) * NC * 4 + col0 * 4;
         const bool whole = j0 >= all_lo && j0 + kTile <= all_hi;
 #pragma unroll
-        for (int x = 0; x < N; ++x) {
-          u[x] = fmaf(u[x] * ks, qf[x], lv);
-          bool see = there;
-          if (!whole) {
+        for (int x = 0; x < N; ++x) u[x] = there ? fmaf(u[x] * ks, qf[x], lv) : -CUDART_INF_F;
+        if (!whole) {
+#pragma unroll
+          for (int x = 0; x < N; ++x) {
             const int pos = first + tok[x];
-            see = see && (!a.causal || j <= pos) && (a.window == 0 || j > pos - a.window);
+            if ((a.causal && j > pos) || (a.window > 0 && j <= pos - a.window)) u[x] = -CUDART_INF_F;
           }
-          if (!see) u[x] = -CUDART_INF_F;
-          const float top = warp_max(u[x]);
-          if (lane == 0) tops[x * 4 + w4] = top;
+        }
+        float* tops = s_max + (n & 1u) * NC * 4 + col0 * 4;
+        {
+          float v[N];
+#pragma unroll
+          for (int x = 0; x < N; ++x) v[x] = u[x];
+          const int col = columns_max<N>(v, lane);
+          if ((lane & (32 / N - 1)) == 0) tops[col * 4 + w4] = v[0];
         }
         if (lane == 0 && !ok) s_bad[n & 1u] = 1;
         group_sync();
@@ -481,31 +533,18 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           ok = false;
           break;
         }
-        // the weighted sum of the tile before: this thread's dim of its columns
-        if (i > g.i0) {
-          ok = warp_wait(o_full, (n - 1u) & 1u, abort_flag, c.status);
-          if (ok) {
-            tc_fence_after();
-            add_product<N>(mine + C::kOCol, NC, acc);
-            tc_fence_before();
-          }
-        }
-        const float un = ex2(-lv);
-        float top[N];
+        float f[N];
         bool moved = false;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
           const float4 m = *reinterpret_cast<const float4*>(tops + x * 4);
-          top[x] = fmaxf(r[x], fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
-          moved |= top[x] != r[x];
-        }
-        if (moved) {  // the same for the whole group
-#pragma unroll
-          for (int x = 0; x < N; ++x) {
-            const float f = top[x] == -CUDART_INF_F ? 0.f : ex2(r[x] - top[x]);
-            l[x] *= f;
-            acc[x] *= f;
-            r[x] = top[x];
+          const float top = fmaxf(r[x], fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
+          f[x] = 1.f;
+          if (top != r[x]) {  // the same for the whole group
+            moved = true;
+            f[x] = ex2(r[x] - top);
+            l[x] *= f[x];
+            r[x] = top;
           }
         }
         uint32_t hi[N / 4], lo[N / 4];
@@ -524,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           lo[x / 4] = l0 | l1 << 16;
         }
         // 16 columns to a block of 16 bytes a key: the hi parts of all columns, then the lo parts
-        uint8_t* pw = smem + C::kPOff + key * 16;
+        uint8_t* pw = smem + C::kPOff + (n & 1u) * C::kPBytes + key * 16;
 #pragma unroll
         for (int x = 0; x < N / 4; ++x) {
           const int at = col0 + 4 * x;
@@ -534,7 +573,6 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         // A key that no row sees has weight 0, but its value bytes may be anything: 0 * NaN.  They become zeros.
         const bool gone = !there || j < g.r.lo;
         if (group == 0 && ok && __any_sync(0xffffffffu, gone)) {
-          const int st = (int)(n % C::kStages);
           ok = warp_wait(&v_full[st], (n / C::kStages) & 1u, abort_flag, c.status);
           if (ok && gone) {
             uint4* vr = reinterpret_cast<uint4*>(smem + st * 2 * kTileBytes + kTileBytes + key * 128);
@@ -544,15 +582,25 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         }
         fence_async_shared();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(p_full);
-        pg = pg1;
-        pg1 = pg2;
-        sc = sc1;
+        if (ok && lane == 0) mbar_arrive(&p_full[n & 1u]);
+        // While this tile's product runs: the one before, this thread's dim of its columns, and both to the new maxima
+        if (i > g.i0) {
+          ok = ok && warp_wait(&o_full[(n - 1u) & 1u], ((n - 1u) >> 1) & 1u, abort_flag, c.status);
+          if (ok) {
+            tc_fence_after();
+            add_product<N>(mine + C::kOCol + ((n - 1u) & 1u) * C::kRows, NC, acc);
+            tc_fence_before();
+          }
+        }
+        if (moved) {
+#pragma unroll
+          for (int x = 0; x < N; ++x) acc[x] *= f[x];
+        }
       }
-      if (ok) ok = warp_wait(o_full, (n - 1u) & 1u, abort_flag, c.status);
+      if (ok) ok = warp_wait(&o_full[(n - 1u) & 1u], ((n - 1u) >> 1) & 1u, abort_flag, c.status);
       if (ok) {
         tc_fence_after();
-        add_product<N>(mine + C::kOCol, NC, acc);
+        add_product<N>(mine + C::kOCol + ((n - 1u) & 1u) * C::kRows, NC, acc);
         tc_fence_before();
       }
       // the denominators: over the warp, then over the group

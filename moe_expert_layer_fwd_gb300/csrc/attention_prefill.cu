@@ -170,16 +170,6 @@ struct Reader {
   }
 };
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
 __device__ __forceinline__ uint32_t idesc_pv() {
   uint32_t d = 0;
   d |= 1u << 4;                          // D f32, A and B f16

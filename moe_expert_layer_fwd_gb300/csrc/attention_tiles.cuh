@@ -53,6 +53,17 @@ __device__ __forceinline__ KeyRange key_range(const SeqRange& s, const Attention
   return r;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- tcgen05 with E4M3 operands
 // Instruction descriptor of kind::f8f6f4, E4M3 A and B, fp32 accumulator; a_mn, b_mn: A, B stored with M, N
 // contiguous (else K).
