@@ -1,11 +1,81 @@
 // Softmax attention of new queries over the paged 8-bit cache.
-#include "attention_internal.h"
+#include "attention_tiles.cuh"
 
 #include <cudaTypedefs.h>
 
 #include <mutex>
 
 namespace moe {
+namespace {
+
+constexpr int kJoinThreads = 256;
+
+// out = sum_k 2^(r_k - r) o_k / sum_k 2^(r_k - r) l_k over an item's parts, in their order.  kWarps warps share a row and
+// split its parts (few rows, many parts: decoding), or each has a row (kWarps = 1); a lane has four dims.  Blocks whose run
+// (blockIdx.x) does not hold an item's second part have nothing to do.
+template <int kWarps>
+__global__ void __launch_bounds__(kJoinThreads)
+    attention_join_kernel(const KvBatch c, const AttentionArgs a, int rows, const float* part_o, const float2* part_rl,
+                          const JoinInfo* info) {
+  __shared__ float4 s_acc[kJoinThreads];
+  __shared__ float s_sum[kJoinThreads / 32];
+  pdl_wait();
+  const JoinInfo j = info[blockIdx.x];
+  if (!j.split || j.c0 != (int)blockIdx.x - 1) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = c.Hq / c.Hkv;
+  const int row = (int)blockIdx.y * (kJoinThreads / 32 / kWarps) + warp / kWarps, sub = warp % kWarps;
+  const int t0 = __ldg(c.q_start + j.b), t1 = __ldg(c.q_start + j.b + 1);
+  const bool live = row < rows && j.row0 + row < (t1 - t0) * G;
+  auto part = [&](int k) { return (size_t)(2 * k + (k == j.c0 ? j.slot0 : 0)) * rows + row; };
+  float top = -CUDART_INF_F, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
+    for (int k = j.c0 + lane; k <= j.c1; k += 32) top = fmaxf(top, part_rl[part(k)].x);
+    top = warp_max(top);
+    const float ref = top == -CUDART_INF_F ? 0.f : top;
+#pragma unroll 4
+    for (int k = j.c0 + sub; k <= j.c1; k += kWarps) {
+      const float2 rl = part_rl[part(k)];
+      const float4 o = reinterpret_cast<const float4*>(part_o + part(k) * kHeadDim)[lane];
+      const float f = ex2(rl.x - ref);
+      sum = fmaf(rl.y, f, sum);
+      acc.x = fmaf(o.x, f, acc.x);
+      acc.y = fmaf(o.y, f, acc.y);
+      acc.z = fmaf(o.z, f, acc.z);
+      acc.w = fmaf(o.w, f, acc.w);
+    }
+  }
+  if (kWarps > 1) {
+    s_acc[threadIdx.x] = acc;
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 o = s_acc[threadIdx.x + 32 * w];
+      sum += s_sum[warp + w];
+      acc.x += o.x;
+      acc.y += o.y;
+      acc.z += o.z;
+      acc.w += o.w;
+    }
+  }
+  if (!live) return;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  const int rho = j.row0 + row, i = rho / G;
+  uint16_t* out = a.out + ((size_t)(t0 + i) * c.Hq + j.h * G + rho - i * G) * kHeadDim;
+  reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
+}  // namespace
+
+cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int blocks, int rows, const float* part_o,
+                                  const float2* part_rl, const JoinInfo* info, cudaStream_t stream) {
+  constexpr int kAll = kJoinThreads / 32;
+  if (rows <= 32) return launch_kernel(attention_join_kernel<kAll>, dim3(blocks, rows), dim3(kJoinThreads), 0, stream, true, c, a, rows, part_o, part_rl, info);
+  return launch_kernel(attention_join_kernel<1>, dim3(blocks, (rows + kAll - 1) / kAll), dim3(kJoinThreads), 0, stream, true, c, a, rows, part_o, part_rl, info);
+}
+
 bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c, int box_rows) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;

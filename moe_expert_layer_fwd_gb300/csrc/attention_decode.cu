@@ -185,7 +185,8 @@ __device__ __forceinline__ int columns_max(float (&v)[N], int lane) {
 template <int NC>
 __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     attention_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                            const KvBatch c, const AttentionArgs a, int split, float* part_o, float2* part_rl) {
+                            const KvBatch c, const AttentionArgs a, int split, float* part_o, float2* part_rl,
+                            JoinInfo* info) {
   using C = Cfg<NC>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -224,7 +225,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     const long long all = total * c.Hkv, per = tiles_per_block(all, gridDim.x);
     const long long begin = (long long)blockIdx.x * per;
     run = min(per, all - begin);
-    if (run <= 0) return;
+    if (run <= 0) {
+      if (tid == 0) info[blockIdx.x].split = 0;
+      return;
+    }
     if (before * c.Hkv <= begin && begin < (before + mine) * c.Hkv) {
       long long at = before;
       int b = tid * ((c.B + C::kThreads - 1) / C::kThreads), nt;
@@ -236,6 +240,17 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       s_begin[0] = b;
       s_begin[1] = (int)(rel / nt);
       s_begin[2] = (int)(rel % nt);
+      JoinInfo j = {};
+      j.split = s_begin[2] != 0;
+      if (j.split) {
+        const long long i0 = begin - s_begin[2];
+        j.b = b;
+        j.h = s_begin[1];
+        j.c0 = (int)(i0 / per);
+        j.c1 = (int)((i0 + nt - 1) / per);
+        j.slot0 = i0 > j.c0 * per ? 1 : 0;
+      }
+      info[blockIdx.x] = j;
     }
   } else {
     const int b = (int)blockIdx.x / c.Hkv;
@@ -250,7 +265,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&k_full[i], 1);
+      mbar_init(&k_full[i], 2);  // the copies, and the scales
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
@@ -322,13 +337,6 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         const int y = load ? (int)(((long long)pg * c.Hkv + g.h) << c.page_log2) : 0;
         ok = warp_wait(&k_empty[st], ph ^ 1u, abort_flag, c.status) && warp_wait(&v_empty[st], ph ^ 1u, abort_flag, c.status);
         if (!ok) break;
-        if (lane < 8) {
-          infos[st].kf[lane] = exp2_byte(sc & 255u);
-          infos[st].lv[lane] = (float)((int)(sc >> 8) - 127);
-          infos[st].un[lane] = ex2((float)(127 - (int)(sc >> 8)));
-          if (lane == 0) infos[st].have = have;
-        }
-        __syncwarp();
         if (lane == 0) {
           mbar_arrive_expect_tx(&k_full[st], bytes);
           mbar_arrive_expect_tx(&v_full[st], bytes);
@@ -338,6 +346,15 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           tma_load_2d(dst, &tm_k, 0, y, &k_full[st], pol);
           tma_load_2d(dst + kTileBytes, &tm_v, 0, y, &v_full[st], pol);
         }
+        // the scales, which take longer to come than the copies to be issued: the keys' barrier wants them too
+        if (lane < 8) {
+          infos[st].kf[lane] = exp2_byte(sc & 255u);
+          infos[st].lv[lane] = (float)((int)(sc >> 8) - 127);
+          infos[st].un[lane] = ex2((float)(127 - (int)(sc >> 8)));
+          if (lane == 0) infos[st].have = have;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[st]);
         ++n;
         pg = pg1;
         pg1 = pg2;
@@ -648,52 +665,6 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
   }
 }
 
-// Joins the parts of the rows that were split: block (sequence and head, column), thread = dim.
-template <int NC>
-__global__ void __launch_bounds__(kHeadDim)
-    attention_join_kernel(const KvBatch c, const AttentionArgs a, int blocks, const float* part_o, const float2* part_rl) {
-  __shared__ long long s_warp[4];
-  __shared__ long long s_begin;
-  pdl_wait();
-  const int b = (int)blockIdx.x / c.Hkv, h = (int)blockIdx.x - b * c.Hkv, x = (int)blockIdx.y, tid = threadIdx.x;
-  const int G = c.Hq / c.Hkv;
-  long long mine, total;
-  const long long before = scan_tiles(c, a, kHeadDim, s_warp, mine, total);
-  const int share = (c.B + kHeadDim - 1) / kHeadDim;
-  if (tid == b / share) {
-    long long at = before;
-    for (int i = tid * share; i < b; ++i) at += seq_tiles(c, a, i);
-    s_begin = at * c.Hkv;
-  }
-  __syncthreads();
-  SeqRange s;
-  if (!load_seq(c, b, s) || x >= min(NC, (s.t1 - s.t0) * G)) return;
-  const int nt = key_range(s, a).nt;
-  const long long per = tiles_per_block(total * c.Hkv, blocks);
-  const long long i0 = s_begin + (long long)h * nt, i1 = i0 + nt;
-  const long long c0 = i0 / per, c1 = (i1 - 1) / per;
-  if (c0 == c1) return;
-  // the part of block c0 is its last one (slot 1) unless its run begins with this row
-  float top = -CUDART_INF_F;
-  for (long long k = c0; k <= c1; ++k) {
-    const size_t slot = 2 * k + (k == c0 && i0 > c0 * per ? 1 : 0);
-    top = fmaxf(top, part_rl[slot * NC + x].x);
-  }
-  const float ref = top == -CUDART_INF_F ? 0.f : top;
-  float sum = 0.f, acc = 0.f;
-#pragma unroll 4
-  for (long long k = c0; k <= c1; ++k) {
-    const size_t slot = 2 * k + (k == c0 && i0 > c0 * per ? 1 : 0);
-    const float2 rl = part_rl[slot * NC + x];
-    const float f = ex2(rl.x - ref);
-    sum = fmaf(rl.y, f, sum);
-    acc = fmaf(part_o[(slot * NC + x) * kHeadDim + tid], f, acc);
-  }
-  const int i = x / G;
-  a.out[((size_t)(s.t0 + i) * c.Hq + h * G + x - i * G) * kHeadDim + tid] =
-      f32_to_bf16_rne(sum != 0.f ? acc / sum : 0.f);
-}
-
 // The columns' width that holds `cols` of them; 0: too many.
 int width_of(int cols) { return cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 32 ? 32 : 0; }
 
@@ -712,11 +683,11 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   const int blocks = split ? blocks_of(NC, n_sms) : c.B * c.Hkv;
   float* part_o = reinterpret_cast<float*>(a.scratch);
   float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)2 * blocks_of(NC, n_sms) * NC * kHeadDim);
-  e = launch_kernel(kern, dim3(blocks), dim3(C::kThreads), C::kBytes, stream, false, tk, tv, c, a, (int)split, part_o,
-                    part_rl);
+  JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)2 * blocks_of(NC, n_sms) * NC);
+  e = launch_kernel(kern, dim3(blocks), dim3(C::kThreads), C::kBytes, stream, false, tk, tv, c, a, (int)split, part_o, part_rl,
+                    info);
   if (e != cudaSuccess || !split) return e;
-  return launch_kernel(attention_join_kernel<NC>, dim3(c.B * c.Hkv, min(NC, a.max_q * (c.Hq / c.Hkv))), dim3(kHeadDim),
-                       0, stream, true, c, a, blocks, part_o, part_rl);
+  return launch_attention_join(c, a, blocks, NC, part_o, part_rl, info, stream);
 }
 
 }  // namespace
@@ -725,7 +696,7 @@ bool attention_decode_fits(int G, int max_q) { return (long long)G * max_q <= 32
 
 size_t attention_decode_scratch(int G, int max_q, int n_sms) {
   const int nc = width_of(G * max_q);
-  return (size_t)2 * blocks_of(nc, n_sms) * nc * (kHeadDim * sizeof(float) + sizeof(float2));
+  return blocks_of(nc, n_sms) * ((size_t)2 * nc * (kHeadDim * sizeof(float) + sizeof(float2)) + sizeof(JoinInfo));
 }
 
 cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {

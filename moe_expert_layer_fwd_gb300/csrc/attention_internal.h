@@ -64,6 +64,20 @@ cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, in
 size_t attention_prefill_scratch(int n_sms);
 cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
 
+// ---------------------------------------------------------------- rows that were split
+// What block k of a kernel that cuts its work into runs tells the joining kernel: whether its run begins with a part of
+// an item (some rows of one sequence and head) that is not the item's first.  Blocks c0 .. c1 have the item's parts, block
+// k's part is number 2k, but c0's is 2 c0 + slot0 (a run's second kind of part: an item that it does not begin with).
+struct JoinInfo {
+  int split;
+  int b, h, row0;     // rows row0 .. of the sequence's new tokens x grouped heads
+  int c0, c1, slot0;
+  int pad;
+};
+// part_o [parts][rows][128], part_rl [parts][rows]: unscaled sums, their reference exponent r and denominator l.
+cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int blocks, int rows, const float* part_o,
+                                  const float2* part_rl, const JoinInfo* info, cudaStream_t stream);
+
 // The codes as a matrix of 128-byte rows (one token of one head each), boxes of box_rows rows with the 128-byte swizzle.
 bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c, int box_rows);
 

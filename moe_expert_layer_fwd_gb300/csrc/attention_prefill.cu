@@ -277,14 +277,6 @@ __device__ __forceinline__ void rescale_lane64(uint32_t taddr, float f) {
   }
 }
 
-// What a block tells the joining kernel about the part that its run begins with.
-struct JoinInfo {
-  int split;       // the part is not the item's first: blocks c0 .. c1 hold its parts
-  int b, h, qt;
-  int c0, c1, slot0;  // slot0: which part of block c0
-  int pad;
-};
-
 __global__ void __launch_bounds__(kThreads, 1)
     attention_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                              const KvBatch c, const AttentionArgs a, float* part_o, float2* part_rl, JoinInfo* info) {
@@ -370,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long start = begin - rel, last = start + (nt == 1 ? 0 : kItemCost + nt - 1);
         j.b = p.b;
         j.h = s_begin[1];
-        j.qt = qt;
+        j.row0 = qt * kItemRows;
         j.c0 = (int)(start / share);
         j.c1 = (int)(last / share);
         j.slot0 = start > (long long)j.c0 * share ? 1 : 0;
@@ -805,37 +797,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the items that runs cut: block (run, 16 rows), acting where this run holds an item's second part.
-constexpr int kJoinRows = 16;
-__global__ void __launch_bounds__(kHeadDim)
-    attention_join_rows_kernel(const KvBatch c, const AttentionArgs a, const float* part_o, const float2* part_rl,
-                               const JoinInfo* info) {
-  pdl_wait();
-  const JoinInfo j = info[blockIdx.x];
-  if (!j.split || j.c0 != (int)blockIdx.x - 1) return;
-  SeqRange s;
-  if (!load_seq(c, j.b, s)) return;
-  const int G = c.Hq / c.Hkv, rows = (s.t1 - s.t0) * G, tid = threadIdx.x;
-  for (int x = 0; x < kJoinRows; ++x) {
-    const int in_item = (int)blockIdx.y * kJoinRows + x, rho = j.qt * kItemRows + in_item;
-    if (rho >= rows) return;
-    auto part_at = [&](int k) { return (size_t)(2 * k + (k == j.c0 ? j.slot0 : 0)) * kItemRows + in_item; };
-    float top = -CUDART_INF_F;
-    for (int k = j.c0; k <= j.c1; ++k) top = fmaxf(top, part_rl[part_at(k)].x);
-    const float ref = top == -CUDART_INF_F ? 0.f : top;
-    float sum = 0.f, acc = 0.f;
-    for (int k = j.c0; k <= j.c1; ++k) {
-      const float2 rl = part_rl[part_at(k)];
-      const float f = ex2(rl.x - ref);
-      sum = fmaf(rl.y, f, sum);
-      acc = fmaf(part_o[part_at(k) * kHeadDim + tid], f, acc);
-    }
-    const int i = rho / G;
-    a.out[((size_t)(s.t0 + i) * c.Hq + j.h * G + rho - i * G) * kHeadDim + tid] =
-        f32_to_bf16_rne(sum != 0.f ? acc / sum : 0.f);
-  }
-}
-
 }  // namespace
 
 size_t attention_prefill_scratch(int n_sms) {
@@ -854,8 +815,7 @@ cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, i
   e = launch_kernel(attention_prefill_kernel, dim3(n_sms), dim3(kThreads), kBytes, stream, false, tk, tv, c, a, part_o,
                     part_rl, info);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attention_join_rows_kernel, dim3(n_sms, kItemRows / kJoinRows), dim3(kHeadDim), 0, stream, true, c,
-                       a, part_o, part_rl, info);
+  return launch_attention_join(c, a, n_sms, kItemRows, part_o, part_rl, info, stream);
 }
 
 }  // namespace moe
