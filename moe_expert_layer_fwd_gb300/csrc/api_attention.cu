@@ -5,6 +5,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/moe.h"
 #include "attention_internal.h"
 
@@ -16,10 +18,14 @@ constexpr long long kMaxRows = 1LL << 31;
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool ok_ptr(const void* p) { return p && aligned16(p); }
 
+// SMs of the current device, asked once per device.
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

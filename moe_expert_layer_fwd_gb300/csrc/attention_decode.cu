@@ -676,7 +676,8 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   CUtensorMap tk, tv;
   if (!make_cache_map(&tk, c.k_codes, c, c.page) || !make_cache_map(&tv, c.v_codes, c, c.page)) return cudaErrorInvalidValue;
   auto kern = attention_decode_kernel<NC>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::kBytes, allowed);
   if (e != cudaSuccess) return e;
   // Rows of a few tiles at most (the table's width bounds them) are one block's each: nothing to join.
   const bool split = (long long)c.max_pages * c.page > kWholeTiles * kTile;

@@ -807,7 +807,8 @@ cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, i
   CUtensorMap tk, tv;
   const int box = c.page < kKeys ? c.page : kKeys;
   if (!make_cache_map(&tk, c.k_codes, c, box) || !make_cache_map(&tv, c.v_codes, c, box)) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(attention_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(attention_prefill_kernel), kBytes, allowed);
   if (e != cudaSuccess) return e;
   float* part_o = reinterpret_cast<float*>(a.scratch);
   float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)n_sms * 2 * kItemRows * kHeadDim);
