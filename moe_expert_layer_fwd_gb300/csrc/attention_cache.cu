@@ -18,10 +18,11 @@
 namespace moe {
 namespace {
 
-constexpr int kAppendThreads = 512;
+constexpr int kAppendThreads = 128;
 constexpr int kWarps = kAppendThreads / 32;
-constexpr int kRowsPerWarp = 8;    // cache rows of one page a warp holds: 4 steps of 2 rows, 16 lanes x 8 elements each
-constexpr int kQHeads = 8;         // query heads of one token that a warp rotates: 4 steps of 2
+constexpr int kSteps = 4;          // rows of keys (and of values) that a half-warp has in flight: 16 lanes x 8 elements each
+constexpr int kQSteps = 8;         // rows of queries that a half-warp has in flight
+constexpr int kQHeads = 16;        // query heads of one token that a warp rotates, two at a time
 
 // A row in registers: lane l of a half-warp holds elements 8l .. 8l+7.
 __device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
@@ -146,119 +147,130 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= 3.402823466e38f ? a : 0.f;  // infinities and NaN do not set the scale
 }
 
-// Blocks [0, kv_blocks): cache units.  A unit is one touched page of one sequence and one head; page / 8 warps hold
-// its rows.  Sequence b's touched pages take the slots from q_start[b] / page + 2b on: n new tokens touch at most
-// (n - 1) / page + 2 pages, so the slots of different sequences never meet and T / page + 2B of them are enough.
-// Every unit is found from the lengths on the device: the host never needs them.
-// The other blocks: queries, a warp per (token, 8 heads).
-__global__ void __launch_bounds__(kAppendThreads)
-    kv_append_kernel(const KvBatch c, const KvAppendArgs a, int kv_blocks, int slots) {
-  __shared__ float s_amax[2][kWarps];
+// Queries: a warp per (token, 16 heads).
+__global__ void __launch_bounds__(kAppendThreads, 6) rope_queries_kernel(const KvBatch c, const KvAppendArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
+  pdl_launch_dependents();
   Rotary rt;
   rotary_lane(rt, a, l);
-
-  if ((int)blockIdx.x >= kv_blocks) {
-    const int chunks = (c.Hq + kQHeads - 1) / kQHeads;
-    const long long w = (long long)(blockIdx.x - kv_blocks) * kWarps + warp;
-    const int t = (int)(w / chunks), h0 = (int)(w - (long long)t * chunks) * kQHeads;
-    if (t >= c.T) return;
-    const int b = warp_search(c.B, t, [&](int i) { return __ldg(c.q_start + i); });
-    // the rows do not depend on the position: start them before its loads
-    uint4 raw[kQHeads / 2];
+  const int chunks = (c.Hq + kQHeads - 1) / kQHeads;
+  const long long w = (long long)blockIdx.x * kWarps + warp;
+  const int t = (int)(w / chunks), h0 = (int)(w - (long long)t * chunks) * kQHeads + half;
+  if (t >= c.T) return;
+  const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)t * a.q_stride + (size_t)h0 * kHeadDim) + l;
+  // the rows do not depend on the position: start the first of them before its loads
+  uint4 raw[kQSteps];
 #pragma unroll
-    for (int i = 0; i < kQHeads / 2; ++i) {
-      const int h = h0 + 2 * i + half;
-      raw[i] = h < c.Hq ? __ldg(reinterpret_cast<const uint4*>(a.q + (size_t)t * a.q_stride + (size_t)h * kHeadDim) + l)
-                        : make_uint4(0, 0, 0, 0);
-    }
-    SeqRange s;
-    const bool ok = load_seq(c, b, s) && t >= s.t0 && t < s.t1;
-    const int pos = ok ? s.first() + t - s.t0 : -1;
-    if (pos < 0 || pos >= a.max_pos) {
-      if (lane == 0) set_status(c.status, DEV_ERR_BOUNDS);
-      return;
-    }
-    rotary_load(rt, a, l, pos);
-    uint4 own = make_uint4(0, 0, 0, 0);
-    if (a.q_norm) own = __ldg(reinterpret_cast<const uint4*>(a.q_norm) + l);
-    const uint4 other = shfl4(own, rt.partner);
+  for (int i = 0; i < kQSteps; ++i)
+    raw[i] = h0 + 2 * i < c.Hq ? __ldg(src + 2 * i * (kHeadDim / 8)) : make_uint4(0, 0, 0, 0);
+  const int b = warp_search(c.B, t, [&](int i) { return __ldg(c.q_start + i); });
+  SeqRange s;
+  const bool ok = load_seq(c, b, s) && t >= s.t0 && t < s.t1;
+  const int pos = ok ? s.first() + t - s.t0 : -1;
+  if (pos < 0 || pos >= a.max_pos) {
+    if (lane == 0) set_status(c.status, DEV_ERR_BOUNDS);
+    return;
+  }
+  rotary_load(rt, a, l, pos);
+  uint4 own = make_uint4(0, 0, 0, 0);
+  if (a.q_norm) own = __ldg(reinterpret_cast<const uint4*>(a.q_norm) + l);
+  const uint4 other = shfl4(own, rt.partner);
 #pragma unroll
-    for (int i = 0; i < kQHeads / 2; ++i) {
+  for (int i0 = 0; i0 < kQHeads / 2; i0 += kQSteps) {
+#pragma unroll
+    for (int i = 0; i < kQSteps; ++i) {
       float x[8];
       norm_rotate(raw[i], rt, a, a.q_norm != nullptr, own, other, x);
-      const int h = h0 + 2 * i + half;
+      const int next = i0 + kQSteps + i, h = h0 + 2 * (i0 + i);
+      if (next < kQHeads / 2) raw[i] = h0 + 2 * next < c.Hq ? __ldg(src + 2 * next * (kHeadDim / 8)) : make_uint4(0, 0, 0, 0);
       if (h < c.Hq) {
         const uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                                    pack_bf16x2(x[6], x[7]));
         reinterpret_cast<uint4*>(a.q_out + ((size_t)t * c.Hq + h) * kHeadDim)[l] = o;
       }
     }
+  }
+}
+
+// Keys and values: a block per unit, one touched page of one sequence and one head.  Sequence b's touched pages take the
+// slots from q_start[b] / page + 2b on: n new tokens touch at most (n - 1) / page + 2 pages, so the slots of different
+// sequences never meet and T / page + 2B of them are enough.  Every unit is found from the lengths on the device: the host
+// never needs them.  The rotated keys wait in shared memory for their scale; the
+// values are read a second time (from L1 or L2).
+// Launched so that it may overlap the queries' kernel, of which it needs nothing; it ends after it.
+__device__ __forceinline__ void append_unit(const KvBatch& c, const KvAppendArgs& a, float (*s_amax)[kWarps], float4* s_k) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
+  Rotary rt;
+  rotary_lane(rt, a, l);
+  const int slot = (int)blockIdx.x / c.Hkv, h = (int)blockIdx.x - slot * c.Hkv;
+  const int b = warp_search(c.B, slot, [&](int i) { return (__ldg(c.q_start + i) >> c.page_log2) + 2 * i; });
+  SeqRange s;
+  if (!load_seq(c, b, s) || s.t1 == s.t0) return;
+  const int first = s.first(), j = (first >> c.page_log2) + slot - ((s.t0 >> c.page_log2) + 2 * b);
+  if (first < 0 || s.len > a.max_pos) {
+    if (threadIdx.x == 0) set_status(c.status, first < 0 ? DEV_ERR_CONFIG : DEV_ERR_BOUNDS);
     return;
   }
-
-  const int wpu = c.page / kRowsPerWarp;  // warps per unit
-  const int wu = warp % wpu;
-  const int unit = (int)blockIdx.x * (kWarps / wpu) + warp / wpu;
-  const int slot = unit / c.Hkv, h = unit - slot * c.Hkv;
-  // Everything up to the scale is done under `active` without leaving: the block meets at a barrier below.
-  bool active = slot < slots;
-  int b = 0, j = 0, pg = -1;
-  SeqRange s = {0, 0, 0};
-  if (active) {
-    b = warp_search(c.B, slot, [&](int i) { return (__ldg(c.q_start + i) >> c.page_log2) + 2 * i; });
-    active = load_seq(c, b, s) && s.t1 > s.t0;
-    if (active && s.first() < 0) {
-      set_status(c.status, DEV_ERR_CONFIG);
-      active = false;
-    }
-    j = (s.first() >> c.page_log2) + slot - ((s.t0 >> c.page_log2) + 2 * b);
-    active = active && j <= ((s.len - 1) >> c.page_log2) && s.len <= a.max_pos;
-    if (s.t1 > s.t0 && s.len > a.max_pos) set_status(c.status, DEV_ERR_BOUNDS);
-    if (active) active = (pg = load_page(c, b, j)) >= 0;
-  }
-  const int first = s.first();
-  const int p0 = (j << c.page_log2) + wu * kRowsPerWarp + half;  // position of this half-warp's first row
-  const size_t base = ((size_t)(pg < 0 ? 0 : pg) * c.Hkv + h) << c.page_log2;  // the unit's first code row
+  if (j > ((s.len - 1) >> c.page_log2)) return;
+  const int pg = load_page(c, b, j);
+  if (pg < 0) return;
+  const size_t unit = (size_t)pg * c.Hkv + h;
+  const int p0 = j << c.page_log2;                                 // position of the page's first token
+  const int r0 = max(0, first - p0), r1 = min(c.page, s.len - p0);  // its new rows
   int old_k = kMinScaleExp, old_v = kMinScaleExp;
-  const bool partial = active && (j << c.page_log2) < first;
-  if (partial) {
-    old_k = min((int)c.k_scale[(size_t)pg * c.Hkv + h] - 127, 126);
-    old_v = min((int)c.v_scale[(size_t)pg * c.Hkv + h] - 127, 126);
+  if (r0 > 0) {
+    old_k = min((int)c.k_scale[unit] - 127, 126);
+    old_v = min((int)c.v_scale[unit] - 127, 126);
   }
-
-  constexpr int kSteps = kRowsPerWarp / 2;
-  uint4 kr[kSteps], vr[kSteps];
-  float kx[kSteps][8] = {};
-  unsigned here = 0;
-  float amax_k = 0.f, amax_v = 0.f;
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int p = p0 + 2 * i;
-    kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-    if (active && p >= first && p < s.len) {
-      here |= 1u << i;
-      const size_t t = (size_t)(s.t0 + p - first);
-      kr[i] = __ldg(reinterpret_cast<const uint4*>(a.k + t * a.k_stride + (size_t)h * kHeadDim) + l);
-      vr[i] = __ldg(reinterpret_cast<const uint4*>(a.v + t * a.v_stride + (size_t)h * kHeadDim) + l);
-    }
-  }
+  const uint16_t* k_rows = a.k + (size_t)h * kHeadDim + 8 * l;
+  const uint16_t* v_rows = a.v + (size_t)h * kHeadDim + 8 * l;
   uint4 own = make_uint4(0, 0, 0, 0);
   if (a.k_norm) own = __ldg(reinterpret_cast<const uint4*>(a.k_norm) + l);
   const uint4 other = shfl4(own, rt.partner);
+  const bool norm = a.k_norm != nullptr;
+
+  // the first step that has new rows; whole warps, as the shuffles below need both halves
+  const int base0 = r0 / (2 * kWarps) * 2 * kWarps + warp * 2;
+  float amax_k = 0.f, amax_v = 0.f;
+#pragma unroll 1
+  for (int base = base0; base < r1; base += kSteps * 2 * kWarps) {
+    uint4 kr[kSteps], vr[kSteps];
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    // A step that neither half-warp has a row in is skipped whole (the shuffles below need both).
-    if (!__any_sync(0xffffffffu, here >> i & 1)) continue;
-    if (here >> i & 1) rotary_load(rt, a, l, p0 + 2 * i);
-    norm_rotate(kr[i], rt, a, a.k_norm != nullptr, own, other, kx[i]);
-    if (here >> i & 1) {
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = base + half + i * 2 * kWarps;
+      kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+      if (r >= r0 && r < r1) {
+        const size_t t = (size_t)(s.t0 + p0 + r - first);
+        kr[i] = __ldg(reinterpret_cast<const uint4*>(k_rows + t * a.k_stride));
+        vr[i] = __ldg(reinterpret_cast<const uint4*>(v_rows + t * a.v_stride));
+      }
+    }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax_k = fmaxf(amax_k, finite_abs(kx[i][e]));
-      float x[8];
-      unpack8(vr[i], x);
+    for (int i = 0; i < kSteps; ++i) {
+      if (base + i * 2 * kWarps >= r1) break;
+      const int r = base + half + i * 2 * kWarps;
+      const bool here = r >= r0 && r < r1;
+      if (here) rotary_load(rt, a, l, p0 + r);
+      float x[8], v[8];
+      norm_rotate(kr[i], rt, a, norm, own, other, x);
+      unpack8(vr[i], v);
+      // A NaN in a token's value is kept in its key instead, as a NaN key row: the queries that see the token become
+      // NaN through their score, and those that do not are untouched (0 * NaN in the product with V would reach them).
+      bool bad = false;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax_v = fmaxf(amax_v, finite_abs(x[e]));
+      for (int e = 0; e < 8; ++e) {
+        bad |= v[e] != v[e] || x[e] != x[e];
+        amax_k = fmaxf(amax_k, finite_abs(x[e]));
+        amax_v = fmaxf(amax_v, finite_abs(v[e]));
+      }
+      if (__ballot_sync(0xffffffffu, bad) >> (16 * half) & 0xFFFFu) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __int_as_float(0x7FFFFFFF);
+      }
+      if (here) {
+        s_k[(r * 2) * 16 + l] = make_float4(x[0], x[1], x[2], x[3]);
+        s_k[(r * 2 + 1) * 16 + l] = make_float4(x[4], x[5], x[6], x[7]);
+      }
     }
   }
 #pragma unroll
@@ -271,53 +283,56 @@ __global__ void __launch_bounds__(kAppendThreads)
     s_amax[1][warp] = amax_v;
   }
   __syncthreads();
-  if (!active) return;
-  const int w0 = warp - wu;
-  for (int i = 0; i < wpu; ++i) {
-    amax_k = fmaxf(amax_k, s_amax[0][w0 + i]);
-    amax_v = fmaxf(amax_v, s_amax[1][w0 + i]);
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    amax_k = fmaxf(amax_k, s_amax[0][i]);
+    amax_v = fmaxf(amax_v, s_amax[1][i]);
   }
   const int ek = max(scale_exponent(amax_k), old_k), ev = max(scale_exponent(amax_v), old_v);
-  if (wu == 0 && lane == 0) {
-    c.k_scale[(size_t)pg * c.Hkv + h] = (uint8_t)(ek + 127);
-    c.v_scale[(size_t)pg * c.Hkv + h] = (uint8_t)(ev + 127);
+  if (threadIdx.x == 0) {
+    c.k_scale[unit] = (uint8_t)(ek + 127);
+    c.v_scale[unit] = (uint8_t)(ev + 127);
   }
-  const float ik = exp2_int(-ek), iv = exp2_int(-ev);
+  const float inv_k = exp2_int(-ek), inv_v = exp2_int(-ev);
+  // new tokens: each half-warp its own rows again
+#pragma unroll 4
+  for (int r = base0 + half; r < r1; r += 2 * kWarps) {
+    if (r < r0) continue;
+    const uint4 vr = __ldg(reinterpret_cast<const uint4*>(v_rows + (size_t)(s.t0 + p0 + r - first) * a.v_stride));
+    const float4 x0 = s_k[(r * 2) * 16 + l], x1 = s_k[(r * 2 + 1) * 16 + l];
+    const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    float v[8];
+    unpack8(vr, v);
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int p = p0 + 2 * i;
-    const size_t row = base + (size_t)(wu * kRowsPerWarp + half + 2 * i);
-    uint2* kc = reinterpret_cast<uint2*>(c.k_codes + row * kHeadDim) + l;
-    uint2* vc = reinterpret_cast<uint2*>(c.v_codes + row * kHeadDim) + l;
-    // A NaN in a token's value is kept in its key instead, as a NaN key row: the queries that see the token become
-    // NaN through their score, and those that do not are untouched (0 * NaN in the product with V would reach them).
-    float x[8];
-    unpack8(vr[i], x);
-    bool bad = false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      bad |= x[e] != x[e] || kx[i][e] != kx[i][e];
-      if (x[e] != x[e]) x[e] = 0.f;
-    }
-    const unsigned mask = __ballot_sync(0xffffffffu, (here >> i & 1) && bad);
-    if (here >> i & 1) {
-      uint2 o = quantise8(kx[i], ik);
-      if (mask >> (16 * half) & 0xFFFFu) o = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-      *kc = o;
-      *vc = quantise8(x, iv);
-    } else if (partial && p < first) {
+    for (int e = 0; e < 8; ++e) v[e] = v[e] != v[e] ? 0.f : v[e];
+    const size_t row = ((unit << c.page_log2) + r) * kHeadDim;
+    reinterpret_cast<uint2*>(c.k_codes + row)[l] = quantise8(x, inv_k);
+    reinterpret_cast<uint2*>(c.v_codes + row)[l] = quantise8(v, inv_v);
+  }
+  // earlier tokens of the page, when the scale grew
+  if (ek > old_k || ev > old_v) {
+    const float fk = exp2_int(max(old_k - ek, -126)), fv = exp2_int(max(old_v - ev, -126));
+    for (int r = warp * 2 + half; r < r0; r += 2 * kWarps) {
+      const size_t row = ((unit << c.page_log2) + r) * kHeadDim;
       if (ek > old_k) {
-        const float f = exp2_int(max(old_k - ek, -126));
+        uint2* kc = reinterpret_cast<uint2*>(c.k_codes + row) + l;
         const uint2 o = *kc;
-        *kc = make_uint2(rescale4(o.x, f), rescale4(o.y, f));
+        *kc = make_uint2(rescale4(o.x, fk), rescale4(o.y, fk));
       }
       if (ev > old_v) {
-        const float f = exp2_int(max(old_v - ev, -126));
+        uint2* vc = reinterpret_cast<uint2*>(c.v_codes + row) + l;
         const uint2 o = *vc;
-        *vc = make_uint2(rescale4(o.x, f), rescale4(o.y, f));
+        *vc = make_uint2(rescale4(o.x, fv), rescale4(o.y, fv));
       }
     }
   }
+}
+
+__global__ void __launch_bounds__(kAppendThreads, 5) kv_append_kernel(const KvBatch c, const KvAppendArgs a) {
+  extern __shared__ float4 s_k[];  // the page's new keys, rotated: [row][2][16 lanes]
+  __shared__ float s_amax[2][kWarps];
+  append_unit(c, a, s_amax, s_k);
+  pdl_wait();
 }
 
 constexpr int kGatherRowsPerBlock = 32;
@@ -395,12 +410,16 @@ __global__ void rope_table_kernel(int max_pos, int rot, double base, float* cos_
 
 cudaError_t launch_kv_append(const KvBatch& c, const KvAppendArgs& a, cudaStream_t stream) {
   const long long slots = (long long)c.T / c.page + 2LL * c.B;
-  const int per_block = kWarps / (c.page / kRowsPerWarp);
-  const long long kv_blocks = (slots * c.Hkv + per_block - 1) / per_block;
-  const long long chunks = (c.Hq + kQHeads - 1) / kQHeads;
-  const long long q_blocks = a.q ? ((long long)c.T * chunks + kWarps - 1) / kWarps : 0;
-  kv_append_kernel<<<(unsigned)(kv_blocks + q_blocks), kAppendThreads, 0, stream>>>(c, a, (int)kv_blocks, (int)slots);
-  return cudaGetLastError();
+  if (a.q) {
+    const long long chunks = (c.Hq + kQHeads - 1) / kQHeads, blocks = ((long long)c.T * chunks + kWarps - 1) / kWarps;
+    const cudaError_t e = launch_kernel(rope_queries_kernel, dim3((unsigned)blocks), dim3(kAppendThreads), 0, stream, false, c, a);
+    if (e != cudaSuccess) return e;
+  }
+  const int bytes = c.page * kHeadDim * (int)sizeof(float);
+  static std::atomic<unsigned long long> allowed{0};
+  const cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kv_append_kernel), 128 * kHeadDim * (int)sizeof(float), allowed);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kv_append_kernel, dim3((unsigned)(slots * c.Hkv)), dim3(kAppendThreads), bytes, stream, a.q != nullptr, c, a);
 }
 
 cudaError_t launch_kv_gather(const KvBatch& c, const int32_t* start, const int32_t* out_start, int n_rows, uint16_t* k,

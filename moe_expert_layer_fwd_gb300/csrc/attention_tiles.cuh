@@ -6,8 +6,6 @@
 
 #include <math_constants.h>
 
-#include <atomic>
-
 namespace moe {
 
 constexpr int kTile = 128;                        // keys per tile
@@ -141,18 +139,6 @@ __device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uin
   hi = e4m3x2(a, b);
   const float2 h = e4m3x2_f32(hi);
   lo = e4m3x2(a - h.x, b - h.y);
-}
-
-// Host: gives a kernel its dynamic shared memory, once per device (`done`: one bit each, a static of the caller's).
-inline cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<unsigned long long>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
 }
 
 }  // namespace moe
