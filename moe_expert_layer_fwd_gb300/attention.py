@@ -172,6 +172,8 @@ def moe_kv_gather(cache: KVCache, start, out_start, page_table, n_rows: int, k=N
     n_pages, Hkv, page, D = cache[0].shape
     table, B, max_pages = _table(page_table)
     shape = (n_rows, Hkv, D)
+    if k is None and v is None:
+        k, v = _new(stream, page_table, (2,) + shape, b.bf16).unbind(0)
     k = _new(stream, page_table, shape, b.bf16) if k is None else k
     v = _new(stream, page_table, shape, b.bf16) if v is None else v
     ws = _status_ws(page_table, ws)

@@ -29,6 +29,9 @@ namespace {
 
 constexpr int kWholeTiles = 4;    // rows of at most so many tiles are not split
 constexpr int kMinRun = 2;        // tiles in a block's run, at least
+// p' = 2^(u - r + kBase) with u <= r + kSlack stays below 448, the largest E4M3 number (2^8.8); r itself moves so
+// seldom that the sums in tensor memory are hardly ever rescaled.
+constexpr float kBase = 6.f, kSlack = 2.75f;
 
 struct TileInfo {    // per 16 keys of a tile
   float kf[8];       // 2^e_k
@@ -41,9 +44,9 @@ struct TileInfo {    // per 16 keys of a tile
 template <int NC>
 struct Cfg {
   static constexpr int kPerSm = NC == 32 ? 1 : 2;
-  static constexpr int kStages = NC == 32 ? 5 : NC == 16 ? 2 : 3;
+  static constexpr int kStages = NC == 8 ? 3 : NC == 32 ? 5 : 2;
   static constexpr int kQBufs = 2;                          // the next segment's scores start before this one has ended
-  static constexpr int kCols = NC == 8 ? 4 : 8;             // columns of a softmax thread
+  static constexpr int kCols = NC == 32 ? 8 : NC / 2;       // columns of a softmax thread (16 do not fit its registers)
   static constexpr int kGroups = NC / kCols;                // groups of four softmax warps, each with its columns
   static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kQWarp = kSoftWarps + 2;
@@ -61,7 +64,7 @@ struct Cfg {
   static constexpr int kMaxOff = kQfOff + kQBufs * NC * 8;  // float [3][NC][4]: maxima of even, odd tiles; denominators
   static constexpr int kMiscOff = kMaxOff + 3 * NC * 16;
   static constexpr int kBytes = 1024 + kMiscOff + 64;
-  static constexpr int kTmemCols = 4 * kRows;               // S and O, twice each
+  static constexpr int kTmemCols = NC == 24 ? 256 : 4 * kRows;  // S twice, O (a power of two)
   static constexpr int kOCol = 2 * kRows;
   static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
@@ -149,17 +152,37 @@ __device__ __forceinline__ long long tiles_per_block(long long n, int blocks) {
 // acc[x] += column x + column `lo` + x of this thread's tensor-memory lane.
 template <int N>
 __device__ __forceinline__ void add_product(uint32_t taddr, int lo, float (&acc)[N]) {
-  uint32_t s[N], t[N];
-  if constexpr (N == 4) {
-    tmem_ld4_async(taddr, s);
-    tmem_ld4_async(taddr + lo, t);
-  } else {
-    tmem_ld8_async(taddr, s);
-    tmem_ld8_async(taddr + lo, t);
-  }
-  tmem_wait_ld();
+  constexpr int kStep = N % 8 ? 4 : 8;
 #pragma unroll
-  for (int x = 0; x < N; ++x) acc[x] += __uint_as_float(s[x]) + __uint_as_float(t[x]);
+  for (int y = 0; y < N; y += kStep) {
+    uint32_t s[kStep], t[kStep];
+    tmem_ld_async(taddr + y, s);
+    tmem_ld_async(taddr + lo + y, t);
+    tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < kStep; ++x) acc[y + x] += __uint_as_float(s[x]) + __uint_as_float(t[x]);
+  }
+}
+
+// Columns x and `lo` + x of this thread's tensor-memory lane, times f[x].
+template <int N>
+__device__ __forceinline__ void scale_columns(uint32_t taddr, int lo, const float (&f)[N]) {
+  constexpr int kStep = N % 8 ? 4 : 8;
+#pragma unroll
+  for (int y = 0; y < N; y += kStep) {
+    uint32_t s[kStep], t[kStep];
+    tmem_ld_async(taddr + y, s);
+    tmem_ld_async(taddr + lo + y, t);
+    tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < kStep; ++x) {
+      s[x] = __float_as_uint(__uint_as_float(s[x]) * f[y + x]);
+      t[x] = __float_as_uint(__uint_as_float(t[x]) * f[y + x]);
+    }
+    tmem_st(taddr + y, s);
+    tmem_st(taddr + lo + y, t);
+  }
+  tmem_wait_st();
 }
 
 // The warp's maxima of N columns, each lane bringing one value of each: v[0] is that of the returned column.  Lanes halve
@@ -379,6 +402,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     const uint64_t pdesc = umma_desc_mn16(smem_u32(smem) + C::kPOff, C::kPBlock);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     uint32_t n = 0, segs = 0;  // n: tiles whose scores were issued
+    uint32_t begins = 0;       // bit m & 1: tile m is its segment's first
     bool ok = true, more = walk.next(g);
     int i = more ? g.i0 : 0;
 #pragma unroll 1
@@ -392,6 +416,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         tc_fence_after();
         const uint64_t ad = desc + (uint64_t)((st * 2 * kTileBytes) >> 4);
         const uint64_t bd = desc + (uint64_t)((C::kQOff + qb * C::kQBytes) >> 4);
+        begins = (begins & ~(1u << sb)) | (i == g.i0 ? 1u : 0u) << sb;
         const bool ends = ++i == g.i1;
         if (elect_one()) {
 #pragma unroll
@@ -418,11 +443,12 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         // V[token][dim]: the 128-byte rows are the K index, eight rows (1 KB) to a swizzle atom, 32 tokens an MMA
         const uint64_t ad = desc + (uint64_t)((st * 2 * kTileBytes + kTileBytes) >> 4);
         const uint64_t bd = pdesc + (uint64_t)((pb * C::kPBytes) >> 4);
+        const bool adds = !(begins >> pb & 1u);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTile / 32; ++k)
-            umma_e4m3(tm + C::kOCol + pb * C::kRows, ad + (uint64_t)((k * 32 * 128) >> 4), bd + (uint64_t)((k * 32 * 16) >> 4),
-                      id_o, k != 0);
+            umma_e4m3(tm + C::kOCol, ad + (uint64_t)((k * 32 * 128) >> 4), bd + (uint64_t)((k * 32 * 16) >> 4), id_o,
+                      k != 0 || adds);
           umma_commit(&v_empty[st]);
           umma_commit(&o_full[pb]);
         }
@@ -438,44 +464,52 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     uint32_t n = 0;
     while (walk.next(g)) {
       const int qb = (int)(n % C::kQBufs), rows = g.s.t1 - g.s.t0, cols = min(NC, rows * G);
-      uint2 raw[NC];
+      constexpr int kAtOnce = 8;  // rows
+      uint2 raw[kAtOnce];
+      auto load = [&](int x0) {
 #pragma unroll
-      for (int x = 0; x < NC; ++x) {
-        raw[x] = make_uint2(0, 0);
-        if (x < cols) {
-          const int i = x / G;
-          raw[x] = __ldg(reinterpret_cast<const uint2*>(a.q + (size_t)(g.s.t0 + i) * a.q_stride +
-                                                       (size_t)(g.h * G + x - i * G) * kHeadDim) + lane);
+        for (int x = 0; x < kAtOnce; ++x) {
+          raw[x] = make_uint2(0, 0);
+          if (x0 + x < cols) {
+            const int i = (x0 + x) / G;
+            raw[x] = __ldg(reinterpret_cast<const uint2*>(a.q + (size_t)(g.s.t0 + i) * a.q_stride +
+                                                         (size_t)(g.h * G + x0 + x - i * G) * kHeadDim) + lane);
+          }
         }
-      }
+      };
+      load(0);
       if (!warp_wait(&q_empty[qb], ((n / C::kQBufs) & 1u) ^ 1u, abort_flag, c.status)) break;
       uint8_t* op = smem + C::kQOff + qb * C::kQBytes;
+#pragma unroll 1
+      for (int x0 = 0; x0 < NC; x0 += kAtOnce) {
+        if (x0 > 0) load(x0);
 #pragma unroll
-      for (int x = 0; x < NC; ++x) {
-        const float v[4] = {bf16_lo(raw[x].x), bf16_hi(raw[x].x), bf16_lo(raw[x].y), bf16_hi(raw[x].y)};
-        float top = 0.f;
-        bool bad = false;
+        for (int x = 0; x < kAtOnce; ++x) {
+          const float v[4] = {bf16_lo(raw[x].x), bf16_hi(raw[x].x), bf16_lo(raw[x].y), bf16_hi(raw[x].y)};
+          float top = 0.f;
+          bool bad = false;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float m = fabsf(v[e]);
-          bad |= !(m <= 3.402823466e38f);
-          top = fmaxf(top, m);
-        }
-        top = warp_max(top);
-        bad = __any_sync(0xffffffffu, bad);
-        const int e = bad ? 0 : query_exponent(top);
-        const float inv = exp2_int(-e);
-        uint32_t h0, l0, h1, l1;
-        split_e4m3x2(v[0] * inv, v[1] * inv, h0, l0);
-        split_e4m3x2(v[2] * inv, v[3] * inv, h1, l1);
-        uint32_t hi = h0 | (h1 << 16), lo = l0 | (l1 << 16);
-        if (bad) hi = lo = 0x7F7F7F7Fu;  // a row with an infinity or NaN has NaN scores
-        const uint32_t sw = ((((uint32_t)lane >> 2) ^ (x & 7)) << 4) + (lane & 3) * 4;
-        *reinterpret_cast<uint32_t*>(op + x * 128 + sw) = hi;
-        *reinterpret_cast<uint32_t*>(op + (NC + x) * 128 + sw) = lo;
-        if (lane == 0) {
-          s_qf[qb * NC + x] = a.scale_log2 * exp2_int(e);
-          s_tok[qb * NC + x] = x < cols ? x / G : 0;
+          for (int e = 0; e < 4; ++e) {
+            const float m = fabsf(v[e]);
+            bad |= !(m <= 3.402823466e38f);
+            top = fmaxf(top, m);
+          }
+          top = warp_max(top);
+          bad = __any_sync(0xffffffffu, bad);
+          const int e = bad ? 0 : query_exponent(top);
+          const float inv = exp2_int(-e);
+          uint32_t h0, l0, h1, l1;
+          split_e4m3x2(v[0] * inv, v[1] * inv, h0, l0);
+          split_e4m3x2(v[2] * inv, v[3] * inv, h1, l1);
+          uint32_t hi = h0 | (h1 << 16), lo = l0 | (l1 << 16);
+          if (bad) hi = lo = 0x7F7F7F7Fu;  // a row with an infinity or NaN has NaN scores
+          const uint32_t sw = ((((uint32_t)lane >> 2) ^ (x & 7)) << 4) + (lane & 3) * 4;
+          *reinterpret_cast<uint32_t*>(op + (x0 + x) * 128 + sw) = hi;
+          *reinterpret_cast<uint32_t*>(op + (NC + x0 + x) * 128 + sw) = lo;
+          if (lane == 0) {
+            s_qf[qb * NC + x0 + x] = a.scale_log2 * exp2_int(e);
+            s_tok[qb * NC + x0 + x] = x0 + x < cols ? (x0 + x) / G : 0;
+          }
         }
       }
       if (rows * G > NC && lane == 0) set_status(c.status, DEV_ERR_CONFIG);  // more new tokens than max_q
@@ -492,7 +526,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     bool ok = true;
     const uint32_t mine = tmem + ((uint32_t)(w4 * 32) << 16) + col0;  // this thread's lane and columns
     auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };
-    float r[N], l[N], acc[N];
+    float r[N], l[N];
     while (walk.next(g)) {
       const int qb = (int)(segs % C::kQBufs);
       const float* qf = s_qf + qb * NC + col0;
@@ -504,7 +538,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
 #pragma unroll
       for (int x = 0; x < N; ++x) {
         r[x] = -CUDART_INF_F;
-        l[x] = acc[x] = 0.f;
+        l[x] = 0.f;
       }
       ok = ok && warp_wait(&q_full[qb], (segs / C::kQBufs) & 1u, abort_flag, c.status);
 #pragma unroll 1
@@ -536,12 +570,14 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           }
         }
         float* tops = s_max + (n & 1u) * NC * 4 + col0 * 4;
-        {
-          float v[N];
+        constexpr int kStep = N % 8 ? 4 : 8;
 #pragma unroll
-          for (int x = 0; x < N; ++x) v[x] = u[x];
-          const int col = columns_max<N>(v, lane);
-          if ((lane & (32 / N - 1)) == 0) tops[col * 4 + w4] = v[0];
+        for (int y = 0; y < N; y += kStep) {
+          float v[kStep];
+#pragma unroll
+          for (int x = 0; x < kStep; ++x) v[x] = u[y + x];
+          const int col = y + columns_max<kStep>(v, lane);
+          if ((lane & (32 / kStep - 1)) == 0) tops[col * 4 + w4] = v[0];
         }
         if (lane == 0 && !ok) s_bad[n & 1u] = 1;
         group_sync();
@@ -550,18 +586,28 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           ok = false;
           break;
         }
+        // The reference follows the maximum when that has grown by more than kSlack (the same for the whole group)
         float f[N];
         bool moved = false;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
           const float4 m = *reinterpret_cast<const float4*>(tops + x * 4);
-          const float top = fmaxf(r[x], fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
+          const float top = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w));
           f[x] = 1.f;
-          if (top != r[x]) {  // the same for the whole group
+          if (top > r[x] + kSlack || (r[x] == -CUDART_INF_F && top > r[x])) {
             moved = true;
             f[x] = ex2(r[x] - top);
             l[x] *= f[x];
             r[x] = top;
+          }
+        }
+        if (moved && i > g.i0) {
+          // the sums so far, of which the tile before is the last, to the new reference: this thread's dim of its columns
+          ok = ok && warp_wait(&o_full[(n - 1u) & 1u], ((n - 1u) >> 1) & 1u, abort_flag, c.status);
+          if (ok) {
+            tc_fence_after();
+            scale_columns<N>(mine + C::kOCol, NC, f);
+            tc_fence_before();
           }
         }
         uint32_t hi[N / 4], lo[N / 4];
@@ -570,7 +616,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           float p[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            p[y] = ex2(u[x + y] - (r[x + y] == -CUDART_INF_F ? 0.f : r[x + y]) + 8.f);
+            p[y] = ex2(u[x + y] - (r[x + y] == -CUDART_INF_F ? 0.f : r[x + y]) + kBase);
             l[x + y] = fmaf(p[y], un, l[x + y]);
           }
           uint32_t h0, l0, h1, l1;
@@ -579,7 +625,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           hi[x / 4] = h0 | h1 << 16;
           lo[x / 4] = l0 | l1 << 16;
         }
-        // 16 columns to a block of 16 bytes a key: the hi parts of all columns, then the lo parts
+        // 16 columns to a block of 16 bytes a key: the hi parts of all columns, then the lo parts.  (The product that read
+        // these bytes two tiles ago was issued before this tile's scores, so it has finished.)
         uint8_t* pw = smem + C::kPOff + (n & 1u) * C::kPBytes + key * 16;
 #pragma unroll
         for (int x = 0; x < N / 4; ++x) {
@@ -600,24 +647,14 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         fence_async_shared();
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&p_full[n & 1u]);
-        // While this tile's product runs: the one before, this thread's dim of its columns, and both to the new maxima
-        if (i > g.i0) {
-          ok = ok && warp_wait(&o_full[(n - 1u) & 1u], ((n - 1u) >> 1) & 1u, abort_flag, c.status);
-          if (ok) {
-            tc_fence_after();
-            add_product<N>(mine + C::kOCol + ((n - 1u) & 1u) * C::kRows, NC, acc);
-            tc_fence_before();
-          }
-        }
-        if (moved) {
-#pragma unroll
-          for (int x = 0; x < N; ++x) acc[x] *= f[x];
-        }
       }
       if (ok) ok = warp_wait(&o_full[(n - 1u) & 1u], ((n - 1u) >> 1) & 1u, abort_flag, c.status);
+      float acc[N];
+#pragma unroll
+      for (int x = 0; x < N; ++x) acc[x] = 0.f;
       if (ok) {
         tc_fence_after();
-        add_product<N>(mine + C::kOCol + ((n - 1u) & 1u) * C::kRows, NC, acc);
+        add_product<N>(mine + C::kOCol, NC, acc);
         tc_fence_before();
       }
       // the denominators: over the warp, then over the group
@@ -666,7 +703,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
 }
 
 // The columns' width that holds `cols` of them; 0: too many.
-int width_of(int cols) { return cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 32 ? 32 : 0; }
+int width_of(int cols) { return cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 24 ? 24 : cols <= 32 ? 32 : 0; }
 
 int blocks_of(int nc, int n_sms) { return n_sms * (nc == 32 ? 1 : 2); }
 
@@ -704,6 +741,7 @@ cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, in
   switch (width_of(c.Hq / c.Hkv * a.max_q)) {
     case 8: return launch<8>(c, a, n_sms, stream);
     case 16: return launch<16>(c, a, n_sms, stream);
+    case 24: return launch<24>(c, a, n_sms, stream);
     default: return launch<32>(c, a, n_sms, stream);
   }
 }

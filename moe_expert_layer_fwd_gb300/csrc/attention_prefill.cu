@@ -16,7 +16,7 @@
 // (one at each end of a run, at most) are joined by a second kernel.
 //
 // Warps (24): 0-7 and 8-15 softmax of the M tiles (thread = row and half of a tile's keys; they also load the queries,
-// rescale and write the output), 16-19 values, 20 TMA, 21 MMA, 22 scales of the tiles' pages, 23 walks the run.  Registers: 96 a
+// rescale and write the output), 16-19 values, 20 TMA, 21 MMA, 22 scales of the tiles' pages, 23 walks the run.  Registers: 208 a
 // thread for the softmax, 48 for the rest.  Every wait is bounded (2 s).
 #include "attention_tiles.cuh"
 
@@ -199,7 +199,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float d;
@@ -267,13 +266,11 @@ __device__ __forceinline__ void rescale_lane64(uint32_t taddr, float f) {
 #pragma unroll
   for (int x = 0; x < 64; x += 8) {
     uint32_t o[8];
-    tmem_ld8_async(taddr + x, o);
+    tmem_ld_async(taddr + x, o);
     tmem_wait_ld();
 #pragma unroll
     for (int y = 0; y < 8; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr + x), "r"(o[0]),
-                 "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                 : "memory");
+    tmem_st(taddr + x, o);
   }
 }
 
@@ -413,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Part g;
 
   if (warp < kSoftWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------ softmax: thread = row of M tile mt
     const int mt = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -578,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp < kTmaWarp) {
       // ---------------------------------------------------------- values: E4M3 -> f16, keys nobody sees -> zeros
       uint32_t n = 0;
