@@ -43,10 +43,10 @@ struct TileInfo {    // per 16 keys of a tile
 
 template <int NC>
 struct Cfg {
-  static constexpr int kPerSm = NC == 32 ? 1 : 2;
-  static constexpr int kStages = NC == 8 ? 3 : NC == 32 ? 5 : 2;
+  static constexpr int kPerSm = NC >= 24 ? 1 : 2;
+  static constexpr int kStages = NC == 8 ? 3 : NC >= 24 ? 5 : 2;
   static constexpr int kQBufs = 2;                          // the next segment's scores start before this one has ended
-  static constexpr int kCols = NC == 32 ? 8 : NC / 2;       // columns of a softmax thread (16 do not fit its registers)
+  static constexpr int kCols = NC % 16 ? 4 : 8;             // columns of a softmax thread
   static constexpr int kGroups = NC / kCols;                // groups of four softmax warps, each with its columns
   static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kQWarp = kSoftWarps + 2;
@@ -587,18 +587,23 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           break;
         }
         // The reference follows the maximum when that has grown by more than kSlack (the same for the whole group)
-        float f[N];
+        // (without a branch per column, which would have each of these loads wait for the one before)
+        float top[N], f[N];
         bool moved = false;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
           const float4 m = *reinterpret_cast<const float4*>(tops + x * 4);
-          const float top = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w));
-          f[x] = 1.f;
-          if (top > r[x] + kSlack || (r[x] == -CUDART_INF_F && top > r[x])) {
-            moved = true;
-            f[x] = ex2(r[x] - top);
+          const float t = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w));
+          const bool up = t > r[x] + kSlack;  // r = -infinity: any finite t
+          top[x] = up ? t : r[x];
+          moved |= up;
+        }
+        if (moved) {
+#pragma unroll
+          for (int x = 0; x < N; ++x) {
+            f[x] = top[x] == r[x] ? 1.f : ex2(r[x] - top[x]);
             l[x] *= f[x];
-            r[x] = top;
+            r[x] = top[x];
           }
         }
         if (moved && i > g.i0) {
@@ -705,7 +710,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
 // The columns' width that holds `cols` of them; 0: too many.
 int width_of(int cols) { return cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 24 ? 24 : cols <= 32 ? 32 : 0; }
 
-int blocks_of(int nc, int n_sms) { return n_sms * (nc == 32 ? 1 : 2); }
+int blocks_of(int nc, int n_sms) { return n_sms * (nc >= 24 ? 1 : 2); }
 
 template <int NC>
 cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
