@@ -76,7 +76,7 @@ cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int 
   return launch_kernel(attention_join_kernel<1>, dim3(blocks, (rows + kAll - 1) / kAll), dim3(kJoinThreads), 0, stream, true, c, a, rows, part_o, part_rl, info);
 }
 
-bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c, int box_rows) {
+bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -89,7 +89,7 @@ bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c, int 
   if (!encode) return false;
   const cuuint64_t rows = (cuuint64_t)(c.n_pages > 0 ? c.n_pages : 1) * c.Hkv * c.page;
   const cuuint64_t dims[2] = {kHeadDim, rows}, strides[1] = {kHeadDim};
-  const cuuint32_t box[2] = {kHeadDim, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {kHeadDim, (cuuint32_t)c.page}, step[2] = {1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -99,7 +99,7 @@ bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c, int 
 // the large operand reads the cache at its rate; above, a 128-row product is no longer mostly padding.
 size_t attention_scratch_bytes(int Hq, int Hkv, int max_q, int n_sms) {
   const int G = Hq / Hkv;
-  return attention_decode_fits(G, max_q) ? attention_decode_scratch(G, max_q, n_sms) : attention_prefill_scratch(n_sms);
+  return attention_decode_fits(G, max_q) ? attention_decode_scratch(G, max_q, n_sms) : attention_prefill_scratch(G, max_q, n_sms);
 }
 
 cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {

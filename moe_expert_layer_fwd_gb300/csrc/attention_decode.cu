@@ -716,7 +716,7 @@ template <int NC>
 cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
   using C = Cfg<NC>;
   CUtensorMap tk, tv;
-  if (!make_cache_map(&tk, c.k_codes, c, c.page) || !make_cache_map(&tv, c.v_codes, c, c.page)) return cudaErrorInvalidValue;
+  if (!make_cache_map(&tk, c.k_codes, c) || !make_cache_map(&tv, c.v_codes, c)) return cudaErrorInvalidValue;
   auto kern = attention_decode_kernel<NC>;
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::kBytes, allowed);

@@ -61,7 +61,7 @@ size_t attention_decode_scratch(int G, int max_q, int n_sms);
 cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
 
 // Any number of rows.
-size_t attention_prefill_scratch(int n_sms);
+size_t attention_prefill_scratch(int G, int max_q, int n_sms);
 cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
 
 // ---------------------------------------------------------------- rows that were split
@@ -78,7 +78,7 @@ struct JoinInfo {
 cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int blocks, int rows, const float* part_o,
                                   const float2* part_rl, const JoinInfo* info, cudaStream_t stream);
 
-// The codes as a matrix of 128-byte rows (one token of one head each), boxes of box_rows rows with the 128-byte swizzle.
-bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c, int box_rows);
+// The codes as a matrix of 128-byte rows (one token of one head each), boxes of one page with the 128-byte swizzle.
+bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c);
 
 }  // namespace moe

@@ -28,21 +28,12 @@ constexpr int kValWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kScaleWarp = 14;
 constexpr int kThreads = 512;
 constexpr int kReaders = kSoftWarps + 4 + 1 + 1;  // warps that read the run's parts
 constexpr int kM = 128;
-constexpr int kItemRows = 2 * kM;
-constexpr int kKeys = 128;                 // keys of a tile
-constexpr int kSBufs = 1;                  // places in tensor memory for an M tile's scores
-constexpr int kCodeBytes = kKeys * kHeadDim; // a tile's codes of keys or values: 8 KB
-constexpr int kKStages = 3, kVStages = 2, kV16s = 2, kInfos = 4, kParts = 4;
+constexpr int kKeys = kTile;                 // keys of a tile
+constexpr int kInfos = 4, kParts = 2;
 constexpr int kPieces = kKeys / 16;
-constexpr int kMinRun = 4;   // cost of a block's run, at least
-constexpr int kItemCost = 3;  // an item's own cost (loading its queries, writing its rows), in tiles
+constexpr int kMinRun = 4;                   // cost of a block's run, at least
+constexpr int kItemCost = 3;                 // an item's own cost (loading its queries, writing its rows), in tiles
 
-constexpr int kQOff = 0;                                 // [2 tiles][hi, lo][128 rows of 128 bytes]
-constexpr int kKOff = kQOff + 4 * kTileBytes;
-constexpr int kVOff = kKOff + kKStages * kCodeBytes;     // E4M3 as cached
-constexpr int kV16Off = kVOff + kVStages * kCodeBytes;   // f16 [2 halves of the dims][64 tokens of 128 bytes]
-constexpr int kV16Bytes = 2 * kCodeBytes;
-constexpr int kInfoOff = kV16Off + kV16s * kV16Bytes;
 struct TileInfo {    // per 16 keys of a tile
   float kf[8];       // 2^e_k
   float lv[8];       // e_v
@@ -50,21 +41,39 @@ struct TileInfo {    // per 16 keys of a tile
   uint32_t have;     // bit i: the page of keys 16 i .. 16 i + 15 is there
   uint32_t pad[3];
 };
-struct Part {  // an item (rows [256 qt, 256 qt + 256) of a sequence's n * G for head h) and the tiles [i0, i1) of it in this run
+struct Part {  // an item (rows [qt * kRows, (qt + 1) * kRows) of a sequence's n * G for head h) and its tiles [i0, i1) in this run
   int b, h, qt, i0, i1, nt, tile0, lo, hi;  // keys [lo, hi) are seen by some row; nt == 0: the run is over
   int later;                                // not the item that the run begins in
   int t0, n, first;                         // first new token, new tokens, position of the first
   int pad[3];
 };
-constexpr int kPartOff = kInfoOff + kInfos * (int)sizeof(TileInfo);
-constexpr int kBarOff = kPartOff + kParts * (int)sizeof(Part);
-constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * kV16s + 2 * kInfos + 2 * kParts + 2 + 6 * kSBufs + 1;
-constexpr int kMiscOff = kBarOff + kNumBars * 8;
-constexpr int kBytes = 1024 + kMiscOff + 128;
-static_assert(kBytes <= 232448, "shared memory");
 
+// kSplit: both M tiles hold the same 128 rows and take an item's key tiles in turn (else 256 rows, the same tiles).
+template <bool kSplit>
+struct Cfg {
+  static constexpr int kRows = kSplit ? kM : 2 * kM;   // rows of an item
+  static constexpr int kStep = kSplit ? 2 : 1;         // tiles that the two M tiles take at a time
+  static constexpr int kKStages = kSplit ? 4 : 3, kVStages = 2, kV16s = kSplit ? 3 : 2;
+  static constexpr int kQOff = 0;                      // [hi, lo][128 rows of 128 bytes], one for each M tile unless kSplit
+  static constexpr int kKOff = kQOff + (kSplit ? 2 : 4) * kTileBytes;
+  static constexpr int kVOff = kKOff + kKStages * kTileBytes;     // E4M3 as cached
+  static constexpr int kV16Off = kVOff + kVStages * kTileBytes;   // f16 [2 halves of the dims][128 tokens of 128 bytes]
+  static constexpr int kV16Bytes = 2 * kTileBytes;
+  static constexpr int kInfoOff = kV16Off + kV16s * kV16Bytes;
+  static constexpr int kPartOff = kInfoOff + kInfos * (int)sizeof(TileInfo);
+  static constexpr int kRlOff = kPartOff + kParts * (int)sizeof(Part);  // kSplit: float2 [128], M tile 1's r and l
+  static constexpr int kBarOff = kRlOff + (kSplit ? kM * 8 : 0);
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * kV16s + 2 * kInfos + 2 * kParts + 2 + 2 + 2 + 2 + 2 + 1;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr int kBytes = 1024 + kMiscOff + 32;
+  static_assert(kBytes <= 232448, "shared memory");
+  // Tiles of a part, made whole steps: one past its end is there, and empty.
+  static __device__ __forceinline__ int tiles(const Part& g) { return (g.i1 - g.i0 + kStep - 1) / kStep * kStep; }
+};
+
+template <int kRows>
 __device__ __forceinline__ void item_range(const SeqRange& s, const AttentionArgs& a, int G, int qt, int& lo, int& hi) {
-  const int i_min = qt * kItemRows / G, i_max = min(s.t1 - s.t0 - 1, (qt * kItemRows + kItemRows - 1) / G);
+  const int i_min = qt * kRows / G, i_max = min(s.t1 - s.t0 - 1, (qt * kRows + kRows - 1) / G);
   hi = a.causal ? max(0, min(s.len, s.first() + i_max + 1)) : s.len;
   lo = a.window > 0 ? max(0, s.first() + i_min - a.window + 1) : 0;
 }
@@ -72,14 +81,17 @@ __device__ __forceinline__ int item_tiles(int lo, int hi) { return max(1, (hi + 
 
 __device__ __forceinline__ int item_cost(int nt) { return nt > 0 ? nt + kItemCost : 0; }
 
-// Sequence b's items take the places from q_start[b] * G / 256 + b on (some stay empty), so that a place's item is
+// Sequence b's items take the places from q_start[b] * G / kRows + b on (some stay empty), so that a place's item is
 // found without a table of all of them.
+template <int kRows>
 __device__ __forceinline__ int place_of(const KvBatch& c, int G, int b) {
-  return (int)((long long)__ldg(c.q_start + b) * G / kItemRows) + b;
+  return (int)((long long)__ldg(c.q_start + b) * G / kRows) + b;
 }
-__device__ __forceinline__ int places(const KvBatch& c, int G) { return (int)((long long)c.T * G / kItemRows) + c.B; }
+template <int kRows>
+__device__ __forceinline__ int places(const KvBatch& c, int G) { return (int)((long long)c.T * G / kRows) + c.B; }
 
 // Walks places in order.
+template <int kRows>
 struct Places {
   const KvBatch& c;
   const AttentionArgs& a;
@@ -90,21 +102,21 @@ struct Places {
     int lo = 0, hi = c.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (place_of(c, G, mid) <= place) lo = mid; else hi = mid;
+      if (place_of<kRows>(c, G, mid) <= place) lo = mid; else hi = mid;
     }
     b = lo;
     ok = load_seq(c, b, s);
   }
   // tiles of the item at this place (0: empty), for one head
   __device__ int tiles(int& qt, int& lo, int& hi) const {
-    qt = place - place_of(c, G, b);
-    if (!ok || qt < 0 || (long long)qt * kItemRows >= (long long)(s.t1 - s.t0) * G) return 0;
-    item_range(s, a, G, qt, lo, hi);
+    qt = place - place_of<kRows>(c, G, b);
+    if (!ok || qt < 0 || (long long)qt * kRows >= (long long)(s.t1 - s.t0) * G) return 0;
+    item_range<kRows>(s, a, G, qt, lo, hi);
     return item_tiles(lo, hi);
   }
   __device__ void next() {
     ++place;
-    if (b + 1 < c.B && place_of(c, G, b + 1) <= place) {
+    if (b + 1 < c.B && place_of<kRows>(c, G, b + 1) <= place) {
       ++b;
       ok = load_seq(c, b, s);
     }
@@ -117,12 +129,13 @@ __device__ __forceinline__ int first_tile_from(long long rel, int nt) {
   return rel <= 0 ? 0 : (int)min((long long)nt, max(1LL, rel - kItemCost));
 }
 
+template <int kRows>
 struct Walk {
-  Places p;
+  Places<kRows> p;
   long long left, rel;  // cost left in the run; where it starts in the present item
   int h, end, later = 0;
   __device__ Walk(const KvBatch& c, const AttentionArgs& a, int G, long long n, int place, int h_, int rel_)
-      : p(c, a, G, place), left(n), rel(rel_), h(h_), end(places(c, G)) {}
+      : p(c, a, G, place), left(n), rel(rel_), h(h_), end(places<kRows>(c, G)) {}
   __device__ bool next(Part& g) {
     while (left > 0 && p.place < end) {
       g.nt = p.tiles(g.qt, g.lo, g.hi);
@@ -274,31 +287,36 @@ __device__ __forceinline__ void rescale_lane64(uint32_t taddr, float f) {
   }
 }
 
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                              const KvBatch c, const AttentionArgs a, float* part_o, float2* part_rl, JoinInfo* info) {
+  using C = Cfg<kSplit>;
+  constexpr int kRows = C::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  TileInfo* infos = reinterpret_cast<TileInfo*>(smem + kInfoOff);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + kBarOff);
-  uint64_t* k_empty = k_full + kKStages;
-  uint64_t* v_full = k_empty + kKStages;
-  uint64_t* v_empty = v_full + kVStages;
-  uint64_t* v16_full = v_empty + kVStages;
-  uint64_t* v16_empty = v16_full + kV16s;
-  uint64_t* i_full = v16_empty + kV16s;
+  TileInfo* infos = reinterpret_cast<TileInfo*>(smem + C::kInfoOff);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* k_empty = k_full + C::kKStages;
+  uint64_t* v_full = k_empty + C::kKStages;
+  uint64_t* v_empty = v_full + C::kVStages;
+  uint64_t* v16_full = v_empty + C::kVStages;
+  uint64_t* v16_empty = v16_full + C::kV16s;
+  uint64_t* i_full = v16_empty + C::kV16s;
   uint64_t* i_empty = i_full + kInfos;
   uint64_t* r_full = i_empty + kInfos;
   uint64_t* r_empty = r_full + kParts;
-  uint64_t* q_full = r_empty + kParts;       // [2], by M tile
-  uint64_t* s_full = q_full + 2;             // [2 M tiles][kSBufs], as the next two
-  uint64_t* p_full = s_full + 2 * kSBufs;
-  uint64_t* o_full = p_full + 2 * kSBufs;
-  uint64_t* done = o_full + 2 * kSBufs;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
-  int* s_begin = reinterpret_cast<int*>(smem + kMiscOff + 8);  // place, head, cost into the item
-  Part* parts = reinterpret_cast<Part*>(smem + kPartOff);
+  uint64_t* q_full = r_empty + kParts;       // [2], by M tile, as the next three
+  uint64_t* s_full = q_full + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* x_full = o_full + 2;             // kSplit: M tile 1's sums are in the queries' place
+  uint64_t* x_empty = x_full + 1;            // that place is free
+  uint64_t* done = x_empty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+  int* s_begin = reinterpret_cast<int*>(smem + C::kMiscOff + 8);  // place, head, cost into the item
+  Part* parts = reinterpret_cast<Part*>(smem + C::kPartOff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = c.Hq / c.Hkv;
   pdl_launch_dependents();
@@ -307,12 +325,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long run;
   {
     long long* s_warp = reinterpret_cast<long long*>(smem);
-    const int n = places(c, G), per = (n + kThreads - 1) / kThreads;
+    const int n = places<kRows>(c, G), per = (n + kThreads - 1) / kThreads;
     const int p0 = min(n, tid * per), p1 = min(n, p0 + per);
     long long mine = 0;
     int qt, lo, hi;
     if (p0 < p1) {
-      Places p(c, a, G, p0);
+      Places<kRows> p(c, a, G, p0);
 #pragma unroll 1
       for (; p.place < p1; p.next()) mine += item_cost(p.tiles(qt, lo, hi));
     }
@@ -338,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return;
     }
     if (before * c.Hkv <= begin && begin < (before + mine) * c.Hkv) {
-      Places p(c, a, G, p0);
+      Places<kRows> p(c, a, G, p0);
       long long at = before;
       int nt;
       for (;; p.next()) {
@@ -359,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long start = begin - rel, last = start + (nt == 1 ? 0 : kItemCost + nt - 1);
         j.b = p.b;
         j.h = s_begin[1];
-        j.row0 = qt * kItemRows;
+        j.row0 = qt * kRows;
         j.c0 = (int)(start / share);
         j.c1 = (int)(last / share);
         j.slot0 = start > (long long)j.c0 * share ? 1 : 0;
@@ -369,33 +387,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (tid == 0) {
-    for (int i = 0; i < kKStages; ++i) {
+    // who reads a stage: both M tiles' products (the second one's commit tells), or one's
+    for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
     }
-    for (int i = 0; i < kVStages; ++i) {
+    for (int i = 0; i < C::kVStages; ++i) {
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 4);
     }
-    for (int i = 0; i < kInfos; ++i) {
-      mbar_init(&i_full[i], 1);
-      mbar_init(&i_empty[i], kSoftWarps + 4);
-    }
-    for (int i = 0; i < kV16s; ++i) {
+    for (int i = 0; i < C::kV16s; ++i) {
       mbar_init(&v16_full[i], 4);
       mbar_init(&v16_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 4);
-    mbar_init(done, 1);
-    for (int i = 0; i < 2 * kSBufs; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&o_full[i], 1);
+    for (int i = 0; i < kInfos; ++i) {
+      mbar_init(&i_full[i], 1);
+      mbar_init(&i_empty[i], (kSplit ? 4 : 8) + 4);
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&r_full[i], 1);
       mbar_init(&r_empty[i], kReaders);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(x_full, 4);
+    mbar_init(x_empty, 4);
+    mbar_init(done, 1);
     *abort_flag = 0;
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -415,10 +436,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int mt = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t t_s = lanes + mt * 128, t_o = lanes + 256 + mt * kHeadDim;
-    uint32_t n = 0;
+    uint32_t n0 = 0, steps = 0, xs = 0;  // tiles of earlier parts; steps of this M tile; uses of the queries' place for sums
     bool ok = true;
     while (ok && reader.next(g, abort_flag, c.status)) {
-      const int rho = g.qt * kItemRows + mt * kM + row;
+      const int row0 = g.qt * kRows + (kSplit ? 0 : mt * kM);  // this M tile's first
+      const int rho = row0 + row;
       const bool live = rho < g.n * G;
       const int i_row = rho / G, head = g.h * G + rho - i_row * G;
       const int pos = g.first + i_row;
@@ -437,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = bad ? 0 : query_exponent(__uint_as_float(top << 16));
         const float inv = exp2_int(-e);
         qf = a.scale_log2 * exp2_int(e);
-        uint8_t* hi_row = smem + kQOff + mt * 2 * kTileBytes + row * 128;
+        uint8_t* hi_row = smem + C::kQOff + (kSplit ? 0 : mt * 2 * kTileBytes) + row * 128;
+        if (!kSplit || mt == 0) {
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
           const uint32_t w[8] = {raw[2 * x].x, raw[2 * x].y, raw[2 * x].z, raw[2 * x].w,
@@ -458,25 +481,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[mt]);
+        }
       }
       // keys [w_lo, w_hi) are seen by every row of this warp
-      const int warp_rho = g.qt * kItemRows + warp * 32;
+      const int warp_rho = row0 + quarter * 32, tiles = C::tiles(g);
       const int w_hi = a.causal ? min(g.hi, g.first + warp_rho / G + 1) : g.hi;
       const int w_lo = a.window > 0 ? g.first + (warp_rho + 31) / G - a.window + 1 : 0;
       float r = -CUDART_INF_F, l = 0.f;
-      for (int i = g.i0; i < g.i1; ++i, ++n) {
+#pragma unroll 1
+      for (int x = kSplit ? mt : 0; x < tiles; x += C::kStep, ++steps) {
+        const int i = g.i0 + x;
+        const uint32_t n = n0 + x;
         const int slot = (int)(n % kInfos);
-        const uint32_t sb = n % kSBufs, bar = mt * kSBufs + sb;
         ok = warp_wait(&i_full[slot], (n / kInfos) & 1u, abort_flag, c.status) &&
-             warp_wait(&s_full[bar], (n / kSBufs) & 1u, abort_flag, c.status);
+             warp_wait(&s_full[mt], steps & 1u, abort_flag, c.status);
         if (!ok) break;
         const TileInfo& ti = infos[slot];
         const uint32_t have = ti.have;
         tc_fence_after();
-        const uint32_t t_s2 = t_s + sb * kKeys;
         uint32_t s[kKeys / 32][32];
 #pragma unroll
-        for (int w = 0; w < kKeys / 32; ++w) tmem_ld32_async(t_s2 + 32 * w, s[w]);
+        for (int w = 0; w < kKeys / 32; ++w) tmem_ld32_async(t_s + 32 * w, s[w]);
         float kf[kPieces], lv[kPieces];
 #pragma unroll
         for (int b = 0; b < kPieces; ++b) {
@@ -499,9 +524,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int b = 0; b < kPieces; ++b) m = fmaxf(m, fmaf(max16(&s[b >> 1][(b & 1) * 16]), kf[b], lv[b]));
         const bool grow = m > r + 8.f || (r == -CUDART_INF_F && m > r);
-        if (i > g.i0 && __any_sync(0xffffffffu, grow)) {
+        if (x >= C::kStep && __any_sync(0xffffffffu, grow)) {
           // the sums so far are of the tile before: wait for its product, then bring them to the new reference
-          ok = warp_wait(&o_full[mt * kSBufs + (n - 1u) % kSBufs], ((n - 1u) / kSBufs) & 1u, abort_flag, c.status);
+          ok = warp_wait(&o_full[mt], (steps - 1u) & 1u, abort_flag, c.status);
           if (!ok) break;
           tc_fence_after();
           const float f = grow ? ex2(r - m) : 1.f;
@@ -532,46 +557,103 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = fmaf(s0 + s1, ti.un[b], l);
         }
 #pragma unroll
-        for (int w = 0; w < kKeys / 64; ++w) tmem_st32(t_s2 + 32 * w, s[w]);  // over the scores
+        for (int w = 0; w < kKeys / 64; ++w) tmem_st32(t_s + 32 * w, s[w]);  // over the scores
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&p_full[bar]);
+          mbar_arrive(&p_full[mt]);
           mbar_arrive(&i_empty[slot]);
         }
       }
+      n0 += tiles;
       // ---- the rows' outputs
-      ok = ok && warp_wait(&o_full[mt * kSBufs + (n - 1u) % kSBufs], ((n - 1u) / kSBufs) & 1u, abort_flag, c.status);
+      ok = ok && warp_wait(&o_full[mt], (steps - 1u) & 1u, abort_flag, c.status);
       if (!ok) break;
       tc_fence_after();
       const bool complete = g.i0 == 0 && g.i1 == g.nt;
-      const float inv = complete ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
-      const size_t part = (size_t)(2 * (int)blockIdx.x + g.later) * kItemRows + mt * kM + row;
+      const size_t part = (size_t)(2 * (int)blockIdx.x + g.later) * kRows + (kSplit ? 0 : mt * kM) + row;
       uint16_t* out = a.out + ((size_t)(g.t0 + i_row) * c.Hq + head) * kHeadDim;
-      if (!complete) part_rl[part] = make_float2(r, l);
-#pragma unroll
-      for (int x = 0; x < kHeadDim; x += 32) {
-        uint32_t o[32];
-        tmem_ld32_async(t_o + x, o);
-        tmem_wait_ld();
+      // kSplit: M tile 1 puts its r and l, and its sums in two halves of the dims, where the queries were once both tiles'
+      // scores are done with them; M tile 0 adds them to its own.  A row's 16-byte pieces are rotated by the row.
+      float2* other_rl = reinterpret_cast<float2*>(smem + C::kRlOff) + row;
+      float4* sums = reinterpret_cast<float4*>(smem + C::kQOff) + row * 16;
+      float f = 1.f, f1 = 0.f;
+      if (kSplit && mt == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x_empty);
+      }
+      if (kSplit && mt == 1) *other_rl = make_float2(r, l);
+      auto write = [&](int d, const float (&o)[32], float inv) {  // dims d .. d + 31 of this row
         if (complete) {
           if (live) {
 #pragma unroll
-            for (int y = 0; y < 32; y += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z)
-                w[z] = pack_bf16x2(__uint_as_float(o[y + 2 * z]) * inv, __uint_as_float(o[y + 2 * z + 1]) * inv);
-              *reinterpret_cast<uint4*>(out + x + y) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int y = 0; y < 32; y += 8)
+              *reinterpret_cast<uint4*>(out + d + y) =
+                  make_uint4(pack_bf16x2(o[y] * inv, o[y + 1] * inv), pack_bf16x2(o[y + 2] * inv, o[y + 3] * inv),
+                             pack_bf16x2(o[y + 4] * inv, o[y + 5] * inv), pack_bf16x2(o[y + 6] * inv, o[y + 7] * inv));
           }
         } else {
 #pragma unroll
           for (int y = 0; y < 32; y += 4)
-            *reinterpret_cast<uint4*>(part_o + part * kHeadDim + x + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            *reinterpret_cast<float4*>(part_o + part * kHeadDim + d + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
         }
+      };
+      float inv = l != 0.f ? 1.f / l : 0.f;
+      if (!complete && !kSplit) part_rl[part] = make_float2(r, l);
+#pragma unroll 1
+      for (int d = 0; d < kHeadDim; d += 32) {
+        uint32_t v[32];
+        tmem_ld32_async(t_o + d, v);
+        tmem_wait_ld();
+        float o[32];
+#pragma unroll
+        for (int y = 0; y < 32; ++y) o[y] = __uint_as_float(v[y]);
+        if (!kSplit) {
+          write(d, o, inv);
+          continue;
+        }
+        const int piece0 = (d & 32) / 4;
+        if (mt == 1) {
+          if ((d & 32) == 0) {
+            ok = warp_wait(x_empty, xs & 1u, abort_flag, c.status);
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            sums[(piece0 + y) ^ (row & 15)] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          __syncwarp();
+          if ((d & 32) && lane == 0) mbar_arrive(x_full);
+        } else {
+          if ((d & 32) == 0) {
+            ok = warp_wait(x_full, xs & 1u, abort_flag, c.status);
+            if (!ok) break;
+          }
+          if (d == 0) {
+            const float2 rl = *other_rl;
+            const float top = fmaxf(r, rl.x), ref = top == -CUDART_INF_F ? 0.f : top;
+            f = ex2(r - ref);
+            f1 = ex2(rl.x - ref);
+            l = l * f + rl.y * f1;
+            r = top;
+            inv = l != 0.f ? 1.f / l : 0.f;
+            if (!complete) part_rl[part] = make_float2(r, l);
+          }
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const float4 w = sums[(piece0 + y) ^ (row & 15)];
+            o[4 * y] = o[4 * y] * f + w.x * f1;
+            o[4 * y + 1] = o[4 * y + 1] * f + w.y * f1;
+            o[4 * y + 2] = o[4 * y + 2] * f + w.z * f1;
+            o[4 * y + 3] = o[4 * y + 3] * f + w.w * f1;
+          }
+          write(d, o, inv);
+          __syncwarp();
+          if (d == 32 && lane == 0) mbar_arrive(x_empty);
+        }
+        if (d & 32) ++xs;
       }
+      if (!ok) break;
       tc_fence_before();
     }
   } else {
@@ -582,16 +664,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const int w = warp - kValWarp;
       while (ok && reader.next(g, abort_flag, c.status)) {
-        for (int i = g.i0; i < g.i1; ++i, ++n) {
-          const int st = (int)(n % kVStages), slot = (int)(n % kInfos);
+        for (int i = g.i0; i < g.i0 + C::tiles(g); ++i, ++n) {
+          const int st = (int)(n % C::kVStages), slot = (int)(n % kInfos);
           ok = warp_wait(&i_full[slot], (n / kInfos) & 1u, abort_flag, c.status) &&
-               warp_wait(&v_full[st], (n / kVStages) & 1u, abort_flag, c.status) &&
-               warp_wait(&v16_empty[n % kV16s], ((n / kV16s) & 1u) ^ 1u, abort_flag, c.status);
+               warp_wait(&v_full[st], (n / C::kVStages) & 1u, abort_flag, c.status) &&
+               warp_wait(&v16_empty[n % C::kV16s], ((n / C::kV16s) & 1u) ^ 1u, abort_flag, c.status);
           if (!ok) break;
           const uint32_t have = infos[slot].have;
           const int j0 = (g.tile0 + i) * kKeys;
-          const uint8_t* src = smem + kVOff + st * kCodeBytes;
-          uint8_t* dst = smem + kV16Off + (n % kV16s) * kV16Bytes;
+          const uint8_t* src = smem + C::kVOff + st * kTileBytes;
+          uint8_t* dst = smem + C::kV16Off + (n % C::kV16s) * C::kV16Bytes;
           // a warp step: 4 tokens, 8 lanes of 16 dims each
 #pragma unroll 2
           for (int x = 0; x < kKeys / 16; ++x) {
@@ -608,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             o1.z = e4m3x2_f16x2(v.w & 0xFFFFu);
             o1.w = e4m3x2_f16x2(v.w >> 16);
             // dims 16 ch .. +15: two 16-byte pieces of the row of their half (64 dims, 128 bytes, swizzled)
-            uint8_t* to = dst + (ch >> 2) * kCodeBytes + tok * 128;
+            uint8_t* to = dst + (ch >> 2) * kTileBytes + tok * 128;
             const int piece = (ch & 3) * 2;
             *reinterpret_cast<uint4*>(to + ((piece ^ (tok & 7)) << 4)) = o0;
             *reinterpret_cast<uint4*>(to + (((piece + 1) ^ (tok & 7)) << 4)) = o1;
@@ -616,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&v16_full[n % kV16s]);
+            mbar_arrive(&v16_full[n % C::kV16s]);
             mbar_arrive(&v_empty[st]);
             mbar_arrive(&i_empty[slot]);
           }
@@ -625,48 +707,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kTmaWarp) {
       // ---------------------------------------------------------- TMA: lane = page of the tile
       const uint64_t pol = policy_evict_last();
-      const int keys_log2 = min(c.page_log2, kKeys == 64 ? 6 : 7), boxes = kKeys >> keys_log2;  // keys of a box: a page, or half a page of 128
-      const uint32_t box = kHeadDim << keys_log2;
+      const int boxes = kKeys >> c.page_log2;
+      const uint32_t box = kHeadDim << c.page_log2;
       uint32_t n = 0, nv = 0;
       bool ok = true;
       while (ok && reader.next(g, abort_flag, c.status)) {
         const int32_t* row = c.page_table + (size_t)g.b * c.max_pages;
         // page of this lane's box of tile i, read one tile ahead; -1: nothing to load
         auto page_at = [&](int i) {
-          const int j = (g.tile0 + i) * kKeys + (lane << keys_log2);
-          return lane < boxes && i < g.i1 && j + (1 << keys_log2) > g.lo && j < g.hi ? __ldg(row + (j >> c.page_log2)) : -1;
+          const int j = (g.tile0 + i) * kKeys + (lane << c.page_log2);
+          return lane < boxes && i < g.i1 && j + c.page > g.lo && j < g.hi ? __ldg(row + (j >> c.page_log2)) : -1;
         };
         int pg = page_at(g.i0);
-        for (int i = g.i0; i < g.i1; ++i) {
+        for (int i = g.i0; i < g.i0 + C::tiles(g); ++i) {
           const int next = page_at(i + 1);
-          const int in_page = ((g.tile0 + i) * kKeys + (lane << keys_log2)) & (c.page - 1);
           const bool have = pg >= 0 && pg < c.n_pages;
           const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have)) * box;
-          const int y = have ? (int)(((long long)pg * c.Hkv + g.h) << c.page_log2) + in_page : 0;
-          const int ks = (int)(n % kKStages), vs = (int)(nv % kVStages);
-          ok = warp_wait(&k_empty[ks], ((n / kKStages) & 1u) ^ 1u, abort_flag, c.status);
+          const int y = have ? (int)(((long long)pg * c.Hkv + g.h) << c.page_log2) : 0;
+          const int ks = (int)(n % C::kKStages), vs = (int)(nv % C::kVStages);
+          ok = warp_wait(&k_empty[ks], ((n / C::kKStages) & 1u) ^ 1u, abort_flag, c.status);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], bytes);
           __syncwarp();
-          if (have) tma_load_2d(smem + kKOff + ks * kCodeBytes + lane * box, &tm_k, 0, y, &k_full[ks], pol);
+          if (have) tma_load_2d(smem + C::kKOff + ks * kTileBytes + lane * box, &tm_k, 0, y, &k_full[ks], pol);
           ++n;
-          ok = warp_wait(&v_empty[vs], ((nv / kVStages) & 1u) ^ 1u, abort_flag, c.status);
+          ok = warp_wait(&v_empty[vs], ((nv / C::kVStages) & 1u) ^ 1u, abort_flag, c.status);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], bytes);
           __syncwarp();
-          if (have) tma_load_2d(smem + kVOff + vs * kCodeBytes + lane * box, &tm_v, 0, y, &v_full[vs], pol);
+          if (have) tma_load_2d(smem + C::kVOff + vs * kTileBytes + lane * box, &tm_v, 0, y, &v_full[vs], pol);
           ++nv;
           pg = next;
         }
       }
       // every copy lands before the block ends
       if (lane == 0) {
-        for (int st = 0; st < kKStages; ++st) {
-          const uint32_t fills = n / kKStages + ((uint32_t)st < n % kKStages ? 1u : 0u);
+        for (int st = 0; st < C::kKStages; ++st) {
+          const uint32_t fills = n / C::kKStages + ((uint32_t)st < n % C::kKStages ? 1u : 0u);
           if (fills) mbar_wait_bounded(&k_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
         }
-        for (int st = 0; st < kVStages; ++st) {
-          const uint32_t fills = nv / kVStages + ((uint32_t)st < nv % kVStages ? 1u : 0u);
+        for (int st = 0; st < C::kVStages; ++st) {
+          const uint32_t fills = nv / C::kVStages + ((uint32_t)st < nv % C::kVStages ? 1u : 0u);
           if (fills) mbar_wait_bounded(&v_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
         }
       }
@@ -674,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kScaleWarp) {
       // ---------------------------------------------------------- scales: lane = 16 keys of the tile
       // It also walks the run, and gives the others its parts.
-      Walk walk(c, a, G, run, s_begin[0], s_begin[1], s_begin[2]);
+      Walk<kRows> walk(c, a, G, run, s_begin[0], s_begin[1], s_begin[2]);
       uint32_t n = 0;
       bool ok = true;
       for (uint32_t np = 0; ok; ++np) {
@@ -696,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return p < c.n_pages ? p : -1;
         };
         int pg = page_at(g.i0);
-        for (int i = g.i0; i < g.i1; ++i, ++n) {
+        for (int i = g.i0; i < g.i0 + C::tiles(g); ++i, ++n) {
           const int slot = (int)(n % kInfos);
           uint32_t sk = 127, sv = 127;
           if (pg >= 0) {
@@ -726,58 +807,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       // overwrites S starts after the one before it in the stream that reads p' there.
       const uint32_t id_s = umma_idesc_e4m3(kM, kKeys, false, false), id_o = idesc_pv();
       const uint64_t desc = umma_desc_sw128(smem_u32(smem));
-      // V16: 64-dim halves kCodeBytes apart (leading), groups of 8 tokens 1 KB apart (stride)
-      const uint64_t vdesc = (desc & ~((uint64_t)0x3FFFu << 16)) | (uint64_t)(kCodeBytes >> 4) << 16;
-      uint32_t n0 = 0, segs = 0;
+      // V16: 64-dim halves kTileBytes apart (leading), groups of 8 tokens 1 KB apart (stride)
+      const uint64_t vdesc = (desc & ~((uint64_t)0x3FFFu << 16)) | (uint64_t)(kTileBytes >> 4) << 16;
+      uint32_t n0 = 0, steps0 = 0, segs = 0;
       bool ok = true;
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       while (ok && reader.next(g, abort_flag, c.status)) {
-        const int tiles = __shfl_sync(0xffffffffu, g.i1 - g.i0, 0);
-        // Step i: the weights of tile i against V (from i = 0 on), then the scores of tile i + kSBufs.  One copy of
-        // either's instructions for all steps and M tiles.
+        const int tiles = __shfl_sync(0xffffffffu, C::tiles(g), 0), steps = tiles / C::kStep;
+        // Step i: the weights of an M tile's i-th tile against V (from i = 0 on), then the scores of its next one.  One copy
+        // of either's instructions for all steps and M tiles.
 #pragma unroll 1
-        for (int i = -kSBufs; ok && i < tiles; ++i) {
-          const uint32_t tp = n0 + i, tn = tp + kSBufs;  // number of the tile whose weights, whose scores are next
-          const bool more = i + kSBufs < tiles;
-          if (i >= 0) ok = warp_wait(&v16_full[tp % kV16s], (tp / kV16s) & 1u, abort_flag, c.status);
-          if (ok && more) ok = warp_wait(&k_full[tn % kKStages], (tn / kKStages) & 1u, abort_flag, c.status);
+        for (int i = -1; ok && i < steps; ++i) {
+          const bool more = i + 1 < steps;
 #pragma unroll 1
           for (int mt = 0; ok && mt < 2; ++mt) {
-            const uint32_t place = mt * kSBufs + tn % kSBufs, s_at = tm + mt * 128 + (tn % kSBufs) * kKeys;
+            // number of the tile whose weights, whose scores are next
+            const uint32_t tp = n0 + i * C::kStep + (kSplit ? mt : 0), tn = tp + C::kStep;
+            if (kSplit || mt == 0) {
+              if (i >= 0) ok = warp_wait(&v16_full[tp % C::kV16s], (tp / C::kV16s) & 1u, abort_flag, c.status);
+              if (ok && more) ok = warp_wait(&k_full[tn % C::kKStages], (tn / C::kKStages) & 1u, abort_flag, c.status);
+            }
+            const uint32_t s_at = tm + mt * kTile;
             if (i >= 0) {
-              ok = warp_wait(&p_full[place], (tp / kSBufs) & 1u, abort_flag, c.status);
+              ok = ok && warp_wait(&p_full[mt], (steps0 + i) & 1u, abort_flag, c.status);
               if (!ok) break;
               tc_fence_after();
               const uint32_t o = tm + 256 + mt * kHeadDim;
-              const uint64_t bd = vdesc + (uint64_t)(((kV16Off + (tp % kV16s) * kV16Bytes)) >> 4);
+              const uint64_t bd = vdesc + (uint64_t)((C::kV16Off + (tp % C::kV16s) * C::kV16Bytes) >> 4);
               if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
                   umma_f16_ts(o, s_at + 8 * k, bd + (uint64_t)((k * 16 * 128) >> 4), id_o, k > 0 || i > 0);
-                umma_commit(&o_full[place]);
-                if (mt == 1) umma_commit(&v16_empty[tp % kV16s]);
+                umma_commit(&o_full[mt]);
+                if (kSplit || mt == 1) umma_commit(&v16_empty[tp % C::kV16s]);
               }
               __syncwarp();
-            } else if (i == -kSBufs) {
-              ok = warp_wait(&q_full[mt], segs & 1u, abort_flag, c.status);
+            } else {
+              ok = ok && warp_wait(&q_full[kSplit ? 0 : mt], segs & 1u, abort_flag, c.status);
               if (!ok) break;
               tc_fence_after();
             }
             if (more) {
-              const uint64_t bd = desc + (uint64_t)((kKOff + (tn % kKStages) * kCodeBytes) >> 4);
-              const uint64_t ad = desc + (uint64_t)((kQOff + mt * 2 * kTileBytes) >> 4);
+              const uint64_t bd = desc + (uint64_t)((C::kKOff + (tn % C::kKStages) * kTileBytes) >> 4);
+              const uint64_t ad = desc + (uint64_t)((C::kQOff + (kSplit ? 0 : mt * 2 * kTileBytes)) >> 4);
               if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 2 * kHeadDim / 32; ++k)  // the hi half of the queries, then the lo half
                   umma_e4m3(s_at, ad + (k >> 2) * (kTileBytes >> 4) + 2 * (k & 3), bd + 2 * (k & 3), id_s, k != 0);
-                umma_commit(&s_full[place]);
-                if (mt == 1) umma_commit(&k_empty[tn % kKStages]);
+                umma_commit(&s_full[mt]);
+                if (kSplit || mt == 1) umma_commit(&k_empty[tn % C::kKStages]);
               }
               __syncwarp();
             }
           }
         }
         n0 += tiles;
+        steps0 += steps;
         ++segs;
       }
       // whatever was issued has finished before tensor memory is given back (after an abort too)
@@ -794,26 +879,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+template <bool kSplit>
+cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
+  using C = Cfg<kSplit>;
+  CUtensorMap tk, tv;
+  if (!make_cache_map(&tk, c.k_codes, c) || !make_cache_map(&tv, c.v_codes, c)) return cudaErrorInvalidValue;
+  auto kern = attention_prefill_kernel<kSplit>;
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::kBytes, allowed);
+  if (e != cudaSuccess) return e;
+  float* part_o = reinterpret_cast<float*>(a.scratch);
+  float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)n_sms * 2 * C::kRows * kHeadDim);
+  JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)n_sms * 2 * C::kRows);
+  e = launch_kernel(kern, dim3(n_sms), dim3(kThreads), C::kBytes, stream, false, tk, tv, c, a, part_o, part_rl, info);
+  if (e != cudaSuccess) return e;
+  return launch_attention_join(c, a, n_sms, C::kRows, part_o, part_rl, info, stream);
+}
+
+// Whether a sequence's rows of one head fit an M tile: it is then the keys that the two tiles share out.
+bool splits_keys(int G, int max_q) { return (long long)G * max_q <= kM; }
+
 }  // namespace
 
-size_t attention_prefill_scratch(int n_sms) {
-  return (size_t)n_sms * (2 * kItemRows * (kHeadDim * sizeof(float) + sizeof(float2)) + sizeof(JoinInfo));
+size_t attention_prefill_scratch(int G, int max_q, int n_sms) {
+  const int rows = splits_keys(G, max_q) ? Cfg<true>::kRows : Cfg<false>::kRows;
+  return (size_t)n_sms * (2 * rows * (kHeadDim * sizeof(float) + sizeof(float2)) + sizeof(JoinInfo));
 }
 
 cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
-  CUtensorMap tk, tv;
-  const int box = c.page < kKeys ? c.page : kKeys;
-  if (!make_cache_map(&tk, c.k_codes, c, box) || !make_cache_map(&tv, c.v_codes, c, box)) return cudaErrorInvalidValue;
-  static std::atomic<unsigned long long> allowed{0};
-  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(attention_prefill_kernel), kBytes, allowed);
-  if (e != cudaSuccess) return e;
-  float* part_o = reinterpret_cast<float*>(a.scratch);
-  float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)n_sms * 2 * kItemRows * kHeadDim);
-  JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)n_sms * 2 * kItemRows);
-  e = launch_kernel(attention_prefill_kernel, dim3(n_sms), dim3(kThreads), kBytes, stream, false, tk, tv, c, a, part_o,
-                    part_rl, info);
-  if (e != cudaSuccess) return e;
-  return launch_attention_join(c, a, n_sms, kItemRows, part_o, part_rl, info, stream);
+  return splits_keys(c.Hq / c.Hkv, a.max_q) ? launch<true>(c, a, n_sms, stream) : launch<false>(c, a, n_sms, stream);
 }
 
 }  // namespace moe
