@@ -493,8 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = g.i0 + x;
         const uint32_t n = n0 + x;
         const int slot = (int)(n % kInfos);
-        ok = warp_wait(&i_full[slot], (n / kInfos) & 1u, abort_flag, c.status) &&
-             warp_wait(&s_full[mt], steps & 1u, abort_flag, c.status);
+        ok = warp_wait2(&i_full[slot], (n / kInfos) & 1u, &s_full[mt], steps & 1u, abort_flag, c.status);
         if (!ok) break;
         const TileInfo& ti = infos[slot];
         const uint32_t have = ti.have;
@@ -662,38 +661,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- values: E4M3 -> f16, keys nobody sees -> zeros
       uint32_t n = 0;
       bool ok = true;
-      const int w = warp - kValWarp;
+      // A warp has 32 tokens, eight (1 KB of codes) at a time, first the lower half of their dims, then the upper.  A lane has 16
+      // dims of a token: four lanes are one token's, the next four that token's whose place in the eight differs by 5
+      // (0 and 5, 1 and 4, ..): then eight lanes meet eight different banks in the reads (16-byte pieces c ^ place of a row)
+      // as in the writes (pieces 2c ^ place and, after it, (2c + 1) ^ place).
+      const int place = (lane >> 3) ^ ((lane & 4) ? 5 : 0), quad = lane & 3, tok0 = (warp - kValWarp) * 32 + place;
+      const uint32_t from = tok0 * 128 + ((quad ^ place) << 4), to = tok0 * 128 + (((2 * quad) ^ place) << 4);
       while (ok && reader.next(g, abort_flag, c.status)) {
         for (int i = g.i0; i < g.i0 + C::tiles(g); ++i, ++n) {
           const int st = (int)(n % C::kVStages), slot = (int)(n % kInfos);
-          ok = warp_wait(&i_full[slot], (n / kInfos) & 1u, abort_flag, c.status) &&
-               warp_wait(&v_full[st], (n / C::kVStages) & 1u, abort_flag, c.status) &&
-               warp_wait(&v16_empty[n % C::kV16s], ((n / C::kV16s) & 1u) ^ 1u, abort_flag, c.status);
+          ok = warp_wait3(&i_full[slot], (n / kInfos) & 1u, &v_full[st], (n / C::kVStages) & 1u, &v16_empty[n % C::kV16s],
+                          ((n / C::kV16s) & 1u) ^ 1u, abort_flag, c.status);
           if (!ok) break;
           const uint32_t have = infos[slot].have;
           const int j0 = (g.tile0 + i) * kKeys;
           const uint8_t* src = smem + C::kVOff + st * kTileBytes;
           uint8_t* dst = smem + C::kV16Off + (n % C::kV16s) * C::kV16Bytes;
-          // a warp step: 4 tokens, 8 lanes of 16 dims each
-#pragma unroll 2
-          for (int x = 0; x < kKeys / 16; ++x) {
-            const int tok = w * (kKeys / 4) + x * 4 + (lane >> 3), ch = lane & 7;
-            uint4 v = *reinterpret_cast<const uint4*>(src + tok * 128 + ((ch ^ (tok & 7)) << 4));
-            if (j0 + tok < g.lo || j0 + tok >= g.hi || !(have >> (tok >> 4) & 1u)) v = make_uint4(0, 0, 0, 0);
-            uint4 o0, o1;
-            o0.x = e4m3x2_f16x2(v.x & 0xFFFFu);
-            o0.y = e4m3x2_f16x2(v.x >> 16);
-            o0.z = e4m3x2_f16x2(v.y & 0xFFFFu);
-            o0.w = e4m3x2_f16x2(v.y >> 16);
-            o1.x = e4m3x2_f16x2(v.z & 0xFFFFu);
-            o1.y = e4m3x2_f16x2(v.z >> 16);
-            o1.z = e4m3x2_f16x2(v.w & 0xFFFFu);
-            o1.w = e4m3x2_f16x2(v.w >> 16);
-            // dims 16 ch .. +15: two 16-byte pieces of the row of their half (64 dims, 128 bytes, swizzled)
-            uint8_t* to = dst + (ch >> 2) * kTileBytes + tok * 128;
-            const int piece = (ch & 3) * 2;
-            *reinterpret_cast<uint4*>(to + ((piece ^ (tok & 7)) << 4)) = o0;
-            *reinterpret_cast<uint4*>(to + (((piece + 1) ^ (tok & 7)) << 4)) = o1;
+          const bool whole = j0 >= g.lo && j0 + kKeys <= g.hi && have == (1u << kPieces) - 1u;
+#pragma unroll
+          for (int x = 0; x < 8; x += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) v[y] = *reinterpret_cast<const uint4*>(src + (from ^ ((y & 1) << 6)) + ((x + y) >> 1) * 1024);
+            if (!whole) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int tok = tok0 + ((x + y) >> 1) * 8;
+                if (j0 + tok < g.lo || j0 + tok >= g.hi || !(have >> (tok >> 4) & 1u)) v[y] = make_uint4(0, 0, 0, 0);
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint8_t* at = dst + (y & 1) * kTileBytes + ((x + y) >> 1) * 1024;
+              *reinterpret_cast<uint4*>(at + to) = make_uint4(e4m3x2_f16x2(v[y].x & 0xFFFFu), e4m3x2_f16x2(v[y].x >> 16),
+                                                              e4m3x2_f16x2(v[y].y & 0xFFFFu), e4m3x2_f16x2(v[y].y >> 16));
+              *reinterpret_cast<uint4*>(at + (to ^ 16)) = make_uint4(e4m3x2_f16x2(v[y].z & 0xFFFFu), e4m3x2_f16x2(v[y].z >> 16),
+                                                                     e4m3x2_f16x2(v[y].w & 0xFFFFu), e4m3x2_f16x2(v[y].w >> 16));
+            }
           }
           fence_async_shared();
           __syncwarp();
@@ -824,8 +828,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // number of the tile whose weights, whose scores are next
             const uint32_t tp = n0 + i * C::kStep + (kSplit ? mt : 0), tn = tp + C::kStep;
             if (kSplit || mt == 0) {
-              if (i >= 0) ok = warp_wait(&v16_full[tp % C::kV16s], (tp / C::kV16s) & 1u, abort_flag, c.status);
-              if (ok && more) ok = warp_wait(&k_full[tn % C::kKStages], (tn / C::kKStages) & 1u, abort_flag, c.status);
+              uint64_t *v = &v16_full[tp % C::kV16s], *k = &k_full[tn % C::kKStages];
+              const uint32_t vp = (tp / C::kV16s) & 1u, kp = (tn / C::kKStages) & 1u;
+              ok = i < 0 ? warp_wait(k, kp, abort_flag, c.status) : warp_wait2(v, vp, more ? k : v, more ? kp : vp, abort_flag, c.status);
             }
             const uint32_t s_at = tm + mt * kTile;
             if (i >= 0) {

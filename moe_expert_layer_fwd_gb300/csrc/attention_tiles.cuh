@@ -38,6 +38,18 @@ __device__ __forceinline__ bool mbar_wait_tries(uint64_t* bar, uint32_t parity, 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
   return __all_sync(0xffffffffu, mbar_wait_tries(bar, parity, abort_flag, status));
 }
+// Two or three barriers at a time, the lanes sharing them out: a try takes 100 cycles and more while the tensor core's
+// operands keep shared memory busy, and tries one after another add up.
+__device__ __forceinline__ bool warp_wait2(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, volatile int* abort_flag,
+                                           unsigned* status) {
+  const bool second = threadIdx.x & 1;
+  return warp_wait(second ? b1 : b0, second ? p1 : p0, abort_flag, status);
+}
+__device__ __forceinline__ bool warp_wait3(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2, uint32_t p2,
+                                           volatile int* abort_flag, unsigned* status) {
+  const int which = (threadIdx.x & 31) < 11 ? 0 : (threadIdx.x & 1) + 1;
+  return warp_wait(which == 0 ? b0 : which == 1 ? b1 : b2, which == 0 ? p0 : which == 1 ? p1 : p2, abort_flag, status);
+}
 
 // The keys that any new token of a sequence sees: [lo, hi), in tiles [tile0, tile0 + nt).  A sequence with new
 // tokens has at least one tile, so that its rows are written even when they see nothing.
