@@ -9,19 +9,23 @@
 //   O^T[128 dims, 2 NC] = V^T . [p'_hi | p'_lo]          the same instruction, V read with its dims contiguous
 // so that neither keys nor values pass through a register: TMA writes the pages' codes to shared memory with the
 // 128-byte swizzle and the tensor core reads them there, once each.  Scales never touch the codes: those of the keys
-// are multiplied onto S, those of the values are added to the exponent.  The running maximum r is the
-// one of u: the largest p' is 2^8 whatever the pages' scales are, errors are relative to the largest term of
-// the sum that is being computed, and the denominator takes the scale out again.  hi + lo keeps 8 bits of p'.
-// A thread owns one key (S, p') and one output dim (O): the accumulator stays in its registers, each tile's product is
-// read from tensor memory and added, so nothing in tensor memory is ever rescaled.
+// are multiplied onto S, those of the values are added to the exponent.  The reference r follows the running maximum of u:
+// the largest p' lies within 2^6 .. 2^8.8 whatever the pages' scales are, errors are relative to the largest
+// term of the sum that is being computed, and the denominator takes the scale out again.  hi + lo keeps 8 bits of p' down to
+// 2^-8 of the largest.
+// A softmax thread owns one key and half of the columns (S, p'), and one output dim of them (O, accumulated in tensor memory
+// and rescaled only when r moves).
 //
 // Work: all (sequence, head, tile) in one order, cut into equal runs, one per block (two blocks per SM): a long sequence is
 // split over as many blocks as it takes, a short one shares a block.  A row whose tiles lie in one block
 // is finished there; otherwise the parts (sum, maximum, denominator) go to the workspace and a second kernel joins them in a
 // fixed order.  The host knows none of the lengths.
 //
-// Warps: 8 or 16 softmax warps (four for each group of 4 or 8 columns), then TMA, MMA, queries.  Every wait is
-// bounded (2 s).
+// Measured (64 sequences of 1500-8190 tokens, 64 query heads on 8, 685 MB of cache): 123 us; from the first copy to the last
+// product 94 us = 7.3 TB/s, the memory's rate; the rest is 6 us until the first scores (lengths, page table, first copies, one
+// after another), 10 us in which the slowest blocks finish, and the join.  Small sequences are bound by that chain of waits.
+//
+// Warps: 8 softmax (four for each half of the columns), then TMA, MMA, queries.  Every wait is bounded (2 s).
 #include "attention_tiles.cuh"
 
 namespace moe {
@@ -43,11 +47,11 @@ struct TileInfo {    // per 16 keys of a tile
 
 template <int NC>
 struct Cfg {
-  static constexpr int kPerSm = NC >= 24 ? 1 : 2;
-  static constexpr int kStages = NC == 8 ? 3 : NC >= 24 ? 5 : 2;
+  static constexpr int kPerSm = 2;
+  static constexpr int kStages = NC == 8 ? 3 : 2;
   static constexpr int kQBufs = 2;                          // the next segment's scores start before this one has ended
-  static constexpr int kCols = NC % 16 ? 4 : 8;             // columns of a softmax thread
-  static constexpr int kGroups = NC / kCols;                // groups of four softmax warps, each with its columns
+  static constexpr int kGroups = 2;                         // groups of four softmax warps, each with half of the columns
+  static constexpr int kCols = NC / kGroups;
   static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kQWarp = kSoftWarps + 2;
   static constexpr int kThreads = 32 * (kSoftWarps + 3);
@@ -64,7 +68,7 @@ struct Cfg {
   static constexpr int kMaxOff = kQfOff + kQBufs * NC * 8;  // float [3][NC][4]: maxima of even, odd tiles; denominators
   static constexpr int kMiscOff = kMaxOff + 3 * NC * 16;
   static constexpr int kBytes = 1024 + kMiscOff + 64;
-  static constexpr int kTmemCols = NC == 24 ? 256 : 4 * kRows;  // S twice, O (a power of two)
+  static constexpr int kTmemCols = 4 * kRows;               // S twice, O (a power of two)
   static constexpr int kOCol = 2 * kRows;
   static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
@@ -152,36 +156,28 @@ __device__ __forceinline__ long long tiles_per_block(long long n, int blocks) {
 // acc[x] += column x + column `lo` + x of this thread's tensor-memory lane.
 template <int N>
 __device__ __forceinline__ void add_product(uint32_t taddr, int lo, float (&acc)[N]) {
-  constexpr int kStep = N % 8 ? 4 : 8;
+  uint32_t s[N], t[N];
+  tmem_ld_async(taddr, s);
+  tmem_ld_async(taddr + lo, t);
+  tmem_wait_ld();
 #pragma unroll
-  for (int y = 0; y < N; y += kStep) {
-    uint32_t s[kStep], t[kStep];
-    tmem_ld_async(taddr + y, s);
-    tmem_ld_async(taddr + lo + y, t);
-    tmem_wait_ld();
-#pragma unroll
-    for (int x = 0; x < kStep; ++x) acc[y + x] += __uint_as_float(s[x]) + __uint_as_float(t[x]);
-  }
+  for (int x = 0; x < N; ++x) acc[x] += __uint_as_float(s[x]) + __uint_as_float(t[x]);
 }
 
 // Columns x and `lo` + x of this thread's tensor-memory lane, times f[x].
 template <int N>
 __device__ __forceinline__ void scale_columns(uint32_t taddr, int lo, const float (&f)[N]) {
-  constexpr int kStep = N % 8 ? 4 : 8;
+  uint32_t s[N], t[N];
+  tmem_ld_async(taddr, s);
+  tmem_ld_async(taddr + lo, t);
+  tmem_wait_ld();
 #pragma unroll
-  for (int y = 0; y < N; y += kStep) {
-    uint32_t s[kStep], t[kStep];
-    tmem_ld_async(taddr + y, s);
-    tmem_ld_async(taddr + lo + y, t);
-    tmem_wait_ld();
-#pragma unroll
-    for (int x = 0; x < kStep; ++x) {
-      s[x] = __float_as_uint(__uint_as_float(s[x]) * f[y + x]);
-      t[x] = __float_as_uint(__uint_as_float(t[x]) * f[y + x]);
-    }
-    tmem_st(taddr + y, s);
-    tmem_st(taddr + lo + y, t);
+  for (int x = 0; x < N; ++x) {
+    s[x] = __float_as_uint(__uint_as_float(s[x]) * f[x]);
+    t[x] = __float_as_uint(__uint_as_float(t[x]) * f[x]);
   }
+  tmem_st(taddr, s);
+  tmem_st(taddr + lo, t);
   tmem_wait_st();
 }
 
@@ -570,14 +566,12 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           }
         }
         float* tops = s_max + (n & 1u) * NC * 4 + col0 * 4;
-        constexpr int kStep = N % 8 ? 4 : 8;
+        {
+          float v[N];
 #pragma unroll
-        for (int y = 0; y < N; y += kStep) {
-          float v[kStep];
-#pragma unroll
-          for (int x = 0; x < kStep; ++x) v[x] = u[y + x];
-          const int col = y + columns_max<kStep>(v, lane);
-          if ((lane & (32 / kStep - 1)) == 0) tops[col * 4 + w4] = v[0];
+          for (int x = 0; x < N; ++x) v[x] = u[x];
+          const int col = columns_max<N>(v, lane);
+          if ((lane & (32 / N - 1)) == 0) tops[col * 4 + w4] = v[0];
         }
         if (lane == 0 && !ok) s_bad[n & 1u] = 1;
         group_sync();
@@ -707,10 +701,9 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
   }
 }
 
-// The columns' width that holds `cols` of them; 0: too many.
-int width_of(int cols) { return cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 24 ? 24 : cols <= 32 ? 32 : 0; }
+int width_of(int cols) { return cols <= 8 ? 8 : 16; }
 
-int blocks_of(int nc, int n_sms) { return n_sms * (nc >= 24 ? 1 : 2); }
+int blocks_of(int n_sms) { return 2 * n_sms; }
 
 template <int NC>
 cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
@@ -723,10 +716,10 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   if (e != cudaSuccess) return e;
   // Rows of a few tiles at most (the table's width bounds them) are one block's each: nothing to join.
   const bool split = (long long)c.max_pages * c.page > kWholeTiles * kTile;
-  const int blocks = split ? blocks_of(NC, n_sms) : c.B * c.Hkv;
+  const int blocks = split ? blocks_of(n_sms) : c.B * c.Hkv;
   float* part_o = reinterpret_cast<float*>(a.scratch);
-  float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)2 * blocks_of(NC, n_sms) * NC * kHeadDim);
-  JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)2 * blocks_of(NC, n_sms) * NC);
+  float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)2 * blocks_of(n_sms) * NC * kHeadDim);
+  JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)2 * blocks_of(n_sms) * NC);
   e = launch_kernel(kern, dim3(blocks), dim3(C::kThreads), C::kBytes, stream, false, tk, tv, c, a, (int)split, part_o, part_rl,
                     info);
   if (e != cudaSuccess || !split) return e;
@@ -735,20 +728,15 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
 
 }  // namespace
 
-bool attention_decode_fits(int G, int max_q) { return (long long)G * max_q <= 32; }
+bool attention_decode_fits(int G, int max_q) { return (long long)G * max_q <= 16; }
 
 size_t attention_decode_scratch(int G, int max_q, int n_sms) {
   const int nc = width_of(G * max_q);
-  return blocks_of(nc, n_sms) * ((size_t)2 * nc * (kHeadDim * sizeof(float) + sizeof(float2)) + sizeof(JoinInfo));
+  return blocks_of(n_sms) * ((size_t)2 * nc * (kHeadDim * sizeof(float) + sizeof(float2)) + sizeof(JoinInfo));
 }
 
 cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
-  switch (width_of(c.Hq / c.Hkv * a.max_q)) {
-    case 8: return launch<8>(c, a, n_sms, stream);
-    case 16: return launch<16>(c, a, n_sms, stream);
-    case 24: return launch<24>(c, a, n_sms, stream);
-    default: return launch<32>(c, a, n_sms, stream);
-  }
+  return width_of(c.Hq / c.Hkv * a.max_q) == 8 ? launch<8>(c, a, n_sms, stream) : launch<16>(c, a, n_sms, stream);
 }
 
 }  // namespace moe

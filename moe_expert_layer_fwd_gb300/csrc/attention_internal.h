@@ -55,7 +55,7 @@ size_t attention_scratch_bytes(int Hq, int Hkv, int max_q, int n_sms);
 cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
 
 
-// Few query rows per key/value head: G grouped heads times max_q new tokens at most 32.
+// Few query rows per key/value head: G grouped heads times max_q new tokens at most 16.
 bool attention_decode_fits(int G, int max_q);
 size_t attention_decode_scratch(int G, int max_q, int n_sms);
 cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);

@@ -16,8 +16,8 @@
 // (one at each end of a run, at most) are joined by a second kernel.
 //
 // Warps (24): 0-7 and 8-15 softmax of the M tiles (thread = row and half of a tile's keys; they also load the queries,
-// rescale and write the output), 16-19 values, 20 TMA, 21 MMA, 22 scales of the tiles' pages, 23 walks the run.  Registers: 208 a
-// thread for the softmax, 48 for the rest.  Every wait is bounded (2 s).
+// rescale and write the output), 16-19 values, 20 TMA, 21 MMA, 22 scales of the tiles' pages, 23 walks the run.  Registers: 192 a
+// thread for the softmax, 64 for the rest.  Every wait is bounded (2 s).
 #include "attention_tiles.cuh"
 
 namespace moe {
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Part g;
 
   if (warp < kSoftWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     // ------------------------------------------------------------ softmax: thread = row of M tile mt
     const int mt = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp < kTmaWarp) {
       // ---------------------------------------------------------- values: E4M3 -> f16, keys nobody sees -> zeros
       uint32_t n = 0;
