@@ -115,13 +115,14 @@ MOE_API int moe_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Failure injection, for testing the bounded waits (process-wide, not thread-safe; set it back to
- * 0 afterwards).  what = 1: the limit, in ns, of every wait inside the grouped GEMMs (0: the
- * default, 2 s).  what = 2: value != 0 makes the gate/up GEMM's in-kernel row gather (taken by
+ * 0 afterwards).  what = 1: the limit, in ns, of every wait inside the grouped GEMMs and the
+ * attention kernels (0: the default, 2 s).  what = 2: value != 0 makes the gate/up GEMM's in-kernel row gather (taken by
  * compute-bound problems inside moe_layer_forward) write nothing and set none of its flags, so its
  * producers wait for flags that nothing sets: after the limit the kernel records MOE_ERR_TIMEOUT in
  * the workspace status, every CTA leaves its loops, waits for nothing in flight, frees its tensor
- * memory and returns; the rest of the layer runs on whatever act then holds.  Unknown `what` ->
- * MOE_ERR_INVALID_ARG.  The pages have no counterpart.
+ * memory and returns; the rest of the layer runs on whatever act then holds.  what = 4: value != 0
+ * makes moe_paged_attention withhold the copies of the values that its tensor-core role waits for,
+ * with the same end (MOE_ERR_TIMEOUT; out is undefined).  Unknown `what` -> MOE_ERR_INVALID_ARG.  The pages have no counterpart.
  */
 MOE_API int moe_debug_set(int what, unsigned long long value);
 
@@ -567,9 +568,10 @@ MOE_API int moe_layer_workspace_offsets(const moe_layer_desc* d, size_t* out, in
  * n_pages * Hkv * page and max_pages * page below 2^31 (the cache itself may pass 2^31 bytes).
  *
  * On the device: starts or lengths that contradict each other, a page outside the pool or the
- * table, and a position beyond max_pos set the workspace's status to MOE_ERR_DEVICE_CHECK; tokens
- * concerned are left out (append: not stored, their rows of q_out not written; gather: rows of
- * zeros; attention: keys on such a page are not seen, a row that sees no key is zero).
+ * table, and a position beyond max_pos set the workspace's status to MOE_ERR_DEVICE_CHECK; what
+ * they concern is left out (append: tokens not stored, their rows of q_out not written; gather: rows
+ * of zeros; attention: rows of a sequence with contradicting lengths not written, keys on a page
+ * that is not in the pool not seen, and a row that sees no key is zero).
  */
 typedef struct moe_kv_desc {
   int32_t B;          /* sequences */
@@ -638,8 +640,8 @@ MOE_API int moe_kv_gather(const moe_kv_desc* d, const int32_t* start, const int3
  * window > 0 (causal only).  A row that sees nothing is zero.
  *
  *  q [T,Hq,D] bf16, token stride q_stride (elements, a multiple of 8); normally q_out of moe_kv_append.
- *  max_q: at least the new tokens of any one sequence (1 when decoding); sequences that bring more set
- *      the status and their rows past max_q are not written.
+ *  max_q: at least the new tokens of any one sequence (1 when decoding).  With it and the heads the host
+ *      chooses a kernel; rows of sequences that bring more may be left unwritten, and then the status is set.
  *  scale > 0, finite.
  *  out [T,Hq,D] bf16, dense.
  *  ws: at least moe_paged_attention_workspace_size(d, max_q) bytes (0: invalid d), which suits every

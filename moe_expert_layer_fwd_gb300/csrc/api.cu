@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include "../../include/moe.h"
+#include "attention_internal.h"
 #include "moe_common.cuh"
 #include "moe_internal.h"
 
@@ -191,7 +192,8 @@ int moe_init_routing_range(const int32_t* topk_idx, int T, int E, int k, int e0,
 }
 
 int moe_debug_set(int what, unsigned long long value) {
-  return moe::grouped_gemm_debug_set(what, value) == 0 ? MOE_OK : MOE_ERR_INVALID_ARG;
+  const int gemm = moe::grouped_gemm_debug_set(what, value), attention = moe::attention_debug_set(what, value);
+  return gemm == 0 || attention == 0 ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
 
 int moe_add_rms_norm_cast(const uint16_t* hidden, const uint16_t* residual, const uint16_t* norm_weight, int T,

@@ -153,7 +153,15 @@ int moe_paged_attention(const moe_kv_desc* d, const uint16_t* q, long long q_str
   moe::KvBatch c = make_batch(d, kv, page_table, (unsigned*)ws);
   c.q_start = q_start;
   c.kv_len = kv_len;
-  moe::AttentionArgs a = {q, q_stride, out, scale * 1.44269504088896341f, causal != 0, window, max_q, (char*)ws + kHeader};
+  moe::AttentionArgs a = {};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.scale_log2 = scale * 1.44269504088896341f;
+  a.causal = causal != 0;
+  a.window = window;
+  a.max_q = max_q;
+  a.scratch = (char*)ws + kHeader;
   return cuda_status(moe::launch_paged_attention(c, a, sm_count(), (cudaStream_t)stream));
 }
 

@@ -103,7 +103,20 @@ size_t attention_scratch_bytes(int Hq, int Hkv, int max_q, int n_sms) {
   return attention_decode_fits(G, max_q) ? attention_decode_scratch(G, max_q, n_sms) : attention_prefill_scratch(G, max_q, n_sms);
 }
 
-cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
+static unsigned g_limit_us = 2000000;
+static int g_withhold = 0;
+
+int attention_debug_set(int what, unsigned long long value) {
+  if (what == 1) g_limit_us = value == 0 ? 2000000u : value < 2000000000ull ? (unsigned)(value / 1000 + 1) : 2000000u;
+  else if (what == 4) g_withhold = value != 0;
+  else return -1;
+  return 0;
+}
+
+cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& args, int n_sms, cudaStream_t stream) {
+  AttentionArgs a = args;
+  a.limit_us = g_limit_us;
+  a.withhold = g_withhold;
   return attention_decode_fits(c.Hq / c.Hkv, a.max_q) ? launch_attention_decode(c, a, n_sms, stream)
                                                       : launch_attention_prefill(c, a, n_sms, stream);
 }

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
   float* s_max = reinterpret_cast<float*>(smem + C::kMaxOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
-  int* s_begin = reinterpret_cast<int*>(smem + C::kMiscOff + 8);  // b, h, tile
+  int* s_begin = reinterpret_cast<int*>(smem + C::kMiscOff + 12);  // b, h, tile
   volatile int* s_bad = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 24);  // [3] a softmax warp gave up (as s_max)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       mbar_init(&o_full[i], 1);
     }
     mbar_init(done, 1);
-    *abort_flag = 0;
+    abort_flag[0] = 0;
+    abort_flag[1] = (int)a.limit_us;
     for (int i = 0; i < 3; ++i) s_bad[i] = 0;
     fence_mbar_init();
   }
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         __syncwarp();
         if (load) {
           tma_load_2d(dst, &tm_k, 0, y, &k_full[st], pol);
-          tma_load_2d(dst + kTileBytes, &tm_v, 0, y, &v_full[st], pol);
+          if (!a.withhold) tma_load_2d(dst + kTileBytes, &tm_v, 0, y, &v_full[st], pol);
         }
         // the scales, which take longer to come than the copies to be issued: the keys' barrier wants them too
         if (lane < 8) {
@@ -385,8 +386,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       for (int st = 0; st < C::kStages; ++st) {
         const uint32_t fills = n / C::kStages + ((uint32_t)st < n % C::kStages ? 1u : 0u);
         if (!fills) continue;
-        mbar_wait_bounded(&k_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
-        mbar_wait_bounded(&v_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
+        mbar_wait_bounded(&k_full[st], (fills - 1u) & 1u, abort_flag, 1000ull * a.limit_us, c.status, false);
+        mbar_wait_bounded(&v_full[st], (fills - 1u) & 1u, abort_flag, 1000ull * a.limit_us, c.status, false);
       }
     }
     __syncwarp();
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     // whatever was issued has finished before tensor memory is given back (after an abort too)
     if (elect_one()) umma_commit(done);
     __syncwarp();
-    mbar_wait_bounded(done, 0, abort_flag, kAttnTimeoutNs, c.status, false);
+    mbar_wait_bounded(done, 0, abort_flag, 1000ull * a.limit_us, c.status, false);
   } else if (warp == C::kQWarp) {
     // ------------------------------------------------------------ queries
     uint32_t n = 0;

@@ -49,11 +49,17 @@ struct AttentionArgs {
   uint16_t* out;              // [T, Hq, 128]
   float scale_log2;           // softmax scale * log2(e)
   int causal, window, max_q;
+  unsigned limit_us;          // of every wait inside the kernels
+  int withhold;               // failure injection (tests only): the values' copies are not issued, so that waits run out
   void* scratch;              // after the status word of the workspace
 };
 size_t attention_scratch_bytes(int Hq, int Hkv, int max_q, int n_sms);
 cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
 
+
+// Failure injection (tests only): what 1 = wait limit in ns (0: the default 2 s), what 4 = nonzero: withhold the values'
+// copies.  Returns 0, or -1 for another `what`.
+int attention_debug_set(int what, unsigned long long value);
 
 // Few query rows per key/value head: G grouped heads times max_q new tokens at most 16.
 bool attention_decode_fits(int G, int max_q);

@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* done = x_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
-  int* s_begin = reinterpret_cast<int*>(smem + C::kMiscOff + 8);  // place, head, cost into the item
+  int* s_begin = reinterpret_cast<int*>(smem + C::kMiscOff + 12);  // place, head, cost into the item
   Part* parts = reinterpret_cast<Part*>(smem + C::kPartOff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = c.Hq / c.Hkv;
@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(x_full, 4);
     mbar_init(x_empty, 4);
     mbar_init(done, 1);
-    *abort_flag = 0;
+    abort_flag[0] = 0;
+    abort_flag[1] = (int)a.limit_us;
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     fence_mbar_init();
@@ -739,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], bytes);
           __syncwarp();
-          if (have) tma_load_2d(smem + C::kVOff + vs * kTileBytes + lane * box, &tm_v, 0, y, &v_full[vs], pol);
+          if (have && !a.withhold) tma_load_2d(smem + C::kVOff + vs * kTileBytes + lane * box, &tm_v, 0, y, &v_full[vs], pol);
           ++nv;
           pg = next;
         }
@@ -748,11 +749,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         for (int st = 0; st < C::kKStages; ++st) {
           const uint32_t fills = n / C::kKStages + ((uint32_t)st < n % C::kKStages ? 1u : 0u);
-          if (fills) mbar_wait_bounded(&k_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
+          if (fills) mbar_wait_bounded(&k_full[st], (fills - 1u) & 1u, abort_flag, 1000ull * a.limit_us, c.status, false);
         }
         for (int st = 0; st < C::kVStages; ++st) {
           const uint32_t fills = nv / C::kVStages + ((uint32_t)st < nv % C::kVStages ? 1u : 0u);
-          if (fills) mbar_wait_bounded(&v_full[st], (fills - 1u) & 1u, abort_flag, kAttnTimeoutNs, c.status, false);
+          if (fills) mbar_wait_bounded(&v_full[st], (fills - 1u) & 1u, abort_flag, 1000ull * a.limit_us, c.status, false);
         }
       }
       __syncwarp();
@@ -873,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // whatever was issued has finished before tensor memory is given back (after an abort too)
       if (elect_one()) umma_commit(done);
       __syncwarp();
-      mbar_wait_bounded(done, 0, abort_flag, kAttnTimeoutNs, c.status, false);
+      mbar_wait_bounded(done, 0, abort_flag, 1000ull * a.limit_us, c.status, false);
     }
   }
   tc_fence_before();

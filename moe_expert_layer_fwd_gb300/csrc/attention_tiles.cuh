@@ -11,15 +11,14 @@ namespace moe {
 constexpr int kTile = 128;                        // keys per tile
 constexpr int kTileBytes = kTile * kHeadDim;      // E4M3 codes of one head's keys (or values) of a tile: 16 KB
 
-// Now and then while a wait lasts: has it lasted kAttnTimeoutNs (then the abort flag and DEV_ERR_TIMEOUT are set), or has
-// another role given up?  Not inline: these kernels have some thirty waits in their loops, and with a timer's code in each
+// Now and then while a wait lasts: has it lasted longer than the limit (abort_flag[1], in us; then the abort flag and
+// DEV_ERR_TIMEOUT are set), or has another role given up?  Not inline: these kernels have some thirty waits in their loops, and with a timer's code in each
 // of them instruction fetch became what the loops waited for.
-constexpr unsigned long long kAttnTimeoutNs = 2000000000ull;
 static __device__ __noinline__ bool wait_is_over(unsigned long long* since, volatile int* abort_flag, unsigned* status) {
   const unsigned long long now = globaltimer_ns();
   if (*since == 0) *since = now;
   if (*abort_flag == 1) return true;
-  if (now - *since < kAttnTimeoutNs) return false;
+  if (now - *since < 1000ull * (unsigned)abort_flag[1]) return false;
   *abort_flag = 1;
   set_status(status, DEV_ERR_TIMEOUT);
   return true;

@@ -432,3 +432,80 @@ def test_long_cache_is_split_and_joined(env):
     for new in (1, 40):
         b = Batch(rng, [new, new], [20000, 3000], 1, 128).fill(rng).dev(env)
         check(env, b, bf16(rng, 2 * new, 2, D, mul=3.0))
+
+
+@pytest.mark.parametrize("new", [1, 4, 60])
+def test_wait_limit_is_reported_and_recoverable(env, new):
+    """The values' copies are withheld: the waits for them run out, the kernel records it and returns, and the next call on the
+    same context is correct."""
+    moe, torch = env
+    rng = np.random.default_rng(59)
+    b = Batch(rng, [new] * 3, [400, 90, 1500], 2, 64).fill(rng).dev(env)
+    q = bf16(rng, 3 * new, 8, D)
+    L = moe.lib()
+    try:
+        assert L.moe_debug_set(1, 20_000_000) == moe.MOE_OK and L.moe_debug_set(4, 1) == moe.MOE_OK
+        attend(env, b, q, status=moe.MOE_ERR_TIMEOUT)
+    finally:
+        L.moe_debug_set(4, 0)
+        L.moe_debug_set(1, 0)
+    check(env, b, q)
+
+
+def test_guards_around_every_output(env):
+    """Outputs in the middle of larger buffers, whose 4 KB before and after stay as they were."""
+    moe, torch = env
+    rng = np.random.default_rng(61)
+
+    def guarded(*shape, dtype=torch.bfloat16):
+        n = int(np.prod(shape))
+        g = 4096 // torch.empty((), dtype=dtype).element_size()
+        buf = torch.full((n + 2 * g,), 77, dtype=dtype, device="cuda")
+        return buf[g:g + n].view(*shape), lambda: bool((buf[:g] == 77).all()) and bool((buf[g + n:] == 77).all())
+
+    for new in ([1, 1], [3, 5], [45, 200]):
+        T = sum(new)
+        b = Batch(rng, new, [70, 13], 2, 16).fill(rng, upto=[70, 13]).dev(env)
+        fields, intact = [], []
+        for x in b.cache:
+            y, ok = guarded(*x.shape, dtype=torch.uint8)
+            y.copy_(x)
+            fields.append(y)
+            intact.append(ok)
+        b.cache = moe.KVCache(*fields)
+        k, v, q = bf16(rng, T, 2, D), bf16(rng, T, 2, D), bf16(rng, T, 8, D)
+        rq, ok = guarded(T, 8, D)
+        intact.append(ok)
+        moe.moe_kv_append(q.cuda(), k.cuda(), v.cuda(), b.cache, b.d_start, b.d_len, b.d_table, None, q_out=rq, ws=b.ws)
+        oa.append(f64(k), f64(v), b.host, b.q_start, b.kv_len, b.table)
+        out, ok = guarded(T, 8, D)
+        intact.append(ok)
+        ws, ok = guarded(moe.lib().moe_paged_attention_workspace_size(
+            moe.ctypes.byref(moe.moe_kv_desc(2, T, 8, 2, D, 16, 0, 0)), max(new)), dtype=torch.uint8)
+        intact.append(ok)
+        moe.moe_workspace_init(ws)
+        moe.moe_paged_attention(rq, b.cache, b.d_start, b.d_len, b.d_table, max_q=max(new), out=out, ws=ws)
+        n = sum(b.total)
+        gk, ok = guarded(n, 2, D)
+        intact.append(ok)
+        gv, ok = guarded(n, 2, D)
+        intact.append(ok)
+        start = torch.zeros(2, dtype=torch.int32, device="cuda")
+        ends = torch.tensor([0, b.total[0], n], dtype=torch.int32, device="cuda")
+        moe.moe_kv_gather(b.cache, start, ends, b.d_table, n, k=gk, v=gv, ws=b.ws)
+        torch.cuda.synchronize()
+        assert all(ok() for ok in intact)
+        ref, spread = oa.attention(f64(q), b.host, b.q_start, b.kv_len, b.table, D ** -0.5)
+        assert (np.abs(f64(out) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7 * spread).all()
+
+
+@pytest.mark.parametrize("B", [1, 33, 300])
+def test_many_sequences(env, B):
+    """More sequences than one step of the searches and scans covers, some of them without new tokens or without any."""
+    rng = np.random.default_rng(67 + B)
+    for most in (1, 40):
+        new = [int(x) for x in rng.integers(0, most + 1, B)]
+        new[0] = most
+        ctx = [int(x) for x in rng.integers(0, 150, B)]
+        b = Batch(rng, new, ctx, 1, 16).fill(rng).dev(env)
+        check(env, b, bf16(rng, sum(new), 4, D), max_q=most)
