@@ -509,3 +509,16 @@ def test_many_sequences(env, B):
         ctx = [int(x) for x in rng.integers(0, 150, B)]
         b = Batch(rng, new, ctx, 1, 16).fill(rng).dev(env)
         check(env, b, bf16(rng, sum(new), 4, D), max_q=most)
+
+
+def test_decoder_layer_example(env):
+    """Decoding token by token ends in the state that the whole sequences give at once, up to the layer's bf16 roundings (and the
+    8-bit cache's second rounding where a page's scale grew: half an E4M3 step of single keys and values, averaged over the
+    sequence).  Every expert is chosen, so that no near tie of the router turns a rounding into another choice."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_layer.py")
+    spec = importlib.util.spec_from_file_location("decoder_layer", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    assert m.run(prompt=100, steps=20, batch=3, k=16, say=lambda *_: None) < 5e-2
