@@ -114,7 +114,7 @@ int moe_kv_append(const moe_kv_desc* d, const uint16_t* q, long long q_stride, c
   c.kv_len = kv_len;
   moe::KvAppendArgs a = {q, k, v, q_stride, k_stride, v_stride, cos_sin, rot_dim > 0 ? max_pos : INT32_MAX, rot_dim,
                          interleaved != 0, q_norm_weight, k_norm_weight, eps, q_out};
-  return cuda_status(moe::launch_kv_append(c, a, (cudaStream_t)stream));
+  return cuda_status(moe::launch_kv_append(c, a, sm_count(), (cudaStream_t)stream));
 }
 
 int moe_kv_gather(const moe_kv_desc* d, const int32_t* start, const int32_t* out_start, const int32_t* page_table,

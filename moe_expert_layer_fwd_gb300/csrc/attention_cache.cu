@@ -21,7 +21,6 @@ namespace {
 constexpr int kAppendThreads = 128;
 constexpr int kWarps = kAppendThreads / 32;
 constexpr int kSteps = 4;          // rows of keys (and of values) that a half-warp has in flight: 16 lanes x 8 elements each
-constexpr int kQSteps = 8;         // rows of queries that a half-warp has in flight
 constexpr int kQHeads = 16;        // query heads of one token that a warp rotates, two at a time
 
 // A row in registers: lane l of a half-warp holds elements 8l .. 8l+7.
@@ -34,18 +33,10 @@ __device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
   }
 }
 
-__device__ __forceinline__ uint4 shfl4(const uint4& r, int src) {
-  uint4 o;
-  o.x = __shfl_sync(0xffffffffu, r.x, src, 16);
-  o.y = __shfl_sync(0xffffffffu, r.y, src, 16);
-  o.z = __shfl_sync(0xffffffffu, r.z, src, 16);
-  o.w = __shfl_sync(0xffffffffu, r.w, src, 16);
-  return o;
-}
-
 // What a lane needs of the rotation, the same for every row of a token.
 struct Rotary {
-  float cs[8], sn[8];  // half-split: of elements 8 (l mod rot/16) + i; interleaved: of pairs 4l + (i / 2)
+  float cs[8], sn[8];  // half-split: of elements 8 (l mod rot/16) + i, the sine negated in the lower half;
+                       // interleaved: of pairs 4l + (i / 2)
   int partner;         // lane holding the other halves of the pairs (half-split)
   bool on, upper;
 };
@@ -72,55 +63,91 @@ __device__ __forceinline__ void rotary_load(Rotary& r, const KvAppendArgs& a, in
   } else {
     const float* p = row + 8 * (r.upper ? l - (a.rot >> 4) : l);
     const float* q = p + (a.rot >> 1);
+    const float sign = r.upper ? 1.f : -1.f;
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
       const float4 c = __ldg(reinterpret_cast<const float4*>(p + i));
       const float4 s = __ldg(reinterpret_cast<const float4*>(q + i));
       r.cs[i] = c.x; r.cs[i + 1] = c.y; r.cs[i + 2] = c.z; r.cs[i + 3] = c.w;
-      r.sn[i] = s.x; r.sn[i + 1] = s.y; r.sn[i + 2] = s.z; r.sn[i + 3] = s.w;
+      r.sn[i] = sign * s.x; r.sn[i + 1] = sign * s.y; r.sn[i + 2] = sign * s.z; r.sn[i + 3] = sign * s.w;
     }
   }
 }
 
-// Normalises (own / other: the norm weights of this lane's and of its partner's elements) and rotates one row.
-// Products and sums are rounded one by one (no fused multiply-add), so that the result does not depend on which
-// of a pair's two products a compiler chooses to fuse.
+// Pairs of floats in one 64-bit register: one instruction for two products or sums, each rounded by itself.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  return d;
+}
+
+// Normalises (w: the norm weights of this lane's elements) and rotates one row.  Products and sums are rounded one by one
+// (no fused multiply-add), so that the result does not depend on which of a pair's two products is fused.  The
+// queries' kernel is bound by these instructions: 173 for a row of two half-warps scalar, about 90 in pairs.
 __device__ __forceinline__ void norm_rotate(const uint4& raw, const Rotary& r, const KvAppendArgs& a, bool norm,
-                                            const uint4& own, const uint4& other, float (&x)[8]) {
-  float y[8];
+                                            const float (&w)[8], float (&x)[8]) {
   unpack8(raw, x);
-  unpack8(shfl4(raw, r.partner), y);
   if (norm) {
-    float ss = 0.f;
+    uint64_t sq = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+    for (int i = 0; i < 8; i += 2) sq = fma2(pair(x[i], x[i + 1]), pair(x[i], x[i + 1]), sq);
+    float ss, s1;
+    unpair(sq, ss, s1);
+    ss += s1;
 #pragma unroll
     for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, 16);
     const float rs = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
-    float w[8], u[8];
-    unpack8(own, w);
-    unpack8(other, u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = __fmul_rn(__fmul_rn(x[i], rs), w[i]);
-      y[i] = __fmul_rn(__fmul_rn(y[i], rs), u[i]);
-    }
+    for (int i = 0; i < 8; i += 2) unpair(mul2(mul2(pair(x[i], x[i + 1]), pair(rs, rs)), pair(w[i], w[i + 1])), x[i], x[i + 1]);
   }
-  if (!r.on) return;
   if (a.interleaved) {
+    if (!r.on) return;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       const float p = x[i], q = x[i + 1];
       x[i] = __fsub_rn(__fmul_rn(p, r.cs[i]), __fmul_rn(q, r.sn[i]));
       x[i + 1] = __fadd_rn(__fmul_rn(p, r.sn[i]), __fmul_rn(q, r.cs[i]));
     }
-  } else {
+  } else if (a.rot > 0) {
+    float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = __fmul_rn(x[i], r.cs[i]), s = __fmul_rn(y[i], r.sn[i]);
-      x[i] = r.upper ? __fadd_rn(s, c) : __fsub_rn(c, s);
-    }
+    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], r.partner, 16);
+    if (!r.on) return;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      unpair(add2(mul2(pair(x[i], x[i + 1]), pair(r.cs[i], r.cs[i + 1])), mul2(pair(y[i], y[i + 1]), pair(r.sn[i], r.sn[i + 1]))),
+             x[i], x[i + 1]);
   }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// This lane's norm weights (ones when there are none).
+__device__ __forceinline__ void load_weights(const uint16_t* weight, int l, float (&w)[8]) {
+  uint4 v = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  if (weight) v = __ldg(reinterpret_cast<const uint4*>(weight) + l);
+  unpack8(v, w);
 }
 
 // The smallest exponent >= -64 with amax * 2^-e <= 448 = 1.75 * 2^8.
@@ -147,49 +174,68 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= 3.402823466e38f ? a : 0.f;  // infinities and NaN do not set the scale
 }
 
-// Queries: a warp per (token, 16 heads).
+// 16 bytes from global to shared memory, in the background (a later cp_async_wait<n> waits for all but the last n groups).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Queries: a warp takes (token, 16 heads) items in turn, the next one's rows on their way to shared memory while it works on
+// the present one's (a lane reads back only what it fetched itself).  Holding the rows in registers kept too few reads in
+// flight: 64 heads of 16384 tokens 115 us, so 85 us.
+constexpr int kQPieces = kQHeads / 2;  // of 16 bytes a lane, per item
 __global__ void __launch_bounds__(kAppendThreads, 6) rope_queries_kernel(const KvBatch c, const KvAppendArgs a) {
+  __shared__ __align__(16) uint4 s_rows[2][kWarps][kQPieces][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
   pdl_launch_dependents();
   Rotary rt;
   rotary_lane(rt, a, l);
+  float weight[8];
+  load_weights(a.q_norm, l, weight);
   const int chunks = (c.Hq + kQHeads - 1) / kQHeads;
-  const long long w = (long long)blockIdx.x * kWarps + warp;
-  const int t = (int)(w / chunks), h0 = (int)(w - (long long)t * chunks) * kQHeads + half;
-  if (t >= c.T) return;
-  const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)t * a.q_stride + (size_t)h0 * kHeadDim) + l;
-  // the rows do not depend on the position: start the first of them before its loads
-  uint4 raw[kQSteps];
+  const long long items = (long long)c.T * chunks, stride = (long long)gridDim.x * kWarps;
+  auto fetch = [&](long long w, int stage) {
+    if (w < items) {
+      const int t = (int)(w / chunks), h = (int)(w - (long long)t * chunks) * kQHeads + half;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)t * a.q_stride + (size_t)h * kHeadDim) + l;
 #pragma unroll
-  for (int i = 0; i < kQSteps; ++i)
-    raw[i] = h0 + 2 * i < c.Hq ? __ldg(src + 2 * i * (kHeadDim / 8)) : make_uint4(0, 0, 0, 0);
-  const int b = warp_search(c.B, t, [&](int i) { return __ldg(c.q_start + i); });
-  SeqRange s;
-  const bool ok = load_seq(c, b, s) && t >= s.t0 && t < s.t1;
-  const int pos = ok ? s.first() + t - s.t0 : -1;
-  if (pos < 0 || pos >= a.max_pos) {
-    if (lane == 0) set_status(c.status, DEV_ERR_BOUNDS);
-    return;
-  }
-  rotary_load(rt, a, l, pos);
-  uint4 own = make_uint4(0, 0, 0, 0);
-  if (a.q_norm) own = __ldg(reinterpret_cast<const uint4*>(a.q_norm) + l);
-  const uint4 other = shfl4(own, rt.partner);
+      for (int i = 0; i < kQPieces; ++i)
+        if (h + 2 * i < c.Hq) cp_async16(smem_u32(&s_rows[stage][warp][i][lane]), src + 2 * i * (kHeadDim / 8));
+    }
+    cp_async_commit();
+  };
+  long long w = (long long)blockIdx.x * kWarps + warp;
+  fetch(w, 0);
+  int stage = 0;
+#pragma unroll 1
+  for (; w < items; w += stride, stage ^= 1) {
+    fetch(w + stride, stage ^ 1);
+    const int t = (int)(w / chunks), h0 = (int)(w - (long long)t * chunks) * kQHeads + half;
+    const int b = warp_search(c.B, t, [&](int i) { return __ldg(c.q_start + i); });
+    SeqRange s;
+    const bool ok = load_seq(c, b, s) && t >= s.t0 && t < s.t1;
+    const int pos = ok ? s.first() + t - s.t0 : -1;
+    const bool there = pos >= 0 && pos < a.max_pos;
+    if (!there && lane == 0) set_status(c.status, DEV_ERR_BOUNDS);
+    if (there) rotary_load(rt, a, l, pos);
+    cp_async_wait<1>();
+    if (!there) continue;
 #pragma unroll
-  for (int i0 = 0; i0 < kQHeads / 2; i0 += kQSteps) {
-#pragma unroll
-    for (int i = 0; i < kQSteps; ++i) {
+    for (int i = 0; i < kQPieces; ++i) {
       float x[8];
-      norm_rotate(raw[i], rt, a, a.q_norm != nullptr, own, other, x);
-      const int next = i0 + kQSteps + i, h = h0 + 2 * (i0 + i);
-      if (next < kQHeads / 2) raw[i] = h0 + 2 * next < c.Hq ? __ldg(src + 2 * next * (kHeadDim / 8)) : make_uint4(0, 0, 0, 0);
+      norm_rotate(s_rows[stage][warp][i][lane], rt, a, a.q_norm != nullptr, weight, x);
+      const int h = h0 + 2 * i;
       if (h < c.Hq) {
-        const uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                   pack_bf16x2(x[6], x[7]));
+        const uint4 o = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
         reinterpret_cast<uint4*>(a.q_out + ((size_t)t * c.Hq + h) * kHeadDim)[l] = o;
       }
     }
   }
+  cp_async_wait<0>();
 }
 
 // Keys and values: a block per unit, one touched page of one sequence and one head.  Sequence b's touched pages take the
@@ -224,9 +270,8 @@ __device__ __forceinline__ void append_unit(const KvBatch& c, const KvAppendArgs
   }
   const uint16_t* k_rows = a.k + (size_t)h * kHeadDim + 8 * l;
   const uint16_t* v_rows = a.v + (size_t)h * kHeadDim + 8 * l;
-  uint4 own = make_uint4(0, 0, 0, 0);
-  if (a.k_norm) own = __ldg(reinterpret_cast<const uint4*>(a.k_norm) + l);
-  const uint4 other = shfl4(own, rt.partner);
+  float weight[8];
+  load_weights(a.k_norm, l, weight);
   const bool norm = a.k_norm != nullptr;
 
   // the first step that has new rows; whole warps, as the shuffles below need both halves
@@ -252,7 +297,7 @@ __device__ __forceinline__ void append_unit(const KvBatch& c, const KvAppendArgs
       const bool here = r >= r0 && r < r1;
       if (here) rotary_load(rt, a, l, p0 + r);
       float x[8], v[8];
-      norm_rotate(kr[i], rt, a, norm, own, other, x);
+      norm_rotate(kr[i], rt, a, norm, weight, x);
       unpack8(vr[i], v);
       // A NaN in a token's value is kept in its key instead, as a NaN key row: the queries that see the token become
       // NaN through their score, and those that do not are untouched (0 * NaN in the product with V would reach them).
@@ -379,8 +424,8 @@ __global__ void __launch_bounds__(kGatherThreads)
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const float2 a = e4m3x2_f32(w[m] & 0xFFFFu), b = e4m3x2_f32(w[m] >> 16);
-        u[2 * m] = pack_bf16x2(a.x * f0 * f1, a.y * f0 * f1);
-        u[2 * m + 1] = pack_bf16x2(b.x * f0 * f1, b.y * f0 * f1);
+        u[2 * m] = bf16_pair(a.x * f0 * f1, a.y * f0 * f1);
+        u[2 * m + 1] = bf16_pair(b.x * f0 * f1, b.y * f0 * f1);
       }
       o[0] = make_uint4(u[0], u[1], u[2], u[3]);
       o[1] = make_uint4(u[4], u[5], u[6], u[7]);
@@ -408,10 +453,11 @@ __global__ void rope_table_kernel(int max_pos, int rot, double base, float* cos_
 
 }  // namespace
 
-cudaError_t launch_kv_append(const KvBatch& c, const KvAppendArgs& a, cudaStream_t stream) {
+cudaError_t launch_kv_append(const KvBatch& c, const KvAppendArgs& a, int n_sms, cudaStream_t stream) {
   const long long slots = (long long)c.T / c.page + 2LL * c.B;
   if (a.q) {
-    const long long chunks = (c.Hq + kQHeads - 1) / kQHeads, blocks = ((long long)c.T * chunks + kWarps - 1) / kWarps;
+    const long long chunks = (c.Hq + kQHeads - 1) / kQHeads, need = ((long long)c.T * chunks + kWarps - 1) / kWarps;
+    const long long blocks = need < 6LL * n_sms ? need : 6LL * n_sms;
     const cudaError_t e = launch_kernel(rope_queries_kernel, dim3((unsigned)blocks), dim3(kAppendThreads), 0, stream, false, c, a);
     if (e != cudaSuccess) return e;
   }

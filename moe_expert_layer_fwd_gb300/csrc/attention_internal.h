@@ -35,7 +35,7 @@ struct KvAppendArgs {
   float eps;
   uint16_t* q_out;            // [T, Hq, 128]
 };
-cudaError_t launch_kv_append(const KvBatch& c, const KvAppendArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_append(const KvBatch& c, const KvAppendArgs& a, int n_sms, cudaStream_t stream);
 
 // Rows [0, n_rows): row r of sequence b (out_start[b] <= r < out_start[b+1]) is token start[b] + r - out_start[b].
 cudaError_t launch_kv_gather(const KvBatch& c, const int32_t* start, const int32_t* out_start, int n_rows, uint16_t* k,
