@@ -85,7 +85,7 @@ class KVCache(NamedTuple):
 
     def _struct(self) -> "_m.moe_kv_cache":
         k_codes, v_codes, k_scale, v_scale = self
-        u8, shape = _m._torch().uint8, k_codes.shape
+        u8, shape = _m._torch().uint8 if _bound is None else _bound.u8, k_codes.shape
         if len(shape) != 4:
             raise ValueError(f"k_codes: expected [n_pages, Hkv, page, D], got {tuple(shape)}")
         return _m.moe_kv_cache(_need(k_codes, "k_codes", u8, shape), _need(v_codes, "v_codes", u8, shape),
@@ -172,8 +172,6 @@ def moe_kv_gather(cache: KVCache, start, out_start, page_table, n_rows: int, k=N
     n_pages, Hkv, page, D = cache[0].shape
     table, B, max_pages = _table(page_table)
     shape = (n_rows, Hkv, D)
-    if k is None and v is None:
-        k, v = _new(stream, page_table, (2,) + shape, b.bf16).unbind(0)
     k = _new(stream, page_table, shape, b.bf16) if k is None else k
     v = _new(stream, page_table, shape, b.bf16) if v is None else v
     ws = _status_ws(page_table, ws)

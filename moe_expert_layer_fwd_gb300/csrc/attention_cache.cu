@@ -21,6 +21,7 @@ namespace {
 constexpr int kAppendThreads = 128;
 constexpr int kWarps = kAppendThreads / 32;
 constexpr int kSteps = 4;          // rows of keys (and of values) that a half-warp has in flight: 16 lanes x 8 elements each
+constexpr int kQBlocksPerSm = 5;   // blocks that rotate queries
 constexpr int kQHeads = 16;        // query heads of one token that a warp rotates, two at a time
 
 // A row in registers: lane l of a half-warp holds elements 8l .. 8l+7.
@@ -101,7 +102,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
 
 // Normalises (w: the norm weights of this lane's elements) and rotates one row.  Products and sums are rounded one by one
 // (no fused multiply-add), so that the result does not depend on which of a pair's two products is fused.  The
-// queries' kernel is bound by these instructions: 173 for a row of two half-warps scalar, about 90 in pairs.
+// queries' part is bound by these instructions (scalar, with both halves of a pair normalised by either lane, 173 of them for two
+// rows: 152 us for 16384 tokens where 127 us are needed so).
 __device__ __forceinline__ void norm_rotate(const uint4& raw, const Rotary& r, const KvAppendArgs& a, bool norm,
                                             const float (&w)[8], float (&x)[8]) {
   unpack8(raw, x);
@@ -185,19 +187,18 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // Queries: a warp takes (token, 16 heads) items in turn, the next one's rows on their way to shared memory while it works on
-// the present one's (a lane reads back only what it fetched itself).  Holding the rows in registers kept too few reads in
-// flight: 64 heads of 16384 tokens 115 us, so 85 us.
-constexpr int kQPieces = kQHeads / 2;  // of 16 bytes a lane, per item
-__global__ void __launch_bounds__(kAppendThreads, 6) rope_queries_kernel(const KvBatch c, const KvAppendArgs a) {
-  __shared__ __align__(16) uint4 s_rows[2][kWarps][kQPieces][32];
+// the present one's (a lane reads back only what it fetched itself).
+constexpr int kQPieces = kQHeads / 2;                                   // of 16 bytes a lane, per item
+constexpr int kQShared = 2 * kWarps * kQPieces * 32 * (int)sizeof(uint4);  // 32 KB
+__device__ __forceinline__ void rope_queries(const KvBatch& c, const KvAppendArgs& a, int block, int blocks, uint4* shared) {
+  uint4(*s_rows)[kWarps][kQPieces][32] = reinterpret_cast<uint4(*)[kWarps][kQPieces][32]>(shared);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
-  pdl_launch_dependents();
   Rotary rt;
   rotary_lane(rt, a, l);
   float weight[8];
   load_weights(a.q_norm, l, weight);
   const int chunks = (c.Hq + kQHeads - 1) / kQHeads;
-  const long long items = (long long)c.T * chunks, stride = (long long)gridDim.x * kWarps;
+  const long long items = (long long)c.T * chunks, stride = (long long)blocks * kWarps;
   auto fetch = [&](long long w, int stage) {
     if (w < items) {
       const int t = (int)(w / chunks), h = (int)(w - (long long)t * chunks) * kQHeads + half;
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) rope_queries_kernel(const K
     }
     cp_async_commit();
   };
-  long long w = (long long)blockIdx.x * kWarps + warp;
+  long long w = (long long)block * kWarps + warp;
   fetch(w, 0);
   int stage = 0;
 #pragma unroll 1
@@ -241,14 +242,13 @@ __global__ void __launch_bounds__(kAppendThreads, 6) rope_queries_kernel(const K
 // Keys and values: a block per unit, one touched page of one sequence and one head.  Sequence b's touched pages take the
 // slots from q_start[b] / page + 2b on: n new tokens touch at most (n - 1) / page + 2 pages, so the slots of different
 // sequences never meet and T / page + 2B of them are enough.  Every unit is found from the lengths on the device: the host
-// never needs them.  The rotated keys wait in shared memory for their scale; the
-// values are read a second time (from L1 or L2).
-// Launched so that it may overlap the queries' kernel, of which it needs nothing; it ends after it.
-__device__ __forceinline__ void append_unit(const KvBatch& c, const KvAppendArgs& a, float (*s_amax)[kWarps], float4* s_k) {
+// never needs them.  The rotated keys wait in shared memory for their scale; the values are read a second time (from L1 or L2).
+__device__ __forceinline__ void append_unit(const KvBatch& c, const KvAppendArgs& a, int unit_block, float (*s_amax)[kWarps],
+                                            float4* s_k) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
   Rotary rt;
   rotary_lane(rt, a, l);
-  const int slot = (int)blockIdx.x / c.Hkv, h = (int)blockIdx.x - slot * c.Hkv;
+  const int slot = unit_block / c.Hkv, h = unit_block - slot * c.Hkv;
   const int b = warp_search(c.B, slot, [&](int i) { return (__ldg(c.q_start + i) >> c.page_log2) + 2 * i; });
   SeqRange s;
   if (!load_seq(c, b, s) || s.t1 == s.t0) return;
@@ -373,11 +373,16 @@ __device__ __forceinline__ void append_unit(const KvBatch& c, const KvAppendArgs
   }
 }
 
-__global__ void __launch_bounds__(kAppendThreads, 5) kv_append_kernel(const KvBatch c, const KvAppendArgs a) {
-  extern __shared__ float4 s_k[];  // the page's new keys, rotated: [row][2][16 lanes]
+// Blocks [0, q_blocks): queries; the others: a cache unit each.  One launch, which a decode step notices (64 sequences: 5.4 us,
+// 8.3 us as two).  Of a long prompt the queries come first and the units fill their places as they end: 132 us for 16384
+// tokens (64 + 8 + 8 heads, 638 MB, 71 % of the memory's copy rate); 127 us as two kernels with registers of their own, and
+// 141-160 us with the two kinds of blocks mixed or fewer of the first.  The queries are bound by their instructions (issue
+// slots 69 % busy before they went to pairs), the units by a chain of reads: lengths, page, rows, table, scale.
+__global__ void __launch_bounds__(kAppendThreads, 5) kv_append_kernel(const KvBatch c, const KvAppendArgs a, int q_blocks) {
+  extern __shared__ uint4 shared[];  // queries on their way, or the page's new keys, rotated: [row][2][16 lanes] of float4
   __shared__ float s_amax[2][kWarps];
-  append_unit(c, a, s_amax, s_k);
-  pdl_wait();
+  if ((int)blockIdx.x < q_blocks) rope_queries(c, a, (int)blockIdx.x, q_blocks, shared);
+  else append_unit(c, a, (int)blockIdx.x - q_blocks, s_amax, reinterpret_cast<float4*>(shared));
 }
 
 constexpr int kGatherRowsPerBlock = 32;
@@ -455,17 +460,14 @@ __global__ void rope_table_kernel(int max_pos, int rot, double base, float* cos_
 
 cudaError_t launch_kv_append(const KvBatch& c, const KvAppendArgs& a, int n_sms, cudaStream_t stream) {
   const long long slots = (long long)c.T / c.page + 2LL * c.B;
-  if (a.q) {
-    const long long chunks = (c.Hq + kQHeads - 1) / kQHeads, need = ((long long)c.T * chunks + kWarps - 1) / kWarps;
-    const long long blocks = need < 6LL * n_sms ? need : 6LL * n_sms;
-    const cudaError_t e = launch_kernel(rope_queries_kernel, dim3((unsigned)blocks), dim3(kAppendThreads), 0, stream, false, c, a);
-    if (e != cudaSuccess) return e;
-  }
-  const int bytes = c.page * kHeadDim * (int)sizeof(float);
+  const long long chunks = (c.Hq + kQHeads - 1) / kQHeads, need = a.q ? ((long long)c.T * chunks + kWarps - 1) / kWarps : 0;
+  const long long most = (long long)kQBlocksPerSm * n_sms, q_blocks = need < most ? need : most;
+  const int keys = c.page * kHeadDim * (int)sizeof(float), bytes = q_blocks && keys < kQShared ? kQShared : keys;
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kv_append_kernel), 128 * kHeadDim * (int)sizeof(float), allowed);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kv_append_kernel, dim3((unsigned)(slots * c.Hkv)), dim3(kAppendThreads), bytes, stream, a.q != nullptr, c, a);
+  return launch_kernel(kv_append_kernel, dim3((unsigned)(q_blocks + slots * c.Hkv)), dim3(kAppendThreads), bytes, stream, false, c,
+                       a, (int)q_blocks);
 }
 
 cudaError_t launch_kv_gather(const KvBatch& c, const int32_t* start, const int32_t* out_start, int n_rows, uint16_t* k,
