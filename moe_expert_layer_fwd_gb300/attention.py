@@ -42,9 +42,9 @@ def _stream_of(stream, t):
 def _new(stream, like, shape, dtype=None):
     """A new tensor on the stream that the call runs on."""
     if stream is None:
-        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+        return _b().torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
     with _b().torch.cuda.stream(stream):
-        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+        return _b().torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
 
 
 def _need(t, what: str, dtype, shape):
