@@ -437,7 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int mt = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t t_s = lanes + mt * 128, t_o = lanes + 256 + mt * kHeadDim;
-    uint32_t n0 = 0, steps = 0, xs = 0;  // tiles of earlier parts; steps of this M tile; uses of the queries' place for sums
+    uint32_t n0 = 0, steps = 0, xs = 0;  // tiles of earlier parts; steps of this M tile; halves of sums handed over
+    uint32_t segs = 0;                   // parts
     bool ok = true;
     while (ok && reader.next(g, abort_flag, c.status)) {
       const int row0 = g.qt * kRows + (kSplit ? 0 : mt * kM);  // this M tile's first
@@ -447,6 +448,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = g.first + i_row;
       // ---- this row's query, split into two E4M3 halves
       float qf;
+      // the other warps of M tile 0 have read the sums of the part before, which lie here too
+      if (kSplit && mt == 0 && segs > 0) {
+        ok = warp_wait(x_empty, (segs & 1u) ^ 1u, abort_flag, c.status);
+        if (!ok) break;
+      }
+      ++segs;
       {
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(g.t0 + i_row) * a.q_stride + (size_t)head * kHeadDim);
         uint32_t top = 0;  // bf16 magnitudes order as integers
@@ -576,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint16_t* out = a.out + ((size_t)(g.t0 + i_row) * c.Hq + head) * kHeadDim;
       // kSplit: M tile 1 puts its r and l, and its sums in two halves of the dims, where the queries were once both tiles'
       // scores are done with them; M tile 0 adds them to its own.  A row's 16-byte pieces are rotated by the row.
+      // x_empty completes three times a part: for the first half, for the second, and for the next part's queries.
       float2* other_rl = reinterpret_cast<float2*>(smem + C::kRlOff) + row;
       float4* sums = reinterpret_cast<float4*>(smem + C::kQOff) + row * 16;
       float f = 1.f, f1 = 0.f;
@@ -616,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int piece0 = (d & 32) / 4;
         if (mt == 1) {
           if ((d & 32) == 0) {
-            ok = warp_wait(x_empty, xs & 1u, abort_flag, c.status);
+            ok = warp_wait(x_empty, (segs - 1u + (uint32_t)(d >> 6)) & 1u, abort_flag, c.status);
             if (!ok) break;
           }
 #pragma unroll
@@ -649,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           write(d, o, inv);
           __syncwarp();
-          if (d == 32 && lane == 0) mbar_arrive(x_empty);
+          if ((d & 32) && lane == 0) mbar_arrive(x_empty);
         }
         if (d & 32) ++xs;
       }
