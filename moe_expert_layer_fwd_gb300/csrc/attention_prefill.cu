@@ -31,8 +31,11 @@ constexpr int kM = 128;
 constexpr int kKeys = kTile;                 // keys of a tile
 constexpr int kInfos = 4, kParts = 2;
 constexpr int kPieces = kKeys / 16;
-constexpr int kMinRun = 4;                   // cost of a block's run, at least
-constexpr int kItemCost = 3;                 // an item's own cost (loading its queries, writing its rows), in tiles
+constexpr int kMinRun = 6;                   // cost of a block's run, at least
+constexpr int kItemCost = 5;                 // an item's own cost (loading its queries, writing its rows), in tiles
+
+// A run that begins within an item has a tile of it, then: the joins count on that.
+static_assert(kMinRun > kItemCost, "runs");
 
 struct TileInfo {    // per 16 keys of a tile
   float kf[8];       // 2^e_k
