@@ -176,16 +176,6 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= 3.402823466e38f ? a : 0.f;  // infinities and NaN do not set the scale
 }
 
-// 16 bytes from global to shared memory, in the background (a later cp_async_wait<n> waits for all but the last n groups).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Queries: a warp takes (token, 16 heads) items in turn, the next one's rows on their way to shared memory while it works on
 // the present one's (a lane reads back only what it fetched itself).
 constexpr int kQPieces = kQHeads / 2;                                   // of 16 bytes a lane, per item
@@ -205,7 +195,7 @@ __device__ __forceinline__ void rope_queries(const KvBatch& c, const KvAppendArg
       const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)t * a.q_stride + (size_t)h * kHeadDim) + l;
 #pragma unroll
       for (int i = 0; i < kQPieces; ++i)
-        if (h + 2 * i < c.Hq) cp_async16(smem_u32(&s_rows[stage][warp][i][lane]), src + 2 * i * (kHeadDim / 8));
+        if (h + 2 * i < c.Hq) cp_async16(smem_u32(&s_rows[stage][warp][i][lane]), src + 2 * i * (kHeadDim / 8), 16);
     }
     cp_async_commit();
   };

@@ -69,6 +69,22 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t codes) {
   return __half22float2(__half2(h));
 }
 
+// 16 bytes from global to shared memory, in the background: the first `bytes` of them (0 or 16), then zeros.  A later
+// cp_async_wait<n> waits for all but the last n groups.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// An arrival of this thread at an mbarrier once all its copies so far are there.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // Host: gives a kernel its dynamic shared memory, once per device (`done`: one bit each, a static of the caller's).
 inline cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<unsigned long long>& done) {
   int dev = 0;

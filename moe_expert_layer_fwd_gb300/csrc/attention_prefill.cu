@@ -15,8 +15,16 @@
 // any length fill all SMs evenly, and a chunk of few rows over a long cache is split along its keys.  The rows of a split item
 // (one at each end of a run, at most) are joined by a second kernel.
 //
-// Warps (24): 0-7 and 8-15 softmax of the M tiles (thread = row and half of a tile's keys; they also load the queries,
-// rescale and write the output), 16-19 values, 20 TMA, 21 MMA, 22 scales of the tiles' pages, 23 walks the run.  Registers: 192 a
+// Items of at most 128 rows (kSplit): both M tiles hold the same rows and take its key tiles in turn, and the second one's
+// sums are added to the first one's at the end (32 rows a head over long caches: 87 us, and 103 as a half-empty item).
+//
+// Measured (8 query heads per key/value head, causal): a prompt of 16,384 tokens 1.70 ms, 1,290 TFLOP/s; a ragged batch of
+// chunks 0.49 ms, 1,050 TFLOP/s.  What bounds it is the chain of one M tile: scores read, weights made and written
+// (2,400 cycles), then the products of these weights and of the next scores (1,250), against 2,500 cycles of products
+// for both M tiles; and an item's own 11,000 cycles or so between its neighbours' tiles.
+//
+// Warps (16): 0-3 and 4-7 softmax of the M tiles (thread = row; they also fetch the queries, rescale and write the output),
+// 8-11 values, 12 TMA, 13 MMA, 14 scales of the tiles' pages, and it walks the run; 15 has nothing to do.  Registers: 192 a
 // thread for the softmax, 64 for the rest.  Every wait is bounded (2 s).
 #include "attention_tiles.cuh"
 
@@ -32,7 +40,8 @@ constexpr int kKeys = kTile;                 // keys of a tile
 constexpr int kInfos = 4, kParts = 2;
 constexpr int kPieces = kKeys / 16;
 constexpr int kMinRun = 6;                   // cost of a block's run, at least
-constexpr int kItemCost = 5;                 // an item's own cost (loading its queries, writing its rows), in tiles
+constexpr int kItemCost = 5;                 // an item's own cost (loading its queries, writing its rows), in tiles:
+                                             // a prompt of 16,384 takes 1,808 us at 3, 1,700 at 5, 1,711 at 6
 
 // A run that begins within an item has a tile of it, then: the joins count on that.
 static_assert(kMinRun > kItemCost, "runs");
@@ -64,7 +73,7 @@ struct Cfg {
   static constexpr int kV16Bytes = 2 * kTileBytes;
   static constexpr int kInfoOff = kV16Off + kV16s * kV16Bytes;
   static constexpr int kPartOff = kInfoOff + kInfos * (int)sizeof(TileInfo);
-  static constexpr int kRlOff = kPartOff + kParts * (int)sizeof(Part);  // kSplit: float2 [128], M tile 1's r and l
+  static constexpr int kRlOff = kPartOff + kParts * (int)sizeof(Part);  // kSplit: float2 [128], the queries' factors (x), then M tile 1's r and l
   static constexpr int kBarOff = kRlOff + (kSplit ? kM * 8 : 0);
   static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * kV16s + 2 * kInfos + 2 * kParts + 2 + 2 + 2 + 2 + 2 + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
@@ -184,6 +193,10 @@ struct Reader {
     ++n;
     return g.nt != 0;
   }
+  // The part that next() will give, as it stands in shared memory until then (whole warp); nullptr after a timeout.
+  __device__ const Part* peek(volatile int* abort_flag, unsigned* status) const {
+    return warp_wait(&full[n % kParts], (n / kParts) & 1u, abort_flag, status) ? &parts[n % kParts] : nullptr;
+  }
 };
 
 __device__ __forceinline__ uint32_t idesc_pv() {
@@ -267,6 +280,17 @@ __device__ __forceinline__ float max16(const uint32_t* v) {
     t1 = max3(t1, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
   }
   return fmaxf(max3(t0, __uint_as_float(v[14]), __uint_as_float(v[15])), t1);
+}
+
+// Two bf16 numbers times inv as split_e4m3x2 does it, by way of f16: 8 bits below 2^9 are exact there down to 2^-16, and
+// what is smaller has two halves of zero.
+__device__ __forceinline__ void split_bf16x2(uint32_t w, float inv, uint32_t& hi, uint32_t& lo) {
+  __half2_raw v, h;
+  *reinterpret_cast<uint32_t*>(&v) = pack_f16x2(bf16_lo(w) * inv, bf16_hi(w) * inv);
+  hi = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+  h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3);
+  h = __hsub2(__half2(v), __half2(h));
+  lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
 }
 
 // The larger bf16 magnitudes of pairs.
@@ -443,6 +467,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n0 = 0, steps = 0, xs = 0;  // tiles of earlier parts; steps of this M tile; halves of sums handed over
     uint32_t segs = 0;                   // parts
     bool ok = true;
+    float2* other_rl = reinterpret_cast<float2*>(smem + C::kRlOff) + row;  // kSplit only
+    uint8_t* hi_row = smem + C::kQOff + (kSplit ? 0 : mt * 2 * kTileBytes) + row * 128;
+    // Copies this warp's 32 query rows of a part to where their E4M3 halves will be, two whole rows at a time: a row's 16-byte
+    // pieces in turn where its hi half and where its lo half goes, so that a row can be split in place piece by piece.
+    // Threads that loaded their own rows touched 32 lines with each instruction, and that, with the loops below written
+    // out, made a ragged batch take 515 us for 490.
+    auto fetch_queries = [&](const Part& p) {
+      const int piece = lane & 15, rows = p.n * G;
+      int r = quarter * 32 + (lane >> 4), at = p.qt * kRows + (kSplit ? 0 : mt * kM) + r;
+      int i = at / G, head = at - i * G;
+      uint8_t* dst = smem + C::kQOff + (kSplit ? 0 : mt * 2 * kTileBytes) + (piece & 1) * kTileBytes;
+      const uint16_t* src = a.q + (size_t)p.t0 * a.q_stride + (size_t)p.h * G * kHeadDim + piece * 8;
+#pragma unroll 2
+      for (int k = 0; k < 16; ++k, r += 2, at += 2) {
+        const bool live = at < rows;
+        cp_async16(smem_u32(dst + r * 128 + (((piece >> 1) ^ (r & 7)) << 4)),
+                   live ? src + (size_t)i * a.q_stride + (size_t)head * kHeadDim : a.q, live ? 16 : 0);
+        head += 2;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)  // G may be 1
+          if (head >= G) {
+            head -= G;
+            ++i;
+          }
+      }
+      cp_async_commit();
+    };
+    if (!kSplit) {
+      const Part* next = reader.peek(abort_flag, c.status);
+      if (next && next->nt) fetch_queries(*next);
+    }
     while (ok && reader.next(g, abort_flag, c.status)) {
       const int row0 = g.qt * kRows + (kSplit ? 0 : mt * kM);  // this M tile's first
       const int rho = row0 + row;
@@ -451,49 +506,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = g.first + i_row;
       // ---- this row's query, split into two E4M3 halves
       float qf;
-      // the other warps of M tile 0 have read the sums of the part before, which lie here too
-      if (kSplit && mt == 0 && segs > 0) {
-        ok = warp_wait(x_empty, (segs & 1u) ^ 1u, abort_flag, c.status);
-        if (!ok) break;
-      }
-      ++segs;
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(g.t0 + i_row) * a.q_stride + (size_t)head * kHeadDim);
+      if (!kSplit || mt == 0) {
+        if (kSplit) {
+          if (segs > 0) {  // the other warps of M tile 0 have read the sums of the part before, which lie here too
+            ok = warp_wait(x_empty, (segs & 1u) ^ 1u, abort_flag, c.status);
+            if (!ok) break;
+          }
+          fetch_queries(g);
+        }
+        cp_async_wait<0>();
+        __syncwarp();
         uint32_t top = 0;  // bf16 magnitudes order as integers
-        uint4 raw[16];
-#pragma unroll
-        for (int x = 0; x < 16; ++x) raw[x] = live ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int x = 0; x < 16; ++x) top = max_magnitude(top, raw[x]);
+#pragma unroll 4
+        for (int x = 0; x < 8; ++x) {
+          const uint8_t* at = hi_row + ((x ^ (row & 7)) << 4);
+          top = max_magnitude(top, *reinterpret_cast<const uint4*>(at));
+          top = max_magnitude(top, *reinterpret_cast<const uint4*>(at + kTileBytes));
+        }
         top = max(top & 0xFFFFu, top >> 16);
         const bool bad = top >= 0x7F80u;
         const int e = bad ? 0 : query_exponent(__uint_as_float(top << 16));
-        const float inv = exp2_int(-e);
+        const float inv = bad ? CUDART_NAN_F : exp2_int(-e);  // a row with an infinity or NaN has NaN scores
         qf = a.scale_log2 * exp2_int(e);
-        uint8_t* hi_row = smem + C::kQOff + (kSplit ? 0 : mt * 2 * kTileBytes) + row * 128;
-        if (!kSplit || mt == 0) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const uint32_t w[8] = {raw[2 * x].x, raw[2 * x].y, raw[2 * x].z, raw[2 * x].w,
-                                 raw[2 * x + 1].x, raw[2 * x + 1].y, raw[2 * x + 1].z, raw[2 * x + 1].w};
+#pragma unroll 2
+        for (int x = 0; x < 8; ++x) {  // 16 dims: two pieces of bf16, then one of either half in their places
+          uint8_t* at = hi_row + ((x ^ (row & 7)) << 4);
+          const uint4 v0 = *reinterpret_cast<const uint4*>(at), v1 = *reinterpret_cast<const uint4*>(at + kTileBytes);
+          const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             uint32_t h0, l0, h1, l1;
-            split_e4m3x2(bf16_lo(w[2 * y]) * inv, bf16_hi(w[2 * y]) * inv, h0, l0);
-            split_e4m3x2(bf16_lo(w[2 * y + 1]) * inv, bf16_hi(w[2 * y + 1]) * inv, h1, l1);
-            hi[y] = bad ? 0x7F7F7F7Fu : h0 | h1 << 16;  // a row with an infinity or NaN has NaN scores
-            lo[y] = bad ? 0x7F7F7F7Fu : l0 | l1 << 16;
+            split_bf16x2(w[2 * y], inv, h0, l0);
+            split_bf16x2(w[2 * y + 1], inv, h1, l1);
+            hi[y] = h0 | h1 << 16;
+            lo[y] = l0 | l1 << 16;
           }
-          const int at = (x ^ (row & 7)) << 4;
-          *reinterpret_cast<uint4*>(hi_row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(hi_row + kTileBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(at + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
+        if (kSplit) other_rl->x = qf;
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[mt]);
-        }
+      } else {  // M tile 0's rows are this one's
+        ok = warp_wait(&q_full[0], segs & 1u, abort_flag, c.status);
+        if (!ok) break;
+        qf = other_rl->x;
       }
+      ++segs;
       // keys [w_lo, w_hi) are seen by every row of this warp
       const int warp_rho = row0 + quarter * 32, tiles = C::tiles(g);
       const int w_hi = a.causal ? min(g.hi, g.first + warp_rho / G + 1) : g.hi;
@@ -577,6 +638,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       n0 += tiles;
+      // all of this M tile's scores are done: the next part's queries may come over these
+      if (!kSplit && ok) {
+        const Part* next = reader.peek(abort_flag, c.status);
+        ok = next != nullptr;
+        if (ok && next->nt) fetch_queries(*next);
+      }
       // ---- the rows' outputs
       ok = ok && warp_wait(&o_full[mt], (steps - 1u) & 1u, abort_flag, c.status);
       if (!ok) break;
@@ -587,7 +654,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // kSplit: M tile 1 puts its r and l, and its sums in two halves of the dims, where the queries were once both tiles'
       // scores are done with them; M tile 0 adds them to its own.  A row's 16-byte pieces are rotated by the row.
       // x_empty completes three times a part: for the first half, for the second, and for the next part's queries.
-      float2* other_rl = reinterpret_cast<float2*>(smem + C::kRlOff) + row;
       float4* sums = reinterpret_cast<float4*>(smem + C::kQOff) + row * 16;
       float f = 1.f, f1 = 0.f;
       if (kSplit && mt == 0) {
@@ -667,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_before();
     }
+    cp_async_wait<0>();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp < kTmaWarp) {
