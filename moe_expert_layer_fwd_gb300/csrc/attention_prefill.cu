@@ -573,12 +573,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s[kKeys / 32][32];
 #pragma unroll
         for (int w = 0; w < kKeys / 32; ++w) tmem_ld32_async(t_s + 32 * w, s[w]);
-        float kf[kPieces], lv[kPieces];
-#pragma unroll
-        for (int b = 0; b < kPieces; ++b) {
-          kf[b] = qf * ti.kf[b];
-          lv[b] = ti.lv[b];
-        }
         tmem_wait_ld();
         const int j0 = (g.tile0 + i) * kKeys;
         if (j0 < w_lo || j0 + kKeys > w_hi || have != (1u << kPieces) - 1u) {
@@ -593,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float m = -CUDART_INF_F;
 #pragma unroll
-        for (int b = 0; b < kPieces; ++b) m = fmaxf(m, fmaf(max16(&s[b >> 1][(b & 1) * 16]), kf[b], lv[b]));
+        for (int b = 0; b < kPieces; ++b) m = fmaxf(m, fmaf(max16(&s[b >> 1][(b & 1) * 16]), qf * ti.kf[b], ti.lv[b]));
         const bool grow = m > r + 8.f || (r == -CUDART_INF_F && m > r);
         if (x >= C::kStep && __any_sync(0xffffffffu, grow)) {
           // the sums so far are of the tile before: wait for its product, then bring them to the new reference
@@ -610,8 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float base = 7.f - (r == -CUDART_INF_F ? 0.f : r);
 #pragma unroll
         for (int b = 0; b < kPieces; ++b) {
-          const float add = base + lv[b];
-          const uint64_t kf2 = f32x2(kf[b], kf[b]), add2 = f32x2(add, add);
+          const float kf = qf * ti.kf[b], add = base + ti.lv[b];
+          const uint64_t kf2 = f32x2(kf, kf), add2 = f32x2(add, add);
           uint64_t sum = 0;
           const uint32_t* v = &s[b >> 1][(b & 1) * 16];
 #pragma unroll
