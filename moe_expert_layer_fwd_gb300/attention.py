@@ -139,10 +139,7 @@ def moe_kv_append(q, k, v, cache: KVCache, q_start, kv_len, page_table, cos_sin=
     if q is not None:
         Hq = q.shape[1]
         qp, qs = _rows(q, "q", Hq, D)
-        if q_out is None:
-            q_out = _new(stream, k, (T, Hq, D))
-            op = q_out.data_ptr()
-        else:
+        if q_out is not None:
             op = _need(q_out, "q_out", b.bf16, (T, Hq, D))
     max_pos, cs = 0, None
     if cos_sin is None:
@@ -153,12 +150,15 @@ def moe_kv_append(q, k, v, cache: KVCache, q_start, kv_len, page_table, cos_sin=
             rot_dim = cos_sin.shape[1]
         cs = _need(cos_sin, "cos_sin", b.f32, (max_pos, rot_dim))
     ws = _status_ws(k, ws)
-    status = b.append(
-        _byref(_m.moe_kv_desc(B, T, Hq, Hkv, D, page, n_pages, max_pages)), qp, qs, kp, ks, vp, vs,
-        _need(q_start, "q_start", b.i32, (B + 1,)), _need(kv_len, "kv_len", b.i32, (B,)), table, cs, max_pos, rot_dim,
-        interleaved, None if q_norm_weight is None else _need(q_norm_weight, "q_norm_weight", b.bf16, (D,)),
-        None if k_norm_weight is None else _need(k_norm_weight, "k_norm_weight", b.bf16, (D,)), eps, op, _byref(kv),
-        ws.data_ptr(), ws.numel(), _stream_of(stream, k))
+    starts, lens = _need(q_start, "q_start", b.i32, (B + 1,)), _need(kv_len, "kv_len", b.i32, (B,))
+    qw = None if q_norm_weight is None else _need(q_norm_weight, "q_norm_weight", b.bf16, (D,))
+    kw = None if k_norm_weight is None else _need(k_norm_weight, "k_norm_weight", b.bf16, (D,))
+    d = _m.moe_kv_desc(B, T, Hq, Hkv, D, page, n_pages, max_pages)
+    if q is not None and q_out is None:
+        q_out = _new(stream, k, (T, Hq, D))
+        op = q_out.data_ptr()
+    status = b.append(_byref(d), qp, qs, kp, ks, vp, vs, starts, lens, table, cs, max_pos, rot_dim, interleaved, qw, kw, eps,
+                      op, _byref(kv), ws.data_ptr(), ws.numel(), _stream_of(stream, k))
     if status:
         _m._check(status, "moe_kv_append")
     return q_out
@@ -172,13 +172,19 @@ def moe_kv_gather(cache: KVCache, start, out_start, page_table, n_rows: int, k=N
     n_pages, Hkv, page, D = cache[0].shape
     table, B, max_pages = _table(page_table)
     shape = (n_rows, Hkv, D)
-    k = _new(stream, page_table, shape, b.bf16) if k is None else k
-    v = _new(stream, page_table, shape, b.bf16) if v is None else v
+    starts, out_starts = _need(start, "start", b.i32, (B,)), _need(out_start, "out_start", b.i32, (B + 1,))
+    d = _m.moe_kv_desc(B, 0, Hkv, Hkv, D, page, n_pages, max_pages)
     ws = _status_ws(page_table, ws)
-    status = b.gather(
-        _byref(_m.moe_kv_desc(B, 0, Hkv, Hkv, D, page, n_pages, max_pages)), _need(start, "start", b.i32, (B,)),
-        _need(out_start, "out_start", b.i32, (B + 1,)), table, _byref(kv), n_rows, _need(k, "k", b.bf16, shape),
-        _need(v, "v", b.bf16, shape), ws.data_ptr(), ws.numel(), _stream_of(stream, page_table))
+    kp = None if k is None else _need(k, "k", b.bf16, shape)
+    vp = None if v is None else _need(v, "v", b.bf16, shape)
+    if k is None:
+        k = _new(stream, page_table, shape, b.bf16)
+        kp = k.data_ptr()
+    if v is None:
+        v = _new(stream, page_table, shape, b.bf16)
+        vp = v.data_ptr()
+    status = b.gather(_byref(d), starts, out_starts, table, _byref(kv), n_rows, kp, vp, ws.data_ptr(), ws.numel(),
+                      _stream_of(stream, page_table))
     if status:
         _m._check(status, "moe_kv_gather")
     return k, v
@@ -210,13 +216,15 @@ def moe_paged_attention(q, cache: KVCache, q_start, kv_len, page_table, max_q: i
     T, Hq = q.shape[0], q.shape[1]
     qp, qs = _rows(q, "q", Hq, D)
     d = _m.moe_kv_desc(B, T, Hq, Hkv, D, page, n_pages, max_pages)
+    starts, lens = _need(q_start, "q_start", b.i32, (B + 1,)), _need(kv_len, "kv_len", b.i32, (B,))
+    ws = _workspace(d, max_q, q, stream) if ws is None else _status_ws(q, ws)
     if out is None:
         out = _new(stream, q, (T, Hq, D))
-    ws = _workspace(d, max_q, q, stream) if ws is None else _status_ws(q, ws)
-    status = b.attention(
-        _byref(d), qp, qs, _need(q_start, "q_start", b.i32, (B + 1,)), _need(kv_len, "kv_len", b.i32, (B,)), table,
-        _byref(kv), max_q, D ** -0.5 if scale is None else scale, causal, window,
-        _need(out, "out", b.bf16, (T, Hq, D)), ws.data_ptr(), ws.numel(), _stream_of(stream, q))
+        op = out.data_ptr()
+    else:
+        op = _need(out, "out", b.bf16, (T, Hq, D))
+    status = b.attention(_byref(d), qp, qs, starts, lens, table, _byref(kv), max_q, D ** -0.5 if scale is None else scale,
+                         causal, window, op, ws.data_ptr(), ws.numel(), _stream_of(stream, q))
     if status:
         _m._check(status, "moe_paged_attention")
     return out

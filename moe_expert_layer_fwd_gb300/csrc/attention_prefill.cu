@@ -20,8 +20,8 @@
 //
 // Measured (8 query heads per key/value head, causal): a prompt of 16,384 tokens 1.70 ms, 1,290 TFLOP/s; a ragged batch of
 // chunks 0.49 ms, 1,050 TFLOP/s.  What bounds it is the chain of one M tile: scores read, weights made and written
-// (2,400 cycles), then the products of these weights and of the next scores (1,250), against 2,500 cycles of products
-// for both M tiles; and an item's own 11,000 cycles or so between its neighbours' tiles.
+// (1,900 cycles), then the products of these weights and of the next scores (1,400 with their latency), where the products
+// of both M tiles would take 2,050; and an item's own 11,000 cycles or so between its neighbours' tiles.
 //
 // Warps (16): 0-3 and 4-7 softmax of the M tiles (thread = row; they also fetch the queries, rescale and write the output),
 // 8-11 values, 12 TMA, 13 MMA, 14 scales of the tiles' pages, and it walks the run; 15 has nothing to do.  Registers: 192 a
