@@ -100,10 +100,11 @@ def _table(page_table):
     return _need(page_table, "page_table", _b().i32, shape), shape[0], shape[1]
 
 
-def _status_ws(like, ws):
-    """The workspace given, or a new one with a clear status word."""
+def _status_ws(like, ws, stream=None):
+    """The workspace given, or a new one with a clear status word, on the stream that the call runs on."""
     if ws is None:
-        return _b().torch.zeros(max(_b().status_bytes, 256), dtype=_b().u8, device=like.device)
+        with _b().torch.cuda.stream(stream):
+            return _b().torch.zeros(max(_b().status_bytes, 256), dtype=_b().u8, device=like.device)
     if not ws.is_cuda or not ws.is_contiguous():
         raise ValueError("ws: expected a contiguous CUDA tensor")
     return ws
@@ -149,7 +150,7 @@ def moe_kv_append(q, k, v, cache: KVCache, q_start, kv_len, page_table, cos_sin=
         if rot_dim is None:
             rot_dim = cos_sin.shape[1]
         cs = _need(cos_sin, "cos_sin", b.f32, (max_pos, rot_dim))
-    ws = _status_ws(k, ws)
+    ws = _status_ws(k, ws, stream)
     starts, lens = _need(q_start, "q_start", b.i32, (B + 1,)), _need(kv_len, "kv_len", b.i32, (B,))
     qw = None if q_norm_weight is None else _need(q_norm_weight, "q_norm_weight", b.bf16, (D,))
     kw = None if k_norm_weight is None else _need(k_norm_weight, "k_norm_weight", b.bf16, (D,))
@@ -174,7 +175,7 @@ def moe_kv_gather(cache: KVCache, start, out_start, page_table, n_rows: int, k=N
     shape = (n_rows, Hkv, D)
     starts, out_starts = _need(start, "start", b.i32, (B,)), _need(out_start, "out_start", b.i32, (B + 1,))
     d = _m.moe_kv_desc(B, 0, Hkv, Hkv, D, page, n_pages, max_pages)
-    ws = _status_ws(page_table, ws)
+    ws = _status_ws(page_table, ws, stream)
     kp = None if k is None else _need(k, "k", b.bf16, shape)
     vp = None if v is None else _need(v, "v", b.bf16, shape)
     if k is None:
@@ -246,16 +247,19 @@ class AttentionLayer:
         self.cos_sin = moe_rope_table(max_pos, rot_dim, rope_base, device=device) if rot_dim else None
         self.interleaved, self.q_norm_weight, self.k_norm_weight, self.eps = interleaved, q_norm_weight, k_norm_weight, eps
         self.scale, self.window = scale, window
-        self.ws = _status_ws(self.cache.k_codes, None)
+        self.ws, self._outgrown = _status_ws(self.cache.k_codes, None), []
 
     def forward(self, qkv, q_start, kv_len, page_table, max_q: int, out=None, stream=None):
         T = qkv.shape[0]
         q, k, v = qkv.view(T, self.Hq + 2 * self.Hkv, self.D).split([self.Hq, self.Hkv, self.Hkv], dim=1)
         d = _m.moe_kv_desc(page_table.shape[0], T, self.Hq, self.Hkv, self.D, 16, 0, 0)
         if self.ws.numel() < _b().workspace_size(_byref(d), max_q):
-            status = self.ws[:_b().status_bytes]
+            # The smaller one is kept: a captured graph, or a call still running on another stream, goes on using it (there
+            # are few sizes).
+            self._outgrown.append(self.ws)
             self.ws = _workspace(d, max_q, self.ws, stream)
-            self.ws[:_b().status_bytes].copy_(status)  # what an earlier call reported stays readable
+            with _b().torch.cuda.stream(stream):  # what an earlier call reported stays readable
+                self.ws[:_b().status_bytes].copy_(self._outgrown[-1][:_b().status_bytes])
         rq = moe_kv_append(q, k, v, self.cache, q_start, kv_len, page_table, self.cos_sin, None, self.interleaved,
                            self.q_norm_weight, self.k_norm_weight, self.eps, ws=self.ws, stream=stream)
         o = moe_paged_attention(rq, self.cache, q_start, kv_len, page_table, max_q, self.scale, True, self.window,

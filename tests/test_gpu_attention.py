@@ -406,6 +406,39 @@ def test_graph_follows_the_lengths(env):
     assert moe.moe_get_device_status(layer.ws) == moe.MOE_OK
 
 
+def test_layer_workspace_grows_behind_a_graph(env):
+    """A decode graph captured before a prompt made the layer's workspace grow still has its own: replays give the same
+    bits, and write nothing into memory that was allocated since.  The prompt runs on a stream of its own."""
+    moe, torch = env
+    rng = np.random.default_rng(53)
+    layers = [moe.AttentionLayer(80, 8, 2, page=16, max_pos=1024) for _ in range(2)]
+    table = torch.from_numpy(rng.permutation(80).reshape(1, 80).astype(np.int32)).cuda()
+    start, lens = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 1], [1]))
+    qkv = torch.zeros(1, 12 * D, dtype=torch.bfloat16, device="cuda")
+    prompt, p_start, p_len = bf16(rng, 700, 12 * D).cuda(), *(torch.tensor(x, dtype=torch.int32, device="cuda") for x in
+                                                             ([0, 700], [700]))
+    for layer in layers:
+        layer.forward(qkv, start, lens, table, 1)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = layers[0].forward(qkv, start, lens, table, 1)
+    small = layers[0].ws.numel()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    one = layers[0].forward(prompt, p_start, p_len, table, 700, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert layers[0].ws.numel() > small
+    assert torch.equal(one, layers[1].forward(prompt, p_start, p_len, table, 700))
+    since = [torch.full((small,), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for step in range(4):
+        lens.fill_(701 + step)
+        qkv.copy_(bf16(rng, 1, 12 * D))
+        g.replay()
+        assert torch.equal(out, layers[1].forward(qkv, start, lens, table, 1))
+    assert all(bool((t == 7).all()) for t in since)
+    assert all(moe.moe_get_device_status(layer.ws) == moe.MOE_OK for layer in layers)
+
+
 def test_cache_beyond_2_31_bytes(env):
     """Pages whose codes start past 2^31 bytes of the pool."""
     moe, torch = env
