@@ -228,7 +228,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
   int* s_begin = reinterpret_cast<int*>(smem + C::kMiscOff + 12);  // b, h, tile
-  volatile int* s_bad = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 24);  // [3] a softmax warp gave up (as s_max)
+  // [group][3]: a softmax warp of the group gave up (as s_max).  A group's own: its warps read it between two of the group's
+  // barriers, where no other warp writes it, so all of them leave or all stay; a flag of both groups' could be set by the
+  // other one while they read it, and those that stayed would wait at the barrier for those that left, with no limit.
+  volatile int* s_bad_all = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 24);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = c.Hq / c.Hkv;
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     mbar_init(done, 1);
     abort_flag[0] = 0;
     abort_flag[1] = (int)a.limit_us;
-    for (int i = 0; i < 3; ++i) s_bad[i] = 0;
+    for (int i = 0; i < 3 * C::kGroups; ++i) s_bad_all[i] = 0;
     fence_mbar_init();
   }
   if (warp == C::kMmaWarp) tmem_alloc(tmem_slot, C::kTmemCols);
@@ -523,6 +526,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     uint32_t n = 0, segs = 0;
     bool ok = true;
     const uint32_t mine = tmem + ((uint32_t)(w4 * 32) << 16) + col0;  // this thread's lane and columns
+    volatile int* s_bad = s_bad_all + 3 * group;
     auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };
     float r[N], l[N];
     while (walk.next(g)) {
