@@ -5,14 +5,21 @@
 // this head (columns: new tokens x grouped heads, NC of them),
 //   S^T[128 keys, 2 NC] = K . [q_hi | q_lo]^T           tcgen05 kind::f8f6f4, M = 128, N = 2 NC
 //   u = (S_hi + S_lo) * scale * 2^(e_k + e_q) + e_v     log2 of the weight times the size of the page's values
-//   r = max(r, max_j u),  p'_j = 2^(u_j - r + 8) = hi + lo in E4M3,  l = l f + sum_j p'_j 2^-e_v
-//   O^T[128 dims, 2 NC] = V^T . [p'_hi | p'_lo]          the same instruction, V read with its dims contiguous
+//   r = max(r, max_j u),  p'_j = 2^(u_j - r + 6),  l = l f + sum_j p'_j 2^-e_v
+//   p'_j = hi + lo / 32 if p'_j >= 2^-7, else 2^-15 (hi + lo / 32); hi, lo in E4M3
+//   O^T[128 dims, 4 NC] = V^T . [hi | lo | hi of small weights | lo of them]   the same instruction, V read with its dims contiguous
 // so that neither keys nor values pass through a register: TMA writes the pages' codes to shared memory with the
 // 128-byte swizzle and the tensor core reads them there, once each.  Scales never touch the codes: those of the keys
 // are multiplied onto S, those of the values are added to the exponent.  The reference r follows the running maximum of u:
-// the largest p' lies within 2^6 .. 2^8.8 whatever the pages' scales are, errors are relative to the largest
-// term of the sum that is being computed, and the denominator takes the scale out again.  hi + lo keeps 8 bits of p' down to
-// 2^-8 of the largest.
+// the largest p' lies within 2^6 .. 2^8 whatever the pages' scales are, errors are relative to the largest
+// term of the sum that is being computed, and the denominator takes the scale out again.
+//
+// Range of the weights: the four kinds of parts have accumulators of their own, so each has a scale of its own.  A weight keeps
+// 8 bits down to 2^-28 of the largest and is rounded to multiples of 2^-35 of it below.  That is needed: a key that takes
+// most of the softmax leaves thousands of others with 2^-16 .. 2^-24 of its weight and, together, a share that counts.  (Two parts
+// of one scale keep multiples of 2^-15: 8000 equal keys 12 nats below one lose their whole share, 5 % of the output.)  The parts of
+// the small weights cost a decode batch of 64 sequences 2 us (117 -> 119).
+//
 // A softmax thread owns one key and half of the columns (S, p'), and one output dim of them (O, accumulated in tensor memory
 // and rescaled only when r moves).
 //
@@ -34,9 +41,13 @@ namespace {
 constexpr int kWholeTiles = 4;    // rows of at most so many tiles are not split
 constexpr int kMinRun = 4;        // tiles in a block's run, at least (4 sequences of 2000, 8 key/value heads: 21.6 us at 2,
                                   // 19.6 at 4, 23.7 at 6; one of 1000: 17.5, 17.5, 21.6)
-// p' = 2^(u - r + kBase) with u <= r + kSlack stays below 448, the largest E4M3 number (2^8.8); r itself moves so
-// seldom that the sums in tensor memory are hardly ever rescaled.
-constexpr float kBase = 6.f, kSlack = 2.75f;
+// p' = 2^(u - r + kBase) with u <= r + kSlack is at most 2^8; r moves so seldom that the sums in tensor memory are hardly ever
+// rescaled.
+constexpr float kBase = 6.f, kSlack = 2.f;
+// What hi leaves of a number up to 2^8 is at most 8, so lo can be stored 32 times larger; weights below 2^kSmall are stored 2^15
+// times larger, at most 2^8 then.  Rounded to multiples of E4M3's smallest number, 2^-9 / 32, a number has 8 bits from 2^-7 on.
+constexpr float kSmall = -7.f, kSmallDown = 1.f / 32768.f;
+constexpr float kLoUp = 32.f, kLoDown = 1.f / 32.f;
 
 struct TileInfo {    // per 16 keys of a tile
   float kf[8];       // 2^e_k
@@ -56,11 +67,12 @@ struct Cfg {
   static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kQWarp = kSoftWarps + 2;
   static constexpr int kThreads = 32 * (kSoftWarps + 3);
-  static constexpr int kRows = 2 * NC;                      // hi and lo rows of the queries, of the weights
+  static constexpr int kRows = 2 * NC;                      // hi and lo rows of the queries
+  static constexpr int kPRows = 4 * NC;                     // columns of the weights' product: hi, lo; hi, lo of small ones
   static constexpr int kQBytes = kRows * 128;
   static constexpr int kPBlock = kTile * 16;                // the weights of 16 columns: 16 bytes a key
   static constexpr int kPOff = kStages * 2 * kTileBytes;
-  static constexpr int kPBytes = kRows / 16 * kPBlock;
+  static constexpr int kPBytes = kPRows / 16 * kPBlock;
   static constexpr int kQOff = kPOff + 2 * kPBytes;         // the weights of even and odd tiles
   static constexpr int kBarOff = kQOff + kQBufs * kQBytes;
   static constexpr int kNumBars = 4 * kStages + 2 * kQBufs + 9;
@@ -69,7 +81,7 @@ struct Cfg {
   static constexpr int kMaxOff = kQfOff + kQBufs * NC * 8;  // float [3][NC][4]: maxima of even, odd tiles; denominators
   static constexpr int kMiscOff = kMaxOff + 3 * NC * 16;
   static constexpr int kBytes = 1024 + kMiscOff + 64;
-  static constexpr int kTmemCols = 4 * kRows;               // S twice, O (a power of two)
+  static constexpr int kTmemCols = 2 * kRows + kPRows;      // S twice, O (a power of two)
   static constexpr int kOCol = 2 * kRows;
   static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
@@ -165,6 +177,22 @@ __device__ __forceinline__ void add_product(uint32_t taddr, int lo, float (&acc)
   for (int x = 0; x < N; ++x) acc[x] += __uint_as_float(s[x]) + __uint_as_float(t[x]);
 }
 
+// The sums of the weights' parts: columns x, `lo` + x, 2 `lo` + x and 3 `lo` + x of this thread's tensor-memory lane.
+template <int N>
+__device__ __forceinline__ void add_parts(uint32_t taddr, int lo, float (&acc)[N]) {
+  uint32_t s[N], t[N];
+  tmem_ld_async(taddr + 2 * lo, s);
+  tmem_ld_async(taddr + 3 * lo, t);
+  tmem_wait_ld();
+#pragma unroll
+  for (int x = 0; x < N; ++x) acc[x] = fmaf(__uint_as_float(t[x]), kLoDown, __uint_as_float(s[x])) * kSmallDown;
+  tmem_ld_async(taddr, s);
+  tmem_ld_async(taddr + lo, t);
+  tmem_wait_ld();
+#pragma unroll
+  for (int x = 0; x < N; ++x) acc[x] += fmaf(__uint_as_float(t[x]), kLoDown, __uint_as_float(s[x]));
+}
+
 // Columns x and `lo` + x of this thread's tensor-memory lane, times f[x].
 template <int N>
 __device__ __forceinline__ void scale_columns(uint32_t taddr, int lo, const float (&f)[N]) {
@@ -200,6 +228,13 @@ __device__ __forceinline__ int columns_max(float (&v)[N], int lane) {
 #pragma unroll
   for (; off >= 1; off /= 2) v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], off));
   return col;
+}
+
+// Two weights as hi + lo / kLoUp.
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = e4m3x2(a, b);
+  const float2 h = e4m3x2_f32(hi);
+  lo = e4m3x2((a - h.x) * kLoUp, (b - h.y) * kLoUp);
 }
 
 template <int NC>
@@ -398,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
   } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMA: scores run one tile ahead of the weighted sums.  The
     // whole warp walks along and one lane issues: descriptors stay in uniform registers.
-    const uint32_t id_s = umma_idesc_e4m3(kTile, C::kRows, false, false), id_o = umma_idesc_e4m3(kHeadDim, C::kRows, true, true);
+    const uint32_t id_s = umma_idesc_e4m3(kTile, C::kRows, false, false), id_o = umma_idesc_e4m3(kHeadDim, C::kPRows, true, true);
     const uint64_t desc = umma_desc_sw128(smem_u32(smem));
     const uint64_t pdesc = umma_desc_mn16(smem_u32(smem) + C::kPOff, C::kPBlock);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -586,21 +621,20 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           ok = false;
           break;
         }
-        // The reference follows the maximum when that has grown by more than kSlack (the same for the whole group)
+        // The references follow the maxima when one of them has grown by more than kSlack (the same for the whole group)
         // (without a branch per column, which would have each of these loads wait for the one before)
         float top[N], f[N];
         bool moved = false;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
           const float4 m = *reinterpret_cast<const float4*>(tops + x * 4);
-          const float t = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w));
-          const bool up = t > r[x] + kSlack;  // r = -infinity: any finite t
-          top[x] = up ? t : r[x];
-          moved |= up;
+          top[x] = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w));
+          moved |= top[x] > r[x] + kSlack;  // r = -infinity: any finite maximum
         }
         if (moved) {
 #pragma unroll
           for (int x = 0; x < N; ++x) {
+            top[x] = fmaxf(top[x], r[x]);
             f[x] = top[x] == r[x] ? 1.f : ex2(r[x] - top[x]);
             l[x] *= f[x];
             r[x] = top[x];
@@ -612,32 +646,36 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           if (ok) {
             tc_fence_after();
             scale_columns<N>(mine + C::kOCol, NC, f);
+            scale_columns<N>(mine + C::kOCol + 2 * NC, NC, f);
             tc_fence_before();
           }
         }
-        uint32_t hi[N / 4], lo[N / 4];
+        // 16 columns to a block of 16 bytes a key: the hi parts of all columns, then the lo parts, then both of small weights.  (The
+        // product that read these bytes two tiles ago was issued before this tile's scores, so it has finished.)
+        uint8_t* pw = smem + C::kPOff + (n & 1u) * C::kPBytes + key * 16;
+        auto put = [&](int col, uint32_t v) { *reinterpret_cast<uint32_t*>(pw + col / 16 * C::kPBlock + col % 16) = v; };
 #pragma unroll
         for (int x = 0; x < N; x += 4) {
           float p[4];
+          uint32_t small = 0;  // a byte of ones where the weight is
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            p[y] = ex2(u[x + y] - (r[x + y] == -CUDART_INF_F ? 0.f : r[x + y]) + kBase);
+            const float z = u[x + y] - (r[x + y] == -CUDART_INF_F ? 0.f : r[x + y]) + kBase;
+            p[y] = ex2(z);
             l[x + y] = fmaf(p[y], un, l[x + y]);
+            const bool is_small = z < kSmall;  // not a NaN
+            p[y] *= is_small ? 1.f / kSmallDown : 1.f;
+            small |= is_small ? 0xFFu << (8 * y) : 0u;
           }
           uint32_t h0, l0, h1, l1;
-          split_e4m3x2(p[0], p[1], h0, l0);
-          split_e4m3x2(p[2], p[3], h1, l1);
-          hi[x / 4] = h0 | h1 << 16;
-          lo[x / 4] = l0 | l1 << 16;
-        }
-        // 16 columns to a block of 16 bytes a key: the hi parts of all columns, then the lo parts.  (The product that read
-        // these bytes two tiles ago was issued before this tile's scores, so it has finished.)
-        uint8_t* pw = smem + C::kPOff + (n & 1u) * C::kPBytes + key * 16;
-#pragma unroll
-        for (int x = 0; x < N / 4; ++x) {
-          const int at = col0 + 4 * x;
-          *reinterpret_cast<uint32_t*>(pw + at / 16 * C::kPBlock + at % 16) = hi[x];
-          *reinterpret_cast<uint32_t*>(pw + (NC + at) / 16 * C::kPBlock + (NC + at) % 16) = lo[x];
+          split_weights(p[0], p[1], h0, l0);
+          split_weights(p[2], p[3], h1, l1);
+          const uint32_t hi = h0 | h1 << 16, lo = l0 | l1 << 16;
+          const int at = col0 + x;
+          put(at, hi & ~small);
+          put(NC + at, lo & ~small);
+          put(2 * NC + at, hi & small);
+          put(3 * NC + at, lo & small);
         }
         // A key that no row sees has weight 0, but its value bytes may be anything: 0 * NaN.  They become zeros.
         const bool gone = !there || j < g.r.lo;
@@ -659,7 +697,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       for (int x = 0; x < N; ++x) acc[x] = 0.f;
       if (ok) {
         tc_fence_after();
-        add_product<N>(mine + C::kOCol, NC, acc);
+        add_parts<N>(mine + C::kOCol, NC, acc);
         tc_fence_before();
       }
       // the denominators: over the warp, then over the group
