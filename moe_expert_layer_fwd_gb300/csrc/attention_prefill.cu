@@ -4,12 +4,15 @@
 // that take turns on the tensor core -- while one's softmax runs, the other's products do -- against key tiles of 128:
 //   S[128, 128 keys] = Q_hi . K^T + Q_lo . K^T     kind::f8f6f4: queries split in two E4M3 halves, keys as cached
 //   u = S * scale * 2^(e_k + e_q) + e_v            per page of the tile: a factor and a summand for its columns
-//   p' = 2^(u - r + 7) in f16,  l += 2^-e_v sum p'
+//   p' = 2^(u - r + 9) in f16,  l += 2^-e_v sum p'
 //   O[128, 128 dims] += p' . V                     kind::f16, p' in tensor memory over S, V as exact f16 numbers
 // Two products of E4M3 cost what one of bf16 does, and the keys need no conversion; the values are converted once per tile
 // for both M tiles by four warps of their own (an E4M3 code is an f16 number; their scales stay out of them).  r follows the
-// running maximum of u, and with it O is rescaled, only when that has grown by more than 2^8 since: p' then stays below
-// 2^15, and f16 keeps 11 bits of it down to 2^-21 of the largest.
+// running maximum of u, and with it O is rescaled, only when that of one of a warp's rows has grown by more than 2^6.9 since (then
+// all of them follow): p' stays below 2^15.9 of f16's 65504 and keeps 11 bits down to 2^-23 of the largest, 8 down to 2^-26; below, it
+// is rounded to multiples of 2^-33 of that one.  (One key may take most of a row, whose thousands of others then count together.
+// Each factor of two more costs rescaling: a ragged batch of chunks takes 487 us at 2^8 and a smallest step of 2^-31, 490 so,
+// 499 at 2^5.9 and 521 at 2^3.9.)
 //
 // Work: the items' tiles in one order, cut into equal runs, one per block and SM, as in the decode kernel: causal items of
 // any length fill all SMs evenly, and a chunk of few rows over a long cache is split along its keys.  The rows of a split item
@@ -45,6 +48,8 @@ constexpr int kItemCost = 5;                 // an item's own cost (loading its 
 
 // A run that begins within an item has a tile of it, then: the joins count on that.
 static_assert(kMinRun > kItemCost, "runs");
+
+constexpr float kBase = 9.f, kSlack = 6.9f;  // p' = 2^(u - r + kBase), u <= r + kSlack: below 65504, the largest f16 number
 
 struct TileInfo {    // per 16 keys of a tile
   float kf[8];       // 2^e_k
@@ -588,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m = -CUDART_INF_F;
 #pragma unroll
         for (int b = 0; b < kPieces; ++b) m = fmaxf(m, fmaf(max16(&s[b >> 1][(b & 1) * 16]), qf * ti.kf[b], ti.lv[b]));
-        const bool grow = m > r + 8.f || (r == -CUDART_INF_F && m > r);
-        if (x >= C::kStep && __any_sync(0xffffffffu, grow)) {
+        const bool grows = __any_sync(0xffffffffu, m > r + kSlack), grow = grows && m > r;  // r = -infinity: any finite m
+        if (x >= C::kStep && grows) {
           // the sums so far are of the tile before: wait for its product, then bring them to the new reference
           ok = warp_wait(&o_full[mt], (steps - 1u) & 1u, abort_flag, c.status);
           if (!ok) break;
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
         }
         if (grow) r = m;
-        const float base = 7.f - (r == -CUDART_INF_F ? 0.f : r);
+        const float base = kBase - (r == -CUDART_INF_F ? 0.f : r);
 #pragma unroll
         for (int b = 0; b < kPieces; ++b) {
           const float kf = qf * ti.kf[b], add = base + ti.lv[b];

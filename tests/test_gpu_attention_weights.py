@@ -96,5 +96,5 @@ def test_pages_of_far_apart_values_beside_a_dominant_key(env):  # noqa: F811
         b.host["v_scale"][b.table[0, 2003 // 64]] += np.uint8(up % 256)
         b.dev(env)
         ref = reference(b, q, range(10))
-        for sequences, max_q in ((10, 1), (300, 1)):
+        for sequences, max_q in ((10, 1), (300, 1), (10, 10), (300, 40)):
             assert off(attention(env, b, q, sequences, max_q), ref, 1) <= 1.0, (up, sequences, max_q)
