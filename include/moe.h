@@ -564,8 +564,8 @@ MOE_API int moe_layer_workspace_offsets(const moe_layer_desc* d, size_t* out, in
  * the call, the new ones being the last.  Lengths, starts and page table are device arrays, so a
  * captured graph follows them.  Different sequences' pages must differ where a call appends.
  *
- * Limits: D == 128; page one of 16, 32, 64, 128; Hq % Hkv == 0, Hq <= 1024; B <= 65536; T * Hq,
- * n_pages * Hkv * page and max_pages * page below 2^31 (the cache itself may pass 2^31 bytes).
+ * Limits: D == 128; page one of 16, 32, 64, 128; Hq % Hkv == 0, Hq <= 1024; B <= 65536; T * Hq and
+ * n_pages * Hkv * page below 2^31 (the cache itself may pass 2^31 bytes), max_pages * page below 2^31 - 1024.
  *
  * On the device: starts or lengths that contradict each other, a page outside the pool or the
  * table, and a position beyond max_pos set the workspace's status to MOE_ERR_DEVICE_CHECK; what
@@ -637,7 +637,8 @@ MOE_API int moe_kv_gather(const moe_kv_desc* d, const int32_t* start, const int3
 /*
  * out[t,h] = sum_j p_j v_j,  p = softmax over the keys j that token t sees of scale * q[t,h] . k_j.
  * The new token at position i sees the keys j < kv_len[b], j <= i if causal, and j > i - window if
- * window > 0 (causal only).  A row that sees nothing is zero.
+ * window > 0 (causal only, any int).  A row that sees nothing is zero, that of a token before position 0 (kv_len[b] below
+ * the sequence's new tokens) among them, which is no error here.
  *
  *  q [T,Hq,D] bf16, token stride q_stride (elements, a multiple of 8); normally q_out of moe_kv_append.
  *  max_q: at least the new tokens of any one sequence (1 when decoding).  With it and the heads the host

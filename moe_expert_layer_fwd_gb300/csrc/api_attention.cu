@@ -14,6 +14,7 @@ namespace {
 
 constexpr size_t kHeader = 256;  // status word + padding, as in every workspace
 constexpr long long kMaxRows = 1LL << 31;
+constexpr long long kMaxLen = kMaxRows - 1024;  // tokens of a sequence: the ends of its tiles and rows are ints, too
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool ok_ptr(const void* p) { return p && aligned16(p); }
@@ -38,7 +39,7 @@ int check_desc(const moe_kv_desc* d) {
   if (d->D != moe::kHeadDim || d->Hq > 1024) return MOE_ERR_UNSUPPORTED;
   if (d->page != 16 && d->page != 32 && d->page != 64 && d->page != 128) return MOE_ERR_UNSUPPORTED;
   if (d->B > 65536) return MOE_ERR_UNSUPPORTED;
-  if ((long long)d->max_pages * d->page >= kMaxRows || (long long)d->n_pages * d->Hkv * d->page >= kMaxRows ||
+  if ((long long)d->max_pages * d->page >= kMaxLen || (long long)d->n_pages * d->Hkv * d->page >= kMaxRows ||
       (long long)d->T * d->Hq >= kMaxRows)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;

@@ -570,8 +570,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       const int* tok = s_tok + qb * NC + col0;
       const int first = g.s.first(), rows = g.s.t1 - g.s.t0;
       const int last = a.causal ? first + rows : g.r.hi;         // one past the last visible key of any row
-      const int all_lo = a.window > 0 ? max(0, first + rows - a.window) : 0;  // keys [all_lo, all_hi) are seen by
-      const int all_hi = a.causal ? first + 1 : g.r.hi;                     // every row
+      const int all_lo = window_lo(first + rows - 1, a.window);  // keys [all_lo, all_hi) are seen by
+      const int all_hi = a.causal ? first + 1 : g.r.hi;          // every row
 #pragma unroll
       for (int x = 0; x < N; ++x) {
         r[x] = -CUDART_INF_F;
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
 #pragma unroll
           for (int x = 0; x < N; ++x) {
             const int pos = first + tok[x];
-            if ((a.causal && j > pos) || (a.window > 0 && j <= pos - a.window)) u[x] = -CUDART_INF_F;
+            if ((a.causal && j > pos) || j < window_lo(pos, a.window)) u[x] = -CUDART_INF_F;
           }
         }
         float* tops = s_max + (n & 1u) * NC * 4 + col0 * 4;

@@ -92,7 +92,7 @@ template <int kRows>
 __device__ __forceinline__ void item_range(const SeqRange& s, const AttentionArgs& a, int G, int qt, int& lo, int& hi) {
   const int i_min = qt * kRows / G, i_max = min(s.t1 - s.t0 - 1, (qt * kRows + kRows - 1) / G);
   hi = a.causal ? max(0, min(s.len, s.first() + i_max + 1)) : s.len;
-  lo = a.window > 0 ? max(0, s.first() + i_min - a.window + 1) : 0;
+  lo = window_lo(s.first() + i_min, a.window);
 }
 __device__ __forceinline__ int item_tiles(int lo, int hi) { return max(1, (hi + kKeys - 1) / kKeys - lo / kKeys); }
 
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // keys [w_lo, w_hi) are seen by every row of this warp
       const int warp_rho = row0 + quarter * 32, tiles = C::tiles(g);
       const int w_hi = a.causal ? min(g.hi, g.first + warp_rho / G + 1) : g.hi;
-      const int w_lo = a.window > 0 ? g.first + (warp_rho + 31) / G - a.window + 1 : 0;
+      const int w_lo = window_lo(g.first + (warp_rho + 31) / G, a.window);
       float r = -CUDART_INF_F, l = 0.f;
 #pragma unroll 1
       for (int x = kSplit ? mt : 0; x < tiles; x += C::kStep, ++steps) {
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j0 = (g.tile0 + i) * kKeys;
         if (j0 < w_lo || j0 + kKeys > w_hi || have != (1u << kPieces) - 1u) {
           // bit x of word w: this row sees key 32 w + x of the tile
-          const int hi_col = (a.causal ? min(g.hi, pos + 1) : g.hi) - j0, lo_col = a.window > 0 ? pos - a.window + 1 - j0 : 0;
+          const int hi_col = (a.causal ? min(g.hi, pos + 1) : g.hi) - j0, lo_col = window_lo(pos, a.window) - j0;
 #pragma unroll
           for (int w = 0; w < kKeys / 32; ++w) {
             const uint32_t pages = have >> (2 * w);

@@ -50,6 +50,11 @@ __device__ __forceinline__ bool warp_wait3(uint64_t* b0, uint32_t p0, uint64_t* 
   return warp_wait(which == 0 ? b0 : which == 1 ? b1 : b2, which == 0 ? p0 : which == 1 ? p1 : p2, abort_flag, status);
 }
 
+// The first key that a query at this position sees.  Positions may be negative (a sequence may bring more new tokens than it
+// has) and a window as large as an int: no step of this leaves an int's range, as pos - window + 1 would there -- and then
+// the first key, with the page of it, could be anything.
+__device__ __forceinline__ int window_lo(int pos, int window) { return window > 0 ? max(0, max(pos, -1) - (window - 1)) : 0; }
+
 // The keys that any new token of a sequence sees: [lo, hi), in tiles [tile0, tile0 + nt).  A sequence with new
 // tokens has at least one tile, so that its rows are written even when they see nothing.
 struct KeyRange {
@@ -58,7 +63,7 @@ struct KeyRange {
 __device__ __forceinline__ KeyRange key_range(const SeqRange& s, const AttentionArgs& a) {
   KeyRange r;
   r.hi = s.len;
-  r.lo = a.window > 0 ? max(0, s.first() - a.window + 1) : 0;
+  r.lo = window_lo(s.first(), a.window);
   r.tile0 = r.lo / kTile;
   r.nt = s.t1 > s.t0 ? max(1, (r.hi + kTile - 1) / kTile - r.tile0) : 0;
   return r;
