@@ -243,16 +243,14 @@ __device__ __forceinline__ void append_unit(const KvBatch& c, const KvAppendArgs
   SeqRange s;
   if (!load_seq(c, b, s) || s.t1 == s.t0) return;
   const int first = s.first(), j = (first >> c.page_log2) + slot - ((s.t0 >> c.page_log2) + 2 * b);
-  if (first < 0 || s.len > a.max_pos) {
-    if (threadIdx.x == 0) set_status(c.status, first < 0 ? DEV_ERR_CONFIG : DEV_ERR_BOUNDS);
-    return;
-  }
-  if (j > ((s.len - 1) >> c.page_log2)) return;
+  const int end = min(s.len, a.max_pos);  // tokens at positions that the table does not have are left out, as their queries are
+  if ((first < 0 || s.len > end) && threadIdx.x == 0) set_status(c.status, first < 0 ? DEV_ERR_CONFIG : DEV_ERR_BOUNDS);
+  if (first < 0 || first >= end || j > ((end - 1) >> c.page_log2)) return;
   const int pg = load_page(c, b, j);
   if (pg < 0) return;
   const size_t unit = (size_t)pg * c.Hkv + h;
   const int p0 = j << c.page_log2;                                 // position of the page's first token
-  const int r0 = max(0, first - p0), r1 = min(c.page, s.len - p0);  // its new rows
+  const int r0 = max(0, first - p0), r1 = min(c.page, end - p0);    // its new rows
   int old_k = kMinScaleExp, old_v = kMinScaleExp;
   if (r0 > 0) {
     old_k = min((int)c.k_scale[unit] - 127, 126);

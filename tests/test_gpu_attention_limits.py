@@ -8,6 +8,60 @@ pytestmark = pytest.mark.gpu
 from test_gpu_attention import D, Batch, bf16, env, f64  # noqa: E402,F401
 from oracle import attention as oa  # noqa: E402
 
+SENTINEL = 77.0
+
+
+def append(env, b, q, k, v, table, status):  # noqa: F811
+    """moe_kv_append into b.cache; q_out was full of sentinels."""
+    moe, torch = env
+    out = torch.full(q.shape, SENTINEL, dtype=torch.bfloat16, device="cuda")
+    b.ws.zero_()
+    moe.moe_kv_append(q.cuda(), k.cuda(), v.cuda(), b.cache, b.d_start, b.d_len, b.d_table, table, q_out=out, ws=b.ws)
+    assert moe.moe_get_device_status(b.ws) == status
+    return out
+
+
+def codes_are(b, host):
+    """Keys and values of the device's cache are the given ones, byte for byte (NaN codes aside)."""
+    for name, got in zip(("k_codes", "v_codes", "k_scale", "v_scale"), b.cache):
+        got, want = got.cpu().numpy(), host[name]
+        if "codes" in name:
+            assert np.array_equal(oa.values(got, 0), oa.values(want, 0), equal_nan=True), name
+        else:
+            assert (got == want).all(), name
+
+
+def turned(env, x, pos, rot, max_pos):  # noqa: F811
+    """(table, x rotated in 64 bits): angles of 0 and quarter turns only, so that rounding has no part in the codes."""
+    moe, torch = env
+    p = np.arange(max_pos)[:, None] + np.zeros(rot // 2, int)[None]
+    cos, sin = np.array([1, 0, -1, 0])[p % 4], np.array([0, 1, 0, -1])[p % 4]
+    cs = np.concatenate([cos, sin], 1).astype(np.float32)
+    inside = pos < max_pos
+    y = np.full(x.shape, np.nan)
+    y[inside] = oa.norm_rotate(x[inside], pos[inside], cs, rot, False)
+    return torch.from_numpy(cs).cuda(), y
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("max_pos", [37, 32, 28, 20])
+def test_tokens_beyond_the_table_of_angles(env, page, max_pos):  # noqa: F811
+    """A chunk that passes the table's end inside a page, at a page's end, before its first token: the tokens before that end
+    are stored as if they were the chunk, their queries rotated, the others left out; the other sequence has all of its own."""
+    moe, torch = env
+    rng = np.random.default_rng(page + max_pos)
+    b = Batch(rng, [30, 9], [20, 0], 2, page).fill(rng, upto=[20, 0]).dev(env)
+    x = bf16(rng, 39, 8, D, mul=3.0)
+    pos = np.concatenate([np.arange(20, 50), np.arange(9)])
+    table, y = turned(env, f64(x), pos, 128, max_pos)
+    out = append(env, b, x[:, :4], x[:, 4:6], x[:, 6:], table, moe.MOE_ERR_DEVICE_CHECK)
+    inside = pos < max_pos
+    assert np.array_equal(f64(out)[inside], y[inside, :4]) and (f64(out)[~inside] == SENTINEL).all()
+    kept = [int(inside[:30].sum()), int(inside[30:].sum())]
+    rows = np.r_[0:kept[0], 30:30 + kept[1]]
+    oa.append(y[rows, 4:6], f64(x)[rows, 6:], b.host, [0, kept[0], sum(kept)], [20 + kept[0], kept[1]], b.table)
+    codes_are(b, b.host)
+
 
 def rows_ok(got, ref, spread, rows):
     return (np.abs(f64(got) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7 * spread)[rows].all()
