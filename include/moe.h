@@ -567,7 +567,7 @@ MOE_API int moe_layer_workspace_offsets(const moe_layer_desc* d, size_t* out, in
  * Limits: D == 128; page one of 16, 32, 64, 128; Hq % Hkv == 0, Hq <= 1024; B <= 65536; T * Hq and
  * n_pages * Hkv * page below 2^31 (the cache itself may pass 2^31 bytes), max_pages * page below 2^31 - 1024.
  *
- * On the device: starts or lengths that contradict each other, a page outside the pool or the
+ * On the device: starts or lengths that contradict each other (q_start[0] != 0 and q_start[B] != T, too), a page outside the pool or the
  * table, and a position beyond max_pos set the workspace's status to MOE_ERR_DEVICE_CHECK; what
  * they concern is left out (append: tokens not stored, their rows of q_out not written; gather: rows
  * of zeros; attention: rows of a sequence with contradicting lengths not written, keys on a page

@@ -245,7 +245,7 @@ __device__ __forceinline__ void append_unit(const KvBatch& c, const KvAppendArgs
   const int first = s.first(), j = (first >> c.page_log2) + slot - ((s.t0 >> c.page_log2) + 2 * b);
   const int end = min(s.len, a.max_pos);  // tokens at positions that the table does not have are left out, as their queries are
   if ((first < 0 || s.len > end) && threadIdx.x == 0) set_status(c.status, first < 0 ? DEV_ERR_CONFIG : DEV_ERR_BOUNDS);
-  if (first < 0 || first >= end || j > ((end - 1) >> c.page_log2)) return;
+  if (first < 0 || first >= end || j < (first >> c.page_log2) || j > ((end - 1) >> c.page_log2)) return;
   const int pg = load_page(c, b, j);
   if (pg < 0) return;
   const size_t unit = (size_t)pg * c.Hkv + h;
@@ -369,6 +369,7 @@ __device__ __forceinline__ void append_unit(const KvBatch& c, const KvAppendArgs
 __global__ void __launch_bounds__(kAppendThreads, 5) kv_append_kernel(const KvBatch c, const KvAppendArgs a, int q_blocks) {
   extern __shared__ uint4 shared[];  // queries on their way, or the page's new keys, rotated: [row][2][16 lanes] of float4
   __shared__ float s_amax[2][kWarps];
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) check_starts(c);
   if ((int)blockIdx.x < q_blocks) rope_queries(c, a, (int)blockIdx.x, q_blocks, shared);
   else append_unit(c, a, (int)blockIdx.x - q_blocks, s_amax, reinterpret_cast<float4*>(shared));
 }

@@ -41,6 +41,11 @@ __device__ __forceinline__ bool load_seq(const KvBatch& c, int b, SeqRange& s) {
   return ok;
 }
 
+// Every token has a sequence: one thread of a launch looks.
+__device__ __forceinline__ void check_starts(const KvBatch& c) {
+  if (__ldg(c.q_start) != 0 || __ldg(c.q_start + c.B) != c.T) set_status(c.status, DEV_ERR_CONFIG);
+}
+
 // Page of a sequence's tokens [j * page, (j+1) * page), or -1 (and DEV_ERR_BOUNDS) when it is not in the pool.
 __device__ __forceinline__ int load_page(const KvBatch& c, int b, int j) {
   if (j < 0 || j >= c.max_pages) {

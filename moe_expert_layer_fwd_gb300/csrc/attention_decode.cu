@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = c.Hq / c.Hkv;
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && tid == C::kThreads - 1) check_starts(c);
 
   // ---- this block's run of tiles
   long long run = 0;

@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = c.Hq / c.Hkv;
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && tid == kThreads - 1) check_starts(c);
 
   // ---- this block's run: each thread sums a run of places
   long long run;

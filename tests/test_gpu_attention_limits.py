@@ -84,3 +84,30 @@ def test_attention_of_more_new_tokens_than_tokens(env, new, window):  # noqa: F8
     ref, spread = oa.attention(f64(q), b.host, b.q_start, b.kv_len, b.table, D ** -0.5, True, window)
     assert rows_ok(out, ref, spread, slice(None))
     assert (out[:new[0] - new[0] // 2] == 0).all() and (out[new[0]:new[0] + new[1]] == 0).all()
+
+
+@pytest.mark.parametrize("new", [[2, 1, 1], [70, 20, 60], [200, 5, 3]])
+@pytest.mark.parametrize("end", ["first", "last"])
+def test_starts_that_leave_tokens_out(env, new, end):  # noqa: F811
+    """Tokens before the first start or behind the last one belong to no sequence: the status says so, for the attention as
+    for an append with queries or without."""
+    moe, torch = env
+    rng = np.random.default_rng(6)
+    T = sum(new)
+    b = Batch(rng, new, [30, 10, 200], 2, 32).fill(rng).dev(env)
+    q = bf16(rng, T, 4, D)
+    b.d_start[0 if end == "first" else 3] += 1 if end == "first" else -1
+    b.d_len[0 if end == "first" else 2] -= 1
+    ws = moe.moe_paged_attention_workspace(T, 3, 4, 2, D, max(new))
+    out = torch.full(q.shape, SENTINEL, dtype=torch.bfloat16, device="cuda")
+    moe.moe_paged_attention(q.cuda(), b.cache, b.d_start, b.d_len, b.d_table, max_q=max(new), out=out, ws=ws)
+    assert moe.moe_get_device_status(ws) == moe.MOE_ERR_DEVICE_CHECK
+    start, lens = b.d_start.cpu().numpy(), b.d_len.cpu().numpy()
+    ref, spread = oa.attention(f64(q), b.host, start, lens, b.table, D ** -0.5)
+    assert rows_ok(out, ref, spread, slice(start[0], start[3]))
+    assert (out[:start[0]] == SENTINEL).all() and (out[start[3]:] == SENTINEL).all()
+    k = bf16(rng, T, 2, D).cuda()
+    for queries in (q.cuda(), None):
+        b.ws.zero_()
+        moe.moe_kv_append(queries, k, k, b.cache, b.d_start, b.d_len, b.d_table, None, ws=b.ws)
+        assert moe.moe_get_device_status(b.ws) == moe.MOE_ERR_DEVICE_CHECK
