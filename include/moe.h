@@ -567,11 +567,16 @@ MOE_API int moe_layer_workspace_offsets(const moe_layer_desc* d, size_t* out, in
  * Limits: D == 128; page one of 16, 32, 64, 128; Hq % Hkv == 0, Hq <= 1024; B <= 65536; T * Hq and
  * n_pages * Hkv * page below 2^31 (the cache itself may pass 2^31 bytes), max_pages * page below 2^31 - 1024.
  *
- * On the device: starts or lengths that contradict each other (q_start[0] != 0 and q_start[B] != T, too), a page outside the pool or the
- * table, and a position beyond max_pos set the workspace's status to MOE_ERR_DEVICE_CHECK; what
- * they concern is left out (append: tokens not stored, their rows of q_out not written; gather: rows
- * of zeros; attention: rows of a sequence with contradicting lengths not written, keys on a page
- * that is not in the pool not seen, and a row that sees no key is zero).
+ * On the device, each of these sets the workspace's status to MOE_ERR_DEVICE_CHECK, and what it concerns
+ * is left out:
+ *  - a sequence with a start outside 0 .. T, an end before its start, or a length below 0 or beyond the table
+ *    (append: tokens not stored, their rows of q_out not written; attention: rows not written);
+ *  - q_start[0] != 0 or q_start[B] != T (tokens of no sequence: the same);
+ *  - append of a sequence whose length is below its new tokens (none stored; rows of q_out not written for those before
+ *    position 0) -- attention takes such a length, see there;
+ *  - a position from max_pos on (append: token not stored, row of q_out not written);
+ *  - a page outside the pool (append: its tokens not stored, while rows of q_out are; gather: rows of zeros;
+ *    attention: its keys not seen).
  */
 typedef struct moe_kv_desc {
   int32_t B;          /* sequences */

@@ -63,6 +63,41 @@ def test_tokens_beyond_the_table_of_angles(env, page, max_pos):  # noqa: F811
     codes_are(b, b.host)
 
 
+@pytest.mark.parametrize("bad", [1 << 20, -7])
+def test_append_on_a_page_that_is_not_there(env, bad):  # noqa: F811
+    """The tokens of that page are not stored; those of the pages around it are, and all queries are rotated."""
+    moe, torch = env
+    rng = np.random.default_rng(3)
+    b = Batch(rng, [40, 5], [10, 0], 2, 16).fill(rng, upto=[10, 0]).dev(env)
+    x = bf16(rng, 45, 8, D)
+    pos = np.concatenate([np.arange(10, 50), np.arange(5)])
+    table, y = turned(env, f64(x), pos, 128, 64)
+    b.d_table[0, 1] = bad
+    out = append(env, b, x[:, :4], x[:, 4:6], x[:, 6:], table, moe.MOE_ERR_DEVICE_CHECK)
+    assert np.array_equal(f64(out), y[:, :4])
+    lost = b.table[0, 1]
+    before = {n: a[lost].copy() for n, a in b.host.items()}
+    oa.append(y[:, 4:6], f64(x)[:, 6:], b.host, b.q_start, b.kv_len, b.table)
+    for n, a in before.items():
+        b.host[n][lost] = a
+    codes_are(b, b.host)
+
+
+def test_append_of_more_new_tokens_than_tokens(env):  # noqa: F811
+    """A length below the sequence's new tokens: none of them is stored, queries before position 0 are left out."""
+    moe, torch = env
+    rng = np.random.default_rng(4)
+    b = Batch(rng, [6, 5], [20, 3], 2, 16).fill(rng, upto=[20, 3]).dev(env)
+    x = bf16(rng, 11, 8, D)
+    b.d_len[0] = 4
+    pos = np.concatenate([np.arange(-2, 4), np.arange(3, 8)])
+    table, y = turned(env, f64(x), pos.clip(0), 128, 64)
+    out = append(env, b, x[:, :4], x[:, 4:6], x[:, 6:], table, moe.MOE_ERR_DEVICE_CHECK)
+    assert (f64(out)[:2] == SENTINEL).all() and np.array_equal(f64(out)[2:], y[2:, :4])
+    oa.append(y[6:, 4:6], f64(x)[6:, 6:], b.host, [0, 0, 5], [20, 8], b.table)
+    codes_are(b, b.host)
+
+
 def rows_ok(got, ref, spread, rows):
     return (np.abs(f64(got) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7 * spread)[rows].all()
 
