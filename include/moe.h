@@ -575,8 +575,9 @@ MOE_API int moe_layer_workspace_offsets(const moe_layer_desc* d, size_t* out, in
  *  - append of a sequence whose length is below its new tokens (none stored; rows of q_out not written for those before
  *    position 0) -- attention takes such a length, see there;
  *  - a position from max_pos on (append: token not stored, row of q_out not written);
- *  - a page outside the pool (append: its tokens not stored, while rows of q_out are; gather: rows of zeros;
- *    attention: its keys not seen).
+ *  - a page outside the pool (append: its tokens not stored, while rows of q_out are written; gather: rows of zeros;
+ *    attention: its keys not seen);
+ *  - gather of a row that no sequence has, or of a token outside the table (a row of zeros).
  */
 typedef struct moe_kv_desc {
   int32_t B;          /* sequences */

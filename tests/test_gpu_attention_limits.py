@@ -146,3 +146,33 @@ def test_starts_that_leave_tokens_out(env, new, end):  # noqa: F811
         b.ws.zero_()
         moe.moe_kv_append(queries, k, k, b.cache, b.d_start, b.d_len, b.d_table, None, ws=b.ws)
         assert moe.moe_get_device_status(b.ws) == moe.MOE_ERR_DEVICE_CHECK
+
+
+def test_gather_around_a_page_that_is_not_there(env):  # noqa: F811
+    """The rows of that page are zeros, keys and values alike, and all others are the cached tokens."""
+    moe, torch = env
+    rng = np.random.default_rng(8)
+    b = Batch(rng, [0] * 3, [40, 150, 64], 3, 32).fill(rng, 3.0, 0.01).dev(env)
+    start, count = [3, 13, 0], [37, 137, 64]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    b.d_table[1, 2] = 1 << 20
+    b.table[1, 2] = 1 << 20
+    k, v = moe.moe_kv_gather(b.cache, i32(start), i32(np.cumsum([0] + count)), b.d_table, sum(count), ws=b.ws)
+    assert moe.moe_get_device_status(b.ws) == moe.MOE_ERR_DEVICE_CHECK
+    for name, got in (("k", k), ("v", v)):
+        ref = np.concatenate([oa.read(b.host, name, s, x, x + n, b.table) for s, (x, n) in enumerate(zip(start, count))])
+        lost = slice(37 + 64 - 13, 37 + 96 - 13)
+        assert np.isnan(ref[lost]).all()
+        ref[lost] = 0.0
+        assert np.array_equal(f64(got), ref)
+
+
+def test_gather_of_rows_that_no_sequence_has(env):  # noqa: F811
+    """Rows behind the last end are zeros, and reported."""
+    moe, torch = env
+    rng = np.random.default_rng(9)
+    b = Batch(rng, [0], [12], 2, 16).fill(rng).dev(env)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    k, v = moe.moe_kv_gather(b.cache, i32([0]), i32([0, 5]), b.d_table, 9, ws=b.ws)
+    assert moe.moe_get_device_status(b.ws) == moe.MOE_ERR_DEVICE_CHECK
+    assert np.array_equal(f64(k)[:5], oa.read(b.host, "k", 0, 0, 5, b.table)) and (k[5:] == 0).all() and (v[5:] == 0).all()
