@@ -647,8 +647,8 @@ MOE_API int moe_kv_gather(const moe_kv_desc* d, const int32_t* start, const int3
  * the sequence's new tokens) among them, which is no error here.
  *
  *  q [T,Hq,D] bf16, token stride q_stride (elements, a multiple of 8); normally q_out of moe_kv_append.
- *  max_q: at least the new tokens of any one sequence (1 when decoding).  With it and the heads the host
- *      chooses a kernel; rows of sequences that bring more may be left unwritten, and then the status is set.
+ *  max_q: at least the new tokens of any one sequence (1 when decoding), and at most T.  With it and the heads the
+ *      host chooses a kernel; rows of sequences that bring more may be left unwritten, and then the status is set.
  *  scale > 0, finite.
  *  out [T,Hq,D] bf16, dense.
  *  ws: at least moe_paged_attention_workspace_size(d, max_q) bytes (0: invalid d), which suits every

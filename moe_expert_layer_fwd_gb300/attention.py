@@ -209,12 +209,13 @@ def moe_paged_attention_workspace(T: int, B: int, Hq: int, Hkv: int, D: int, max
 def moe_paged_attention(q, cache: KVCache, q_start, kv_len, page_table, max_q: int, scale: Optional[float] = None,
                         causal: bool = True, window: int = 0, out=None, ws=None, stream=None):
     """Softmax attention of the new queries q [T, Hq, D] over their sequences' cached tokens; returns [T, Hq, D] bf16.
-    scale defaults to D ** -0.5; max_q: at least the new tokens of any one sequence."""
+    scale defaults to D ** -0.5; max_q: at least the new tokens of any one sequence (more than T counts as T)."""
     b = _b()
     kv = cache._struct()
     n_pages, Hkv, page, D = cache[0].shape
     table, B, max_pages = _table(page_table)
     T, Hq = q.shape[0], q.shape[1]
+    max_q = min(max_q, T)
     qp, qs = _rows(q, "q", Hq, D)
     d = _m.moe_kv_desc(B, T, Hq, Hkv, D, page, n_pages, max_pages)
     starts, lens = _need(q_start, "q_start", b.i32, (B + 1,)), _need(kv_len, "kv_len", b.i32, (B,))
@@ -241,6 +242,8 @@ class AttentionLayer:
     def __init__(self, n_pages: int, Hq: int, Hkv: int, D: int = 128, page: int = 64, max_pos: int = 32768,
                  rot_dim: Optional[int] = None, rope_base: float = 1e6, interleaved: bool = False, q_norm_weight=None,
                  k_norm_weight=None, eps: float = 1e-6, scale: Optional[float] = None, window: int = 0, device="cuda"):
+        if window < 0 or (scale is not None and not 0.0 < scale < float("inf")):
+            raise ValueError(f"expected window >= 0 and a positive finite scale, got {window} and {scale}")
         self.Hq, self.Hkv, self.D = Hq, Hkv, D
         self.cache = KVCache.empty(n_pages, Hkv, page, D, device)
         rot_dim = D if rot_dim is None else rot_dim
@@ -250,9 +253,18 @@ class AttentionLayer:
         self.ws, self._outgrown = _status_ws(self.cache.k_codes, None), []
 
     def forward(self, qkv, q_start, kv_len, page_table, max_q: int, out=None, stream=None):
-        T = qkv.shape[0]
+        T, B = qkv.shape[0], page_table.shape[0]
         q, k, v = qkv.view(T, self.Hq + 2 * self.Hkv, self.D).split([self.Hq, self.Hkv, self.Hkv], dim=1)
-        d = _m.moe_kv_desc(page_table.shape[0], T, self.Hq, self.Hkv, self.D, 16, 0, 0)
+        # What the attention refuses is refused before the tokens are in the cache.
+        max_q = min(max_q, T)
+        if max_q * B < T or (max_q < 1 and T > 0):
+            raise _m.MoEError(_m.MOE_ERR_INVALID_ARG, "AttentionLayer.forward: max_q")
+        if out is not None:
+            if out.numel() != T * self.Hq * self.D or not out.is_contiguous():
+                raise ValueError(f"out: expected a contiguous tensor [{T}, {self.Hq * self.D}], got {tuple(out.shape)}")
+            out = out.view(T, self.Hq, self.D)
+            _need(out, "out", _b().bf16, out.shape)
+        d = _m.moe_kv_desc(B, T, self.Hq, self.Hkv, self.D, 16, 0, 0)
         if self.ws.numel() < _b().workspace_size(_byref(d), max_q):
             # The smaller one is kept: a captured graph, or a call still running on another stream, goes on using it (there
             # are few sizes).
@@ -263,5 +275,5 @@ class AttentionLayer:
         rq = moe_kv_append(q, k, v, self.cache, q_start, kv_len, page_table, self.cos_sin, None, self.interleaved,
                            self.q_norm_weight, self.k_norm_weight, self.eps, ws=self.ws, stream=stream)
         o = moe_paged_attention(rq, self.cache, q_start, kv_len, page_table, max_q, self.scale, True, self.window,
-                                out.view(T, self.Hq, self.D) if out is not None else None, self.ws, stream)
+                                out, self.ws, stream)
         return o.view(T, self.Hq * self.D)

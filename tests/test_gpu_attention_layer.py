@@ -1,0 +1,56 @@
+"""AttentionLayer against the float64 oracle, its arguments, its workspaces and their status words (GPU)."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+from test_gpu_attention import D, bf16, env, f64  # noqa: E402,F401
+from oracle import attention as oa  # noqa: E402
+
+HQ, HKV, PAGE = 8, 2, 16
+
+
+def i32(x):
+    import torch
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def test_more_than_all_tokens_as_the_most(env):  # noqa: F811
+    """max_q is an upper bound: a program that knows only that no sequence brings more than 40 tokens gives 40, also with 3."""
+    moe, torch = env
+    rng = np.random.default_rng(1)
+    layers = [moe.AttentionLayer(16, HQ, HKV, page=PAGE, max_pos=128) for _ in range(2)]
+    table = torch.from_numpy(rng.permutation(16).reshape(2, 8).astype(np.int32)).cuda()
+    lens = [0, 0]
+    for new in ([20, 9], [2, 1], [0, 1]):
+        lens = [a + n for a, n in zip(lens, new)]
+        x = bf16(rng, sum(new), (HQ + 2 * HKV) * D).cuda()
+        args = x, i32([0, new[0], sum(new)]), i32(lens), table
+        assert torch.equal(layers[0].forward(*args, sum(new)), layers[1].forward(*args, 400 if lens[0] > 20 else 40))
+    q = bf16(rng, 1, HQ, D).cuda()
+    call = lambda m: moe.moe_paged_attention(q, layers[0].cache, i32([0, 0, 1]), i32(lens), table, max_q=m)
+    assert torch.equal(call(1), call(7))
+
+
+@pytest.mark.parametrize("kw", [dict(max_q=0), dict(max_q=-1), dict(max_q=2), dict(out=(5, 3)), dict(out=(5, HQ * D), dtype="float32")])
+def test_refused_calls_leave_the_cache_alone(env, kw):  # noqa: F811
+    """What the attention refuses, the layer refuses before it appends.  (5 tokens of 2 sequences: one of them brings 3.)"""
+    moe, torch = env
+    rng = np.random.default_rng(2)
+    layer = moe.AttentionLayer(16, HQ, HKV, page=PAGE, max_pos=128)
+    for t in layer.cache:
+        t.fill_(3)
+    before = [t.clone() for t in layer.cache]
+    table = torch.from_numpy(rng.permutation(16).reshape(2, 8).astype(np.int32)).cuda()
+    out = torch.empty(kw["out"], dtype=getattr(torch, kw.get("dtype", "bfloat16")), device="cuda") if "out" in kw else None
+    with pytest.raises((ValueError, moe.MoEError)):
+        layer.forward(bf16(rng, 5, (HQ + 2 * HKV) * D).cuda(), i32([0, 2, 5]), i32([2, 3]), table, kw.get("max_q", 3), out=out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, layer.cache))
+
+
+def test_layer_arguments_are_checked(env):  # noqa: F811
+    moe, torch = env
+    for kw in (dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(window=-1)):
+        with pytest.raises(ValueError):
+            moe.AttentionLayer(4, HQ, HKV, **kw)
