@@ -68,7 +68,7 @@ def run(prompt=512, steps=32, batch=4, page=64, k=4, say=print):
     torch.cuda.synchronize()
     ms = (time.perf_counter() - t) / max(1, steps) * 1e3
     whole = send(total, total).view(batch, total, layer.H)[:, -1]
-    assert moe.moe_get_device_status(layer.attention.ws) == moe.MOE_OK
+    assert layer.attention.status() == moe.MOE_OK
     off = float((last.float() - whole.float()).abs().max() / whole.float().abs().max())
     say(f"{batch} sequences of {prompt} + {steps} tokens: {ms:.3f} ms a decode step, last states differ by {off:.2e}")
     return off

@@ -237,7 +237,8 @@ class AttentionLayer:
 
     ``forward`` takes the rows of the merged projection [T, (Hq + 2 Hkv) * D] (query heads, key heads, value heads)
     and returns the attention output [T, Hq * D], the input of the output projection.  Pages are the caller's to hand
-    out: page_table names them, and a page freed by one sequence may be given to another at any time."""
+    out: page_table names them, and a page freed by one sequence may be given to another at any time.  Calls of one layer share its
+    workspace and run one after another; ``status`` says what they found."""
 
     def __init__(self, n_pages: int, Hq: int, Hkv: int, D: int = 128, page: int = 64, max_pos: int = 32768,
                  rot_dim: Optional[int] = None, rope_base: float = 1e6, interleaved: bool = False, q_norm_weight=None,
@@ -265,15 +266,40 @@ class AttentionLayer:
             out = out.view(T, self.Hq, self.D)
             _need(out, "out", _b().bf16, out.shape)
         d = _m.moe_kv_desc(B, T, self.Hq, self.Hkv, self.D, 16, 0, 0)
-        if self.ws.numel() < _b().workspace_size(_byref(d), max_q):
-            # The smaller one is kept: a captured graph, or a call still running on another stream, goes on using it (there
-            # are few sizes).
-            self._outgrown.append(self.ws)
-            self.ws = _workspace(d, max_q, self.ws, stream)
-            with _b().torch.cuda.stream(stream):  # what an earlier call reported stays readable
-                self.ws[:_b().status_bytes].copy_(self._outgrown[-1][:_b().status_bytes])
+        ws = self._workspace_for(d, max_q, stream)
         rq = moe_kv_append(q, k, v, self.cache, q_start, kv_len, page_table, self.cos_sin, None, self.interleaved,
-                           self.q_norm_weight, self.k_norm_weight, self.eps, ws=self.ws, stream=stream)
+                           self.q_norm_weight, self.k_norm_weight, self.eps, ws=ws, stream=stream)
         o = moe_paged_attention(rq, self.cache, q_start, kv_len, page_table, max_q, self.scale, True, self.window,
-                                out, self.ws, stream)
+                                out, ws, stream)
+        if ws is not self.ws:
+            with _b().torch.cuda.stream(stream):
+                self.ws[:_b().status_bytes].bitwise_or_(ws[:_b().status_bytes])
         return o.view(T, self.Hq * self.D)
+
+    def _workspace_for(self, d, max_q: int, stream):
+        """The layer's workspace, a larger one from now on if this call needs it.
+
+        The smaller one is kept: a captured graph, or a call still running on another stream, goes on using it (there are few
+        sizes).  A call that is being captured does not make the layer's workspace grow -- clearing the new one's status word would
+        become a part of the graph, done again by every replay -- but has one of its own, whose status is added to the layer's."""
+        b = _b()
+        if self.ws.numel() >= b.workspace_size(_byref(d), max_q):
+            return self.ws
+        with b.torch.cuda.stream(stream):
+            ws = _workspace(d, max_q, self.ws, stream)
+            if not b.torch.cuda.is_current_stream_capturing():
+                self._outgrown.append(self.ws)
+                ws[:b.status_bytes].copy_(self.ws[:b.status_bytes])  # what an earlier call reported stays readable
+                self.ws = ws
+        return ws
+
+    def status(self, stream=None) -> int:
+        """What the calls so far reported, MOE_OK or the first error found (synchronises): that of the present workspace or, from graphs
+        captured before it grew, of the ones before it."""
+        found = (_m.moe_get_device_status(ws, stream) for ws in (self.ws, *self._outgrown))
+        return next((s for s in found if s != _m.MOE_OK), _m.MOE_OK)
+
+    def clear_status(self, stream=None) -> None:
+        """Forgets what was reported."""
+        for ws in (self.ws, *self._outgrown):
+            _m.moe_workspace_init(ws, stream)

@@ -54,3 +54,56 @@ def test_layer_arguments_are_checked(env):  # noqa: F811
     for kw in (dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(window=-1)):
         with pytest.raises(ValueError):
             moe.AttentionLayer(4, HQ, HKV, **kw)
+
+
+def capture(torch, f):
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = f()
+    return g, out
+
+
+def test_status_of_a_graph_whose_workspace_was_outgrown(env):  # noqa: F811
+    """A decode graph goes on using the workspace that it was captured with: what it reports there reaches layer.status()."""
+    moe, torch = env
+    rng = np.random.default_rng(3)
+    layer = moe.AttentionLayer(40, HQ, HKV, page=PAGE, max_pos=1024)
+    table = torch.from_numpy(rng.permutation(40).reshape(1, 40).astype(np.int32)).cuda()
+    start, lens, x = i32([0, 1]), i32([1]), bf16(rng, 1, (HQ + 2 * HKV) * D).cuda()
+    layer.forward(x, start, lens, table, 1)
+    g, _ = capture(torch, lambda: layer.forward(x, start, lens, table, 1))
+    layer.forward(bf16(rng, 300, (HQ + 2 * HKV) * D).cuda(), i32([0, 300]), i32([300]), table, 300)
+    lens.fill_(301)
+    g.replay()
+    assert layer.status() == moe.MOE_OK
+    table[0, 4] = 1 << 20
+    g.replay()
+    assert layer.status() == moe.MOE_ERR_DEVICE_CHECK
+    layer.clear_status()
+    assert layer.status() == moe.MOE_OK
+
+
+def test_first_call_inside_a_capture(env):  # noqa: F811
+    """A graph captured before any other call: right, and what its replays report stays, as the eager calls' around them does."""
+    moe, torch = env
+    rng = np.random.default_rng(4)
+    layers = [moe.AttentionLayer(40, HQ, HKV, page=PAGE, max_pos=1024) for _ in range(2)]
+    table = torch.from_numpy(rng.permutation(40).reshape(1, 40).astype(np.int32)).cuda()
+    start, lens, x = i32([0, 1]), i32([1]), bf16(rng, 1, (HQ + 2 * HKV) * D).cuda()
+    junk = [torch.full((8 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    del junk
+    g, out = capture(torch, lambda: layers[0].forward(x, start, lens, table, 1))
+    assert layers[0].status() == moe.MOE_OK
+    g.replay()
+    assert torch.equal(out, layers[1].forward(x, start, lens, table, 1)) and layers[0].status() == moe.MOE_OK
+    prompt = bf16(rng, 300, (HQ + 2 * HKV) * D).cuda(), i32([0, 300]), i32([301]), table, 300
+    assert torch.equal(layers[0].forward(*prompt), layers[1].forward(*prompt)) and layers[0].status() == moe.MOE_OK
+    lens.fill_(302)
+    good = int(table[0, 4])
+    table[0, 4] = 1 << 20
+    g.replay()
+    table[0, 4] = good
+    g.replay()
+    assert layers[0].status() == moe.MOE_ERR_DEVICE_CHECK
+    layers[1].forward(x, start, lens, table, 1)
+    assert torch.equal(out, layers[1].forward(x, start, lens, table, 1))
