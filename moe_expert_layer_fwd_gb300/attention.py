@@ -67,7 +67,7 @@ def _rows(t, what: str, heads: int, D: int):
     row, head, one = t.stride()
     if one != 1 or (head != D and heads > 1):
         raise ValueError(f"{what}: the heads of a token must be dense, got strides {t.stride()}")
-    return t.data_ptr(), row if t.shape[0] > 1 else max(row, heads * D)
+    return t.data_ptr(), row if t.shape[0] > 1 else heads * D  # one token has no stride
 
 
 class KVCache(NamedTuple):

@@ -107,3 +107,17 @@ def test_first_call_inside_a_capture(env):  # noqa: F811
     assert layers[0].status() == moe.MOE_ERR_DEVICE_CHECK
     layers[1].forward(x, start, lens, table, 1)
     assert torch.equal(out, layers[1].forward(x, start, lens, table, 1))
+
+
+def test_strides_of_a_single_token(env):  # noqa: F811
+    """One token's rows have no stride: any will do."""
+    moe, torch = env
+    rng = np.random.default_rng(5)
+    cache = moe.KVCache.empty(4, HKV, PAGE)
+    table = i32([[2, 0]])
+    q, k = bf16(rng, 1, HQ, D).cuda(), bf16(rng, 1, HKV, D).cuda()
+    odd = lambda t: torch.as_strided(t, t.shape, (10001, D, 1))
+    plain = moe.moe_kv_append(q, k, k, cache, i32([0, 1]), i32([1]), table)
+    assert torch.equal(moe.moe_kv_append(odd(q), odd(k), odd(k), cache, i32([0, 1]), i32([1]), table), plain)
+    one = moe.moe_paged_attention(plain, cache, i32([0, 1]), i32([1]), table, max_q=1)
+    assert torch.equal(moe.moe_paged_attention(odd(plain), cache, i32([0, 1]), i32([1]), table, max_q=1), one)
