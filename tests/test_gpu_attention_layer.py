@@ -15,6 +15,54 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
+@pytest.mark.parametrize("kw", [
+    dict(), dict(window=25, interleaved=True, rot_dim=64, scale=0.05, norms=True), dict(window=7, rot_dim=32, rope_base=500.0),
+    dict(rot_dim=0, scale=0.2, norms=True, eps=0.5), dict(interleaved=True, rope_base=1e4, norms=True)])
+def test_layer_against_the_oracle(env, kw):  # noqa: F811
+    """Prompts, single tokens and chunks in turn.  Queries and cached keys are compared with rotations in 64 bits that know nothing of
+    the layer, its outputs with the oracle's attention over the cache that it left.  Tolerances: queries are rounded once to bf16; a
+    cached number is rounded to E4M3 (2^-4 of it, 2^-10 of the page's scale at least) and once more, to smaller numbers' absolute
+    steps, whenever the page's scale grows: 2^-10 (1 + 1/2 + 1/4 ..) of the last scale."""
+    moe, torch = env
+    rng = np.random.default_rng(len(kw))
+    args = dict(kw)
+    norms = [bf16(rng, D).cuda(), bf16(rng, D).cuda()] if args.pop("norms", False) else [None, None]
+    layer = moe.AttentionLayer(16, HQ, HKV, page=PAGE, max_pos=128, q_norm_weight=norms[0], k_norm_weight=norms[1], **args)
+    rot, il, base, eps = args.get("rot_dim", D), args.get("interleaved", False), args.get("rope_base", 1e6), args.get("eps", 1e-6)
+    angles = oa.rope_table(128, rot, base) if rot else np.zeros((128, 0))
+    weights = [None if w is None else f64(w) for w in norms]
+    table = rng.permutation(16).reshape(2, 8).astype(np.int32)
+    d_table = torch.from_numpy(table).cuda()
+    other = moe.KVCache.empty(16, HKV, PAGE)          # the same tokens by moe_kv_append alone, for its queries
+    keys = [np.zeros((0, HKV, D))] * 2
+    lens = [0, 0]
+    for new in ([50, 13], [1, 1], [5, 2], [0, 1], [40, 60]):
+        T = sum(new)
+        first, lens = list(lens), [a + n for a, n in zip(lens, new)]
+        starts = np.cumsum([0] + new).astype(np.int32)
+        pos = np.concatenate([np.arange(a, a + n) for a, n in zip(first, new)])
+        x = bf16(rng, T, HQ + 2 * HKV, D, mul=2.0)
+        out = layer.forward(x.view(T, -1).cuda(), i32(starts), i32(lens), d_table, max(new))
+        assert layer.status() == moe.MOE_OK and out.shape == (T, HQ * D)
+        q, k, v = x.cuda().split([HQ, HKV, HKV], dim=1)
+        cos_sin = torch.from_numpy(angles.astype(np.float32)).cuda() if rot else None
+        rq = moe.moe_kv_append(q, k, v, other, i32(starts), i32(lens), d_table, cos_sin, interleaved=il, q_norm_weight=norms[0],
+                               k_norm_weight=norms[1], eps=eps)
+        turned = [oa.norm_rotate(f64(x)[:, a:b], pos, angles, rot, il, w, eps)
+                  for a, b, w in ((0, HQ, weights[0]), (HQ, HQ + HKV, weights[1]))]
+        size = np.abs(turned[0]).max(-1, keepdims=True)
+        assert (np.abs(f64(rq) - turned[0]) <= 2.0 ** -8 * np.abs(turned[0]) + 2.0 ** -18 * size).all()
+        host = {n: getattr(layer.cache, n).cpu().numpy() for n in ("k_codes", "v_codes", "k_scale", "v_scale")}
+        for b in range(2):
+            keys[b] = np.concatenate([keys[b], turned[1][starts[b]:starts[b + 1]]])
+            got = oa.read(host, "k", b, 0, lens[b], table)
+            unit = 2.0 ** (host["k_scale"][table[b, np.arange(lens[b]) // PAGE]].astype(int) - 127)[..., None]
+            size = np.abs(keys[b]).max(-1, keepdims=True)
+            assert (np.abs(got - keys[b]) <= 2.0 ** -4 * np.abs(keys[b]) + 2.0 ** -9 * unit + 2.0 ** -18 * size).all()
+        ref, spread = oa.attention(f64(rq), host, starts, lens, table, args.get("scale", D ** -0.5), True, args.get("window", 0))
+        assert (np.abs(f64(out).reshape(T, HQ, D) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7 * spread).all()
+
+
 def test_more_than_all_tokens_as_the_most(env):  # noqa: F811
     """max_q is an upper bound: a program that knows only that no sequence brings more than 40 tokens gives 40, also with 3."""
     moe, torch = env
