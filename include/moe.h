@@ -646,6 +646,11 @@ MOE_API int moe_kv_gather(const moe_kv_desc* d, const int32_t* start, const int3
  * window > 0 (causal only, any int).  A row that sees nothing is zero, that of a token before position 0 (kv_len[b] below
  * the sequence's new tokens) among them, which is no error here.
  *
+ * Scores, weights and sums are fp32: scale * q . k has to be finite there, and the scales of one sequence's value
+ * pages to lie within 2^100 of each other, or keys on the pages of the smallest values lose their part of the
+ * denominator (a page of zeros has the smallest, 2^-64, so values up to 2^44 always do).  A weight keeps 8 bits down
+ * to 2^-26 of the row's largest p_j times its page's scale, and is rounded to multiples of 2^-33 of it below.
+ *
  *  q [T,Hq,D] bf16, token stride q_stride (elements, a multiple of 8); normally q_out of moe_kv_append.
  *  max_q: at least the new tokens of any one sequence (1 when decoding), and at most T.  With it and the heads the
  *      host chooses a kernel; rows of sequences that bring more may be left unwritten, and then the status is set.

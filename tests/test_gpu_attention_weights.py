@@ -61,7 +61,7 @@ def off(out, ref, new):
     """The largest error, in units of the tolerance, of the sequences that there is a reference of."""
     out = f64(out).reshape(-1, new, *out.shape[1:])
     assert not np.isnan(out).any()
-    return max(float((np.abs(out[s] - r) / tol).max()) for s, (r, tol) in ref.items() if s < len(out))
+    return max(float((np.abs(out[s] - r) / np.maximum(tol, 1e-300)).max()) for s, (r, tol) in ref.items() if s < len(out))
 
 
 def attention(env, b, q, sequences, max_q):  # noqa: F811
@@ -98,3 +98,21 @@ def test_pages_of_far_apart_values_beside_a_dominant_key(env):  # noqa: F811
         ref = reference(b, q, range(10))
         for sequences, max_q in ((10, 1), (300, 1), (10, 10), (300, 40)):
             assert off(attention(env, b, q, sequences, max_q), ref, 1) <= 1.0, (up, sequences, max_q)
+
+
+@pytest.mark.parametrize("large", ["first", "last"])
+def test_zeros_beside_large_values(env, large):  # noqa: F811
+    """A page of values up to 2^44 among pages of zeros, whose scale is 2^-64, all keys' scores being much the same: the keys of the zeros
+    take their share of the denominator although their terms of the sum are 2^100 times smaller than the others'."""
+    rng = np.random.default_rng(7)
+    for new, Hq, limits in ((1, 4, (1, 20)), (2, 16, (2, 20)), (140, 4, (140,))):
+        b, q = dominated(rng, 1000, "middle", new, Hq, 20)
+        q[..., 0] = 0.0
+        n = -(-1000 // 64)
+        p = b.table[0, 0 if large == "first" else n - 2]
+        rest = [x for x in b.table[0, :n] if x != p]
+        b.host["v_codes"][rest], b.host["v_scale"][rest], b.host["v_scale"][p] = 0, 63, 127 + 36
+        b.dev(env)
+        ref = reference(b, q, range(4))
+        for max_q in limits:
+            assert off(attention(env, b, q, 20, max_q), ref, new) <= 1.0, (new, Hq, max_q)
