@@ -28,7 +28,7 @@
 // is finished there; otherwise the parts (sum, maximum, denominator) go to the workspace and a second kernel joins them in a
 // fixed order.  The host knows none of the lengths.
 //
-// Measured (64 sequences of 1500-8190 tokens, 64 query heads on 8, 685 MB of cache): 123 us; from the first copy to the last
+// Measured (64 sequences of 1500-8190 tokens, 64 query heads on 8, 685 MB of cache): 119 us a call; from the first copy to the last
 // product 94 us = 7.3 TB/s, the memory's rate; the rest is 6 us until the first scores (lengths, page table, first copies, one
 // after another), 10 us in which the slowest blocks finish, and the join.  Small sequences are bound by that chain of waits.
 //

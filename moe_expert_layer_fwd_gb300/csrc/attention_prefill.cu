@@ -21,7 +21,7 @@
 // Items of at most 128 rows (kSplit): both M tiles hold the same rows and take its key tiles in turn, and the second one's
 // sums are added to the first one's at the end (32 rows a head over long caches: 87 us, and 103 as a half-empty item).
 //
-// Measured (8 query heads per key/value head, causal): a prompt of 16,384 tokens 1.70 ms, 1,290 TFLOP/s; a ragged batch of
+// Measured (8 query heads per key/value head, causal): a prompt of 16,384 tokens 1.74 ms a call, 1,270 TFLOP/s; a ragged batch of
 // chunks 0.49 ms, 1,050 TFLOP/s.  What bounds it is the chain of one M tile: scores read, weights made and written
 // (1,900 cycles), then the products of these weights and of the next scores (1,400 with their latency), where the products
 // of both M tiles would take 2,050; and an item's own 11,000 cycles or so between its neighbours' tiles.
