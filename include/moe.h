@@ -665,6 +665,102 @@ MOE_API int moe_paged_attention(const moe_kv_desc* d, const uint16_t* q, long lo
                                 float scale, int causal, int window, uint16_t* out, void* ws, size_t ws_bytes,
                                 void* stream);
 
+/*
+ * Long conversations: prompts of images and text, positions that are not a token's place in the cache, a
+ * long prompt that many sequences share, and a cache that keeps a budget of tokens.
+ *
+ * Rotation at given positions.  moe_rope_rows gives every new token its row of the rotation, once for all
+ * layers of a step: frequency f < rot_dim / 2 turns by the token's position on axis axes[f] (time, height and
+ * width of an image's patches, say; one axis: any positions, such as those of tokens behind an eviction),
+ *   rows[t, f] = cos_sin[p, f],  rows[t, rot_dim/2 + f] = cos_sin[p, rot_dim/2 + f],  p = positions[axes[f], t].
+ *  positions: int32 [n_axes, T], axis a at positions + a * positions_stride (elements, >= T); n_axes <= 8.
+ *  axes: rot_dim / 2 bytes on the host.    cos_sin [max_pos, rot_dim] as for moe_kv_append.
+ *  rows [T, rot_dim] fp32 out.  A position outside 0 .. max_pos - 1 makes its part of the row NaN (and so the
+ *      token's query and key) and sets the status to MOE_ERR_DEVICE_CHECK.
+ * moe_kv_append_at is moe_kv_append with the rotation of token t in rows[t] instead of in the table's row of
+ * its place in the sequence; everything else, the place in the cache among it, is the same.
+ */
+MOE_API int moe_rope_rows(int n_axes, int T, const int32_t* positions, long long positions_stride, const uint8_t* axes,
+                          const float* cos_sin, int max_pos, int rot_dim, float* rows, void* ws, size_t ws_bytes,
+                          void* stream);
+MOE_API int moe_kv_append_at(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const uint16_t* k,
+                             long long k_stride, const uint16_t* v, long long v_stride, const int32_t* q_start,
+                             const int32_t* kv_len, const int32_t* page_table, const float* rows, int rot_dim,
+                             int interleaved, const uint16_t* q_norm_weight, const uint16_t* k_norm_weight, float eps,
+                             uint16_t* q_out, const moe_kv_cache* kv, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of a batch whose sequences share long prefixes.  New token t of a sequence sees all tokens of
+ * its prefix and its sequence's own tokens as in moe_paged_attention; one softmax over both:
+ *   out[t,h] = sum_j p_j v_j,   lse[t,h] = log sum_j exp(scale * q[t,h] . k_j).
+ * A prefix is read once for all its readers.  Its keys were rotated for positions 0 .. len - 1, so those
+ * of a sequence's own tokens go on from there (moe_kv_append_at).
+ *
+ *  prefix: NULL (none: moe_paged_attention with lse), or n prefixes in the same pool.  Tokens q_start[i] ..
+ *      q_start[i+1] - 1 of the T read prefix i (it may have no readers, or no tokens), whichever sequences they
+ *      belong to; q_start[0] = 0, q_start[n] = T.  q_start [n+1], len [n], page_table [n, max_pages]: int32 on
+ *      the device.  max_q: at least the readers' tokens of any one prefix, at most T, as max_q.
+ *  window > 0 only without prefixes.
+ *  lse [T,Hq] fp32 out, natural logarithm, -inf for a row that sees nothing; or NULL.
+ *  ws: at least moe_paged_attention_shared_workspace_size(d, max_q, prefix) bytes, of which n, max_pages and max_q of
+ *      prefix are read (0: invalid).  It grows with T * Hq when there are prefixes.
+ * Prefixes are checked as sequences are; rows whose prefix is left out are undefined (and the status is set).
+ */
+typedef struct moe_kv_prefix {
+  int32_t n;                  /* prefixes */
+  int32_t max_pages;          /* columns of page_table */
+  int32_t max_q;
+  const int32_t* q_start;
+  const int32_t* len;
+  const int32_t* page_table;
+} moe_kv_prefix;
+MOE_API size_t moe_paged_attention_shared_workspace_size(const moe_kv_desc* d, int max_q, const moe_kv_prefix* prefix);
+MOE_API int moe_paged_attention_shared(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const int32_t* q_start,
+                                       const int32_t* kv_len, const int32_t* page_table, const moe_kv_cache* kv,
+                                       int max_q, float scale, int causal, int window, const moe_kv_prefix* prefix,
+                                       uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Adds up the attention weights of cached tokens.  For key/value head h and token j of a sequence with new
+ * tokens, over the new tokens t and the query heads of h that see j (as in moe_paged_attention),
+ *   weight_out[page of j, h, place of j] = before + sum exp(scale * q[t,head] . k_j - lse[t,head]),
+ * before = weight_in there, or 0 for the sequence's new tokens (whatever their page held) and when weight_in is NULL.
+ * Of tokens that no new one sees (behind a window), and of sequences without new tokens, nothing is written.
+ *
+ *  lse [T,Hq] fp32: the denominators' logarithms as moe_paged_attention_shared gives them -- over more keys than
+ *      these, if need be: with a shared prefix the weights of a sequence's own tokens are their shares of it all.
+ *      A row whose lse, or whose query, is not finite adds nothing; a key with a NaN gets 0.
+ *  weight_in, weight_out [n_pages,Hkv,page] fp32, beside the cache; they may be the same.
+ *  max_q: as for moe_paged_attention, but only a hint.
+ *  ws: at least moe_status_bytes().
+ * A page belongs to one sequence of the batch.
+ */
+MOE_API int moe_kv_weights(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const float* lse,
+                           const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                           const moe_kv_cache* kv, int max_q, float scale, int causal, int window,
+                           const float* weight_in, float* weight_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Packs what stays of each sequence into new pages.  Of the kv_len[b] tokens of sequence b the m = min(kv_len[b],
+ * keep[b]) of the largest weight stay, for each key/value head by its own weights and in their order; of
+ * equal weights the first.  The first `sink` and the last `recent` tokens have the largest weight of all;
+ * one that is not above 0 (a NaN among them) counts as 0.
+ *
+ *  T and Hq of d are not used.  keep [B], new_table [B,new_max_pages]: int32 on the device.
+ *  New pages come from the same pool and are none of the pages that this call reads.  They get the kept
+ *      tokens' codes, weights and scales: a page's scale is the largest of those that its tokens had, and codes of
+ *      smaller ones are rounded again to it.  The old pages stay as they are.
+ *  new_len [B] int32 out: m.    kept [B,Hkv,new_max_pages*page] int32 out: the tokens that stayed, then -1.
+ *  ws: at least moe_status_bytes().
+ * keep[b] < 0, or m beyond the new table, sets the status to MOE_ERR_DEVICE_CHECK and leaves the sequence out
+ * (new_len[b] = -1); so do pages outside the pool (a token on such a page counts as weight 0, and as zeros if it stays).
+ * Positions: the next token's place in the cache is new_len[b], its position is not (moe_kv_append_at).
+ */
+MOE_API int moe_kv_evict(const moe_kv_desc* d, float* weight, const int32_t* kv_len, const int32_t* page_table,
+                         const int32_t* keep, int sink, int recent, const int32_t* new_table, int new_max_pages,
+                         const moe_kv_cache* kv, int32_t* new_len, int32_t* kept, void* ws, size_t ws_bytes,
+                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,7 +11,9 @@ Functions carry the C names:
     moe_finalize_routing, moe_layer_forward (+ MoELayer, which owns a workspace); the front end
     moe_add_rms_norm_cast and moe_router_logits; moe_init_routing_range; the attention over a paged
     8-bit key/value cache: moe_kv_append, moe_kv_gather, moe_paged_attention, moe_rope_table (+ KVCache,
-    its buffers, and AttentionLayer, which owns a cache and a workspace).
+    its buffers, and AttentionLayer, which owns a cache and a workspace); for long conversations
+    moe_rope_rows and moe_kv_append_at (positions on several axes), moe_paged_attention_shared (prefixes that
+    sequences share), moe_kv_weights and moe_kv_evict (a budget of tokens by accumulated attention weight).
 """
 from __future__ import annotations
 
@@ -48,6 +50,11 @@ class moe_kv_desc(ctypes.Structure):
 
 class moe_kv_cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scale", "v_scale")]
+
+
+class moe_kv_prefix(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n", "max_pages", "max_q")] + \
+        [(n, ctypes.c_void_p) for n in ("q_start", "len", "page_table")]
 
 
 class moe_layer_desc(ctypes.Structure):
@@ -156,6 +163,24 @@ _SIGS = {
                             [ctypes.c_void_p] * 3 + [ctypes.POINTER(moe_kv_cache), ctypes.c_int, ctypes.c_float,
                                                      ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                                      ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_rope_rows": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_char_p, ctypes.c_void_p,
+                                     ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_kv_append_at": (ctypes.c_int, [ctypes.POINTER(moe_kv_desc)] + [ctypes.c_void_p, ctypes.c_longlong] * 3 +
+                         [ctypes.c_void_p] * 4 + [ctypes.c_int] * 2 + [ctypes.c_void_p] * 2 +
+                         [ctypes.c_float, ctypes.c_void_p, ctypes.POINTER(moe_kv_cache), ctypes.c_void_p,
+                          ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_paged_attention_shared_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(moe_kv_desc), ctypes.c_int,
+                                                                    ctypes.POINTER(moe_kv_prefix)]),
+    "moe_paged_attention_shared": (ctypes.c_int, [ctypes.POINTER(moe_kv_desc), ctypes.c_void_p, ctypes.c_longlong] +
+                                   [ctypes.c_void_p] * 3 + [ctypes.POINTER(moe_kv_cache), ctypes.c_int, ctypes.c_float, ctypes.c_int,
+                                                            ctypes.c_int, ctypes.POINTER(moe_kv_prefix)] +
+                                   [ctypes.c_void_p] * 3 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_kv_weights": (ctypes.c_int, [ctypes.POINTER(moe_kv_desc), ctypes.c_void_p, ctypes.c_longlong] + [ctypes.c_void_p] * 4 +
+                       [ctypes.POINTER(moe_kv_cache), ctypes.c_int, ctypes.c_float, ctypes.c_int, ctypes.c_int] +
+                       [ctypes.c_void_p] * 3 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_kv_evict": (ctypes.c_int, [ctypes.POINTER(moe_kv_desc)] + [ctypes.c_void_p] * 4 + [ctypes.c_int] * 2 +
+                     [ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(moe_kv_cache)] + [ctypes.c_void_p] * 3 +
+                     [ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 
@@ -789,5 +814,6 @@ class MoELayer:
         return self.ws[off:off + nbytes].view(dt).view(shape)
 
 
-from .attention import (AttentionLayer, KVCache, moe_kv_append, moe_kv_gather, moe_paged_attention,  # noqa: E402,F401
-                        moe_paged_attention_workspace, moe_rope_table)
+from .attention import (AttentionLayer, KVCache, moe_kv_append, moe_kv_append_at, moe_kv_evict, moe_kv_gather,  # noqa: E402,F401
+                        moe_kv_weights, moe_kv_workspace, moe_paged_attention, moe_paged_attention_shared,
+                        moe_paged_attention_shared_workspace, moe_paged_attention_workspace, moe_rope_rows, moe_rope_table)

@@ -1,4 +1,4 @@
-"""Attention over a paged 8-bit key/value cache: Python binding of the moe_kv_* and moe_paged_attention entry points.
+"""Attention over a paged 8-bit key/value cache: Python binding of the moe_kv_*, moe_rope_* and moe_paged_attention* entry points.
 
 Argument marshalling only, as in the rest of the package; ``include/moe.h`` states formats, limits and errors.
 """
@@ -20,6 +20,8 @@ class _Bound:
         torch, lib = _m._torch(), _m.lib()
         self.torch, self.bf16, self.i32, self.u8, self.f32 = torch, torch.bfloat16, torch.int32, torch.uint8, torch.float32
         self.append, self.gather, self.attention = lib.moe_kv_append, lib.moe_kv_gather, lib.moe_paged_attention
+        self.rope_rows, self.append_at, self.shared = lib.moe_rope_rows, lib.moe_kv_append_at, lib.moe_paged_attention_shared
+        self.weights, self.evict, self.shared_size = lib.moe_kv_weights, lib.moe_kv_evict, lib.moe_paged_attention_shared_workspace_size
         self.workspace_size, self.status_bytes = lib.moe_paged_attention_workspace_size, lib.moe_status_bytes()
         self.raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -122,11 +124,59 @@ def moe_rope_table(max_pos: int, rot_dim: int = 128, base: float = 1e6, cos_sin=
     return cos_sin
 
 
+def moe_kv_workspace(device="cuda"):
+    """A workspace for the calls that need no more than a status word: all of this module but the attention's."""
+    return _b().torch.zeros(max(_b().status_bytes, 256), dtype=_b().u8, device=device)
+
+
+def moe_rope_rows(positions, axes, cos_sin, rows=None, ws=None, stream=None):
+    """The rotation of each new token, rows [T, rot_dim] fp32 for moe_kv_append_at: frequency f turns by positions[axes[f], t].
+    positions [n_axes, T] int32 (a row's tokens dense), axes: rot_dim / 2 ints, cos_sin as moe_rope_table makes it."""
+    b = _b()
+    if positions.dim() != 2 or positions.dtype is not b.i32 or not positions.is_cuda:
+        raise ValueError(f"positions: expected a CUDA int32 tensor [n_axes, T], got {positions.dtype} {tuple(positions.shape)}")
+    n_axes, T = positions.shape
+    if T > 1 and positions.stride(1) != 1:
+        raise ValueError(f"positions: the tokens of an axis must be dense, got strides {positions.stride()}")
+    if cos_sin.dim() != 2 or len(axes) * 2 != cos_sin.shape[1]:
+        raise ValueError(f"axes: expected one for each frequency of cos_sin {tuple(cos_sin.shape)}, got {len(axes)}")
+    if any(not 0 <= x < n_axes for x in axes):
+        raise ValueError(f"axes: expected numbers of the {n_axes} axes, got {tuple(axes)}")
+    max_pos, rot_dim = cos_sin.shape
+    cs = _need(cos_sin, "cos_sin", b.f32, cos_sin.shape)
+    rp = None if rows is None else _need(rows, "rows", b.f32, (T, rot_dim))
+    ws = _status_ws(positions, ws, stream)
+    if rows is None:
+        rows = _new(stream, positions, (T, rot_dim), b.f32)
+        rp = rows.data_ptr()
+    stride = positions.stride(0) if n_axes > 1 else T
+    status = b.rope_rows(n_axes, T, positions.data_ptr(), stride, bytes(axes), cs, max_pos, rot_dim, rp, ws.data_ptr(), ws.numel(),
+                         _stream_of(stream, positions))
+    if status:
+        _m._check(status, "moe_rope_rows")
+    return rows
+
+
+def moe_kv_append_at(q, k, v, cache: KVCache, q_start, kv_len, page_table, rows, interleaved: bool = False, q_norm_weight=None,
+                     k_norm_weight=None, eps: float = 1e-6, q_out=None, ws=None, stream=None):
+    """moe_kv_append with the rotation of token t in rows[t] (of moe_rope_rows), wherever in the cache it goes."""
+    if rows.dim() != 2 or rows.shape[0] != k.shape[0]:
+        raise ValueError(f"rows: expected [{k.shape[0]}, rot_dim], got {tuple(rows.shape)}")
+    return _append(q, k, v, cache, q_start, kv_len, page_table, rows, rows.shape[1], interleaved, q_norm_weight, k_norm_weight, eps, q_out,
+                   ws, stream, True)
+
+
 def moe_kv_append(q, k, v, cache: KVCache, q_start, kv_len, page_table, cos_sin=None, rot_dim: Optional[int] = None,
                   interleaved: bool = False, q_norm_weight=None, k_norm_weight=None, eps: float = 1e-6, q_out=None,
                   ws=None, stream=None):
     """Normalises (when weights are given) and rotates the new queries and keys, stores the new keys and values in the
     cache; returns the queries [T, Hq, D] (None when q is None).  q, k, v may be views of one projection's rows."""
+    return _append(q, k, v, cache, q_start, kv_len, page_table, cos_sin, rot_dim, interleaved, q_norm_weight, k_norm_weight, eps, q_out,
+                   ws, stream, False)
+
+
+def _append(q, k, v, cache, q_start, kv_len, page_table, cos_sin, rot_dim, interleaved, q_norm_weight, k_norm_weight, eps, q_out, ws,
+            stream, by_token):
     b = _b()
     kv = cache._struct()
     n_pages, Hkv, page, D = cache[0].shape
@@ -158,10 +208,14 @@ def moe_kv_append(q, k, v, cache: KVCache, q_start, kv_len, page_table, cos_sin=
     if q is not None and q_out is None:
         q_out = _new(stream, k, (T, Hq, D))
         op = q_out.data_ptr()
-    status = b.append(_byref(d), qp, qs, kp, ks, vp, vs, starts, lens, table, cs, max_pos, rot_dim, interleaved, qw, kw, eps,
-                      op, _byref(kv), ws.data_ptr(), ws.numel(), _stream_of(stream, k))
+    if by_token:
+        status = b.append_at(_byref(d), qp, qs, kp, ks, vp, vs, starts, lens, table, cs, rot_dim, interleaved, qw, kw, eps, op,
+                             _byref(kv), ws.data_ptr(), ws.numel(), _stream_of(stream, k))
+    else:
+        status = b.append(_byref(d), qp, qs, kp, ks, vp, vs, starts, lens, table, cs, max_pos, rot_dim, interleaved, qw, kw, eps,
+                          op, _byref(kv), ws.data_ptr(), ws.numel(), _stream_of(stream, k))
     if status:
-        _m._check(status, "moe_kv_append")
+        _m._check(status, "moe_kv_append_at" if by_token else "moe_kv_append")
     return q_out
 
 
@@ -230,6 +284,121 @@ def moe_paged_attention(q, cache: KVCache, q_start, kv_len, page_table, max_q: i
     if status:
         _m._check(status, "moe_paged_attention")
     return out
+
+
+def _prefix_struct(prefix, T: int):
+    """moe_kv_prefix of (q_start [n+1], len [n], page_table [n, max_pages], max_q)."""
+    b = _b()
+    q_start, length, page_table, max_q = prefix
+    table, n, max_pages = _table(page_table)
+    return _m.moe_kv_prefix(n, max_pages, min(max_q, T), _need(q_start, "prefix q_start", b.i32, (n + 1,)),
+                            _need(length, "prefix len", b.i32, (n,)), table)
+
+
+def moe_paged_attention_shared_workspace(T: int, B: int, Hq: int, Hkv: int, D: int, max_q: int, n_prefixes: int = 0,
+                                         max_prefix_q: int = 0, device="cuda"):
+    """An initialised workspace for moe_paged_attention_shared calls of these sizes (n_prefixes = 0: without prefixes)."""
+    p = _m.moe_kv_prefix(n_prefixes, 0, min(max_prefix_q, T), None, None, None) if n_prefixes else None
+    return _shared_workspace(_m.moe_kv_desc(B, T, Hq, Hkv, D, 16, 0, 0), min(max_q, T), p, _b().torch.empty(0, device=device))
+
+
+def _shared_workspace(desc, max_q: int, prefix, like, stream=None):
+    b = _b()
+    need = b.shared_size(_byref(desc), max_q, None if prefix is None else _byref(prefix))
+    if need == 0:
+        raise _m.MoEError(_m.MOE_ERR_UNSUPPORTED, "moe_paged_attention_shared_workspace_size")
+    ws = _new(stream, like, (need,), b.u8)
+    _m._check(_m.lib().moe_workspace_init(ws.data_ptr(), need, _stream_of(stream, ws)), "moe_workspace_init")
+    return ws
+
+
+def moe_paged_attention_shared(q, cache: KVCache, q_start, kv_len, page_table, max_q: int, prefix=None, scale: Optional[float] = None,
+                               causal: bool = True, window: int = 0, out=None, lse=None, ws=None, stream=None):
+    """moe_paged_attention of sequences that share prefixes, with the rows' denominators: returns (out [T, Hq, D] bf16,
+    lse [T, Hq] fp32).
+
+    prefix: None, or (q_start [n+1], len [n], page_table [n, max_pages], max_q): tokens q_start[i] .. q_start[i+1] - 1 see the
+    len[i] tokens of prefix i before their sequence's own; max_q: at least the tokens of any one prefix's readers."""
+    b = _b()
+    kv = cache._struct()
+    n_pages, Hkv, page, D = cache[0].shape
+    table, B, max_pages = _table(page_table)
+    T, Hq = q.shape[0], q.shape[1]
+    max_q = min(max_q, T)
+    qp, qs = _rows(q, "q", Hq, D)
+    d = _m.moe_kv_desc(B, T, Hq, Hkv, D, page, n_pages, max_pages)
+    starts, lens = _need(q_start, "q_start", b.i32, (B + 1,)), _need(kv_len, "kv_len", b.i32, (B,))
+    p = None if prefix is None else _prefix_struct(prefix, T)
+    op = None if out is None else _need(out, "out", b.bf16, (T, Hq, D))
+    lp = None if lse is None else _need(lse, "lse", b.f32, (T, Hq))
+    ws = _shared_workspace(d, max_q, p, q, stream) if ws is None else _status_ws(q, ws)
+    if out is None:
+        out = _new(stream, q, (T, Hq, D))
+        op = out.data_ptr()
+    if lse is None:
+        lse = _new(stream, q, (T, Hq), b.f32)
+        lp = lse.data_ptr()
+    status = b.shared(_byref(d), qp, qs, starts, lens, table, _byref(kv), max_q, D ** -0.5 if scale is None else scale, causal, window,
+                      None if p is None else _byref(p), op, lp, ws.data_ptr(), ws.numel(), _stream_of(stream, q))
+    if status:
+        _m._check(status, "moe_paged_attention_shared")
+    return out, lse
+
+
+def moe_kv_weights(q, lse, cache: KVCache, q_start, kv_len, page_table, max_q: int, weight=None, out=None, scale: Optional[float] = None,
+                   causal: bool = True, window: int = 0, ws=None, stream=None):
+    """Adds what the new queries q [T, Hq, D] give to each cached token of their sequences, with the denominators lse [T, Hq] of
+    moe_paged_attention_shared, to weight [n_pages, Hkv, page] fp32 (None: from zero on), in place or into out; returns that."""
+    b = _b()
+    kv = cache._struct()
+    n_pages, Hkv, page, D = cache[0].shape
+    table, B, max_pages = _table(page_table)
+    T, Hq = q.shape[0], q.shape[1]
+    max_q = min(max_q, T)
+    qp, qs = _rows(q, "q", Hq, D)
+    d = _m.moe_kv_desc(B, T, Hq, Hkv, D, page, n_pages, max_pages)
+    starts, lens = _need(q_start, "q_start", b.i32, (B + 1,)), _need(kv_len, "kv_len", b.i32, (B,))
+    lp, shape = _need(lse, "lse", b.f32, (T, Hq)), (n_pages, Hkv, page)
+    wp = None if weight is None else _need(weight, "weight", b.f32, shape)
+    op = wp if out is None else _need(out, "out", b.f32, shape)
+    if op is None:
+        raise ValueError("out: needed when there is no weight to add to")
+    ws = _status_ws(q, ws, stream)
+    status = b.weights(_byref(d), qp, qs, lp, starts, lens, table, _byref(kv), max_q, D ** -0.5 if scale is None else scale, causal,
+                       window, wp, op, ws.data_ptr(), ws.numel(), _stream_of(stream, q))
+    if status:
+        _m._check(status, "moe_kv_weights")
+    return weight if out is None else out
+
+
+def moe_kv_evict(cache: KVCache, weight, kv_len, page_table, keep, new_table, sink: int = 0, recent: int = 0, new_len=None, kept=None,
+                 ws=None, stream=None):
+    """Packs the keep[b] tokens of the largest weight [n_pages, Hkv, page] of each sequence and head, with their weights, into the
+    pages of new_table; returns (new_len [B], kept [B, Hkv, new_max_pages * page]: the tokens that stayed, then -1)."""
+    b = _b()
+    kv = cache._struct()
+    n_pages, Hkv, page, D = cache[0].shape
+    table, B, max_pages = _table(page_table)
+    new, new_B, new_max = _table(new_table)
+    if new_B != B:
+        raise ValueError(f"new_table: expected [{B}, new_max_pages], got {tuple(new_table.shape)}")
+    d = _m.moe_kv_desc(B, 0, Hkv, Hkv, D, page, n_pages, max_pages)
+    wp = _need(weight, "weight", b.f32, (n_pages, Hkv, page))
+    lens, keeps = _need(kv_len, "kv_len", b.i32, (B,)), _need(keep, "keep", b.i32, (B,))
+    np_ = None if new_len is None else _need(new_len, "new_len", b.i32, (B,))
+    kp = None if kept is None else _need(kept, "kept", b.i32, (B, Hkv, new_max * page))
+    ws = _status_ws(weight, ws, stream)
+    if new_len is None:
+        new_len = _new(stream, weight, (B,), b.i32)
+        np_ = new_len.data_ptr()
+    if kept is None:
+        kept = _new(stream, weight, (B, Hkv, new_max * page), b.i32)
+        kp = kept.data_ptr()
+    status = b.evict(_byref(d), wp, lens, table, keeps, sink, recent, new, new_max, _byref(kv), np_, kp, ws.data_ptr(), ws.numel(),
+                     _stream_of(stream, weight))
+    if status:
+        _m._check(status, "moe_kv_evict")
+    return new_len, kept
 
 
 class AttentionLayer:

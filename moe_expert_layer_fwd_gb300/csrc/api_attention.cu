@@ -92,11 +92,29 @@ int moe_rope_table(int max_pos, int rot_dim, double base, float* cos_sin, void* 
   return cuda_status(moe::launch_rope_table(max_pos, rot_dim, base, cos_sin, (cudaStream_t)stream));
 }
 
-int moe_kv_append(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const uint16_t* k, long long k_stride,
-                  const uint16_t* v, long long v_stride, const int32_t* q_start, const int32_t* kv_len,
-                  const int32_t* page_table, const float* cos_sin, int max_pos, int rot_dim, int interleaved,
-                  const uint16_t* q_norm_weight, const uint16_t* k_norm_weight, float eps, uint16_t* q_out,
-                  const moe_kv_cache* kv, void* ws, size_t ws_bytes, void* stream) {
+int moe_rope_rows(int n_axes, int T, const int32_t* positions, long long positions_stride, const uint8_t* axes, const float* cos_sin,
+                  int max_pos, int rot_dim, float* rows, void* ws, size_t ws_bytes, void* stream) {
+  if (n_axes < 1 || T < 0 || max_pos < 0 || rot_dim < 1 || positions_stride < T) return MOE_ERR_INVALID_ARG;
+  if (n_axes > moe::kMaxAxes || rot_dim > moe::kHeadDim || rot_dim % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (!axes) return MOE_ERR_INVALID_ARG;
+  moe::RopeAxes x = {};
+  for (int f = 0; f < rot_dim / 2; ++f) {
+    if (axes[f] >= n_axes) return MOE_ERR_INVALID_ARG;
+    x.axis[f] = axes[f];
+  }
+  if (T == 0) return MOE_OK;
+  if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3u) || !ok_ptr(cos_sin) || !ok_ptr(rows)) return MOE_ERR_INVALID_ARG;
+  const int s = check_ws(ws, ws_bytes, kHeader);
+  if (s) return s;
+  return cuda_status(moe::launch_rope_rows(x, T, positions, positions_stride, cos_sin, max_pos, rot_dim, rows, (unsigned*)ws,
+                                           (cudaStream_t)stream));
+}
+
+static int kv_append(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const uint16_t* k, long long k_stride,
+                     const uint16_t* v, long long v_stride, const int32_t* q_start, const int32_t* kv_len,
+                     const int32_t* page_table, const float* cos_sin, int max_pos, bool by_token, int rot_dim, int interleaved,
+                     const uint16_t* q_norm_weight, const uint16_t* k_norm_weight, float eps, uint16_t* q_out,
+                     const moe_kv_cache* kv, void* ws, size_t ws_bytes, void* stream) {
   int s = check_desc(d);
   if (s) return s;
   if (max_pos < 0 || rot_dim < 0 || !(eps >= 0)) return MOE_ERR_INVALID_ARG;
@@ -113,9 +131,27 @@ int moe_kv_append(const moe_kv_desc* d, const uint16_t* q, long long q_stride, c
   moe::KvBatch c = make_batch(d, kv, page_table, (unsigned*)ws);
   c.q_start = q_start;
   c.kv_len = kv_len;
-  moe::KvAppendArgs a = {q, k, v, q_stride, k_stride, v_stride, cos_sin, rot_dim > 0 ? max_pos : INT32_MAX, rot_dim,
-                         interleaved != 0, q_norm_weight, k_norm_weight, eps, q_out};
+  moe::KvAppendArgs a = {q, k, v, q_stride, k_stride, v_stride, cos_sin, rot_dim > 0 && !by_token ? max_pos : INT32_MAX, rot_dim,
+                         interleaved != 0, by_token, q_norm_weight, k_norm_weight, eps, q_out};
   return cuda_status(moe::launch_kv_append(c, a, sm_count(), (cudaStream_t)stream));
+}
+
+int moe_kv_append(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const uint16_t* k, long long k_stride,
+                  const uint16_t* v, long long v_stride, const int32_t* q_start, const int32_t* kv_len,
+                  const int32_t* page_table, const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                  const uint16_t* q_norm_weight, const uint16_t* k_norm_weight, float eps, uint16_t* q_out,
+                  const moe_kv_cache* kv, void* ws, size_t ws_bytes, void* stream) {
+  return kv_append(d, q, q_stride, k, k_stride, v, v_stride, q_start, kv_len, page_table, cos_sin, max_pos, false, rot_dim, interleaved,
+                   q_norm_weight, k_norm_weight, eps, q_out, kv, ws, ws_bytes, stream);
+}
+
+int moe_kv_append_at(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const uint16_t* k, long long k_stride,
+                     const uint16_t* v, long long v_stride, const int32_t* q_start, const int32_t* kv_len,
+                     const int32_t* page_table, const float* rows, int rot_dim, int interleaved, const uint16_t* q_norm_weight,
+                     const uint16_t* k_norm_weight, float eps, uint16_t* q_out, const moe_kv_cache* kv, void* ws, size_t ws_bytes,
+                     void* stream) {
+  return kv_append(d, q, q_stride, k, k_stride, v, v_stride, q_start, kv_len, page_table, rows, 0, true, rot_dim, interleaved,
+                   q_norm_weight, k_norm_weight, eps, q_out, kv, ws, ws_bytes, stream);
 }
 
 int moe_kv_gather(const moe_kv_desc* d, const int32_t* start, const int32_t* out_start, const int32_t* page_table,
@@ -136,6 +172,125 @@ int moe_kv_gather(const moe_kv_desc* d, const int32_t* start, const int32_t* out
 size_t moe_paged_attention_workspace_size(const moe_kv_desc* d, int max_q) {
   if (check_desc(d) || max_q < 0) return 0;
   return kHeader + moe::attention_scratch_bytes(d->Hq, d->Hkv, max_q, sm_count());
+}
+
+static int check_attention(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const int32_t* q_start, const int32_t* kv_len,
+                           const int32_t* page_table, int max_q) {
+  if (max_q < 1 || max_q > d->T || (long long)max_q * d->B < d->T) return MOE_ERR_INVALID_ARG;
+  if (!ok_ptr(q) || !ok_ptr(q_start) || !ok_ptr(kv_len) || !ok_ptr(page_table)) return MOE_ERR_INVALID_ARG;
+  return ok_stride(q_stride, d->Hq) ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
+// The prefixes of a shared attention as a batch of their own: its sequences are the prefixes, its tokens their readers'.
+static int prefix_desc(const moe_kv_desc* d, const moe_kv_prefix* p, moe_kv_desc* out) {
+  if (p->n < 1 || p->max_pages < 0 || p->max_q < 0) return MOE_ERR_INVALID_ARG;
+  *out = *d;
+  out->B = p->n;
+  out->max_pages = p->max_pages;
+  return check_desc(out);
+}
+
+static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t moe_paged_attention_shared_workspace_size(const moe_kv_desc* d, int max_q, const moe_kv_prefix* prefix) {
+  if (check_desc(d) || max_q < 0) return 0;
+  size_t scratch = moe::attention_scratch_bytes(d->Hq, d->Hkv, max_q, sm_count());
+  if (!prefix) return kHeader + scratch;
+  moe_kv_desc pd;
+  if (prefix_desc(d, prefix, &pd)) return 0;
+  const size_t other = moe::attention_scratch_bytes(d->Hq, d->Hkv, prefix->max_q, sm_count());
+  if (other > scratch) scratch = other;
+  const size_t rows = (size_t)d->T * d->Hq;
+  return kHeader + up256(rows * moe::kHeadDim * sizeof(float)) + up256(rows * sizeof(float)) + scratch;
+}
+
+int moe_paged_attention_shared(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const int32_t* q_start,
+                               const int32_t* kv_len, const int32_t* page_table, const moe_kv_cache* kv, int max_q, float scale,
+                               int causal, int window, const moe_kv_prefix* prefix, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                               void* stream) {
+  int s = check_desc(d);
+  if (s) return s;
+  if (max_q < 0 || window < 0 || !(scale > 0) || !isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  if (window > 0 && (!causal || prefix)) return MOE_ERR_INVALID_ARG;
+  moe_kv_desc pd = {};
+  if (prefix && (s = prefix_desc(d, prefix, &pd))) return s;
+  if (d->T == 0) return MOE_OK;
+  if ((s = check_attention(d, q, q_stride, q_start, kv_len, page_table, max_q))) return s;
+  if (prefix && (s = check_attention(&pd, q, q_stride, prefix->q_start, prefix->len, prefix->page_table, prefix->max_q))) return s;
+  if (!ok_ptr(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return MOE_ERR_INVALID_ARG;
+  if ((s = check_cache(kv))) return s;
+  if ((s = check_ws(ws, ws_bytes, moe_paged_attention_shared_workspace_size(d, max_q, prefix)))) return s;
+  moe::KvBatch c = make_batch(d, kv, page_table, (unsigned*)ws), pc = {};
+  c.q_start = q_start;
+  c.kv_len = kv_len;
+  char* at = (char*)ws + kHeader;
+  float *rows = nullptr, *rows_lse = nullptr;
+  if (prefix) {
+    pc = make_batch(&pd, kv, prefix->page_table, (unsigned*)ws);
+    pc.q_start = prefix->q_start;
+    pc.kv_len = prefix->len;
+    rows = (float*)at;
+    at += up256((size_t)d->T * d->Hq * moe::kHeadDim * sizeof(float));
+    rows_lse = (float*)at;
+    at += up256((size_t)d->T * d->Hq * sizeof(float));
+  }
+  moe::AttentionArgs a = {};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.scale_log2 = scale * 1.44269504088896341f;
+  a.causal = causal != 0;
+  a.window = window;
+  a.max_q = max_q;
+  a.scratch = at;
+  a.lse = lse;
+  a.lse_unit = 0.693147180559945309f;
+  return cuda_status(moe::launch_shared_attention(pc, prefix ? prefix->max_q : 0, c, a, rows, rows_lse, sm_count(), (cudaStream_t)stream));
+}
+
+int moe_kv_weights(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const float* lse, const int32_t* q_start,
+                   const int32_t* kv_len, const int32_t* page_table, const moe_kv_cache* kv, int max_q, float scale, int causal,
+                   int window, const float* weight_in, float* weight_out, void* ws, size_t ws_bytes, void* stream) {
+  int s = check_desc(d);
+  if (s) return s;
+  if (max_q < 0 || window < 0 || !(scale > 0) || !isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  if (window > 0 && !causal) return MOE_ERR_INVALID_ARG;
+  if (d->T == 0) return MOE_OK;
+  if ((s = check_attention(d, q, q_stride, q_start, kv_len, page_table, max_q))) return s;
+  if (!ok_ptr(lse) || !aligned16(weight_in) || !ok_ptr(weight_out)) return MOE_ERR_INVALID_ARG;
+  if ((s = check_cache(kv))) return s;
+  if ((s = check_ws(ws, ws_bytes, kHeader))) return s;
+  moe::KvBatch c = make_batch(d, kv, page_table, (unsigned*)ws);
+  c.q_start = q_start;
+  c.kv_len = kv_len;
+  moe::AttentionArgs a = {};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.scale_log2 = scale * 1.44269504088896341f;
+  a.causal = causal != 0;
+  a.window = window;
+  a.max_q = max_q;
+  return cuda_status(moe::launch_kv_weights(c, a, lse, weight_in, weight_out, sm_count(), (cudaStream_t)stream));
+}
+
+int moe_kv_evict(const moe_kv_desc* d, float* weight, const int32_t* kv_len, const int32_t* page_table, const int32_t* keep, int sink,
+                 int recent, const int32_t* new_table, int new_max_pages, const moe_kv_cache* kv, int32_t* new_len, int32_t* kept,
+                 void* ws, size_t ws_bytes, void* stream) {
+  int s = check_desc(d);
+  if (s) return s;
+  if (sink < 0 || recent < 0 || new_max_pages < 1) return MOE_ERR_INVALID_ARG;
+  if ((long long)new_max_pages * d->page > (1LL << 30) || (long long)d->B * d->Hkv * new_max_pages >= kMaxRows ||
+      (long long)d->B * d->Hkv * 8 >= kMaxRows)
+    return MOE_ERR_UNSUPPORTED;
+  if (d->B == 0) return MOE_OK;
+  if (!ok_ptr(weight) || !ok_ptr(kv_len) || !ok_ptr(page_table) || !ok_ptr(keep) || !ok_ptr(new_table) || !ok_ptr(new_len) || !ok_ptr(kept))
+    return MOE_ERR_INVALID_ARG;
+  if ((s = check_cache(kv))) return s;
+  if ((s = check_ws(ws, ws_bytes, kHeader))) return s;
+  moe::KvBatch c = make_batch(d, kv, page_table, (unsigned*)ws);
+  c.kv_len = kv_len;
+  const moe::KvEvictArgs e = {weight, keep, sink, recent, new_table, new_max_pages, new_len, kept};
+  return cuda_status(moe::launch_kv_evict(c, e, sm_count(), (cudaStream_t)stream));
 }
 
 int moe_paged_attention(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const int32_t* q_start,

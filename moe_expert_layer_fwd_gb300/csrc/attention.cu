@@ -15,8 +15,8 @@ constexpr int kJoinThreads = 256;
 // (blockIdx.x) does not hold an item's second part have nothing to do.
 template <int kWarps>
 __global__ void __launch_bounds__(kJoinThreads)
-    attention_join_kernel(const KvBatch c, const AttentionArgs a, int rows, const float* part_o, const float2* part_rl,
-                          const JoinInfo* info) {
+    attention_join_kernel(const KvBatch c, const AttentionArgs a, int rows, float base, const float* part_o,
+                          const float2* part_rl, const JoinInfo* info) {
   __shared__ float4 s_acc[kJoinThreads];
   __shared__ float s_sum[kJoinThreads / 32];
   pdl_wait();
@@ -63,17 +63,29 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (!live) return;
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
   const int rho = j.row0 + row, i = rho / G;
-  uint16_t* out = a.out + ((size_t)(t0 + i) * c.Hq + j.h * G + rho - i * G) * kHeadDim;
+  const size_t at = (size_t)(t0 + i) * c.Hq + j.h * G + rho - i * G;
+  if (a.extra) {
+    const RowEnd e = end_row(a, at, inv, top - base, sum, lane == 0);
+    acc = make_float4(acc.x * e.f, acc.y * e.f, acc.z * e.f, acc.w * e.f);
+    if (a.prior) {
+      const float4 p = reinterpret_cast<const float4*>(a.prior + at * kHeadDim)[lane];
+      acc = make_float4(fmaf(p.x, e.f1, acc.x), fmaf(p.y, e.f1, acc.y), fmaf(p.z, e.f1, acc.z), fmaf(p.w, e.f1, acc.w));
+    }
+    if (a.out32) reinterpret_cast<float4*>(a.out32 + at * kHeadDim)[lane] = acc;
+    else reinterpret_cast<uint2*>(a.out + at * kHeadDim)[lane] = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    return;
+  }
+  uint16_t* out = a.out + at * kHeadDim;
   reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 }  // namespace
 
-cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int blocks, int rows, const float* part_o,
+cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int blocks, int rows, float base, const float* part_o,
                                   const float2* part_rl, const JoinInfo* info, cudaStream_t stream) {
   constexpr int kAll = kJoinThreads / 32;
-  if (rows <= 32) return launch_kernel(attention_join_kernel<kAll>, dim3(blocks, rows), dim3(kJoinThreads), 0, stream, true, c, a, rows, part_o, part_rl, info);
-  return launch_kernel(attention_join_kernel<1>, dim3(blocks, (rows + kAll - 1) / kAll), dim3(kJoinThreads), 0, stream, true, c, a, rows, part_o, part_rl, info);
+  if (rows <= 32) return launch_kernel(attention_join_kernel<kAll>, dim3(blocks, rows), dim3(kJoinThreads), 0, stream, true, c, a, rows, base, part_o, part_rl, info);
+  return launch_kernel(attention_join_kernel<1>, dim3(blocks, (rows + kAll - 1) / kAll), dim3(kJoinThreads), 0, stream, true, c, a, rows, base, part_o, part_rl, info);
 }
 
 bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c) {
@@ -111,6 +123,36 @@ int attention_debug_set(int what, unsigned long long value) {
   else if (what == 4) g_withhold = value != 0;
   else return -1;
   return 0;
+}
+
+// Two passes, each with the kernel that its rows per key/value head call for: over the prefixes, whose readers' tokens are one
+// sequence that sees all of it (so a prefix is read once for all of them, and its rows fill the tiles), then over the
+// sequences' own tokens, whose ends add the first pass's rows.  The rows in between are fp32.
+cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, const KvBatch& c, const AttentionArgs& args, float* rows,
+                                    float* rows_lse, int n_sms, cudaStream_t stream) {
+  AttentionArgs a = args;
+  a.extra = 1;
+  if (rows) {
+    AttentionArgs p = a;
+    p.causal = p.window = 0;
+    p.max_q = max_prefix_q;
+    p.out32 = rows;
+    p.lse = rows_lse;
+    p.lse_unit = 1.f;
+    const cudaError_t e = launch_paged_attention(prefixes, p, n_sms, stream);
+    if (e != cudaSuccess) return e;
+    a.prior = rows;
+    a.prior_lse = rows_lse;
+  }
+  return launch_paged_attention(c, a, n_sms, stream);
+}
+
+cudaError_t launch_kv_weights(const KvBatch& c, const AttentionArgs& args, const float* lse, const float* weight_in, float* weight_out,
+                              int n_sms, cudaStream_t stream) {
+  AttentionArgs a = args;
+  a.limit_us = g_limit_us;
+  a.withhold = g_withhold;
+  return launch_kv_weights_rows(c, a, lse, weight_in, weight_out, n_sms, stream);
 }
 
 cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& args, int n_sms, cudaStream_t stream) {

@@ -166,11 +166,6 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv) {
   return o;
 }
 
-__device__ __forceinline__ uint32_t rescale4(uint32_t codes, float f) {
-  const float2 a = e4m3x2_f32(codes & 0xFFFFu), b = e4m3x2_f32(codes >> 16);
-  return e4m3x2(a.x * f, a.y * f) | (e4m3x2(b.x * f, b.y * f) << 16);
-}
-
 __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);
   return a <= 3.402823466e38f ? a : 0.f;  // infinities and NaN do not set the scale
@@ -212,7 +207,7 @@ __device__ __forceinline__ void rope_queries(const KvBatch& c, const KvAppendArg
     const int pos = ok ? s.first() + t - s.t0 : -1;
     const bool there = pos >= 0 && pos < a.max_pos;
     if (!there && lane == 0) set_status(c.status, DEV_ERR_BOUNDS);
-    if (there) rotary_load(rt, a, l, pos);
+    if (there) rotary_load(rt, a, l, a.by_token ? t : pos);
     cp_async_wait<1>();
     if (!there) continue;
 #pragma unroll
@@ -283,7 +278,7 @@ __device__ __forceinline__ void append_unit(const KvBatch& c, const KvAppendArgs
       if (base + i * 2 * kWarps >= r1) break;
       const int r = base + half + i * 2 * kWarps;
       const bool here = r >= r0 && r < r1;
-      if (here) rotary_load(rt, a, l, p0 + r);
+      if (here) rotary_load(rt, a, l, a.by_token ? s.t0 + p0 + r - first : p0 + r);
       float x[8], v[8];
       norm_rotate(kr[i], rt, a, norm, weight, x);
       unpack8(vr[i], v);
@@ -445,7 +440,41 @@ __global__ void rope_table_kernel(int max_pos, int rot, double base, float* cos_
   }
 }
 
+// The rotation of each new token, positions on one axis per frequency: read from the table once a step, for every layer's append
+// (which then reads whole rows as it does from the table).  Four frequencies a thread; a position that the table does not have
+// makes the row's part of it NaN, so that the token does not pass for one at another place.
+__global__ void __launch_bounds__(256) rope_rows_kernel(const __grid_constant__ RopeAxes axes, int T, const int32_t* positions, long long stride,
+                                                        const float* cos_sin, int max_pos, int rot, float* rows, unsigned* status) {
+  const int half = rot >> 1, quads = half >> 2;
+  const long long n = (long long)T * quads;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+    const long long t = i / quads;
+    const int f = (int)(i - t * quads) * 4;
+    float c[4], s[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int pos = __ldg(positions + axes.axis[f + x] * stride + t);
+      const bool ok = pos >= 0 && pos < max_pos;
+      if (!ok) set_status(status, DEV_ERR_BOUNDS);
+      const float* row = cos_sin + (size_t)(ok ? pos : 0) * rot + f + x;
+      c[x] = ok ? __ldg(row) : __int_as_float(0x7FFFFFFF);
+      s[x] = ok ? __ldg(row + half) : __int_as_float(0x7FFFFFFF);
+    }
+    float* out = rows + t * rot + f;
+    *reinterpret_cast<float4*>(out) = make_float4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<float4*>(out + half) = make_float4(s[0], s[1], s[2], s[3]);
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_rope_rows(const RopeAxes& axes, int T, const int32_t* positions, long long stride, const float* cos_sin,
+                             int max_pos, int rot, float* rows, unsigned* status, cudaStream_t stream) {
+  const long long blocks = ((long long)T * (rot >> 3) + 255) / 256;
+  rope_rows_kernel<<<(unsigned)(blocks < 8192 ? blocks : 8192), 256, 0, stream>>>(axes, T, positions, stride, cos_sin, max_pos, rot,
+                                                                                rows, status);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_kv_append(const KvBatch& c, const KvAppendArgs& a, int n_sms, cudaStream_t stream) {
   const long long slots = (long long)c.T / c.page + 2LL * c.B;

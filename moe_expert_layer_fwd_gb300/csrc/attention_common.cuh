@@ -74,6 +74,12 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t codes) {
   return __half22float2(__half2(h));
 }
 
+// Four codes times f, rounded again.
+__device__ __forceinline__ uint32_t rescale4(uint32_t codes, float f) {
+  const float2 a = e4m3x2_f32(codes & 0xFFFFu), b = e4m3x2_f32(codes >> 16);
+  return e4m3x2(a.x * f, a.y * f) | (e4m3x2(b.x * f, b.y * f) << 16);
+}
+
 // 16 bytes from global to shared memory, in the background: the first `bytes` of them (0 or 16), then zeros.  A later
 // cp_async_wait<n> waits for all but the last n groups.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {

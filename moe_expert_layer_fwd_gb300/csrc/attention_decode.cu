@@ -134,33 +134,6 @@ __device__ __forceinline__ int seq_tiles(const KvBatch& c, const AttentionArgs& 
   return load_seq(c, b, s) ? key_range(s, a).nt : 0;
 }
 
-// Tiles of all sequences before this thread's share of them, and of all: `threads` threads each take a run of sequences.
-__device__ __forceinline__ long long scan_tiles(const KvBatch& c, const AttentionArgs& a, int threads, long long* s_warp,
-                                                long long& mine, long long& total) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per = (c.B + threads - 1) / threads;
-  mine = 0;
-#pragma unroll 1
-  for (int b = tid * per; b < min(c.B, (tid + 1) * per); ++b) mine += seq_tiles(c, a, b);
-  long long x = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s_warp[warp] = x;
-  __syncthreads();
-  long long before = 0;
-  total = 0;
-#pragma unroll 1
-  for (int w = 0; w < threads / 32; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
-  }
-  __syncthreads();
-  return before + x - mine;
-}
-
 // Tiles per block: equal runs over the grid.
 __device__ __forceinline__ long long tiles_per_block(long long n, int blocks) {
   return max((long long)kMinRun, (n + blocks - 1) / blocks);
@@ -237,7 +210,7 @@ __device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, ui
   lo = e4m3x2((a - h.x) * kLoUp, (b - h.y) * kLoUp);
 }
 
-template <int NC>
+template <int NC, bool kExtra>
 __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     attention_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const KvBatch c, const AttentionArgs a, int split, float* part_o, float2* part_rl,
@@ -280,7 +253,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     long long mine, total;
     // the scan's scratch is the weights' operand, free until the roles start
     long long* s_warp = reinterpret_cast<long long*>(smem + C::kPOff);
-    const long long before = scan_tiles(c, a, C::kThreads, s_warp, mine, total);
+    const long long before = scan_batch(c, C::kThreads, s_warp, mine, total, [&](int b) { return seq_tiles(c, a, b); });
     const long long all = total * c.Hkv, per = tiles_per_block(all, gridDim.x);
     const long long begin = (long long)blockIdx.x * per;
     run = min(per, all - begin);
@@ -727,8 +700,16 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         if (col < cols) {
           if (complete) {
             const int i = col / G;
-            a.out[((size_t)(g.s.t0 + i) * c.Hq + g.h * G + col - i * G) * kHeadDim + key] =
-                f32_to_bf16_rne(sum != 0.f ? acc[x] / sum : 0.f);
+            const size_t at = (size_t)(g.s.t0 + i) * c.Hq + g.h * G + col - i * G;
+            if (kExtra) {
+              const RowEnd e = end_row(a, at, sum != 0.f ? 1.f / sum : 0.f, r[x] - kBase, sum, key == 0);
+              float o = acc[x] * e.f;
+              if (a.prior) o = fmaf(a.prior[at * kHeadDim + key], e.f1, o);
+              if (a.out32) a.out32[at * kHeadDim + key] = o;
+              else a.out[at * kHeadDim + key] = f32_to_bf16_rne(o);
+            } else {
+              a.out[at * kHeadDim + key] = f32_to_bf16_rne(sum != 0.f ? acc[x] / sum : 0.f);
+            }
           } else {
             part_o[((size_t)slot * NC + col) * kHeadDim + key] = acc[x];
             if (key == 0) part_rl[(size_t)slot * NC + col] = make_float2(r[x], sum);
@@ -750,12 +731,12 @@ int width_of(int cols) { return cols <= 8 ? 8 : 16; }
 
 int blocks_of(int n_sms) { return 2 * n_sms; }
 
-template <int NC>
+template <int NC, bool kExtra>
 cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
   using C = Cfg<NC>;
   CUtensorMap tk, tv;
   if (!make_cache_map(&tk, c.k_codes, c) || !make_cache_map(&tv, c.v_codes, c)) return cudaErrorInvalidValue;
-  auto kern = attention_decode_kernel<NC>;
+  auto kern = attention_decode_kernel<NC, kExtra>;
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::kBytes, allowed);
   if (e != cudaSuccess) return e;
@@ -768,7 +749,7 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   e = launch_kernel(kern, dim3(blocks), dim3(C::kThreads), C::kBytes, stream, false, tk, tv, c, a, (int)split, part_o, part_rl,
                     info);
   if (e != cudaSuccess || !split) return e;
-  return launch_attention_join(c, a, blocks, NC, part_o, part_rl, info, stream);
+  return launch_attention_join(c, a, blocks, NC, kBase, part_o, part_rl, info, stream);
 }
 
 }  // namespace
@@ -781,7 +762,9 @@ size_t attention_decode_scratch(int G, int max_q, int n_sms) {
 }
 
 cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
-  return width_of(c.Hq / c.Hkv * a.max_q) == 8 ? launch<8>(c, a, n_sms, stream) : launch<16>(c, a, n_sms, stream);
+  const bool narrow = width_of(c.Hq / c.Hkv * a.max_q) == 8;
+  if (a.extra) return narrow ? launch<8, true>(c, a, n_sms, stream) : launch<16, true>(c, a, n_sms, stream);
+  return narrow ? launch<8, false>(c, a, n_sms, stream) : launch<16, false>(c, a, n_sms, stream);
 }
 
 }  // namespace moe

@@ -28,8 +28,8 @@ struct KvAppendArgs {
   const uint16_t* k;
   const uint16_t* v;
   long long q_stride, k_stride, v_stride;
-  const float* cos_sin;       // [max_pos, rot]: cosines, then sines
-  int max_pos, rot, interleaved;
+  const float* cos_sin;       // [max_pos, rot]: cosines, then sines; or [T, rot], a row for each new token
+  int max_pos, rot, interleaved, by_token;
   const uint16_t* q_norm;     // [128] bf16 or NULL
   const uint16_t* k_norm;
   float eps;
@@ -40,6 +40,14 @@ cudaError_t launch_kv_append(const KvBatch& c, const KvAppendArgs& a, int n_sms,
 // Rows [0, n_rows): row r of sequence b (out_start[b] <= r < out_start[b+1]) is token start[b] + r - out_start[b].
 cudaError_t launch_kv_gather(const KvBatch& c, const int32_t* start, const int32_t* out_start, int n_rows, uint16_t* k,
                              uint16_t* v, cudaStream_t stream);
+
+// rows [T, rot]: of token t and frequency f the cosine and sine at position positions[axis[f] * stride + t].
+constexpr int kMaxAxes = 8;
+struct RopeAxes {
+  uint8_t axis[kHeadDim / 2];
+};
+cudaError_t launch_rope_rows(const RopeAxes& axes, int T, const int32_t* positions, long long stride, const float* cos_sin,
+                             int max_pos, int rot, float* rows, unsigned* status, cudaStream_t stream);
 
 cudaError_t launch_rope_table(int max_pos, int rot, double base, float* cos_sin, cudaStream_t stream);
 
@@ -52,14 +60,45 @@ struct AttentionArgs {
   unsigned limit_us;          // of every wait inside the kernels
   int withhold;               // failure injection (tests only): the values' copies are not issued, so that waits run out
   void* scratch;              // after the status word of the workspace
+  // Attention in two passes over different keys: the first leaves out32 and lse, the second takes them as its prior and
+  // writes the rows of both.  All NULL, extra = 0: neither.
+  int extra;
+  const float* prior;         // [T, Hq, 128] rows of the pass before, and
+  const float* prior_lse;     // [T, Hq] the logarithms (base 2) of their denominators; NULL: no pass before
+  float* out32;               // the rows go here, in fp32, instead of out
+  float* lse;                 // [T, Hq] or NULL: lse_unit times the logarithm (base 2) of the rows' denominators (-inf: nothing seen)
+  float lse_unit;
 };
 size_t attention_scratch_bytes(int Hq, int Hkv, int max_q, int n_sms);
 cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
+
+// Sequences b of `prefixes` are the prefixes, its q_start cuts the T tokens into their readers; rows [T, Hq, 128] and rows_lse
+// [T, Hq]: what is passed from the first pass to the second (NULL: no prefixes).
+cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, const KvBatch& c, const AttentionArgs& a, float* rows,
+                                    float* rows_lse, int n_sms, cudaStream_t stream);
 
 
 // Failure injection (tests only): what 1 = wait limit in ns (0: the default 2 s), what 4 = nonzero: withhold the values'
 // copies.  Returns 0, or -1 for another `what`.
 int attention_debug_set(int what, unsigned long long value);
+
+// weight_out [n_pages, Hkv, page]: for each cached token that a query of a sees, and each new one, weight_in (0 for new ones; NULL: 0)
+// plus the weights that the queries give it; lse [T, Hq] their denominators' natural logarithms.
+cudaError_t launch_kv_weights(const KvBatch& c, const AttentionArgs& a, const float* lse, const float* weight_in, float* weight_out,
+                              int n_sms, cudaStream_t stream);
+cudaError_t launch_kv_weights_rows(const KvBatch& c, const AttentionArgs& a, const float* lse, const float* weight_in, float* weight_out,
+                                   int n_sms, cudaStream_t stream);
+
+struct KvEvictArgs {
+  float* weight;             // [n_pages, Hkv, page]
+  const int32_t* keep;       // [B] tokens that stay
+  int sink, recent;          // first and last tokens that stay before all others
+  const int32_t* new_table;  // [B, new_max_pages]
+  int new_max_pages;
+  int32_t* new_len;          // [B]
+  int32_t* kept;             // [B, Hkv, new_max_pages * page]
+};
+cudaError_t launch_kv_evict(const KvBatch& c, const KvEvictArgs& e, int n_sms, cudaStream_t stream);
 
 // Few query rows per key/value head: G grouped heads times max_q new tokens at most 16.
 bool attention_decode_fits(int G, int max_q);
@@ -81,7 +120,8 @@ struct JoinInfo {
   int pad;
 };
 // part_o [parts][rows][128], part_rl [parts][rows]: unscaled sums, their reference exponent r and denominator l.
-cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int blocks, int rows, const float* part_o,
+// `base`: the sums are of 2^(u - r + base).
+cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int blocks, int rows, float base, const float* part_o,
                                   const float2* part_rl, const JoinInfo* info, cudaStream_t stream);
 
 // The codes as a matrix of 128-byte rows (one token of one head each), boxes of one page with the 128-byte swizzle.

@@ -239,25 +239,6 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
   return d;
 }
-// Pairs of floats in one 64-bit register: one instruction for two products or sums.
-__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ void f32x2_split(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t x, uint64_t y, uint64_t z) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
-  return d;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t x, uint64_t y) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
-  return d;
-}
 // The lowest n bits (none for n <= 0, all from 32 on).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
@@ -319,7 +300,7 @@ __device__ __forceinline__ void rescale_lane64(uint32_t taddr, float f) {
   }
 }
 
-template <bool kSplit>
+template <bool kSplit, bool kExtra>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                              const KvBatch c, const AttentionArgs a, float* part_o, float2* part_rl, JoinInfo* info) {
@@ -663,7 +644,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kSplit && mt == 1) *other_rl = make_float2(r, l);
       auto write = [&](int d, const float (&o)[32], float inv) {  // dims d .. d + 31 of this row
         if (complete) {
-          if (live) {
+          if (kExtra && live) {
+            const size_t at = (size_t)(g.t0 + i_row) * c.Hq + head;
+            const RowEnd e = end_row(a, at, inv, r - kBase, l, d == 0);
+#pragma unroll
+            for (int y = 0; y < 32; y += 4) {
+              float4 v = make_float4(o[y] * e.f, o[y + 1] * e.f, o[y + 2] * e.f, o[y + 3] * e.f);
+              if (a.prior) {
+                const float4 p = *reinterpret_cast<const float4*>(a.prior + at * kHeadDim + d + y);
+                v = make_float4(fmaf(p.x, e.f1, v.x), fmaf(p.y, e.f1, v.y), fmaf(p.z, e.f1, v.z), fmaf(p.w, e.f1, v.w));
+              }
+              if (a.out32) *reinterpret_cast<float4*>(a.out32 + at * kHeadDim + d + y) = v;
+              else *reinterpret_cast<uint2*>(out + d + y) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            }
+          } else if (live) {
 #pragma unroll
             for (int y = 0; y < 32; y += 8)
               *reinterpret_cast<uint4*>(out + d + y) =
@@ -963,12 +957,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool kSplit>
+template <bool kSplit, bool kExtra>
 cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
   using C = Cfg<kSplit>;
   CUtensorMap tk, tv;
   if (!make_cache_map(&tk, c.k_codes, c) || !make_cache_map(&tv, c.v_codes, c)) return cudaErrorInvalidValue;
-  auto kern = attention_prefill_kernel<kSplit>;
+  auto kern = attention_prefill_kernel<kSplit, kExtra>;
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::kBytes, allowed);
   if (e != cudaSuccess) return e;
@@ -977,7 +971,7 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)n_sms * 2 * C::kRows);
   e = launch_kernel(kern, dim3(n_sms), dim3(kThreads), C::kBytes, stream, false, tk, tv, c, a, part_o, part_rl, info);
   if (e != cudaSuccess) return e;
-  return launch_attention_join(c, a, n_sms, C::kRows, part_o, part_rl, info, stream);
+  return launch_attention_join(c, a, n_sms, C::kRows, kBase, part_o, part_rl, info, stream);
 }
 
 // Whether a sequence's rows of one head fit an M tile: it is then the keys that the two tiles share out.
@@ -991,7 +985,9 @@ size_t attention_prefill_scratch(int G, int max_q, int n_sms) {
 }
 
 cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
-  return splits_keys(c.Hq / c.Hkv, a.max_q) ? launch<true>(c, a, n_sms, stream) : launch<false>(c, a, n_sms, stream);
+  const bool split = splits_keys(c.Hq / c.Hkv, a.max_q);
+  if (a.extra) return split ? launch<true, true>(c, a, n_sms, stream) : launch<false, true>(c, a, n_sms, stream);
+  return split ? launch<true, false>(c, a, n_sms, stream) : launch<false, false>(c, a, n_sms, stream);
 }
 
 }  // namespace moe

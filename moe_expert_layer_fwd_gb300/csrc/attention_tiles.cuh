@@ -69,6 +69,34 @@ __device__ __forceinline__ KeyRange key_range(const SeqRange& s, const Attention
   return r;
 }
 
+// What all sequences before this thread's share of them cost, and all together: `threads` threads each take a run of sequences.
+template <typename Cost>
+__device__ __forceinline__ long long scan_batch(const KvBatch& c, int threads, long long* s_warp, long long& mine, long long& total,
+                                                Cost cost) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (c.B + threads - 1) / threads;
+  mine = 0;
+#pragma unroll 1
+  for (int b = tid * per; b < min(c.B, (tid + 1) * per); ++b) mine += cost(b);
+  long long x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+#pragma unroll 1
+  for (int w = 0; w < threads / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  __syncthreads();
+  return before + x - mine;
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -154,6 +182,45 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
+// How a row of a call with `extra` is finished.  The row's own part is o = f o' of o' unscaled sums with the denominator l = sum of
+// 2^(u - r) (f = 1 / l, 0 for a row that sees nothing); L = r + log2 l.  With L1 of the pass before and M = max(L, L1):
+//   out = (2^(L - M) o + 2^(L1 - M) prior) / (2^(L - M) + 2^(L1 - M)),   lse = M + log2 of that sum
+struct RowEnd {
+  float f, f1;  // out = f o' + f1 prior
+};
+__device__ __forceinline__ RowEnd end_row(const AttentionArgs& a, size_t row, float f, float r, float l, bool writes_lse) {
+  RowEnd e = {f, 0.f};
+  float lse = r + log2f(l);
+  if (a.prior) {
+    const float before = a.prior_lse[row], top = fmaxf(lse, before), ref = top == -CUDART_INF_F ? 0.f : top;
+    const float w = ex2(lse - ref), w1 = ex2(before - ref), sum = w + w1, inv = sum != 0.f ? 1.f / sum : 0.f;
+    e.f = f * w * inv;
+    e.f1 = w1 * inv;
+    lse = ref + log2f(sum);
+  }
+  if (a.lse && writes_lse) a.lse[row] = lse * a.lse_unit;
+  return e;
+}
+
+// Pairs of floats in one 64-bit register: one instruction for two products or sums.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void f32x2_split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t x, uint64_t y) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
 // A query row in E4M3 twice over: q * 2^-e = hi + lo with hi the nearest E4M3 value and lo the rest's, e chosen so that
 // the row's largest element lies in [128, 256).  bf16 has 8 significant bits and an E4M3 value 4: the rest of a
 // rounding to 4 bits fits 4 bits again, so the sum is exact for every element above 2^-9 of the row's largest and
