@@ -194,14 +194,13 @@ static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t moe_paged_attention_shared_workspace_size(const moe_kv_desc* d, int max_q, const moe_kv_prefix* prefix) {
   if (check_desc(d) || max_q < 0) return 0;
-  size_t scratch = moe::attention_scratch_bytes(d->Hq, d->Hkv, max_q, sm_count());
+  const size_t scratch = moe::attention_scratch_bytes(d->Hq, d->Hkv, max_q, sm_count());
   if (!prefix) return kHeader + scratch;
   moe_kv_desc pd;
   if (prefix_desc(d, prefix, &pd)) return 0;
-  const size_t other = moe::attention_scratch_bytes(d->Hq, d->Hkv, prefix->max_q, sm_count());
-  if (other > scratch) scratch = other;
   const size_t rows = (size_t)d->T * d->Hq;
-  return kHeader + up256(rows * moe::kHeadDim * sizeof(float)) + up256(rows * sizeof(float)) + scratch;
+  return kHeader + up256(rows * moe::kHeadDim * sizeof(float)) + up256(rows * sizeof(float)) +
+         up256(moe::attention_scratch_bytes(d->Hq, d->Hkv, prefix->max_q, sm_count())) + scratch;
 }
 
 int moe_paged_attention_shared(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const int32_t* q_start,
@@ -225,6 +224,7 @@ int moe_paged_attention_shared(const moe_kv_desc* d, const uint16_t* q, long lon
   c.kv_len = kv_len;
   char* at = (char*)ws + kHeader;
   float *rows = nullptr, *rows_lse = nullptr;
+  void* prefix_scratch = nullptr;
   if (prefix) {
     pc = make_batch(&pd, kv, prefix->page_table, (unsigned*)ws);
     pc.q_start = prefix->q_start;
@@ -233,6 +233,8 @@ int moe_paged_attention_shared(const moe_kv_desc* d, const uint16_t* q, long lon
     at += up256((size_t)d->T * d->Hq * moe::kHeadDim * sizeof(float));
     rows_lse = (float*)at;
     at += up256((size_t)d->T * d->Hq * sizeof(float));
+    prefix_scratch = at;
+    at += up256(moe::attention_scratch_bytes(d->Hq, d->Hkv, prefix->max_q, sm_count()));
   }
   moe::AttentionArgs a = {};
   a.q = q;
@@ -245,7 +247,8 @@ int moe_paged_attention_shared(const moe_kv_desc* d, const uint16_t* q, long lon
   a.scratch = at;
   a.lse = lse;
   a.lse_unit = 0.693147180559945309f;
-  return cuda_status(moe::launch_shared_attention(pc, prefix ? prefix->max_q : 0, c, a, rows, rows_lse, sm_count(), (cudaStream_t)stream));
+  return cuda_status(moe::launch_shared_attention(pc, prefix ? prefix->max_q : 0, prefix_scratch, c, a, rows, rows_lse, sm_count(),
+                                                  (cudaStream_t)stream));
 }
 
 int moe_kv_weights(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const float* lse, const int32_t* q_start,

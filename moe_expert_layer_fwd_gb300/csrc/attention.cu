@@ -13,12 +13,13 @@ constexpr int kJoinThreads = 256;
 // out = sum_k 2^(r_k - r) o_k / sum_k 2^(r_k - r) l_k over an item's parts, in their order.  kWarps warps share a row and
 // split its parts (few rows, many parts: decoding), or each has a row (kWarps = 1); a lane has four dims.  Blocks whose run
 // (blockIdx.x) does not hold an item's second part have nothing to do.
-template <int kWarps>
+template <int kWarps, int kPass>
 __global__ void __launch_bounds__(kJoinThreads)
     attention_join_kernel(const KvBatch c, const AttentionArgs a, int rows, float base, const float* part_o,
                           const float2* part_rl, const JoinInfo* info) {
   __shared__ float4 s_acc[kJoinThreads];
   __shared__ float s_sum[kJoinThreads / 32];
+  if (kPass == 1) pdl_launch_dependents();
   pdl_wait();
   const JoinInfo j = info[blockIdx.x];
   if (!j.split || j.c0 != (int)blockIdx.x - 1) return;
@@ -27,6 +28,14 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int t0 = __ldg(c.q_start + j.b), t1 = __ldg(c.q_start + j.b + 1);
   const bool live = row < rows && j.row0 + row < (t1 - t0) * G;
   auto part = [&](int k) { return (size_t)(2 * k + (k == j.c0 ? j.slot0 : 0)) * rows + row; };
+  const int rho = j.row0 + row, i = rho / G;
+  const size_t at = (size_t)(t0 + i) * c.Hq + j.h * G + rho - i * G;
+  float before = -CUDART_INF_F;  // of the pass before, on its way while the parts are read
+  float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (kPass == 2 && live && a.prior) {
+    before = prior_lse(a, at);
+    p = reinterpret_cast<const float4*>(a.prior + at * kHeadDim)[lane];
+  }
   float top = -CUDART_INF_F, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (live) {
@@ -62,16 +71,13 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
   if (!live) return;
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
-  const int rho = j.row0 + row, i = rho / G;
-  const size_t at = (size_t)(t0 + i) * c.Hq + j.h * G + rho - i * G;
-  if (a.extra) {
-    const RowEnd e = end_row(a, at, inv, top - base, sum, lane == 0);
+  if (kPass > 0) {
+    const RowEnd e = end_row<kPass>(a, at, inv, top - base, sum, before, lane == 0);
     acc = make_float4(acc.x * e.f, acc.y * e.f, acc.z * e.f, acc.w * e.f);
-    if (a.prior) {
-      const float4 p = reinterpret_cast<const float4*>(a.prior + at * kHeadDim)[lane];
+    if (kPass == 2 && a.prior) {
       acc = make_float4(fmaf(p.x, e.f1, acc.x), fmaf(p.y, e.f1, acc.y), fmaf(p.z, e.f1, acc.z), fmaf(p.w, e.f1, acc.w));
     }
-    if (a.out32) reinterpret_cast<float4*>(a.out32 + at * kHeadDim)[lane] = acc;
+    if (kPass == 1) reinterpret_cast<float4*>(a.out32 + at * kHeadDim)[lane] = acc;
     else reinterpret_cast<uint2*>(a.out + at * kHeadDim)[lane] = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
     return;
   }
@@ -84,8 +90,10 @@ __global__ void __launch_bounds__(kJoinThreads)
 cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int blocks, int rows, float base, const float* part_o,
                                   const float2* part_rl, const JoinInfo* info, cudaStream_t stream) {
   constexpr int kAll = kJoinThreads / 32;
-  if (rows <= 32) return launch_kernel(attention_join_kernel<kAll>, dim3(blocks, rows), dim3(kJoinThreads), 0, stream, true, c, a, rows, base, part_o, part_rl, info);
-  return launch_kernel(attention_join_kernel<1>, dim3(blocks, (rows + kAll - 1) / kAll), dim3(kJoinThreads), 0, stream, true, c, a, rows, base, part_o, part_rl, info);
+  auto kern = rows <= 32 ? (a.pass == 0 ? attention_join_kernel<kAll, 0> : a.pass == 1 ? attention_join_kernel<kAll, 1> : attention_join_kernel<kAll, 2>)
+                         : (a.pass == 0 ? attention_join_kernel<1, 0> : a.pass == 1 ? attention_join_kernel<1, 1> : attention_join_kernel<1, 2>);
+  const dim3 grid(blocks, rows <= 32 ? rows : (rows + kAll - 1) / kAll);
+  return launch_kernel(kern, grid, dim3(kJoinThreads), 0, stream, true, c, a, rows, base, part_o, part_rl, info);
 }
 
 bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c) {
@@ -127,15 +135,19 @@ int attention_debug_set(int what, unsigned long long value) {
 
 // Two passes, each with the kernel that its rows per key/value head call for: over the prefixes, whose readers' tokens are one
 // sequence that sees all of it (so a prefix is read once for all of them, and its rows fill the tiles), then over the
-// sequences' own tokens, whose ends add the first pass's rows.  The rows in between are fp32.
-cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, const KvBatch& c, const AttentionArgs& args, float* rows,
-                                    float* rows_lse, int n_sms, cudaStream_t stream) {
+// sequences' own tokens, whose ends add the first pass's rows.  The rows in between are fp32.  The second pass starts while the
+// first one ends (scratch of its own, and it waits for the first one's rows where it needs them): a block's way to its first
+// scores takes 6 us.
+cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, void* prefix_scratch, const KvBatch& c,
+                                    const AttentionArgs& args, float* rows, float* rows_lse, int n_sms, cudaStream_t stream) {
   AttentionArgs a = args;
-  a.extra = 1;
+  a.pass = 2;
   if (rows) {
     AttentionArgs p = a;
+    p.pass = 1;
     p.causal = p.window = 0;
     p.max_q = max_prefix_q;
+    p.scratch = prefix_scratch;
     p.out32 = rows;
     p.lse = rows_lse;
     p.lse_unit = 1.f;

@@ -86,44 +86,56 @@ struct Cfg {
   static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
 
+// What a (sequence, head) costs besides its tiles, in tiles, all of it at its first one: lengths, page table, queries and output take
+// 10,000 cycles, a tile 2,400.  Calls of two passes have short sequences behind a long prefix, and a run of nine
+// one-tile sequences took 59 us where nine tiles of two took 17.  (Calls of one pass are cut as they always were.)
+template <int kPass>
+constexpr int kOwnCost = kPass == 0 ? 0 : 4;
+
+__device__ __forceinline__ long long item_cost(int nt, int own) { return nt > 0 ? nt + own : 0; }
+// The first tile of an item that a run has which begins rel into the item's cost.
+__device__ __forceinline__ int first_tile_from(long long rel, int nt, int own) {
+  return rel <= 0 ? 0 : (int)min((long long)nt, max(own > 0 ? 1LL : 0LL, rel - own));
+}
+
 // A run of tiles of one (sequence, head): the tiles [i0, i1) of its nt.
 struct Segment {
-  int b, h, i0, i1;
+  int b, h, i0, i1, later;  // later: not the item that the block's run begins in
   SeqRange s;
   KeyRange r;
 };
 
-// Walks the segments of a block's run of tiles.
+// Walks the segments of a block's run: `left` of cost, from `rel` on in its first item.
+template <int kOwn>
 struct Walk {
   const KvBatch& c;
   const AttentionArgs& a;
   long long left;
-  int b, h, i;
-  __device__ Walk(const KvBatch& c_, const AttentionArgs& a_, long long n, int b_, int h_, int i_)
-      : c(c_), a(a_), left(n), b(b_), h(h_), i(i_) {}
+  int b, h, rel, later = 0;
+  __device__ Walk(const KvBatch& c_, const AttentionArgs& a_, long long n, int b_, int h_, int rel_)
+      : c(c_), a(a_), left(n), b(b_), h(h_), rel(rel_) {}
   __device__ bool next(Segment& g) {
     while (left > 0 && b < c.B) {
       const bool ok = load_seq(c, b, g.s);
       g.r = key_range(g.s, a);
       if (!ok || g.r.nt == 0) {
         ++b;
-        h = i = 0;
+        h = rel = 0;
         continue;
       }
       g.b = b;
       g.h = h;
-      g.i0 = i;
-      g.i1 = (int)min((long long)g.r.nt, i + left);
-      left -= g.i1 - i;
-      i = g.i1;
-      if (i == g.r.nt) {
-        i = 0;
-        if (++h == c.Hkv) {
-          h = 0;
-          ++b;
-        }
+      g.i0 = first_tile_from(rel, g.r.nt, kOwn);
+      g.i1 = first_tile_from(rel + left, g.r.nt, kOwn);
+      g.later = later;
+      left -= g.r.nt + kOwn - rel;
+      rel = 0;
+      later = 1;
+      if (++h == c.Hkv) {
+        h = 0;
+        ++b;
       }
-      return true;
+      if (g.i0 < g.i1) return true;
     }
     return false;
   }
@@ -134,9 +146,9 @@ __device__ __forceinline__ int seq_tiles(const KvBatch& c, const AttentionArgs& 
   return load_seq(c, b, s) ? key_range(s, a).nt : 0;
 }
 
-// Tiles per block: equal runs over the grid.
-__device__ __forceinline__ long long tiles_per_block(long long n, int blocks) {
-  return max((long long)kMinRun, (n + blocks - 1) / blocks);
+// Cost per block: equal runs over the grid.  (A run that begins within an item has a tile of it: the joins count on that.)
+__device__ __forceinline__ long long cost_per_block(long long n, int blocks, int own) {
+  return max((long long)max(kMinRun, own + 2), (n + blocks - 1) / blocks);
 }
 
 // acc[x] += column x + column `lo` + x of this thread's tensor-memory lane.
@@ -210,7 +222,7 @@ __device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, ui
   lo = e4m3x2((a - h.x) * kLoUp, (b - h.y) * kLoUp);
 }
 
-template <int NC, bool kExtra>
+template <int NC, int kPass>
 __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     attention_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const KvBatch c, const AttentionArgs a, int split, float* part_o, float2* part_rl,
@@ -243,51 +255,58 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = c.Hq / c.Hkv;
+  constexpr int kOwn = kOwnCost<kPass>;
   pdl_launch_dependents();
   if (blockIdx.x == 0 && tid == C::kThreads - 1) check_starts(c);
 
   // ---- this block's run of tiles
   long long run = 0;
-  int slot0 = 2 * (int)blockIdx.x;
   if (split) {
     long long mine, total;
     // the scan's scratch is the weights' operand, free until the roles start
     long long* s_warp = reinterpret_cast<long long*>(smem + C::kPOff);
-    const long long before = scan_batch(c, C::kThreads, s_warp, mine, total, [&](int b) { return seq_tiles(c, a, b); });
-    const long long all = total * c.Hkv, per = tiles_per_block(all, gridDim.x);
+    const long long before = scan_batch(c, C::kThreads, s_warp, mine, total, [&](int b) { return item_cost(seq_tiles(c, a, b), kOwn); });
+    const long long all = total * c.Hkv, per = cost_per_block(all, gridDim.x, kOwn);
     const long long begin = (long long)blockIdx.x * per;
     run = min(per, all - begin);
     if (run <= 0) {
       if (tid == 0) info[blockIdx.x].split = 0;
+      if (kPass == 2) pdl_wait();  // this pass does not end before the one that it may overlap
       return;
     }
     if (before * c.Hkv <= begin && begin < (before + mine) * c.Hkv) {
       long long at = before;
       int b = tid * ((c.B + C::kThreads - 1) / C::kThreads), nt;
-      while ((at + (nt = seq_tiles(c, a, b))) * c.Hkv <= begin) {
-        at += nt;
+      while ((at + item_cost(nt = seq_tiles(c, a, b), kOwn)) * c.Hkv <= begin) {
+        at += item_cost(nt, kOwn);
         ++b;
       }
-      const long long rel = begin - at * c.Hkv;
+      const int cost = nt + kOwn;
+      const long long rel = (begin - at * c.Hkv) % cost;
       s_begin[0] = b;
-      s_begin[1] = (int)(rel / nt);
-      s_begin[2] = (int)(rel % nt);
+      s_begin[1] = (int)((begin - at * c.Hkv) / cost);
+      s_begin[2] = (int)rel;
+      // does this run begin inside an item, with a part of it that is not its first?
       JoinInfo j = {};
-      j.split = s_begin[2] != 0;
+      const int i0 = first_tile_from(rel, nt, kOwn);
+      j.split = i0 > 0 && i0 < nt;
       if (j.split) {
-        const long long i0 = begin - s_begin[2];
+        const long long start = begin - rel;
         j.b = b;
         j.h = s_begin[1];
-        j.c0 = (int)(i0 / per);
-        j.c1 = (int)((i0 + nt - 1) / per);
-        j.slot0 = i0 > j.c0 * per ? 1 : 0;
+        j.c0 = (int)(start / per);
+        j.c1 = (int)((start + cost - 1) / per);
+        j.slot0 = start > j.c0 * per ? 1 : 0;
       }
       info[blockIdx.x] = j;
     }
   } else {
     const int b = (int)blockIdx.x / c.Hkv;
-    run = seq_tiles(c, a, b);
-    if (run <= 0) return;
+    run = item_cost(seq_tiles(c, a, b), kOwn);
+    if (run <= 0) {
+      if (kPass == 2) pdl_wait();
+      return;
+    }
     if (tid == 0) {
       s_begin[0] = b;
       s_begin[1] = (int)blockIdx.x - b * c.Hkv;
@@ -327,7 +346,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk walk(c, a, run, s_begin[0], s_begin[1], s_begin[2]);
+  Walk<kOwn> walk(c, a, run, s_begin[0], s_begin[1], s_begin[2]);
   Segment g;
 
   if (warp == C::kTmaWarp) {
@@ -416,7 +435,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     bool ok = true, more = walk.next(g);
     int i = more ? g.i0 : 0;
 #pragma unroll 1
-    for (long long x = -1; ok && x < run; ++x) {
+    for (long long x = -1; ok && (more || x < (long long)n); ++x) {
       if (more) {
         const int st = (int)(n % C::kStages), qb = (int)(segs % C::kQBufs), sb = (int)(n & 1u);
         if (i == g.i0) ok = warp_wait(&q_full[qb], (segs / C::kQBufs) & 1u, abort_flag, c.status);
@@ -665,6 +684,20 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&p_full[n & 1u]);
       }
+      const bool complete = g.i0 == 0 && g.i1 == g.r.nt;
+      const int cols = min(NC, rows * G);
+      auto row_of = [&](int col) { return (size_t)(g.s.t0 + col / G) * c.Hq + g.h * G + col % G; };
+      float before[N], prior[N];  // of the pass before, on their way while the last sums are waited for
+      if (kPass == 2 && complete) {
+        pdl_wait();
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+          const int col = col0 + x;
+          const bool has = a.prior && col < cols;
+          before[x] = has ? prior_lse(a, row_of(col)) : -CUDART_INF_F;
+          prior[x] = has ? a.prior[row_of(col) * kHeadDim + key] : 0.f;
+        }
+      }
       if (ok) ok = warp_wait(&o_full[(n - 1u) & 1u], ((n - 1u) >> 1) & 1u, abort_flag, c.status);
       float acc[N];
 #pragma unroll
@@ -689,9 +722,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       }
       group_sync();
       if (s_bad[2]) break;
-      const bool complete = g.i0 == 0 && g.i1 == g.r.nt;
-      const int slot = slot0 + (g.i0 == 0 && segs > 0 ? 1 : 0);
-      const int cols = min(NC, rows * G);
+      const int slot = 2 * (int)blockIdx.x + g.later;
 #pragma unroll
       for (int x = 0; x < N; ++x) {
         const float4 m = *reinterpret_cast<const float4*>(sums + x * 4);
@@ -699,13 +730,12 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         const int col = col0 + x;
         if (col < cols) {
           if (complete) {
-            const int i = col / G;
-            const size_t at = (size_t)(g.s.t0 + i) * c.Hq + g.h * G + col - i * G;
-            if (kExtra) {
-              const RowEnd e = end_row(a, at, sum != 0.f ? 1.f / sum : 0.f, r[x] - kBase, sum, key == 0);
+            const size_t at = row_of(col);
+            if (kPass > 0) {
+              const RowEnd e = end_row<kPass>(a, at, sum != 0.f ? 1.f / sum : 0.f, r[x] - kBase, sum, before[x], key == 0);
               float o = acc[x] * e.f;
-              if (a.prior) o = fmaf(a.prior[at * kHeadDim + key], e.f1, o);
-              if (a.out32) a.out32[at * kHeadDim + key] = o;
+              if (kPass == 2 && a.prior) o = fmaf(prior[x], e.f1, o);
+              if (kPass == 1) a.out32[at * kHeadDim + key] = o;
               else a.out[at * kHeadDim + key] = f32_to_bf16_rne(o);
             } else {
               a.out[at * kHeadDim + key] = f32_to_bf16_rne(sum != 0.f ? acc[x] / sum : 0.f);
@@ -719,6 +749,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       ++segs;
     }
   }
+  if (kPass == 2) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == C::kMmaWarp) {
@@ -731,12 +762,12 @@ int width_of(int cols) { return cols <= 8 ? 8 : 16; }
 
 int blocks_of(int n_sms) { return 2 * n_sms; }
 
-template <int NC, bool kExtra>
+template <int NC, int kPass>
 cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
   using C = Cfg<NC>;
   CUtensorMap tk, tv;
   if (!make_cache_map(&tk, c.k_codes, c) || !make_cache_map(&tv, c.v_codes, c)) return cudaErrorInvalidValue;
-  auto kern = attention_decode_kernel<NC, kExtra>;
+  auto kern = attention_decode_kernel<NC, kPass>;
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::kBytes, allowed);
   if (e != cudaSuccess) return e;
@@ -746,7 +777,7 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   float* part_o = reinterpret_cast<float*>(a.scratch);
   float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)2 * blocks_of(n_sms) * NC * kHeadDim);
   JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)2 * blocks_of(n_sms) * NC);
-  e = launch_kernel(kern, dim3(blocks), dim3(C::kThreads), C::kBytes, stream, false, tk, tv, c, a, (int)split, part_o, part_rl,
+  e = launch_kernel(kern, dim3(blocks), dim3(C::kThreads), C::kBytes, stream, a.prior != nullptr, tk, tv, c, a, (int)split, part_o, part_rl,
                     info);
   if (e != cudaSuccess || !split) return e;
   return launch_attention_join(c, a, blocks, NC, kBase, part_o, part_rl, info, stream);
@@ -763,8 +794,9 @@ size_t attention_decode_scratch(int G, int max_q, int n_sms) {
 
 cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
   const bool narrow = width_of(c.Hq / c.Hkv * a.max_q) == 8;
-  if (a.extra) return narrow ? launch<8, true>(c, a, n_sms, stream) : launch<16, true>(c, a, n_sms, stream);
-  return narrow ? launch<8, false>(c, a, n_sms, stream) : launch<16, false>(c, a, n_sms, stream);
+  if (a.pass == 0) return narrow ? launch<8, 0>(c, a, n_sms, stream) : launch<16, 0>(c, a, n_sms, stream);
+  if (a.pass == 1) return narrow ? launch<8, 1>(c, a, n_sms, stream) : launch<16, 1>(c, a, n_sms, stream);
+  return narrow ? launch<8, 2>(c, a, n_sms, stream) : launch<16, 2>(c, a, n_sms, stream);
 }
 
 }  // namespace moe

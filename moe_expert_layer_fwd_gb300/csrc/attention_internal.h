@@ -61,11 +61,11 @@ struct AttentionArgs {
   int withhold;               // failure injection (tests only): the values' copies are not issued, so that waits run out
   void* scratch;              // after the status word of the workspace
   // Attention in two passes over different keys: the first leaves out32 and lse, the second takes them as its prior and
-  // writes the rows of both.  All NULL, extra = 0: neither.
-  int extra;
+  // writes the rows of both.
+  int pass;                   // 0: a call of its own, with rows only; 1: the first; 2: the second, or a call of its own with lse
   const float* prior;         // [T, Hq, 128] rows of the pass before, and
   const float* prior_lse;     // [T, Hq] the logarithms (base 2) of their denominators; NULL: no pass before
-  float* out32;               // the rows go here, in fp32, instead of out
+  float* out32;               // pass 1: the rows go here, in fp32, instead of out
   float* lse;                 // [T, Hq] or NULL: lse_unit times the logarithm (base 2) of the rows' denominators (-inf: nothing seen)
   float lse_unit;
 };
@@ -74,8 +74,8 @@ cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int
 
 // Sequences b of `prefixes` are the prefixes, its q_start cuts the T tokens into their readers; rows [T, Hq, 128] and rows_lse
 // [T, Hq]: what is passed from the first pass to the second (NULL: no prefixes).
-cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, const KvBatch& c, const AttentionArgs& a, float* rows,
-                                    float* rows_lse, int n_sms, cudaStream_t stream);
+cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, void* prefix_scratch, const KvBatch& c,
+                                    const AttentionArgs& a, float* rows, float* rows_lse, int n_sms, cudaStream_t stream);
 
 
 // Failure injection (tests only): what 1 = wait limit in ns (0: the default 2 s), what 4 = nonzero: withhold the values'

@@ -242,11 +242,6 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 // The lowest n bits (none for n <= 0, all from 32 on).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
   return (uint32_t)h.x | (uint32_t)h.y << 16;
@@ -266,17 +261,6 @@ __device__ __forceinline__ float max16(const uint32_t* v) {
     t1 = max3(t1, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
   }
   return fmaxf(max3(t0, __uint_as_float(v[14]), __uint_as_float(v[15])), t1);
-}
-
-// Two bf16 numbers times inv as split_e4m3x2 does it, by way of f16: 8 bits below 2^9 are exact there down to 2^-16, and
-// what is smaller has two halves of zero.
-__device__ __forceinline__ void split_bf16x2(uint32_t w, float inv, uint32_t& hi, uint32_t& lo) {
-  __half2_raw v, h;
-  *reinterpret_cast<uint32_t*>(&v) = pack_f16x2(bf16_lo(w) * inv, bf16_hi(w) * inv);
-  hi = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-  h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3);
-  h = __hsub2(__half2(v), __half2(h));
-  lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
 }
 
 // The larger bf16 magnitudes of pairs.
@@ -300,7 +284,7 @@ __device__ __forceinline__ void rescale_lane64(uint32_t taddr, float f) {
   }
 }
 
-template <bool kSplit, bool kExtra>
+template <bool kSplit, int kPass>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                              const KvBatch c, const AttentionArgs a, float* part_o, float2* part_rl, JoinInfo* info) {
@@ -367,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     run = min(share, all - begin);
     if (run <= 0) {
       if (tid == 0) info[blockIdx.x].split = 0;
+      if (kPass == 2) pdl_wait();  // this pass does not end before the one that it may overlap
       return;
     }
     if (before * c.Hkv <= begin && begin < (before + mine) * c.Hkv) {
@@ -626,10 +611,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && next->nt) fetch_queries(*next);
       }
       // ---- the rows' outputs
+      const bool complete = g.i0 == 0 && g.i1 == g.nt;
+      float before = -CUDART_INF_F;  // of the pass before, on its way while the last sums are waited for
+      if (kPass == 2) pdl_wait();
+      if (kPass == 2 && complete && live) before = prior_lse(a, (size_t)(g.t0 + i_row) * c.Hq + head);
+      RowEnd e = {};
       ok = ok && warp_wait(&o_full[mt], (steps - 1u) & 1u, abort_flag, c.status);
       if (!ok) break;
       tc_fence_after();
-      const bool complete = g.i0 == 0 && g.i1 == g.nt;
       const size_t part = (size_t)(2 * (int)blockIdx.x + g.later) * kRows + (kSplit ? 0 : mt * kM) + row;
       uint16_t* out = a.out + ((size_t)(g.t0 + i_row) * c.Hq + head) * kHeadDim;
       // kSplit: M tile 1 puts its r and l, and its sums in two halves of the dims, where the queries were once both tiles'
@@ -644,18 +633,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kSplit && mt == 1) *other_rl = make_float2(r, l);
       auto write = [&](int d, const float (&o)[32], float inv) {  // dims d .. d + 31 of this row
         if (complete) {
-          if (kExtra && live) {
+          if (kPass > 0 && live) {
             const size_t at = (size_t)(g.t0 + i_row) * c.Hq + head;
-            const RowEnd e = end_row(a, at, inv, r - kBase, l, d == 0);
+            if (d == 0) e = end_row<kPass>(a, at, inv, r - kBase, l, before, true);
 #pragma unroll
-            for (int y = 0; y < 32; y += 4) {
-              float4 v = make_float4(o[y] * e.f, o[y + 1] * e.f, o[y + 2] * e.f, o[y + 3] * e.f);
-              if (a.prior) {
-                const float4 p = *reinterpret_cast<const float4*>(a.prior + at * kHeadDim + d + y);
-                v = make_float4(fmaf(p.x, e.f1, v.x), fmaf(p.y, e.f1, v.y), fmaf(p.z, e.f1, v.z), fmaf(p.w, e.f1, v.w));
+            for (int y0 = 0; y0 < 32; y0 += 16) {
+              float4 prior[4];  // loads before stores, which they cannot pass
+              if (kPass == 2 && a.prior) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) prior[y] = reinterpret_cast<const float4*>(a.prior + at * kHeadDim + d + y0)[y];
               }
-              if (a.out32) *reinterpret_cast<float4*>(a.out32 + at * kHeadDim + d + y) = v;
-              else *reinterpret_cast<uint2*>(out + d + y) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float* w = o + y0 + 4 * y;
+                float4 v = make_float4(w[0] * e.f, w[1] * e.f, w[2] * e.f, w[3] * e.f);
+                if (kPass == 2 && a.prior)
+                  v = make_float4(fmaf(prior[y].x, e.f1, v.x), fmaf(prior[y].y, e.f1, v.y), fmaf(prior[y].z, e.f1, v.z),
+                                  fmaf(prior[y].w, e.f1, v.w));
+                if (kPass == 1) reinterpret_cast<float4*>(a.out32 + at * kHeadDim + d + y0)[y] = v;
+                else reinterpret_cast<uint2*>(out + d + y0)[y] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+              }
             }
           } else if (live) {
 #pragma unroll
@@ -949,6 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(done, 0, abort_flag, 1000ull * a.limit_us, c.status, false);
     }
   }
+  if (kPass == 2) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -957,19 +955,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool kSplit, bool kExtra>
+template <bool kSplit, int kPass>
 cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
   using C = Cfg<kSplit>;
   CUtensorMap tk, tv;
   if (!make_cache_map(&tk, c.k_codes, c) || !make_cache_map(&tv, c.v_codes, c)) return cudaErrorInvalidValue;
-  auto kern = attention_prefill_kernel<kSplit, kExtra>;
+  auto kern = attention_prefill_kernel<kSplit, kPass>;
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::kBytes, allowed);
   if (e != cudaSuccess) return e;
   float* part_o = reinterpret_cast<float*>(a.scratch);
   float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)n_sms * 2 * C::kRows * kHeadDim);
   JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)n_sms * 2 * C::kRows);
-  e = launch_kernel(kern, dim3(n_sms), dim3(kThreads), C::kBytes, stream, false, tk, tv, c, a, part_o, part_rl, info);
+  e = launch_kernel(kern, dim3(n_sms), dim3(kThreads), C::kBytes, stream, a.prior != nullptr, tk, tv, c, a, part_o, part_rl, info);
   if (e != cudaSuccess) return e;
   return launch_attention_join(c, a, n_sms, C::kRows, kBase, part_o, part_rl, info, stream);
 }
@@ -986,8 +984,9 @@ size_t attention_prefill_scratch(int G, int max_q, int n_sms) {
 
 cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
   const bool split = splits_keys(c.Hq / c.Hkv, a.max_q);
-  if (a.extra) return split ? launch<true, true>(c, a, n_sms, stream) : launch<false, true>(c, a, n_sms, stream);
-  return split ? launch<true, false>(c, a, n_sms, stream) : launch<false, false>(c, a, n_sms, stream);
+  if (a.pass == 0) return split ? launch<true, 0>(c, a, n_sms, stream) : launch<false, 0>(c, a, n_sms, stream);
+  if (a.pass == 1) return split ? launch<true, 1>(c, a, n_sms, stream) : launch<false, 1>(c, a, n_sms, stream);
+  return split ? launch<true, 2>(c, a, n_sms, stream) : launch<false, 2>(c, a, n_sms, stream);
 }
 
 }  // namespace moe

@@ -182,17 +182,20 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
-// How a row of a call with `extra` is finished.  The row's own part is o = f o' of o' unscaled sums with the denominator l = sum of
+// How a row of a call in one of two passes is finished.  The row's own part is o = f o' of o' unscaled sums with the denominator l = sum of
 // 2^(u - r) (f = 1 / l, 0 for a row that sees nothing); L = r + log2 l.  With L1 of the pass before and M = max(L, L1):
 //   out = (2^(L - M) o + 2^(L1 - M) prior) / (2^(L - M) + 2^(L1 - M)),   lse = M + log2 of that sum
 struct RowEnd {
   float f, f1;  // out = f o' + f1 prior
 };
-__device__ __forceinline__ RowEnd end_row(const AttentionArgs& a, size_t row, float f, float r, float l, bool writes_lse) {
+// (before: L1, -infinity without a pass before; the caller has it early, a load takes longer than the rest)
+__device__ __forceinline__ float prior_lse(const AttentionArgs& a, size_t row) { return a.prior ? a.prior_lse[row] : -CUDART_INF_F; }
+template <int kPass>
+__device__ __forceinline__ RowEnd end_row(const AttentionArgs& a, size_t row, float f, float r, float l, float before, bool writes_lse) {
   RowEnd e = {f, 0.f};
   float lse = r + log2f(l);
-  if (a.prior) {
-    const float before = a.prior_lse[row], top = fmaxf(lse, before), ref = top == -CUDART_INF_F ? 0.f : top;
+  if (kPass == 2 && a.prior) {
+    const float top = fmaxf(lse, before), ref = top == -CUDART_INF_F ? 0.f : top;
     const float w = ex2(lse - ref), w1 = ex2(before - ref), sum = w + w1, inv = sum != 0.f ? 1.f / sum : 0.f;
     e.f = f * w * inv;
     e.f1 = w1 * inv;
@@ -216,6 +219,11 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t x, uint64_t y, uint64_t z
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
   return d;
 }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t x, uint64_t y) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t x, uint64_t y) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
@@ -233,6 +241,23 @@ __device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uin
   hi = e4m3x2(a, b);
   const float2 h = e4m3x2_f32(hi);
   lo = e4m3x2(a - h.x, b - h.y);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// Two bf16 numbers times inv as split_e4m3x2 does it, by way of f16: 8 bits below 2^9 are exact there down to 2^-16, and
+// what is smaller has two halves of zero.
+__device__ __forceinline__ void split_bf16x2(uint32_t w, float inv, uint32_t& hi, uint32_t& lo) {
+  __half2_raw v, h;
+  *reinterpret_cast<uint32_t*>(&v) = pack_f16x2(bf16_lo(w) * inv, bf16_hi(w) * inv);
+  hi = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+  h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3);
+  h = __hsub2(__half2(v), __half2(h));
+  lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
 }
 
 }  // namespace moe

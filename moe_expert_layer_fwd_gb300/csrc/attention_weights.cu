@@ -10,14 +10,15 @@
 // Rows beyond NC are taken in chunks: a block keeps kStages tiles of keys in shared memory and walks the chunks over them, so that a
 // chunk's conversion to E4M3 serves that many tiles.
 //
-// Work: all (sequence, head, tile) in one order, a tile costing its sequence's chunks, cut into equal runs, one per block (two blocks
-// per SM).  The sums of a key are one thread's in a fixed order: the same inputs give the same bits.
+// Work: all (sequence, head, tile) in one order, a tile costing its sequence's chunks, cut into equal runs, one per block.  The sums of a key are one thread's in a fixed order: the same inputs give the same bits.
 //
 // What bounds it: few rows, the bytes of the keys; many, exponentials (32 a cycle and SM) and the products, which take the same
 // 256 cycles for a tile and 64 rows.
 //
-// Warps: 8 softmax (four for the even tiles of a group, four for the odd), TMA, MMA, then queries.  Every wait is bounded (2 s).
+// Warps: softmax (groups of four, which take the tiles in turn), TMA, MMA, then queries.  Every wait is bounded (2 s).
 #include "attention_tiles.cuh"
+
+#include <limits.h>
 
 namespace moe {
 namespace {
@@ -27,33 +28,40 @@ struct TileInfo {    // per 16 keys of a tile
   int page[8];       // -1: none
 };
 
-struct RowInfo {     // a query row: its score is S * qf, its weight 2^(S qf kf - lse2)
-  float qf, lse2;
+struct RowPair {     // two query rows: a weight is 2^(S kf qf + minus)
+  float qf[2], minus[2];  // minus = -lse2
+};
+struct RowSeen {     // the keys lo .. lo + span that a row sees
+  int lo;
+  unsigned span;
 };
 
 template <int NC>
 struct Cfg {
   static constexpr bool kWide = NC > 16;                    // hi and lo products in the same columns (else side by side: half
                                                             // the instructions, which small ones are bound by)
-  static constexpr int kStages = kWide ? 4 : 6;             // tiles of keys
+  static constexpr int kPerSm = kWide ? 1 : 2;              // blocks
+  static constexpr int kStages = kWide ? 8 : 6;             // tiles of keys
+  static constexpr int kGroups = 2, kSBufs = 2 * kGroups;   // groups of four softmax warps, and buffers of scores
   static constexpr int kQBufs = 2;
   static constexpr int kQWarps = kWide ? 4 : 1;
-  static constexpr int kSoftWarps = 8;
+  static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kQWarp = kSoftWarps + 2;
   static constexpr int kThreads = 32 * (kQWarp + kQWarps);
   static constexpr int kQBytes = 2 * NC * 128;
   static constexpr int kQOff = kStages * kTileBytes;
   static constexpr int kBarOff = kQOff + kQBufs * kQBytes;
-  static constexpr int kNumBars = 3 * kStages + 2 * kQBufs + 5;
+  static constexpr int kNumBars = 3 * kStages + 2 * kQBufs + 2 * kSBufs + 1;
   static constexpr int kInfoOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;           // TileInfo [kStages]
-  static constexpr int kRowOff = kInfoOff + kStages * (int)sizeof(TileInfo);         // RowInfo [kQBufs][NC]
-  static constexpr int kPosOff = kRowOff + kQBufs * NC * (int)sizeof(RowInfo);       // int [kQBufs][NC]
-  static constexpr int kAccOff = kPosOff + kQBufs * NC * 4;                          // float [kStages][128]
+  static constexpr int kRowOff = kInfoOff + kStages * (int)sizeof(TileInfo);         // RowPair [kQBufs][NC / 2]
+  static constexpr int kSeenOff = kRowOff + kQBufs * NC / 2 * (int)sizeof(RowPair);  // RowSeen [kQBufs][NC]
+  static constexpr int kAllOff = kSeenOff + kQBufs * NC * (int)sizeof(RowSeen);      // int2 [kQBufs]
+  static constexpr int kAccOff = kAllOff + kQBufs * (int)sizeof(int2);               // float [kStages][128]
   static constexpr int kMiscOff = kAccOff + (kWide ? kStages * kTile * 4 : 0);
   static constexpr int kBytes = 1024 + kMiscOff + 32;
   static constexpr int kSCols = kWide ? NC : 2 * NC;
-  static constexpr int kTmemCols = 2 * kSCols;              // a power of two, at least 32
-  static_assert(2 * (kBytes + 1024) <= 228 * 1024, "shared memory");
+  static constexpr int kTmemCols = kSBufs * kSCols;         // a power of two, at least 32
+  static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory");
   static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
 };
 
@@ -118,18 +126,67 @@ __device__ __forceinline__ void chunks_of(const Segment& g, const AttentionArgs&
   c0 = 0;
   c1 = g.chunks - 1;
   if (g.chunks == 1) return;
-  const int first = g.s.first(), last = g.s.t1 - g.s.t0 - 1;  // rows i of positions first + i
-  if (a.causal) c0 = (int)((long long)min(max(0, j0 - first), last) * G / nc);
+  const int first = g.s.first(), last = g.s.t1 - g.s.t0 - 1;  // new token i has position first + i; rows are below 2^31
+  if (a.causal) c0 = (int)((unsigned)(min(max(0, j0 - first), last) * G) / (unsigned)nc);
   if (a.window > 0) {
-    // row i sees keys from first + i - window + 1 on: the last row that sees j1 - 1
+    // token i sees keys from first + i - window + 1 on: the last one that sees j1 - 1
     const long long i = (long long)j1 - 1 - first + a.window - 1;
-    c1 = (int)(((i < 0 ? 0 : i > last ? last : i) * G + G - 1) / nc);
+    c1 = (int)((unsigned)((i < 0 ? 0 : i > last ? last : (int)i) * G + G - 1) / (unsigned)nc);
     c1 = max(c0, min(c1, g.chunks - 1));
   }
 }
 
+// A key's weights of a chunk's rows, from its lane of tensor memory; frees the scores once they are in registers.
+template <int NC, bool kMasked>
+__device__ __forceinline__ float add_weights(uint32_t taddr, const RowPair* row, const RowSeen* seen, float ks, int j, uint64_t* s_empty,
+                                             int lane) {
+  constexpr int P = Cfg<NC>::kWide ? 32 : 8, kSteps = NC / P;  // columns at a time: the next ones come while these are added up
+  const uint64_t ks2 = f32x2(ks, ks);
+  uint64_t sum = 0;
+  uint32_t v[2][P], w[2][P];
+  auto load = [&](int k) {
+    if constexpr (Cfg<NC>::kWide) {
+      tmem_ld32_async(taddr + k * P, v[k & 1]);
+    } else {
+      tmem_ld_async(taddr + k * P, v[k & 1]);
+      tmem_ld_async(taddr + NC + k * P, w[k & 1]);
+    }
+  };
+  load(0);
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    tmem_wait_ld();
+    if (k + 1 < kSteps) {
+      load(k + 1);
+    } else {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_empty);
+    }
+    float s[P];
+#pragma unroll
+    for (int x = 0; x < P; ++x)
+      s[x] = Cfg<NC>::kWide ? __uint_as_float(v[k & 1][x]) : __uint_as_float(v[k & 1][x]) + __uint_as_float(w[k & 1][x]);
+#pragma unroll
+    for (int x = 0; x < P; x += 2) {
+      const float4 r = *reinterpret_cast<const float4*>(row + (k * P + x) / 2);
+      float z0, z1;
+      f32x2_split(fma_f32x2(mul_f32x2(f32x2(s[x], s[x + 1]), ks2), f32x2(r.x, r.y), f32x2(r.z, r.w)), z0, z1);
+      if (kMasked) {
+        const int4 see = *reinterpret_cast<const int4*>(seen + k * P + x);
+        if ((unsigned)(j - see.x) > (unsigned)see.y) z0 = -CUDART_INF_F;
+        if ((unsigned)(j - see.z) > (unsigned)see.w) z1 = -CUDART_INF_F;
+      }
+      sum = add_f32x2(sum, f32x2(ex2(z0), ex2(z1)));
+    }
+  }
+  float s0, s1;
+  f32x2_split(sum, s0, s1);
+  return s0 + s1;
+}
+
 template <int NC>
-__global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
+__global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     kv_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const KvBatch c, const AttentionArgs a, const float* lse,
                       const float* weight_in, float* weight_out) {
   using C = Cfg<NC>;
@@ -140,12 +197,13 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
   uint64_t* i_full = k_empty + C::kStages;
   uint64_t* q_full = i_full + C::kStages;
   uint64_t* q_empty = q_full + C::kQBufs;
-  uint64_t* s_full = q_empty + C::kQBufs;   // [2]
-  uint64_t* s_empty = s_full + 2;           // [2]
-  uint64_t* done = s_empty + 2;
+  uint64_t* s_full = q_empty + C::kQBufs;   // [kSBufs]: a group's in turn
+  uint64_t* s_empty = s_full + C::kSBufs;   // [kSBufs]
+  uint64_t* done = s_empty + C::kSBufs;
   TileInfo* infos = reinterpret_cast<TileInfo*>(smem + C::kInfoOff);
-  RowInfo* s_row = reinterpret_cast<RowInfo*>(smem + C::kRowOff);
-  int* s_pos = reinterpret_cast<int*>(smem + C::kPosOff);
+  RowPair* s_row = reinterpret_cast<RowPair*>(smem + C::kRowOff);
+  int2* s_all = reinterpret_cast<int2*>(smem + C::kAllOff);  // keys [x, y) are seen by every row of the chunk
+  RowSeen* s_seen = reinterpret_cast<RowSeen*>(smem + C::kSeenOff);
   float* s_acc = reinterpret_cast<float*>(smem + C::kAccOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
@@ -191,7 +249,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
       mbar_init(&q_full[i], C::kQWarps);
       mbar_init(&q_empty[i], 1 + C::kSoftWarps);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kSBufs; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 4);
     }
@@ -267,38 +325,42 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
     }
     __syncwarp();
   } else if (warp == C::kMmaWarp) {
-    // ------------------------------------------------------------ MMA: the whole warp walks along and one lane issues
+    // ------------------------------------------------------------ MMA: the whole warp walks along and one lane issues;
+    // bounds by shuffle, so that loops and descriptors are the warp's and not a lane's
     const uint32_t idesc = umma_idesc_e4m3(kTile, C::kSCols, false, false);
     const uint64_t desc = umma_desc_sw128(smem_u32(smem));
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    uint32_t n = 0, fills = 0, used[2] = {0, 0};  // tiles of earlier groups; query buffers; uses of the score buffers
+    uint32_t n = 0, fills = 0, used[2] = {0, 0};  // tiles of earlier groups; query buffers; tiles given to a group of warps
     bool ok = true;
     while (ok && walk.next(g)) {
-      if (g.chunks == 1) {
+      const int i0 = __shfl_sync(0xffffffffu, g.i0, 0), i1 = __shfl_sync(0xffffffffu, g.i1, 0), chunks = __shfl_sync(0xffffffffu, g.chunks, 0);
+      if (chunks == 1) {
         ok = warp_wait(&q_full[fills % C::kQBufs], (fills / C::kQBufs) & 1u, abort_flag, c.status);
         ++fills;
       }
 #pragma unroll 1
-      for (int i = g.i0; ok && i < g.i1; i += C::kStages) {
-        const int nt = min(C::kStages, g.i1 - i), j0 = (g.r.tile0 + i) * kTile;
+      for (int i = i0; ok && i < i1; i += C::kStages) {
+        const int nt = min(C::kStages, i1 - i), j0 = (g.r.tile0 + i) * kTile;
         int c0, c1;
         chunks_of(g, a, G, NC, j0, j0 + nt * kTile, c0, c1);
+        c0 = __shfl_sync(0xffffffffu, c0, 0);
+        c1 = __shfl_sync(0xffffffffu, c1, 0);
 #pragma unroll 1
         for (int ch = c0; ok && ch <= c1; ++ch) {
-          if (g.chunks > 1) {
+          if (chunks > 1) {
             ok = warp_wait(&q_full[fills % C::kQBufs], (fills / C::kQBufs) & 1u, abort_flag, c.status);
             ++fills;
           }
           const int qb = (int)((fills - 1u) % C::kQBufs);
           const uint64_t bd = desc + (uint64_t)((C::kQOff + qb * C::kQBytes) >> 4);
-          const bool q_ends = g.chunks > 1 || i + nt == g.i1;
+          const bool q_ends = chunks > 1 || i + nt == i1;
 #pragma unroll 1
           for (int t = 0; ok && t < nt; ++t) {
             const uint32_t m = n + t;
-            const int st = (int)(m % C::kStages), sb = t & 1;
-            ok = warp_wait2(&k_full[st], (m / C::kStages) & 1u, &s_empty[sb], (used[sb] & 1u) ^ 1u, abort_flag, c.status);
+            const uint32_t u = t & 1 ? used[1]++ : used[0]++;
+            const int st = (int)(m % C::kStages), sb = (t & 1) * 2 + (int)(u & 1u);
+            ok = warp_wait2(&k_full[st], (m / C::kStages) & 1u, &s_empty[sb], ((u >> 1) & 1u) ^ 1u, abort_flag, c.status);
             if (!ok) break;
-            ++used[sb];
             tc_fence_after();
             const uint64_t ad = desc + (uint64_t)((st * kTileBytes) >> 4);
             if (elect_one()) {
@@ -330,69 +392,67 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
     uint32_t fills = 0;
     bool ok = true;
     auto fill = [&](int ch) {
-      const int qb = (int)(fills % C::kQBufs), first = g.s.first();
-      const long long rows = (long long)(g.s.t1 - g.s.t0) * G;
+      const int qb = (int)(fills % C::kQBufs), first = g.s.first(), rows = (g.s.t1 - g.s.t0) * G;
       uint8_t* op = smem + C::kQOff + qb * C::kQBytes;
 #pragma unroll 1
       for (int x0 = x_first; x0 < x_first + kMine; x0 += kAtOnce) {
+        const int rho0 = ch * NC + x0;
+        int i = rho0 / G, head = rho0 - i * G;
+        const uint16_t* src = a.q + (size_t)(g.s.t0 + i) * a.q_stride + (size_t)(g.h * G + head) * kHeadDim + lane * 4;
         uint2 raw[kAtOnce];
 #pragma unroll
         for (int x = 0; x < kAtOnce; ++x) {
-          const long long rho = (long long)ch * NC + x0 + x;
           raw[x] = make_uint2(0, 0);
-          if (rho < rows) {
-            const int i = (int)(rho / G), head = g.h * G + (int)(rho - (long long)i * G);
-            raw[x] = __ldg(reinterpret_cast<const uint2*>(a.q + (size_t)(g.s.t0 + i) * a.q_stride + (size_t)head * kHeadDim) + lane);
+          if (rho0 + x < rows) raw[x] = __ldg(reinterpret_cast<const uint2*>(src));
+          src += kHeadDim;
+          if (++head == G) {
+            head = 0;
+            src += a.q_stride - (long long)G * kHeadDim;
           }
         }
-        // lane x has the row x's denominator
-        float row_lse = CUDART_INF_F;
-        int pos = 0;
-        if (lane < kAtOnce) {
-          const long long rho = (long long)ch * NC + x0 + lane;
-          if (rho < rows) {
-            const int i = (int)(rho / G), head = g.h * G + (int)(rho - (long long)i * G);
-            const float v = __ldg(lse + (size_t)(g.s.t0 + i) * c.Hq + head) * 1.44269504088896341f;
-            if (fabsf(v) <= 3.402823466e38f) row_lse = v;  // a row that saw nothing, or whose denominator is no number, gives nothing
-            pos = first + i;
-          }
+        // lane x has row x's denominator
+        float minus = -CUDART_INF_F, qf = 0.f;
+        RowSeen seen = {INT_MAX, 0u};
+        if (lane < kAtOnce && rho0 + lane < rows) {
+          const int il = (rho0 + lane) / G;
+          const float v = __ldg(lse + (size_t)(g.s.t0 + il) * c.Hq + g.h * G + rho0 + lane - il * G) * 1.44269504088896341f;
+          if (fabsf(v) <= 3.402823466e38f) minus = -v;  // a row that saw nothing, or whose denominator is no number, gives nothing
+          const int pos = first + il;
+          if (!a.causal) seen = {0, INT_MAX};
+          else if (pos >= 0) seen = {window_lo(pos, a.window), (unsigned)(pos - window_lo(pos, a.window))};
         }
         if (x0 == x_first) {
           ok = warp_wait(&q_empty[qb], ((fills / C::kQBufs) & 1u) ^ 1u, abort_flag, c.status);
           if (!ok) return;
         }
-        float qf = 0.f;
 #pragma unroll
         for (int x = 0; x < kAtOnce; ++x) {
-          const float v[4] = {bf16_lo(raw[x].x), bf16_hi(raw[x].x), bf16_lo(raw[x].y), bf16_hi(raw[x].y)};
-          float top = 0.f;
-          bool bad = false;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float m = fabsf(v[e]);
-            bad |= !(m <= 3.402823466e38f);
-            top = fmaxf(top, m);
-          }
-          top = warp_max(top);
-          bad = __any_sync(0xffffffffu, bad);
-          const int e = bad ? 0 : query_exponent(top);
+          uint32_t top = __vmaxu2(raw[x].x & 0x7FFF7FFFu, raw[x].y & 0x7FFF7FFFu);  // bf16 magnitudes order as integers
+          top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+          const bool bad = top >= 0x7F80u;
+          const int e = bad ? 0 : query_exponent(__uint_as_float(top << 16));
           const float inv = exp2_int(-e);
           uint32_t h0, l0, h1, l1;
-          split_e4m3x2(v[0] * inv, v[1] * inv, h0, l0);
-          split_e4m3x2(v[2] * inv, v[3] * inv, h1, l1);
-          const uint32_t hi = bad ? 0u : h0 | (h1 << 16), lo = bad ? 0u : l0 | (l1 << 16);
+          split_bf16x2(bad ? 0u : raw[x].x, inv, h0, l0);
+          split_bf16x2(bad ? 0u : raw[x].y, inv, h1, l1);
           const uint32_t sw = ((((uint32_t)lane >> 2) ^ (x & 7)) << 4) + (lane & 3) * 4;
-          *reinterpret_cast<uint32_t*>(op + (x0 + x) * 128 + sw) = hi;
-          *reinterpret_cast<uint32_t*>(op + (NC + x0 + x) * 128 + sw) = lo;
+          *reinterpret_cast<uint32_t*>(op + (x0 + x) * 128 + sw) = h0 | (h1 << 16);
+          *reinterpret_cast<uint32_t*>(op + (NC + x0 + x) * 128 + sw) = l0 | (l1 << 16);
           if (lane == x) {
             qf = a.scale_log2 * exp2_int(e);
-            if (bad) row_lse = CUDART_INF_F;  // a row with an infinity or NaN has no weights
+            if (bad) minus = -CUDART_INF_F;  // a row with an infinity or NaN has no weights
           }
         }
         if (lane < kAtOnce) {
-          s_row[qb * NC + x0 + lane] = {qf, row_lse};
-          s_pos[qb * NC + x0 + lane] = pos;
+          RowPair& r = s_row[(qb * NC + x0 + lane) / 2];
+          r.qf[lane & 1] = qf;
+          r.minus[lane & 1] = minus;
+          s_seen[qb * NC + x0 + lane] = seen;
         }
+      }
+      if (x_first == 0 && lane == 0) {
+        const int pos_lo = first + ch * NC / G, pos_hi = first + min(rows - 1, ch * NC + NC - 1) / G;
+        s_all[qb] = make_int2(window_lo(pos_hi, a.window), a.causal ? pos_lo + 1 : INT_MAX);
       }
       fence_async_shared();
       __syncwarp();
@@ -414,14 +474,12 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
       }
     }
   } else {
-    // ------------------------------------------------------------ softmax: thread = key; a group of four warps has every other tile
+    // ------------------------------------------------------------ softmax: thread = key; a group of four warps has every kGroups-th tile
     const int group = warp >> 2, w4 = warp & 3, key = tid & 127;
-    const uint32_t mine = tmem + ((uint32_t)(w4 * 32) << 16) + group * C::kSCols;
+    const uint32_t mine = tmem + ((uint32_t)(w4 * 32) << 16);
     uint32_t n = 0, fills = 0, used = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
-      const int first = g.s.first();
-      const long long rows = (long long)(g.s.t1 - g.s.t0) * G;
       if (g.chunks == 1) {
         ok = warp_wait(&q_full[fills % C::kQBufs], (fills / C::kQBufs) & 1u, abort_flag, c.status);
         ++fills;
@@ -439,80 +497,42 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             ++fills;
           }
           const int qb = (int)((fills - 1u) % C::kQBufs);
-          const RowInfo* row = s_row + qb * NC;
-          const int* pos = s_pos + qb * NC;
-          const int pos_lo = first + (int)((long long)ch * NC / G);  // positions of the chunk's rows
-          const int pos_hi = first + (int)(min(rows, (long long)(ch + 1) * NC) - 1) / G;
+          const int2 all = s_all[qb];
 #pragma unroll 1
-          for (int t = group; t < nt; t += 2) {
+          for (int t = group; t < nt; t += C::kGroups) {
             const uint32_t m = n + t;
             const int st = (int)(m % C::kStages), j0 = jg + t * kTile, j = j0 + key;
-            ok = warp_wait(&i_full[st], (m / C::kStages) & 1u, abort_flag, c.status);
+            if (ch == c0) ok = warp_wait(&i_full[st], (m / C::kStages) & 1u, abort_flag, c.status);
             if (!ok) break;
             const float ks = infos[st].kf[key >> 4];
-            const int pg = infos[st].page[key >> 4];
             float acc = C::kWide && ch > c0 ? s_acc[st * kTile + key] : 0.f;
             // the key's weight so far, on its way while the scores are waited for
-            const bool ends = ch == c1, writes = ends && pg >= 0 && j >= g.r.lo && j < g.r.hi;
-            const size_t at = writes ? ((((size_t)pg * c.Hkv + g.h) << c.page_log2) + (j & (c.page - 1))) : 0;
+            const bool ends = ch == c1;
             float before = 0.f;
-            if (writes && weight_in && j < first) before = weight_in[at];
+            float* to = nullptr;
             if (ends) {
+              const int pg = infos[st].page[key >> 4];
+              if (pg >= 0 && j >= g.r.lo && j < g.r.hi) {
+                const size_t at = (((size_t)pg * c.Hkv + g.h) << c.page_log2) + (j & (c.page - 1));
+                to = weight_out + at;
+                if (weight_in && j < g.s.first()) before = weight_in[at];
+              }
               __syncwarp();
               if (lane == 0) mbar_arrive(&k_empty[st]);
             }
-            ok = warp_wait(&s_full[group], used & 1u, abort_flag, c.status);
+            const int sb = group * 2 + (int)(used & 1u);
+            ok = warp_wait(&s_full[sb], (used >> 1) & 1u, abort_flag, c.status);
             if (!ok) break;
             ++used;
             tc_fence_after();
-            const bool whole = (!a.causal || j0 + kTile - 1 <= pos_lo) && j0 >= window_lo(pos_hi, a.window);
-            constexpr int P = C::kWide ? 32 : 8;  // columns at a time
-#pragma unroll
-            for (int x0 = 0; x0 < NC; x0 += P) {
-              float s[P];
-              if constexpr (C::kWide) {
-                uint32_t v[32];
-                tmem_ld32_async(mine + x0, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int x = 0; x < P; ++x) s[x] = __uint_as_float(v[x]);
-              } else {
-                uint32_t v[8], w[8];
-                tmem_ld_async(mine + x0, v);
-                tmem_ld_async(mine + NC + x0, w);
-                tmem_wait_ld();
-#pragma unroll
-                for (int x = 0; x < P; ++x) s[x] = __uint_as_float(v[x]) + __uint_as_float(w[x]);
-              }
-              if (x0 + P == NC) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[group]);
-              }
-              const uint64_t ks2 = f32x2(ks, ks);
-              uint64_t sum = 0;
-#pragma unroll
-              for (int x = 0; x < P; x += 2) {
-                const float4 r = *reinterpret_cast<const float4*>(row + x0 + x);  // qf, lse2 of two rows
-                float z0, z1;
-                uint64_t u;
-                asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(u) : "l"(f32x2(s[x], s[x + 1])), "l"(ks2));
-                f32x2_split(fma_f32x2(u, f32x2(r.x, r.z), f32x2(-r.y, -r.w)), z0, z1);
-                if (!whole) {
-                  const int2 ps = *reinterpret_cast<const int2*>(pos + x0 + x);
-                  if ((a.causal && j > ps.x) || j < window_lo(ps.x, a.window)) z0 = -CUDART_INF_F;
-                  if ((a.causal && j > ps.y) || j < window_lo(ps.y, a.window)) z1 = -CUDART_INF_F;
-                }
-                sum = add_f32x2(sum, f32x2(ex2(z0), ex2(z1)));
-              }
-              float s0, s1;
-              f32x2_split(sum, s0, s1);
-              acc += s0 + s1;
-            }
+            // (two copies of the loop: masks written out under a condition are issued whether it holds or not, twice the rest)
+            acc += j0 >= all.x && j0 + kTile <= all.y
+                       ? add_weights<NC, false>(mine + sb * C::kSCols, s_row + qb * NC / 2, s_seen + qb * NC, ks, j, &s_empty[sb], lane)
+                       : add_weights<NC, true>(mine + sb * C::kSCols, s_row + qb * NC / 2, s_seen + qb * NC, ks, j, &s_empty[sb], lane);
             if (!ends) {
               if (C::kWide) s_acc[st * kTile + key] = acc;
-            } else if (writes) {
-              weight_out[at] = before + (acc == acc ? acc : 0.f);  // a key that is no number has no weight
+            } else if (to) {
+              *to = before + (acc == acc ? acc : 0.f);  // a key that is no number has no weight
             }
           }
           if (ok && (g.chunks > 1 || i + nt == g.i1)) {
@@ -542,7 +562,7 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, const float* lse, c
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::kBytes, allowed);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(2 * n_sms), dim3(C::kThreads), C::kBytes, stream, false, tk, c, a, lse, weight_in, weight_out);
+  return launch_kernel(kern, dim3(C::kPerSm * n_sms), dim3(C::kThreads), C::kBytes, stream, false, tk, c, a, lse, weight_in, weight_out);
 }
 
 }  // namespace
@@ -552,7 +572,7 @@ cudaError_t launch_kv_weights_rows(const KvBatch& c, const AttentionArgs& a, con
   const long long rows = (long long)(c.Hq / c.Hkv) * a.max_q;
   if (rows <= 8) return launch<8>(c, a, lse, weight_in, weight_out, n_sms, stream);
   if (rows <= 16) return launch<16>(c, a, lse, weight_in, weight_out, n_sms, stream);
-  return launch<64>(c, a, lse, weight_in, weight_out, n_sms, stream);
+  return launch<128>(c, a, lse, weight_in, weight_out, n_sms, stream);
 }
 
 }  // namespace moe
