@@ -1,8 +1,8 @@
 // Eviction from the paged cache: each key/value head of a sequence keeps its tokens of the largest accumulated weights.
 //
 // Choosing.  The weights are ordered by their bits (a float above 0 orders as an unsigned integer; anything else counts as 0, a
-// token that stays in any case as the largest), and the m-th largest is found digit by digit from the top: 11, 11 and 10 bits, a
-// histogram of the tokens that agree so far at each.  Tokens above it stay, and of its equals the first ones that there is
+// token that stays in any case as the largest), and the m-th largest is found digit by digit from the top: 11, 10 and 10 bits
+// below the sign, a histogram of the tokens that agree so far at each.  Tokens above it stay, and of its equals the first ones that there is
 // room for.  A cluster of blocks shares one (sequence, head): each holds a piece of the tokens in shared memory, reads the others'
 // histograms there, and knows from the others' counts where its own tokens go.  So the weights are read once, and the choice
 // and its order depend on nothing but them.
@@ -15,14 +15,36 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 2048, kPerThread = kBins / kThreads;
 constexpr int kMaxRanks = 8;
 constexpr int kMostKeys = 49152;  // keys that a block keeps in shared memory; of a longer piece the rest is read for every digit
 
+constexpr uint32_t kStays = 0xFFFFFFFFu;  // the key of a token that stays in any case
+static_assert(kWarps == 32 && kPerThread == 2, "scans");
+
+// The sum of the values of this warp's lanes below this one.
+__device__ __forceinline__ uint32_t warp_before(uint32_t v, uint32_t& all) {
+  const int lane = threadIdx.x & 31;
+  uint32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  all = __shfl_sync(0xffffffffu, x, 31);
+  return x - v;
+}
+
 __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cluster_addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint2 ld_shared_cluster_u32x2(uint32_t cluster_addr) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cluster_addr) : "memory");
   return v;
 }
 
@@ -37,8 +59,8 @@ __device__ __forceinline__ bool load_evict(const KvBatch& c, const KvEvictArgs& 
 }
 
 __global__ void __launch_bounds__(kThreads) kv_select_kernel(const KvBatch c, const KvEvictArgs e, int ranks, int cap) {
-  extern __shared__ uint32_t s_keys[];  // [cap]
-  __shared__ uint32_t s_hist[2][kBins];
+  extern __shared__ __align__(16) uint32_t s_keys[];  // [cap]
+  __shared__ __align__(8) uint32_t s_hist[2][kBins];
   __shared__ uint32_t s_warp[kWarps], s_above[kWarps], s_equal[kWarps];
   __shared__ uint32_t s_digit, s_need;
   __shared__ uint32_t s_count[2];       // this block's tokens above the m-th weight, and equal to it
@@ -58,29 +80,40 @@ __global__ void __launch_bounds__(kThreads) kv_select_kernel(const KvBatch c, co
   const int share = ((len + ranks - 1) / ranks + kThreads - 1) / kThreads * kThreads;
   const int lo = (int)min((long long)len, (long long)rank * share), n = min(share, len - lo);
   const int32_t* table = c.page_table + (size_t)b * c.max_pages;
-  const int recent = len - min(e.recent, len);
-  auto load_key = [&](int i) -> uint32_t {
-    const int j = lo + i;
-    if (j < e.sink || j >= recent) return 0xFFFFFFFFu;
-    const int p = __ldg(table + (j >> c.page_log2));
+  const int stay0 = min(e.sink, len), stay1 = max(stay0, len - min(e.recent, len));  // tokens before the one and from the other on
+  auto to_key = [&](float w, int j) { return j < stay0 || j >= stay1 ? kStays : w > 0.f ? __float_as_uint(w) : 0u; };
+  // the weights of the tokens from lo + i on, as far as their page goes (nullptr: on no page)
+  auto weights_at = [&](int i) -> const float* {
+    const int j = lo + i, p = __ldg(table + (j >> c.page_log2));
     if (p < 0 || p >= c.n_pages) {
       set_status(c.status, DEV_ERR_BOUNDS);
-      return 0u;
+      return nullptr;
     }
-    const float w = e.weight[(((size_t)p * c.Hkv + h) << c.page_log2) + (j & (c.page - 1))];
-    return w > 0.f ? __float_as_uint(w) : 0u;
+    return e.weight + (((size_t)p * c.Hkv + h) << c.page_log2) + (j & (c.page - 1));
   };
   const int cached = min(n, cap);
 #pragma unroll 4
-  for (int i = tid; i < cached; i += kThreads) s_keys[i] = load_key(i);
-  auto key = [&](int i) { return i < cached ? s_keys[i] : load_key(i); };
+  for (int i = 4 * tid; i < cached; i += 4 * kThreads) {  // four at a time: pages hold multiples of 16
+    const float* w = weights_at(i);
+    const float4 v = w ? *reinterpret_cast<const float4*>(w) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const int j = lo + i;
+    *reinterpret_cast<uint4*>(s_keys + i) = make_uint4(to_key(v.x, j), to_key(v.y, j + 1), to_key(v.z, j + 2), to_key(v.w, j + 3));
+  }
+  auto key = [&](int i) {
+    if (i < cached) return s_keys[i];
+    const float* w = weights_at(i);
+    return to_key(w ? *w : 0.f, lo + i);
+  };
 
-  uint32_t prefix = 0, need = (uint32_t)m;
+  __syncthreads();
+  const int stay = len - (stay1 - stay0);
+  uint32_t prefix = m <= stay ? kStays : 0u, need = (uint32_t)(m <= stay ? m : m - stay);
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    const uint32_t seen = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + bits), mask = (1u << bits) - 1u;
+  for (int pass = 0; pass < (m <= stay ? 0 : 3); ++pass) {
+    const int shift = pass == 0 ? 20 : pass == 1 ? 10 : 0;
+    const uint32_t seen = pass == 0 ? 0x80000000u : 0xFFFFFFFFu << (shift + 10), mask = pass == 0 ? 0x7FFu : 0x3FFu;
     uint32_t* hist = s_hist[pass & 1];
+#pragma unroll
     for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += kThreads) {
@@ -88,37 +121,28 @@ __global__ void __launch_bounds__(kThreads) kv_select_kernel(const KvBatch c, co
       if ((k & seen) == prefix) atomicAdd(&hist[k >> shift & mask], 1u);
     }
     if (ranks > 1) cluster_sync(); else __syncthreads();
-    // the digit, from the top: thread t has the bins below kBins - kPerThread t
-    uint32_t v[kPerThread], sum = 0;
-    const int top = kBins - 1 - kPerThread * tid;
-#pragma unroll
-    for (int x = 0; x < kPerThread; ++x) v[x] = ranks > 1 ? 0u : hist[top - x];
-    for (int r = 0; r < (ranks > 1 ? ranks : 0); ++r) {
-      const uint32_t at = mapa_shared(smem_u32(hist), (uint32_t)r);
-#pragma unroll
-      for (int x = 0; x < kPerThread; ++x) v[x] += ld_shared_cluster_u32(at + 4 * (top - x));
-    }
-#pragma unroll
-    for (int x = 0; x < kPerThread; ++x) sum += v[x];
-    uint32_t before = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += y;
-    }
-    if (lane == 31) s_warp[warp] = before;
-    before -= sum;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) before += s_warp[w];
-    if (before < need && need <= before + sum) {  // one thread
-#pragma unroll
-      for (int x = 0; x < kPerThread; ++x) {
-        if (before < need && need <= before + v[x]) {
-          s_digit = (uint32_t)(top - x);
-          s_need = need - before;
-        }
-        before += v[x];
+    // the digit, from the top: thread t has the bins kBins - 1 - 2t and the one below it
+    const int top = kBins - 1 - 2 * tid;
+    uint32_t v0 = 0, v1 = 0, all;
+    if (ranks > 1) {
+      for (int r = 0; r < ranks; ++r) {
+        const uint2 v = ld_shared_cluster_u32x2(mapa_shared(smem_u32(hist + top - 1), (uint32_t)r));
+        v0 += v.y;
+        v1 += v.x;
       }
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(hist + top - 1);
+      v0 = v.y;
+      v1 = v.x;
+    }
+    uint32_t before = warp_before(v0 + v1, all);
+    if (lane == 0) s_warp[warp] = all;
+    __syncthreads();
+    before += __shfl_sync(0xffffffffu, warp_before(s_warp[lane], all), warp);
+    if (before < need && need <= before + v0 + v1) {  // one thread
+      const bool first = need <= before + v0;
+      s_digit = (uint32_t)(first ? top : top - 1);
+      s_need = need - before - (first ? 0u : v0);
     }
     __syncthreads();
     prefix |= s_digit << shift;
@@ -138,15 +162,13 @@ __global__ void __launch_bounds__(kThreads) kv_select_kernel(const KvBatch c, co
     s_equal[warp] = equal;
   }
   __syncthreads();
-  above = equal = 0;
-  for (int w = 0; w < warp; ++w) {
-    above += s_above[w];
-    equal += s_equal[w];
-  }
+  uint32_t all_above, all_equal;
+  above = __shfl_sync(0xffffffffu, warp_before(s_above[lane], all_above), warp);
+  equal = __shfl_sync(0xffffffffu, warp_before(s_equal[lane], all_equal), warp);
   if (ranks > 1) {
-    if (tid == kThreads - 1) {
-      s_count[0] = above + s_above[warp];
-      s_count[1] = equal + s_equal[warp];
+    if (tid == 0) {
+      s_count[0] = all_above;
+      s_count[1] = all_equal;
     }
     cluster_sync();
     for (int r = 0; r < rank; ++r) {
@@ -252,7 +274,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_pack_kernel(const KvBatch c, 
 cudaError_t launch_kv_evict(const KvBatch& c, const KvEvictArgs& e, int n_sms, cudaStream_t stream) {
   const long long units = (long long)c.B * c.Hkv, most = (long long)c.max_pages * c.page;
   int ranks = 1;
-  while (ranks < kMaxRanks && (most / ranks > kMostKeys || (most / ranks > 4096 && units * ranks < 2 * n_sms))) ranks *= 2;
+  while (ranks < kMaxRanks && (most / ranks > kMostKeys || (most / ranks > 16384 && units * ranks < 2 * n_sms))) ranks *= 2;
   const long long share = ((most + ranks - 1) / ranks + kThreads - 1) / kThreads * kThreads;
   const int cap = (int)(share < kMostKeys ? share : kMostKeys);
   static std::atomic<unsigned long long> allowed{0};
