@@ -22,8 +22,9 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
 SOURCES = ["gating.cu", "routing.cu", "routing_static.cu", "grouped_gemm.cu", "grouped_gemm_mxfp4.cu", "grouped_gemm_w4a8.cu",
            "finalize.cu", "frontend.cu", "api.cu", "attention_cache.cu", "attention.cu", "attention_decode.cu",
-           "attention_prefill.cu", "attention_weights.cu", "attention_evict.cu", "api_attention.cu"]
-HEADERS = ["moe_common.cuh", "moe_internal.h", "attention_common.cuh", "attention_tiles.cuh",
+           "attention_prefill.cu", "attention_weights.cu", "attention_weights_many.cu",
+           "attention_evict.cu", "api_attention.cu"]
+HEADERS = ["moe_common.cuh", "moe_internal.h", "attention_common.cuh", "attention_tiles.cuh", "attention_weights.cuh",
            "attention_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

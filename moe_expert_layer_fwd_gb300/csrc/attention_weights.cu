@@ -16,9 +16,7 @@
 // 256 cycles for a tile and 64 rows.
 //
 // Warps: softmax (groups of four, which take the tiles in turn), TMA, MMA, then queries.  Every wait is bounded (2 s).
-#include "attention_tiles.cuh"
-
-#include <limits.h>
+#include "attention_weights.cuh"
 
 namespace moe {
 namespace {
@@ -31,23 +29,15 @@ struct TileInfo {    // per 16 keys of a tile
 struct RowPair {     // two query rows: a weight is 2^(S kf qf + minus)
   float qf[2], minus[2];  // minus = -lse2
 };
-struct RowSeen {     // the keys lo .. lo + span that a row sees
-  int lo;
-  unsigned span;
-};
-
 template <int NC>
 struct Cfg {
-  static constexpr bool kWide = NC > 16;                    // hi and lo products in the same columns (else side by side: half
-                                                            // the instructions, which small ones are bound by)
-  static constexpr int kPerSm = kWide ? 1 : 2;              // blocks
-  static constexpr int kStages = kWide ? 8 : 6;             // tiles of keys
+  static constexpr int kPerSm = 2;                          // blocks
+  static constexpr int kStages = 6;                         // tiles of keys
   static constexpr int kGroups = 2, kSBufs = 2 * kGroups;   // groups of four softmax warps, and buffers of scores
   static constexpr int kQBufs = 2;
-  static constexpr int kQWarps = kWide ? 4 : 1;
   static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kQWarp = kSoftWarps + 2;
-  static constexpr int kThreads = 32 * (kQWarp + kQWarps);
+  static constexpr int kThreads = 32 * (kQWarp + 1);
   static constexpr int kQBytes = 2 * NC * 128;
   static constexpr int kQOff = kStages * kTileBytes;
   static constexpr int kBarOff = kQOff + kQBufs * kQBytes;
@@ -57,107 +47,31 @@ struct Cfg {
   static constexpr int kSeenOff = kRowOff + kQBufs * NC / 2 * (int)sizeof(RowPair);  // RowSeen [kQBufs][NC]
   static constexpr int kAllOff = kSeenOff + kQBufs * NC * (int)sizeof(RowSeen);      // int2 [kQBufs]
   static constexpr int kAccOff = kAllOff + kQBufs * (int)sizeof(int2);               // float [kStages][128]
-  static constexpr int kMiscOff = kAccOff + (kWide ? kStages * kTile * 4 : 0);
+  static constexpr int kMiscOff = kAccOff + kStages * kTile * 4;
   static constexpr int kBytes = 1024 + kMiscOff + 32;
-  static constexpr int kSCols = kWide ? NC : 2 * NC;
+  static constexpr int kSCols = 2 * NC;                     // hi and lo products side by side: half the instructions of sums in
+                                                            // one column
   static constexpr int kTmemCols = kSBufs * kSCols;         // a power of two, at least 32
   static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory");
   static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
 };
 
-// Tiles [i0, i1) of one (sequence, head), and the chunks of its rows.
-struct Segment {
-  int b, h, i0, i1, chunks;
-  SeqRange s;
-  KeyRange r;
-};
-
-__device__ __forceinline__ int row_chunks(const SeqRange& s, int G, int nc) {
-  return (int)(((long long)(s.t1 - s.t0) * G + nc - 1) / nc);
-}
-
-template <int NC>
-__device__ __forceinline__ long long seq_cost(const KvBatch& c, const AttentionArgs& a, int G, int b) {
-  SeqRange s;
-  if (!load_seq(c, b, s)) return 0;
-  return (long long)key_range(s, a).nt * row_chunks(s, G, NC);
-}
-
-// Walks the segments of a block's run: the tiles whose cost begins within it.
-template <int NC>
-struct Walk {
-  const KvBatch& c;
-  const AttentionArgs& a;
-  int G;
-  long long at, left;  // where the run begins in the present (sequence, head); how much of it is left
-  int b, h;
-  __device__ Walk(const KvBatch& c_, const AttentionArgs& a_, int G_, long long n, int b_, int h_, long long at_)
-      : c(c_), a(a_), G(G_), at(at_), left(n), b(b_), h(h_) {}
-  __device__ bool next(Segment& g) {
-    while (left > 0 && b < c.B) {
-      const bool ok = load_seq(c, b, g.s);
-      g.r = key_range(g.s, a);
-      if (!ok || g.r.nt == 0) {
-        ++b;
-        h = 0;
-        at = 0;
-        continue;
-      }
-      g.b = b;
-      g.h = h;
-      g.chunks = row_chunks(g.s, G, NC);
-      const long long cost = (long long)g.r.nt * g.chunks;
-      g.i0 = (int)((at + g.chunks - 1) / g.chunks);
-      g.i1 = (int)min((long long)g.r.nt, (at + left + g.chunks - 1) / g.chunks);
-      left -= cost - at;
-      at = 0;
-      if (++h == c.Hkv) {
-        h = 0;
-        ++b;
-      }
-      if (g.i0 < g.i1) return true;
-    }
-    return false;
-  }
-};
-
-// The chunks with a row that sees a key of [j0, j1): c0 .. c1, one at least (the keys' sums are written all the same).
-__device__ __forceinline__ void chunks_of(const Segment& g, const AttentionArgs& a, int G, int nc, int j0, int j1, int& c0, int& c1) {
-  c0 = 0;
-  c1 = g.chunks - 1;
-  if (g.chunks == 1) return;
-  const int first = g.s.first(), last = g.s.t1 - g.s.t0 - 1;  // new token i has position first + i; rows are below 2^31
-  if (a.causal) c0 = (int)((unsigned)(min(max(0, j0 - first), last) * G) / (unsigned)nc);
-  if (a.window > 0) {
-    // token i sees keys from first + i - window + 1 on: the last one that sees j1 - 1
-    const long long i = (long long)j1 - 1 - first + a.window - 1;
-    c1 = (int)((unsigned)((i < 0 ? 0 : i > last ? last : (int)i) * G + G - 1) / (unsigned)nc);
-    c1 = max(c0, min(c1, g.chunks - 1));
-  }
-}
-
 // A key's weights of a chunk's rows, from its lane of tensor memory; frees the scores once they are in registers.
 template <int NC, bool kMasked>
 __device__ __forceinline__ float add_weights(uint32_t taddr, const RowPair* row, const RowSeen* seen, float ks, int j, uint64_t* s_empty,
                                              int lane) {
-  constexpr int P = Cfg<NC>::kWide ? 32 : 8, kSteps = NC / P;  // columns at a time: the next ones come while these are added up
+  constexpr int P = 8, kSteps = NC / P;  // columns at a time: the next ones come while these are added up
   const uint64_t ks2 = f32x2(ks, ks);
   uint64_t sum = 0;
   uint32_t v[2][P], w[2][P];
-  auto load = [&](int k) {
-    if constexpr (Cfg<NC>::kWide) {
-      tmem_ld32_async(taddr + k * P, v[k & 1]);
-    } else {
-      tmem_ld_async(taddr + k * P, v[k & 1]);
-      tmem_ld_async(taddr + NC + k * P, w[k & 1]);
-    }
-  };
-  load(0);
+  tmem_ld_async(taddr, v[0]);
+  tmem_ld_async(taddr + NC, w[0]);
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
     tmem_wait_ld();
     if (k + 1 < kSteps) {
-      load(k + 1);
+      tmem_ld_async(taddr + (k + 1) * P, v[(k + 1) & 1]);
+      tmem_ld_async(taddr + NC + (k + 1) * P, w[(k + 1) & 1]);
     } else {
       tc_fence_before();
       __syncwarp();
@@ -165,8 +79,7 @@ __device__ __forceinline__ float add_weights(uint32_t taddr, const RowPair* row,
     }
     float s[P];
 #pragma unroll
-    for (int x = 0; x < P; ++x)
-      s[x] = Cfg<NC>::kWide ? __uint_as_float(v[k & 1][x]) : __uint_as_float(v[k & 1][x]) + __uint_as_float(w[k & 1][x]);
+    for (int x = 0; x < P; ++x) s[x] = __uint_as_float(v[k & 1][x]) + __uint_as_float(w[k & 1][x]);
 #pragma unroll
     for (int x = 0; x < P; x += 2) {
       const float4 r = *reinterpret_cast<const float4*>(row + (k * P + x) / 2);
@@ -214,30 +127,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
   const int G = c.Hq / c.Hkv;
   if (blockIdx.x == 0 && tid == C::kThreads - 1) check_starts(c);
 
-  // ---- this block's run
   long long run;
-  {
-    auto cost = [&](int b) { return seq_cost<NC>(c, a, G, b); };
-    long long mine, total;
-    long long* s_warp = reinterpret_cast<long long*>(s_row);  // free until the roles start
-    const long long before = scan_batch(c, C::kThreads, s_warp, mine, total, cost);
-    const long long all = total * c.Hkv, per = max(1LL, (all + gridDim.x - 1) / (long long)gridDim.x);
-    const long long begin = (long long)blockIdx.x * per;
-    run = min(per, all - begin);
-    if (run <= 0) return;
-    if (before * c.Hkv <= begin && begin < (before + mine) * c.Hkv) {
-      long long at = before, u;
-      int b = tid * ((c.B + C::kThreads - 1) / C::kThreads);
-      while ((at + (u = cost(b))) * c.Hkv <= begin) {
-        at += u;
-        ++b;
-      }
-      const long long rel = begin - at * c.Hkv;
-      s_begin[0] = b;
-      s_begin[1] = (int)(rel / u);
-      *s_at = rel % u;
-    }
-  }
+  if (!weight_run<NC>(c, a, G, C::kThreads, reinterpret_cast<long long*>(s_row), run, s_begin, s_at)) return;
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -246,7 +137,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       mbar_init(&i_full[i], 1);
     }
     for (int i = 0; i < C::kQBufs; ++i) {
-      mbar_init(&q_full[i], C::kQWarps);
+      mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1 + C::kSoftWarps);
     }
     for (int i = 0; i < C::kSBufs; ++i) {
@@ -264,8 +155,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk<NC> walk(c, a, G, run, s_begin[0], s_begin[1], *s_at);
-  Segment g;
+  WeightWalk<NC> walk(c, a, G, run, s_begin[0], s_begin[1], *s_at);
+  WeightSegment g;
 
   if (warp == C::kTmaWarp) {
     // ------------------------------------------------------------ TMA: lane = 16 keys of the tile.  It also brings the scales.
@@ -366,11 +257,6 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
             if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < kHeadDim / 32; ++k) umma_e4m3(tm + sb * C::kSCols, ad + 2 * k, bd + 2 * k, idesc, k != 0);
-              if (C::kWide) {
-#pragma unroll
-                for (int k = 0; k < kHeadDim / 32; ++k)
-                  umma_e4m3(tm + sb * C::kSCols, ad + 2 * k, bd + (uint64_t)((NC * 128) >> 4) + 2 * k, idesc, 1);
-              }
               umma_commit(&s_full[sb]);
               if (ch == c1) umma_commit(&k_empty[st]);
               if (q_ends && t == nt - 1) umma_commit(&q_empty[qb]);
@@ -385,17 +271,16 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     if (elect_one()) umma_commit(done);
     __syncwarp();
     mbar_wait_bounded(done, 0, abort_flag, 1000ull * a.limit_us, c.status, false);
-  } else if (warp >= C::kQWarp) {
-    // ------------------------------------------------------------ queries: each warp a part of the chunk's rows
-    constexpr int kMine = NC / C::kQWarps, kAtOnce = 8;
-    const int x_first = (warp - C::kQWarp) * kMine;
+  } else if (warp == C::kQWarp) {
+    // ------------------------------------------------------------ queries
+    constexpr int kAtOnce = 8;
     uint32_t fills = 0;
     bool ok = true;
     auto fill = [&](int ch) {
       const int qb = (int)(fills % C::kQBufs), first = g.s.first(), rows = (g.s.t1 - g.s.t0) * G;
       uint8_t* op = smem + C::kQOff + qb * C::kQBytes;
 #pragma unroll 1
-      for (int x0 = x_first; x0 < x_first + kMine; x0 += kAtOnce) {
+      for (int x0 = 0; x0 < NC; x0 += kAtOnce) {
         const int rho0 = ch * NC + x0;
         int i = rho0 / G, head = rho0 - i * G;
         const uint16_t* src = a.q + (size_t)(g.s.t0 + i) * a.q_stride + (size_t)(g.h * G + head) * kHeadDim + lane * 4;
@@ -421,7 +306,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           if (!a.causal) seen = {0, INT_MAX};
           else if (pos >= 0) seen = {window_lo(pos, a.window), (unsigned)(pos - window_lo(pos, a.window))};
         }
-        if (x0 == x_first) {
+        if (x0 == 0) {
           ok = warp_wait(&q_empty[qb], ((fills / C::kQBufs) & 1u) ^ 1u, abort_flag, c.status);
           if (!ok) return;
         }
@@ -450,7 +335,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           s_seen[qb * NC + x0 + lane] = seen;
         }
       }
-      if (x_first == 0 && lane == 0) {
+      if (lane == 0) {
         const int pos_lo = first + ch * NC / G, pos_hi = first + min(rows - 1, ch * NC + NC - 1) / G;
         s_all[qb] = make_int2(window_lo(pos_hi, a.window), a.causal ? pos_lo + 1 : INT_MAX);
       }
@@ -505,7 +390,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
             if (ch == c0) ok = warp_wait(&i_full[st], (m / C::kStages) & 1u, abort_flag, c.status);
             if (!ok) break;
             const float ks = infos[st].kf[key >> 4];
-            float acc = C::kWide && ch > c0 ? s_acc[st * kTile + key] : 0.f;
+            float acc = ch > c0 ? s_acc[st * kTile + key] : 0.f;
             // the key's weight so far, on its way while the scores are waited for
             const bool ends = ch == c1;
             float before = 0.f;
@@ -530,7 +415,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
                        ? add_weights<NC, false>(mine + sb * C::kSCols, s_row + qb * NC / 2, s_seen + qb * NC, ks, j, &s_empty[sb], lane)
                        : add_weights<NC, true>(mine + sb * C::kSCols, s_row + qb * NC / 2, s_seen + qb * NC, ks, j, &s_empty[sb], lane);
             if (!ends) {
-              if (C::kWide) s_acc[st * kTile + key] = acc;
+              s_acc[st * kTile + key] = acc;
             } else if (to) {
               *to = before + (acc == acc ? acc : 0.f);  // a key that is no number has no weight
             }
@@ -571,8 +456,9 @@ cudaError_t launch_kv_weights_rows(const KvBatch& c, const AttentionArgs& a, con
                                    int n_sms, cudaStream_t stream) {
   const long long rows = (long long)(c.Hq / c.Hkv) * a.max_q;
   if (rows <= 8) return launch<8>(c, a, lse, weight_in, weight_out, n_sms, stream);
-  if (rows <= 16) return launch<16>(c, a, lse, weight_in, weight_out, n_sms, stream);
-  return launch<128>(c, a, lse, weight_in, weight_out, n_sms, stream);
+  // (the other kernel takes the rows' denominators through its product, divided by the scale)
+  if (rows <= 16 || a.scale_log2 < 1e-9f) return launch<16>(c, a, lse, weight_in, weight_out, n_sms, stream);
+  return launch_kv_weights_many(c, a, lse, weight_in, weight_out, n_sms, stream);
 }
 
 }  // namespace moe
