@@ -11,8 +11,8 @@
 //
 // A block keeps kTiles tiles of keys in shared memory, converted, and walks the chunks of NC rows over them.
 //
-// Warps: 8 softmax (two groups of four, which take the tiles in turn, two buffers of scores each), 4 that convert keys, TMA, MMA, 4 for the
-// queries (two for either buffer).  Every wait is bounded (2 s).
+// Warps: 8 softmax (two groups of four, which take the tiles in turn, two buffers of scores each), 4 that convert keys, TMA, MMA, 4 for
+// the queries (two for either buffer).  Every wait is bounded (2 s).
 #include "attention_weights.cuh"
 
 namespace moe {
@@ -65,7 +65,8 @@ __device__ __forceinline__ uint32_t extra_at(int row) { return (uint32_t)(row >>
 // Two E4M3 codes as bf16, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_bf16x2(uint32_t codes) {
   const float2 f = e4m3x2_f32(codes);
-  return pack_bf16x2(f.x, f.y);
+  const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // A key's weights of a chunk's rows, from its lane of tensor memory.  kFinite: leaves out those that are not finite.
@@ -247,16 +248,17 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
         const int st = (int)(n % C::kCodes), slot = (int)(n % C::kTiles);
         ok = warp_wait2(&c_full[st], (n / C::kCodes) & 1u, &k_empty[slot], ((n / C::kTiles) & 1u) ^ 1u, abort_flag, c.status);
         if (!ok) break;
-        const uint32_t* inv = infos[n % C::kInfos].inv;
+        const uint32_t* inv = infos[n % C::kInfos].inv + w * 2;  // of the warp's keys, 16 each
         const uint8_t* src = smem + C::kCodeOff + st * kTileBytes;
         uint8_t* dst = smem + slot * C::kKBytes;
 #pragma unroll
         for (int x = 0; x < 8; x += 4) {
           uint4 v[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            v[y] = *reinterpret_cast<const uint4*>(src + (from ^ ((y & 1) << 6)) + ((x + y) >> 1) * 1024);
-            if (inv[(key0 + ((x + y) >> 1) * 8) >> 4] == 0u) v[y] = make_uint4(0, 0, 0, 0);
+          for (int y = 0; y < 4; ++y) v[y] = *reinterpret_cast<const uint4*>(src + (from ^ ((y & 1) << 6)) + ((x + y) >> 1) * 1024);
+          if (inv[x >> 2] == 0u) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) v[y] = make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
@@ -268,9 +270,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
           }
         }
         {
-          const int key = w * 32 + lane;
-          const uint32_t u = inv[key >> 4] ? inv[key >> 4] : 0x3F80u;
-          *reinterpret_cast<uint4*>(smem + C::kKxOff + slot * kTile * 32 + extra_at(key)) = make_uint4(u | u << 16, u, 0, 0);
+          const uint32_t u = inv[lane >> 4] ? inv[lane >> 4] : 0x3F80u;
+          *reinterpret_cast<uint4*>(smem + C::kKxOff + slot * kTile * 32 + extra_at(w * 32 + lane)) = make_uint4(u | u << 16, u, 0, 0);
         }
         fence_async_shared();
         __syncwarp();
