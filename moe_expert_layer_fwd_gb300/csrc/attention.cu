@@ -96,7 +96,7 @@ cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int 
   return launch_kernel(kern, grid, dim3(kJoinThreads), 0, stream, true, c, a, rows, base, part_o, part_rl, info);
 }
 
-bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c) {
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -106,11 +106,27 @@ bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c) {
         q == cudaDriverEntryPointSuccess)
       encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
   });
+  return encode;
+}
+
+bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c) {
+  const auto encode = tensor_map_encoder();
   if (!encode) return false;
   const cuuint64_t rows = (cuuint64_t)(c.n_pages > 0 ? c.n_pages : 1) * c.Hkv * c.page;
   const cuuint64_t dims[2] = {kHeadDim, rows}, strides[1] = {kHeadDim};
   const cuuint32_t box[2] = {kHeadDim, (cuuint32_t)c.page}, step[2] = {1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_query_map(CUtensorMap* m, const AttentionArgs& a, const KvBatch& c, int heads, int tokens) {
+  const auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {kHeadDim, (cuuint64_t)c.Hq, (cuuint64_t)c.T};
+  const cuuint64_t strides[2] = {kHeadDim * sizeof(uint16_t), (cuuint64_t)a.q_stride * sizeof(uint16_t)};
+  const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens}, step[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.q), dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

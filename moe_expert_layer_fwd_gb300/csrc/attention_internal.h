@@ -127,4 +127,7 @@ cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int 
 // The codes as a matrix of 128-byte rows (one token of one head each), boxes of one page with the 128-byte swizzle.
 bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c);
 
+// The queries [T][Hq][128], boxes of `tokens` times `heads` rows of 64 dims with the 128-byte swizzle.
+bool make_query_map(CUtensorMap* m, const AttentionArgs& a, const KvBatch& c, int heads, int tokens);
+
 }  // namespace moe

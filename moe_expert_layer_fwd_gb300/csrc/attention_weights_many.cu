@@ -107,8 +107,8 @@ __device__ __forceinline__ float add_weights(uint32_t taddr, const RowSeen* seen
 
 template <int NC>
 __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
-    kv_weights_many_kernel(const __grid_constant__ CUtensorMap tm_k, const KvBatch c, const AttentionArgs a, const float* lse,
-                           const float* weight_in, float* weight_out) {
+    kv_weights_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, int q_boxes, const KvBatch c,
+                           const AttentionArgs a, const float* lse, const float* weight_in, float* weight_out) {
   using C = Cfg<NC>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
     abort_flag[0] = 0;
     abort_flag[1] = (int)a.limit_us;
     tma_prefetch_desc(&tm_k);
+    if (q_boxes) tma_prefetch_desc(&tm_q);
     fence_mbar_init();
   }
   // of the extra step only the first 16 bytes of a row are ever written again
@@ -347,8 +348,29 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
     // ------------------------------------------------------------ queries: two warps for either buffer, half of the chunk's rows each
     constexpr int kMine = NC / 2;  // rows, two at a time: 16 lanes x 16 bytes a row
     const int mine_qb = (warp - C::kQWarp) >> 1, r_first = ((warp - C::kQWarp) & 1) * kMine, piece = lane & 15;
+    const uint64_t pol = policy_evict_last();
     uint32_t fills = 0;
     bool ok = true;
+    // Where G does not divide NC: 16 bytes a lane, where the copies of whole boxes would put them.
+    auto copy_rows = [&](int ch, int rows, int qb) {
+      int r = r_first + (lane >> 4), i = (ch * NC + r) / G, head = ch * NC + r - i * G, left = rows - (ch * NC + r);
+      const uint16_t* src = a.q + (size_t)(g.s.t0 + i) * a.q_stride + (size_t)(g.h * G + head) * kHeadDim + piece * 8;
+      const long long wrap = a.q_stride - (long long)G * kHeadDim;
+      const uint32_t op = smem_u32(smem) + C::kQOff + qb * C::kQBytes + (piece >> 3) * NC * 128;
+#pragma unroll 4
+      for (int k = 0; k < kMine / 2; ++k, r += 2, left -= 2) {
+        cp_async16(op + r * 128 + (((piece & 7) ^ (r & 7)) << 4), left > 0 ? src : a.q, left > 0 ? 16 : 0);
+        src += 2 * kHeadDim;
+        head += 2;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)  // G may be 1
+          if (head >= G) {
+            head -= G;
+            src += wrap;
+          }
+      }
+      cp_async_commit();
+    };
     auto fill = [&](int ch) {
       const int qb = (int)(fills % C::kQBufs);
       if (qb != mine_qb) {
@@ -377,25 +399,9 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
         m -= bf16_lo(m1);
         part[k] = make_uint4(m0 | m1 << 16, f32_to_bf16_rne(m), 0, 0);
       }
-      int r = r_first + (lane >> 4), i = (ch * NC + r) / G, head = ch * NC + r - i * G, left = rows - (ch * NC + r);
-      const uint16_t* src = a.q + (size_t)(g.s.t0 + i) * a.q_stride + (size_t)(g.h * G + head) * kHeadDim + piece * 8;
-      const long long wrap = a.q_stride - (long long)G * kHeadDim;
       ok = warp_wait(&q_empty[qb], ((fills / C::kQBufs) & 1u) ^ 1u, abort_flag, c.status);
       if (!ok) return;
-      const uint32_t op = smem_u32(smem) + C::kQOff + qb * C::kQBytes + (piece >> 3) * NC * 128;
-#pragma unroll 4
-      for (int k = 0; k < kMine / 2; ++k, r += 2, left -= 2) {
-        cp_async16(op + r * 128 + (((piece & 7) ^ (r & 7)) << 4), left > 0 ? src : a.q, left > 0 ? 16 : 0);
-        src += 2 * kHeadDim;
-        head += 2;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)  // G may be 1
-          if (head >= G) {
-            head -= G;
-            src += wrap;
-          }
-      }
-      cp_async_commit();
+      if (!q_boxes) copy_rows(ch, rows, qb);
 #pragma unroll
       for (int k = 0; k < kMine / 32; ++k) {
         const int x = r_first + k * 32 + lane;
@@ -406,10 +412,18 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
         const int pos_lo = first + ch * NC / G, pos_hi = first + min(rows - 1, ch * NC + NC - 1) / G;
         s_all[qb] = make_int2(window_lo(pos_hi, a.window), a.causal ? pos_lo + 1 : INT_MAX);
       }
-      cp_async_wait<0>();
+      if (!q_boxes) cp_async_wait<0>();
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[qb]);
+      if (lane == 0) {
+        if (q_boxes && r_first == 0) {
+          mbar_arrive_expect_tx(&q_full[qb], C::kQBytes);
+          for (int half = 0; half < 2; ++half)
+            tma_load_3d(smem + C::kQOff + qb * C::kQBytes + half * NC * 128, &tm_q, half * 64, g.h * G, g.s.t0 + ch * NC / G, &q_full[qb], pol);
+        } else {
+          mbar_arrive(&q_full[qb]);
+        }
+      }
       ++fills;
     };
     while (ok && walk.next(g)) {
@@ -426,6 +440,12 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
         for (int ch = c0; ok && ch <= c1; ++ch) fill(ch);
       }
     }
+    // every copy lands before the block ends
+    if (q_boxes && r_first == 0 && lane == 0) {
+      const uint32_t mine = fills / C::kQBufs + ((uint32_t)mine_qb < fills % C::kQBufs ? 1u : 0u);  // fills of this buffer
+      if (mine) mbar_wait_bounded(&q_full[mine_qb], (mine - 1u) & 1u, abort_flag, 1000ull * a.limit_us, c.status, false);
+    }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax: thread = key
     const int group = warp >> 2, w4 = warp & 3, key = tid & 127;
@@ -519,11 +539,14 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, const float* lse, c
   using C = Cfg<NC>;
   CUtensorMap tk;
   if (!make_cache_map(&tk, c.k_codes, c)) return cudaErrorInvalidValue;
+  const int G = c.Hq / c.Hkv, q_boxes = NC % G == 0;
+  CUtensorMap tq = {};
+  if (q_boxes && !make_query_map(&tq, a, c, G, NC / G)) return cudaErrorInvalidValue;
   auto kern = kv_weights_many_kernel<NC>;
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::kBytes, allowed);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(n_sms), dim3(C::kThreads), C::kBytes, stream, false, tk, c, a, lse, weight_in, weight_out);
+  return launch_kernel(kern, dim3(n_sms), dim3(C::kThreads), C::kBytes, stream, false, tk, tq, q_boxes, c, a, lse, weight_in, weight_out);
 }
 
 }  // namespace
