@@ -121,8 +121,8 @@ MOE_API int moe_workspace_init(void* ws, size_t ws_bytes, void* stream);
  * producers wait for flags that nothing sets: after the limit the kernel records MOE_ERR_TIMEOUT in
  * the workspace status, every CTA leaves its loops, waits for nothing in flight, frees its tensor
  * memory and returns; the rest of the layer runs on whatever act then holds.  what = 4: value != 0
- * makes moe_paged_attention withhold the copies of the values that its tensor-core role waits for,
- * with the same end (MOE_ERR_TIMEOUT; out is undefined).  Unknown `what` -> MOE_ERR_INVALID_ARG.  The pages have no counterpart.
+ * makes moe_paged_attention and moe_paged_attention_shared withhold the copies of the values that their tensor-core
+ * role waits for, and moe_kv_weights those of the keys, with the same end (MOE_ERR_TIMEOUT; out is undefined).  Unknown `what` -> MOE_ERR_INVALID_ARG.  The pages have no counterpart.
  */
 MOE_API int moe_debug_set(int what, unsigned long long value);
 

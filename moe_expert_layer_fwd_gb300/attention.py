@@ -407,11 +407,16 @@ class AttentionLayer:
     ``forward`` takes the rows of the merged projection [T, (Hq + 2 Hkv) * D] (query heads, key heads, value heads)
     and returns the attention output [T, Hq * D], the input of the output projection.  Pages are the caller's to hand
     out: page_table names them, and a page freed by one sequence may be given to another at any time.  Calls of one layer share its
-    workspace and run one after another; ``status`` says what they found."""
+    workspace and run one after another; ``status`` says what they found.
+
+    Long conversations: ``rows`` (of ``rotation``) turns the tokens by given positions instead of their places in the cache; ``prefix``
+    lets sequences share what another one stored; with ``track_weights`` every call adds the attention weights that the cached
+    tokens got to ``weight``, and ``evict`` packs the tokens of the largest ones into new pages."""
 
     def __init__(self, n_pages: int, Hq: int, Hkv: int, D: int = 128, page: int = 64, max_pos: int = 32768,
                  rot_dim: Optional[int] = None, rope_base: float = 1e6, interleaved: bool = False, q_norm_weight=None,
-                 k_norm_weight=None, eps: float = 1e-6, scale: Optional[float] = None, window: int = 0, device="cuda"):
+                 k_norm_weight=None, eps: float = 1e-6, scale: Optional[float] = None, window: int = 0, device="cuda",
+                 track_weights: bool = False):
         if window < 0 or (scale is not None and not 0.0 < scale < float("inf")):
             raise ValueError(f"expected window >= 0 and a positive finite scale, got {window} and {scale}")
         self.Hq, self.Hkv, self.D = Hq, Hkv, D
@@ -421,8 +426,19 @@ class AttentionLayer:
         self.interleaved, self.q_norm_weight, self.k_norm_weight, self.eps = interleaved, q_norm_weight, k_norm_weight, eps
         self.scale, self.window = scale, window
         self.ws, self._outgrown = _status_ws(self.cache.k_codes, None), []
+        self.weight = _b().torch.zeros((n_pages, Hkv, page), dtype=_b().f32, device=device) if track_weights else None
 
-    def forward(self, qkv, q_start, kv_len, page_table, max_q: int, out=None, stream=None):
+    def rotation(self, positions, axes=None, rows=None, stream=None):
+        """The rows of ``forward`` for tokens at positions [n_axes, T] (int32), frequency f on axis axes[f] (the first one): once a
+        step serves all layers of a model."""
+        if self.cos_sin is None:
+            raise ValueError("rotation: this layer rotates nothing")
+        axes = [0] * (self.cos_sin.shape[1] // 2) if axes is None else axes
+        return moe_rope_rows(positions, axes, self.cos_sin, rows, self.ws, stream)
+
+    def forward(self, qkv, q_start, kv_len, page_table, max_q: int, out=None, stream=None, rows=None, prefix=None):
+        """rows: None (a token's position is its place in the cache) or [T, rot_dim] of ``rotation``.  prefix: None, or as in
+        moe_paged_attention_shared; the positions of tokens behind one go on from its end, so rows must be given."""
         T, B = qkv.shape[0], page_table.shape[0]
         q, k, v = qkv.view(T, self.Hq + 2 * self.Hkv, self.D).split([self.Hq, self.Hkv, self.Hkv], dim=1)
         # What the attention refuses is refused before the tokens are in the cache.
@@ -434,28 +450,59 @@ class AttentionLayer:
                 raise ValueError(f"out: expected a contiguous tensor [{T}, {self.Hq * self.D}], got {tuple(out.shape)}")
             out = out.view(T, self.Hq, self.D)
             _need(out, "out", _b().bf16, out.shape)
+        p = None
+        if prefix is not None:
+            if self.window or (rows is None and self.cos_sin is not None):
+                raise ValueError("prefix: not with a window, and not without the rows of its readers' positions")
+            p = _prefix_struct(prefix, T)
+            if p.n < 1 or p.max_q * p.n < T or (p.max_q < 1 and T > 0):
+                raise _m.MoEError(_m.MOE_ERR_INVALID_ARG, "AttentionLayer.forward: prefix")
+        if rows is not None:
+            if self.cos_sin is None:
+                raise ValueError("rows: this layer rotates nothing")
+            _need(rows, "rows", _b().f32, (T, self.cos_sin.shape[1]))
+        shared = p is not None or self.weight is not None
         d = _m.moe_kv_desc(B, T, self.Hq, self.Hkv, self.D, 16, 0, 0)
-        ws = self._workspace_for(d, max_q, stream)
-        rq = moe_kv_append(q, k, v, self.cache, q_start, kv_len, page_table, self.cos_sin, None, self.interleaved,
-                           self.q_norm_weight, self.k_norm_weight, self.eps, ws=ws, stream=stream)
-        o = moe_paged_attention(rq, self.cache, q_start, kv_len, page_table, max_q, self.scale, True, self.window,
-                                out, ws, stream)
+        ws = self._workspace_for(d, max_q, stream, p)
+        if rows is None:
+            rq = moe_kv_append(q, k, v, self.cache, q_start, kv_len, page_table, self.cos_sin, None, self.interleaved,
+                               self.q_norm_weight, self.k_norm_weight, self.eps, ws=ws, stream=stream)
+        else:
+            rq = moe_kv_append_at(q, k, v, self.cache, q_start, kv_len, page_table, rows, self.interleaved, self.q_norm_weight,
+                                  self.k_norm_weight, self.eps, ws=ws, stream=stream)
+        if shared:
+            o, lse = moe_paged_attention_shared(rq, self.cache, q_start, kv_len, page_table, max_q, prefix, self.scale, True,
+                                                self.window, out, None, ws, stream)
+        else:
+            o = moe_paged_attention(rq, self.cache, q_start, kv_len, page_table, max_q, self.scale, True, self.window,
+                                    out, ws, stream)
+        if self.weight is not None:
+            moe_kv_weights(rq, lse, self.cache, q_start, kv_len, page_table, max_q, self.weight, None, self.scale, True, self.window, ws,
+                           stream)
         if ws is not self.ws:
             with _b().torch.cuda.stream(stream):
                 self.ws[:_b().status_bytes].bitwise_or_(ws[:_b().status_bytes])
         return o.view(T, self.Hq * self.D)
 
-    def _workspace_for(self, d, max_q: int, stream):
+    def evict(self, kv_len, page_table, keep, new_table, sink: int = 0, recent: int = 0, stream=None):
+        """Packs the keep[b] tokens of the largest weights of each sequence into the pages of new_table (moe_kv_evict); returns
+        (new_len, kept).  The old pages are free then, and the next token's place is new_len[b], its position what it was."""
+        if self.weight is None:
+            raise ValueError("evict: the layer has no weights (track_weights)")
+        return moe_kv_evict(self.cache, self.weight, kv_len, page_table, keep, new_table, sink, recent, ws=self.ws, stream=stream)
+
+    def _workspace_for(self, d, max_q: int, stream, prefix=None):
         """The layer's workspace, a larger one from now on if this call needs it.
 
         The smaller one is kept: a captured graph, or a call still running on another stream, goes on using it (there are few
         sizes).  A call that is being captured does not make the layer's workspace grow -- clearing the new one's status word would
         become a part of the graph, done again by every replay -- but has one of its own, whose status is added to the layer's."""
         b = _b()
-        if self.ws.numel() >= b.workspace_size(_byref(d), max_q):
+        need = b.workspace_size(_byref(d), max_q) if prefix is None else b.shared_size(_byref(d), max_q, _byref(prefix))
+        if self.ws.numel() >= need > 0:
             return self.ws
         with b.torch.cuda.stream(stream):
-            ws = _workspace(d, max_q, self.ws, stream)
+            ws = _workspace(d, max_q, self.ws, stream) if prefix is None else _shared_workspace(d, max_q, prefix, self.ws, stream)
             if not b.torch.cuda.is_current_stream_capturing():
                 self._outgrown.append(self.ws)
                 ws[:b.status_bytes].copy_(self.ws[:b.status_bytes])  # what an earlier call reported stays readable
