@@ -611,14 +611,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && next->nt) fetch_queries(*next);
       }
       // ---- the rows' outputs
-      const bool complete = g.i0 == 0 && g.i1 == g.nt;
       float before = -CUDART_INF_F;  // of the pass before, on its way while the last sums are waited for
-      if (kPass == 2) pdl_wait();
-      if (kPass == 2 && complete && live) before = prior_lse(a, (size_t)(g.t0 + i_row) * c.Hq + head);
+      if constexpr (kPass == 2) {
+        pdl_wait();
+        if (live && g.i0 == 0 && g.i1 == g.nt) before = prior_lse(a, (size_t)(g.t0 + i_row) * c.Hq + head);
+      }
       RowEnd e = {};
       ok = ok && warp_wait(&o_full[mt], (steps - 1u) & 1u, abort_flag, c.status);
       if (!ok) break;
       tc_fence_after();
+      const bool complete = g.i0 == 0 && g.i1 == g.nt;
       const size_t part = (size_t)(2 * (int)blockIdx.x + g.later) * kRows + (kSplit ? 0 : mt * kM) + row;
       uint16_t* out = a.out + ((size_t)(g.t0 + i_row) * c.Hq + head) * kHeadDim;
       // kSplit: M tile 1 puts its r and l, and its sums in two halves of the dims, where the queries were once both tiles'
