@@ -87,8 +87,10 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 }  // namespace
 
-cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int blocks, int rows, float base, const float* part_o,
+cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& args, int blocks, int rows, float base, const float* part_o,
                                   const float2* part_rl, const JoinInfo* info, cudaStream_t stream) {
+  AttentionArgs a = args;
+  if (a.pass == 3) a.prior = nullptr;  // the prefixes' tables lie there; their keys are in the sums
   constexpr int kAll = kJoinThreads / 32;
   auto kern = rows <= 32 ? (a.pass == 0 ? attention_join_kernel<kAll, 0> : a.pass == 1 ? attention_join_kernel<kAll, 1> : attention_join_kernel<kAll, 2>)
                          : (a.pass == 0 ? attention_join_kernel<1, 0> : a.pass == 1 ? attention_join_kernel<1, 1> : attention_join_kernel<1, 2>);
@@ -149,6 +151,14 @@ int attention_debug_set(int what, unsigned long long value) {
   return 0;
 }
 
+// Above 128 rows per key/value head and sequence, on average, an item of 256 rows is a sequence's own anyhow, and the prefix's tiles come
+// from L2 whoever asks: one pass saves the second one's items and the rows in between (16 sequences of 20-250 tokens, 8 heads a
+// key/value head, behind 4001: 254 us as two passes, 191 as one).  Below, rows of several sequences share the tiles.
+bool shared_attention_joins(const KvBatch& prefixes, const KvBatch& c) {
+  return (long long)c.T * (c.Hq / c.Hkv) > 128LL * c.B &&
+         ((long long)prefixes.max_pages + c.max_pages) * c.page < (1LL << 31) - 2048;
+}
+
 // Two passes, each with the kernel that its rows per key/value head call for: over the prefixes, whose readers' tokens are one
 // sequence that sees all of it (so a prefix is read once for all of them, and its rows fill the tiles), then over the
 // sequences' own tokens, whose ends add the first pass's rows.  The rows in between are fp32.  The second pass starts while the
@@ -158,6 +168,14 @@ cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, v
                                     const AttentionArgs& args, float* rows, float* rows_lse, int n_sms, cudaStream_t stream) {
   AttentionArgs a = args;
   a.pass = 2;
+  if (prefixes.B && !rows) {
+    a.pass = 3;
+    a.n_prefixes = prefixes.B;
+    a.prefix_max_pages = prefixes.max_pages;
+    a.prefix_start = prefixes.q_start;
+    a.prefix_len = prefixes.kv_len;
+    a.prefix_table = prefixes.page_table;
+  }
   if (rows) {
     AttentionArgs p = a;
     p.pass = 1;

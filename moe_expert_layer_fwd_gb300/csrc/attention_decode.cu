@@ -777,7 +777,7 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   float* part_o = reinterpret_cast<float*>(a.scratch);
   float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)2 * blocks_of(n_sms) * NC * kHeadDim);
   JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)2 * blocks_of(n_sms) * NC);
-  e = launch_kernel(kern, dim3(blocks), dim3(C::kThreads), C::kBytes, stream, a.prior != nullptr, tk, tv, c, a, (int)split, part_o, part_rl,
+  e = launch_kernel(kern, dim3(blocks), dim3(C::kThreads), C::kBytes, stream, kPass == 2 && a.prior, tk, tv, c, a, (int)split, part_o, part_rl,
                     info);
   if (e != cudaSuccess || !split) return e;
   return launch_attention_join(c, a, blocks, NC, kBase, part_o, part_rl, info, stream);

@@ -62,16 +62,29 @@ struct AttentionArgs {
   void* scratch;              // after the status word of the workspace
   // Attention in two passes over different keys: the first leaves out32 and lse, the second takes them as its prior and
   // writes the rows of both.
-  int pass;                   // 0: a call of its own, with rows only; 1: the first; 2: the second, or a call of its own with lse
-  const float* prior;         // [T, Hq, 128] rows of the pass before, and
-  const float* prior_lse;     // [T, Hq] the logarithms (base 2) of their denominators; NULL: no pass before
-  float* out32;               // pass 1: the rows go here, in fp32, instead of out
+  int pass;                   // 0: a call of its own, with rows only; 1: the first; 2: the second, or a call of its own with lse; 3: both in
+                              // one, each row over its prefix's keys and then its own
+  union {
+    struct {
+      const float* prior;      // [T, Hq, 128] rows of the pass before, and
+      const float* prior_lse;  // [T, Hq] the logarithms (base 2) of their denominators; NULL: no pass before
+      float* out32;            // pass 1: the rows go here, in fp32, instead of out
+    };
+    struct {                   // pass 3: as KvBatch's q_start, kv_len and page_table
+      const int32_t* prefix_start;
+      const int32_t* prefix_len;
+      const int32_t* prefix_table;
+    };
+  };
   float* lse;                 // [T, Hq] or NULL: lse_unit times the logarithm (base 2) of the rows' denominators (-inf: nothing seen)
   float lse_unit;
+  int n_prefixes, prefix_max_pages;  // pass 3
 };
 size_t attention_scratch_bytes(int Hq, int Hkv, int max_q, int n_sms);
 cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
 
+// Whether sequences bring so many rows that each goes over its prefix by itself: nothing is passed on then (rows = NULL).
+bool shared_attention_joins(const KvBatch& prefixes, const KvBatch& c);
 // Sequences b of `prefixes` are the prefixes, its q_start cuts the T tokens into their readers; rows [T, Hq, 128] and rows_lse
 // [T, Hq]: what is passed from the first pass to the second (NULL: no prefixes).
 cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, void* prefix_scratch, const KvBatch& c,

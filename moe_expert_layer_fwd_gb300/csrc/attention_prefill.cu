@@ -62,7 +62,7 @@ struct Part {  // an item (rows [qt * kRows, (qt + 1) * kRows) of a sequence's n
   int b, h, qt, i0, i1, nt, tile0, lo, hi;  // keys [lo, hi) are seen by some row; nt == 0: the run is over
   int later;                                // not the item that the run begins in
   int t0, n, first;                         // first new token, new tokens, position of the first
-  int pad[3];
+  int own0, plen, prefix;                   // pass 3: the sequence's own keys begin here, behind the plen keys of this prefix
 };
 
 // kSplit: both M tiles hold the same 128 rows and take an item's key tiles in turn (else 256 rows, the same tiles).
@@ -88,10 +88,42 @@ struct Cfg {
   static __device__ __forceinline__ int tiles(const Part& g) { return (g.i1 - g.i0 + kStep - 1) / kStep * kStep; }
 };
 
-template <int kRows>
-__device__ __forceinline__ void item_range(const SeqRange& s, const AttentionArgs& a, int G, int qt, int& lo, int& hi) {
+// Pass 3: the keys of a sequence are its prefix's, in whole tiles (the last one's rest is nobody's), and then its own: a row that has
+// begun its queries and sums goes on with them.  Lengths and positions count the prefix's tiles.
+template <int kPass>
+struct ItemSeq : SeqRange {};
+template <>
+struct ItemSeq<3> : SeqRange {
+  int own0, plen, prefix;
+};
+template <int kPass>
+__device__ __forceinline__ bool load_item_seq(const KvBatch& c, const AttentionArgs& a, int b, ItemSeq<kPass>& s) {
+  bool ok = load_seq(c, b, s);
+  if constexpr (kPass == 3) {
+    s.own0 = s.plen = s.prefix = 0;
+    if (ok && s.t1 > s.t0) {
+      int lo = 0, hi = a.n_prefixes;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(a.prefix_start + mid) <= s.t0) lo = mid; else hi = mid;
+      }
+      s.prefix = lo;
+      s.plen = __ldg(a.prefix_len + lo);
+      ok = __ldg(a.prefix_start + lo) <= s.t0 && __ldg(a.prefix_start + lo + 1) >= s.t1 && s.plen >= 0 &&
+           s.plen <= (long long)a.prefix_max_pages * c.page;
+      if (!ok) set_status(c.status, DEV_ERR_CONFIG);
+      s.own0 = ok ? (s.plen + kKeys - 1) / kKeys * kKeys : 0;
+      s.len += s.own0;
+    }
+  }
+  return ok;
+}
+
+template <int kRows, int kPass>
+__device__ __forceinline__ void item_range(const ItemSeq<kPass>& s, const AttentionArgs& a, int G, int qt, int& lo, int& hi) {
   const int i_min = qt * kRows / G, i_max = min(s.t1 - s.t0 - 1, (qt * kRows + kRows - 1) / G);
   hi = a.causal ? max(0, min(s.len, s.first() + i_max + 1)) : s.len;
+  if constexpr (kPass == 3) hi = max(hi, s.own0);  // every row sees all of the prefix
   lo = window_lo(s.first() + i_min, a.window);
 }
 __device__ __forceinline__ int item_tiles(int lo, int hi) { return max(1, (hi + kKeys - 1) / kKeys - lo / kKeys); }
@@ -108,13 +140,13 @@ template <int kRows>
 __device__ __forceinline__ int places(const KvBatch& c, int G) { return (int)((long long)c.T * G / kRows) + c.B; }
 
 // Walks places in order.
-template <int kRows>
+template <int kRows, int kPass>
 struct Places {
   const KvBatch& c;
   const AttentionArgs& a;
   int G, place, b;
   bool ok;
-  SeqRange s;
+  ItemSeq<kPass> s;
   __device__ Places(const KvBatch& c_, const AttentionArgs& a_, int G_, int place_) : c(c_), a(a_), G(G_), place(place_) {
     int lo = 0, hi = c.B;
     while (hi - lo > 1) {
@@ -122,20 +154,20 @@ struct Places {
       if (place_of<kRows>(c, G, mid) <= place) lo = mid; else hi = mid;
     }
     b = lo;
-    ok = load_seq(c, b, s);
+    ok = load_item_seq<kPass>(c, a, b, s);
   }
   // tiles of the item at this place (0: empty), for one head
   __device__ int tiles(int& qt, int& lo, int& hi) const {
     qt = place - place_of<kRows>(c, G, b);
     if (!ok || qt < 0 || (long long)qt * kRows >= (long long)(s.t1 - s.t0) * G) return 0;
-    item_range<kRows>(s, a, G, qt, lo, hi);
+    item_range<kRows, kPass>(s, a, G, qt, lo, hi);
     return item_tiles(lo, hi);
   }
   __device__ void next() {
     ++place;
     if (b + 1 < c.B && place_of<kRows>(c, G, b + 1) <= place) {
       ++b;
-      ok = load_seq(c, b, s);
+      ok = load_item_seq<kPass>(c, a, b, s);
     }
   }
 };
@@ -146,9 +178,9 @@ __device__ __forceinline__ int first_tile_from(long long rel, int nt) {
   return rel <= 0 ? 0 : (int)min((long long)nt, max(1LL, rel - kItemCost));
 }
 
-template <int kRows>
+template <int kRows, int kPass>
 struct Walk {
-  Places<kRows> p;
+  Places<kRows, kPass> p;
   long long left, rel;  // cost left in the run; where it starts in the present item
   int h, end, later = 0;
   __device__ Walk(const KvBatch& c, const AttentionArgs& a, int G, long long n, int place, int h_, int rel_)
@@ -164,6 +196,11 @@ struct Walk {
       g.t0 = p.s.t0;
       g.n = p.s.t1 - p.s.t0;
       g.first = p.s.first();
+      if constexpr (kPass == 3) {
+        g.own0 = p.s.own0;
+        g.plen = p.s.plen;
+        g.prefix = p.s.prefix;
+      }
       g.h = h;
       g.tile0 = g.lo / kKeys;
       g.i0 = first_tile_from(rel, g.nt);
@@ -328,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long mine = 0;
     int qt, lo, hi;
     if (p0 < p1) {
-      Places<kRows> p(c, a, G, p0);
+      Places<kRows, kPass> p(c, a, G, p0);
 #pragma unroll 1
       for (; p.place < p1; p.next()) mine += item_cost(p.tiles(qt, lo, hi));
     }
@@ -355,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return;
     }
     if (before * c.Hkv <= begin && begin < (before + mine) * c.Hkv) {
-      Places<kRows> p(c, a, G, p0);
+      Places<kRows, kPass> p(c, a, G, p0);
       long long at = before;
       int nt;
       for (;; p.next()) {
@@ -529,7 +566,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++segs;
       // keys [w_lo, w_hi) are seen by every row of this warp
       const int warp_rho = row0 + quarter * 32, tiles = C::tiles(g);
-      const int w_hi = a.causal ? min(g.hi, g.first + warp_rho / G + 1) : g.hi;
+      // one past the last key that a row at this position sees; pass 3: every row sees the keys before own0, up to plen
+      auto seen_end = [&](int pos) {
+        if constexpr (kPass == 3) return a.causal ? min(g.hi, max(pos + 1, g.own0)) : g.hi;
+        return a.causal ? min(g.hi, pos + 1) : g.hi;
+      };
+      const int w_hi = kPass == 3 ? seen_end(g.first + warp_rho / G) : a.causal ? min(g.hi, g.first + warp_rho / G + 1) : g.hi;
       const int w_lo = window_lo(g.first + (warp_rho + 31) / G, a.window);
       float r = -CUDART_INF_F, l = 0.f;
 #pragma unroll 1
@@ -547,9 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int w = 0; w < kKeys / 32; ++w) tmem_ld32_async(t_s + 32 * w, s[w]);
         tmem_wait_ld();
         const int j0 = (g.tile0 + i) * kKeys;
-        if (j0 < w_lo || j0 + kKeys > w_hi || have != (1u << kPieces) - 1u) {
+        const bool rest = kPass == 3 && j0 < g.own0 && j0 + kKeys > g.plen;  // the prefix ends within this tile
+        if (j0 < w_lo || j0 + kKeys > w_hi || have != (1u << kPieces) - 1u || rest) {
           // bit x of word w: this row sees key 32 w + x of the tile
-          const int hi_col = (a.causal ? min(g.hi, pos + 1) : g.hi) - j0, lo_col = window_lo(pos, a.window) - j0;
+          const int hi_col = (kPass == 3 ? (rest ? g.plen : seen_end(pos)) : (a.causal ? min(g.hi, pos + 1) : g.hi)) - j0, lo_col = window_lo(pos, a.window) - j0;
 #pragma unroll
           for (int w = 0; w < kKeys / 32; ++w) {
             const uint32_t pages = have >> (2 * w);
@@ -749,7 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int j0 = (g.tile0 + i) * kKeys;
           const uint8_t* src = smem + C::kVOff + st * kTileBytes;
           uint8_t* dst = smem + C::kV16Off + (n % C::kV16s) * C::kV16Bytes;
-          const bool whole = j0 >= g.lo && j0 + kKeys <= g.hi && have == (1u << kPieces) - 1u;
+          const int end = kPass == 3 && j0 < g.own0 ? g.plen : g.hi;
+          const bool whole = j0 >= g.lo && j0 + kKeys <= end && have == (1u << kPieces) - 1u;
 #pragma unroll
           for (int x = 0; x < 8; x += 4) {
             uint4 v[4];
@@ -759,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 const int tok = tok0 + ((x + y) >> 1) * 8;
-                if (j0 + tok < g.lo || j0 + tok >= g.hi || !(have >> (tok >> 4) & 1u)) v[y] = make_uint4(0, 0, 0, 0);
+                if (j0 + tok < g.lo || j0 + tok >= end || !(have >> (tok >> 4) & 1u)) v[y] = make_uint4(0, 0, 0, 0);
               }
             }
 #pragma unroll
@@ -789,9 +833,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       while (ok && reader.next(g, abort_flag, c.status)) {
         const int32_t* row = c.page_table + (size_t)g.b * c.max_pages;
+        const int32_t* prefix = kPass == 3 ? a.prefix_table + (size_t)g.prefix * a.prefix_max_pages : nullptr;
         // page of this lane's box of tile i, read one tile ahead; -1: nothing to load
         auto page_at = [&](int i) {
           const int j = (g.tile0 + i) * kKeys + (lane << c.page_log2);
+          if (kPass == 3) {
+            if (lane >= boxes || i >= g.i1) return -1;
+            if (j < g.own0) return j < g.plen ? __ldg(prefix + (j >> c.page_log2)) : -1;
+            return j < g.hi ? __ldg(row + ((j - g.own0) >> c.page_log2)) : -1;
+          }
           return lane < boxes && i < g.i1 && j + c.page > g.lo && j < g.hi ? __ldg(row + (j >> c.page_log2)) : -1;
         };
         int pg = page_at(g.i0);
@@ -831,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kScaleWarp) {
       // ---------------------------------------------------------- scales: lane = 16 keys of the tile
       // It also walks the run, and gives the others its parts.
-      Walk<kRows> walk(c, a, G, run, s_begin[0], s_begin[1], s_begin[2]);
+      Walk<kRows, kPass> walk(c, a, G, run, s_begin[0], s_begin[1], s_begin[2]);
       uint32_t n = 0;
       bool ok = true;
       for (uint32_t np = 0; ok; ++np) {
@@ -845,10 +895,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (!more) break;
         const int32_t* row = c.page_table + (size_t)g.b * c.max_pages;
+        const int32_t* prefix = kPass == 3 ? a.prefix_table + (size_t)g.prefix * a.prefix_max_pages : nullptr;
         auto page_at = [&](int i) {
           const int j = (g.tile0 + i) * kKeys + (lane & (kPieces - 1)) * 16;
-          const bool in = i < g.i1 && j + 15 >= g.lo && j < g.hi;
-          const int p = in ? __ldg(row + (j >> c.page_log2)) : -1;
+          const bool in_prefix = kPass == 3 && j < g.own0;
+          const bool in = i < g.i1 && j + 15 >= g.lo && j < (in_prefix ? g.plen : g.hi);
+          const int p = !in ? -1 : in_prefix ? __ldg(prefix + (j >> c.page_log2)) : __ldg(row + ((kPass == 3 ? j - g.own0 : j) >> c.page_log2));
           if (in && (p < 0 || p >= c.n_pages)) set_status(c.status, DEV_ERR_BOUNDS);
           return p < c.n_pages ? p : -1;
         };
@@ -969,7 +1021,7 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   float* part_o = reinterpret_cast<float*>(a.scratch);
   float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)n_sms * 2 * C::kRows * kHeadDim);
   JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)n_sms * 2 * C::kRows);
-  e = launch_kernel(kern, dim3(n_sms), dim3(kThreads), C::kBytes, stream, a.prior != nullptr, tk, tv, c, a, part_o, part_rl, info);
+  e = launch_kernel(kern, dim3(n_sms), dim3(kThreads), C::kBytes, stream, kPass == 2 && a.prior, tk, tv, c, a, part_o, part_rl, info);
   if (e != cudaSuccess) return e;
   return launch_attention_join(c, a, n_sms, C::kRows, kBase, part_o, part_rl, info, stream);
 }
@@ -988,6 +1040,7 @@ cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, i
   const bool split = splits_keys(c.Hq / c.Hkv, a.max_q);
   if (a.pass == 0) return split ? launch<true, 0>(c, a, n_sms, stream) : launch<false, 0>(c, a, n_sms, stream);
   if (a.pass == 1) return split ? launch<true, 1>(c, a, n_sms, stream) : launch<false, 1>(c, a, n_sms, stream);
+  if (a.pass == 3) return launch<false, 3>(c, a, n_sms, stream);
   return split ? launch<true, 2>(c, a, n_sms, stream) : launch<false, 2>(c, a, n_sms, stream);
 }
 

@@ -465,3 +465,48 @@ def test_evict_contradictions_set_the_status(env):
             assert torch.equal(b.cache.k_codes[b.table[2, :3]], before[0][b.table[2, :3]])
         if fault == "page":     # what lay on it counts as nothing, and stays last
             assert (kept[0, :, :40] >= 16).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 1), (16, 2), (10, 2), (24, 2)])
+@pytest.mark.parametrize("new,ctx,prefix,readers", [
+    ([70], [0], [1], [1]), ([90, 40, 60], [0, 200, 31], [129, 600], [1, 2]), ([200, 30], [100, 5], [0, 77], [1, 1]),
+    ([130, 0, 100, 80], [5, 9, 300, 0], [128, 500, 3], [0, 3, 1]), ([64, 300], [1000, 3], [1500], [2])])
+def test_shared_many_rows(env, Hq, Hkv, new, ctx, prefix, readers):
+    """Sequences of many tokens, whose rows go over their prefix and their own keys in one pass: prefixes that end within a tile, at its
+    end, within 16 keys of it, that have no tokens; sequences without tokens, and shorter than what they bring."""
+    rng = np.random.default_rng(Hq + len(new))
+    for page in (16, 128):
+        b = Shared(rng, new, ctx, prefix, readers, Hkv, page)
+        b.dev(env)
+        b.d_start, b.d_len = i32(b.q_start), i32(b.kv_len)
+        q = bf16(rng, sum(new), Hq, D, mul=2.0)
+        check_shared(env, b, q)
+        check_shared(env, b, q, causal=False)
+        b.kv_len = np.maximum(0, b.kv_len - 90).astype(np.int32)
+        b.d_len = i32(b.kv_len)
+        check_shared(env, b, q)
+
+
+def test_shared_many_rows_contradictions(env):
+    """A sequence over the border of two prefixes, a length beyond the table, a page outside the pool."""
+    moe, torch = env
+    rng = np.random.default_rng(7)
+    new = [80, 90, 100]
+    for fault in ("border", "length", "page", "end"):
+        b = Shared(rng, new, [20, 0, 300], [100, 60], [1, 2], 2, 16)
+        b.dev(env)
+        b.d_start, b.d_len = i32(b.q_start), i32(b.kv_len)
+        start, length, table, most = b.prefix()
+        if fault == "border":
+            start[1] = 100
+        elif fault == "length":
+            length[1] = 1 << 20
+        elif fault == "page":
+            table[0, 3] = 1 << 20
+        else:
+            start[2] = 260
+        q = bf16(rng, sum(new), 8, D)
+        ws = moe.moe_paged_attention_shared_workspace(sum(new), 3, 8, 2, D, max(new), 2, sum(new))
+        out, lse = moe.moe_paged_attention_shared(q.cuda(), b.cache, b.d_start, b.d_len, i32(np.ascontiguousarray(b.table)), max(new),
+                                                  (start, length, table, sum(new)), ws=ws)
+        assert moe.moe_get_device_status(ws) == moe.MOE_ERR_DEVICE_CHECK, fault
