@@ -205,8 +205,9 @@ cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& args, 
   AttentionArgs a = args;
   a.limit_us = g_limit_us;
   a.withhold = g_withhold;
-  return attention_decode_fits(c.Hq / c.Hkv, a.max_q) ? launch_attention_decode(c, a, n_sms, stream)
-                                                      : launch_attention_prefill(c, a, n_sms, stream);
+  const bool few = attention_decode_fits(c.Hq / c.Hkv, a.max_q) ||
+                   ((a.pass == 1 || a.pass == 2) && attention_decode_chunks_fit(c, a.max_q, n_sms));
+  return few ? launch_attention_decode(c, a, n_sms, stream) : launch_attention_prefill(c, a, n_sms, stream);
 }
 
 }  // namespace moe

@@ -39,6 +39,7 @@ namespace moe {
 namespace {
 
 constexpr int kWholeTiles = 4;    // rows of at most so many tiles are not split
+constexpr int kSmallTiles = 6;    // tiles a block, at most, for which rows beyond 16 are taken 16 at a time
 constexpr int kMinRun = 4;        // tiles in a block's run, at least (4 sequences of 2000, 8 key/value heads: 21.6 us at 2,
                                   // 19.6 at 4, 23.7 at 6; one of 1000: 17.5, 17.5, 21.6)
 // p' = 2^(u - r + kBase) with u <= r + kSlack is at most 2^8; r moves so seldom that the sums in tensor memory are hardly ever
@@ -98,41 +99,51 @@ __device__ __forceinline__ int first_tile_from(long long rel, int nt, int own) {
   return rel <= 0 ? 0 : (int)min((long long)nt, max(own > 0 ? 1LL : 0LL, rel - own));
 }
 
-// A run of tiles of one (sequence, head): the tiles [i0, i1) of its nt.
+// A run of tiles of one item, the tiles [i0, i1) of its nt.  An item is a (sequence, head), in calls of two passes NC of its rows: each NC
+// of them go over the keys anew.
 struct Segment {
-  int b, h, i0, i1, later;  // later: not the item that the block's run begins in
+  int b, h, row0, i0, i1, later;  // later: not the item that the block's run begins in
   SeqRange s;
   KeyRange r;
 };
 
-// Walks the segments of a block's run: `left` of cost, from `rel` on in its first item.
-template <int kOwn>
+// Items of one head of a sequence.
+template <int NC, int kPass>
+__device__ __forceinline__ int row_chunks(const KvBatch& c, const SeqRange& s) {
+  return kPass == 0 ? 1 : (int)(((long long)(s.t1 - s.t0) * (c.Hq / c.Hkv) + NC - 1) / NC);
+}
+
+// Walks the segments of a block's run: `left` of cost, from `rel` on in its first item (number `u` of its sequence's, head by head).
+template <int NC, int kPass>
 struct Walk {
+  static constexpr int kOwn = kOwnCost<kPass>;
   const KvBatch& c;
   const AttentionArgs& a;
   long long left;
-  int b, h, rel, later = 0;
-  __device__ Walk(const KvBatch& c_, const AttentionArgs& a_, long long n, int b_, int h_, int rel_)
-      : c(c_), a(a_), left(n), b(b_), h(h_), rel(rel_) {}
+  int b, u, rel, later = 0;
+  __device__ Walk(const KvBatch& c_, const AttentionArgs& a_, long long n, int b_, int u_, int rel_)
+      : c(c_), a(a_), left(n), b(b_), u(u_), rel(rel_) {}
   __device__ bool next(Segment& g) {
     while (left > 0 && b < c.B) {
       const bool ok = load_seq(c, b, g.s);
       g.r = key_range(g.s, a);
       if (!ok || g.r.nt == 0) {
         ++b;
-        h = rel = 0;
+        u = rel = 0;
         continue;
       }
+      const int chunks = row_chunks<NC, kPass>(c, g.s);
       g.b = b;
-      g.h = h;
+      g.h = u / chunks;
+      g.row0 = kPass == 0 ? 0 : (u - g.h * chunks) * NC;
       g.i0 = first_tile_from(rel, g.r.nt, kOwn);
       g.i1 = first_tile_from(rel + left, g.r.nt, kOwn);
       g.later = later;
       left -= g.r.nt + kOwn - rel;
       rel = 0;
       later = 1;
-      if (++h == c.Hkv) {
-        h = 0;
+      if (++u == c.Hkv * chunks) {
+        u = 0;
         ++b;
       }
       if (g.i0 < g.i1) return true;
@@ -141,9 +152,14 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ int seq_tiles(const KvBatch& c, const AttentionArgs& a, int b) {
+// Tiles of a sequence's items, and their number for one head.
+template <int NC, int kPass>
+__device__ __forceinline__ int seq_tiles(const KvBatch& c, const AttentionArgs& a, int b, int& chunks) {
   SeqRange s;
-  return load_seq(c, b, s) ? key_range(s, a).nt : 0;
+  chunks = 1;
+  if (!load_seq(c, b, s)) return 0;
+  chunks = row_chunks<NC, kPass>(c, s);
+  return key_range(s, a).nt;
 }
 
 // Cost per block: equal runs over the grid.  (A run that begins within an item has a tile of it: the joins count on that.)
@@ -265,7 +281,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     long long mine, total;
     // the scan's scratch is the weights' operand, free until the roles start
     long long* s_warp = reinterpret_cast<long long*>(smem + C::kPOff);
-    const long long before = scan_batch(c, C::kThreads, s_warp, mine, total, [&](int b) { return item_cost(seq_tiles(c, a, b), kOwn); });
+    int chunks;
+    auto cost_of = [&](int nt) { return item_cost(nt, kOwn) * chunks; };
+    const long long before = scan_batch(c, C::kThreads, s_warp, mine, total,
+                                        [&](int b) { return cost_of(seq_tiles<NC, kPass>(c, a, b, chunks)); });
     const long long all = total * c.Hkv, per = cost_per_block(all, gridDim.x, kOwn);
     const long long begin = (long long)blockIdx.x * per;
     run = min(per, all - begin);
@@ -277,9 +296,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     if (before * c.Hkv <= begin && begin < (before + mine) * c.Hkv) {
       long long at = before;
       int b = tid * ((c.B + C::kThreads - 1) / C::kThreads), nt;
-      while ((at + item_cost(nt = seq_tiles(c, a, b), kOwn)) * c.Hkv <= begin) {
-        at += item_cost(nt, kOwn);
-        ++b;
+      for (;; ++b) {
+        nt = seq_tiles<NC, kPass>(c, a, b, chunks);
+        if ((at + cost_of(nt)) * c.Hkv > begin) break;
+        at += cost_of(nt);
       }
       const int cost = nt + kOwn;
       const long long rel = (begin - at * c.Hkv) % cost;
@@ -293,7 +313,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       if (j.split) {
         const long long start = begin - rel;
         j.b = b;
-        j.h = s_begin[1];
+        j.h = s_begin[1] / chunks;
+        j.row0 = (s_begin[1] - j.h * chunks) * NC;
         j.c0 = (int)(start / per);
         j.c1 = (int)((start + cost - 1) / per);
         j.slot0 = start > j.c0 * per ? 1 : 0;
@@ -301,15 +322,17 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
       info[blockIdx.x] = j;
     }
   } else {
-    const int b = (int)blockIdx.x / c.Hkv;
-    run = item_cost(seq_tiles(c, a, b), kOwn);
-    if (run <= 0) {
+    const int units = (int)gridDim.x / c.B, b = (int)blockIdx.x / units, u = (int)blockIdx.x - b * units;  // the most items of a sequence
+    int chunks;
+    run = item_cost(seq_tiles<NC, kPass>(c, a, b, chunks), kOwn);
+    if (kPass > 0 && run > 0 && c.Hkv * chunks > units && tid == 0) set_status(c.status, DEV_ERR_CONFIG);  // more new tokens than max_q
+    if (run <= 0 || u >= c.Hkv * chunks) {
       if (kPass == 2) pdl_wait();
       return;
     }
     if (tid == 0) {
       s_begin[0] = b;
-      s_begin[1] = (int)blockIdx.x - b * c.Hkv;
+      s_begin[1] = u;
       s_begin[2] = 0;
     }
   }
@@ -346,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk<kOwn> walk(c, a, run, s_begin[0], s_begin[1], s_begin[2]);
+  Walk<NC, kPass> walk(c, a, run, s_begin[0], s_begin[1], s_begin[2]);
   Segment g;
 
   if (warp == C::kTmaWarp) {
@@ -492,7 +515,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     // ------------------------------------------------------------ queries
     uint32_t n = 0;
     while (walk.next(g)) {
-      const int qb = (int)(n % C::kQBufs), rows = g.s.t1 - g.s.t0, cols = min(NC, rows * G);
+      const int qb = (int)(n % C::kQBufs), rows = g.s.t1 - g.s.t0, cols = min(NC, rows * G - g.row0);
       constexpr int kAtOnce = 8;  // rows
       uint2 raw[kAtOnce];
       auto load = [&](int x0) {
@@ -500,9 +523,9 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         for (int x = 0; x < kAtOnce; ++x) {
           raw[x] = make_uint2(0, 0);
           if (x0 + x < cols) {
-            const int i = (x0 + x) / G;
+            const int rho = g.row0 + x0 + x, i = rho / G;
             raw[x] = __ldg(reinterpret_cast<const uint2*>(a.q + (size_t)(g.s.t0 + i) * a.q_stride +
-                                                         (size_t)(g.h * G + x0 + x - i * G) * kHeadDim) + lane);
+                                                         (size_t)(g.h * G + rho - i * G) * kHeadDim) + lane);
           }
         }
       };
@@ -537,11 +560,11 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           *reinterpret_cast<uint32_t*>(op + (NC + x0 + x) * 128 + sw) = lo;
           if (lane == 0) {
             s_qf[qb * NC + x0 + x] = a.scale_log2 * exp2_int(e);
-            s_tok[qb * NC + x0 + x] = x0 + x < cols ? (x0 + x) / G : 0;
+            s_tok[qb * NC + x0 + x] = x0 + x < cols ? (g.row0 + x0 + x) / G : 0;
           }
         }
       }
-      if (rows * G > NC && lane == 0) set_status(c.status, DEV_ERR_CONFIG);  // more new tokens than max_q
+      if (kPass == 0 && rows * G > NC && lane == 0) set_status(c.status, DEV_ERR_CONFIG);  // more new tokens than max_q
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qb]);
@@ -685,8 +708,11 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         if (ok && lane == 0) mbar_arrive(&p_full[n & 1u]);
       }
       const bool complete = g.i0 == 0 && g.i1 == g.r.nt;
-      const int cols = min(NC, rows * G);
-      auto row_of = [&](int col) { return (size_t)(g.s.t0 + col / G) * c.Hq + g.h * G + col % G; };
+      const int cols = min(NC, rows * G - g.row0);
+      auto row_of = [&](int col) {
+        const int rho = g.row0 + col, i = rho / G;
+        return (size_t)(g.s.t0 + i) * c.Hq + g.h * G + rho - i * G;
+      };
       float before[N], prior[N];  // of the pass before, on their way while the last sums are waited for
       if (kPass == 2 && complete) {
         pdl_wait();
@@ -773,7 +799,8 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   if (e != cudaSuccess) return e;
   // Rows of a few tiles at most (the table's width bounds them) are one block's each: nothing to join.
   const bool split = (long long)c.max_pages * c.page > kWholeTiles * kTile;
-  const int blocks = split ? blocks_of(n_sms) : c.B * c.Hkv;
+  const int chunks = kPass == 0 ? 1 : (int)(((long long)(c.Hq / c.Hkv) * a.max_q + NC - 1) / NC);
+  const int blocks = split ? blocks_of(n_sms) : c.B * c.Hkv * chunks;
   float* part_o = reinterpret_cast<float*>(a.scratch);
   float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)2 * blocks_of(n_sms) * NC * kHeadDim);
   JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)2 * blocks_of(n_sms) * NC);
@@ -786,6 +813,15 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
 }  // namespace
 
 bool attention_decode_fits(int G, int max_q) { return (long long)G * max_q <= 16; }
+
+// More rows than that, 16 at a time, where there are so few keys that the way to the first scores counts: it takes this kernel 6 us and the
+// other one 11, and a part's end 2 and 6.  Keys as the tables' widths bound them, six tiles a block at most: 10 sequences of up to 7
+// tokens, 2 key/value heads, behind 86-259 tokens 67 -> 35 us; at seven tiles a block (30 sequences behind 2193-2925, 4 key/value heads)
+// 45 -> 48, at ten (21 of up to 5 tokens over 700, 8 heads) 123 -> 134.
+bool attention_decode_chunks_fit(const KvBatch& c, int max_q, int n_sms) {
+  const long long chunks = ((long long)(c.Hq / c.Hkv) * max_q + 15) / 16, tiles = ((long long)c.max_pages * c.page + kTile - 1) / kTile;
+  return chunks * c.B * c.Hkv * tiles <= (long long)kSmallTiles * blocks_of(n_sms);
+}
 
 size_t attention_decode_scratch(int G, int max_q, int n_sms) {
   const int nc = width_of(G * max_q);

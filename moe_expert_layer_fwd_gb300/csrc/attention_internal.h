@@ -115,6 +115,7 @@ cudaError_t launch_kv_evict(const KvBatch& c, const KvEvictArgs& e, int n_sms, c
 
 // Few query rows per key/value head: G grouped heads times max_q new tokens at most 16.
 bool attention_decode_fits(int G, int max_q);
+bool attention_decode_chunks_fit(const KvBatch& c, int max_q, int n_sms);  // or 16 of them at a time (calls of two passes)
 size_t attention_decode_scratch(int G, int max_q, int n_sms);
 cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
 
