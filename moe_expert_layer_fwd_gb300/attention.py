@@ -140,9 +140,10 @@ def moe_rope_rows(positions, axes, cos_sin, rows=None, ws=None, stream=None):
         raise ValueError(f"positions: the tokens of an axis must be dense, got strides {positions.stride()}")
     if cos_sin.dim() != 2 or len(axes) * 2 != cos_sin.shape[1]:
         raise ValueError(f"axes: expected one for each frequency of cos_sin {tuple(cos_sin.shape)}, got {len(axes)}")
-    if any(not 0 <= x < n_axes for x in axes):
-        raise ValueError(f"axes: expected numbers of the {n_axes} axes, got {tuple(axes)}")
     max_pos, rot_dim = cos_sin.shape
+    codes = bytes(axes)  # (raises for what is no byte)
+    if rot_dim and max(codes) >= n_axes:
+        raise ValueError(f"axes: expected numbers of the {n_axes} axes, got {tuple(axes)}")
     cs = _need(cos_sin, "cos_sin", b.f32, cos_sin.shape)
     rp = None if rows is None else _need(rows, "rows", b.f32, (T, rot_dim))
     ws = _status_ws(positions, ws, stream)
@@ -150,7 +151,7 @@ def moe_rope_rows(positions, axes, cos_sin, rows=None, ws=None, stream=None):
         rows = _new(stream, positions, (T, rot_dim), b.f32)
         rp = rows.data_ptr()
     stride = positions.stride(0) if n_axes > 1 else T
-    status = b.rope_rows(n_axes, T, positions.data_ptr(), stride, bytes(axes), cs, max_pos, rot_dim, rp, ws.data_ptr(), ws.numel(),
+    status = b.rope_rows(n_axes, T, positions.data_ptr(), stride, codes, cs, max_pos, rot_dim, rp, ws.data_ptr(), ws.numel(),
                          _stream_of(stream, positions))
     if status:
         _m._check(status, "moe_rope_rows")
