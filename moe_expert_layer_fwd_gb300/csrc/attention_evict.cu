@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) kv_select_kernel(const KvBatch c, co
   const int lo = (int)min((long long)len, (long long)rank * share), n = min(share, len - lo);
   const int32_t* table = c.page_table + (size_t)b * c.max_pages;
   const int stay0 = min(e.sink, len), stay1 = max(stay0, len - min(e.recent, len));  // tokens before the one and from the other on
-  auto to_key = [&](float w, int j) { return j < stay0 || j >= stay1 ? kStays : w > 0.f ? __float_as_uint(w) : 0u; };
+  auto to_key = [&](float w, int j) { return j < stay0 || j >= stay1 ? kStays : w > 0.f ? __float_as_uint(w) : 0u; };  // (behind the end: stays)
   // the weights of the tokens from lo + i on, as far as their page goes (nullptr: on no page)
   auto weights_at = [&](int i) -> const float* {
     const int j = lo + i, p = __ldg(table + (j >> c.page_log2));
@@ -116,10 +116,18 @@ __global__ void __launch_bounds__(kThreads) kv_select_kernel(const KvBatch c, co
 #pragma unroll
     for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-      const uint32_t k = key(i);
+    auto count = [&](uint32_t k) {
       if ((k & seen) == prefix) atomicAdd(&hist[k >> shift & mask], 1u);
+    };
+#pragma unroll 2
+    for (int i = 4 * tid; i < cached; i += 4 * kThreads) {
+      const uint4 k = *reinterpret_cast<const uint4*>(s_keys + i);
+      count(k.x);
+      count(k.y);
+      count(k.z);
+      count(k.w);
     }
+    for (int i = cached + tid; i < n; i += kThreads) count(key(i));
     if (ranks > 1) cluster_sync(); else __syncthreads();
     // the digit, from the top: thread t has the bins kBins - 1 - 2t and the one below it
     const int top = kBins - 1 - 2 * tid;
