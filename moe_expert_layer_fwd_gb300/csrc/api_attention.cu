@@ -206,7 +206,7 @@ size_t moe_paged_attention_shared_workspace_size(const moe_kv_desc* d, int max_q
   if (prefix_desc(d, prefix, &pd)) return 0;
   if (shared_joins(d, &pd)) return kHeader + scratch;
   const size_t rows = (size_t)d->T * d->Hq;
-  return kHeader + up256(rows * moe::kHeadDim * sizeof(float)) + up256(rows * sizeof(float)) +
+  return kHeader + 2 * (up256(rows * moe::kHeadDim * sizeof(float)) + up256(rows * sizeof(float))) +
          up256(moe::attention_scratch_bytes(d->Hq, d->Hkv, prefix->max_q, sm_count())) + scratch;
 }
 
@@ -230,19 +230,20 @@ int moe_paged_attention_shared(const moe_kv_desc* d, const uint16_t* q, long lon
   c.q_start = q_start;
   c.kv_len = kv_len;
   char* at = (char*)ws + kHeader;
-  float *rows = nullptr, *rows_lse = nullptr;
-  void* prefix_scratch = nullptr;
+  moe::SharedBuffers buffers = {};
   if (prefix) {
     pc = make_batch(&pd, kv, prefix->page_table, (unsigned*)ws);
     pc.q_start = prefix->q_start;
     pc.kv_len = prefix->len;
   }
   if (prefix && !shared_joins(d, &pd)) {
-    rows = (float*)at;
-    at += up256((size_t)d->T * d->Hq * moe::kHeadDim * sizeof(float));
-    rows_lse = (float*)at;
-    at += up256((size_t)d->T * d->Hq * sizeof(float));
-    prefix_scratch = at;
+    for (int i = 0; i < 2; ++i) {
+      buffers.rows[i] = (float*)at;
+      at += up256((size_t)d->T * d->Hq * moe::kHeadDim * sizeof(float));
+      buffers.lse[i] = (float*)at;
+      at += up256((size_t)d->T * d->Hq * sizeof(float));
+    }
+    buffers.prefix_scratch = at;
     at += up256(moe::attention_scratch_bytes(d->Hq, d->Hkv, prefix->max_q, sm_count()));
   }
   moe::AttentionArgs a = {};
@@ -256,8 +257,7 @@ int moe_paged_attention_shared(const moe_kv_desc* d, const uint16_t* q, long lon
   a.scratch = at;
   a.lse = lse;
   a.lse_unit = 0.693147180559945309f;
-  return cuda_status(moe::launch_shared_attention(pc, prefix ? prefix->max_q : 0, prefix_scratch, c, a, rows, rows_lse, sm_count(),
-                                                  (cudaStream_t)stream));
+  return cuda_status(moe::launch_shared_attention(pc, prefix ? prefix->max_q : 0, c, a, buffers, sm_count(), (cudaStream_t)stream));
 }
 
 int moe_kv_weights(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const float* lse, const int32_t* q_start,

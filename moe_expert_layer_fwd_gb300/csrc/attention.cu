@@ -13,39 +13,29 @@ constexpr int kJoinThreads = 256;
 // out = sum_k 2^(r_k - r) o_k / sum_k 2^(r_k - r) l_k over an item's parts, in their order.  kWarps warps share a row and
 // split its parts (few rows, many parts: decoding), or each has a row (kWarps = 1); a lane has four dims.  Blocks whose run
 // (blockIdx.x) does not hold an item's second part have nothing to do.
-template <int kWarps, int kPass>
+template <int kWarps>
 __global__ void __launch_bounds__(kJoinThreads)
-    attention_join_kernel(const KvBatch c, const AttentionArgs a, int rows, float base, const float* part_o,
-                          const float2* part_rl, const JoinInfo* info) {
+    attention_join_kernel(const KvBatch c, const AttentionArgs a, const AttentionParts p) {
   __shared__ float4 s_acc[kJoinThreads];
   __shared__ float s_sum[kJoinThreads / 32];
-  if (kPass == 1) pdl_launch_dependents();
   pdl_wait();
-  const JoinInfo j = info[blockIdx.x];
+  const JoinInfo j = p.info[blockIdx.x];
   if (!j.split || j.c0 != (int)blockIdx.x - 1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = c.Hq / c.Hkv;
   const int row = (int)blockIdx.y * (kJoinThreads / 32 / kWarps) + warp / kWarps, sub = warp % kWarps;
   const int t0 = __ldg(c.q_start + j.b), t1 = __ldg(c.q_start + j.b + 1);
-  const bool live = row < rows && j.row0 + row < (t1 - t0) * G;
-  auto part = [&](int k) { return (size_t)(2 * k + (k == j.c0 ? j.slot0 : 0)) * rows + row; };
-  const int rho = j.row0 + row, i = rho / G;
-  const size_t at = (size_t)(t0 + i) * c.Hq + j.h * G + rho - i * G;
-  float before = -CUDART_INF_F;  // of the pass before, on its way while the parts are read
-  float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (kPass == 2 && live && a.prior) {
-    before = prior_lse(a, at);
-    p = reinterpret_cast<const float4*>(a.prior + at * kHeadDim)[lane];
-  }
+  const bool live = row < p.rows && j.row0 + row < (t1 - t0) * G;
+  auto part = [&](int k) { return (size_t)(2 * k + (k == j.c0 ? j.slot0 : 0)) * p.rows + row; };
   float top = -CUDART_INF_F, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (live) {
-    for (int k = j.c0 + lane; k <= j.c1; k += 32) top = fmaxf(top, part_rl[part(k)].x);
+    for (int k = j.c0 + lane; k <= j.c1; k += 32) top = fmaxf(top, p.rl[part(k)].x);
     top = warp_max(top);
     const float ref = top == -CUDART_INF_F ? 0.f : top;
 #pragma unroll 4
     for (int k = j.c0 + sub; k <= j.c1; k += kWarps) {
-      const float2 rl = part_rl[part(k)];
-      const float4 o = reinterpret_cast<const float4*>(part_o + part(k) * kHeadDim)[lane];
+      const float2 rl = p.rl[part(k)];
+      const float4 o = reinterpret_cast<const float4*>(p.o + part(k) * kHeadDim)[lane];
       const float f = ex2(rl.x - ref);
       sum = fmaf(rl.y, f, sum);
       acc.x = fmaf(o.x, f, acc.x);
@@ -71,31 +61,127 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
   if (!live) return;
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
-  if (kPass > 0) {
-    const RowEnd e = end_row<kPass>(a, at, inv, top - base, sum, before, lane == 0);
-    acc = make_float4(acc.x * e.f, acc.y * e.f, acc.z * e.f, acc.w * e.f);
-    if (kPass == 2 && a.prior) {
-      acc = make_float4(fmaf(p.x, e.f1, acc.x), fmaf(p.y, e.f1, acc.y), fmaf(p.z, e.f1, acc.z), fmaf(p.w, e.f1, acc.w));
-    }
-    if (kPass == 1) reinterpret_cast<float4*>(a.out32 + at * kHeadDim)[lane] = acc;
-    else reinterpret_cast<uint2*>(a.out + at * kHeadDim)[lane] = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-    return;
-  }
+  const int rho = j.row0 + row, i = rho / G;
+  const size_t at = (size_t)(t0 + i) * c.Hq + j.h * G + rho - i * G;
   uint16_t* out = a.out + at * kHeadDim;
   reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (a.lse && lane == 0) write_lse(a, at, top - p.base, sum);
+}
+
+// Ends two passes: out = sum_k 2^(x_k) o_k / sum_k 2^(x_k) l_k over what either left of a row, its parts where it was split (x = r - base)
+// or else the row itself (x the logarithm of its denominator, l = 1), and lse = log2 of that denominator.  kWarps warps a row, as above.
+struct PassRows {
+  const int32_t* q_start;
+  int B;
+  const float* rows;
+  const float* lse;
+  AttentionParts parts;
+};
+// The parts of one row, as a pass left it.
+struct RowParts {
+  int n, c0, slot0;  // n parts, of the blocks from c0 on; c0 < 0: the row itself
+  size_t row;        // of a part
+  float whole;       // the row's denominator
+};
+__device__ __forceinline__ RowParts row_parts(const PassRows& s, int Hq, int G, int t, int head) {
+  const size_t at = (size_t)t * Hq + head;
+  RowParts r = {1, -1, 0, at, s.lse[at]};
+  const unsigned mark = __float_as_uint(r.whole);
+  if ((mark & 0xFFC00000u) != kSplitMark) return r;
+  // (a row that no block wrote may hold anything: what it says is checked before it is used)
+  const int k = (int)(mark & 0x3FFFFFu) + 1;
+  r.n = 0;
+  if (k >= s.parts.blocks) return r;
+  const JoinInfo j = s.parts.info[k];
+  if (!j.split || j.c0 != k - 1 || j.c1 < k || j.c1 >= s.parts.blocks || j.b < 0 || j.b >= s.B || (j.slot0 & ~1)) return r;
+  const int rho = (t - __ldg(s.q_start + j.b)) * G + head - j.h * G - j.row0;
+  if (rho < 0 || rho >= s.parts.rows) return r;
+  r.n = j.c1 - j.c0 + 1;
+  r.c0 = j.c0;
+  r.slot0 = j.slot0;
+  r.row = (size_t)rho;
+  return r;
+}
+__device__ __forceinline__ size_t part_at(const PassRows& s, const RowParts& r, int k) {
+  return (size_t)(2 * (r.c0 + k) + (k == 0 ? r.slot0 : 0)) * s.parts.rows + r.row;
+}
+
+template <int kWarps>
+__global__ void __launch_bounds__(kJoinThreads)
+    attention_end_kernel(const PassRows s0, const PassRows s1, int Hq, int G, long long rows, const AttentionArgs a) {
+  __shared__ float4 s_acc[kJoinThreads];
+  __shared__ float s_sum[kJoinThreads / 32];
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % kWarps;
+  const long long row = (long long)blockIdx.x * (kJoinThreads / 32 / kWarps) + warp / kWarps;
+  const bool live = row < rows;
+  float top = -CUDART_INF_F, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
+    const int t = (int)(row / Hq), head = (int)(row - (long long)t * Hq);
+    const RowParts r0 = row_parts(s0, Hq, G, t, head), r1 = row_parts(s1, Hq, G, t, head);
+    auto highest = [&](const PassRows& s, const RowParts& r) {
+      if (r.c0 < 0) {
+        if (r.n) top = fmaxf(top, r.whole);
+      } else {
+        for (int k = lane; k < r.n; k += 32) top = fmaxf(top, s.parts.rl[part_at(s, r, k)].x - s.parts.base);
+      }
+    };
+    highest(s0, r0);
+    highest(s1, r1);
+    top = warp_max(top);
+    const float ref = top == -CUDART_INF_F ? 0.f : top;
+    auto add = [&](float x, float l, const float4& o) {
+      const float f = ex2(x - ref);
+      sum = fmaf(l, f, sum);
+      acc.x = fmaf(o.x, f, acc.x);
+      acc.y = fmaf(o.y, f, acc.y);
+      acc.z = fmaf(o.z, f, acc.z);
+      acc.w = fmaf(o.w, f, acc.w);
+    };
+    auto add_all = [&](const PassRows& s, const RowParts& r, int from) {
+      if (r.c0 < 0) {
+        if (r.n && sub == from) add(r.whole, 1.f, reinterpret_cast<const float4*>(s.rows + r.row * kHeadDim)[lane]);
+      } else {
+#pragma unroll 4
+        for (int k = sub; k < r.n; k += kWarps) {
+          const size_t at = part_at(s, r, k);
+          const float2 rl = s.parts.rl[at];
+          add(rl.x - s.parts.base, rl.y, reinterpret_cast<const float4*>(s.parts.o + at * kHeadDim)[lane]);
+        }
+      }
+    };
+    add_all(s0, r0, 0);
+    add_all(s1, r1, kWarps - 1);
+  }
+  if (kWarps > 1) {
+    s_acc[threadIdx.x] = acc;
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 o = s_acc[threadIdx.x + 32 * w];
+      sum += s_sum[warp + w];
+      acc.x += o.x;
+      acc.y += o.y;
+      acc.z += o.z;
+      acc.w += o.w;
+    }
+  }
+  if (!live) return;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  reinterpret_cast<uint2*>(a.out + (size_t)row * kHeadDim)[lane] =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0) write_lse(a, (size_t)row, top, sum);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& args, int blocks, int rows, float base, const float* part_o,
-                                  const float2* part_rl, const JoinInfo* info, cudaStream_t stream) {
-  AttentionArgs a = args;
-  if (a.pass == 3) a.prior = nullptr;  // the prefixes' tables lie there; their keys are in the sums
+cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, const AttentionParts& p, cudaStream_t stream) {
   constexpr int kAll = kJoinThreads / 32;
-  auto kern = rows <= 32 ? (a.pass == 0 ? attention_join_kernel<kAll, 0> : a.pass == 1 ? attention_join_kernel<kAll, 1> : attention_join_kernel<kAll, 2>)
-                         : (a.pass == 0 ? attention_join_kernel<1, 0> : a.pass == 1 ? attention_join_kernel<1, 1> : attention_join_kernel<1, 2>);
-  const dim3 grid(blocks, rows <= 32 ? rows : (rows + kAll - 1) / kAll);
-  return launch_kernel(kern, grid, dim3(kJoinThreads), 0, stream, true, c, a, rows, base, part_o, part_rl, info);
+  if (p.rows <= 32) return launch_kernel(attention_join_kernel<kAll>, dim3(p.blocks, p.rows), dim3(kJoinThreads), 0, stream, true, c, a, p);
+  return launch_kernel(attention_join_kernel<1>, dim3(p.blocks, (p.rows + kAll - 1) / kAll), dim3(kJoinThreads), 0, stream, true, c, a, p);
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -153,44 +239,57 @@ int attention_debug_set(int what, unsigned long long value) {
 
 // Above 128 rows per key/value head and sequence, on average, an item of 256 rows is a sequence's own anyhow, and the prefix's tiles come
 // from L2 whoever asks: one pass saves the second one's items and the rows in between (16 sequences of 20-250 tokens, 8 heads a
-// key/value head, behind 4001: 254 us as two passes, 191 as one).  Below, rows of several sequences share the tiles.
+// key/value head, behind 4001: 254 us as two passes, 194 as one).  Below, rows of several sequences share the tiles.
 bool shared_attention_joins(const KvBatch& prefixes, const KvBatch& c) {
   return (long long)c.T * (c.Hq / c.Hkv) > 128LL * c.B &&
          ((long long)prefixes.max_pages + c.max_pages) * c.page < (1LL << 31) - 2048;
 }
 
 // Two passes, each with the kernel that its rows per key/value head call for: over the prefixes, whose readers' tokens are one
-// sequence that sees all of it (so a prefix is read once for all of them, and its rows fill the tiles), then over the
-// sequences' own tokens, whose ends add the first pass's rows.  The rows in between are fp32.  The second pass starts while the
-// first one ends (scratch of its own, and it waits for the first one's rows where it needs them): a block's way to its first
-// scores takes 6 us.
-cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, void* prefix_scratch, const KvBatch& c,
-                                    const AttentionArgs& args, float* rows, float* rows_lse, int n_sms, cudaStream_t stream) {
+// sequence that sees all of it (so a prefix is read once for all of them, and its rows fill the tiles), and over the sequences' own
+// tokens; then one kernel that ends both, parts of split rows among them.  What is between them is fp32.  The second pass starts
+// where the first one's blocks have ended: a block's way to its first scores takes 6 us.  (With each pass's parts joined by itself, and
+// the second one adding the first one's rows: 64 sequences behind 8200 tokens 93 us instead of 84, 12 behind 224-943 64 instead of 33.)
+cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, const KvBatch& c, const AttentionArgs& args,
+                                    const SharedBuffers& s, int n_sms, cudaStream_t stream) {
   AttentionArgs a = args;
-  a.pass = 2;
-  if (prefixes.B && !rows) {
+  if (!prefixes.B) {
+    a.pass = 2;
+    return launch_paged_attention(c, a, n_sms, stream);
+  }
+  if (shared_attention_joins(prefixes, c)) {
     a.pass = 3;
     a.n_prefixes = prefixes.B;
     a.prefix_max_pages = prefixes.max_pages;
     a.prefix_start = prefixes.q_start;
     a.prefix_len = prefixes.kv_len;
     a.prefix_table = prefixes.page_table;
+    return launch_paged_attention(c, a, n_sms, stream);
   }
-  if (rows) {
+  PassRows left[2] = {{prefixes.q_start, prefixes.B, s.rows[0], s.lse[0], {}}, {c.q_start, c.B, s.rows[1], s.lse[1], {}}};
+  for (int i = 0; i < 2; ++i) {
     AttentionArgs p = a;
     p.pass = 1;
-    p.causal = p.window = 0;
-    p.max_q = max_prefix_q;
-    p.scratch = prefix_scratch;
-    p.out32 = rows;
-    p.lse = rows_lse;
+    p.follows = i;
+    p.out32 = s.rows[i];
+    p.lse = s.lse[i];
     p.lse_unit = 1.f;
-    const cudaError_t e = launch_paged_attention(prefixes, p, n_sms, stream);
+    if (i == 0) {
+      p.causal = 0;
+      p.max_q = max_prefix_q;
+      p.scratch = s.prefix_scratch;
+    }
+    const cudaError_t e = launch_paged_attention(i == 0 ? prefixes : c, p, n_sms, stream, &left[i].parts);
     if (e != cudaSuccess) return e;
-    a.prior = rows;
-    a.prior_lse = rows_lse;
   }
-  return launch_paged_attention(c, a, n_sms, stream);
+  // warps enough for all SMs, as far as a row's parts go round
+  constexpr int kAll = kJoinThreads / 32;
+  const long long rows = (long long)c.T * c.Hq;
+  const int G = c.Hq / c.Hkv;
+  if (rows <= 4LL * n_sms)
+    return launch_kernel(attention_end_kernel<kAll>, dim3((unsigned)rows), dim3(kJoinThreads), 0, stream, true, left[0], left[1], c.Hq, G, rows, a);
+  return launch_kernel(attention_end_kernel<1>, dim3((unsigned)((rows + kAll - 1) / kAll)), dim3(kJoinThreads), 0, stream, true, left[0], left[1],
+                       c.Hq, G, rows, a);
 }
 
 cudaError_t launch_kv_weights(const KvBatch& c, const AttentionArgs& args, const float* lse, const float* weight_in, float* weight_out,
@@ -201,13 +300,13 @@ cudaError_t launch_kv_weights(const KvBatch& c, const AttentionArgs& args, const
   return launch_kv_weights_rows(c, a, lse, weight_in, weight_out, n_sms, stream);
 }
 
-cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& args, int n_sms, cudaStream_t stream) {
+cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& args, int n_sms, cudaStream_t stream, AttentionParts* parts) {
   AttentionArgs a = args;
   a.limit_us = g_limit_us;
   a.withhold = g_withhold;
   const bool few = attention_decode_fits(c.Hq / c.Hkv, a.max_q) ||
                    ((a.pass == 1 || a.pass == 2) && attention_decode_chunks_fit(c, a.max_q, n_sms));
-  return few ? launch_attention_decode(c, a, n_sms, stream) : launch_attention_prefill(c, a, n_sms, stream);
+  return few ? launch_attention_decode(c, a, n_sms, stream, parts) : launch_attention_prefill(c, a, n_sms, stream, parts);
 }
 
 }  // namespace moe

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     run = min(per, all - begin);
     if (run <= 0) {
       if (tid == 0) info[blockIdx.x].split = 0;
-      if (kPass == 2) pdl_wait();  // this pass does not end before the one that it may overlap
+      if (kPass == 1) pdl_wait();  // this pass does not end before the one that it may overlap
       return;
     }
     if (before * c.Hkv <= begin && begin < (before + mine) * c.Hkv) {
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     run = item_cost(seq_tiles<NC, kPass>(c, a, b, chunks), kOwn);
     if (kPass > 0 && run > 0 && c.Hkv * chunks > units && tid == 0) set_status(c.status, DEV_ERR_CONFIG);  // more new tokens than max_q
     if (run <= 0 || u >= c.Hkv * chunks) {
-      if (kPass == 2) pdl_wait();
+      if (kPass == 1) pdl_wait();
       return;
     }
     if (tid == 0) {
@@ -713,17 +713,6 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         const int rho = g.row0 + col, i = rho / G;
         return (size_t)(g.s.t0 + i) * c.Hq + g.h * G + rho - i * G;
       };
-      float before[N], prior[N];  // of the pass before, on their way while the last sums are waited for
-      if (kPass == 2 && complete) {
-        pdl_wait();
-#pragma unroll
-        for (int x = 0; x < N; ++x) {
-          const int col = col0 + x;
-          const bool has = a.prior && col < cols;
-          before[x] = has ? prior_lse(a, row_of(col)) : -CUDART_INF_F;
-          prior[x] = has ? a.prior[row_of(col) * kHeadDim + key] : 0.f;
-        }
-      }
       if (ok) ok = warp_wait(&o_full[(n - 1u) & 1u], ((n - 1u) >> 1) & 1u, abort_flag, c.status);
       float acc[N];
 #pragma unroll
@@ -757,25 +746,21 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
         if (col < cols) {
           if (complete) {
             const size_t at = row_of(col);
-            if (kPass > 0) {
-              const RowEnd e = end_row<kPass>(a, at, sum != 0.f ? 1.f / sum : 0.f, r[x] - kBase, sum, before[x], key == 0);
-              float o = acc[x] * e.f;
-              if (kPass == 2 && a.prior) o = fmaf(prior[x], e.f1, o);
-              if (kPass == 1) a.out32[at * kHeadDim + key] = o;
-              else a.out[at * kHeadDim + key] = f32_to_bf16_rne(o);
-            } else {
-              a.out[at * kHeadDim + key] = f32_to_bf16_rne(sum != 0.f ? acc[x] / sum : 0.f);
-            }
+            const float o = sum != 0.f ? acc[x] / sum : 0.f;
+            if (kPass == 1) a.out32[at * kHeadDim + key] = o;
+            else a.out[at * kHeadDim + key] = f32_to_bf16_rne(o);
+            if (kPass > 0 && key == 0) write_lse(a, at, r[x] - kBase, sum);
           } else {
             part_o[((size_t)slot * NC + col) * kHeadDim + key] = acc[x];
             if (key == 0) part_rl[(size_t)slot * NC + col] = make_float2(r[x], sum);
+            if (kPass == 1 && key == 0 && g.i0 == 0) mark_split(a, row_of(col));
           }
         }
       }
       ++segs;
     }
   }
-  if (kPass == 2) pdl_wait();
+  if (kPass == 1) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == C::kMmaWarp) {
@@ -789,7 +774,7 @@ int width_of(int cols) { return cols <= 8 ? 8 : 16; }
 int blocks_of(int n_sms) { return 2 * n_sms; }
 
 template <int NC, int kPass>
-cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
+cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream, AttentionParts* parts) {
   using C = Cfg<NC>;
   CUtensorMap tk, tv;
   if (!make_cache_map(&tk, c.k_codes, c) || !make_cache_map(&tv, c.v_codes, c)) return cudaErrorInvalidValue;
@@ -804,10 +789,12 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   float* part_o = reinterpret_cast<float*>(a.scratch);
   float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)2 * blocks_of(n_sms) * NC * kHeadDim);
   JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)2 * blocks_of(n_sms) * NC);
-  e = launch_kernel(kern, dim3(blocks), dim3(C::kThreads), C::kBytes, stream, kPass == 2 && a.prior, tk, tv, c, a, (int)split, part_o, part_rl,
+  e = launch_kernel(kern, dim3(blocks), dim3(C::kThreads), C::kBytes, stream, kPass == 1 && a.follows, tk, tv, c, a, (int)split, part_o, part_rl,
                     info);
-  if (e != cudaSuccess || !split) return e;
-  return launch_attention_join(c, a, blocks, NC, kBase, part_o, part_rl, info, stream);
+  const AttentionParts p = {split ? blocks : 0, NC, kBase, part_o, part_rl, info};
+  if (kPass == 1) *parts = p;
+  if (kPass == 1 || e != cudaSuccess || !split) return e;
+  return launch_attention_join(c, a, p, stream);
 }
 
 }  // namespace
@@ -828,11 +815,11 @@ size_t attention_decode_scratch(int G, int max_q, int n_sms) {
   return blocks_of(n_sms) * ((size_t)2 * nc * (kHeadDim * sizeof(float) + sizeof(float2)) + sizeof(JoinInfo));
 }
 
-cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
+cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream, AttentionParts* parts) {
   const bool narrow = width_of(c.Hq / c.Hkv * a.max_q) == 8;
-  if (a.pass == 0) return narrow ? launch<8, 0>(c, a, n_sms, stream) : launch<16, 0>(c, a, n_sms, stream);
-  if (a.pass == 1) return narrow ? launch<8, 1>(c, a, n_sms, stream) : launch<16, 1>(c, a, n_sms, stream);
-  return narrow ? launch<8, 2>(c, a, n_sms, stream) : launch<16, 2>(c, a, n_sms, stream);
+  if (a.pass == 0) return narrow ? launch<8, 0>(c, a, n_sms, stream, parts) : launch<16, 0>(c, a, n_sms, stream, parts);
+  if (a.pass == 1) return narrow ? launch<8, 1>(c, a, n_sms, stream, parts) : launch<16, 1>(c, a, n_sms, stream, parts);
+  return narrow ? launch<8, 2>(c, a, n_sms, stream, parts) : launch<16, 2>(c, a, n_sms, stream, parts);
 }
 
 }  // namespace moe

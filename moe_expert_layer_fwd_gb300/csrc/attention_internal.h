@@ -60,17 +60,14 @@ struct AttentionArgs {
   unsigned limit_us;          // of every wait inside the kernels
   int withhold;               // failure injection (tests only): the values' copies are not issued, so that waits run out
   void* scratch;              // after the status word of the workspace
-  // Attention in two passes over different keys: the first leaves out32 and lse, the second takes them as its prior and
-  // writes the rows of both.
-  int pass;                   // 0: a call of its own, with rows only; 1: the first; 2: the second, or a call of its own with lse; 3: both in
-                              // one, each row over its prefix's keys and then its own
+  // What a call is.  0: one of its own, with rows only.  1: one of two passes over different keys, whose rows (out32) and denominators (lse)
+  // another kernel puts together; rows that are split over blocks are marked in lse and stay parts.  2: one of its own, with lse.
+  // 3: both passes in one, each row over its prefix's keys and then its own; with lse.
+  int pass;
+  int follows;                // pass 1: may start while the kernel before it ends
   union {
-    struct {
-      const float* prior;      // [T, Hq, 128] rows of the pass before, and
-      const float* prior_lse;  // [T, Hq] the logarithms (base 2) of their denominators; NULL: no pass before
-      float* out32;            // pass 1: the rows go here, in fp32, instead of out
-    };
-    struct {                   // pass 3: as KvBatch's q_start, kv_len and page_table
+    float* out32;             // pass 1: [T, Hq, 128] fp32, instead of out
+    struct {                  // pass 3: as KvBatch's q_start, kv_len and page_table
       const int32_t* prefix_start;
       const int32_t* prefix_len;
       const int32_t* prefix_table;
@@ -81,14 +78,22 @@ struct AttentionArgs {
   int n_prefixes, prefix_max_pages;  // pass 3
 };
 size_t attention_scratch_bytes(int Hq, int Hkv, int max_q, int n_sms);
-cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
+// parts (pass 1): where the rows are that were split.
+struct AttentionParts;
+cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream, AttentionParts* parts = nullptr);
 
-// Whether sequences bring so many rows that each goes over its prefix by itself: nothing is passed on then (rows = NULL).
+// Whether sequences bring so many rows that each goes over its prefix by itself, in one pass.
 bool shared_attention_joins(const KvBatch& prefixes, const KvBatch& c);
-// Sequences b of `prefixes` are the prefixes, its q_start cuts the T tokens into their readers; rows [T, Hq, 128] and rows_lse
-// [T, Hq]: what is passed from the first pass to the second (NULL: no prefixes).
-cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, void* prefix_scratch, const KvBatch& c,
-                                    const AttentionArgs& a, float* rows, float* rows_lse, int n_sms, cudaStream_t stream);
+// What the two passes leave for the kernel that ends them: rows [T, Hq, 128], denominators [T, Hq], and the scratch of either (the
+// second's is the call's).
+struct SharedBuffers {
+  float* rows[2];
+  float* lse[2];
+  void* prefix_scratch;
+};
+// Sequences b of `prefixes` are the prefixes, its q_start cuts the T tokens into their readers (B = 0: no prefixes).
+cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, const KvBatch& c, const AttentionArgs& a,
+                                    const SharedBuffers& s, int n_sms, cudaStream_t stream);
 
 
 // Failure injection (tests only): what 1 = wait limit in ns (0: the default 2 s), what 4 = nonzero: withhold the values'
@@ -117,11 +122,11 @@ cudaError_t launch_kv_evict(const KvBatch& c, const KvEvictArgs& e, int n_sms, c
 bool attention_decode_fits(int G, int max_q);
 bool attention_decode_chunks_fit(const KvBatch& c, int max_q, int n_sms);  // or 16 of them at a time (calls of two passes)
 size_t attention_decode_scratch(int G, int max_q, int n_sms);
-cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
+cudaError_t launch_attention_decode(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream, AttentionParts* parts);
 
 // Any number of rows.
 size_t attention_prefill_scratch(int G, int max_q, int n_sms);
-cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream);
+cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream, AttentionParts* parts);
 
 // ---------------------------------------------------------------- rows that were split
 // What block k of a kernel that cuts its work into runs tells the joining kernel: whether its run begins with a part of
@@ -133,10 +138,20 @@ struct JoinInfo {
   int c0, c1, slot0;
   int pad;
 };
-// part_o [parts][rows][128], part_rl [parts][rows]: unscaled sums, their reference exponent r and denominator l.
-// `base`: the sums are of 2^(u - r + base).
-cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, int blocks, int rows, float base, const float* part_o,
-                                  const float2* part_rl, const JoinInfo* info, cudaStream_t stream);
+// The parts of a launch of `blocks` blocks: o [2 blocks][rows][128], rl [2 blocks][rows]: unscaled sums, their reference exponent r and
+// denominator l; the sums are of 2^(u - r + base).
+struct AttentionParts {
+  int blocks, rows;
+  float base;
+  const float* o;
+  const float2* rl;
+  const JoinInfo* info;  // [blocks]
+};
+cudaError_t launch_attention_join(const KvBatch& c, const AttentionArgs& a, const AttentionParts& parts, cudaStream_t stream);
+
+// What a pass 1 puts in place of the denominator of a row that is split: a NaN that no arithmetic makes, with the number of the block that
+// has the row's first part.
+constexpr unsigned kSplitMark = 0xFFC00000u;
 
 // The codes as a matrix of 128-byte rows (one token of one head each), boxes of one page with the 128-byte swizzle.
 bool make_cache_map(CUtensorMap* m, const uint8_t* codes, const KvBatch& c);

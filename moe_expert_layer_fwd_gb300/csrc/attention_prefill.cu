@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     run = min(share, all - begin);
     if (run <= 0) {
       if (tid == 0) info[blockIdx.x].split = 0;
-      if (kPass == 2) pdl_wait();  // this pass does not end before the one that it may overlap
+      if (kPass == 1) pdl_wait();  // this pass does not end before the one that it may overlap
       return;
     }
     if (before * c.Hkv <= begin && begin < (before + mine) * c.Hkv) {
@@ -654,12 +654,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && next->nt) fetch_queries(*next);
       }
       // ---- the rows' outputs
-      float before = -CUDART_INF_F;  // of the pass before, on its way while the last sums are waited for
-      if constexpr (kPass == 2) {
-        pdl_wait();
-        if (live && g.i0 == 0 && g.i1 == g.nt) before = prior_lse(a, (size_t)(g.t0 + i_row) * c.Hq + head);
-      }
-      RowEnd e = {};
       ok = ok && warp_wait(&o_full[mt], (steps - 1u) & 1u, abort_flag, c.status);
       if (!ok) break;
       tc_fence_after();
@@ -678,27 +672,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kSplit && mt == 1) *other_rl = make_float2(r, l);
       auto write = [&](int d, const float (&o)[32], float inv) {  // dims d .. d + 31 of this row
         if (complete) {
-          if (kPass > 0 && live) {
-            const size_t at = (size_t)(g.t0 + i_row) * c.Hq + head;
-            if (d == 0) e = end_row<kPass>(a, at, inv, r - kBase, l, before, true);
+          if (kPass == 1 && live) {
 #pragma unroll
-            for (int y0 = 0; y0 < 32; y0 += 16) {
-              float4 prior[4];  // loads before stores, which they cannot pass
-              if (kPass == 2 && a.prior) {
-#pragma unroll
-                for (int y = 0; y < 4; ++y) prior[y] = reinterpret_cast<const float4*>(a.prior + at * kHeadDim + d + y0)[y];
-              }
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const float* w = o + y0 + 4 * y;
-                float4 v = make_float4(w[0] * e.f, w[1] * e.f, w[2] * e.f, w[3] * e.f);
-                if (kPass == 2 && a.prior)
-                  v = make_float4(fmaf(prior[y].x, e.f1, v.x), fmaf(prior[y].y, e.f1, v.y), fmaf(prior[y].z, e.f1, v.z),
-                                  fmaf(prior[y].w, e.f1, v.w));
-                if (kPass == 1) reinterpret_cast<float4*>(a.out32 + at * kHeadDim + d + y0)[y] = v;
-                else reinterpret_cast<uint2*>(out + d + y0)[y] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-              }
-            }
+            for (int y = 0; y < 32; y += 4)
+              *reinterpret_cast<float4*>(a.out32 + ((size_t)(g.t0 + i_row) * c.Hq + head) * kHeadDim + d + y) =
+                  make_float4(o[y] * inv, o[y + 1] * inv, o[y + 2] * inv, o[y + 3] * inv);
           } else if (live) {
 #pragma unroll
             for (int y = 0; y < 32; y += 8)
@@ -767,6 +745,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (d & 32) ++xs;
       }
       if (!ok) break;
+      if (kPass > 0 && live && (!kSplit || mt == 0)) {
+        const size_t at = (size_t)(g.t0 + i_row) * c.Hq + head;
+        if (complete) write_lse(a, at, r - kBase, l);
+        else if (kPass == 1 && g.i0 == 0) mark_split(a, at);
+      }
       tc_fence_before();
     }
     cp_async_wait<0>();
@@ -1000,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(done, 0, abort_flag, 1000ull * a.limit_us, c.status, false);
     }
   }
-  if (kPass == 2) pdl_wait();
+  if (kPass == 1) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -1010,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kSplit, int kPass>
-cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
+cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream, AttentionParts* parts) {
   using C = Cfg<kSplit>;
   CUtensorMap tk, tv;
   if (!make_cache_map(&tk, c.k_codes, c) || !make_cache_map(&tv, c.v_codes, c)) return cudaErrorInvalidValue;
@@ -1021,9 +1004,11 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   float* part_o = reinterpret_cast<float*>(a.scratch);
   float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)n_sms * 2 * C::kRows * kHeadDim);
   JoinInfo* info = reinterpret_cast<JoinInfo*>(part_rl + (size_t)n_sms * 2 * C::kRows);
-  e = launch_kernel(kern, dim3(n_sms), dim3(kThreads), C::kBytes, stream, kPass == 2 && a.prior, tk, tv, c, a, part_o, part_rl, info);
-  if (e != cudaSuccess) return e;
-  return launch_attention_join(c, a, n_sms, C::kRows, kBase, part_o, part_rl, info, stream);
+  e = launch_kernel(kern, dim3(n_sms), dim3(kThreads), C::kBytes, stream, kPass == 1 && a.follows, tk, tv, c, a, part_o, part_rl, info);
+  const AttentionParts p = {n_sms, C::kRows, kBase, part_o, part_rl, info};
+  if (kPass == 1) *parts = p;
+  if (kPass == 1 || e != cudaSuccess) return e;
+  return launch_attention_join(c, a, p, stream);
 }
 
 // Whether a sequence's rows of one head fit an M tile: it is then the keys that the two tiles share out.
@@ -1036,12 +1021,12 @@ size_t attention_prefill_scratch(int G, int max_q, int n_sms) {
   return (size_t)n_sms * (2 * rows * (kHeadDim * sizeof(float) + sizeof(float2)) + sizeof(JoinInfo));
 }
 
-cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream) {
+cudaError_t launch_attention_prefill(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream, AttentionParts* parts) {
   const bool split = splits_keys(c.Hq / c.Hkv, a.max_q);
-  if (a.pass == 0) return split ? launch<true, 0>(c, a, n_sms, stream) : launch<false, 0>(c, a, n_sms, stream);
-  if (a.pass == 1) return split ? launch<true, 1>(c, a, n_sms, stream) : launch<false, 1>(c, a, n_sms, stream);
-  if (a.pass == 3) return launch<false, 3>(c, a, n_sms, stream);
-  return split ? launch<true, 2>(c, a, n_sms, stream) : launch<false, 2>(c, a, n_sms, stream);
+  if (a.pass == 0) return split ? launch<true, 0>(c, a, n_sms, stream, parts) : launch<false, 0>(c, a, n_sms, stream, parts);
+  if (a.pass == 1) return split ? launch<true, 1>(c, a, n_sms, stream, parts) : launch<false, 1>(c, a, n_sms, stream, parts);
+  if (a.pass == 3) return launch<false, 3>(c, a, n_sms, stream, parts);
+  return split ? launch<true, 2>(c, a, n_sms, stream, parts) : launch<false, 2>(c, a, n_sms, stream, parts);
 }
 
 }  // namespace moe

@@ -191,28 +191,11 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
-// How a row of a call in one of two passes is finished.  The row's own part is o = f o' of o' unscaled sums with the denominator l = sum of
-// 2^(u - r) (f = 1 / l, 0 for a row that sees nothing); L = r + log2 l.  With L1 of the pass before and M = max(L, L1):
-//   out = (2^(L - M) o + 2^(L1 - M) prior) / (2^(L - M) + 2^(L1 - M)),   lse = M + log2 of that sum
-struct RowEnd {
-  float f, f1;  // out = f o' + f1 prior
-};
-// (before: L1, -infinity without a pass before; the caller has it early, a load takes longer than the rest)
-__device__ __forceinline__ float prior_lse(const AttentionArgs& a, size_t row) { return a.prior ? a.prior_lse[row] : -CUDART_INF_F; }
-template <int kPass>
-__device__ __forceinline__ RowEnd end_row(const AttentionArgs& a, size_t row, float f, float r, float l, float before, bool writes_lse) {
-  RowEnd e = {f, 0.f};
-  float lse = r + log2f(l);
-  if (kPass == 2 && a.prior) {
-    const float top = fmaxf(lse, before), ref = top == -CUDART_INF_F ? 0.f : top;
-    const float w = ex2(lse - ref), w1 = ex2(before - ref), sum = w + w1, inv = sum != 0.f ? 1.f / sum : 0.f;
-    e.f = f * w * inv;
-    e.f1 = w1 * inv;
-    lse = ref + log2f(sum);
-  }
-  if (a.lse && writes_lse) a.lse[row] = lse * a.lse_unit;
-  return e;
+// The denominator of a row, l = sum of 2^(u - r), as such calls leave it.
+__device__ __forceinline__ void write_lse(const AttentionArgs& a, size_t row, float r, float l) {
+  if (a.lse) a.lse[row] = (r + log2f(l)) * a.lse_unit;
 }
+__device__ __forceinline__ void mark_split(const AttentionArgs& a, size_t row) { a.lse[row] = __uint_as_float(kSplitMark | blockIdx.x); }
 
 // Pairs of floats in one 64-bit register: one instruction for two products or sums.
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
