@@ -27,6 +27,8 @@ What it computes, step by step, each function citing the passage it follows:
   output quantised to MXFP8 before the down projection.
 * ``attention`` -- the paged 8-bit key/value cache: norm and rotation, append, read-back, and
   softmax attention over it (imported by name: ``from oracle import attention``).
+* ``attention_long`` -- rotation rows on several axes, shared prefixes, accumulated attention weights
+  and eviction (imported by name).
 
 Precision: float64 everywhere, except the expert *selection*, which is an
 integer decided by floating point and is therefore taken in float32 with the
