@@ -673,7 +673,8 @@ MOE_API int moe_paged_attention(const moe_kv_desc* d, const uint16_t* q, long lo
  * layers of a step: frequency f < rot_dim / 2 turns by the token's position on axis axes[f] (time, height and
  * width of an image's patches, say; one axis: any positions, such as those of tokens behind an eviction),
  *   rows[t, f] = cos_sin[p, f],  rows[t, rot_dim/2 + f] = cos_sin[p, rot_dim/2 + f],  p = positions[axes[f], t].
- *  positions: int32 [n_axes, T], axis a at positions + a * positions_stride (elements, >= T); n_axes <= 8.
+ *  positions: int32 [n_axes, T], axis a at positions + a * positions_stride (elements, >= 0; 0: the same for all
+ *      axes); n_axes <= 8.
  *  axes: rot_dim / 2 bytes on the host.    cos_sin [max_pos, rot_dim] as for moe_kv_append.
  *  rows [T, rot_dim] fp32 out.  A position outside 0 .. max_pos - 1 makes its part of the row NaN (and so the
  *      token's query and key) and sets the status to MOE_ERR_DEVICE_CHECK.
@@ -705,7 +706,8 @@ MOE_API int moe_kv_append_at(const moe_kv_desc* d, const uint16_t* q, long long 
  *  ws: at least moe_paged_attention_shared_workspace_size(d, max_q, prefix) bytes, of which n, max_pages and max_q of
  *      prefix are read (0: invalid), and max_pages of d.  It grows with T * Hq when there are prefixes with few tokens
  *      a sequence.
- * Prefixes are checked as sequences are; rows whose prefix is left out are undefined (and the status is set).
+ * Prefixes are checked as sequences are; the rows of a prefix or a sequence that is left out are undefined (and the status
+ * is set).
  */
 typedef struct moe_kv_prefix {
   int32_t n;                  /* prefixes */
@@ -748,7 +750,7 @@ MOE_API int moe_kv_weights(const moe_kv_desc* d, const uint16_t* q, long long q_
  * one that is not above 0 (a NaN among them) counts as 0.
  *
  *  T and Hq of d are not used.  keep [B], new_table [B,new_max_pages]: int32 on the device.
- *  New pages come from the same pool and are none of the pages that this call reads.  They get the kept
+ *  New pages come from the same pool, are all different and none of the pages that this call reads.  They get the kept
  *      tokens' codes, weights and scales: a page's scale is the largest of those that its tokens had, and codes of
  *      smaller ones are rounded again to it.  The old pages stay as they are.
  *  new_len [B] int32 out: m.    kept [B,Hkv,new_max_pages*page] int32 out: the tokens that stayed, then -1.

@@ -131,7 +131,7 @@ def moe_kv_workspace(device="cuda"):
 
 def moe_rope_rows(positions, axes, cos_sin, rows=None, ws=None, stream=None):
     """The rotation of each new token, rows [T, rot_dim] fp32 for moe_kv_append_at: frequency f turns by positions[axes[f], t].
-    positions [n_axes, T] int32 (a row's tokens dense), axes: rot_dim / 2 ints, cos_sin as moe_rope_table makes it."""
+    positions [n_axes, T] int32 (a row's tokens dense; one row expanded will do), axes: rot_dim / 2 ints, cos_sin as moe_rope_table makes it."""
     b = _b()
     if positions.dim() != 2 or positions.dtype is not b.i32 or not positions.is_cuda:
         raise ValueError(f"positions: expected a CUDA int32 tensor [n_axes, T], got {positions.dtype} {tuple(positions.shape)}")

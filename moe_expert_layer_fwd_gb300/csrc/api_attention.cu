@@ -94,7 +94,7 @@ int moe_rope_table(int max_pos, int rot_dim, double base, float* cos_sin, void* 
 
 int moe_rope_rows(int n_axes, int T, const int32_t* positions, long long positions_stride, const uint8_t* axes, const float* cos_sin,
                   int max_pos, int rot_dim, float* rows, void* ws, size_t ws_bytes, void* stream) {
-  if (n_axes < 1 || T < 0 || max_pos < 0 || rot_dim < 1 || positions_stride < T) return MOE_ERR_INVALID_ARG;
+  if (n_axes < 1 || T < 0 || max_pos < 0 || rot_dim < 1 || positions_stride < 0) return MOE_ERR_INVALID_ARG;
   if (n_axes > moe::kMaxAxes || rot_dim > moe::kHeadDim || rot_dim % 16 != 0) return MOE_ERR_UNSUPPORTED;
   if (!axes) return MOE_ERR_INVALID_ARG;
   moe::RopeAxes x = {};

@@ -10,6 +10,9 @@
 // Packing.  A block per (new page, head): its tokens' rows come from wherever they were, 128 bytes each, which memory reads
 // whole.  The page's scale is the largest of their pages' scales, known before the codes come: rows of pages of that scale are copied, the
 // others' codes are rounded again (exact unless they become subnormal).  The bytes of the kept rows bound it.
+//
+// Measured (32 sequences of 3000-9000 tokens, 8 heads, cut to 1500-2200): choosing 15-18 us (5,500 cycles until the weights are there, 4,000 a
+// digit, 7,000 for the tokens' places), packing 36-42 (250 MB, 6-7 TB/s).
 #include "attention_common.cuh"
 
 namespace moe {

@@ -7,15 +7,16 @@
 //   S^T[128 keys, NC] = K . q_hi^T + K . q_lo^T       tcgen05 kind::f8f6f4, queries in two E4M3 halves
 // and a softmax thread owns a key: it adds up its lane of S^T, and nothing crosses threads.  Neither values nor joins are needed.
 //
-// Rows beyond NC are taken in chunks: a block keeps kStages tiles of keys in shared memory and walks the chunks over them, so that a
-// chunk's conversion to E4M3 serves that many tiles.
+// Rows beyond NC (a sequence with more than the most that was said) are taken in chunks: a block keeps kStages tiles of keys in shared
+// memory and walks the chunks over them.  More than 16 rows as a rule: the kernel for many rows.
 //
-// Work: all (sequence, head, tile) in one order, a tile costing its sequence's chunks, cut into equal runs, one per block.  The sums of a key are one thread's in a fixed order: the same inputs give the same bits.
+// Work: all (sequence, head, tile) in one order, a tile costing its sequence's chunks, cut into equal runs, one per block (two blocks per
+// SM).  The sums of a key are one thread's in a fixed order: the same inputs give the same bits.
 //
-// What bounds it: few rows, the bytes of the keys; many, exponentials (32 a cycle and SM) and the products, which take the same
-// 256 cycles for a tile and 64 rows.
+// The bytes of the keys bound it: 64 sequences of 1500-8190 tokens, 8 key/value heads, 317 MB of keys, take 61 us (54 at the memory's copy
+// rate), of which 6 are the way to the first scores (lengths, page table, scales, copies, one after another).
 //
-// Warps: softmax (groups of four, which take the tiles in turn), TMA, MMA, then queries.  Every wait is bounded (2 s).
+// Warps: 8 softmax (two groups of four, which take the tiles in turn), TMA, MMA, queries.  Every wait is bounded (2 s).
 #include "attention_weights.cuh"
 
 namespace moe {
@@ -29,6 +30,7 @@ struct TileInfo {    // per 16 keys of a tile
 struct RowPair {     // two query rows: a weight is 2^(S kf qf + minus)
   float qf[2], minus[2];  // minus = -lse2
 };
+
 template <int NC>
 struct Cfg {
   static constexpr int kPerSm = 2;                          // blocks

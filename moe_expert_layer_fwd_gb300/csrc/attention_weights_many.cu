@@ -1,4 +1,5 @@
-// Accumulated attention weights of many query rows per key/value head (the last tokens of a prompt, chunks): exponentials bound it.
+// Accumulated attention weights of many query rows per key/value head (the last tokens of a prompt, chunks): products and
+// exponentials bound it, 576 and 512 cycles for a tile and 128 rows.
 //
 // As in the kernel for few rows the keys are the M operand and a softmax thread owns a key, but with a hundred rows to a tile what the
 // thread does for each row is all that counts, so everything that belongs to a row goes through the product:
@@ -6,10 +7,14 @@
 //   weight = 2^(c S),   c = kf * scale * log2(e),   m = -lse / scale
 // kf = 2^e_k is the key's page's scale; m is three bf16 parts (24 bits) against three times 1 / kf (a power of two), one more K = 16 step of
 // the product.  A row that gives nothing has m = -2^100.  What is left is a product, an exponential and a sum, two and a half
-// instructions for a row; with the row's factor and denominator read from shared memory (16 bytes a thread and row, and E4M3 halves
-// of the queries made anew for every few tiles) prompts' ends took 95 us where they take 40.
+// instructions for a row; with the row's factor and denominator read from shared memory (and E4M3 halves of the queries made anew for
+// every few tiles) a step took 2,900 cycles in the softmax warps where it takes 1,200.
 //
 // A block keeps kTiles tiles of keys in shared memory, converted, and walks the chunks of NC rows over them.
+//
+// Measured: the last 40-64 tokens of 4 prompts of 5000-16000, 8 query heads a key/value head, 64 us (35.6 GFLOP of scores, 18 us at the
+// bf16 rate).  A block's 62 steps take 700 cycles of products each, 500 in which their scores or keys are waited for, and 11,500 pass before
+// the first one.
 //
 // Warps: 8 softmax (two groups of four, which take the tiles in turn, two buffers of scores each), 4 that convert keys, TMA, MMA, 4 for
 // the queries (two for either buffer).  Every wait is bounded (2 s).

@@ -79,7 +79,7 @@ def test_cache_pointers_are_checked(L, call, field):  # noqa: F811
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(n=0), BAD), (dict(n=2), BAD), (dict(n=9), UNS), (dict(T=-1), BAD), (dict(stride=4), BAD), (dict(axes=None), BAD),
+    (dict(n=0), BAD), (dict(n=2), BAD), (dict(n=9), UNS), (dict(T=-1), BAD), (dict(stride=-1), BAD), (dict(axes=None), BAD),
     (dict(axes=bytes([3] * 64)), BAD), (dict(pos=None), BAD), (dict(pos=A + 2), BAD), (dict(cs=None), BAD), (dict(cs=A + 4), BAD),
     (dict(max_pos=-1), BAD), (dict(rot=0), BAD), (dict(rot=24), UNS), (dict(rot=144), UNS), (dict(rows=None), BAD), (dict(rows=A + 4), BAD),
     (dict(ws=None), BAD), (dict(bytes=128), moe.MOE_ERR_WORKSPACE), (dict(T=0, pos=None, rows=None), moe.MOE_OK)])

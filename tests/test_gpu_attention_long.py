@@ -38,6 +38,14 @@ def test_rope_rows(env, n_axes, rot, T):
         assert moe.moe_get_device_status(ws) == moe.MOE_OK
 
 
+def test_rope_rows_of_one_row_for_all_axes(env):
+    """Text alone: one row of positions, expanded."""
+    moe, torch = env
+    table, pos = moe.moe_rope_table(500, 64), i32([[7, 8, 9, 400]])
+    rows = moe.moe_rope_rows(pos.expand(3, -1), [f % 3 for f in range(32)], table)
+    assert torch.equal(rows, table[pos[0].long()])
+
+
 def test_rope_rows_outside_the_table(env):
     moe, torch = env
     table, axes = moe.moe_rope_table(64, 32), [0] * 8 + [1] * 8
@@ -287,6 +295,28 @@ def test_weights_long(env):
         b = Batch(rng, new, ctx, Hkv, 128).fill(rng).dev(env)
         q = bf16(rng, sum(new), Hq, D, mul=2.0)
         check_weights(env, b, q, denominators(b, q))
+
+
+@pytest.mark.parametrize("scale", [D ** -0.5, 1e-10])
+def test_weights_chunks_of_the_kernel_for_few_rows(env, scale):
+    """More rows than max_q says -- it has to cover the tokens in the mean only -- and a scale so small that the other kernel leaves them
+    to this one."""
+    moe, torch = env
+    rng = np.random.default_rng(6)
+    for new, ctx, Hq, Hkv in (([20, 0, 0, 0], [300, 5, 0, 70], 8, 4), ([30, 1, 0, 0, 0, 1, 0, 0], [900, 5, 0, 70, 1, 0, 2, 300], 4, 2)):
+        b = Batch(rng, new, ctx, Hkv, 32).fill(rng).dev(env)
+        q = bf16(rng, sum(new), Hq, D, mul=2.0)
+        lse = torch.from_numpy(ol.shared_attention(f64(q), b.host, b.q_start, b.kv_len, b.table, scale)[2]).float().cuda()
+        before = rng.exponential(size=b.host["k_codes"].shape[:3]).astype(np.float32)
+        for max_q in (-(-sum(new) // len(new)), max(new)):
+            for window in (0, 50):
+                w, ws = torch.from_numpy(before.copy()).cuda(), moe.moe_kv_workspace()
+                moe.moe_kv_weights(q.cuda(), lse, b.cache, b.d_start, b.d_len, b.d_table, max_q, w, scale=scale, window=window, ws=ws)
+                assert moe.moe_get_device_status(ws) == moe.MOE_OK
+                ref, added, written = ol.weights(f64(q), lse.cpu().double().numpy(), b.host, b.q_start, b.kv_len, b.table, scale, before,
+                                                 False, True, window)
+                got = w.cpu().double().numpy()
+                assert (np.abs(got - ref) <= 2.0 ** -9 * added + 2.0 ** -22 * (ref + added)).all()
 
 
 def test_weights_sum_to_the_rows(env):
