@@ -311,3 +311,33 @@ def test_long_caches_pass_32_bits(env):  # noqa: F811
     n, kept = moe.moe_kv_evict(cache, w, lens, table, i32([2]), fresh, 0, 1)
     assert kept[0, :, :2].tolist() == [[263, 299]] * Hkv and (w[n_pages - 3, :, 0] == 5.0).all()
     assert torch.equal(cache.k_codes[n_pages - 3, :, :2], cache.k_codes[n_pages - 2, :, [7, 43]])
+
+
+def test_calls_at_once(env):  # noqa: F811
+    """Shared attention and weights on two streams at the same time, workspaces of their own: what each gives alone.  And one stream's calls
+    right behind one another in one workspace, each of whose passes overlap."""
+    moe, torch = env
+    rng = np.random.default_rng(4)
+    work = []
+    for new, own, prefix, readers, Hq in (([1] * 12, [50 * i for i in range(12)], [3000], [12], 16),
+                                          ([5, 0, 3, 6], [900, 10, 0, 44], [500, 70], [2, 2], 16), ([90, 150], [30, 400], [700], [2], 8)):
+        b = Shared(rng, new, own, prefix, readers, 2, 32)
+        b.dev(env)
+        b.d_start, b.d_len = i32(b.q_start), i32(b.kv_len)
+        q = bf16(rng, sum(new), Hq, D).cuda()
+        ws = moe.moe_paged_attention_shared_workspace(sum(new), len(new), Hq, 2, D, max(new), len(prefix), b.max_p)
+        work.append((b, q, i32(np.ascontiguousarray(b.table)), b.prefix(), ws, torch.zeros(b.host["k_codes"].shape[:3], device="cuda")))
+
+    def call(b, q, table, prefix, ws, w, stream=None):
+        out, lse = moe.moe_paged_attention_shared(q, b.cache, b.d_start, b.d_len, table, max(b.new), prefix, ws=ws, stream=stream)
+        return out, lse, moe.moe_kv_weights(q, lse, b.cache, b.d_start, b.d_len, table, max(b.new), None, w, ws=ws, stream=stream)
+
+    want = [[t.clone() for t in call(*x)] for x in work]
+    streams = [torch.cuda.Stream() for _ in work]
+    torch.cuda.synchronize()
+    for turn in range(20):
+        got = [[call(*x, stream=s) for _ in range(3)][-1] for x, s in zip(work, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b)), turn
+    assert all(moe.moe_get_device_status(x[4]) == moe.MOE_OK for x in work)
