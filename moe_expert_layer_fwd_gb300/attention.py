@@ -5,6 +5,7 @@ Argument marshalling only, as in the rest of the package; ``include/moe.h`` stat
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import NamedTuple, Optional
 
 import moe_expert_layer_fwd_gb300 as _m
@@ -129,21 +130,29 @@ def moe_kv_workspace(device="cuda"):
     return _b().torch.zeros(max(_b().status_bytes, 256), dtype=_b().u8, device=device)
 
 
+def _axis_bytes(axes, n_axes: int, rot_dim: int) -> bytes:
+    """The axis of each frequency as a byte.  Element by element: bytes() of an array or a tensor would be its memory."""
+    codes = bytes(axes if type(axes) in (list, tuple, bytes) else [operator.index(a) for a in axes])  # (raises for what is no byte)
+    if len(codes) * 2 != rot_dim:
+        raise ValueError(f"axes: expected one for each of {rot_dim // 2} frequencies, got {len(codes)}")
+    if codes and max(codes) >= n_axes:
+        raise ValueError(f"axes: expected numbers of the {n_axes} axes, got {tuple(codes)}")
+    return codes
+
+
 def moe_rope_rows(positions, axes, cos_sin, rows=None, ws=None, stream=None):
     """The rotation of each new token, rows [T, rot_dim] fp32 for moe_kv_append_at: frequency f turns by positions[axes[f], t].
-    positions [n_axes, T] int32 (a row's tokens dense; one row expanded will do), axes: rot_dim / 2 ints, cos_sin as moe_rope_table makes it."""
+    positions [n_axes, T] int32 (a row's tokens dense; one row expanded will do), axes: rot_dim / 2 integers (a list, an array), cos_sin as moe_rope_table makes it."""
     b = _b()
     if positions.dim() != 2 or positions.dtype is not b.i32 or not positions.is_cuda:
         raise ValueError(f"positions: expected a CUDA int32 tensor [n_axes, T], got {positions.dtype} {tuple(positions.shape)}")
     n_axes, T = positions.shape
     if T > 1 and positions.stride(1) != 1:
         raise ValueError(f"positions: the tokens of an axis must be dense, got strides {positions.stride()}")
-    if cos_sin.dim() != 2 or len(axes) * 2 != cos_sin.shape[1]:
-        raise ValueError(f"axes: expected one for each frequency of cos_sin {tuple(cos_sin.shape)}, got {len(axes)}")
+    if cos_sin.dim() != 2:
+        raise ValueError(f"cos_sin: expected [max_pos, rot_dim], got {tuple(cos_sin.shape)}")
     max_pos, rot_dim = cos_sin.shape
-    codes = bytes(axes)  # (raises for what is no byte)
-    if rot_dim and max(codes) >= n_axes:
-        raise ValueError(f"axes: expected numbers of the {n_axes} axes, got {tuple(axes)}")
+    codes = _axis_bytes(axes, n_axes, rot_dim)
     cs = _need(cos_sin, "cos_sin", b.f32, cos_sin.shape)
     rp = None if rows is None else _need(rows, "rows", b.f32, (T, rot_dim))
     ws = _status_ws(positions, ws, stream)

@@ -1,0 +1,29 @@
+"""Arguments of the long conversations' binding that are converted or checked on the host (CPU)."""
+import array
+
+import numpy as np
+import pytest
+import torch
+
+from moe_expert_layer_fwd_gb300 import attention
+
+AXES = [f % 3 for f in range(64)]
+
+
+@pytest.mark.parametrize("make", [list, tuple, bytes, bytearray, lambda a: memoryview(bytes(a)), lambda a: array.array("i", a), torch.tensor,
+                                  *(lambda a, t=t: np.array(a, t) for t in (np.uint8, np.int8, np.int32, np.int64, np.uint16)),
+                                  lambda a: np.array(a, np.int32)[::-1][::-1], lambda a: np.repeat(np.array(a), 2)[::2]])
+def test_axes_of_any_kind_of_sequence(make):
+    """One byte a frequency, whatever holds the numbers (an array's own bytes are not its elements)."""
+    assert attention._axis_bytes(make(AXES), 3, 128) == bytes(AXES)
+
+
+@pytest.mark.parametrize("axes", [AXES[:-1], AXES + [0], [3] + AXES[1:], [-1] + AXES[1:], [300] + AXES[1:], np.array(AXES) + 1,
+                                  np.array(AXES).reshape(32, 2), np.array(AXES) - 1, [0.0] + AXES[1:], np.array(AXES, float)])
+def test_axes_that_are_none(axes):
+    with pytest.raises((ValueError, TypeError)):
+        attention._axis_bytes(axes, 3, 128)
+
+
+def test_axes_of_no_frequency():
+    assert attention._axis_bytes([], 1, 0) == b""
