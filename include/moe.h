@@ -700,7 +700,8 @@ MOE_API int moe_kv_append_at(const moe_kv_desc* d, const uint16_t* q, long long 
  *  prefix: NULL (none: moe_paged_attention with lse), or n prefixes in the same pool.  Tokens q_start[i] ..
  *      q_start[i+1] - 1 of the T read prefix i (it may have no readers, or no tokens), a sequence's all the
  *      same one; q_start[0] = 0, q_start[n] = T.  q_start [n+1], len [n], page_table [n, max_pages]: int32 on
- *      the device.  max_q: at least the readers' tokens of any one prefix, at most T, as max_q.
+ *      the device; page_table may be NULL when max_pages is 0 (prefixes without tokens).  max_q: at least the readers' tokens of
+ *      any one prefix, at most T, as max_q.
  *  window > 0 only without prefixes.
  *  lse [T,Hq] fp32 out, natural logarithm, -inf for a row that sees nothing; or NULL.
  *  ws: at least moe_paged_attention_shared_workspace_size(d, max_q, prefix) bytes, of which n, max_pages and max_q of

@@ -175,9 +175,10 @@ size_t moe_paged_attention_workspace_size(const moe_kv_desc* d, int max_q) {
 }
 
 static int check_attention(const moe_kv_desc* d, const uint16_t* q, long long q_stride, const int32_t* q_start, const int32_t* kv_len,
-                           const int32_t* page_table, int max_q) {
+                           const int32_t* page_table, int max_q, bool table_needed = true) {
   if (max_q < 1 || max_q > d->T || (long long)max_q * d->B < d->T) return MOE_ERR_INVALID_ARG;
-  if (!ok_ptr(q) || !ok_ptr(q_start) || !ok_ptr(kv_len) || !ok_ptr(page_table)) return MOE_ERR_INVALID_ARG;
+  if (!ok_ptr(q) || !ok_ptr(q_start) || !ok_ptr(kv_len) || !aligned16(page_table)) return MOE_ERR_INVALID_ARG;
+  if (!page_table && table_needed) return MOE_ERR_INVALID_ARG;
   return ok_stride(q_stride, d->Hq) ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
 
@@ -222,7 +223,9 @@ int moe_paged_attention_shared(const moe_kv_desc* d, const uint16_t* q, long lon
   if (prefix && (s = prefix_desc(d, prefix, &pd))) return s;
   if (d->T == 0) return MOE_OK;
   if ((s = check_attention(d, q, q_stride, q_start, kv_len, page_table, max_q))) return s;
-  if (prefix && (s = check_attention(&pd, q, q_stride, prefix->q_start, prefix->len, prefix->page_table, prefix->max_q))) return s;
+  // (a table without columns is not read: its prefixes have no tokens)
+  if (prefix && (s = check_attention(&pd, q, q_stride, prefix->q_start, prefix->len, prefix->page_table, prefix->max_q, prefix->max_pages > 0)))
+    return s;
   if (!ok_ptr(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return MOE_ERR_INVALID_ARG;
   if ((s = check_cache(kv))) return s;
   if ((s = check_ws(ws, ws_bytes, moe_paged_attention_shared_workspace_size(d, max_q, prefix)))) return s;

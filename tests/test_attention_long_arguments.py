@@ -27,3 +27,15 @@ def test_axes_that_are_none(axes):
 
 def test_axes_of_no_frequency():
     assert attention._axis_bytes([], 1, 0) == b""
+
+
+def test_prefix_tables_without_columns():
+    """NULL for a table that has no columns, not for one that has; what comes behind that check still refuses."""
+    from test_attention_abi import A, BAD
+    from test_attention_long_abi import prefix, shared
+    import moe_expert_layer_fwd_gb300 as moe
+    L = moe.lib()
+    empty = prefix(max_pages=0, page_table=None)
+    assert shared(L, p=empty, n=256) == moe.MOE_ERR_WORKSPACE and shared(L, p=empty, out=None) == BAD
+    assert shared(L, p=prefix(page_table=None)) == BAD and shared(L, p=prefix(max_pages=0, page_table=A + 4)) == BAD
+    assert shared(L, p=empty, table=None) == BAD
