@@ -73,6 +73,12 @@ def _rows(t, what: str, heads: int, D: int):
     return t.data_ptr(), row if t.shape[0] > 1 else heads * D  # one token has no stride
 
 
+def _need_aligned(what: str, *addresses):
+    """Refuses what the library refuses, before anything else of the call has run."""
+    if any(a and a & 15 for a in addresses):
+        raise _m.MoEError(_m.MOE_ERR_INVALID_ARG, f"{what}: expected tensors that begin on 16 bytes")
+
+
 class KVCache(NamedTuple):
     """The pool of one layer: E4M3 codes [n_pages, Hkv, page, D] and E8M0 scales [n_pages, Hkv], all uint8."""
     k_codes: object
@@ -427,8 +433,8 @@ class AttentionLayer:
                  rot_dim: Optional[int] = None, rope_base: float = 1e6, interleaved: bool = False, q_norm_weight=None,
                  k_norm_weight=None, eps: float = 1e-6, scale: Optional[float] = None, window: int = 0, device="cuda",
                  track_weights: bool = False):
-        if window < 0 or (scale is not None and not 0.0 < scale < float("inf")):
-            raise ValueError(f"expected window >= 0 and a positive finite scale, got {window} and {scale}")
+        if not 0 <= window < 1 << 31 or (scale is not None and not 0.0 < ctypes.c_float(scale).value < float("inf")):
+            raise ValueError(f"expected an int's window >= 0 and a positive finite fp32 scale, got {window} and {scale}")
         self.Hq, self.Hkv, self.D = Hq, Hkv, D
         self.cache = KVCache.empty(n_pages, Hkv, page, D, device)
         rot_dim = D if rot_dim is None else rot_dim
@@ -459,7 +465,7 @@ class AttentionLayer:
             if out.numel() != T * self.Hq * self.D or not out.is_contiguous():
                 raise ValueError(f"out: expected a contiguous tensor [{T}, {self.Hq * self.D}], got {tuple(out.shape)}")
             out = out.view(T, self.Hq, self.D)
-            _need(out, "out", _b().bf16, out.shape)
+            _need_aligned("out", _need(out, "out", _b().bf16, out.shape))
         p = None
         if prefix is not None:
             if self.window or (rows is None and self.cos_sin is not None):
@@ -467,12 +473,14 @@ class AttentionLayer:
             p = _prefix_struct(prefix, T)
             if p.n < 1 or p.max_q * p.n < T or (p.max_q < 1 and T > 0):
                 raise _m.MoEError(_m.MOE_ERR_INVALID_ARG, "AttentionLayer.forward: prefix")
+            _need_aligned("prefix", p.q_start, p.len, p.page_table)
         if rows is not None:
             if self.cos_sin is None:
                 raise ValueError("rows: this layer rotates nothing")
             _need(rows, "rows", _b().f32, (T, self.cos_sin.shape[1]))
         shared = p is not None or self.weight is not None
-        d = _m.moe_kv_desc(B, T, self.Hq, self.Hkv, self.D, 16, 0, 0)
+        n_pages, _, page, _ = self.cache.k_codes.shape
+        d = _m.moe_kv_desc(B, T, self.Hq, self.Hkv, self.D, page, n_pages, page_table.shape[1])
         ws = self._workspace_for(d, max_q, stream, p)
         if rows is None:
             rq = moe_kv_append(q, k, v, self.cache, q_start, kv_len, page_table, self.cos_sin, None, self.interleaved,

@@ -29,6 +29,15 @@ def test_axes_of_no_frequency():
     assert attention._axis_bytes([], 1, 0) == b""
 
 
+def test_layer_numbers():
+    """Windows and scales that are none in the types of the C interface are refused when the layer is made."""
+    import moe_expert_layer_fwd_gb300 as moe
+    for kw in (dict(window=1 << 31), dict(window=(1 << 32) + 5), dict(window=-1), dict(scale=1e-60), dict(scale=1e60), dict(scale=0.0),
+               dict(scale=float("nan"))):
+        with pytest.raises(ValueError, match="window"):
+            moe.AttentionLayer(4, 8, 2, device="cpu", **kw)
+
+
 def test_prefix_tables_without_columns():
     """NULL for a table that has no columns, not for one that has; what comes behind that check still refuses."""
     from test_attention_abi import A, BAD

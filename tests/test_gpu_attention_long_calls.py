@@ -21,6 +21,33 @@ def test_axes_as_arrays(env):  # noqa: F811
         assert torch.equal(layer.rotation(pos, kind), want)
 
 
+def layer_inputs(torch, T=5):
+    x = torch.randn(T, 12 * D, device="cuda").to(torch.bfloat16)
+    return x, i32([0, 2, 5]), i32([2, 3]), i32([[0, 1], [2, 3]])
+
+
+def test_refused_prefixes_leave_the_cache_alone(env):  # noqa: F811
+    """Starts, lengths and tables of prefixes that begin anywhere, tables wider than any: refused before a token is stored."""
+    moe, torch = env
+    x, starts, lens, table = layer_inputs(torch)
+    start, length, pages = i32([7, 0, 2, 5]), i32([7, 9, 9]), i32([[0], [4], [5]])
+    good = start[1:].clone(), length[1:].clone(), pages[1:].clone()
+    wide = torch.zeros(2, 1 << 24, dtype=torch.int32, device="cuda")   # 2^31 tokens
+    out = torch.zeros(5 * 8 * D + 8, dtype=torch.bfloat16, device="cuda")
+    for bad in ((start[1:], good[1], good[2], 3), (good[0], length[1:], good[2], 3), (good[0], good[1], pages[1:], 3),
+                (good[0], good[1], wide, 3), None):
+        layer = moe.AttentionLayer(8, 8, 2, page=128, rot_dim=0)
+        for t in layer.cache:
+            t.fill_(3)
+        kw = dict(prefix=bad) if bad else dict(out=out[1:1 + 5 * 8 * D].view(5, -1))
+        with pytest.raises((ValueError, moe.MoEError)):
+            layer.forward(x, starts, lens, table, 3, **kw)
+        torch.cuda.synchronize()
+        assert all((t == 3).all() for t in layer.cache)
+        layer.forward(x, starts, lens, table, 3, prefix=(*good, 3))
+        assert layer.status() == moe.MOE_OK
+
+
 @pytest.mark.parametrize("new", [[2, 3], [200, 300], [0, 40]])
 def test_prefixes_without_tokens_or_columns(env, new):  # noqa: F811
     """All prefixes empty, their table without a column: what the sequences give alone."""
