@@ -73,6 +73,12 @@ def _rows(t, what: str, heads: int, D: int):
     return t.data_ptr(), row if t.shape[0] > 1 else heads * D  # one token has no stride
 
 
+def _count(n):
+    """A window or a number of tokens as the int of the C interface: beyond all tokens is all of them, and below none is refused
+    there.  (ctypes would keep the low bits.)"""
+    return max(-1, min(n, (1 << 31) - 1))
+
+
 def _need_aligned(what: str, *addresses):
     """Refuses what the library refuses, before anything else of the call has run."""
     if any(a and a & 15 for a in addresses):
@@ -296,7 +302,7 @@ def moe_paged_attention(q, cache: KVCache, q_start, kv_len, page_table, max_q: i
     else:
         op = _need(out, "out", b.bf16, (T, Hq, D))
     status = b.attention(_byref(d), qp, qs, starts, lens, table, _byref(kv), max_q, D ** -0.5 if scale is None else scale,
-                         causal, window, op, ws.data_ptr(), ws.numel(), _stream_of(stream, q))
+                         causal, _count(window), op, ws.data_ptr(), ws.numel(), _stream_of(stream, q))
     if status:
         _m._check(status, "moe_paged_attention")
     return out
@@ -354,8 +360,8 @@ def moe_paged_attention_shared(q, cache: KVCache, q_start, kv_len, page_table, m
     if lse is None:
         lse = _new(stream, q, (T, Hq), b.f32)
         lp = lse.data_ptr()
-    status = b.shared(_byref(d), qp, qs, starts, lens, table, _byref(kv), max_q, D ** -0.5 if scale is None else scale, causal, window,
-                      None if p is None else _byref(p), op, lp, ws.data_ptr(), ws.numel(), _stream_of(stream, q))
+    status = b.shared(_byref(d), qp, qs, starts, lens, table, _byref(kv), max_q, D ** -0.5 if scale is None else scale, causal,
+                      _count(window), None if p is None else _byref(p), op, lp, ws.data_ptr(), ws.numel(), _stream_of(stream, q))
     if status:
         _m._check(status, "moe_paged_attention_shared")
     return out, lse
@@ -381,7 +387,7 @@ def moe_kv_weights(q, lse, cache: KVCache, q_start, kv_len, page_table, max_q: i
         raise ValueError("out: needed when there is no weight to add to")
     ws = _status_ws(q, ws, stream)
     status = b.weights(_byref(d), qp, qs, lp, starts, lens, table, _byref(kv), max_q, D ** -0.5 if scale is None else scale, causal,
-                       window, wp, op, ws.data_ptr(), ws.numel(), _stream_of(stream, q))
+                       _count(window), wp, op, ws.data_ptr(), ws.numel(), _stream_of(stream, q))
     if status:
         _m._check(status, "moe_kv_weights")
     return weight if out is None else out
@@ -410,8 +416,8 @@ def moe_kv_evict(cache: KVCache, weight, kv_len, page_table, keep, new_table, si
     if kept is None:
         kept = _new(stream, weight, (B, Hkv, new_max * page), b.i32)
         kp = kept.data_ptr()
-    status = b.evict(_byref(d), wp, lens, table, keeps, sink, recent, new, new_max, _byref(kv), np_, kp, ws.data_ptr(), ws.numel(),
-                     _stream_of(stream, weight))
+    status = b.evict(_byref(d), wp, lens, table, keeps, _count(sink), _count(recent), new, new_max, _byref(kv), np_, kp,
+                     ws.data_ptr(), ws.numel(), _stream_of(stream, weight))
     if status:
         _m._check(status, "moe_kv_evict")
     return new_len, kept
@@ -433,8 +439,8 @@ class AttentionLayer:
                  rot_dim: Optional[int] = None, rope_base: float = 1e6, interleaved: bool = False, q_norm_weight=None,
                  k_norm_weight=None, eps: float = 1e-6, scale: Optional[float] = None, window: int = 0, device="cuda",
                  track_weights: bool = False):
-        if not 0 <= window < 1 << 31 or (scale is not None and not 0.0 < ctypes.c_float(scale).value < float("inf")):
-            raise ValueError(f"expected an int's window >= 0 and a positive finite fp32 scale, got {window} and {scale}")
+        if window < 0 or (scale is not None and not 0.0 < ctypes.c_float(scale).value < float("inf")):
+            raise ValueError(f"expected window >= 0 and a scale that is positive and finite in fp32, got {window} and {scale}")
         self.Hq, self.Hkv, self.D = Hq, Hkv, D
         self.cache = KVCache.empty(n_pages, Hkv, page, D, device)
         rot_dim = D if rot_dim is None else rot_dim

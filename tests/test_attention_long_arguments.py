@@ -30,9 +30,9 @@ def test_axes_of_no_frequency():
 
 
 def test_layer_numbers():
-    """Windows and scales that are none in the types of the C interface are refused when the layer is made."""
+    """Scales that are none in fp32, and windows below zero, are refused when the layer is made."""
     import moe_expert_layer_fwd_gb300 as moe
-    for kw in (dict(window=1 << 31), dict(window=(1 << 32) + 5), dict(window=-1), dict(scale=1e-60), dict(scale=1e60), dict(scale=0.0),
+    for kw in (dict(window=-1), dict(window=-1 << 32), dict(scale=1e-60), dict(scale=1e60), dict(scale=0.0),
                dict(scale=float("nan"))):
         with pytest.raises(ValueError, match="window"):
             moe.AttentionLayer(4, 8, 2, device="cpu", **kw)
@@ -48,3 +48,9 @@ def test_prefix_tables_without_columns():
     assert shared(L, p=empty, n=256) == moe.MOE_ERR_WORKSPACE and shared(L, p=empty, out=None) == BAD
     assert shared(L, p=prefix(page_table=None)) == BAD and shared(L, p=prefix(max_pages=0, page_table=A + 4)) == BAD
     assert shared(L, p=empty, table=None) == BAD
+
+
+def test_counts_beyond_an_int():
+    """All tokens, not the low bits; negative ones stay negative and are refused."""
+    assert [attention._count(n) for n in (0, 5, (1 << 31) - 1, 1 << 31, 1 << 32, (1 << 32) + 5)] == [0, 5] + [(1 << 31) - 1] * 4
+    assert attention._count(-1) == attention._count(-1 << 40) == -1

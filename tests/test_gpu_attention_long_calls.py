@@ -64,3 +64,26 @@ def test_prefixes_without_tokens_or_columns(env, new):  # noqa: F811
     # one rounding of each, and the weights' 2^-7 of the values that a row may weigh
     assert (got - want).abs().max() <= 2 * (2.0 ** -8 + 2.0 ** -7) * x.abs().max()
     assert (layer.weight - weight).abs().max() <= 2.0 ** -8 * T * 4
+
+
+@pytest.mark.parametrize("n", [1 << 31, 1 << 32, (1 << 32) + 5])
+def test_counts_of_more_than_32_bits(env, n):  # noqa: F811
+    """A window, a sink or recent tokens beyond any length are all tokens, not the number's low bits."""
+    moe, torch = env
+    cache = moe.KVCache(*(torch.randint(0, 100, (4, 2, 16, D), dtype=torch.uint8, device="cuda") for _ in range(2)),
+                        *(torch.full((4, 2), 127, dtype=torch.uint8, device="cuda") for _ in range(2)))
+    q = torch.randn(1, 8, D, device="cuda").to(torch.bfloat16)
+    w = torch.rand(4, 2, 16, device="cuda")
+    lens, start, table, fresh = i32([20]), i32([0, 1]), i32([[0, 1]]), i32([[2]])
+    assert torch.equal(moe.moe_paged_attention(q, cache, start, lens, table, 1, window=n), moe.moe_paged_attention(q, cache, start, lens, table, 1))
+    out, lse = moe.moe_paged_attention_shared(q, cache, start, lens, table, 1)
+    assert torch.equal(moe.moe_paged_attention_shared(q, cache, start, lens, table, 1, window=n)[0], out)
+    assert torch.equal(moe.moe_kv_weights(q, lse, cache, start, lens, table, 1, w, w.clone(), window=n),
+                       moe.moe_kv_weights(q, lse, cache, start, lens, table, 1, w, w.clone()))
+    for kw in (dict(sink=n), dict(recent=n)):
+        _, kept = moe.moe_kv_evict(cache, w, lens, table, i32([7]), fresh, **kw)
+        assert kept[0, :, :7].tolist() == [list(range(7))] * 2      # all tokens alike: the first ones
+    for call in (lambda: moe.moe_paged_attention(q, cache, start, lens, table, 1, window=-n),
+                 lambda: moe.moe_kv_evict(cache, w, lens, table, i32([7]), fresh, recent=-n)):
+        with pytest.raises(moe.MoEError):
+            call()
