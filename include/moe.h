@@ -733,7 +733,8 @@ MOE_API int moe_paged_attention_shared(const moe_kv_desc* d, const uint16_t* q, 
  *
  *  lse [T,Hq] fp32: the denominators' logarithms as moe_paged_attention_shared gives them -- over more keys than
  *      these, if need be: with a shared prefix the weights of a sequence's own tokens are their shares of it all.
- *      A row whose lse, or whose query, is not finite adds nothing; a key with a NaN gets 0.
+ *      A row whose lse, or whose query, is not finite adds nothing; a key with a NaN gets 0.  Nor does a weight that is not finite
+ *      in fp32 (an lse 88 and more below its scores) add anything.
  *  weight_in, weight_out [n_pages,Hkv,page] fp32, beside the cache; they may be the same.
  *  max_q: as for moe_paged_attention, but only a hint.
  *  ws: at least moe_status_bytes().

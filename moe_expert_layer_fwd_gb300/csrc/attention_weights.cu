@@ -58,7 +58,8 @@ struct Cfg {
   static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
 };
 
-// A key's weights of a chunk's rows, from its lane of tensor memory; frees the scores once they are in registers.
+// A key's weights of a chunk's rows, from its lane of tensor memory, those left out that are not finite (a key with a NaN, a denominator
+// far below its scores: as in the kernel for many rows); frees the scores once they are in registers.
 template <int NC, bool kMasked>
 __device__ __forceinline__ float add_weights(uint32_t taddr, const RowPair* row, const RowSeen* seen, float ks, int j, uint64_t* s_empty,
                                              int lane) {
@@ -92,7 +93,8 @@ __device__ __forceinline__ float add_weights(uint32_t taddr, const RowPair* row,
         if ((unsigned)(j - see.x) > (unsigned)see.y) z0 = -CUDART_INF_F;
         if ((unsigned)(j - see.z) > (unsigned)see.w) z1 = -CUDART_INF_F;
       }
-      sum = add_f32x2(sum, f32x2(ex2(z0), ex2(z1)));
+      const float p0 = ex2(z0), p1 = ex2(z1);
+      sum = add_f32x2(sum, f32x2(p0 < CUDART_INF_F ? p0 : 0.f, p1 < CUDART_INF_F ? p1 : 0.f));
     }
   }
   float s0, s1;
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
             if (!ends) {
               s_acc[st * kTile + key] = acc;
             } else if (to) {
-              *to = before + (acc == acc ? acc : 0.f);  // a key that is no number has no weight
+              *to = before + acc;
             }
           }
           if (ok && (g.chunks > 1 || i + nt == g.i1)) {

@@ -5,7 +5,7 @@ import pytest
 
 pytestmark = pytest.mark.gpu
 
-from test_gpu_attention import D, env  # noqa: E402,F401
+from test_gpu_attention import D, Batch, bf16, env  # noqa: E402,F401
 from test_gpu_attention_long import i32  # noqa: E402
 
 
@@ -87,3 +87,24 @@ def test_counts_of_more_than_32_bits(env, n):  # noqa: F811
                  lambda: moe.moe_kv_evict(cache, w, lens, table, i32([7]), fresh, recent=-n)):
         with pytest.raises(moe.MoEError):
             call()
+
+
+@pytest.mark.parametrize("new,Hq", [(1, 2), (1, 8), (3, 8), (2, 24), (20, 8), (70, 16)])
+@pytest.mark.parametrize("fresh", [False, True])
+def test_weights_that_overflow(env, new, Hq, fresh):  # noqa: F811
+    """A denominator so far below a row's scores that all its weights pass fp32 adds nothing, like one that is not there: the same bits,
+    whatever max_q says."""
+    moe, torch = env
+    rng = np.random.default_rng(new + Hq)
+    b = Batch(rng, [new, new], [300, 40], 2, 32).fill(rng).dev(env)
+    q = bf16(rng, 2 * new, Hq, D).cuda()
+    # scores lie within +-88 of zero by far, so e^(score + 200) is above fp32 and e^(score - 4) is not
+    lse = torch.full((2 * new, Hq), 4.0, device="cuda")
+    none = lse.clone()
+    for t, h in ((0, 0), (2 * new - 1, Hq - 1)):
+        lse[t, h], none[t, h] = -200.0, -float("inf")
+    before = torch.rand(b.host["k_codes"].shape[:3], device="cuda")
+    for max_q in (new, 2 * new):
+        got, want = (moe.moe_kv_weights(q, x, b.cache, b.d_start, b.d_len, b.d_table, max_q, None if fresh else before, before.clone())
+                     for x in (lse, none))
+        assert torch.isfinite(got).all() and torch.equal(got, want)
