@@ -697,7 +697,7 @@ MOE_API int moe_kv_append_at(const moe_kv_desc* d, const uint16_t* q, long long 
  * A prefix is read once for all its readers.  Its keys were rotated for positions 0 .. len - 1, so those
  * of a sequence's own tokens go on from there (moe_kv_append_at).
  *
- *  prefix: NULL (none: moe_paged_attention with lse), or n prefixes in the same pool.  Tokens q_start[i] ..
+ *  prefix: NULL (none: moe_paged_attention's rows, bit for bit, and lse), or n prefixes in the same pool.  Tokens q_start[i] ..
  *      q_start[i+1] - 1 of the T read prefix i (it may have no readers, or no tokens), a sequence's all the
  *      same one; q_start[0] = 0, q_start[n] = T.  q_start [n+1], len [n], page_table [n, max_pages]: int32 on
  *      the device; page_table may be NULL when max_pages is 0 (prefixes without tokens).  max_q: at least the readers' tokens of

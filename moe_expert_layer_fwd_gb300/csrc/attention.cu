@@ -305,7 +305,7 @@ cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& args, 
   a.limit_us = g_limit_us;
   a.withhold = g_withhold;
   const bool few = attention_decode_fits(c.Hq / c.Hkv, a.max_q) ||
-                   ((a.pass == 1 || a.pass == 2) && attention_decode_chunks_fit(c, a.max_q, n_sms));
+                   (a.pass == 1 && attention_decode_chunks_fit(c, a.max_q, n_sms));
   return few ? launch_attention_decode(c, a, n_sms, stream, parts) : launch_attention_prefill(c, a, n_sms, stream, parts);
 }
 

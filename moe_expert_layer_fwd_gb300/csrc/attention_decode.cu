@@ -89,9 +89,10 @@ struct Cfg {
 
 // What a (sequence, head) costs besides its tiles, in tiles, all of it at its first one: lengths, page table, queries and output take
 // 10,000 cycles, a tile 2,400.  Calls of two passes have short sequences behind a long prefix, and a run of nine
-// one-tile sequences took 59 us where nine tiles of two took 17.  (Calls of one pass are cut as they always were.)
+// one-tile sequences took 59 us where nine tiles of two took 17.  (Calls of one pass are all cut as those without denominators, whose rows
+// they then give bit for bit.)
 template <int kPass>
-constexpr int kOwnCost = kPass == 0 ? 0 : 4;
+constexpr int kOwnCost = kPass == 1 ? 4 : 0;
 
 __device__ __forceinline__ long long item_cost(int nt, int own) { return nt > 0 ? nt + own : 0; }
 // The first tile of an item that a run has which begins rel into the item's cost.
@@ -110,7 +111,7 @@ struct Segment {
 // Items of one head of a sequence.
 template <int NC, int kPass>
 __device__ __forceinline__ int row_chunks(const KvBatch& c, const SeqRange& s) {
-  return kPass == 0 ? 1 : (int)(((long long)(s.t1 - s.t0) * (c.Hq / c.Hkv) + NC - 1) / NC);
+  return kPass == 1 ? (int)(((long long)(s.t1 - s.t0) * (c.Hq / c.Hkv) + NC - 1) / NC) : 1;
 }
 
 // Walks the segments of a block's run: `left` of cost, from `rel` on in its first item (number `u` of its sequence's, head by head).
@@ -135,7 +136,7 @@ struct Walk {
       const int chunks = row_chunks<NC, kPass>(c, g.s);
       g.b = b;
       g.h = u / chunks;
-      g.row0 = kPass == 0 ? 0 : (u - g.h * chunks) * NC;
+      g.row0 = kPass == 1 ? (u - g.h * chunks) * NC : 0;
       g.i0 = first_tile_from(rel, g.r.nt, kOwn);
       g.i1 = first_tile_from(rel + left, g.r.nt, kOwn);
       g.later = later;
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
     const int units = (int)gridDim.x / c.B, b = (int)blockIdx.x / units, u = (int)blockIdx.x - b * units;  // the most items of a sequence
     int chunks;
     run = item_cost(seq_tiles<NC, kPass>(c, a, b, chunks), kOwn);
-    if (kPass > 0 && run > 0 && c.Hkv * chunks > units && tid == 0) set_status(c.status, DEV_ERR_CONFIG);  // more new tokens than max_q
+    if (kPass == 1 && run > 0 && c.Hkv * chunks > units && tid == 0) set_status(c.status, DEV_ERR_CONFIG);  // more new tokens than max_q
     if (run <= 0 || u >= c.Hkv * chunks) {
       if (kPass == 1) pdl_wait();
       return;
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, Cfg<NC>::kPerSm)
           }
         }
       }
-      if (kPass == 0 && rows * G > NC && lane == 0) set_status(c.status, DEV_ERR_CONFIG);  // more new tokens than max_q
+      if (kPass != 1 && rows * G > NC && lane == 0) set_status(c.status, DEV_ERR_CONFIG);  // more new tokens than max_q
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qb]);
@@ -784,7 +785,7 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStre
   if (e != cudaSuccess) return e;
   // Rows of a few tiles at most (the table's width bounds them) are one block's each: nothing to join.
   const bool split = (long long)c.max_pages * c.page > kWholeTiles * kTile;
-  const int chunks = kPass == 0 ? 1 : (int)(((long long)(c.Hq / c.Hkv) * a.max_q + NC - 1) / NC);
+  const int chunks = kPass == 1 ? (int)(((long long)(c.Hq / c.Hkv) * a.max_q + NC - 1) / NC) : 1;
   const int blocks = split ? blocks_of(n_sms) : c.B * c.Hkv * chunks;
   float* part_o = reinterpret_cast<float*>(a.scratch);
   float2* part_rl = reinterpret_cast<float2*>(part_o + (size_t)2 * blocks_of(n_sms) * NC * kHeadDim);

@@ -108,3 +108,31 @@ def test_weights_that_overflow(env, new, Hq, fresh):  # noqa: F811
         got, want = (moe.moe_kv_weights(q, x, b.cache, b.d_start, b.d_len, b.d_table, max_q, None if fresh else before, before.clone())
                      for x in (lse, none))
         assert torch.isfinite(got).all() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("new,ctx", [([1] * 4, [0, 30, 129, 800]), ([1] * 40, [100 * i for i in range(40)]), ([7] * 10, [0, 5, 20, 9, 0, 1, 30, 2, 3, 4]),
+                                     ([3, 1, 0, 6], [0, 60, 5, 300]), ([5] * 6, [700] * 6), ([100, 30], [0, 150]), ([300, 2], [900, 4000])])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (32, 4), (5, 5), (24, 2)])
+def test_denominators_change_no_output(env, new, ctx, Hq, Hkv):  # noqa: F811
+    """Without prefixes the rows are those of moe_paged_attention, bit for bit, in short tables too."""
+    moe, torch = env
+    rng = np.random.default_rng(len(new))
+    for page in (16, 128):
+        b = Batch(rng, new, ctx, Hkv, page).fill(rng, 1.0, 2.0).dev(env)
+        q = bf16(rng, sum(new), Hq, D, mul=2.0).cuda()
+        for kw in (dict(), dict(window=40), dict(causal=False)):
+            want = moe.moe_paged_attention(q, b.cache, b.d_start, b.d_len, b.d_table, max(new), **kw)
+            out, _ = moe.moe_paged_attention_shared(q, b.cache, b.d_start, b.d_len, b.d_table, max(new), **kw)
+            assert torch.equal(out, want), kw
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [7, 5, 6], [90, 3, 200]])
+def test_tracked_weights_change_no_output(env, new):  # noqa: F811
+    moe, torch = env
+    T = sum(new)
+    layers = [moe.AttentionLayer(60, 32, 4, page=16, max_pos=512, track_weights=track) for track in (False, True)]
+    starts, table = i32(np.cumsum([0] + new)), i32(np.random.default_rng(0).permutation(60).reshape(3, 20))
+    for step in range(1, 3):
+        x = torch.randn(T, 40 * D, device="cuda").to(torch.bfloat16)
+        outs = [layer.forward(x, starts, i32([n * step for n in new]) if max(new) < 100 else i32(new), table, max(new)) for layer in layers]
+        assert torch.equal(*outs)
