@@ -694,8 +694,9 @@ MOE_API int moe_kv_append_at(const moe_kv_desc* d, const uint16_t* q, long long 
  * Attention of a batch whose sequences share long prefixes.  New token t of a sequence sees all tokens of
  * its prefix and its sequence's own tokens as in moe_paged_attention; one softmax over both:
  *   out[t,h] = sum_j p_j v_j,   lse[t,h] = log sum_j exp(scale * q[t,h] . k_j).
- * A prefix is read once for all its readers.  Its keys were rotated for positions 0 .. len - 1, so those
- * of a sequence's own tokens go on from there (moe_kv_append_at).
+ * A prefix is read once for all its readers -- or, when the sequences bring more than 128 rows (new tokens times query
+ * heads of a key/value head) each in the mean and, by max_q, much the same numbers, once for every 256 rows of a sequence, which is faster then.  Its
+ * keys were rotated for positions 0 .. len - 1, so those of a sequence's own tokens go on from there (moe_kv_append_at).
  *
  *  prefix: NULL (none: moe_paged_attention's rows, bit for bit, and lse), or n prefixes in the same pool.  Tokens q_start[i] ..
  *      q_start[i+1] - 1 of the T read prefix i (it may have no readers, or no tokens), a sequence's all the
@@ -705,8 +706,9 @@ MOE_API int moe_kv_append_at(const moe_kv_desc* d, const uint16_t* q, long long 
  *  window > 0 only without prefixes.
  *  lse [T,Hq] fp32 out, natural logarithm, -inf for a row that sees nothing; or NULL.
  *  ws: at least moe_paged_attention_shared_workspace_size(d, max_q, prefix) bytes, of which n, max_pages and max_q of
- *      prefix are read (0: invalid), and max_pages of d.  It grows with T * Hq when there are prefixes with few tokens
- *      a sequence.
+ *      prefix are read (0: invalid), and max_pages of d.  It suits every call with the same B, T, Hq, Hkv, max_q and
+ *      prefix sizes.  Where a prefix is read once for all it grows with T * Hq, and where it is not that part is not needed:
+ *      a call of fewer tokens may need more than one of more.
  * Prefixes are checked as sequences are; the rows of a prefix or a sequence that is left out are undefined (and the status
  * is set).
  */

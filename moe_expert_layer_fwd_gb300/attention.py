@@ -319,7 +319,8 @@ def _prefix_struct(prefix, T: int):
 
 def moe_paged_attention_shared_workspace(T: int, B: int, Hq: int, Hkv: int, D: int, max_q: int, n_prefixes: int = 0,
                                          max_prefix_q: int = 0, device="cuda"):
-    """An initialised workspace for moe_paged_attention_shared calls of these sizes (n_prefixes = 0: without prefixes)."""
+    """An initialised workspace for moe_paged_attention_shared calls of these sizes (n_prefixes = 0: without prefixes).  A call of
+    fewer tokens, or of another max_q, may need a larger one."""
     p = _m.moe_kv_prefix(n_prefixes, 0, min(max_prefix_q, T), None, None, None) if n_prefixes else None
     return _shared_workspace(_m.moe_kv_desc(B, T, Hq, Hkv, D, 16, 0, 0), min(max_q, T), p, _b().torch.empty(0, device=device))
 

@@ -194,9 +194,9 @@ static int prefix_desc(const moe_kv_desc* d, const moe_kv_prefix* p, moe_kv_desc
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // (no more than the sizes: neither pointers nor lengths)
-static bool shared_joins(const moe_kv_desc* d, const moe_kv_desc* pd) {
+static bool shared_joins(const moe_kv_desc* d, const moe_kv_desc* pd, int max_q) {
   const moe_kv_cache none = {};
-  return moe::shared_attention_joins(make_batch(pd, &none, nullptr, nullptr), make_batch(d, &none, nullptr, nullptr));
+  return moe::shared_attention_joins(make_batch(pd, &none, nullptr, nullptr), make_batch(d, &none, nullptr, nullptr), max_q);
 }
 
 size_t moe_paged_attention_shared_workspace_size(const moe_kv_desc* d, int max_q, const moe_kv_prefix* prefix) {
@@ -205,7 +205,7 @@ size_t moe_paged_attention_shared_workspace_size(const moe_kv_desc* d, int max_q
   if (!prefix) return kHeader + scratch;
   moe_kv_desc pd;
   if (prefix_desc(d, prefix, &pd)) return 0;
-  if (shared_joins(d, &pd)) return kHeader + scratch;
+  if (shared_joins(d, &pd, max_q)) return kHeader + scratch;
   const size_t rows = (size_t)d->T * d->Hq;
   return kHeader + 2 * (up256(rows * moe::kHeadDim * sizeof(float)) + up256(rows * sizeof(float))) +
          up256(moe::attention_scratch_bytes(d->Hq, d->Hkv, prefix->max_q, sm_count())) + scratch;
@@ -239,7 +239,7 @@ int moe_paged_attention_shared(const moe_kv_desc* d, const uint16_t* q, long lon
     pc.q_start = prefix->q_start;
     pc.kv_len = prefix->len;
   }
-  if (prefix && !shared_joins(d, &pd)) {
+  if (prefix && !shared_joins(d, &pd, max_q)) {
     for (int i = 0; i < 2; ++i) {
       buffers.rows[i] = (float*)at;
       at += up256((size_t)d->T * d->Hq * moe::kHeadDim * sizeof(float));

@@ -238,11 +238,17 @@ int attention_debug_set(int what, unsigned long long value) {
 }
 
 // Above 128 rows per key/value head and sequence, on average, an item of 256 rows is a sequence's own anyhow, and the prefix's tiles come
-// from L2 whoever asks: one pass saves the second one's items and the rows in between (16 sequences of 20-250 tokens, 8 heads a
-// key/value head, behind 4001: 254 us as two passes, 194 as one).  Below, rows of several sequences share the tiles.
-bool shared_attention_joins(const KvBatch& prefixes, const KvBatch& c) {
-  return (long long)c.T * (c.Hq / c.Hkv) > 128LL * c.B &&
-         ((long long)prefixes.max_pages + c.max_pages) * c.page < (1LL << 31) - 2048;
+// from L2 whoever asks: one pass saves the second one's items and the rows in between (16 sequences of 20-240 tokens, 8 heads a
+// key/value head, behind 4001: 241 us as two passes, 176 as one; 16 of 17 tokens 87 and 68; 64 of 33 tokens 255 and 268).  Below, rows of several
+// sequences share the tiles.  But a mean says nothing of a batch of long and short ones: at least T / max_q of them are long, and each of
+// the others may be an item of its own that goes over the whole prefix with a few rows.  So one pass is for batches where those are at
+// most 0.4 of the items' number.  Decoding sequences and one chunk of tokens, 8 heads, behind 8200, as two passes and as one: 63 and 1100 tokens (1.7)
+// 462 and 741 us, 63 and 4000 (0.5) 1373 and 1520, 15 and 1100 (0.43) 390 and 404, 63 and 8000 (0.25) 3081 and 3036, 15 and 4000 (0.12) 1304
+// and 1174; 16 beside 8 of 200 tokens (0.32), behind 4001, 196 and 174.
+bool shared_attention_joins(const KvBatch& prefixes, const KvBatch& c, int max_q) {
+  const long long rows = (long long)c.T * (c.Hq / c.Hkv);
+  const double items = (double)rows / 256.0, others = c.B - (double)c.T / (max_q > 0 ? max_q : 1);
+  return rows > 128LL * c.B && others <= 0.4 * items && ((long long)prefixes.max_pages + c.max_pages) * c.page < (1LL << 31) - 2048;
 }
 
 // Two passes, each with the kernel that its rows per key/value head call for: over the prefixes, whose readers' tokens are one
@@ -257,7 +263,7 @@ cudaError_t launch_shared_attention(const KvBatch& prefixes, int max_prefix_q, c
     a.pass = 2;
     return launch_paged_attention(c, a, n_sms, stream);
   }
-  if (shared_attention_joins(prefixes, c)) {
+  if (shared_attention_joins(prefixes, c, a.max_q)) {
     a.pass = 3;
     a.n_prefixes = prefixes.B;
     a.prefix_max_pages = prefixes.max_pages;

@@ -82,8 +82,8 @@ size_t attention_scratch_bytes(int Hq, int Hkv, int max_q, int n_sms);
 struct AttentionParts;
 cudaError_t launch_paged_attention(const KvBatch& c, const AttentionArgs& a, int n_sms, cudaStream_t stream, AttentionParts* parts = nullptr);
 
-// Whether sequences bring so many rows that each goes over its prefix by itself, in one pass.
-bool shared_attention_joins(const KvBatch& prefixes, const KvBatch& c);
+// Whether sequences (of at most max_q new tokens) bring so many rows that each goes over its prefix by itself, in one pass.
+bool shared_attention_joins(const KvBatch& prefixes, const KvBatch& c, int max_q);
 // What the two passes leave for the kernel that ends them: rows [T, Hq, 128], denominators [T, Hq], and the scratch of either (the
 // second's is the call's).
 struct SharedBuffers {

@@ -54,3 +54,19 @@ def test_counts_beyond_an_int():
     """All tokens, not the low bits; negative ones stay negative and are refused."""
     assert [attention._count(n) for n in (0, 5, (1 << 31) - 1, 1 << 31, 1 << 32, (1 << 32) + 5)] == [0, 5] + [(1 << 31) - 1] * 4
     assert attention._count(-1) == attention._count(-1 << 40) == -1
+
+
+@pytest.mark.parametrize("new,Hq,Hkv,joined", [
+    ([1] * 63 + [1100], 64, 8, False), ([1] * 63 + [4000], 64, 8, False), ([1] * 15 + [1100], 64, 8, False), ([1, 4000], 64, 8, True),
+    ([1] * 15 + [4000], 32, 4, True), ([17] * 16, 32, 4, True), ([16] * 16, 32, 4, False), ([200] * 8 + [1] * 16, 32, 4, True),
+    ([200] * 8 + [1] * 40, 32, 4, False), ([20, 250, 100, 180], 32, 4, True), ([129], 1, 1, True), ([128], 1, 1, False), ([1] * 64, 64, 8, False)])
+def test_batches_of_long_and_short_sequences_share_their_prefix(new, Hq, Hkv, joined):
+    """Decoding sequences beside a chunk of tokens keep the reading that all share, which needs room for its rows; batches of much the same
+    lengths go over their prefixes by themselves."""
+    import ctypes
+    import moe_expert_layer_fwd_gb300 as moe
+    L, T = moe.lib(), sum(new)
+    d = moe.moe_kv_desc(len(new), T, Hq, Hkv, 128, 64, 1000, 100)
+    size = lambda p: L.moe_paged_attention_shared_workspace_size(ctypes.byref(d), max(new), p)
+    alone, behind = size(None), size(ctypes.byref(moe.moe_kv_prefix(1, 200, T, None, None, None)))
+    assert behind == alone if joined else behind >= alone + 2 * T * Hq * 129 * 4

@@ -6,7 +6,7 @@ import pytest
 pytestmark = pytest.mark.gpu
 
 from test_gpu_attention import D, Batch, bf16, env  # noqa: E402,F401
-from test_gpu_attention_long import i32  # noqa: E402
+from test_gpu_attention_long import Shared, check_shared, i32  # noqa: E402
 
 
 def test_axes_as_arrays(env):  # noqa: F811
@@ -136,3 +136,19 @@ def test_tracked_weights_change_no_output(env, new):  # noqa: F811
         x = torch.randn(T, 40 * D, device="cuda").to(torch.bfloat16)
         outs = [layer.forward(x, starts, i32([n * step for n in new]) if max(new) < 100 else i32(new), table, max(new)) for layer in layers]
         assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("new,readers", [([1] * 12 + [150], [13]), ([1] * 3 + [150], [4]), ([1] * 12 + [150], [5, 8]), ([150, 0] + [1] * 9, [11]),
+                                         ([40, 90, 0, 1, 1, 120], [2, 4])])
+def test_long_and_short_sequences_behind_one_prefix(env, new, readers):  # noqa: F811
+    """Both sides of the border between one pass and two, tight tables and tables much wider than their sequences."""
+    moe, torch = env
+    rng = np.random.default_rng(len(new))
+    for wide in (0, 3000):
+        b = Shared(rng, new, [int(x) for x in rng.integers(0, 200, len(new))], [700, 90][:len(readers)], readers, 2, 32)
+        if wide:
+            b.table, b.p_table = (np.concatenate([np.maximum(t, -1), np.full((len(t), wide), -1, np.int32)], 1) for t in (b.table, b.p_table))
+        b.dev(env)
+        b.d_start, b.d_len = i32(b.q_start), i32(b.kv_len)
+        for Hq in (8, 16):
+            check_shared(env, b, bf16(rng, sum(new), Hq, D, mul=2.0))
