@@ -6,7 +6,7 @@ import pytest
 pytestmark = pytest.mark.gpu
 
 from test_gpu_attention import D, Batch, bf16, env  # noqa: E402,F401
-from test_gpu_attention_long import Shared, check_shared, i32  # noqa: E402
+from test_gpu_attention_long import Shared, check_shared, check_weights, denominators, i32  # noqa: E402
 
 
 def test_axes_as_arrays(env):  # noqa: F811
@@ -152,3 +152,46 @@ def test_long_and_short_sequences_behind_one_prefix(env, new, readers):  # noqa:
         b.d_start, b.d_len = i32(b.q_start), i32(b.kv_len)
         for Hq in (8, 16):
             check_shared(env, b, bf16(rng, sum(new), Hq, D, mul=2.0))
+
+
+@pytest.mark.parametrize("new", [[1] * 4, [30, 7], [200, 90]])
+def test_tables_much_wider_than_their_sequences(env, new):  # noqa: F811
+    """A server's tables are as wide as its longest context, whatever is in them."""
+    moe, torch = env
+    rng = np.random.default_rng(len(new))
+    B = len(new)
+    for wide in (0, 5, 2048):
+        rng = np.random.default_rng(1)
+        b = Shared(rng, new, [20, 0, 300, 11][:B], [100, 9], [1, B - 1], 2, 16)
+        if wide:
+            b.table, b.p_table = (np.concatenate([t, np.full((len(t), wide), -1, np.int32)], 1) for t in (b.table, b.p_table))
+        b.dev(env)
+        b.d_start, b.d_len, b.d_table = i32(b.q_start), i32(b.kv_len), i32(np.ascontiguousarray(b.table))
+        q = bf16(rng, sum(new), 8, D, mul=2.0)
+        check_shared(env, b, q)
+        check_shared(env, b, q, prefix=False)
+        check_weights(env, b, q, denominators(b, q))
+
+
+@pytest.mark.parametrize("new", [[1] * 4, [30, 7], [200, 90]])
+def test_denominators_are_optional(env, new):  # noqa: F811
+    """lse = NULL at the C entry point: the same rows."""
+    import ctypes
+    moe, torch = env
+    rng = np.random.default_rng(3)
+    B, T = len(new), sum(new)
+    b = Shared(rng, new, [20, 0, 300, 11][:B], [400, 9], [1, B - 1], 2, 16)
+    b.dev(env)
+    b.d_start, b.d_len, table = i32(b.q_start), i32(b.kv_len), i32(np.ascontiguousarray(b.table))
+    q = bf16(rng, T, 8, D, mul=2.0).cuda()
+    for prefix in (b.prefix(), None):
+        want, _ = moe.moe_paged_attention_shared(q, b.cache, b.d_start, b.d_len, table, max(new), prefix)
+        n, n_pages = table.shape[1], b.cache.k_codes.shape[0]
+        d, kv = moe.moe_kv_desc(B, T, 8, 2, D, 16, n_pages, n), b.cache._struct()
+        p = None if prefix is None else ctypes.byref(moe.moe_kv_prefix(2, prefix[2].shape[1], prefix[3], *(t.data_ptr() for t in prefix[:3])))
+        need = moe.lib().moe_paged_attention_shared_workspace_size(ctypes.byref(d), max(new), p)
+        ws, out = torch.zeros(need, dtype=torch.uint8, device="cuda"), torch.empty_like(want)
+        assert moe.lib().moe_paged_attention_shared(ctypes.byref(d), q.data_ptr(), 8 * D, b.d_start.data_ptr(), b.d_len.data_ptr(), table.data_ptr(),
+                                                    ctypes.byref(kv), max(new), D ** -0.5, 1, 0, p, out.data_ptr(), None, ws.data_ptr(), need,
+                                                    torch.cuda.current_stream().cuda_stream) == moe.MOE_OK
+        assert torch.equal(out, want) and moe.moe_get_device_status(ws) == moe.MOE_OK
