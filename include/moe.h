@@ -694,9 +694,10 @@ MOE_API int moe_kv_append_at(const moe_kv_desc* d, const uint16_t* q, long long 
  * Attention of a batch whose sequences share long prefixes.  New token t of a sequence sees all tokens of
  * its prefix and its sequence's own tokens as in moe_paged_attention; one softmax over both:
  *   out[t,h] = sum_j p_j v_j,   lse[t,h] = log sum_j exp(scale * q[t,h] . k_j).
- * A prefix is read once for all its readers -- or, when the sequences bring more than 128 rows (new tokens times query
- * heads of a key/value head) each in the mean and, by max_q, much the same numbers, once for every 256 rows of a sequence, which is faster then.  Its
- * keys were rotated for positions 0 .. len - 1, so those of a sequence's own tokens go on from there (moe_kv_append_at).
+ * A prefix is read once for all its readers -- or, when the sequences bring more than 128 rows (new tokens times query heads of a
+ * key/value head) each in the mean and, by max_q, much the same numbers, once for every 256 rows of a sequence, which is faster then.
+ * Its keys were rotated for positions 0 .. len - 1, so those of a sequence's own tokens go on from there (moe_kv_append_at).  Ranges and
+ * the bits of scores and weights are those of moe_paged_attention; what two passes leave for one another is fp32.
  *
  *  prefix: NULL (none: moe_paged_attention's rows, bit for bit, and lse), or n prefixes in the same pool.  Tokens q_start[i] ..
  *      q_start[i+1] - 1 of the T read prefix i (it may have no readers, or no tokens), a sequence's all the
@@ -731,12 +732,16 @@ MOE_API int moe_paged_attention_shared(const moe_kv_desc* d, const uint16_t* q, 
  * tokens, over the new tokens t and the query heads of h that see j (as in moe_paged_attention),
  *   weight_out[page of j, h, place of j] = before + sum exp(scale * q[t,head] . k_j - lse[t,head]),
  * before = weight_in there, or 0 for the sequence's new tokens (whatever their page held) and when weight_in is NULL.
- * Of tokens that no new one sees (behind a window), and of sequences without new tokens, nothing is written.
+ * Of tokens that no new one sees (behind a window), and of sequences without new tokens, nothing is written.  The tokens of a
+ * shared prefix are no sequence's of a batch, and get nothing by its call.  What its readers give them: a call with the prefixes' q_start,
+ * len and page_table as the sequences, causal 0 and weight_in NULL, into a buffer of its own (all their tokens begin at 0); the
+ * caller adds that to what they had.
  *
  *  lse [T,Hq] fp32: the denominators' logarithms as moe_paged_attention_shared gives them -- over more keys than
  *      these, if need be: with a shared prefix the weights of a sequence's own tokens are their shares of it all.
  *      A row whose lse, or whose query, is not finite adds nothing; a key with a NaN gets 0.  Nor does a weight that is not finite
- *      in fp32 (an lse 88 and more below its scores) add anything.
+ *      in fp32 (an lse 88 and more below its scores) add anything.  Scores are fp32; up to 16 rows a key/value head, elements of a
+ *      query below 2^-9 of its head's largest are off by up to 2^-17 of that.
  *  weight_in, weight_out [n_pages,Hkv,page] fp32, beside the cache; they may be the same.
  *  max_q: as for moe_paged_attention, but only a hint.
  *  ws: at least moe_status_bytes().
@@ -751,7 +756,8 @@ MOE_API int moe_kv_weights(const moe_kv_desc* d, const uint16_t* q, long long q_
  * Packs what stays of each sequence into new pages.  Of the kv_len[b] tokens of sequence b the m = min(kv_len[b],
  * keep[b]) of the largest weight stay, for each key/value head by its own weights and in their order; of
  * equal weights the first.  The first `sink` and the last `recent` tokens have the largest weight of all;
- * one that is not above 0 (a NaN among them) counts as 0.
+ * one that is not above 0 (a NaN among them) counts as 0.  As they are equals, too, a keep[b] below sink + recent keeps the first ones of
+ * them and not the newest: whoever wants these asks for sink + recent at least, or for fewer recent ones.
  *
  *  T and Hq of d are not used.  keep [B], new_table [B,new_max_pages]: int32 on the device.
  *  New pages come from the same pool, are all different and none of the pages that this call reads.  They get the kept
@@ -761,7 +767,8 @@ MOE_API int moe_kv_weights(const moe_kv_desc* d, const uint16_t* q, long long q_
  *  ws: at least moe_status_bytes().
  * keep[b] < 0, or m beyond the new table, sets the status to MOE_ERR_DEVICE_CHECK and leaves the sequence out
  * (new_len[b] = -1); so do pages outside the pool (a token on such a page counts as weight 0, and as zeros if it stays).
- * Positions: the next token's place in the cache is new_len[b], its position is not (moe_kv_append_at).
+ * Positions: the next token's place in the cache is new_len[b], its position is not (moe_kv_append_at).  A `window` of the
+ * attention counts places, so behind an eviction it is one of tokens that stayed.
  */
 MOE_API int moe_kv_evict(const moe_kv_desc* d, float* weight, const int32_t* kv_len, const int32_t* page_table,
                          const int32_t* keep, int sink, int recent, const int32_t* new_table, int new_max_pages,

@@ -397,7 +397,8 @@ def moe_kv_weights(q, lse, cache: KVCache, q_start, kv_len, page_table, max_q: i
 def moe_kv_evict(cache: KVCache, weight, kv_len, page_table, keep, new_table, sink: int = 0, recent: int = 0, new_len=None, kept=None,
                  ws=None, stream=None):
     """Packs the keep[b] tokens of the largest weight [n_pages, Hkv, page] of each sequence and head, with their weights, into the
-    pages of new_table; returns (new_len [B], kept [B, Hkv, new_max_pages * page]: the tokens that stayed, then -1)."""
+    pages of new_table; the first ``sink`` and last ``recent`` tokens stay before all others (of keep[b] below their number the first);
+    returns (new_len [B], kept [B, Hkv, new_max_pages * page]: the tokens that stayed, then -1)."""
     b = _b()
     kv = cache._struct()
     n_pages, Hkv, page, D = cache[0].shape
@@ -433,8 +434,10 @@ class AttentionLayer:
     workspace and run one after another; ``status`` says what they found.
 
     Long conversations: ``rows`` (of ``rotation``) turns the tokens by given positions instead of their places in the cache; ``prefix``
-    lets sequences share what another one stored; with ``track_weights`` every call adds the attention weights that the cached
-    tokens got to ``weight``, and ``evict`` packs the tokens of the largest ones into new pages."""
+    lets sequences share what another one stored; with ``track_weights`` every call adds the attention weights that the sequences' own
+    cached tokens got to ``weight`` (not those of a prefix's tokens, whose readers' weights moe_kv_weights gives in a call of its own: see
+    include/moe.h), and ``evict`` packs the tokens of the largest ones into new pages.  With weights, a page is in one row of
+    ``page_table`` only; after an eviction a ``window`` counts the tokens that stayed."""
 
     def __init__(self, n_pages: int, Hq: int, Hkv: int, D: int = 128, page: int = 64, max_pos: int = 32768,
                  rot_dim: Optional[int] = None, rope_base: float = 1e6, interleaved: bool = False, q_norm_weight=None,

@@ -5,7 +5,8 @@ import pytest
 
 pytestmark = pytest.mark.gpu
 
-from test_gpu_attention import D, Batch, bf16, env  # noqa: E402,F401
+from oracle import attention_long as ol  # noqa: E402
+from test_gpu_attention import D, Batch, bf16, env, f64  # noqa: E402,F401
 from test_gpu_attention_long import Shared, check_shared, check_weights, denominators, i32  # noqa: E402
 
 
@@ -171,6 +172,30 @@ def test_tables_much_wider_than_their_sequences(env, new):  # noqa: F811
         check_shared(env, b, q)
         check_shared(env, b, q, prefix=False)
         check_weights(env, b, q, denominators(b, q))
+
+
+@pytest.mark.parametrize("new,readers", [([1] * 4, [3, 1]), ([5, 0, 2, 3], [2, 2]), ([70, 30, 9], [1, 2])])
+def test_weights_of_the_prefixes_tokens(env, new, readers):  # noqa: F811
+    """What the readers give a prefix's tokens: the prefixes as the sequences, without a mask, from zero on.  With the sequences' own
+    weights all rows add up."""
+    moe, torch = env
+    rng = np.random.default_rng(len(new))
+    b = Shared(rng, new, [30, 0, 100, 4][:len(new)], [300, 77], readers, 2, 32)
+    b.dev(env)
+    b.d_start, b.d_len, b.d_table = i32(b.q_start), i32(b.kv_len), i32(np.ascontiguousarray(b.table))
+    q, shape, ws = bf16(rng, sum(new), 8, D, mul=2.0).cuda(), b.host["k_codes"].shape[:3], moe.moe_kv_workspace()
+    _, lse = moe.moe_paged_attention_shared(q, b.cache, b.d_start, b.d_len, b.d_table, max(new), b.prefix())
+    start, length, table, most = b.prefix()
+    own, of_prefix = torch.zeros(shape, device="cuda"), torch.zeros(shape, device="cuda")
+    moe.moe_kv_weights(q, lse, b.cache, b.d_start, b.d_len, b.d_table, max(new), own, ws=ws)
+    moe.moe_kv_weights(q, lse, b.cache, start, length, table, most, None, of_prefix, causal=False, ws=ws)
+    assert moe.moe_get_device_status(ws) == moe.MOE_OK
+    want, added, written = ol.weights(f64(q), lse.cpu().double().numpy(), b.host, b.p_start, b.p_len, b.p_table, D ** -0.5,
+                                      np.zeros(shape), True, False)
+    got = of_prefix.cpu().double().numpy()
+    assert (np.abs(got - want) <= 2.0 ** -9 * added + 2.0 ** -22 * added).all() and (got[~written] == 0).all()
+    total = (own + of_prefix).double().sum((0, 2))
+    assert ((total - 4 * sum(new)).abs() <= 2.0 ** -9 * 4 * sum(new)).all()
 
 
 @pytest.mark.parametrize("new", [[1] * 4, [30, 7], [200, 90]])
