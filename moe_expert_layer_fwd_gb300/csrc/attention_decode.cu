@@ -805,7 +805,8 @@ bool attention_decode_fits(int G, int max_q) { return (long long)G * max_q <= 16
 // More rows than that, 16 at a time, where there are so few keys that the way to the first scores counts: it takes this kernel 6 us and the
 // other one 11, and a part's end 2 and 6.  Keys as the tables' widths bound them, six tiles a block at most: 10 sequences of up to 7
 // tokens, 2 key/value heads, behind 86-259 tokens 67 -> 35 us; at seven tiles a block (30 sequences behind 2193-2925, 4 key/value heads)
-// 45 -> 48, at ten (21 of up to 5 tokens over 700, 8 heads) 123 -> 134.
+// 45 -> 48, at ten (21 of up to 5 tokens over 700, 8 heads) 123 -> 134.  Short sequences in wide tables go to the other kernel for that: the 10
+// sequences take 24 us, and 44 in tables of 131072 tokens.
 bool attention_decode_chunks_fit(const KvBatch& c, int max_q, int n_sms) {
   const long long chunks = ((long long)(c.Hq / c.Hkv) * max_q + 15) / 16, tiles = ((long long)c.max_pages * c.page + kTile - 1) / kTile;
   return chunks * c.B * c.Hkv * tiles <= (long long)kSmallTiles * blocks_of(n_sms);

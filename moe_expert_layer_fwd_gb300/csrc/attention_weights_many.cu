@@ -13,8 +13,9 @@
 // A block keeps kTiles tiles of keys in shared memory, converted, and walks the chunks of NC rows over them.
 //
 // Measured: the last 40-64 tokens of 4 prompts of 5000-16000, 8 query heads a key/value head, 64 us (35.6 GFLOP of scores, 18 us at the
-// bf16 rate).  A block's 62 steps take 700 cycles of products each, 500 in which their scores or keys are waited for, and 11,500 pass before
-// the first one.
+// bf16 rate).  Of a block's 111,000 cycles (the slowest of 150 has 125,000) 4,700 pass before its roles begin, 10,700 more before its first
+// product and 2,900 after its last.  The 61 steps between take 1,520 each: the MMA warp waits 300 for keys, 180 for room for scores and
+// 80 for queries, and is 960 at issuing a step's nine products (576 at the tensor core's rate).
 //
 // Warps: 8 softmax (two groups of four, which take the tiles in turn, two buffers of scores each), 4 that convert keys, TMA, MMA, 4 for
 // the queries (two for either buffer).  Every wait is bounded (2 s).
@@ -558,6 +559,8 @@ cudaError_t launch(const KvBatch& c, const AttentionArgs& a, const float* lse, c
 
 cudaError_t launch_kv_weights_many(const KvBatch& c, const AttentionArgs& a, const float* lse, const float* weight_in, float* weight_out,
                                    int n_sms, cudaStream_t stream) {
+  // By the most rows of a sequence.  32 sequences of 1000-4000 tokens and 4 of 5000-16000, 8 key/value heads, chunks of 64 and of 128: 32 rows
+  // 49 and 64 us, 29 and 31; 64 rows 47 and 59, 29 and 33; 72 rows (two chunks of 64) 86 and 62, 45 and 37; 128 rows 76 and 59, 39 and 31.
   const long long rows = (long long)(c.Hq / c.Hkv) * a.max_q;
   return rows <= 64 ? launch<64>(c, a, lse, weight_in, weight_out, n_sms, stream) : launch<128>(c, a, lse, weight_in, weight_out, n_sms, stream);
 }
