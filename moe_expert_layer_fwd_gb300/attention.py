@@ -490,7 +490,7 @@ class AttentionLayer:
             _need(rows, "rows", _b().f32, (T, self.cos_sin.shape[1]))
         shared = p is not None or self.weight is not None
         n_pages, _, page, _ = self.cache.k_codes.shape
-        d = _m.moe_kv_desc(B, T, self.Hq, self.Hkv, self.D, page, n_pages, page_table.shape[1])
+        d = _m.moe_kv_desc(B, T, self.Hq, self.Hkv, self.D, page, n_pages, page_table.shape[-1])
         ws = self._workspace_for(d, max_q, stream, p)
         if rows is None:
             rq = moe_kv_append(q, k, v, self.cache, q_start, kv_len, page_table, self.cos_sin, None, self.interleaved,

@@ -220,3 +220,11 @@ def test_denominators_are_optional(env, new):  # noqa: F811
                                                     ctypes.byref(kv), max(new), D ** -0.5, 1, 0, p, out.data_ptr(), None, ws.data_ptr(), need,
                                                     torch.cuda.current_stream().cuda_stream) == moe.MOE_OK
         assert torch.equal(out, want) and moe.moe_get_device_status(ws) == moe.MOE_OK
+
+
+def test_tables_of_one_dimension_are_refused(env):  # noqa: F811
+    moe, torch = env
+    x, starts, lens, table = layer_inputs(torch)
+    layer = moe.AttentionLayer(8, 8, 2, page=16)
+    with pytest.raises(ValueError, match="page_table"):
+        layer.forward(x, starts, lens, table[:, 0].contiguous(), 3)
